@@ -11,6 +11,9 @@
  *   fast step    sfi_sparse_decode_attn   attention over the packed rows + recent window
  *                sfi_fast_decode_step     the append and that attention in one launch
  *   host         sfi_schedule             trigger policy: slow or fast for each step
+ *   around it    sfi_append_chunk, sfi_window_attn   a prompt into the cache, and its attention
+ *                sfi_pages_reserve, _release, _evict, _compact   the pages of a paged cache
+ *                sfi_beam_select, sfi_reorder        beam search, and forking sequences
  *
  * Conventions for every call:
  *   - All tensors are device memory owned by the caller; the library never allocates.
@@ -56,6 +59,10 @@ typedef enum sfi_status {
 #define SFI_DEVERR_TIMEOUT 0x4u    /* a bounded pipeline wait gave up: outputs invalid,      */
                                    /* re-initialise the workspace before further use         */
 #define SFI_DEVERR_LENGTH 0x8u     /* seq_len[b] > max_len: that sequence's work skipped     */
+#define SFI_DEVERR_POOL 0x10u      /* sfi_pages_reserve: not enough free pages               */
+#define SFI_DEVERR_ROWS 0x20u      /* row_start inconsistent: that sequence's rows skipped   */
+#define SFI_DEVERR_SEQ 0x40u       /* sfi_reorder: src[b] outside [0, batch): b left alone   */
+#define SFI_DEVERR_REFS 0x80u      /* a page given up that page_refs counts no holder of     */
 
 /*
  * The KV cache of all layers (summary section 3: recent tokens are read straight from the
@@ -377,6 +384,163 @@ typedef struct sfi_decode_plan {
 sfi_status sfi_decode_run(const sfi_kv_cache *kv, const sfi_budget *budget,
                           const sfi_sparse_mem *mem, const sfi_decode_plan *plan, void *ws,
                           size_t ws_bytes, void *stream);
+
+/*
+ * Pages of a paged cache. The paper has no counterpart of these calls (it reads a paged cache
+ * that a server keeps): they keep it, on the device, without a host round trip.
+ *   page_table  int32 [batch][max_pages_per_seq], the cache's own table, here written.
+ *               A negative entry holds no page; every other entry is one reference.
+ *   refs        int32 [n_pages]: the table entries that hold each page; 0 = free.
+ * Start with every entry -1 and every count 0. The table is the only record of what a
+ * sequence holds: entries past its length (reserved ahead) count too. All calls of this group
+ * need a paged cache (page_size 16), SFI_ERR_INVALID_ARG otherwise; `active` (device uint8
+ * [batch], NULL = all) leaves the other sequences alone. What they do depends on their inputs
+ * alone, never on timing: pages are handed out lowest first, in order of sequence and position.
+ */
+typedef struct sfi_page_pool {
+    int32_t *page_table;
+    int32_t *refs;
+} sfi_page_pool;
+
+/* Bytes of device workspace of sfi_pages_reserve and sfi_pages_compact (256-byte aligned; it
+ * needs no initialisation). 0 on invalid arguments. */
+size_t sfi_pages_workspace_bytes(const sfi_kv_cache *kv);
+
+/*
+ * Make positions [seq_len[b], seq_len[b] + n_new[b]) of every active sequence writable
+ * (n_new: device int32 [batch], NULL = one each; <= 0: none): entries without a page get one,
+ * and an entry whose page other sequences hold too (after sfi_reorder) is replaced by a page
+ * of its own, into which the rows below seq_len[b] are copied in every layer. Of several
+ * sequences that reserve on one shared page in the same call, all but the last copy it (the
+ * last keeps it if nobody else holds it). seq_len is not changed.
+ * A sequence that does not fit its capacity (SFI_DEVERR_CAPACITY), whose current page is
+ * missing (SFI_DEVERR_PAGE_RANGE), or that the free pages do not cover, counted in order of
+ * sequence (SFI_DEVERR_POOL, it and every later one that needs a page), is left as it was.
+ *   ok  optional device uint8 [batch]: 1 for the active sequences whose positions are
+ *       writable, else 0; may be given as `active` to the calls that write them.
+ */
+sfi_status sfi_pages_reserve(const sfi_kv_cache *kv, const sfi_page_pool *pool,
+                             const int32_t *n_new, const uint8_t *active, uint8_t *ok, void *ws,
+                             size_t ws_bytes, void *stream);
+
+/* Give up every page of the active sequences: their entries become -1, their lengths 0. */
+sfi_status sfi_pages_release(const sfi_kv_cache *kv, const sfi_page_pool *pool,
+                             const uint8_t *active, void *stream);
+
+/*
+ * Give up the pages of the active sequences that lie wholly outside the first n_sink positions
+ * and the recent window [seq_len - n_window, seq_len): what sfi_window_attn with the same
+ * n_sink and n_window reads from then on, for new rows and for the last one written, is kept.
+ * Lengths and the pages reserved ahead stay. Calls that read the whole history
+ * (sfi_dense_decode_attn, sfi_compact of an evicted position) find a bad entry afterwards.
+ */
+sfi_status sfi_pages_evict(const sfi_kv_cache *kv, const sfi_page_pool *pool, int32_t n_sink,
+                           int32_t n_window, const uint8_t *active, void *stream);
+
+/*
+ * Move the pages in use to the front of the pool: with U pages in use, the i-th used page
+ * with id >= U (ascending) moves to the i-th free id below U, in every layer, and table and
+ * refs follow, so that pages [U, n_pages) are free and the pool can be cut to any n_pages >=
+ * U. n_used: device int32, receives U. The contents of pages left behind are not cleared.
+ */
+sfi_status sfi_pages_compact(const sfi_kv_cache *kv, const sfi_page_pool *pool, int32_t *n_used,
+                             void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * Rows of a chunk. sfi_append_chunk and sfi_window_attn take several rows per sequence,
+ * packed: sequence b owns rows [row_start[b], row_start[b + 1]) of [n_rows] (row_start: device
+ * int32 [batch + 1], ascending). n_rows bounds row_start[batch] and max_rows every sequence's
+ * count; rows behind row_start[batch] are not touched. row_start == NULL: one row each
+ * (n_rows == batch). A sequence whose rows run backwards, past n_rows or past max_rows is
+ * skipped (SFI_DEVERR_ROWS).
+ *
+ * sfi_append_chunk writes a chunk of new tokens (a prompt or a part of one):
+ * k_new, v_new: bf16 [n_layers][n_rows][n_kv_heads][128]. Row i of an active sequence goes to
+ * position seq_len[b] + i of every layer; then seq_len[b] advances by the row count. A
+ * sequence that would pass its capacity (SFI_DEVERR_CAPACITY), is longer than max_len
+ * (SFI_DEVERR_LENGTH) or lacks a page (SFI_DEVERR_PAGE_RANGE) does not advance; of the last,
+ * the rows that have a page are written. max_len bounds the lengths before the call.
+ */
+sfi_status sfi_append_chunk(const sfi_kv_cache *kv, const void *k_new, const void *v_new,
+                            const int32_t *row_start, int32_t n_rows, int32_t max_rows,
+                            const uint8_t *active, void *stream);
+
+/*
+ * Attention of a chunk under the sinks and the sliding window of the sparse state (summary
+ * 2A), with nothing packed: the prompt's form of the fast step, and for one row per sequence
+ * its single-token form. The rows of an active sequence are its last positions, already in
+ * the cache: row i of m is at position P = seq_len[b] - m + i and attends
+ *     j <= P with j < n_sink or j > P - n_window,
+ * softmax(q_h . k_j / sqrt(128)) over those j (n_window >= seq_len: all of j <= P).
+ *   q    bf16 [n_layers][n_rows][n_q_heads][128]
+ *   out  [n_layers][n_rows][n_q_heads][128], fp32 if out_fp32 else bf16; rows of inactive or
+ *        skipped sequences and rows behind row_start[batch] are not written
+ * Cache rows that no row of the call attends to are never looked at (their pages may be
+ * missing, their contents may be anything). Softmax weights enter the product with V as bf16;
+ * with out_fp32 as bf16 part and bf16 remainder. n_sink >= 0, n_window >= 1. A sequence longer
+ * than max_len, or with more rows than its length, is skipped (SFI_DEVERR_LENGTH).
+ *   ws   workspace of at least sfi_window_workspace_bytes(), 256-byte aligned and initialised
+ *        (sfi_workspace_init, once); calls sharing it must not overlap.
+ */
+sfi_status sfi_window_attn(const sfi_kv_cache *kv, const void *q, void *out, int32_t out_fp32,
+                           const int32_t *row_start, int32_t n_rows, int32_t max_rows,
+                           int32_t n_sink, int32_t n_window, const uint8_t *active, void *ws,
+                           size_t ws_bytes, void *stream);
+size_t sfi_window_workspace_bytes(const sfi_kv_cache *kv, int32_t n_rows, int32_t max_rows,
+                                  int32_t n_sink, int32_t n_window);
+
+/*
+ * Sequence b takes over the state of sequence src[b] (src: device int32 [batch]; src[b] == b
+ * stays; any map, several may take the same): beam search's reordering, and the fork of a
+ * prompt into several sequences. All sequences are read before any is written.
+ *   lengths; of a paged cache (pool given, required then) the table row, with refs; of a
+ *   contiguous cache (pool NULL) the K and V rows below the length;
+ *   with mem given (budget required then) the packed memory: the first rows[u] rows of kc and
+ *   vc, sel_idx, sel_cnt and rows.
+ * A src[b] outside [0, batch) raises SFI_DEVERR_SEQ and leaves b alone. Forked sequences share
+ * all their pages: call sfi_pages_reserve before anything writes to them.
+ */
+sfi_status sfi_reorder(const sfi_kv_cache *kv, const sfi_page_pool *pool,
+                       const sfi_budget *budget, const sfi_sparse_mem *mem, const int32_t *src,
+                       void *stream);
+
+/*
+ * Beam search's selection. n_groups prompts of n_beams beams each; row r = group * n_beams +
+ * beam. With x = logits[r], a live row offers every token v at score
+ *     s(r, v) = cum[r] + x[v] - log sum_w exp(x[w]),
+ * a finished one (done[r] != 0) only (r, eos) at s = cum[r]. Each group keeps the n_beams
+ * candidates that are highest by s * rank_scale[r] (NULL: by s), ties to the lowest (beam,
+ * token); within a row, by logit. A score that is not a number (a row of -inf, an infinite or
+ * NaN logit) counts as -inf.
+ *   logits      bf16, or fp32 if logits_fp32: [rows] of vocab, row_stride elements apart
+ *   cum         fp32 [rows]; done: uint8 [rows], NULL = none; rank_scale: fp32 [rows], > 0 and
+ *               finite (a length penalty 1 / length^alpha, say)
+ *   parent, token  int32 [rows]: the kept candidates, best first; parent as a row, ready to be
+ *               sfi_reorder's src
+ *   cum_out     fp32 [rows]: their scores s; done_out: uint8 [rows] or NULL: done[parent], or
+ *               token == eos. Outputs must not overlap the inputs.
+ * eos < 0: no token ends a beam (done must be NULL then). 1 <= n_beams <= 16, else
+ * SFI_ERR_UNSUPPORTED; n_groups * n_beams <= 65535; vocab < 2^31 / n_beams.
+ */
+typedef struct sfi_beam {
+    int32_t n_groups, n_beams, vocab, logits_fp32;
+    int64_t row_stride;
+    int32_t eos;
+    int32_t reserved;           /* 0 */
+    const void *logits;
+    const float *cum;
+    const uint8_t *done;
+    const float *rank_scale;
+    int32_t *parent;
+    int32_t *token;
+    float *cum_out;
+    uint8_t *done_out;
+} sfi_beam;
+
+/* Workspace of sfi_beam_select (256-byte aligned, initialised once with sfi_workspace_init;
+ * calls sharing it must not overlap). 0 on invalid arguments. */
+size_t sfi_beam_workspace_bytes(const sfi_beam *beam);
+sfi_status sfi_beam_select(const sfi_beam *beam, void *ws, size_t ws_bytes, void *stream);
 
 /* Copy the device error word to *bits (synchronises `stream`). Returns SFI_OK when it is
  * zero, SFI_ERR_DEVICE when any bit is set. */

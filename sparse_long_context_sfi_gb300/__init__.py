@@ -25,6 +25,10 @@ SFI_DEVERR_PAGE_RANGE = 0x1
 SFI_DEVERR_CAPACITY = 0x2
 SFI_DEVERR_TIMEOUT = 0x4
 SFI_DEVERR_LENGTH = 0x8
+SFI_DEVERR_POOL = 0x10
+SFI_DEVERR_ROWS = 0x20
+SFI_DEVERR_SEQ = 0x40
+SFI_DEVERR_REFS = 0x80
 
 ENTRY_POINTS = (
     "sfi_status_string", "sfi_version", "sfi_workspace_bytes", "sfi_workspace_init",
@@ -34,6 +38,9 @@ ENTRY_POINTS = (
     "sfi_schedule",
     "sfi_schedule_tokens", "sfi_decode_run", "sfi_read_error", "sfi_clear_error",
     "sfi_test_inject_stall",
+    "sfi_pages_workspace_bytes", "sfi_pages_reserve", "sfi_pages_release", "sfi_pages_evict",
+    "sfi_pages_compact", "sfi_append_chunk", "sfi_window_attn", "sfi_window_workspace_bytes",
+    "sfi_reorder", "sfi_beam_workspace_bytes", "sfi_beam_select",
 )
 
 
@@ -69,6 +76,18 @@ class SfiDecodePlan(C.Structure):
                 ("concurrent_fast", C.c_int32)]
 
 
+class SfiPagePool(C.Structure):
+    _fields_ = [("page_table", C.c_void_p), ("refs", C.c_void_p)]
+
+
+class SfiBeam(C.Structure):
+    _fields_ = [("n_groups", C.c_int32), ("n_beams", C.c_int32), ("vocab", C.c_int32),
+                ("logits_fp32", C.c_int32), ("row_stride", C.c_int64), ("eos", C.c_int32),
+                ("reserved", C.c_int32), ("logits", C.c_void_p), ("cum", C.c_void_p),
+                ("done", C.c_void_p), ("rank_scale", C.c_void_p), ("parent", C.c_void_p),
+                ("token", C.c_void_p), ("cum_out", C.c_void_p), ("done_out", C.c_void_p)]
+
+
 class SfiError(RuntimeError):
     def __init__(self, fn: str, status: int):
         self.status = status
@@ -87,6 +106,7 @@ def lib():
         l = C.CDLL(LIB_PATH)
         P, I32, SZ = C.c_void_p, C.c_int32, C.c_size_t
         KV, BD, MEM = C.POINTER(SfiKvCache), C.POINTER(SfiBudget), C.POINTER(SfiSparseMem)
+        PP = C.POINTER(SfiPagePool)
         sig = {
             "sfi_status_string": (C.c_char_p, [C.c_int]),
             "sfi_version": (C.c_char_p, []),
@@ -107,6 +127,17 @@ def lib():
             "sfi_read_error": (C.c_int, [KV, C.POINTER(C.c_uint32), P]),
             "sfi_clear_error": (C.c_int, [KV, P]),
             "sfi_test_inject_stall": (C.c_int, [I32]),
+            "sfi_pages_workspace_bytes": (SZ, [KV]),
+            "sfi_pages_reserve": (C.c_int, [KV, PP, P, P, P, P, SZ, P]),
+            "sfi_pages_release": (C.c_int, [KV, PP, P, P]),
+            "sfi_pages_evict": (C.c_int, [KV, PP, I32, I32, P, P]),
+            "sfi_pages_compact": (C.c_int, [KV, PP, P, P, SZ, P]),
+            "sfi_append_chunk": (C.c_int, [KV, P, P, P, I32, I32, P, P]),
+            "sfi_window_attn": (C.c_int, [KV, P, P, I32, P, I32, I32, I32, I32, P, P, SZ, P]),
+            "sfi_window_workspace_bytes": (SZ, [KV, I32, I32, I32, I32]),
+            "sfi_reorder": (C.c_int, [KV, PP, BD, MEM, P, P]),
+            "sfi_beam_workspace_bytes": (SZ, [C.POINTER(SfiBeam)]),
+            "sfi_beam_select": (C.c_int, [C.POINTER(SfiBeam), P, SZ, P]),
         }
         for name, (res, args) in sig.items():
             f = getattr(l, name)
@@ -266,3 +297,87 @@ def sfi_test_inject_stall(on: bool = True):
     """Test hook: the next attention launch waits on a barrier that never completes, so its
     bounded waits give up and report SFI_DEVERR_TIMEOUT."""
     _check("sfi_test_inject_stall", lib().sfi_test_inject_stall(1 if on else 0))
+
+
+# ------------------------------------------------- pages, prompt chunks, beam search
+
+def _ref(x):
+    return None if x is None else C.byref(x)
+
+
+def sfi_pages_workspace_bytes(kv: SfiKvCache) -> int:
+    n = lib().sfi_pages_workspace_bytes(C.byref(kv))
+    if n == 0:
+        raise SfiError("sfi_pages_workspace_bytes", SFI_ERR_INVALID_ARG)
+    return n
+
+
+def sfi_pages_reserve(kv: SfiKvCache, pool: SfiPagePool, n_new, ws, ws_bytes: int, active=None,
+                      ok=None, stream=None):
+    """Make the next n_new[b] positions (None: one) of every sequence writable: missing pages,
+    and copies of pages that forks share. ok: optional uint8 [batch], 1 where that holds."""
+    _check("sfi_pages_reserve", lib().sfi_pages_reserve(
+        C.byref(kv), _ref(pool), _ptr(n_new), _ptr(active), _ptr(ok), _ptr(ws), ws_bytes,
+        _stream(stream)))
+
+
+def sfi_pages_release(kv: SfiKvCache, pool: SfiPagePool, active=None, stream=None):
+    _check("sfi_pages_release", lib().sfi_pages_release(C.byref(kv), _ref(pool), _ptr(active),
+                                                        _stream(stream)))
+
+
+def sfi_pages_evict(kv: SfiKvCache, pool: SfiPagePool, n_sink: int, n_window: int, active=None,
+                    stream=None):
+    """Give up the pages wholly outside the first n_sink positions and the recent window."""
+    _check("sfi_pages_evict", lib().sfi_pages_evict(C.byref(kv), _ref(pool), n_sink, n_window,
+                                                    _ptr(active), _stream(stream)))
+
+
+def sfi_pages_compact(kv: SfiKvCache, pool: SfiPagePool, n_used, ws, ws_bytes: int, stream=None):
+    """Move the pages in use to the front of the pool; n_used: int32 device scalar, their number."""
+    _check("sfi_pages_compact", lib().sfi_pages_compact(
+        C.byref(kv), _ref(pool), _ptr(n_used), _ptr(ws), ws_bytes, _stream(stream)))
+
+
+def sfi_append_chunk(kv: SfiKvCache, k_new, v_new, row_start, n_rows: int, max_rows: int,
+                     active=None, stream=None):
+    """Append several rows per sequence (packed; row_start None: one each)."""
+    _check("sfi_append_chunk", lib().sfi_append_chunk(
+        C.byref(kv), _ptr(k_new), _ptr(v_new), _ptr(row_start), n_rows, max_rows, _ptr(active),
+        _stream(stream)))
+
+
+def sfi_window_workspace_bytes(kv: SfiKvCache, n_rows: int, max_rows: int, n_sink: int,
+                               n_window: int) -> int:
+    n = lib().sfi_window_workspace_bytes(C.byref(kv), n_rows, max_rows, n_sink, n_window)
+    if n == 0:
+        raise SfiError("sfi_window_workspace_bytes", SFI_ERR_INVALID_ARG)
+    return n
+
+
+def sfi_window_attn(kv: SfiKvCache, q, out, out_fp32: bool, row_start, n_rows: int, max_rows: int,
+                    n_sink: int, n_window: int, ws, ws_bytes: int, active=None, stream=None):
+    """Attention of the sequences' last rows (packed; row_start None: one each) over the first
+    n_sink positions and a sliding window of n_window, straight from the cache."""
+    _check("sfi_window_attn", lib().sfi_window_attn(
+        C.byref(kv), _ptr(q), _ptr(out), 1 if out_fp32 else 0, _ptr(row_start), n_rows, max_rows,
+        n_sink, n_window, _ptr(active), _ptr(ws), ws_bytes, _stream(stream)))
+
+
+def sfi_reorder(kv: SfiKvCache, src, pool: SfiPagePool | None = None,
+                budget: SfiBudget | None = None, mem: SfiSparseMem | None = None, stream=None):
+    """Sequence b takes over the state of sequence src[b] (int32 device [batch])."""
+    _check("sfi_reorder", lib().sfi_reorder(C.byref(kv), _ref(pool), _ref(budget), _ref(mem),
+                                            _ptr(src), _stream(stream)))
+
+
+def sfi_beam_workspace_bytes(beam: SfiBeam) -> int:
+    n = lib().sfi_beam_workspace_bytes(C.byref(beam))
+    if n == 0:
+        raise SfiError("sfi_beam_workspace_bytes", SFI_ERR_INVALID_ARG)
+    return n
+
+
+def sfi_beam_select(beam: SfiBeam, ws, ws_bytes: int, stream=None):
+    _check("sfi_beam_select", lib().sfi_beam_select(C.byref(beam), _ptr(ws), ws_bytes,
+                                                    _stream(stream)))

@@ -8,108 +8,12 @@
 #include <cmath>
 #include <cstdint>
 #include <cstring>
-#include <mutex>
 
-#include "sfi.h"
-#include "sfi_internal.h"
+#include "api_common.h"
 
 using namespace sfi;
 
 namespace {
-
-typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
-                                  const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
-                                  const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn()
-{
-    static EncodeTiledFn fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void *p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000,
-                                             cudaEnableDefault, &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<EncodeTiledFn>(p);
-    });
-    return fn;
-}
-
-// 2-D bf16 view [rows][128] with 256-byte rows; box = 64 columns x box_rows rows, 128-byte
-// swizzle (the canonical K-major / MN-major operand layout of the UMMA descriptors).
-bool make_map(CUtensorMap *m, const void *base, uint64_t rows, uint32_t box_rows)
-{
-    EncodeTiledFn fn = encode_fn();
-    if (!fn || rows == 0)
-        return false;
-    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(kHeadDim), rows};
-    const cuuint64_t strides[1] = {kHeadDim * 2};
-    const cuuint32_t box[2] = {64, box_rows};
-    const cuuint32_t estr[2] = {1, 1};
-    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base), dims, strides, box,
-              estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-sfi_status check_kv(const sfi_kv_cache *kv)
-{
-    if (!kv || !kv->k || !kv->v || !kv->seq_len || !kv->err)
-        return SFI_ERR_INVALID_ARG;
-    if (kv->n_layers < 1 || kv->batch < 1 || kv->n_kv_heads < 1 || kv->n_q_heads < 1)
-        return SFI_ERR_INVALID_ARG;
-    if (kv->head_dim != kHeadDim || kv->batch > kMaxBatch)
-        return SFI_ERR_UNSUPPORTED;
-    if (kv->n_q_heads % kv->n_kv_heads != 0)
-        return SFI_ERR_INVALID_ARG;
-    const int g = kv->n_q_heads / kv->n_kv_heads;
-    if (g != 1 && g != 2 && g != 4 && g != 8)
-        return SFI_ERR_UNSUPPORTED;
-    if (!aligned16(kv->k) || !aligned16(kv->v))
-        return SFI_ERR_INVALID_ARG;
-    if (kv->max_len < 0 || kv->capacity < 1)
-        return SFI_ERR_INVALID_ARG;
-    if (kv->page_size != 0) {
-        if (kv->page_size != 16)
-            return SFI_ERR_UNSUPPORTED;
-        if (!kv->page_table || kv->n_pages < 1 || kv->max_pages_per_seq < 1 ||
-            kv->capacity != kv->max_pages_per_seq * kv->page_size)
-            return SFI_ERR_INVALID_ARG;
-    }
-    if (kv->max_len > kv->capacity)
-        return SFI_ERR_CAPACITY;
-    const long long units = 1LL * kv->n_layers * kv->batch * kv->n_kv_heads;
-    const long long rows = kv->page_size ? 1LL * kv->n_layers * kv->n_pages * kv->n_kv_heads * 16
-                                         : units * kv->capacity;
-    if (units > 65535 || rows >= (1LL << 31))
-        return SFI_ERR_UNSUPPORTED;
-    return SFI_OK;
-}
-
-sfi_status check_budget(const sfi_budget *bd)
-{
-    if (!bd || bd->n_sink < 0 || bd->n_window < 1 || bd->n_select < 0 || bd->prior_tau < 1)
-        return SFI_ERR_INVALID_ARG;
-    if ((bd->prior_tau & (bd->prior_tau - 1)) != 0 || !(bd->lambda >= 0.0 && bd->lambda <= 1.0))
-        return SFI_ERR_INVALID_ARG;
-    if (bd->n_sink + bd->n_select < 1)
-        return SFI_ERR_INVALID_ARG;
-    return SFI_OK;
-}
-
-int sm_count()
-{
-    int dev = 0, n = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-        return 0;
-    return n;
-}
-
-size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
 struct WsLayout {
     size_t tickets_dense, tickets_sparse, append_ctr, append_ctr_dense, stats, part_dense,
@@ -135,8 +39,6 @@ WsLayout ws_layout(const sfi_kv_cache *kv, int sms)
     return w;
 }
 
-cudaStream_t as_stream(void *s) { return static_cast<cudaStream_t>(s); }
-
 // Timing events: recorded as external event nodes while the stream is being captured
 // (so graph replays time the kernel), as plain records otherwise.
 cudaError_t record_event(cudaEvent_t e, cudaStream_t s)
@@ -148,8 +50,6 @@ cudaError_t record_event(cudaEvent_t e, cudaStream_t s)
     return cudaEventRecordWithFlags(e, s, cs == cudaStreamCaptureStatusActive ? cudaEventRecordExternal
                                                                               : cudaEventRecordDefault);
 }
-
-sfi_status launch_status(cudaError_t e) { return e == cudaSuccess ? SFI_OK : SFI_ERR_CUDA; }
 
 // One-shot test hook of sfi_test_inject_stall: consumed by the next attention launch.
 std::atomic<int> g_test_stall{0};
@@ -171,13 +71,6 @@ void fill_common(AttnParams &p, const sfi_kv_cache *kv, const uint8_t *active)
     p.active = active;
     p.err = kv->err;
     p.scale_log2 = static_cast<float>(1.4426950408889634074 / std::sqrt(static_cast<double>(kHeadDim)));
-}
-
-uint64_t cache_rows(const sfi_kv_cache *kv)
-{
-    if (kv->page_size)
-        return static_cast<uint64_t>(kv->n_layers) * kv->n_pages * kv->n_kv_heads * kv->page_size;
-    return static_cast<uint64_t>(kv->n_layers) * kv->batch * kv->n_kv_heads * kv->capacity;
 }
 
 // ws_kv/unit0: the descriptor whose workspace layout `ws` follows and the first of its units

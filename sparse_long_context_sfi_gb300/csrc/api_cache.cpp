@@ -1,0 +1,353 @@
+// api_cache.cpp -- the extern "C" entry points of include/sfi.h that keep the cache around the
+// decode path: pages, prompt chunks and their attention, beam search. Argument checks,
+// workspace layout and launches; no allocation, no synchronisation.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cstring>
+
+#include "api_common.h"
+
+using namespace sfi;
+
+namespace {
+
+bool misaligned256(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 255u) != 0; }
+
+PageParams page_params(const sfi_kv_cache *kv, int32_t *table, int32_t *refs, const uint8_t *active)
+{
+    PageParams p;
+    p.batch = kv->batch;
+    p.n_kv_heads = kv->n_kv_heads;
+    p.capacity = kv->capacity;
+    p.page_size = kv->page_size;
+    p.n_pages = kv->n_pages;
+    p.max_pages = kv->max_pages_per_seq;
+    p.max_len = kv->max_len;
+    p.table = table;
+    p.refs = refs;
+    p.seq_len = kv->seq_len;
+    p.active = active;
+    p.err = kv->err;
+    return p;
+}
+
+// The table is written through the pool, so it must be the one that the cache reads.
+sfi_status check_pool(const sfi_kv_cache *kv, const sfi_page_pool *pool)
+{
+    const sfi_status st = check_kv(kv);
+    if (st != SFI_OK)
+        return st;
+    if (kv->page_size == 0 || !pool || !pool->page_table || !pool->refs ||
+        pool->page_table != kv->page_table)
+        return SFI_ERR_INVALID_ARG;
+    return SFI_OK;
+}
+
+size_t page_scratch(const sfi_kv_cache *kv, char *base, PageScratch *s)
+{
+    const size_t pages = static_cast<size_t>(kv->n_pages) * sizeof(int32_t);
+    const int words = (kv->max_pages_per_seq + 31) / 32;
+    size_t o = 0;
+    auto take = [&](size_t bytes) {
+        char *at = base + o;
+        o = align256(o + bytes);
+        return static_cast<void *>(at);
+    };
+    s->list = static_cast<int32_t *>(take(pages));
+    s->movers = static_cast<int32_t *>(take(pages));
+    s->remap = static_cast<int32_t *>(take(pages));
+    s->n_moves = static_cast<int32_t *>(take(sizeof(int32_t)));
+    s->marks = static_cast<uint32_t *>(take(static_cast<size_t>(kv->batch) * words * sizeof(uint32_t)));
+    s->copies = static_cast<int4 *>(take(static_cast<size_t>(kv->batch) * sizeof(int4)));
+    s->words = words;
+    return o;
+}
+
+sfi_status check_ws(void *ws, size_t ws_bytes, size_t need)
+{
+    return !ws || ws_bytes < need || misaligned256(ws) ? SFI_ERR_WORKSPACE : SFI_OK;
+}
+
+// Rows of a chunk: row_start NULL means one row per sequence.
+sfi_status check_rows(const sfi_kv_cache *kv, const int32_t *row_start, int32_t n_rows,
+                      int32_t max_rows)
+{
+    if (n_rows < 0 || max_rows < 0 || (!row_start && n_rows != kv->batch) ||
+        (!row_start && max_rows < 1))
+        return SFI_ERR_INVALID_ARG;
+    if (1LL * n_rows * kv->n_q_heads * kv->n_layers >= (1LL << 31))
+        return SFI_ERR_UNSUPPORTED;
+    return SFI_OK;
+}
+
+sfi_status check_beam(const sfi_beam *b)
+{
+    if (!b || b->n_groups < 1 || b->n_beams < 1 || b->vocab < 1 || b->row_stride < b->vocab ||
+        b->eos >= b->vocab)
+        return SFI_ERR_INVALID_ARG;
+    if (b->n_beams > kMaxBeams || 1LL * b->n_groups * b->n_beams > 65535 ||
+        1LL * b->vocab * b->n_beams >= (1LL << 31))
+        return SFI_ERR_UNSUPPORTED;
+    return SFI_OK;
+}
+
+// Slices of a row: enough CTAs for about two per SM, at least 2048 tokens each.
+int beam_splits(const sfi_beam *b)
+{
+    const int rows = b->n_groups * b->n_beams, sms = sm_count();
+    int s = (2 * sms + rows - 1) / rows;
+    const int most = (b->vocab + 2047) / 2048;
+    s = s < most ? s : most;
+    return s < 1 ? 1 : s > 64 ? 64 : s;
+}
+
+size_t beam_scratch(const sfi_beam *b, char *base, BeamParams *p)
+{
+    const size_t rows = static_cast<size_t>(b->n_groups) * b->n_beams;
+    size_t o = 0;
+    auto take = [&](size_t bytes) {
+        char *at = base + o;
+        o = align256(o + bytes);
+        return static_cast<void *>(at);
+    };
+    p->splits = beam_splits(b);
+    p->tickets = static_cast<int *>(take(b->n_groups * sizeof(int)));
+    p->part_stat = static_cast<float2 *>(take(rows * p->splits * sizeof(float2)));
+    p->part_x = static_cast<float *>(take(rows * p->splits * b->n_beams * sizeof(float)));
+    p->part_v = static_cast<int32_t *>(take(rows * p->splits * b->n_beams * sizeof(int32_t)));
+    return o;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t sfi_pages_workspace_bytes(const sfi_kv_cache *kv)
+{
+    if (check_kv(kv) != SFI_OK || kv->page_size == 0)
+        return 0;
+    PageScratch s;
+    return page_scratch(kv, nullptr, &s);
+}
+
+sfi_status sfi_pages_reserve(const sfi_kv_cache *kv, const sfi_page_pool *pool,
+                             const int32_t *n_new, const uint8_t *active, uint8_t *ok, void *ws,
+                             size_t ws_bytes, void *stream)
+{
+    sfi_status st = check_pool(kv, pool);
+    if (st != SFI_OK)
+        return st;
+    PageScratch s;
+    if ((st = check_ws(ws, ws_bytes, page_scratch(kv, static_cast<char *>(ws), &s))) != SFI_OK)
+        return st;
+    return launch_status(launch_reserve(page_params(kv, pool->page_table, pool->refs, active), n_new,
+                                        ok, s, kv->k, kv->v, kv->n_layers, as_stream(stream)));
+}
+
+sfi_status sfi_pages_release(const sfi_kv_cache *kv, const sfi_page_pool *pool,
+                             const uint8_t *active, void *stream)
+{
+    const sfi_status st = check_pool(kv, pool);
+    if (st != SFI_OK)
+        return st;
+    return launch_status(launch_drop_pages(page_params(kv, pool->page_table, pool->refs, active), 0,
+                                           0, 0, as_stream(stream)));
+}
+
+sfi_status sfi_pages_evict(const sfi_kv_cache *kv, const sfi_page_pool *pool, int32_t n_sink,
+                           int32_t n_window, const uint8_t *active, void *stream)
+{
+    const sfi_status st = check_pool(kv, pool);
+    if (st != SFI_OK)
+        return st;
+    if (n_sink < 0 || n_window < 1)
+        return SFI_ERR_INVALID_ARG;
+    return launch_status(launch_drop_pages(page_params(kv, pool->page_table, pool->refs, active), 1,
+                                           n_sink, n_window, as_stream(stream)));
+}
+
+sfi_status sfi_pages_compact(const sfi_kv_cache *kv, const sfi_page_pool *pool, int32_t *n_used,
+                             void *ws, size_t ws_bytes, void *stream)
+{
+    sfi_status st = check_pool(kv, pool);
+    if (st != SFI_OK)
+        return st;
+    if (!n_used)
+        return SFI_ERR_INVALID_ARG;
+    PageScratch s;
+    if ((st = check_ws(ws, ws_bytes, page_scratch(kv, static_cast<char *>(ws), &s))) != SFI_OK)
+        return st;
+    const int sms = sm_count();
+    if (sms <= 0)
+        return SFI_ERR_CUDA;
+    return launch_status(launch_pages_compact(page_params(kv, pool->page_table, pool->refs, nullptr),
+                                              n_used, s, kv->k, kv->v, kv->n_layers, sms * 8,
+                                              as_stream(stream)));
+}
+
+sfi_status sfi_append_chunk(const sfi_kv_cache *kv, const void *k_new, const void *v_new,
+                            const int32_t *row_start, int32_t n_rows, int32_t max_rows,
+                            const uint8_t *active, void *stream)
+{
+    sfi_status st = check_kv(kv);
+    if (st != SFI_OK)
+        return st;
+    if ((st = check_rows(kv, row_start, n_rows, max_rows)) != SFI_OK)
+        return st;
+    if (n_rows == 0)
+        return SFI_OK;
+    if (!k_new || !v_new || !aligned16(k_new) || !aligned16(v_new))
+        return SFI_ERR_INVALID_ARG;
+    ChunkParams p;
+    p.pg = page_params(kv, const_cast<int32_t *>(kv->page_table), nullptr, active);
+    p.row_start = row_start;
+    p.n_rows = n_rows;
+    p.max_rows = max_rows;
+    return launch_status(launch_append_chunk(p, k_new, v_new, kv->k, kv->v, kv->n_layers,
+                                             as_stream(stream)));
+}
+
+size_t sfi_window_workspace_bytes(const sfi_kv_cache *kv, int32_t n_rows, int32_t max_rows,
+                                  int32_t n_sink, int32_t n_window)
+{
+    if (check_kv(kv) != SFI_OK || n_rows < 0 || max_rows < 0 || n_sink < 0 || n_window < 1)
+        return 0;
+    return 256;
+}
+
+sfi_status sfi_window_attn(const sfi_kv_cache *kv, const void *q, void *out, int32_t out_fp32,
+                           const int32_t *row_start, int32_t n_rows, int32_t max_rows,
+                           int32_t n_sink, int32_t n_window, const uint8_t *active, void *ws,
+                           size_t ws_bytes, void *stream)
+{
+    sfi_status st = check_kv(kv);
+    if (st != SFI_OK)
+        return st;
+    if (n_sink < 0 || n_window < 1)
+        return SFI_ERR_INVALID_ARG;
+    if ((st = check_rows(kv, row_start, n_rows, max_rows)) != SFI_OK)
+        return st;
+    if ((st = check_ws(ws, ws_bytes, sfi_window_workspace_bytes(kv, n_rows, max_rows, n_sink,
+                                                                n_window))) != SFI_OK)
+        return st;
+    if (n_rows == 0 || max_rows == 0)
+        return SFI_OK;
+    if (!q || !out || !aligned16(q) || !aligned16(out))
+        return SFI_ERR_INVALID_ARG;
+    WindowParams p;
+    std::memset(&p, 0, sizeof p);
+    p.n_layers = kv->n_layers;
+    p.batch = kv->batch;
+    p.n_kv_heads = kv->n_kv_heads;
+    p.group = kv->n_q_heads / kv->n_kv_heads;
+    p.capacity = kv->capacity;
+    p.page_size = kv->page_size;
+    p.n_pages = kv->n_pages;
+    p.max_pages = kv->max_pages_per_seq;
+    p.max_len = kv->max_len;
+    p.page_table = kv->page_table;
+    p.seq_len = kv->seq_len;
+    p.active = active;
+    p.row_start = row_start;
+    p.n_rows = n_rows;
+    p.max_rows = max_rows;
+    p.n_sink = n_sink;
+    p.n_window = n_window;
+    p.q = q;
+    p.k = kv->k;
+    p.v = kv->v;
+    p.out = out;
+    p.out_fp32 = out_fp32 ? 1 : 0;
+    p.err = kv->err;
+    return launch_status(launch_window(p, as_stream(stream)));
+}
+
+sfi_status sfi_reorder(const sfi_kv_cache *kv, const sfi_page_pool *pool,
+                       const sfi_budget *budget, const sfi_sparse_mem *mem, const int32_t *src,
+                       void *stream)
+{
+    sfi_status st = kv && kv->page_size ? check_pool(kv, pool) : check_kv(kv);
+    if (st != SFI_OK)
+        return st;
+    if (!src || (kv->page_size == 0 && pool))
+        return SFI_ERR_INVALID_ARG;
+    if (mem) {
+        if ((st = check_budget(budget)) != SFI_OK)
+            return st;
+        if (!mem->kc || !mem->vc || !mem->sel_cnt || !mem->rows || !aligned16(mem->kc) ||
+            !aligned16(mem->vc) || (budget->n_select > 0 && !mem->sel_idx))
+            return SFI_ERR_INVALID_ARG;
+    }
+    ReorderParams p;
+    std::memset(&p, 0, sizeof p);
+    p.batch = kv->batch;
+    p.n_kv_heads = kv->n_kv_heads;
+    p.n_pages = kv->n_pages;
+    p.src = src;
+    p.err = kv->err;
+    auto part = [&](int i, int32_t *data, int layers, int cols, int32_t *refs) {
+        p.ints[i].data = data;
+        p.ints[i].cols = cols;
+        p.ints[i].slices = layers * ((cols + 31) / 32);
+        p.ints[i].refs = refs;
+    };
+    if (pool)
+        part(0, pool->page_table, 1, kv->max_pages_per_seq, pool->refs);
+    if (mem) {
+        if (budget->n_select > 0)
+            part(1, mem->sel_idx, kv->n_layers, kv->n_kv_heads * budget->n_select, nullptr);
+        part(2, mem->sel_cnt, kv->n_layers, kv->n_kv_heads, nullptr);
+        part(3, mem->rows, kv->n_layers, kv->n_kv_heads, nullptr);
+    }
+    part(4, kv->seq_len, 1, 1, nullptr);
+    cudaError_t e = cudaSuccess;
+    if (mem)
+        e = launch_reorder_rows(p, mem->kc, mem->vc, kv->n_layers, budget->n_sink + budget->n_select,
+                                mem->rows, 1, as_stream(stream));
+    if (e == cudaSuccess && kv->page_size == 0)
+        e = launch_reorder_rows(p, kv->k, kv->v, kv->n_layers, kv->capacity, kv->seq_len, 0,
+                                as_stream(stream));
+    if (e == cudaSuccess)
+        e = launch_reorder_ints(p, as_stream(stream));
+    return launch_status(e);
+}
+
+size_t sfi_beam_workspace_bytes(const sfi_beam *beam)
+{
+    if (check_beam(beam) != SFI_OK)
+        return 0;
+    BeamParams p;
+    return beam_scratch(beam, nullptr, &p);
+}
+
+sfi_status sfi_beam_select(const sfi_beam *beam, void *ws, size_t ws_bytes, void *stream)
+{
+    sfi_status st = check_beam(beam);
+    if (st != SFI_OK)
+        return st;
+    if (!beam->logits || !beam->cum || !beam->parent || !beam->token || !beam->cum_out ||
+        (beam->done && beam->eos < 0))
+        return SFI_ERR_INVALID_ARG;
+    BeamParams p;
+    std::memset(&p, 0, sizeof p);
+    if ((st = check_ws(ws, ws_bytes, beam_scratch(beam, static_cast<char *>(ws), &p))) != SFI_OK)
+        return st;
+    p.n_groups = beam->n_groups;
+    p.n_beams = beam->n_beams;
+    p.vocab = beam->vocab;
+    p.logits_fp32 = beam->logits_fp32 ? 1 : 0;
+    p.eos = beam->eos < 0 ? -1 : beam->eos;
+    p.row_stride = beam->row_stride;
+    p.logits = beam->logits;
+    p.cum = beam->cum;
+    p.done = beam->done;
+    p.rank_scale = beam->rank_scale;
+    p.parent = beam->parent;
+    p.token = beam->token;
+    p.cum_out = beam->cum_out;
+    p.done_out = beam->done_out;
+    return launch_status(launch_beam_select(p, as_stream(stream)));
+}
+
+}  // extern "C"

@@ -1,0 +1,660 @@
+// pages.cu -- upkeep of a paged KV cache on the device (page tables and reference counts), the
+// rows of a prompt chunk, and the reordering of whole sequences.
+//
+// Integer bookkeeping is done by one CTA per call where it needs an order (lowest free page
+// first), so that the result never depends on timing; everything that moves K and V bytes
+// runs on the whole GPU. A page of one layer and tensor is n_kv_heads * 4 KB, contiguous.
+//
+// Kernels here that write what a fast step may read before its own wait (packed memory, `ok`
+// masks) let no dependent start early; the others start theirs at entry.
+#include "sfi_device.cuh"
+
+namespace sfi {
+namespace {
+
+constexpr int kPlanThreads = 1024;
+constexpr uint32_t kFull = 0xffffffffu;
+
+// ------------------------------------------------------------------- release and eviction
+
+// Drops the references of the entries in columns [c0, c1) of each active sequence: all of them
+// (release) or the pages wholly between the sinks and the window (evict). Latency-bound: a
+// table row is a few KB.
+__global__ void __launch_bounds__(256) drop_pages_kernel(const PageParams p, int evict, int n_sink,
+                                                         int n_window)
+{
+    pdl_trigger();
+    pdl_wait();
+    const int b = blockIdx.y;
+    if (p.active && !p.active[b])
+        return;
+    const int c = blockIdx.x * 256 + threadIdx.x;
+    if (!evict && blockIdx.x == 0 && threadIdx.x == 0)
+        p.seq_len[b] = 0;
+    int c0 = 0, c1 = p.max_pages;
+    if (evict) {
+        const int dead = p.seq_len[b] - n_window;   // positions below it are out of the window
+        c0 = n_sink / 16 + (n_sink % 16 != 0);
+        c1 = dead > 0 ? min(dead / 16, p.max_pages) : 0;
+    }
+    if (c < c0 || c >= c1)
+        return;
+    int32_t *e = p.table + static_cast<size_t>(b) * p.max_pages + c;
+    const int page = *e;
+    if (page < 0)
+        return;
+    *e = -1;
+    if (page >= p.n_pages) {
+        raise_error(p.err, 0x1u);  // SFI_DEVERR_PAGE_RANGE
+    } else if (atomicSub(p.refs + page, 1) <= 0) {
+        atomicAdd(p.refs + page, 1);
+        raise_error(p.err, 0x80u);  // SFI_DEVERR_REFS
+    }
+}
+
+// ------------------------------------------------------------------------------- reserving
+
+// Sum over the block's 32 warps of `v` (one value per warp, from lane 0), as an exclusive
+// prefix per warp and the total; every thread calls it.
+__device__ __forceinline__ int warp_prefix(int v, int *sh, int &total)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (lane == 0)
+        sh[warp] = v;
+    __syncthreads();
+    int x = sh[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(kFull, x, o);
+        if (lane >= o)
+            x += y;
+    }
+    total = __shfl_sync(kFull, x, 31);
+    const int mine = __shfl_sync(kFull, x, warp) - v;
+    __syncthreads();
+    return mine;
+}
+
+// One CTA: (A) a warp per sequence marks the entries that need a page, (B) the lowest free
+// pages are listed, (C) a warp per sequence hands them out. The marks are kept because the
+// sharing rule reads other sequences' entries, which (C) changes.
+__global__ void __launch_bounds__(kPlanThreads) reserve_kernel(const PageParams p,
+                                                               const int32_t *n_new, uint8_t *ok,
+                                                               const PageScratch s)
+{
+    __shared__ int first[kMaxBatch], last[kMaxBatch], need[kMaxBatch], base[kMaxBatch];
+    __shared__ int sh[32], sh_total;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    pdl_wait();
+    for (int b = tid; b < p.batch; b += kPlanThreads) {
+        const bool on = !p.active || p.active[b];
+        const int L = p.seq_len[b], n = n_new ? n_new[b] : 1;
+        int f = 0, l = -1, state = on ? 0 : -1;
+        if (on && (L < 0 || L > p.max_len)) {
+            raise_error(p.err, 0x8u);  // SFI_DEVERR_LENGTH
+            state = -1;
+        } else if (on && n > 0) {
+            if (n > p.capacity - L) {
+                raise_error(p.err, 0x2u);  // SFI_DEVERR_CAPACITY
+                state = -1;
+            } else {
+                f = L >> 4;
+                l = (L + n - 1) >> 4;
+                const int e = (L & 15) ? p.table[static_cast<size_t>(b) * p.max_pages + f] : 0;
+                if (e < 0 || e >= p.n_pages) {
+                    raise_error(p.err, 0x1u);  // SFI_DEVERR_PAGE_RANGE
+                    state = -1;
+                    l = -1;
+                }
+            }
+        }
+        first[b] = f;
+        last[b] = l;
+        need[b] = state;
+    }
+    __syncthreads();
+    // (A)
+    for (int b = warp; b < p.batch; b += 32) {
+        const int32_t *row = p.table + static_cast<size_t>(b) * p.max_pages;
+        int count = 0;
+        for (int c0 = first[b]; c0 <= last[b]; c0 += 32) {
+            const int c = c0 + lane;
+            bool want = false;
+            if (c <= last[b]) {
+                const int e = row[c];
+                want = e < 0;
+                if (e >= p.n_pages) {
+                    raise_error(p.err, 0x1u);
+                    want = true;   // a bad entry ahead is replaced
+                } else if (e >= 0) {
+                    const int holders = p.refs[e];
+                    if (holders > 1) {
+                        int before = 0;
+                        for (int o = 0; o < b; ++o)
+                            before += (c >= first[o] && c <= last[o] &&
+                                       p.table[static_cast<size_t>(o) * p.max_pages + c] == e);
+                        want = holders - before > 1;
+                    }
+                }
+            }
+            const uint32_t m = __ballot_sync(kFull, want);
+            if (lane == 0)
+                s.marks[static_cast<size_t>(b) * s.words + ((c0 - first[b]) >> 5)] = m;
+            count += __popc(m);
+        }
+        if (lane == 0 && need[b] == 0)
+            need[b] = count;
+    }
+    __syncthreads();
+    if (warp == 0) {
+        int run = 0;
+        for (int b0 = 0; b0 < p.batch; b0 += 32) {
+            const int v = b0 + lane < p.batch ? max(0, need[b0 + lane]) : 0;
+            int x = v;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(kFull, x, o);
+                if (lane >= o)
+                    x += y;
+            }
+            if (b0 + lane < p.batch)
+                base[b0 + lane] = run + x - v;
+            run += __shfl_sync(kFull, x, 31);
+        }
+        if (lane == 0)
+            sh_total = run;
+    }
+    __syncthreads();
+    const int total = sh_total;
+    // (B) each warp takes 512 consecutive pages of a chunk of 16384
+    int found = 0;
+    for (int chunk = 0; chunk < p.n_pages && found < total; chunk += 16384) {
+        const int at = chunk + warp * 512 + lane;
+        uint32_t bits[16];
+        int mine = 0;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const int id = at + 32 * i;
+            bits[i] = __ballot_sync(kFull, id < p.n_pages && p.refs[id] == 0);
+            mine += __popc(bits[i]);
+        }
+        int sum;
+        int pos = found + warp_prefix(mine, sh, sum);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const int k = pos + __popc(bits[i] & ((1u << lane) - 1u));
+            if (((bits[i] >> lane) & 1u) && k < total)
+                s.list[k] = at + 32 * i;
+            pos += __popc(bits[i]);
+        }
+        found += sum;
+    }
+    __syncthreads();
+    // (C)
+    for (int b = warp; b < p.batch; b += 32) {
+        const bool fits = need[b] <= 0 || base[b] + need[b] <= found;
+        int4 copy = make_int4(0, 0, 0, 0);   // page to, page from, rows
+        if (need[b] > 0 && fits) {
+            int32_t *row = p.table + static_cast<size_t>(b) * p.max_pages;
+            int k = base[b];
+            const int rows = p.seq_len[b] & 15;
+            for (int c0 = first[b]; c0 <= last[b]; c0 += 32) {
+                const uint32_t m = s.marks[static_cast<size_t>(b) * s.words + ((c0 - first[b]) >> 5)];
+                if ((m >> lane) & 1u) {
+                    const int c = c0 + lane, old = row[c];
+                    const int page = s.list[k + __popc(m & ((1u << lane) - 1u))];
+                    row[c] = page;
+                    p.refs[page] = 1;
+                    if (old >= 0 && old < p.n_pages) {
+                        atomicSub(p.refs + old, 1);
+                        if (c == first[b])
+                            copy = make_int4(page, old, rows, 0);
+                    }
+                }
+                k += __popc(m);
+            }
+        }
+        if (lane == 0) {
+            if (!fits)
+                raise_error(p.err, 0x10u);  // SFI_DEVERR_POOL
+            s.copies[b] = copy;   // (lane 0 holds column first[b])
+            if (ok)
+                ok[b] = need[b] >= 0 && fits ? 1 : 0;
+        }
+    }
+}
+
+// The rows of the pages that reserve_kernel replaced: grid (batch, layers, K or V).
+__global__ void __launch_bounds__(256) copy_rows_kernel(const PageParams p, const PageScratch s,
+                                                        uint4 *k, uint4 *v)
+{
+    pdl_wait();
+    const int4 c = s.copies[blockIdx.x];
+    if (c.z == 0)
+        return;
+    uint4 *t = blockIdx.z ? v : k;
+    const size_t page = static_cast<size_t>(p.n_kv_heads) * 256, layer = blockIdx.y * (page * p.n_pages);
+    uint4 *to = t + layer + c.x * page;
+    const uint4 *from = t + layer + c.y * page;
+    const int n = c.z * 16;   // 16-byte pieces of one head's rows
+    for (int i = threadIdx.x; i < n * p.n_kv_heads; i += 256) {
+        const int at = (i / n) * 256 + i % n;
+        to[at] = from[at];
+    }
+}
+
+// ------------------------------------------------------------------------------ compaction
+
+// One CTA: U = pages in use, the free ids below U and the used ids from U on, both ascending,
+// paired; remap[id] is where a page ends up.
+__global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const PageParams p,
+                                                                    int32_t *n_used,
+                                                                    const PageScratch s)
+{
+    __shared__ int sh[32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    pdl_wait();
+    int used = 0, sum;
+    for (int id = tid; id < p.n_pages; id += kPlanThreads)
+        used += p.refs[id] != 0;
+    used = __reduce_add_sync(kFull, used);
+    warp_prefix(used, sh, sum);
+    const int U = sum;
+    int holes = 0, movers = 0;
+    for (int chunk = 0; chunk < p.n_pages; chunk += 16384) {
+        const int at = chunk + warp * 512 + lane;
+        uint32_t bits[16];
+        int mine = 0;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const int id = at + 32 * i;
+            const bool in = id < p.n_pages;
+            const bool full = in && p.refs[id] != 0;
+            if (in)
+                s.remap[id] = id;
+            // below U the free ids count, from U on the used ones
+            bits[i] = __ballot_sync(kFull, in && (id < U ? !full : full));
+            const uint32_t below = __ballot_sync(kFull, id < U);
+            mine += __popc(bits[i] & below) + (__popc(bits[i] & ~below) << 16);
+        }
+        // both counts of a chunk in one word: at most 16384 each
+        int pos = warp_prefix(mine, sh, sum);
+        int h = holes + (pos & 0xffff), m = movers + (pos >> 16);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const int id = at + 32 * i;
+            const uint32_t below = __ballot_sync(kFull, id < U);
+            const uint32_t hb = bits[i] & below, mb = bits[i] & ~below, lower = (1u << lane) - 1u;
+            if ((hb >> lane) & 1u)
+                s.list[h + __popc(hb & lower)] = id;
+            if ((mb >> lane) & 1u)
+                s.movers[m + __popc(mb & lower)] = id;
+            h += __popc(hb);
+            m += __popc(mb);
+        }
+        holes += sum & 0xffff;
+        movers += sum >> 16;
+    }
+    __syncthreads();
+    for (int i = tid; i < movers; i += kPlanThreads) {
+        const int from = s.movers[i], to = s.list[i];
+        s.remap[from] = to;
+        p.refs[to] = p.refs[from];
+        p.refs[from] = 0;
+    }
+    if (tid == 0) {
+        *n_used = U;
+        *s.n_moves = movers;
+    }
+}
+
+// Tables through the remap, and the moved pages: one 4 KB piece (a head's page) per warp step.
+__global__ void __launch_bounds__(256) compact_move_kernel(const PageParams p, const PageScratch s,
+                                                           uint4 *k, uint4 *v, int n_layers)
+{
+    pdl_wait();
+    const long long threads = static_cast<long long>(gridDim.x) * 256;
+    const long long t0 = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
+    const long long entries = static_cast<long long>(p.batch) * p.max_pages;
+    for (long long i = t0; i < entries; i += threads) {
+        const int e = p.table[i];
+        if (e >= p.n_pages)
+            raise_error(p.err, 0x1u);
+        else if (e >= 0)
+            p.table[i] = s.remap[e];
+    }
+    const int lane = threadIdx.x & 31;
+    const long long pieces = static_cast<long long>(*s.n_moves) * n_layers * 2 * p.n_kv_heads;
+    const size_t layer = static_cast<size_t>(p.n_pages) * p.n_kv_heads * 256;
+    for (long long w = t0 >> 5; w < pieces; w += threads >> 5) {
+        const int head = static_cast<int>(w % p.n_kv_heads);
+        long long r = w / p.n_kv_heads;
+        const int which = static_cast<int>(r & 1);
+        r >>= 1;
+        const int l = static_cast<int>(r % n_layers), i = static_cast<int>(r / n_layers);
+        uint4 *t = (which ? v : k) + l * layer;
+        const uint4 *from = t + (static_cast<size_t>(s.movers[i]) * p.n_kv_heads + head) * 256;
+        uint4 *to = t + (static_cast<size_t>(s.list[i]) * p.n_kv_heads + head) * 256;
+        uint4 x[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            x[j] = __ldcs(from + j * 32 + lane);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            __stcs(to + j * 32 + lane, x[j]);
+    }
+}
+
+// --------------------------------------------------------------------------- chunk appends
+
+// The sequence that owns packed row r: the last b with row_start[b] <= r. -1 behind the last.
+__device__ __forceinline__ int owner_of_row(const int32_t *start, int batch, int r)
+{
+    if (start == nullptr)
+        return r;
+    if (r < start[0] || r >= start[batch])
+        return -1;
+    int lo = 0, hi = batch;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (start[mid] <= r)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    return lo;
+}
+
+// Whether sequence b's chunk is sound: rows within bounds, room in the cache.
+__device__ __forceinline__ bool chunk_ok(const ChunkParams &p, int b, int &r0, int &n, int &L,
+                                         bool report)
+{
+    r0 = p.row_start ? p.row_start[b] : b;
+    const int r1 = p.row_start ? p.row_start[b + 1] : b + 1;
+    n = r1 - r0;
+    L = p.pg.seq_len[b];
+    uint32_t bad = 0;
+    if (r0 < 0 || n < 0 || r1 > p.n_rows || n > p.max_rows)
+        bad = 0x20u;  // SFI_DEVERR_ROWS
+    else if (L < 0 || L > p.pg.max_len)
+        bad = 0x8u;   // SFI_DEVERR_LENGTH
+    else if (n > p.pg.capacity - L)
+        bad = 0x2u;   // SFI_DEVERR_CAPACITY
+    if (bad && report)
+        raise_error(p.pg.err, bad);
+    return bad == 0;
+}
+
+constexpr int kChunkRows = 8;   // rows per CTA
+
+__global__ void __launch_bounds__(256) append_chunk_kernel(const ChunkParams p,
+                                                           const uint4 *__restrict__ k_new,
+                                                           const uint4 *__restrict__ v_new,
+                                                           uint4 *__restrict__ k,
+                                                           uint4 *__restrict__ v)
+{
+    __shared__ long long dst[kChunkRows];   // cache row of (layer 0, head 0), or -1
+    pdl_trigger();
+    pdl_wait();
+    const int r0 = blockIdx.x * kChunkRows, hkv = p.pg.n_kv_heads;
+    if (threadIdx.x < kChunkRows) {
+        const int r = r0 + threadIdx.x;
+        long long d = -1;
+        const int b = r < p.n_rows ? owner_of_row(p.row_start, p.pg.batch, r) : -1;
+        int s0, n, L;
+        if (b >= 0 && (!p.pg.active || p.pg.active[b]) && chunk_ok(p, b, s0, n, L, false) &&
+            r >= s0 && r < s0 + n) {
+            const int pos = L + r - s0;
+            if (p.pg.page_size == 0) {
+                d = static_cast<long long>(b) * hkv * p.pg.capacity + pos;
+            } else {
+                const int page = p.pg.table[static_cast<size_t>(b) * p.pg.max_pages + (pos >> 4)];
+                if (page >= 0 && page < p.pg.n_pages)
+                    d = static_cast<long long>(page) * hkv * 16 + (pos & 15);
+            }
+        }
+        dst[threadIdx.x] = d;
+    }
+    __syncthreads();
+    const int layer = blockIdx.y;
+    const long long head = p.pg.page_size ? 16 : p.pg.capacity;   // cache rows between heads
+    const long long base = static_cast<long long>(layer) *
+                           (p.pg.page_size ? static_cast<long long>(p.pg.n_pages) * hkv * 16
+                                           : static_cast<long long>(p.pg.batch) * hkv * p.pg.capacity);
+    const int per = hkv * 16;   // 16-byte pieces of one row of one tensor
+    for (int i = threadIdx.x; i < 2 * per; i += 256) {
+        const bool is_v = i >= per;
+        const int j = is_v ? i - per : i;
+        const uint4 *src = (is_v ? v_new : k_new) +
+                           (static_cast<size_t>(layer) * p.n_rows + r0) * per + j;
+        uint4 *to = (is_v ? v : k) + (base + (j >> 4) * head) * 16 + (j & 15);
+        uint4 x[kChunkRows];
+#pragma unroll
+        for (int q = 0; q < kChunkRows; ++q)
+            if (dst[q] >= 0)
+                x[q] = __ldg(src + static_cast<size_t>(q) * per);
+#pragma unroll
+        for (int q = 0; q < kChunkRows; ++q)
+            if (dst[q] >= 0)
+                to[dst[q] * 16] = x[q];
+    }
+}
+
+// The lengths after the rows: a warp per sequence, which first looks over the chunk's pages.
+__global__ void __launch_bounds__(1024) advance_kernel(const ChunkParams p)
+{
+    pdl_trigger();
+    pdl_wait();
+    const int lane = threadIdx.x & 31;
+    for (int b = threadIdx.x >> 5; b < p.pg.batch; b += 32) {
+        if (p.pg.active && !p.pg.active[b])
+            continue;
+        int s0, n, L;
+        if (!chunk_ok(p, b, s0, n, L, lane == 0))
+            continue;
+        bool good = true;
+        if (p.pg.page_size != 0 && n > 0) {
+            for (int c = (L >> 4) + lane; c <= (L + n - 1) >> 4; c += 32) {
+                const int e = p.pg.table[static_cast<size_t>(b) * p.pg.max_pages + c];
+                good = good && e >= 0 && e < p.pg.n_pages;
+            }
+        }
+        good = __all_sync(kFull, good);
+        __syncwarp();
+        if (lane == 0) {
+            if (good)
+                p.pg.seq_len[b] = L + n;
+            else
+                raise_error(p.pg.err, 0x1u);  // SFI_DEVERR_PAGE_RANGE
+        }
+    }
+}
+
+// -------------------------------------------------------------------------------- reorder
+
+// The sequences that move, in order: dst in mv[i].x, src in mv[i].y; returns their number.
+// Every thread of the block calls it (blocks of at least 32 threads).
+__device__ __forceinline__ int moved_list(const int32_t *src, int batch, int2 *mv, int *count,
+                                          uint32_t *err, bool report)
+{
+    if (threadIdx.x < 32) {
+        int n = 0;
+        for (int b0 = 0; b0 < batch; b0 += 32) {
+            const int b = b0 + static_cast<int>(threadIdx.x);
+            const int from = b < batch ? src[b] : b;
+            const bool bad = from < 0 || from >= batch;
+            if (bad && b < batch && report)
+                raise_error(err, 0x40u);  // SFI_DEVERR_SEQ
+            const bool go = b < batch && !bad && from != b;
+            const uint32_t m = __ballot_sync(kFull, go);
+            if (go)
+                mv[n + __popc(m & ((1u << threadIdx.x) - 1u))] = make_int2(b, from);
+            n += __popc(m);
+        }
+        if (threadIdx.x == 0)
+            *count = n;
+    }
+    __syncthreads();
+    return *count;
+}
+
+// Bulk rows: a [layers][batch][row16] matrix of 16-byte pieces whose rows (sequences) are
+// permuted in place. A CTA holds `cols` pieces of every moving sequence: it reads all of them
+// into shared memory, then writes them, so no other CTA and no scratch is involved. A piece
+// moves if its cache row is below the source's row count.
+__global__ void __launch_bounds__(256) reorder_rows_kernel(const ReorderParams p, uint4 *k, uint4 *v,
+                                                           long long row16, int rows_per_head,
+                                                           const int32_t *rows, int rows_by_unit,
+                                                           int cols)
+{
+    extern __shared__ uint4 stage[];
+    __shared__ int2 mv[kMaxBatch];
+    __shared__ int n_mv;
+    pdl_wait();
+    const int n = moved_list(p.src, p.batch, mv, &n_mv, p.err, false);
+    if (n == 0)
+        return;
+    const int layer = blockIdx.y;
+    uint4 *t = (blockIdx.z ? v : k) + static_cast<long long>(layer) * p.batch * row16;
+    const long long c0 = static_cast<long long>(blockIdx.x) * cols;
+    auto live = [&](int i, long long col) {
+        if (col >= row16)
+            return false;
+        const int r = static_cast<int>(col >> 4);
+        const int head = r / rows_per_head, at = r - head * rows_per_head;
+        const int from = mv[i].y;
+        const int have = rows_by_unit ? rows[(static_cast<long long>(layer) * p.batch + from) * p.n_kv_heads + head]
+                                      : rows[from];
+        return at < have;
+    };
+    for (int i = threadIdx.x; i < n * cols; i += 256) {
+        const int m = i / cols;
+        const long long col = c0 + (i - m * cols);
+        if (live(m, col))
+            stage[i] = t[mv[m].y * row16 + col];
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < n * cols; i += 256) {
+        const int m = i / cols;
+        const long long col = c0 + (i - m * cols);
+        if (live(m, col))
+            t[mv[m].x * row16 + col] = stage[i];
+    }
+}
+
+// The int32 matrices [layers][batch][cols] of a sequence's state, permuted the same way, 32
+// columns per CTA: page table (with its reference counts), selections, counts, lengths.
+__global__ void __launch_bounds__(256) reorder_ints_kernel(const ReorderParams p)
+{
+    extern __shared__ int held[];
+    __shared__ int2 mv[kMaxBatch];
+    __shared__ int n_mv;
+    pdl_wait();
+    const int n = moved_list(p.src, p.batch, mv, &n_mv, p.err, blockIdx.x == 0);
+    int part = 0, slice = blockIdx.x;
+    while (slice >= p.ints[part].slices)
+        slice -= p.ints[part++].slices;
+    const ReorderInts &a = p.ints[part];
+    const int per_layer = (a.cols + 31) / 32;
+    const int layer = slice / per_layer, c0 = (slice - layer * per_layer) * 32;
+    int32_t *t = a.data + static_cast<size_t>(layer) * p.batch * a.cols;
+    const int lane = threadIdx.x & 31, c = c0 + lane;
+    if (c < a.cols)
+        for (int i = threadIdx.x >> 5; i < n; i += 8)
+            held[i * 32 + lane] = t[static_cast<size_t>(mv[i].y) * a.cols + c];
+    __syncthreads();
+    if (c >= a.cols)
+        return;
+    for (int i = threadIdx.x >> 5; i < n; i += 8) {
+        int32_t *e = t + static_cast<size_t>(mv[i].x) * a.cols + c;
+        const int now = held[i * 32 + lane];
+        if (a.refs) {
+            const int was = *e;
+            if (was != now) {
+                if (now >= p.n_pages || was >= p.n_pages)
+                    raise_error(p.err, 0x1u);  // SFI_DEVERR_PAGE_RANGE
+                if (now >= 0 && now < p.n_pages)
+                    atomicAdd(a.refs + now, 1);
+                if (was >= 0 && was < p.n_pages)
+                    atomicSub(a.refs + was, 1);
+            }
+        }
+        *e = now;
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_drop_pages(const PageParams &p, int evict, int n_sink, int n_window,
+                              cudaStream_t stream)
+{
+    const cudaError_t e = launch_pdl(drop_pages_kernel, dim3((p.max_pages + 255) / 256, p.batch),
+                                     dim3(256), 0, stream, p, evict, n_sink, n_window);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+cudaError_t launch_reserve(const PageParams &p, const int32_t *n_new, uint8_t *ok,
+                           const PageScratch &s, void *k, void *v, int n_layers,
+                           cudaStream_t stream)
+{
+    cudaError_t e = launch_pdl(reserve_kernel, dim3(1), dim3(kPlanThreads), 0, stream, p, n_new, ok, s);
+    if (e == cudaSuccess)
+        e = launch_pdl(copy_rows_kernel, dim3(p.batch, n_layers, 2), dim3(256), 0, stream, p, s,
+                       static_cast<uint4 *>(k), static_cast<uint4 *>(v));
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+cudaError_t launch_pages_compact(const PageParams &p, int32_t *n_used, const PageScratch &s, void *k,
+                                 void *v, int n_layers, int grid, cudaStream_t stream)
+{
+    cudaError_t e = launch_pdl(compact_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, p, n_used, s);
+    if (e == cudaSuccess)
+        e = launch_pdl(compact_move_kernel, dim3(grid), dim3(256), 0, stream, p, s,
+                       static_cast<uint4 *>(k), static_cast<uint4 *>(v), n_layers);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+cudaError_t launch_append_chunk(const ChunkParams &p, const void *k_new, const void *v_new, void *k,
+                                void *v, int n_layers, cudaStream_t stream)
+{
+    cudaError_t e = cudaSuccess;
+    if (p.n_rows > 0)
+        e = launch_pdl(append_chunk_kernel, dim3((p.n_rows + kChunkRows - 1) / kChunkRows, n_layers),
+                       dim3(256), 0, stream, p, static_cast<const uint4 *>(k_new),
+                       static_cast<const uint4 *>(v_new), static_cast<uint4 *>(k),
+                       static_cast<uint4 *>(v));
+    if (e == cudaSuccess)
+        e = launch_pdl(advance_kernel, dim3(1), dim3(1024), 0, stream, p);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+cudaError_t launch_reorder_rows(const ReorderParams &p, void *k, void *v, int n_layers,
+                                int rows_per_head, const int32_t *rows, int rows_by_unit,
+                                cudaStream_t stream)
+{
+    const long long row16 = static_cast<long long>(p.n_kv_heads) * rows_per_head * 16;
+    // 16 to 256 columns, so that a CTA's shared memory stays at 32 KB (64 KB from batch 129 on)
+    int cols = 2048 / p.batch;
+    cols = cols > 256 ? 256 : cols < 16 ? 16 : cols & ~15;
+    const size_t smem = static_cast<size_t>(p.batch) * cols * sizeof(uint4);
+    cudaError_t e = cudaFuncSetAttribute(reorder_rows_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         kMaxBatch * 16 * static_cast<int>(sizeof(uint4)));
+    if (e == cudaSuccess)
+        e = launch_pdl(reorder_rows_kernel,
+                       dim3(static_cast<unsigned>((row16 + cols - 1) / cols), n_layers, 2), dim3(256),
+                       smem, stream, p, static_cast<uint4 *>(k), static_cast<uint4 *>(v), row16,
+                       rows_per_head, rows, rows_by_unit, cols);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+cudaError_t launch_reorder_ints(const ReorderParams &p, cudaStream_t stream)
+{
+    int slices = 0;
+    for (int i = 0; i < kReorderParts; ++i)
+        slices += p.ints[i].slices;
+    const cudaError_t e = launch_pdl(reorder_ints_kernel, dim3(slices), dim3(256),
+                                     static_cast<size_t>(p.batch) * 32 * sizeof(int), stream, p);
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace sfi

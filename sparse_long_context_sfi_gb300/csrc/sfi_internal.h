@@ -136,6 +136,100 @@ cudaError_t launch_compact(const void *k, const void *v, void *kc, void *vc,
                            int n_select, uint32_t *err, cudaStream_t stream,
                            int n_seq_active = 0);
 
+// ------------------------------------------------------------ pages, chunks, reordering
+
+struct PageParams {
+    int batch, n_kv_heads, capacity, page_size, n_pages, max_pages, max_len;
+    int32_t *table;             // [batch][max_pages]
+    int32_t *refs;              // [n_pages]
+    int32_t *seq_len;
+    const uint8_t *active;
+    uint32_t *err;
+};
+
+// Workspace of the calls that plan page moves.
+struct PageScratch {
+    int32_t *list;              // free pages, ascending [n_pages]
+    int32_t *movers;            // pages that move [n_pages]
+    int32_t *remap;             // where each page ends up [n_pages]
+    int32_t *n_moves;
+    uint32_t *marks;            // entries that need a page, bit per column [batch][words]
+    int4 *copies;               // page to, page from, rows [batch]
+    int words;
+};
+
+struct ChunkParams {
+    PageParams pg;
+    const int32_t *row_start;
+    int n_rows, max_rows;
+};
+
+struct ReorderInts {
+    int32_t *data;              // [layers][batch][cols]
+    int cols;
+    int slices;                 // CTAs: layers * ceil(cols / 32); 0 = absent
+    int32_t *refs;              // page table: its reference counts
+};
+constexpr int kReorderParts = 5;   // page table, sel_idx, sel_cnt, rows, seq_len
+struct ReorderParams {
+    int batch, n_kv_heads, n_pages;
+    const int32_t *src;
+    uint32_t *err;
+    ReorderInts ints[kReorderParts];
+};
+
+cudaError_t launch_drop_pages(const PageParams &p, int evict, int n_sink, int n_window,
+                              cudaStream_t stream);
+cudaError_t launch_reserve(const PageParams &p, const int32_t *n_new, uint8_t *ok,
+                           const PageScratch &s, void *k, void *v, int n_layers,
+                           cudaStream_t stream);
+cudaError_t launch_pages_compact(const PageParams &p, int32_t *n_used, const PageScratch &s, void *k,
+                                 void *v, int n_layers, int grid, cudaStream_t stream);
+cudaError_t launch_append_chunk(const ChunkParams &p, const void *k_new, const void *v_new, void *k,
+                                void *v, int n_layers, cudaStream_t stream);
+cudaError_t launch_reorder_rows(const ReorderParams &p, void *k, void *v, int n_layers,
+                                int rows_per_head, const int32_t *rows, int rows_by_unit,
+                                cudaStream_t stream);
+cudaError_t launch_reorder_ints(const ReorderParams &p, cudaStream_t stream);
+
+// ------------------------------------------------------------------------------ beam search
+
+constexpr int kMaxBeams = 16;
+
+struct BeamParams {
+    int n_groups, n_beams, vocab, logits_fp32, eos, splits;
+    long long row_stride;
+    const void *logits;
+    const float *cum;
+    const uint8_t *done;
+    const float *rank_scale;
+    int32_t *parent, *token;
+    float *cum_out;
+    uint8_t *done_out;
+    int *tickets;               // [n_groups], zero between launches
+    float2 *part_stat;          // [rows][splits]: maximum, sum of exp(x - maximum)
+    float *part_x;              // [rows][splits][n_beams] best logits, descending
+    int32_t *part_v;            // and their tokens (-1: none)
+};
+cudaError_t launch_beam_select(const BeamParams &p, cudaStream_t stream);
+
+// --------------------------------------------------------- attention with sinks and a window
+
+struct WindowParams {
+    int n_layers, batch, n_kv_heads, group;
+    int capacity, page_size, n_pages, max_pages, max_len;
+    const int32_t *page_table;
+    const int32_t *seq_len;
+    const uint8_t *active;
+    const int32_t *row_start;
+    int n_rows, max_rows, n_sink, n_window;
+    const void *q, *k, *v;
+    void *out;
+    int out_fp32;
+    uint32_t *err;
+};
+cudaError_t launch_window(const WindowParams &p, cudaStream_t stream);
+
 size_t attention_smem_bytes();
 // Fast-step attention with its split-KV scratch in a library-owned device array instead of
 // a caller workspace (see sfi_sparse_decode_attn_static). p.partials and p.tickets are
