@@ -4,6 +4,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <cmath>
 #include <cstring>
 
 #include "api_common.h"
@@ -79,6 +80,53 @@ sfi_status check_rows(const sfi_kv_cache *kv, const int32_t *row_start, int32_t 
     if (1LL * n_rows * kv->n_q_heads * kv->n_layers >= (1LL << 31))
         return SFI_ERR_UNSUPPORTED;
     return SFI_OK;
+}
+
+// How sfi_window_attn runs with n_qtiles (1 or 2) 128-row q tiles per CTA.
+struct WindowShape {
+    int rows, slots;        // operand rows per item; CTAs that are resident at once
+    long long items;        // bound of the items before splitting
+    long long most_split;   // splits of an item that fill the slots
+    int part_rows;
+};
+
+WindowShape window_shape(const sfi_kv_cache *kv, int n_rows, int max_rows, int n_qtiles)
+{
+    WindowShape s;
+    const int g = kv->n_q_heads / kv->n_kv_heads, sms = sm_count();
+    s.rows = 128 * n_qtiles;
+    s.slots = n_qtiles == 2 ? sms : 2 * sms;
+    const long long seqs = n_rows < kv->batch ? n_rows : kv->batch;
+    const long long units = 1LL * kv->n_kv_heads * kv->n_layers;
+    s.items = (1LL * n_rows * g / s.rows + seqs) * units;
+    long long likely = (1LL * n_rows * g + s.rows - 1) / s.rows;
+    likely = (likely > seqs ? likely : seqs) * units;
+    const long long split = likely > 0 ? s.slots / likely : 1;
+    s.most_split = split < 1 ? 1 : split > 64 ? 64 : split;
+    s.part_rows = static_cast<int>(1LL * max_rows * g < s.rows ? 1LL * max_rows * g : s.rows);
+    return s;
+}
+
+// Sized for either q tile count and any split, so that it holds for every max_len and window.
+size_t window_scratch(const sfi_kv_cache *kv, int n_rows, int max_rows, char *base, WindowParams *p)
+{
+    size_t o = 0, items = 1, parts = 1;
+    for (int q = 1; q <= 2; ++q) {
+        const WindowShape s = window_shape(kv, n_rows, max_rows, q);
+        const size_t n = s.most_split > 1 ? static_cast<size_t>(s.items) : 1;
+        const size_t m = s.most_split > 1 ? n * s.most_split * s.part_rows : 1;
+        items = n > items ? n : items;
+        parts = m > parts ? m : parts;
+    }
+    auto take = [&](size_t bytes) {
+        char *at = base + o;
+        o = align256(o + bytes);
+        return static_cast<void *>(at);
+    };
+    p->tickets = static_cast<int *>(take(items * sizeof(int)));
+    p->part_ml = static_cast<float2 *>(take(parts * sizeof(float2)));
+    p->parts = static_cast<float *>(take(parts * kHeadDim * sizeof(float)));
+    return o;
 }
 
 sfi_status check_beam(const sfi_beam *b)
@@ -213,7 +261,8 @@ size_t sfi_window_workspace_bytes(const sfi_kv_cache *kv, int32_t n_rows, int32_
 {
     if (check_kv(kv) != SFI_OK || n_rows < 0 || max_rows < 0 || n_sink < 0 || n_window < 1)
         return 0;
-    return 256;
+    WindowParams p;
+    return window_scratch(kv, n_rows, max_rows, nullptr, &p);
 }
 
 sfi_status sfi_window_attn(const sfi_kv_cache *kv, const void *q, void *out, int32_t out_fp32,
@@ -228,15 +277,21 @@ sfi_status sfi_window_attn(const sfi_kv_cache *kv, const void *q, void *out, int
         return SFI_ERR_INVALID_ARG;
     if ((st = check_rows(kv, row_start, n_rows, max_rows)) != SFI_OK)
         return st;
-    if ((st = check_ws(ws, ws_bytes, sfi_window_workspace_bytes(kv, n_rows, max_rows, n_sink,
-                                                                n_window))) != SFI_OK)
+    WindowParams p;
+    std::memset(&p, 0, sizeof p);
+    if ((st = check_ws(ws, ws_bytes, window_scratch(kv, n_rows, max_rows, static_cast<char *>(ws), &p))) !=
+        SFI_OK)
         return st;
     if (n_rows == 0 || max_rows == 0)
         return SFI_OK;
     if (!q || !out || !aligned16(q) || !aligned16(out))
         return SFI_ERR_INVALID_ARG;
-    WindowParams p;
-    std::memset(&p, 0, sizeof p);
+    CUtensorMap tk, tv, tq;
+    if (!make_map(&tk, kv->k, cache_rows(kv), 16u) || !make_map(&tv, kv->v, cache_rows(kv), 16u) ||
+        !make_chunk_map(&tq, q, static_cast<uint64_t>(kv->n_layers) * n_rows,
+                        static_cast<uint32_t>(kv->n_q_heads),
+                        static_cast<uint32_t>(kv->n_q_heads / kv->n_kv_heads)))
+        return SFI_ERR_CUDA;
     p.n_layers = kv->n_layers;
     p.batch = kv->batch;
     p.n_kv_heads = kv->n_kv_heads;
@@ -254,13 +309,25 @@ sfi_status sfi_window_attn(const sfi_kv_cache *kv, const void *q, void *out, int
     p.max_rows = max_rows;
     p.n_sink = n_sink;
     p.n_window = n_window;
-    p.q = q;
-    p.k = kv->k;
-    p.v = kv->v;
     p.out = out;
     p.out_fp32 = out_fp32 ? 1 : 0;
     p.err = kv->err;
-    return launch_status(launch_window(p, as_stream(stream)));
+    const int g = p.group;
+    const long long len = kv->max_len, reach = n_window < len ? n_window : len;
+    const int qtiles = 1LL * max_rows * g > 128 && reach >= 512 ? 2 : 1;
+    const WindowShape s = window_shape(kv, n_rows, max_rows, qtiles);
+    // Fewer items than CTAs that fit: split their keys, four tiles at least to a split.
+    const int kt = qtiles == 2 ? 128 : 64;
+    const long long span = reach + s.rows / g < len ? reach + s.rows / g : len;
+    const long long tiles = (span + n_sink + 32 + kt - 1) / kt;
+    long long split = s.most_split < tiles / 4 ? s.most_split : tiles / 4;
+    split = split < 1 ? 1 : split;
+    p.n_split = static_cast<int>(split);
+    p.part_rows = s.part_rows;
+    const long long all = s.items * split;
+    const int grid = static_cast<int>(all < s.slots ? all : s.slots);
+    p.scale_log2 = static_cast<float>(1.4426950408889634074 / std::sqrt(static_cast<double>(kHeadDim)));
+    return launch_status(launch_window(p, qtiles, tk, tv, tq, grid, as_stream(stream)));
 }
 
 sfi_status sfi_reorder(const sfi_kv_cache *kv, const sfi_page_pool *pool,

@@ -223,12 +223,20 @@ struct WindowParams {
     const uint8_t *active;
     const int32_t *row_start;
     int n_rows, max_rows, n_sink, n_window;
-    const void *q, *k, *v;
     void *out;
     int out_fp32;
     uint32_t *err;
+    float scale_log2;           // log2(e) / sqrt(128)
+    int n_split;                // items that an item's key tiles are split over
+    int part_rows;              // operand rows kept per item and split
+    int *tickets;               // [items], zero between launches
+    float *parts;               // [items][n_split][part_rows][128] unnormalised outputs
+    float2 *part_ml;            // [items][n_split][part_rows] maximum (scaled by nothing), sum
 };
-cudaError_t launch_window(const WindowParams &p, cudaStream_t stream);
+// n_qtiles: 128-row q tiles per CTA, 1 (two CTAs per SM) or 2.
+cudaError_t launch_window(const WindowParams &p, int n_qtiles, const CUtensorMap &tm_k,
+                          const CUtensorMap &tm_v, const CUtensorMap &tm_q, int grid,
+                          cudaStream_t stream);
 
 size_t attention_smem_bytes();
 // Fast-step attention with its split-KV scratch in a library-owned device array instead of

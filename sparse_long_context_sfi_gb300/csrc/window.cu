@@ -1,112 +1,758 @@
 // window.cu -- attention of a chunk of rows under sinks and a sliding window, straight from
-// the cache: one warp per (row, query head), online softmax over the visible positions.
+// the cache (contiguous or paged), on the tcgen05 tensor cores.
+//
+// A row at position i of query head h sees keys j <= i with j < n_sink or j > i - n_window:
+//     z_ij = q_i . k_j / sqrt(128),  o_i = sum_j exp(z_ij - m_i) v_j / sum_j exp(z_ij - m_i).
+//
+// An item is 128 * NQ operand rows of one (layer, sequence, kv head): 128 NQ / G positions of
+// all G query heads that share the head's keys, so one read of a K/V row serves the group.
+// The keys that any of its rows sees are a list of 16-position blocks (a cache page each):
+// the sink blocks, then the blocks of the joint window; a tile is KT / 16 consecutive entries
+// of the list, so few sinks share a tile with the window instead of costing one.
+//
+// One CTA, roles by warp:
+//   0      TMA: the item's queries, then K and V of every tile (16-row boxes)
+//   1      MMA: S = Q K^T and O += P V per q tile (M = 128), P read from tensor memory
+//   2      zeroes the V rows of a landed tile that no row of the item may see (a zero weight
+//          would not cancel a NaN)
+//   4-7    softmax of q tile 0, one row per thread; 8-11 of q tile 1
+// Tensor memory: per q tile NS score buffers of KT columns, each overwritten by its weights,
+// and 128 columns of O. The running maximum is only moved (and O rescaled) when it grows by
+// more than 2^8, so that most tiles leave O alone; weights up to 2^8 are as exact in floating
+// point as weights up to 1.
+//
+// Few rows and a long window: the tiles of an item are split over n_split items, whose
+// unnormalised outputs, maxima and sums the last one to finish joins, in split order.
 #include "sfi_device.cuh"
 
 #include <math_constants.h>
 
+#include <cstddef>
+
 namespace sfi {
 namespace {
 
-__global__ void __launch_bounds__(256) window_simple_kernel(const WindowParams p)
+__device__ __forceinline__ float ex2_approx(float x)
 {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// 32 tensor-memory columns of this thread's lane; the values are there after tmem_landed.
+__device__ __forceinline__ void tmem_ld32(uint32_t addr, float *v)
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+        "%12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, "
+        "%30, %31}, [%32];"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]),
+          "=f"(v[7]), "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]),
+          "=f"(v[14]), "=f"(v[15]), "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]),
+          "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]),
+          "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+        : "r"(addr)
+        : "memory");
+}
+
+// Wait for this thread's tensor-memory loads. The loaded values go through the statement, so
+// that no use of them can be scheduled before it.
+__device__ __forceinline__ void tmem_landed(float *v)
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]),
+                   "+f"(v[7]), "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]),
+                   "+f"(v[13]), "+f"(v[14]), "+f"(v[15]), "+f"(v[16]), "+f"(v[17]), "+f"(v[18]),
+                   "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]), "+f"(v[24]),
+                   "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29])
+                 :
+                 : "memory");
+    asm volatile("" : "+f"(v[30]), "+f"(v[31]) : : "memory");
+}
+
+__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t *v)
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+        "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, "
+        "%29, %30, %31};" ::"r"(v[0]),
+        "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]),
+        "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]),
+        "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]),
+        "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]), "r"(v[30]),
+        "r"(v[31]), "r"(addr)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_st_wait()
+{
+    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// D[tmem] (+)= A[tmem] * B[smem], bf16 inputs, fp32 accumulate; one thread issues.
+__device__ __forceinline__ void umma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                             uint32_t idesc, uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+__device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, uint64_t *bar, int x,
+                                            int y, int z)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+        : "memory");
+}
+
+// Bits [lo, hi) of word w of a column mask (columns 32 w .. 32 w + 31).
+__device__ __forceinline__ uint32_t span_bits(int lo, int hi, int w)
+{
+    const int a = min(max(lo - 32 * w, 0), 32), b = min(max(hi - 32 * w, 0), 32);
+    if (b <= a)
+        return 0u;
+    return (b == 32 ? 0xffffffffu : ((1u << b) - 1u)) & ~((1u << a) - 1u);
+}
+
+constexpr int kMaxStages = 4;
+
+struct WCtrl {
+    uint64_t kf[kMaxStages], ke[kMaxStages], vf[kMaxStages], vr[kMaxStages], ve[kMaxStages];
+    uint64_t qf, qe;
+    uint64_t sf[2][2];          // [q tile][score buffer]: scores complete
+    uint64_t pf[2][2];          // weights stored (one arrival per softmax warp)
+    // an O += P V complete; one per score buffer, because with two the softmax may be two
+    // tiles ahead of the products, and one barrier's parity tells only one phase
+    uint64_t od[2][2];
+    uint64_t oe[2];             // O read out (one arrival per softmax warp)
+    uint64_t drain;
+    uint64_t gs;                // all softmax warps (splits only)
+    uint32_t tmem;
+    int abort;
+    int last;
+    int total;                  // items
+    int tiles;                  // q tiles (of 128 NQ rows) of one layer and kv head
+    int pre[kMaxBatch + 1];     // q tiles before each sequence
+    int len[kMaxBatch], cnt[kMaxBatch], start[kMaxBatch];
+};
+constexpr int kWBars = static_cast<int>((offsetof(WCtrl, tmem)) / sizeof(uint64_t));
+
+struct WItem {
+    int b, layer, kvh;
+    int r0, np, p0;             // first packed row, positions, first position
+    int lo;                     // first position of the joint window
+    int sb, nb, base;           // sink blocks, all blocks; position = list column + base behind the sinks
+    int t0, t1;                 // tiles of this split
+    int slot, sp;
+};
+
+template <int NQ, int KT>
+__device__ __forceinline__ WItem item_of(const WCtrl &c, const WindowParams &p, int idx)
+{
+    WItem it;
+    const int per = 128 * NQ / p.group;
+    it.sp = idx % p.n_split;
+    int q = idx / p.n_split;
+    it.kvh = q % p.n_kv_heads;
+    q /= p.n_kv_heads;
+    it.layer = q / c.tiles;
+    // the last rows of a prompt first: they see the most keys
+    const int t = c.tiles - 1 - (q - it.layer * c.tiles);
+    int lo = 0, hi = p.batch;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (c.pre[mid] <= t)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    it.b = lo;
+    const int first = (t - c.pre[lo]) * per;
+    it.np = min(per, c.cnt[lo] - first);
+    it.p0 = c.len[lo] - c.cnt[lo] + first;
+    it.r0 = c.start[lo] + first;
+    it.lo = max(0, it.p0 - p.n_window + 1);
+    const int lo_blk = it.lo >> 4;
+    it.sb = min((p.n_sink >> 4) + ((p.n_sink & 15) != 0), lo_blk);
+    it.base = (lo_blk - it.sb) * 16;
+    it.nb = it.sb + ((it.p0 + it.np - 1) >> 4) - lo_blk + 1;
+    const int n = (it.nb + KT / 16 - 1) / (KT / 16);
+    it.t0 = static_cast<int>(static_cast<long long>(n) * it.sp / p.n_split);
+    it.t1 = static_cast<int>(static_cast<long long>(n) * (it.sp + 1) / p.n_split);
+    it.slot = (it.layer * c.tiles + t) * p.n_kv_heads + it.kvh;
+    return it;
+}
+
+__device__ __forceinline__ void wfail(WCtrl &c, uint32_t *err)
+{
+    c.abort = 1;
+    raise_error(err, 0x4u);  // SFI_DEVERR_TIMEOUT
+}
+
+// 32 output values of one row.
+__device__ __forceinline__ void store32(const WindowParams &p, size_t at, const float *v)
+{
+    if (p.out_fp32) {
+        float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(p.out) + at);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            o[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+    } else {
+        uint32_t w[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+            w[i] = *reinterpret_cast<const uint32_t *>(&h);
+        }
+        uint4 *o = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) + at);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            o[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    }
+}
+
+template <int NQ, int KT, int ST>
+constexpr int window_smem() { return 1024 + NQ * 32768 + ST * KT * 512 + static_cast<int>(sizeof(WCtrl)); }
+
+// TWO: the weights enter the product with V as bf16 part and bf16 remainder (fp32 outputs).
+template <int NQ, int KT, int ST, int NS, bool TWO>
+__global__ void __launch_bounds__(128 + 128 * NQ, NQ == 1 ? 2 : 1)
+    window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                  const __grid_constant__ CUtensorMap tm_q, const WindowParams p)
+{
+    constexpr int kHalfQ = 16384, kHalfKV = KT * 128, kStage = 4 * kHalfKV, kBlocks = KT / 16;
+    constexpr uint32_t kCols = NQ == 1 ? 256 : 512;
+    static_assert(NQ * (NS * KT + 128) <= static_cast<int>(kCols) && ST <= kMaxStages && NS <= 2);
+    extern __shared__ uint8_t raw[];
+    uint8_t *smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
+    uint8_t *kv_smem = smem + NQ * 2 * kHalfQ;
+    WCtrl &c = *reinterpret_cast<WCtrl *>(kv_smem + ST * kStage);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int G = p.group, per = 128 * NQ / G;
+
+    if (tid < kWBars) {
+        uint64_t *bar = reinterpret_cast<uint64_t *>(&c) + tid;
+        const int off = tid * 8;
+        const bool four = (off >= static_cast<int>(offsetof(WCtrl, pf)) && off < static_cast<int>(offsetof(WCtrl, od))) ||
+                          (off >= static_cast<int>(offsetof(WCtrl, oe)) && off < static_cast<int>(offsetof(WCtrl, drain)));
+        mbar_init(bar, off == static_cast<int>(offsetof(WCtrl, gs)) ? 4 * NQ : four ? 4 : 1);
+        mbar_fence_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(&c.tmem, kCols);
+        tmem_relinquish();
+    }
+    if (tid == 0) {
+        c.abort = 0;
+        tma_prefetch_map(&tm_k);
+        tma_prefetch_map(&tm_v);
+        tma_prefetch_map(&tm_q);
+    }
     pdl_trigger();
     pdl_wait();
-    const int lane = threadIdx.x & 31;
-    const int hq = p.n_kv_heads * p.group;
-    const long long w = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-    if (w >= static_cast<long long>(p.n_layers) * p.n_rows * hq)
-        return;
-    const int h = static_cast<int>(w % hq);
-    const long long lr = w / hq;
-    const int r = static_cast<int>(lr % p.n_rows), layer = static_cast<int>(lr / p.n_rows);
-    int b = r;
-    if (p.row_start) {
-        if (r < p.row_start[0] || r >= p.row_start[p.batch])
-            return;
-        int lo = 0, hi = p.batch;
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (p.row_start[mid] <= r)
-                lo = mid;
-            else
-                hi = mid;
-        }
-        b = lo;
-    }
-    if (p.active && !p.active[b])
-        return;
-    const int s0 = p.row_start ? p.row_start[b] : b, s1 = p.row_start ? p.row_start[b + 1] : b + 1;
-    const int L = p.seq_len[b], n = s1 - s0;
-    uint32_t bad = 0;
-    if (n < 0 || s0 < 0 || s1 > p.n_rows || n > p.max_rows || r < s0 || r >= s1)
-        bad = 0x20u;  // SFI_DEVERR_ROWS
-    else if (L < n || L > p.max_len)
-        bad = 0x8u;   // SFI_DEVERR_LENGTH
-    if (bad) {
-        if (lane == 0)
-            raise_error(p.err, bad);
-        return;
-    }
-    const int pos = L - n + (r - s0);
-    const int low = max(0, pos - p.n_window + 1), ns = min(p.n_sink, low);
-    const uint2 *q = static_cast<const uint2 *>(p.q) + w * 32 + lane;
-    const float2 q01 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&q->x));
-    const float2 q23 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&q->y));
-    float m = -CUDART_INF_F, l = 0.f, o0 = 0.f, o1 = 0.f, o2 = 0.f, o3 = 0.f;
-    const int total = ns + pos - low + 1, kvh = h / p.group;
-    for (int i = 0; i < total; ++i) {
-        const int j = i < ns ? i : low + i - ns;
-        long long row;
-        if (p.page_size == 0) {
-            row = (static_cast<long long>(layer * p.batch + b) * p.n_kv_heads + kvh) * p.capacity + j;
+    // the chunk: every sequence's rows and q tiles
+    for (int b = tid; b < p.batch; b += 128 + 128 * NQ) {
+        const int s0 = p.row_start ? p.row_start[b] : b, s1 = p.row_start ? p.row_start[b + 1] : b + 1;
+        const int L = p.seq_len[b];
+        int n = s1 - s0;
+        if (p.active && !p.active[b]) {
+            n = 0;
         } else {
-            const int page = p.page_table[static_cast<size_t>(b) * p.max_pages + (j >> 4)];
-            if (page < 0 || page >= p.n_pages) {
-                if (lane == 0)
-                    raise_error(p.err, 0x1u);  // SFI_DEVERR_PAGE_RANGE
-                continue;
+            uint32_t bad = 0;
+            if (s0 < 0 || n < 0 || s1 > p.n_rows || n > p.max_rows)
+                bad = 0x20u;  // SFI_DEVERR_ROWS
+            else if (L < n || L > p.max_len)
+                bad = 0x8u;   // SFI_DEVERR_LENGTH
+            if (bad) {
+                n = 0;
+                if (blockIdx.x == 0)
+                    raise_error(p.err, bad);
             }
-            row = (static_cast<long long>(layer * p.n_pages + page) * p.n_kv_heads + kvh) * 16 + (j & 15);
         }
-        const uint2 kx = static_cast<const uint2 *>(p.k)[row * 32 + lane];
-        const uint2 vx = static_cast<const uint2 *>(p.v)[row * 32 + lane];
-        const float2 k01 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&kx.x));
-        const float2 k23 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&kx.y));
-        const float2 v01 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&vx.x));
-        const float2 v23 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&vx.y));
-        float z = q01.x * k01.x + q01.y * k01.y + q23.x * k23.x + q23.y * k23.y;
+        c.cnt[b] = n;
+        c.len[b] = L;
+        c.start[b] = s0;
+    }
+    __syncthreads();
+    if (warp == 0) {
+        int run = 0;
+        for (int b0 = 0; b0 < p.batch; b0 += 32) {
+            const int b = b0 + lane;
+            const int v = b < p.batch ? (c.cnt[b] + per - 1) / per : 0;
+            int x = v;
 #pragma unroll
-        for (int d = 16; d > 0; d >>= 1)
-            z += __shfl_xor_sync(0xffffffffu, z, d);
-        z *= 0.08838834764831845f;   // 1 / sqrt(128)
-        const float mn = fmaxf(m, z), a = expf(m - mn), e = expf(z - mn);
-        m = mn;
-        l = l * a + e;
-        o0 = o0 * a + e * v01.x;
-        o1 = o1 * a + e * v01.y;
-        o2 = o2 * a + e * v23.x;
-        o3 = o3 * a + e * v23.y;
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(0xffffffffu, x, o);
+                if (lane >= o)
+                    x += y;
+            }
+            if (b < p.batch)
+                c.pre[b] = run + x - v;
+            run += __shfl_sync(0xffffffffu, x, 31);
+        }
+        if (lane == 0) {
+            c.tiles = run;
+            c.total = run * p.n_kv_heads * p.n_layers * p.n_split;
+        }
     }
-    const float inv = 1.f / l;
-    const size_t at = static_cast<size_t>(w) * 128 + lane * 4;
-    if (p.out_fp32) {
-        *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + at) =
-            make_float4(o0 * inv, o1 * inv, o2 * inv, o3 * inv);
-    } else {
-        __nv_bfloat162 *o = reinterpret_cast<__nv_bfloat162 *>(static_cast<__nv_bfloat16 *>(p.out) + at);
-        o[0] = __floats2bfloat162_rn(o0 * inv, o1 * inv);
-        o[1] = __floats2bfloat162_rn(o2 * inv, o3 * inv);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = c.tmem;
+    const int total = c.total;
+    auto s_col = [&](int a, int buf) { return tmem + a * (NS * KT + 128) + buf * KT; };
+    auto o_col = [&](int a) { return tmem + a * (NS * KT + 128) + NS * KT; };
+
+    if (warp == 0) {
+        // ------------------------------------------------------------------ TMA producer
+        int use = 0, items = 0;
+        bool ok = true;
+        for (int idx = blockIdx.x; idx < total && ok; idx += gridDim.x) {
+            const WItem it = item_of<NQ, KT>(c, p, idx);
+            if (it.t0 == it.t1)
+                continue;
+            const long long unit = p.page_size
+                                       ? static_cast<long long>(it.layer) * p.n_pages * p.n_kv_heads
+                                       : static_cast<long long>(it.layer * p.batch + it.b) * p.n_kv_heads + it.kvh;
+            // cache row of list block j (a box of 16 rows), -16 (rows of zeros) where there is none
+            auto row_of = [&](int j) -> int {
+                if (j >= it.nb)
+                    return -16;
+                const int pos = j * 16 + (j < it.sb ? 0 : it.base);
+                if (p.page_size == 0)
+                    return static_cast<int>(unit * p.capacity + pos);
+                const int page = __ldg(p.page_table + static_cast<size_t>(it.b) * p.max_pages + (pos >> 4));
+                if (page < 0 || page >= p.n_pages) {
+                    raise_error(p.err, 0x1u);  // SFI_DEVERR_PAGE_RANGE
+                    return -16;
+                }
+                return static_cast<int>((unit + static_cast<long long>(page) * p.n_kv_heads + it.kvh) * 16);
+            };
+            // lane: block lane % kBlocks, 64-column half lane / kBlocks
+            const int blk = lane % kBlocks, half = lane / kBlocks;
+            int row = half < 2 ? row_of(it.t0 * kBlocks + blk) : 0;
+            if (lane == 0) {
+                ok = mbar_wait(&c.qe, (items & 1) ^ 1, &c.abort);
+                if (ok) {
+                    mbar_arrive_expect_tx(&c.qf, NQ * 32768);
+#pragma unroll
+                    for (int a = 0; a < NQ; ++a)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+                            tma_load_3d(smem + (2 * a + h) * kHalfQ, &tm_q, &c.qf, 64 * h, it.kvh * G,
+                                        it.layer * p.n_rows + it.r0 + a * (128 / G));
+                }
+            }
+            ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+            if (!ok)
+                break;
+            ++items;
+            for (int t = it.t0; t < it.t1; ++t) {
+                const int st = use % ST, ph = (use / ST) & 1;
+                uint8_t *k = kv_smem + st * kStage, *v = k + 2 * kHalfKV;
+                const int here = row;
+                if (half < 2 && t + 1 < it.t1)
+                    row = row_of((t + 1) * kBlocks + blk);
+                if (lane == 0) {
+                    ok = mbar_wait(&c.ke[st], ph ^ 1, &c.abort);
+                    if (ok)
+                        mbar_arrive_expect_tx(&c.kf[st], 2 * kHalfKV);
+                }
+                ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+                if (!ok)
+                    break;
+                if (half < 2)
+                    tma_load_2d(k + half * kHalfKV + blk * 2048, &tm_k, &c.kf[st], 64 * half, here);
+                if (lane == 0) {
+                    ok = mbar_wait(&c.ve[st], ph ^ 1, &c.abort);
+                    mbar_arrive_expect_tx(&c.vf[st], ok ? 2 * kHalfKV : 0);
+                }
+                ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+                if (ok && half < 2)
+                    tma_load_2d(v + half * kHalfKV + blk * 2048, &tm_v, &c.vf[st], 64 * half, here);
+                __syncwarp();
+                ++use;
+                if (!ok)
+                    break;
+            }
+        }
+        if (lane == 0) {
+            if (!ok)
+                wfail(c, p.err);
+            // never leave a copy in flight into shared memory that is given up
+            for (int j = max(0, use - ST); j < use; ++j) {
+                mbar_wait(&c.kf[j % ST], (j / ST) & 1, nullptr);
+                mbar_wait(&c.vf[j % ST], (j / ST) & 1, nullptr);
+            }
+            if (items > 0)
+                mbar_wait(&c.qf, (items - 1) & 1, nullptr);
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        // -------------------------------------------------------------------- MMA issuer
+        if (lane == 0) {
+            constexpr uint32_t idesc_s = idesc_bf16(128, KT, false, false);
+            constexpr uint32_t idesc_o = idesc_bf16(128, 128, false, true);
+            int kuse = 0, vuse = 0, items = 0;
+            uint32_t spend[2] = {0, 0};   // tiles of a q tile so far, all items
+            bool ok = true;
+            for (int idx = blockIdx.x; idx < total && ok; idx += gridDim.x) {
+                const WItem it = item_of<NQ, KT>(c, p, idx);
+                const int n = it.t1 - it.t0;
+                if (n == 0)
+                    continue;
+                ok = mbar_wait(&c.qf, items & 1, &c.abort);
+                if (!ok)
+                    break;
+                auto scores = [&](int a, int j, bool wait) -> bool {
+                    const int st = (kuse + j) % ST;
+                    if (wait && !mbar_wait(&c.kf[st], ((kuse + j) / ST) & 1, &c.abort))
+                        return false;
+                    tc_fence_after();
+                    const uint32_t ka = smem_u32(kv_smem + st * kStage), qa = smem_u32(smem + a * 2 * kHalfQ);
+                    const int buf = (spend[a] + j) % NS;
+#pragma unroll
+                    for (int kk = 0; kk < 8; ++kk)
+                        umma_bf16(s_col(a, buf),
+                                  smem_desc_sw128(qa + (kk >> 2) * kHalfQ + (kk & 3) * 32, 16, 1024),
+                                  smem_desc_sw128(ka + (kk >> 2) * kHalfKV + (kk & 3) * 32, 16, 1024),
+                                  idesc_s, kk > 0 ? 1u : 0u);
+                    umma_commit(&c.sf[a][buf]);
+                    return true;
+                };
+                auto scores_done = [&](int j) {
+                    umma_commit(&c.ke[(kuse + j) % ST]);
+                    if (j == n - 1)
+                        umma_commit(&c.qe);
+                };
+                for (int a = 0; a < NQ && ok; ++a)
+                    ok = scores(a, 0, a == 0);
+                if (!ok)
+                    break;
+                scores_done(0);
+                for (int j = 0; j < n && ok; ++j) {
+                    // with two score buffers the next scores are computed ahead of the softmax
+                    if (NS == 2 && j + 1 < n) {
+                        for (int a = 0; a < NQ && ok; ++a)
+                            ok = scores(a, j + 1, a == 0);
+                        if (!ok)
+                            break;
+                        scores_done(j + 1);
+                    }
+                    const int st = (vuse + j) % ST;
+                    for (int a = 0; a < NQ && ok; ++a) {
+                        const int buf = (spend[a] + j) % NS;
+                        ok = mbar_wait(&c.pf[a][buf], ((spend[a] + j) / NS) & 1, &c.abort) &&
+                             (j > 0 || mbar_wait(&c.oe[a], (items & 1) ^ 1, &c.abort)) &&
+                             (a > 0 || mbar_wait(&c.vr[st], ((vuse + j) / ST) & 1, &c.abort));
+                        if (!ok)
+                            break;
+                        tc_fence_after();
+                        const uint32_t va = smem_u32(kv_smem + st * kStage + 2 * kHalfKV);
+#pragma unroll
+                        for (int part = 0; part < (TWO ? 2 : 1); ++part)
+#pragma unroll
+                            for (int kk = 0; kk < kBlocks; ++kk)
+                                umma_bf16_ta(o_col(a), s_col(a, buf) + part * (KT / 2) + kk * 8,
+                                             smem_desc_sw128(va + kk * 2048, kHalfKV, 1024), idesc_o,
+                                             j > 0 || kk > 0 || part > 0 ? 1u : 0u);
+                        umma_commit(&c.od[a][buf]);
+                        if (a == NQ - 1)
+                            umma_commit(&c.ve[st]);
+                        if (NS == 1 && j + 1 < n) {
+                            ok = scores(a, j + 1, a == 0);
+                            if (ok && a == NQ - 1)
+                                scores_done(j + 1);
+                        }
+                    }
+                }
+                kuse += n;
+                vuse += n;
+                for (int a = 0; a < NQ; ++a)
+                    spend[a] += n;
+                ++items;
+            }
+            if (!ok)
+                wfail(c, p.err);
+            umma_commit(&c.drain);
+            mbar_wait(&c.drain, 0, nullptr);
+        }
+        __syncwarp();
+    } else if (warp == 2) {
+        // ------------------------------------------------- V rows that nobody may see := 0
+        int use = 0;
+        bool ok = true;
+        for (int idx = blockIdx.x; idx < total && ok; idx += gridDim.x) {
+            const WItem it = item_of<NQ, KT>(c, p, idx);
+            const int last = it.p0 + it.np - 1;
+            for (int t = it.t0; t < it.t1; ++t, ++use) {
+                const int st = use % ST;
+                ok = mbar_wait(&c.vf[st], (use / ST) & 1, &c.abort);
+                if (!__all_sync(0xffffffffu, ok)) {
+                    ok = false;
+                    break;
+                }
+                uint8_t *v = kv_smem + st * kStage + 2 * kHalfKV;
+                bool wrote = false;
+#pragma unroll
+                for (int i = 0; i < KT / 32; ++i) {
+                    const int r = i * 32 + lane, col = t * KT + r, blk = col >> 4;
+                    const int pos = col + (blk < it.sb ? 0 : it.base);
+                    // (blocks behind the list were filled with zeros)
+                    const bool seen = blk >= it.nb || (pos <= last && (pos < p.n_sink || pos >= it.lo));
+                    uint32_t m = __ballot_sync(0xffffffffu, !seen);
+                    wrote = wrote || m != 0;
+                    while (m) {
+                        const int rr = i * 32 + __ffs(m) - 1;
+                        m &= m - 1;
+                        if (lane < 16)
+                            reinterpret_cast<uint4 *>(v + (lane >> 3) * kHalfKV + rr * 128)[lane & 7] =
+                                make_uint4(0, 0, 0, 0);
+                    }
+                }
+                if (wrote)
+                    fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&c.vr[st]);
+            }
+        }
+        if (!ok && lane == 0)
+            wfail(c, p.err);
+    } else if (warp >= 4) {
+        // ------------------------------------------------------------------------ softmax
+        const int a = (warp - 4) >> 2, quad = warp & 3, rowi = quad * 32 + lane;
+        const uint32_t lane_addr = static_cast<uint32_t>(quad * 32) << 16;
+        const float sc = p.scale_log2;
+        uint32_t done = 0, syncs = 0;   // tiles so far, all items
+        bool ok = true;
+        auto softmax_sync = [&]() -> bool {
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&c.gs);
+            const bool good = mbar_wait(&c.gs, syncs++ & 1, &c.abort);
+            return __all_sync(0xffffffffu, good);
+        };
+        const int rq = a * 128 + rowi;
+        for (int idx = blockIdx.x; idx < total && ok; idx += gridDim.x) {
+            const WItem it = item_of<NQ, KT>(c, p, idx);
+            const int dp = rq / G, h = rq - dp * G;
+            const bool valid = dp < it.np;
+            const int i = it.p0 + dp;                       // this row's position
+            const int e1 = min(p.n_sink, i + 1);            // list columns [0, e1) and [a2, e2)
+            const int a2 = max(i - p.n_window + 1, 0) - it.base, e2 = i - it.base + 1;
+            float m = -CUDART_INF_F, l = 0.f;
+            for (int t = it.t0; t < it.t1; ++t, ++done) {
+                const int buf = done % NS;
+                ok = mbar_wait(&c.sf[a][buf], (done / NS) & 1, &c.abort);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok)
+                    break;
+                tc_fence_after();
+                float s[KT];
+                const uint32_t sa = s_col(a, buf) + lane_addr;
+#pragma unroll
+                for (int q = 0; q < KT / 32; ++q)
+                    tmem_ld32(sa + 32 * q, s + 32 * q);
+#pragma unroll
+                for (int q = 0; q < KT / 32; ++q)
+                    tmem_landed(s + 32 * q);
+                const int c0 = t * KT;
+                const bool whole = a2 <= c0 && e2 >= c0 + KT;
+                if (!__all_sync(0xffffffffu, whole)) {
+#pragma unroll
+                    for (int w = 0; w < KT / 32; ++w) {
+                        const uint32_t see = span_bits(0, e1 - c0, w) | span_bits(a2 - c0, e2 - c0, w);
+#pragma unroll
+                        for (int x = 0; x < 32; ++x)
+                            s[32 * w + x] = (see >> x) & 1u ? s[32 * w + x] : -CUDART_INF_F;
+                    }
+                }
+                float mx[4] = {m, m, m, m};
+#pragma unroll
+                for (int x = 0; x < KT; x += 8) {
+#pragma unroll
+                    for (int y = 0; y < 4; ++y)
+                        mx[y] = fmaxf(mx[y], fmaxf(s[x + y], s[x + 4 + y]));
+                }
+                const float mn = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                const bool grow = (mn - m) * sc > 8.f;      // (from -inf: always, unless still -inf)
+                if (__any_sync(0xffffffffu, grow) && t > it.t0) {
+                    const float alpha = grow ? ex2_approx((m - mn) * sc) : 1.f;
+                    ok = mbar_wait(&c.od[a][(done - 1) % NS], ((done - 1) / NS) & 1, &c.abort);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok)
+                        break;
+                    tc_fence_after();
+                    l *= alpha;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        float o[32];
+                        tmem_ld32(o_col(a) + lane_addr + 32 * q, o);
+                        tmem_landed(o);
+#pragma unroll
+                        for (int x = 0; x < 32; ++x)
+                            o[x] *= alpha;
+                        tmem_st32(o_col(a) + lane_addr + 32 * q, reinterpret_cast<const uint32_t *>(o));
+                    }
+                }
+                m = grow ? mn : m;
+                const float off = m == -CUDART_INF_F ? 0.f : -m * sc;
+                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int q = 0; q < KT / 64; ++q) {
+                    uint32_t w[32], r[TWO ? 32 : 1];
+#pragma unroll
+                    for (int x = 0; x < 32; ++x) {
+                        const float p0 = ex2_approx(fmaf(s[64 * q + 2 * x], sc, off));
+                        const float p1 = ex2_approx(fmaf(s[64 * q + 2 * x + 1], sc, off));
+                        sum[(2 * x) & 3] += p0;
+                        sum[(2 * x + 1) & 3] += p1;
+                        const __nv_bfloat162 hi = __floats2bfloat162_rn(p0, p1);
+                        w[x] = *reinterpret_cast<const uint32_t *>(&hi);
+                        if (TWO) {
+                            const float2 b = __bfloat1622float2(hi);
+                            const __nv_bfloat162 lo = __floats2bfloat162_rn(p0 - b.x, p1 - b.y);
+                            r[TWO ? x : 0] = *reinterpret_cast<const uint32_t *>(&lo);
+                        }
+                    }
+                    tmem_st32(sa + 32 * q, w);
+                    if (TWO)
+                        tmem_st32(sa + KT / 2 + 32 * q, r);
+                }
+                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&c.pf[a][buf]);
+            }
+            if (!ok)
+                break;
+            // ------------------------------------------------------------------ epilogue
+            const bool any = it.t1 > it.t0;
+            if (any) {
+                ok = mbar_wait(&c.od[a][(done - 1) % NS], ((done - 1) / NS) & 1, &c.abort);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok)
+                    break;
+                tc_fence_after();
+            }
+            const size_t out_at = ((static_cast<size_t>(it.layer) * p.n_rows + it.r0 + dp) * p.n_kv_heads * G +
+                                   it.kvh * G + h) * kHeadDim;
+            const size_t part = static_cast<size_t>(it.slot) * p.n_split + it.sp;
+            const float inv = p.n_split == 1 ? 1.f / l : 1.f;
+            if (any) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    float o[32];
+                    tmem_ld32(o_col(a) + lane_addr + 32 * q, o);
+                    tmem_landed(o);
+                    if (valid) {
+#pragma unroll
+                        for (int x = 0; x < 32; ++x)
+                            o[x] *= inv;
+                        if (p.n_split == 1) {
+                            store32(p, out_at + 32 * q, o);
+                        } else {
+                            float4 *w = reinterpret_cast<float4 *>(
+                                p.parts + (part * p.part_rows + rq) * kHeadDim + 32 * q);
+#pragma unroll
+                            for (int x = 0; x < 8; ++x)
+                                w[x] = make_float4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
+                        }
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&c.oe[a]);
+            }
+            if (p.n_split > 1) {
+                if (valid)
+                    p.part_ml[part * p.part_rows + rq] = make_float2(m, l);
+                // every softmax thread's partials before the ticket, the ticket before any read
+                __threadfence();
+                if (!(ok = softmax_sync()))
+                    break;
+                if (tid == 128)
+                    c.last = atomic_add_acq_rel_gpu(p.tickets + it.slot, 1) == p.n_split - 1;
+                if (!(ok = softmax_sync()))
+                    break;
+                if (c.last != 0) {
+                    if (tid == 128)
+                        p.tickets[it.slot] = 0;
+                    __threadfence();
+                    // a thread per (row, dim): 128 dims, NQ rows at a time
+                    const int d = (tid - 128) & 127;
+                    const int nrows = it.np * G;
+                    for (int r = (tid - 128) >> 7; r < nrows; r += NQ) {
+                        const size_t p0 = static_cast<size_t>(it.slot) * p.n_split * p.part_rows + r;
+                        float M = -CUDART_INF_F;
+                        for (int sp = 0; sp < p.n_split; ++sp)
+                            M = fmaxf(M, __ldcg(p.part_ml + p0 + static_cast<size_t>(sp) * p.part_rows).x);
+                        float acc = 0.f, den = 0.f;
+                        for (int sp = 0; sp < p.n_split; ++sp) {
+                            const size_t at = p0 + static_cast<size_t>(sp) * p.part_rows;
+                            const float2 ml = __ldcg(p.part_ml + at);
+                            if (ml.y > 0.f) {
+                                const float w = ex2_approx((ml.x - M) * sc);
+                                acc = fmaf(w, __ldcg(p.parts + at * kHeadDim + d), acc);
+                                den = fmaf(w, ml.y, den);
+                            }
+                        }
+                        const int dpr = r / G;
+                        const size_t o = ((static_cast<size_t>(it.layer) * p.n_rows + it.r0 + dpr) *
+                                              p.n_kv_heads * G + it.kvh * G + (r - dpr * G)) * kHeadDim + d;
+                        if (p.out_fp32)
+                            static_cast<float *>(p.out)[o] = acc / den;
+                        else
+                            static_cast<__nv_bfloat16 *>(p.out)[o] = __float2bfloat16_rn(acc / den);
+                    }
+                }
+            }
+        }
+        if (!ok && lane == 0)
+            wfail(c, p.err);
     }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) {
+        tmem_dealloc(tmem, kCols);
+    }
+}
+
+template <int NQ, int KT, int ST, int NS, bool TWO>
+cudaError_t launch_one(const WindowParams &p, const CUtensorMap &tm_k, const CUtensorMap &tm_v,
+                       const CUtensorMap &tm_q, int grid, cudaStream_t stream)
+{
+    auto *kern = window_kernel<NQ, KT, ST, NS, TWO>;
+    constexpr int smem = window_smem<NQ, KT, ST>();
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess)
+        e = launch_pdl(kern, dim3(grid), dim3(128 + 128 * NQ), smem, stream, tm_k, tm_v, tm_q, p);
+    return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_window(const WindowParams &p, cudaStream_t stream)
+cudaError_t launch_window(const WindowParams &p, int n_qtiles, const CUtensorMap &tm_k,
+                          const CUtensorMap &tm_v, const CUtensorMap &tm_q, int grid,
+                          cudaStream_t stream)
 {
-    const long long warps = static_cast<long long>(p.n_layers) * p.n_rows * p.n_kv_heads * p.group;
-    const cudaError_t e = launch_pdl(window_simple_kernel, dim3(static_cast<unsigned>((warps + 7) / 8)),
-                                     dim3(256), 0, stream, p);
-    return e != cudaSuccess ? e : cudaGetLastError();
+    if (n_qtiles == 2)
+        return p.out_fp32 ? launch_one<2, 128, 2, 1, true>(p, tm_k, tm_v, tm_q, grid, stream)
+                          : launch_one<2, 128, 2, 1, false>(p, tm_k, tm_v, tm_q, grid, stream);
+    return p.out_fp32 ? launch_one<1, 64, 2, 2, true>(p, tm_k, tm_v, tm_q, grid, stream)
+                      : launch_one<1, 64, 2, 2, false>(p, tm_k, tm_v, tm_q, grid, stream);
 }
 
 }  // namespace sfi
