@@ -148,21 +148,41 @@ def lib():
 
 def _ptr(x):
     """Device/host address of a torch tensor, numpy array, int or None."""
-    if x is None:
-        return None
-    if isinstance(x, int):
+    if x is None or type(x) is int:
         return x
-    if hasattr(x, "data_ptr"):
+    try:
         return x.data_ptr()
+    except AttributeError:
+        pass
     if hasattr(x, "ctypes"):
         return x.ctypes.data
+    if isinstance(x, int):
+        return x
     raise TypeError(f"cannot take the address of {type(x).__name__}")
+
+
+_raw_stream = None
+
+
+def _current_stream():
+    """The current stream of the current device. The raw query takes a tenth of the time of
+    building a torch.cuda.Stream, which was a third of a small call."""
+    global _raw_stream
+    if _raw_stream is None:
+        import torch
+        torch.cuda.init()
+        raw, device = (getattr(torch._C, n, None) for n in ("_cuda_getCurrentRawStream",
+                                                           "_cuda_getDevice"))
+        if raw is not None and device is not None:
+            _raw_stream = lambda: raw(device())
+        else:
+            _raw_stream = lambda: torch.cuda.current_stream().cuda_stream
+    return _raw_stream()
 
 
 def _stream(s):
     if s is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        return _current_stream()
     if isinstance(s, int):
         return s
     return s.cuda_stream

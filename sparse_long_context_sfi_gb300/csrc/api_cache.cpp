@@ -140,12 +140,13 @@ sfi_status check_beam(const sfi_beam *b)
     return SFI_OK;
 }
 
-// Slices of a row: enough CTAs for about two per SM, at least 2048 tokens each.
+// CTAs per row: at most the four per SM that are resident at once, each of whose eight warps
+// has a whole 512-token chunk or more.
 int beam_splits(const sfi_beam *b)
 {
     const int rows = b->n_groups * b->n_beams, sms = sm_count();
-    int s = (2 * sms + rows - 1) / rows;
-    const int most = (b->vocab + 2047) / 2048;
+    int s = 4 * sms / rows;
+    const int most = b->vocab / 4096 + 1;
     s = s < most ? s : most;
     return s < 1 ? 1 : s > 64 ? 64 : s;
 }
@@ -311,6 +312,7 @@ sfi_status sfi_window_attn(const sfi_kv_cache *kv, const void *q, void *out, int
     p.n_window = n_window;
     p.out = out;
     p.out_fp32 = out_fp32 ? 1 : 0;
+    p.out_aligned32 = (reinterpret_cast<uintptr_t>(out) & 31u) == 0;
     p.err = kv->err;
     const int g = p.group;
     const long long len = kv->max_len, reach = n_window < len ? n_window : len;

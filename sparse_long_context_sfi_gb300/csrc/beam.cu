@@ -2,8 +2,13 @@
 // maximum and sum and the row's best tokens, then the best n_beams of each group.
 //
 // Within a row s(r, v) = cum + x[v] - lse is monotone in x, so a row's n_beams best tokens by
-// logit are all that its group can need: every CTA reduces a slice of a row to (max, sum, best
-// tokens), and the last CTA of a group joins its rows' slices.
+// logit are all that its group can need. The logits are read once (the floor: their bytes);
+// every warp takes 512-token chunks of its row, 16 tokens per lane in registers, the next
+// chunk's loads in flight. The best tokens so far lie sorted in the warp's lanes, and a chunk
+// whose maximum is below the last of them costs one comparison per lane; the others are
+// inserted one by one, the chunk from its end, so that neither ascending nor descending logits
+// insert every token. Warps of a CTA, the CTAs of a row (splits) and the rows of a group are
+// joined by the same insertion; the last CTA of a group does the last two.
 #include "sfi_device.cuh"
 
 #include <math_constants.h>
@@ -12,244 +17,367 @@ namespace sfi {
 namespace {
 
 constexpr int kBeamThreads = 256;
+constexpr int kBeamWarps = kBeamThreads / 32;
+constexpr int kLaneTok = 16;                 // tokens per lane and chunk
+constexpr uint32_t kAll = 0xffffffffu;
+constexpr float kLog2e = 1.4426950408889634f;
 
 // a before b: higher logit, then lower token (empty places, v < 0, last)
 __device__ __forceinline__ bool better(float xa, int va, float xb, int vb)
 {
-    if (va < 0 || vb < 0)
-        return va >= 0;
-    return xa > xb || (xa == xb && va < vb);
+    // (unsigned: an empty place, -1, is behind every token)
+    return xa > xb || (xa == xb && static_cast<uint32_t>(va) < static_cast<uint32_t>(vb));
 }
 
-struct Cand {
-    float key, x, s;
-    int row, v;
-};
-
-__device__ __forceinline__ bool better(const Cand &a, const Cand &b)
+__device__ __forceinline__ float ex2(float x)
 {
-    if (a.v < 0 || b.v < 0)
-        return a.v >= 0;
-    if (a.key != b.key)
-        return a.key > b.key;
-    if (a.row != b.row)
-        return a.row < b.row;
-    return a.x > b.x || (a.x == b.x && a.v < b.v);
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 
-template <int KT>
-__global__ void __launch_bounds__(kBeamThreads) beam_kernel(const BeamParams p)
-{
-    __shared__ float sh_m[8], sh_s[8], sh_x[8];
-    __shared__ int sh_v[8], sh_t[8];
-    __shared__ Cand sh_c[8];
-    __shared__ int sh_win, sh_last;
-    __shared__ float row_max[kMaxBeams], row_log[kMaxBeams], row_cum[kMaxBeams], row_scale[kMaxBeams];
-    __shared__ int row_kind[kMaxBeams];   // 0 live, 1 finished, 2 all scores -inf
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int K = p.n_beams, row = blockIdx.y, split = blockIdx.x;
-    pdl_wait();
-    if (!(p.done && p.done[row])) {
-        const int per = (p.vocab + p.splits - 1) / p.splits;
-        const int v0 = split * per, v1 = min(p.vocab, v0 + per);
-        float m = -CUDART_INF_F, s = 0.f, bx[KT];
-        int bv[KT];
-#pragma unroll
-        for (int j = 0; j < KT; ++j) {
-            bx[j] = -CUDART_INF_F;
-            bv[j] = -1;
+// The warp's K best so far: lane j holds the j-th, lanes from K on hold nothing.
+struct Best {
+    float x;
+    int v;
+    float tx;      // the last of them (every lane): what a token has to beat
+    int tv;
+
+    __device__ __forceinline__ void clear()
+    {
+        x = tx = -CUDART_INF_F;
+        v = tv = -1;
+    }
+    // every lane calls it with the same (cx, cv), better than (tx, tv)
+    __device__ __forceinline__ void insert(float cx, int cv, int K, int lane)
+    {
+        const uint32_t m = __ballot_sync(kAll, better(cx, cv, x, v));
+        const int pos = __ffs(m) - 1;
+        const float ux = __shfl_up_sync(kAll, x, 1);
+        const int uv = __shfl_up_sync(kAll, v, 1);
+        if (lane >= pos && lane < K) {
+            x = lane == pos ? cx : ux;
+            v = lane == pos ? cv : uv;
         }
-        bool nan = false;
-        for (int v = v0 + tid; v < v1; v += kBeamThreads) {
-            const size_t at = static_cast<size_t>(row) * p.row_stride + v;
-            float x = p.logits_fp32 ? static_cast<const float *>(p.logits)[at]
-                                    : __bfloat162float(static_cast<const __nv_bfloat16 *>(p.logits)[at]);
-            nan = nan || x != x;
-            if (x > m) {
-                s = s * expf(m - x) + 1.f;
-                m = x;
-            } else if (m > -CUDART_INF_F) {
-                s += expf(x - m);
-            }
-            if (better(x, v, bx[KT - 1], bv[KT - 1])) {
-                int w = v;
-#pragma unroll
-                for (int j = 0; j < KT; ++j) {
-                    if (better(x, w, bx[j], bv[j])) {
-                        const float tx = bx[j];
-                        const int tv = bv[j];
-                        bx[j] = x;
-                        bv[j] = w;
-                        x = tx;
-                        w = tv;
-                    }
-                }
-            }
+        tx = __shfl_sync(kAll, x, K - 1);
+        tv = __shfl_sync(kAll, v, K - 1);
+    }
+    // each lane offers one candidate (v < 0: none); from the last lane down
+    __device__ __forceinline__ void offer(float cx, int cv, int K, int lane)
+    {
+        uint32_t m = __ballot_sync(kAll, cv >= 0 && better(cx, cv, tx, tv));
+        while (m) {
+            const int src = 31 - __clz(m);
+            insert(__shfl_sync(kAll, cx, src), __shfl_sync(kAll, cv, src), K, lane);
+            m = __ballot_sync(kAll, cv >= 0 && better(cx, cv, tx, tv)) & ((1u << src) - 1u);
         }
-        if (nan)
-            s = CUDART_NAN_F;
-        // maximum and sum of the slice
-        float bm = m;
+    }
+    // the first candidates, one per lane: sorted over the warp (bitonic), the first K kept
+    __device__ __forceinline__ void start(float cx, int cv, int K, int lane)
+    {
+        x = cv >= 0 ? cx : -CUDART_INF_F;
+        v = cv;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
-            bm = fmaxf(bm, __shfl_xor_sync(0xffffffffu, bm, o));
-        if (lane == 0)
-            sh_m[warp] = bm;
-        __syncthreads();
-        bm = sh_m[0];
-        for (int w = 1; w < 8; ++w)
-            bm = fmaxf(bm, sh_m[w]);
-        // (a sum without a finite maximum is 0, or NaN; inf - inf gives the NaN wanted)
-        float bs = s == 0.f ? 0.f : s * expf(m - bm);
+        for (int size = 2; size <= 32; size <<= 1) {
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
-            bs += __shfl_xor_sync(0xffffffffu, bs, o);
-        if (lane == 0)
-            sh_s[warp] = bs;
-        __syncthreads();
-        const size_t part = static_cast<size_t>(row) * p.splits + split;
-        if (tid == 0) {
-            bs = 0.f;
-            for (int w = 0; w < 8; ++w)
-                bs += sh_s[w];
-            p.part_stat[part] = make_float2(bm, bs);
-        }
-        // K rounds: the best head of all threads' lists
-        for (int k = 0; k < K; ++k) {
-            float x = bx[0];
-            int v = bv[0], t = tid;
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) {
-                const float ox = __shfl_xor_sync(0xffffffffu, x, o);
-                const int ov = __shfl_xor_sync(0xffffffffu, v, o), ot = __shfl_xor_sync(0xffffffffu, t, o);
-                if (better(ox, ov, x, v)) {
+            for (int d = size >> 1; d > 0; d >>= 1) {
+                const float ox = __shfl_xor_sync(kAll, x, d);
+                const int ov = __shfl_xor_sync(kAll, v, d);
+                // descending runs where the size's bit of the lane is clear
+                const bool first = ((lane & d) == 0) == ((lane & size) == 0);
+                if (better(ox, ov, x, v) == first) {
                     x = ox;
                     v = ov;
-                    t = ot;
                 }
             }
-            if (lane == 0) {
-                sh_x[warp] = x;
-                sh_v[warp] = v;
-                sh_t[warp] = t;
-            }
-            __syncthreads();
-            if (tid == 0) {
-                int best = 0;
-                for (int w = 1; w < 8; ++w)
-                    if (better(sh_x[w], sh_v[w], sh_x[best], sh_v[best]))
-                        best = w;
-                p.part_x[part * K + k] = sh_x[best];
-                p.part_v[part * K + k] = sh_v[best];
-                sh_win = sh_v[best] >= 0 ? sh_t[best] : -1;
-            }
-            __syncthreads();
-            if (tid == sh_win) {
+        }
+        if (lane >= K) {
+            x = -CUDART_INF_F;
+            v = -1;
+        }
+        tx = __shfl_sync(kAll, x, K - 1);
+        tv = __shfl_sync(kAll, v, K - 1);
+    }
+};
+
+// 16 tokens of one lane: V = 16 / sizeof(T) of them per 16-byte piece, pieces 32 lanes apart.
+template <typename T>
+struct Chunk;
+
+template <>
+struct Chunk<float> {
+    static constexpr int kV = 4;
+    static __device__ __forceinline__ void unpack(const uint4 &w, float *x)
+    {
+        x[0] = __uint_as_float(w.x);
+        x[1] = __uint_as_float(w.y);
+        x[2] = __uint_as_float(w.z);
+        x[3] = __uint_as_float(w.w);
+    }
+};
+
+template <>
+struct Chunk<__nv_bfloat16> {
+    static constexpr int kV = 8;
+    static __device__ __forceinline__ void unpack(const uint4 &w, float *x)
+    {
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-                for (int j = 0; j + 1 < KT; ++j) {
-                    bx[j] = bx[j + 1];
-                    bv[j] = bv[j + 1];
+        for (int i = 0; i < 4; ++i) {
+            x[2 * i] = __uint_as_float(u[i] << 16);
+            x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+        }
+    }
+};
+
+// The 16-byte pieces of a chunk; pieces that reach over either end of the row are put together
+// from its tokens (others: -inf, which no sum and no list sees).
+template <typename T>
+__device__ __forceinline__ void load_chunk(const T *row, int shift, int vocab, int piece0, int lane,
+                                           uint4 *w)
+{
+    constexpr int V = Chunk<T>::kV;
+#pragma unroll
+    for (int i = 0; i < kLaneTok / V; ++i) {
+        const int at = (piece0 + 32 * i + lane) * V - shift;   // first token of the piece
+        if (at >= 0 && at + V <= vocab) {
+            w[i] = __ldcs(reinterpret_cast<const uint4 *>(row + at));
+        } else {
+            T t[V];
+#pragma unroll
+            for (int j = 0; j < V; ++j)
+                t[j] = at + j >= 0 && at + j < vocab ? row[at + j] : static_cast<T>(-CUDART_INF_F);
+            w[i] = *reinterpret_cast<const uint4 *>(t);
+        }
+    }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kBeamThreads, 4) beam_kernel(const BeamParams p)
+{
+    __shared__ float sh_x[kBeamWarps][kMaxBeams], sh_m[kBeamWarps], sh_s[kBeamWarps];
+    __shared__ int sh_v[kBeamWarps][kMaxBeams];
+    __shared__ float row_x[kMaxBeams][kMaxBeams], row_s[kMaxBeams][kMaxBeams];
+    __shared__ int row_v[kMaxBeams][kMaxBeams];
+    __shared__ uint8_t row_done[kMaxBeams];
+    __shared__ int sh_last;
+    constexpr int V = Chunk<T>::kV;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int K = p.n_beams, row = blockIdx.y, split = blockIdx.x, group = row / K;
+    pdl_wait();
+    if (!(p.done && p.done[row])) {
+        const T *x0 = static_cast<const T *>(p.logits) + static_cast<size_t>(row) * p.row_stride;
+        const int shift = static_cast<int>((reinterpret_cast<uintptr_t>(x0) & 15u) / sizeof(T));
+        const int pieces = (p.vocab + shift + V - 1) / V;
+        constexpr int kStep = 32 * (kLaneTok / V);               // pieces per chunk
+        Best best;
+        best.clear();
+        bool fresh = true;          // (the same in every lane, as is all that decides a branch here)
+        float m = -CUDART_INF_F, s = 0.f;
+        int c = (split * kBeamWarps + warp) * kStep;
+        const int stride = p.splits * kBeamWarps * kStep;
+        uint4 w[kLaneTok / V];
+        if (c < pieces)
+            load_chunk(x0, shift, p.vocab, c, lane, w);
+        for (; c < pieces; c += stride) {
+            float x[kLaneTok];
+#pragma unroll
+            for (int i = 0; i < kLaneTok / V; ++i)
+                Chunk<T>::unpack(w[i], x + V * i);
+            if (c + stride < pieces)
+                load_chunk(x0, shift, p.vocab, c + stride, lane, w);
+            float cm = x[0];
+#pragma unroll
+            for (int j = 1; j < kLaneTok; ++j)
+                cm = fmaxf(cm, x[j]);
+            // sum of exp(x - m), the lane's own running maximum
+            const float mn = fmaxf(m, cm);
+            if (mn > -CUDART_INF_F) {
+                float a0 = 0.f, a1 = 0.f;
+#pragma unroll
+                for (int j = 0; j < kLaneTok; j += 2) {
+                    a0 += ex2((x[j] - mn) * kLog2e);
+                    a1 += ex2((x[j + 1] - mn) * kLog2e);
                 }
-                bv[KT - 1] = -1;
+                s = (m > -CUDART_INF_F ? s * ex2((m - mn) * kLog2e) : s) + (a0 + a1);
+                m = mn;
+            } else {
+                // nothing but -inf, or NaN, which has to show in the sum
+#pragma unroll
+                for (int j = 0; j < kLaneTok; ++j)
+                    s = x[j] == -CUDART_INF_F ? s : CUDART_NAN_F;
             }
+            // Tokens that beat the K-th best (in a warp's first chunk the list is empty): each
+            // lane offers its best, and again as long as some lane has another one.
+            if (__any_sync(kAll, cm > best.tx || best.tv < 0)) {
+                uint32_t left = 0;      // tokens not offered yet
+                const int v0 = (c + lane) * V - shift;
+                // (positions only grow with j, so the first of equal logits is the lowest token)
+                auto token = [&](int j) { return v0 + 32 * V * (j / V) + j % V; };
+#pragma unroll
+                for (int j = 0; j < kLaneTok; ++j)
+                    left |= token(j) >= 0 && token(j) < p.vocab ? 1u << j : 0u;
+                for (;;) {
+                    float cx = -CUDART_INF_F;
+                    int cj = -1;
+#pragma unroll
+                    for (int j = kLaneTok - 1; j >= 0; --j) {
+                        if (((left >> j) & 1u) && x[j] >= cx) {
+                            cx = x[j];
+                            cj = j;
+                        }
+                    }
+                    const int cv = cj < 0 ? -1 : token(cj);
+                    left &= cj < 0 ? 0u : ~(1u << cj);
+                    if (fresh)
+                        best.start(cx, cv, K, lane);
+                    else
+                        best.offer(cx, cv, K, lane);
+                    fresh = false;
+                    bool more = false;
+#pragma unroll
+                    for (int j = 0; j < kLaneTok; ++j)
+                        more = more || (((left >> j) & 1u) && better(x[j], token(j), best.tx, best.tv));
+                    if (!__any_sync(kAll, more))
+                        break;
+                }
+            }
+        }
+        // the warp's maximum and sum
+        float wm = m;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+            wm = fmaxf(wm, __shfl_xor_sync(kAll, wm, o));
+        float ws = s == 0.f ? 0.f : wm > -CUDART_INF_F ? s * ex2((m - wm) * kLog2e) : s;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+            ws += __shfl_xor_sync(kAll, ws, o);
+        if (lane == 0) {
+            sh_m[warp] = wm;
+            sh_s[warp] = ws;
+        }
+        // the CTA's best: warps pair off
+#pragma unroll
+        for (int half = kBeamWarps / 2; half > 0; half >>= 1) {
+            if (warp >= half && warp < 2 * half && lane < K) {
+                sh_x[warp][lane] = best.x;
+                sh_v[warp][lane] = best.v;
+            }
+            __syncthreads();
+            if (warp < half)
+                best.offer(lane < K ? sh_x[warp + half][lane] : 0.f,
+                           lane < K ? sh_v[warp + half][lane] : -1, K, lane);
+        }
+        const size_t part = static_cast<size_t>(row) * p.splits + split;
+        if (warp == 0) {
+            float bm = lane < kBeamWarps ? sh_m[lane] : -CUDART_INF_F;
+            const float mine = bm;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1)
+                bm = fmaxf(bm, __shfl_xor_sync(kAll, bm, o));
+            float bs = lane < kBeamWarps ? sh_s[lane] : 0.f;
+            bs = bs == 0.f ? 0.f : bm > -CUDART_INF_F ? bs * ex2((mine - bm) * kLog2e) : bs;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1)
+                bs += __shfl_xor_sync(kAll, bs, o);
+            if (lane == 0)
+                p.part_stat[part] = make_float2(bm, bs);
+            if (lane < K) {
+                p.part_x[part * K + lane] = best.x;
+                p.part_v[part * K + lane] = best.v;
+            }
+            __threadfence();
         }
     }
     // the last CTA of the group joins
-    const int group = row / K;
     __syncthreads();
     if (tid == 0)
         sh_last = atomic_add_acq_rel_gpu(p.tickets + group, 1) == K * p.splits - 1;
     __syncthreads();
     if (!sh_last)
         return;
+    __threadfence();
     if (tid == 0)
         p.tickets[group] = 0;
-    if (tid < K) {
-        const int r = group * K + tid;
-        const float cum = p.cum[r];
-        int kind = 0;
-        float m = -CUDART_INF_F, ls = 0.f;
-        if (p.done && p.done[r]) {
-            kind = 1;
+    // a warp per row: its statistics, its best tokens and their scores
+    for (int b = warp; b < K; b += kBeamWarps) {
+        const int r = group * K + b;
+        const float cum = p.cum[r], scale = p.rank_scale ? p.rank_scale[r] : 1.f;
+        const bool fin = p.done && p.done[r];
+        Best best;
+        best.clear();
+        float score = -CUDART_INF_F;
+        if (fin) {
+            if (lane == 0) {
+                best.v = p.eos;
+                score = isfinite(cum) ? cum : -CUDART_INF_F;
+            }
         } else {
-            float s = 0.f;
-            for (int i = 0; i < p.splits; ++i) {
-                const float2 st = __ldcg(p.part_stat + static_cast<size_t>(r) * p.splits + i);
-                m = fmaxf(m, st.x);
+            const size_t part = static_cast<size_t>(r) * p.splits;
+            float m = -CUDART_INF_F, s = 0.f;
+            for (int i = lane; i < p.splits; i += 32) {
+                const float2 st = __ldcg(p.part_stat + part + i);
+                const float mn = fmaxf(m, st.x);
+                if (st.y != 0.f) {
+                    const float add = mn > -CUDART_INF_F ? st.y * ex2((st.x - mn) * kLog2e) : st.y;
+                    s = (s != 0.f && mn > -CUDART_INF_F ? s * ex2((m - mn) * kLog2e) : s) + add;
+                    m = mn;
+                }
             }
-            for (int i = 0; i < p.splits; ++i) {
-                const float2 st = __ldcg(p.part_stat + static_cast<size_t>(r) * p.splits + i);
-                s += st.y == 0.f ? 0.f : st.y * expf(st.x - m);
-            }
-            ls = logf(s);   // kept apart from the maximum: their sum would round at |m|
-            if (!isfinite(m) || !isfinite(ls) || !isfinite(cum))
-                kind = 2;
-        }
-        row_kind[tid] = kind;
-        row_max[tid] = m;
-        row_log[tid] = ls;
-        row_cum[tid] = cum;
-        row_scale[tid] = p.rank_scale ? p.rank_scale[r] : 1.f;
-    }
-    __syncthreads();
-    Cand last;
-    last.v = -2;
-    for (int k = 0; k < K; ++k) {
-        Cand best;
-        best.v = -1;
-        best.key = best.x = best.s = 0.f;
-        best.row = 0;
-        const int each = p.splits * K;
-        for (int i = tid; i < K * each; i += kBeamThreads) {
-            Cand c;
-            c.row = i / each;
-            const int j = i - c.row * each, kind = row_kind[c.row];
-            if (kind == 0) {
-                const size_t at = static_cast<size_t>(group * K + c.row) * each + j;
-                c.x = __ldcg(p.part_x + at);
-                c.v = __ldcg(p.part_v + at);
-                c.s = row_cum[c.row] + ((c.x - row_max[c.row]) - row_log[c.row]);
-            } else if (kind == 1) {
-                c.v = j == 0 ? p.eos : -1;
-                c.x = 0.f;
-                c.s = isfinite(row_cum[c.row]) ? row_cum[c.row] : -CUDART_INF_F;
-            } else {
-                c.v = j < p.vocab && j < K ? j : -1;
-                c.x = 0.f;
-                c.s = -CUDART_INF_F;
-            }
-            c.key = c.s * row_scale[c.row];
-            // after the one chosen before it, and ahead of the best so far
-            if (c.v >= 0 && (last.v == -2 || better(last, c)) && better(c, best))
-                best = c;
-        }
+            float wm = m;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            Cand c;
-            c.key = __shfl_xor_sync(0xffffffffu, best.key, o);
-            c.x = __shfl_xor_sync(0xffffffffu, best.x, o);
-            c.s = __shfl_xor_sync(0xffffffffu, best.s, o);
-            c.row = __shfl_xor_sync(0xffffffffu, best.row, o);
-            c.v = __shfl_xor_sync(0xffffffffu, best.v, o);
-            if (better(c, best))
-                best = c;
+            for (int o = 16; o > 0; o >>= 1)
+                wm = fmaxf(wm, __shfl_xor_sync(kAll, wm, o));
+            s = s == 0.f ? 0.f : wm > -CUDART_INF_F ? s * ex2((m - wm) * kLog2e) : s;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1)
+                s += __shfl_xor_sync(kAll, s, o);
+            // maximum and log of the sum stay apart: their sum would round at |m|
+            const float ls = logf(s);
+            const bool dead = !isfinite(wm) || !isfinite(ls) || !isfinite(cum);
+            if (dead) {
+                best.v = lane < K && lane < p.vocab ? lane : -1;
+            } else {
+                float cx = lane < K ? __ldcg(p.part_x + part * K + lane) : 0.f;
+                int cv = lane < K ? __ldcg(p.part_v + part * K + lane) : -1;
+                for (int i = 0; i < p.splits; ++i) {
+                    const float ox = cx;
+                    const int ov = cv;
+                    if (i + 1 < p.splits && lane < K) {
+                        cx = __ldcg(p.part_x + (part + i + 1) * K + lane);
+                        cv = __ldcg(p.part_v + (part + i + 1) * K + lane);
+                    }
+                    best.offer(ox, ov, K, lane);
+                }
+                score = cum + ((best.x - wm) - ls);
+            }
+        }
+        if (lane < K) {
+            row_s[b][lane] = score;
+            row_x[b][lane] = score * scale;
+            row_v[b][lane] = best.v;
         }
         if (lane == 0)
-            sh_c[warp] = best;
-        __syncthreads();
-        best = sh_c[0];
-        for (int w = 1; w < 8; ++w)
-            if (better(sh_c[w], best))
-                best = sh_c[w];
-        __syncthreads();
-        last = best;
-        if (tid == 0) {
-            const int o = group * K + k, r = group * K + best.row;
-            p.parent[o] = r;
-            p.token[o] = best.v;
-            p.cum_out[o] = best.s;
+            row_done[b] = fin ? 1 : 0;
+    }
+    __syncthreads();
+    // the group's best: candidate id = row * 16 + place in the row, so that ties by score go to
+    // the lower row, and within a row to the higher logit, then the lower token
+    if (warp == 0) {
+        Best best;
+        best.clear();
+        for (int b = 0; b < K; ++b)
+            best.offer(lane < K ? row_x[b][lane] : 0.f,
+                       lane < K && row_v[b][lane] >= 0 ? b * kMaxBeams + lane : -1, K, lane);
+        if (lane < K) {
+            const int id = max(best.v, 0);   // (all places are filled unless a scale is not a number)
+            const int b = id / kMaxBeams, j = id % kMaxBeams, o = group * K + lane;
+            const int token = row_v[b][j];
+            p.parent[o] = group * K + b;
+            p.token[o] = token;
+            p.cum_out[o] = row_s[b][j];
             if (p.done_out)
-                p.done_out[o] = row_kind[best.row] == 1 || best.v == p.eos ? 1 : 0;
+                p.done_out[o] = row_done[b] || token == p.eos ? 1 : 0;
         }
     }
 }
@@ -259,15 +387,8 @@ __global__ void __launch_bounds__(kBeamThreads) beam_kernel(const BeamParams p)
 cudaError_t launch_beam_select(const BeamParams &p, cudaStream_t stream)
 {
     const dim3 grid(p.splits, p.n_groups * p.n_beams), block(kBeamThreads);
-    cudaError_t e;
-    if (p.n_beams <= 1)
-        e = launch_pdl(beam_kernel<1>, grid, block, 0, stream, p);
-    else if (p.n_beams <= 4)
-        e = launch_pdl(beam_kernel<4>, grid, block, 0, stream, p);
-    else if (p.n_beams <= 8)
-        e = launch_pdl(beam_kernel<8>, grid, block, 0, stream, p);
-    else
-        e = launch_pdl(beam_kernel<16>, grid, block, 0, stream, p);
+    const cudaError_t e = p.logits_fp32 ? launch_pdl(beam_kernel<float>, grid, block, 0, stream, p)
+                                        : launch_pdl(beam_kernel<__nv_bfloat16>, grid, block, 0, stream, p);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 

@@ -120,22 +120,28 @@ __global__ void __launch_bounds__(kPlanThreads) reserve_kernel(const PageParams 
         for (int c0 = first[b]; c0 <= last[b]; c0 += 32) {
             const int c = c0 + lane;
             bool want = false;
+            int e = -1, holders = 0;
             if (c <= last[b]) {
-                const int e = row[c];
+                e = row[c];
                 want = e < 0;
                 if (e >= p.n_pages) {
                     raise_error(p.err, 0x1u);
                     want = true;   // a bad entry ahead is replaced
                 } else if (e >= 0) {
-                    const int holders = p.refs[e];
-                    if (holders > 1) {
-                        int before = 0;
-                        for (int o = 0; o < b; ++o)
-                            before += (c >= first[o] && c <= last[o] &&
-                                       p.table[static_cast<size_t>(o) * p.max_pages + c] == e);
-                        want = holders - before > 1;
-                    }
+                    holders = p.refs[e];
                 }
+            }
+            // shared pages (as a rule one per sequence, its current page): the warp counts the
+            // earlier sequences that reserve on the same page
+            for (uint32_t sh_m = __ballot_sync(kFull, holders > 1); sh_m != 0; sh_m &= sh_m - 1) {
+                const int src = __ffs(sh_m) - 1, page = __shfl_sync(kFull, e, src), col = c0 + src;
+                int before = 0;
+                for (int o = lane; o < b; o += 32)
+                    before += (col >= first[o] && col <= last[o] &&
+                               p.table[static_cast<size_t>(o) * p.max_pages + col] == page);
+                before = __reduce_add_sync(kFull, before);
+                if (lane == src)
+                    want = holders - before > 1;
             }
             const uint32_t m = __ballot_sync(kFull, want);
             if (lane == 0)
@@ -347,24 +353,6 @@ __global__ void __launch_bounds__(256) compact_move_kernel(const PageParams p, c
 
 // --------------------------------------------------------------------------- chunk appends
 
-// The sequence that owns packed row r: the last b with row_start[b] <= r. -1 behind the last.
-__device__ __forceinline__ int owner_of_row(const int32_t *start, int batch, int r)
-{
-    if (start == nullptr)
-        return r;
-    if (r < start[0] || r >= start[batch])
-        return -1;
-    int lo = 0, hi = batch;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (start[mid] <= r)
-            lo = mid;
-        else
-            hi = mid;
-    }
-    return lo;
-}
-
 // Whether sequence b's chunk is sound: rows within bounds, room in the cache.
 __device__ __forceinline__ bool chunk_ok(const ChunkParams &p, int b, int &r0, int &n, int &L,
                                          bool report)
@@ -387,52 +375,73 @@ __device__ __forceinline__ bool chunk_ok(const ChunkParams &p, int b, int &r0, i
 
 constexpr int kChunkRows = 8;   // rows per CTA
 
+// The cache row of (layer 0, head 0) for packed row r, -1 where it is not written. One warp,
+// every lane the same r: the row's sequence is the last b with row_start[b] <= r, found by
+// counting, so that the starts are read in one round trip.
+__device__ __forceinline__ long long chunk_dst(const ChunkParams &p, int r, int lane)
+{
+    int b = r;
+    if (r >= p.n_rows)
+        return -1;
+    if (p.row_start) {
+        int at = 0;
+        for (int i = lane; i <= p.pg.batch; i += 32)
+            at += p.row_start[i] <= r;
+        b = __reduce_add_sync(kFull, at) - 1;
+        if (b < 0 || b >= p.pg.batch)
+            return -1;
+    }
+    int s0, n, L;
+    if ((p.pg.active && !p.pg.active[b]) || !chunk_ok(p, b, s0, n, L, false) || r < s0 || r >= s0 + n)
+        return -1;
+    const int pos = L + r - s0;
+    if (p.pg.page_size == 0)
+        return static_cast<long long>(b) * p.pg.n_kv_heads * p.pg.capacity + pos;
+    const int page = p.pg.table[static_cast<size_t>(b) * p.pg.max_pages + (pos >> 4)];
+    if (page < 0 || page >= p.pg.n_pages)
+        return -1;
+    return static_cast<long long>(page) * p.pg.n_kv_heads * 16 + (pos & 15);
+}
+
+// The new rows are requested before their places are known (a chain of four loads), and the
+// warps find the places of the CTA's rows, one each, meanwhile.
 __global__ void __launch_bounds__(256) append_chunk_kernel(const ChunkParams p,
                                                            const uint4 *__restrict__ k_new,
                                                            const uint4 *__restrict__ v_new,
                                                            uint4 *__restrict__ k,
                                                            uint4 *__restrict__ v)
 {
-    __shared__ long long dst[kChunkRows];   // cache row of (layer 0, head 0), or -1
+    __shared__ long long dst[kChunkRows];
     pdl_trigger();
     pdl_wait();
-    const int r0 = blockIdx.x * kChunkRows, hkv = p.pg.n_kv_heads;
-    if (threadIdx.x < kChunkRows) {
-        const int r = r0 + threadIdx.x;
-        long long d = -1;
-        const int b = r < p.n_rows ? owner_of_row(p.row_start, p.pg.batch, r) : -1;
-        int s0, n, L;
-        if (b >= 0 && (!p.pg.active || p.pg.active[b]) && chunk_ok(p, b, s0, n, L, false) &&
-            r >= s0 && r < s0 + n) {
-            const int pos = L + r - s0;
-            if (p.pg.page_size == 0) {
-                d = static_cast<long long>(b) * hkv * p.pg.capacity + pos;
-            } else {
-                const int page = p.pg.table[static_cast<size_t>(b) * p.pg.max_pages + (pos >> 4)];
-                if (page >= 0 && page < p.pg.n_pages)
-                    d = static_cast<long long>(page) * hkv * 16 + (pos & 15);
-            }
-        }
-        dst[threadIdx.x] = d;
-    }
-    __syncthreads();
-    const int layer = blockIdx.y;
+    const int r0 = blockIdx.x * kChunkRows, hkv = p.pg.n_kv_heads, layer = blockIdx.y;
+    const int rows = min(kChunkRows, p.n_rows - r0);
+    const int per = hkv * 16;   // 16-byte pieces of one row of one tensor
     const long long head = p.pg.page_size ? 16 : p.pg.capacity;   // cache rows between heads
     const long long base = static_cast<long long>(layer) *
                            (p.pg.page_size ? static_cast<long long>(p.pg.n_pages) * hkv * 16
                                            : static_cast<long long>(p.pg.batch) * hkv * p.pg.capacity);
-    const int per = hkv * 16;   // 16-byte pieces of one row of one tensor
-    for (int i = threadIdx.x; i < 2 * per; i += 256) {
-        const bool is_v = i >= per;
+    bool known = false;
+    for (int i = threadIdx.x; i < 2 * per || !known; i += 256) {
+        const bool is_v = i >= per, on = i < 2 * per;
         const int j = is_v ? i - per : i;
         const uint4 *src = (is_v ? v_new : k_new) +
                            (static_cast<size_t>(layer) * p.n_rows + r0) * per + j;
-        uint4 *to = (is_v ? v : k) + (base + (j >> 4) * head) * 16 + (j & 15);
         uint4 x[kChunkRows];
 #pragma unroll
         for (int q = 0; q < kChunkRows; ++q)
-            if (dst[q] >= 0)
-                x[q] = __ldg(src + static_cast<size_t>(q) * per);
+            if (on && q < rows)
+                x[q] = __ldcs(src + static_cast<size_t>(q) * per);
+        if (!known) {   // (every thread's first step)
+            const long long d = chunk_dst(p, r0 + (threadIdx.x >> 5), threadIdx.x & 31);
+            if ((threadIdx.x & 31) == 0)
+                dst[threadIdx.x >> 5] = d;
+            __syncthreads();
+            known = true;
+        }
+        if (!on)
+            continue;
+        uint4 *to = (is_v ? v : k) + (base + (j >> 4) * head) * 16 + (j & 15);
 #pragma unroll
         for (int q = 0; q < kChunkRows; ++q)
             if (dst[q] >= 0)
@@ -498,48 +507,47 @@ __device__ __forceinline__ int moved_list(const int32_t *src, int batch, int2 *m
     return *count;
 }
 
-// Bulk rows: a [layers][batch][row16] matrix of 16-byte pieces whose rows (sequences) are
-// permuted in place. A CTA holds `cols` pieces of every moving sequence: it reads all of them
-// into shared memory, then writes them, so no other CTA and no scratch is involved. A piece
-// moves if its cache row is below the source's row count.
+// Bulk rows, [layers][batch][heads][rows_per_head] of 256 bytes, permuted over the batch in
+// place. A CTA holds the same few rows of one head of every moving sequence: each of its
+// threads reads its 16-byte pieces of them into registers, all at once, and writes them after
+// a barrier, so that no other CTA and no scratch is involved. A row moves if it is below the
+// source's row count. kPieces: pieces per thread, enough for a whole batch that moves.
+template <int kPieces>
 __global__ void __launch_bounds__(256) reorder_rows_kernel(const ReorderParams p, uint4 *k, uint4 *v,
-                                                           long long row16, int rows_per_head,
-                                                           const int32_t *rows, int rows_by_unit,
-                                                           int cols)
+                                                           int rows_per_head, const int32_t *rows,
+                                                           int rows_by_unit, int cols_log2)
 {
-    extern __shared__ uint4 stage[];
     __shared__ int2 mv[kMaxBatch];
+    __shared__ int have[kMaxBatch];
     __shared__ int n_mv;
     pdl_wait();
     const int n = moved_list(p.src, p.batch, mv, &n_mv, p.err, false);
-    if (n == 0)
-        return;
-    const int layer = blockIdx.y;
-    uint4 *t = (blockIdx.z ? v : k) + static_cast<long long>(layer) * p.batch * row16;
-    const long long c0 = static_cast<long long>(blockIdx.x) * cols;
-    auto live = [&](int i, long long col) {
-        if (col >= row16)
-            return false;
-        const int r = static_cast<int>(col >> 4);
-        const int head = r / rows_per_head, at = r - head * rows_per_head;
-        const int from = mv[i].y;
-        const int have = rows_by_unit ? rows[(static_cast<long long>(layer) * p.batch + from) * p.n_kv_heads + head]
-                                      : rows[from];
-        return at < have;
-    };
-    for (int i = threadIdx.x; i < n * cols; i += 256) {
-        const int m = i / cols;
-        const long long col = c0 + (i - m * cols);
-        if (live(m, col))
-            stage[i] = t[mv[m].y * row16 + col];
+    const int layer = blockIdx.y / p.n_kv_heads, head = blockIdx.y - layer * p.n_kv_heads;
+    for (int i = threadIdx.x; i < n; i += 256)
+        have[i] = rows_by_unit
+                      ? rows[(static_cast<long long>(layer) * p.batch + mv[i].y) * p.n_kv_heads + head]
+                      : rows[mv[i].y];
+    __syncthreads();
+    const long long stride = static_cast<long long>(p.n_kv_heads) * rows_per_head * 16;
+    uint4 *t = (blockIdx.z ? v : k) + static_cast<long long>(layer) * p.batch * stride +
+               static_cast<long long>(head) * rows_per_head * 16;
+    const int col = (static_cast<int>(blockIdx.x) << cols_log2) + (threadIdx.x & ((1 << cols_log2) - 1));
+    const int m0 = threadIdx.x >> cols_log2, step = 256 >> cols_log2;
+    uint4 x[kPieces];
+    uint32_t live = 0;
+#pragma unroll
+    for (int q = 0; q < kPieces; ++q) {
+        const int i = m0 + q * step;
+        if (i < n && (col >> 4) < min(have[i], rows_per_head)) {
+            live |= 1u << q;
+            x[q] = t[mv[i].y * stride + col];
+        }
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < n * cols; i += 256) {
-        const int m = i / cols;
-        const long long col = c0 + (i - m * cols);
-        if (live(m, col))
-            t[mv[m].x * row16 + col] = stage[i];
-    }
+#pragma unroll
+    for (int q = 0; q < kPieces; ++q)
+        if ((live >> q) & 1u)
+            t[mv[m0 + q * step].x * stride + col] = x[q];
 }
 
 // The int32 matrices [layers][batch][cols] of a sequence's state, permuted the same way, 32
@@ -632,18 +640,20 @@ cudaError_t launch_reorder_rows(const ReorderParams &p, void *k, void *v, int n_
                                 int rows_per_head, const int32_t *rows, int rows_by_unit,
                                 cudaStream_t stream)
 {
-    const long long row16 = static_cast<long long>(p.n_kv_heads) * rows_per_head * 16;
-    // 16 to 256 columns, so that a CTA's shared memory stays at 32 KB (64 KB from batch 129 on)
-    int cols = 2048 / p.batch;
-    cols = cols > 256 ? 256 : cols < 16 ? 16 : cols & ~15;
-    const size_t smem = static_cast<size_t>(p.batch) * cols * sizeof(uint4);
-    cudaError_t e = cudaFuncSetAttribute(reorder_rows_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         kMaxBatch * 16 * static_cast<int>(sizeof(uint4)));
-    if (e == cudaSuccess)
-        e = launch_pdl(reorder_rows_kernel,
-                       dim3(static_cast<unsigned>((row16 + cols - 1) / cols), n_layers, 2), dim3(256),
-                       smem, stream, p, static_cast<uint4 *>(k), static_cast<uint4 *>(v), row16,
-                       rows_per_head, rows, rows_by_unit, cols);
+    // pieces per sequence and CTA: a power of two such that the batch fits the threads' registers
+    // (8 each, 16 from batch 129 on); at most 256, at least one row
+    int lg = 8;
+    while (lg > 4 && (p.batch << lg) > 2048)
+        --lg;
+    const long long pieces = static_cast<long long>(rows_per_head) * 16;
+    const dim3 grid(static_cast<unsigned>((pieces + (1 << lg) - 1) >> lg), n_layers * p.n_kv_heads, 2);
+    uint4 *kp = static_cast<uint4 *>(k), *vp = static_cast<uint4 *>(v);
+    const cudaError_t e =
+        (p.batch << lg) <= 2048
+            ? launch_pdl(reorder_rows_kernel<8>, grid, dim3(256), 0, stream, p, kp, vp, rows_per_head,
+                         rows, rows_by_unit, lg)
+            : launch_pdl(reorder_rows_kernel<16>, grid, dim3(256), 0, stream, p, kp, vp, rows_per_head,
+                         rows, rows_by_unit, lg);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 

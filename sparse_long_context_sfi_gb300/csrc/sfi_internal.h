@@ -224,7 +224,7 @@ struct WindowParams {
     const int32_t *row_start;
     int n_rows, max_rows, n_sink, n_window;
     void *out;
-    int out_fp32;
+    int out_fp32, out_aligned32;
     uint32_t *err;
     float scale_log2;           // log2(e) / sqrt(128)
     int n_split;                // items that an item's key tiles are split over

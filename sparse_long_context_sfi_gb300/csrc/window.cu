@@ -84,6 +84,52 @@ __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t *v)
         : "memory");
 }
 
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t *v)
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+        "%11, %12, %13, %14, %15};" ::"r"(v[0]),
+        "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]),
+        "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(addr)
+        : "memory");
+}
+
+// Two floats at a time (sm_100 has packed fp32 adds and multiply-adds).
+__device__ __forceinline__ uint64_t pack2(float a, float b)
+{
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+    return d;
+}
+
+__device__ __forceinline__ float2 unpack2(uint64_t v)
+{
+    float2 f;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
+    return f;
+}
+
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
 __device__ __forceinline__ void tmem_st_wait()
 {
     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
@@ -195,25 +241,47 @@ __device__ __forceinline__ void wfail(WCtrl &c, uint32_t *err)
     raise_error(err, 0x4u);  // SFI_DEVERR_TIMEOUT
 }
 
-// 32 output values of one row.
-__device__ __forceinline__ void store32(const WindowParams &p, size_t at, const float *v)
+__device__ __forceinline__ void st_global32(void *p, const uint32_t *w)
+{
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]),
+                 "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+}
+
+// N (32 or 64) output values of one row, a thread per row: in 32-byte pieces, whole sectors,
+// where the output is aligned to them.
+template <int N>
+__device__ __forceinline__ void store_row(const WindowParams &p, size_t at, const float *v)
 {
     if (p.out_fp32) {
-        float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(p.out) + at);
+        float *o = static_cast<float *>(p.out) + at;
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            o[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-    } else {
-        uint32_t w[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-            w[i] = *reinterpret_cast<const uint32_t *>(&h);
+        for (int i = 0; i < N; i += 8) {
+            const uint32_t *w = reinterpret_cast<const uint32_t *>(v + i);
+            if (p.out_aligned32) {
+                st_global32(o + i, w);
+            } else {
+                *reinterpret_cast<uint4 *>(o + i) = make_uint4(w[0], w[1], w[2], w[3]);
+                *reinterpret_cast<uint4 *>(o + i + 4) = make_uint4(w[4], w[5], w[6], w[7]);
+            }
         }
-        uint4 *o = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) + at);
+    } else {
+        __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(p.out) + at;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            o[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+        for (int i = 0; i < N; i += 16) {
+            uint32_t w[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const __nv_bfloat162 h = __floats2bfloat162_rn(v[i + 2 * j], v[i + 2 * j + 1]);
+                w[j] = *reinterpret_cast<const uint32_t *>(&h);
+            }
+            if (p.out_aligned32) {
+                st_global32(o + i, w);
+            } else {
+                *reinterpret_cast<uint4 *>(o + i) = make_uint4(w[0], w[1], w[2], w[3]);
+                *reinterpret_cast<uint4 *>(o + i + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+            }
+        }
     }
 }
 
@@ -309,223 +377,14 @@ __global__ void __launch_bounds__(128 + 128 * NQ, NQ == 1 ? 2 : 1)
     auto s_col = [&](int a, int buf) { return tmem + a * (NS * KT + 128) + buf * KT; };
     auto o_col = [&](int a) { return tmem + a * (NS * KT + 128) + NS * KT; };
 
-    if (warp == 0) {
-        // ------------------------------------------------------------------ TMA producer
-        int use = 0, items = 0;
-        bool ok = true;
-        for (int idx = blockIdx.x; idx < total && ok; idx += gridDim.x) {
-            const WItem it = item_of<NQ, KT>(c, p, idx);
-            if (it.t0 == it.t1)
-                continue;
-            const long long unit = p.page_size
-                                       ? static_cast<long long>(it.layer) * p.n_pages * p.n_kv_heads
-                                       : static_cast<long long>(it.layer * p.batch + it.b) * p.n_kv_heads + it.kvh;
-            // cache row of list block j (a box of 16 rows), -16 (rows of zeros) where there is none
-            auto row_of = [&](int j) -> int {
-                if (j >= it.nb)
-                    return -16;
-                const int pos = j * 16 + (j < it.sb ? 0 : it.base);
-                if (p.page_size == 0)
-                    return static_cast<int>(unit * p.capacity + pos);
-                const int page = __ldg(p.page_table + static_cast<size_t>(it.b) * p.max_pages + (pos >> 4));
-                if (page < 0 || page >= p.n_pages) {
-                    raise_error(p.err, 0x1u);  // SFI_DEVERR_PAGE_RANGE
-                    return -16;
-                }
-                return static_cast<int>((unit + static_cast<long long>(page) * p.n_kv_heads + it.kvh) * 16);
-            };
-            // lane: block lane % kBlocks, 64-column half lane / kBlocks
-            const int blk = lane % kBlocks, half = lane / kBlocks;
-            int row = half < 2 ? row_of(it.t0 * kBlocks + blk) : 0;
-            if (lane == 0) {
-                ok = mbar_wait(&c.qe, (items & 1) ^ 1, &c.abort);
-                if (ok) {
-                    mbar_arrive_expect_tx(&c.qf, NQ * 32768);
-#pragma unroll
-                    for (int a = 0; a < NQ; ++a)
-#pragma unroll
-                        for (int h = 0; h < 2; ++h)
-                            tma_load_3d(smem + (2 * a + h) * kHalfQ, &tm_q, &c.qf, 64 * h, it.kvh * G,
-                                        it.layer * p.n_rows + it.r0 + a * (128 / G));
-                }
-            }
-            ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-            if (!ok)
-                break;
-            ++items;
-            for (int t = it.t0; t < it.t1; ++t) {
-                const int st = use % ST, ph = (use / ST) & 1;
-                uint8_t *k = kv_smem + st * kStage, *v = k + 2 * kHalfKV;
-                const int here = row;
-                if (half < 2 && t + 1 < it.t1)
-                    row = row_of((t + 1) * kBlocks + blk);
-                if (lane == 0) {
-                    ok = mbar_wait(&c.ke[st], ph ^ 1, &c.abort);
-                    if (ok)
-                        mbar_arrive_expect_tx(&c.kf[st], 2 * kHalfKV);
-                }
-                ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-                if (!ok)
-                    break;
-                if (half < 2)
-                    tma_load_2d(k + half * kHalfKV + blk * 2048, &tm_k, &c.kf[st], 64 * half, here);
-                if (lane == 0) {
-                    ok = mbar_wait(&c.ve[st], ph ^ 1, &c.abort);
-                    mbar_arrive_expect_tx(&c.vf[st], ok ? 2 * kHalfKV : 0);
-                }
-                ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-                if (ok && half < 2)
-                    tma_load_2d(v + half * kHalfKV + blk * 2048, &tm_v, &c.vf[st], 64 * half, here);
-                __syncwarp();
-                ++use;
-                if (!ok)
-                    break;
-            }
-        }
-        if (lane == 0) {
-            if (!ok)
-                wfail(c, p.err);
-            // never leave a copy in flight into shared memory that is given up
-            for (int j = max(0, use - ST); j < use; ++j) {
-                mbar_wait(&c.kf[j % ST], (j / ST) & 1, nullptr);
-                mbar_wait(&c.vf[j % ST], (j / ST) & 1, nullptr);
-            }
-            if (items > 0)
-                mbar_wait(&c.qf, (items - 1) & 1, nullptr);
-        }
-        __syncwarp();
-    } else if (warp == 1) {
-        // -------------------------------------------------------------------- MMA issuer
-        if (lane == 0) {
-            constexpr uint32_t idesc_s = idesc_bf16(128, KT, false, false);
-            constexpr uint32_t idesc_o = idesc_bf16(128, 128, false, true);
-            int kuse = 0, vuse = 0, items = 0;
-            uint32_t spend[2] = {0, 0};   // tiles of a q tile so far, all items
-            bool ok = true;
-            for (int idx = blockIdx.x; idx < total && ok; idx += gridDim.x) {
-                const WItem it = item_of<NQ, KT>(c, p, idx);
-                const int n = it.t1 - it.t0;
-                if (n == 0)
-                    continue;
-                ok = mbar_wait(&c.qf, items & 1, &c.abort);
-                if (!ok)
-                    break;
-                auto scores = [&](int a, int j, bool wait) -> bool {
-                    const int st = (kuse + j) % ST;
-                    if (wait && !mbar_wait(&c.kf[st], ((kuse + j) / ST) & 1, &c.abort))
-                        return false;
-                    tc_fence_after();
-                    const uint32_t ka = smem_u32(kv_smem + st * kStage), qa = smem_u32(smem + a * 2 * kHalfQ);
-                    const int buf = (spend[a] + j) % NS;
-#pragma unroll
-                    for (int kk = 0; kk < 8; ++kk)
-                        umma_bf16(s_col(a, buf),
-                                  smem_desc_sw128(qa + (kk >> 2) * kHalfQ + (kk & 3) * 32, 16, 1024),
-                                  smem_desc_sw128(ka + (kk >> 2) * kHalfKV + (kk & 3) * 32, 16, 1024),
-                                  idesc_s, kk > 0 ? 1u : 0u);
-                    umma_commit(&c.sf[a][buf]);
-                    return true;
-                };
-                auto scores_done = [&](int j) {
-                    umma_commit(&c.ke[(kuse + j) % ST]);
-                    if (j == n - 1)
-                        umma_commit(&c.qe);
-                };
-                for (int a = 0; a < NQ && ok; ++a)
-                    ok = scores(a, 0, a == 0);
-                if (!ok)
-                    break;
-                scores_done(0);
-                for (int j = 0; j < n && ok; ++j) {
-                    // with two score buffers the next scores are computed ahead of the softmax
-                    if (NS == 2 && j + 1 < n) {
-                        for (int a = 0; a < NQ && ok; ++a)
-                            ok = scores(a, j + 1, a == 0);
-                        if (!ok)
-                            break;
-                        scores_done(j + 1);
-                    }
-                    const int st = (vuse + j) % ST;
-                    for (int a = 0; a < NQ && ok; ++a) {
-                        const int buf = (spend[a] + j) % NS;
-                        ok = mbar_wait(&c.pf[a][buf], ((spend[a] + j) / NS) & 1, &c.abort) &&
-                             (j > 0 || mbar_wait(&c.oe[a], (items & 1) ^ 1, &c.abort)) &&
-                             (a > 0 || mbar_wait(&c.vr[st], ((vuse + j) / ST) & 1, &c.abort));
-                        if (!ok)
-                            break;
-                        tc_fence_after();
-                        const uint32_t va = smem_u32(kv_smem + st * kStage + 2 * kHalfKV);
-#pragma unroll
-                        for (int part = 0; part < (TWO ? 2 : 1); ++part)
-#pragma unroll
-                            for (int kk = 0; kk < kBlocks; ++kk)
-                                umma_bf16_ta(o_col(a), s_col(a, buf) + part * (KT / 2) + kk * 8,
-                                             smem_desc_sw128(va + kk * 2048, kHalfKV, 1024), idesc_o,
-                                             j > 0 || kk > 0 || part > 0 ? 1u : 0u);
-                        umma_commit(&c.od[a][buf]);
-                        if (a == NQ - 1)
-                            umma_commit(&c.ve[st]);
-                        if (NS == 1 && j + 1 < n) {
-                            ok = scores(a, j + 1, a == 0);
-                            if (ok && a == NQ - 1)
-                                scores_done(j + 1);
-                        }
-                    }
-                }
-                kuse += n;
-                vuse += n;
-                for (int a = 0; a < NQ; ++a)
-                    spend[a] += n;
-                ++items;
-            }
-            if (!ok)
-                wfail(c, p.err);
-            umma_commit(&c.drain);
-            mbar_wait(&c.drain, 0, nullptr);
-        }
-        __syncwarp();
-    } else if (warp == 2) {
-        // ------------------------------------------------- V rows that nobody may see := 0
-        int use = 0;
-        bool ok = true;
-        for (int idx = blockIdx.x; idx < total && ok; idx += gridDim.x) {
-            const WItem it = item_of<NQ, KT>(c, p, idx);
-            const int last = it.p0 + it.np - 1;
-            for (int t = it.t0; t < it.t1; ++t, ++use) {
-                const int st = use % ST;
-                ok = mbar_wait(&c.vf[st], (use / ST) & 1, &c.abort);
-                if (!__all_sync(0xffffffffu, ok)) {
-                    ok = false;
-                    break;
-                }
-                uint8_t *v = kv_smem + st * kStage + 2 * kHalfKV;
-                bool wrote = false;
-#pragma unroll
-                for (int i = 0; i < KT / 32; ++i) {
-                    const int r = i * 32 + lane, col = t * KT + r, blk = col >> 4;
-                    const int pos = col + (blk < it.sb ? 0 : it.base);
-                    // (blocks behind the list were filled with zeros)
-                    const bool seen = blk >= it.nb || (pos <= last && (pos < p.n_sink || pos >= it.lo));
-                    uint32_t m = __ballot_sync(0xffffffffu, !seen);
-                    wrote = wrote || m != 0;
-                    while (m) {
-                        const int rr = i * 32 + __ffs(m) - 1;
-                        m &= m - 1;
-                        if (lane < 16)
-                            reinterpret_cast<uint4 *>(v + (lane >> 3) * kHalfKV + rr * 128)[lane & 7] =
-                                make_uint4(0, 0, 0, 0);
-                    }
-                }
-                if (wrote)
-                    fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(&c.vr[st]);
-            }
-        }
-        if (!ok && lane == 0)
-            wfail(c, p.err);
-    } else if (warp >= 4) {
+    // Registers: the softmax keeps a whole score row; the first warpgroup gives up what it does
+    // not need (launched with 168 or 128 a thread: 384 * 168 = 256 * 216 + 128 * 72,
+    // 256 * 128 = 128 * 184 + 128 * 72).
+    if (warp >= 4) {
+        if (NQ == 2)
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+        else
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
         // ------------------------------------------------------------------------ softmax
         const int a = (warp - 4) >> 2, quad = warp & 3, rowi = quad * 32 + lane;
         const uint32_t lane_addr = static_cast<uint32_t>(quad * 32) << 16;
@@ -565,21 +424,31 @@ __global__ void __launch_bounds__(128 + 128 * NQ, NQ == 1 ? 2 : 1)
                     tmem_landed(s + 32 * q);
                 const int c0 = t * KT;
                 const bool whole = a2 <= c0 && e2 >= c0 + KT;
+                uint32_t hidden = 0;        // 32-column chunks that no row of the warp sees
                 if (!__all_sync(0xffffffffu, whole)) {
 #pragma unroll
                     for (int w = 0; w < KT / 32; ++w) {
                         const uint32_t see = span_bits(0, e1 - c0, w) | span_bits(a2 - c0, e2 - c0, w);
+                        if (!__any_sync(0xffffffffu, valid && see != 0u)) {
+                            hidden |= 1u << w;
+                        } else if (!__all_sync(0xffffffffu, see == 0xffffffffu)) {
 #pragma unroll
-                        for (int x = 0; x < 32; ++x)
-                            s[32 * w + x] = (see >> x) & 1u ? s[32 * w + x] : -CUDART_INF_F;
+                            for (int x = 0; x < 32; ++x)
+                                s[32 * w + x] = (see >> x) & 1u ? s[32 * w + x] : -CUDART_INF_F;
+                        }
                     }
                 }
                 float mx[4] = {m, m, m, m};
 #pragma unroll
-                for (int x = 0; x < KT; x += 8) {
+                for (int w = 0; w < KT / 32; ++w) {
+                    if ((hidden >> w) & 1u)
+                        continue;
 #pragma unroll
-                    for (int y = 0; y < 4; ++y)
-                        mx[y] = fmaxf(mx[y], fmaxf(s[x + y], s[x + 4 + y]));
+                    for (int x = 0; x < 32; x += 8) {
+#pragma unroll
+                        for (int y = 0; y < 4; ++y)
+                            mx[y] = max3(mx[y], s[32 * w + x + 2 * y], s[32 * w + x + 2 * y + 1]);
+                    }
                 }
                 const float mn = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
                 const bool grow = (mn - m) * sc > 8.f;      // (from -inf: always, unless still -inf)
@@ -592,7 +461,7 @@ __global__ void __launch_bounds__(128 + 128 * NQ, NQ == 1 ? 2 : 1)
                     tc_fence_after();
                     l *= alpha;
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
+                    for (int q = 0; q < 4; ++q) {   // (rare: kept short of registers)
                         float o[32];
                         tmem_ld32(o_col(a) + lane_addr + 32 * q, o);
                         tmem_landed(o);
@@ -604,29 +473,36 @@ __global__ void __launch_bounds__(128 + 128 * NQ, NQ == 1 ? 2 : 1)
                 }
                 m = grow ? mn : m;
                 const float off = m == -CUDART_INF_F ? 0.f : -m * sc;
-                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                const uint64_t sc2 = pack2(sc, sc), off2 = pack2(off, off);
+                uint64_t sum[2] = {0, 0};
 #pragma unroll
-                for (int q = 0; q < KT / 64; ++q) {
-                    uint32_t w[32], r[TWO ? 32 : 1];
+                for (int q = 0; q < KT / 32; ++q) {
+                    uint32_t w[16], r[TWO ? 16 : 1];
+                    if ((hidden >> q) & 1u) {
 #pragma unroll
-                    for (int x = 0; x < 32; ++x) {
-                        const float p0 = ex2_approx(fmaf(s[64 * q + 2 * x], sc, off));
-                        const float p1 = ex2_approx(fmaf(s[64 * q + 2 * x + 1], sc, off));
-                        sum[(2 * x) & 3] += p0;
-                        sum[(2 * x + 1) & 3] += p1;
-                        const __nv_bfloat162 hi = __floats2bfloat162_rn(p0, p1);
-                        w[x] = *reinterpret_cast<const uint32_t *>(&hi);
-                        if (TWO) {
-                            const float2 b = __bfloat1622float2(hi);
-                            const __nv_bfloat162 lo = __floats2bfloat162_rn(p0 - b.x, p1 - b.y);
-                            r[TWO ? x : 0] = *reinterpret_cast<const uint32_t *>(&lo);
+                        for (int x = 0; x < 16; ++x)
+                            w[x] = r[TWO ? x : 0] = 0u;
+                    } else {
+#pragma unroll
+                        for (int x = 0; x < 16; ++x) {
+                            const float2 z = unpack2(fma2(pack2(s[32 * q + 2 * x], s[32 * q + 2 * x + 1]), sc2, off2));
+                            const float p0 = ex2_approx(z.x), p1 = ex2_approx(z.y);
+                            sum[x & 1] = add2(sum[x & 1], pack2(p0, p1));
+                            const __nv_bfloat162 hi = __floats2bfloat162_rn(p0, p1);
+                            w[x] = *reinterpret_cast<const uint32_t *>(&hi);
+                            if (TWO) {
+                                const float2 b = __bfloat1622float2(hi);
+                                const __nv_bfloat162 lo = __floats2bfloat162_rn(p0 - b.x, p1 - b.y);
+                                r[TWO ? x : 0] = *reinterpret_cast<const uint32_t *>(&lo);
+                            }
                         }
                     }
-                    tmem_st32(sa + 32 * q, w);
+                    tmem_st16(sa + 16 * q, w);
                     if (TWO)
-                        tmem_st32(sa + KT / 2 + 32 * q, r);
+                        tmem_st16(sa + KT / 2 + 16 * q, r);
                 }
-                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                const float2 sums = unpack2(add2(sum[0], sum[1]));
+                l += sums.x + sums.y;
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
@@ -650,29 +526,33 @@ __global__ void __launch_bounds__(128 + 128 * NQ, NQ == 1 ? 2 : 1)
             const float inv = p.n_split == 1 ? 1.f / l : 1.f;
             if (any) {
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    float o[32];
-                    tmem_ld32(o_col(a) + lane_addr + 32 * q, o);
+                for (int q = 0; q < 2; ++q) {
+                    float o[64];
+                    tmem_ld32(o_col(a) + lane_addr + 64 * q, o);
+                    tmem_ld32(o_col(a) + lane_addr + 64 * q + 32, o + 32);
                     tmem_landed(o);
+                    tmem_landed(o + 32);
+                    if (q == 1) {
+                        // O is free for the next item
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0)
+                            mbar_arrive(&c.oe[a]);
+                    }
                     if (valid) {
 #pragma unroll
-                        for (int x = 0; x < 32; ++x)
+                        for (int x = 0; x < 64; ++x)
                             o[x] *= inv;
                         if (p.n_split == 1) {
-                            store32(p, out_at + 32 * q, o);
+                            store_row<64>(p, out_at + 64 * q, o);
                         } else {
-                            float4 *w = reinterpret_cast<float4 *>(
-                                p.parts + (part * p.part_rows + rq) * kHeadDim + 32 * q);
+                            float *w = p.parts + (part * p.part_rows + rq) * kHeadDim + 64 * q;
 #pragma unroll
-                            for (int x = 0; x < 8; ++x)
-                                w[x] = make_float4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
+                            for (int x = 0; x < 64; x += 8)
+                                st_global32(w + x, reinterpret_cast<const uint32_t *>(o + x));
                         }
                     }
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(&c.oe[a]);
             }
             if (p.n_split > 1) {
                 if (valid)
@@ -720,6 +600,228 @@ __global__ void __launch_bounds__(128 + 128 * NQ, NQ == 1 ? 2 : 1)
         }
         if (!ok && lane == 0)
             wfail(c, p.err);
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        if (warp == 0) {
+            // ------------------------------------------------------------------ TMA producer
+            int use = 0, items = 0;
+            bool ok = true;
+            for (int idx = blockIdx.x; idx < total && ok; idx += gridDim.x) {
+                const WItem it = item_of<NQ, KT>(c, p, idx);
+                if (it.t0 == it.t1)
+                    continue;
+                const long long unit = p.page_size
+                                           ? static_cast<long long>(it.layer) * p.n_pages * p.n_kv_heads
+                                           : static_cast<long long>(it.layer * p.batch + it.b) * p.n_kv_heads + it.kvh;
+                // cache row of list block j (a box of 16 rows), -16 (rows of zeros) where there is none
+                auto row_of = [&](int j) -> int {
+                    if (j >= it.nb)
+                        return -16;
+                    const int pos = j * 16 + (j < it.sb ? 0 : it.base);
+                    if (p.page_size == 0)
+                        return static_cast<int>(unit * p.capacity + pos);
+                    const int page = __ldg(p.page_table + static_cast<size_t>(it.b) * p.max_pages + (pos >> 4));
+                    if (page < 0 || page >= p.n_pages) {
+                        raise_error(p.err, 0x1u);  // SFI_DEVERR_PAGE_RANGE
+                        return -16;
+                    }
+                    return static_cast<int>((unit + static_cast<long long>(page) * p.n_kv_heads + it.kvh) * 16);
+                };
+                // lane: block lane % kBlocks, 64-column half lane / kBlocks
+                const int blk = lane % kBlocks, half = lane / kBlocks;
+                int row = half < 2 ? row_of(it.t0 * kBlocks + blk) : 0;
+                bool have_q = false;
+                for (int t = it.t0; t < it.t1; ++t) {
+                    const int st = use % ST, ph = (use / ST) & 1;
+                    uint8_t *k = kv_smem + st * kStage, *v = k + 2 * kHalfKV;
+                    const int here = row;
+                    if (half < 2 && t + 1 < it.t1)
+                        row = row_of((t + 1) * kBlocks + blk);
+                    if (lane == 0) {
+                        ok = mbar_wait(&c.ke[st], ph ^ 1, &c.abort);
+                        if (ok)
+                            mbar_arrive_expect_tx(&c.kf[st], 2 * kHalfKV);
+                    }
+                    ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+                    if (!ok)
+                        break;
+                    if (half < 2)
+                        tma_load_2d(k + half * kHalfKV + blk * 2048, &tm_k, &c.kf[st], 64 * half, here);
+                    if (!have_q && lane == 0) {
+                        // the queries behind the first keys: they wait for the last item's scores
+                        ok = mbar_wait(&c.qe, (items & 1) ^ 1, &c.abort);
+                        if (ok) {
+                            mbar_arrive_expect_tx(&c.qf, NQ * 32768);
+#pragma unroll
+                            for (int a = 0; a < NQ; ++a)
+#pragma unroll
+                                for (int h = 0; h < 2; ++h)
+                                    tma_load_3d(smem + (2 * a + h) * kHalfQ, &tm_q, &c.qf, 64 * h, it.kvh * G,
+                                                it.layer * p.n_rows + it.r0 + a * (128 / G));
+                        }
+                    }
+                    if (!have_q) {
+                        have_q = true;
+                        if (__shfl_sync(0xffffffffu, ok ? 1 : 0, 0))
+                            ++items;
+                    }
+                    if (lane == 0) {
+                        ok = ok && mbar_wait(&c.ve[st], ph ^ 1, &c.abort);
+                        mbar_arrive_expect_tx(&c.vf[st], ok ? 2 * kHalfKV : 0);
+                    }
+                    ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+                    if (ok && half < 2)
+                        tma_load_2d(v + half * kHalfKV + blk * 2048, &tm_v, &c.vf[st], 64 * half, here);
+                    __syncwarp();
+                    ++use;
+                    if (!ok)
+                        break;
+                }
+            }
+            if (lane == 0) {
+                if (!ok)
+                    wfail(c, p.err);
+                // never leave a copy in flight into shared memory that is given up
+                for (int j = max(0, use - ST); j < use; ++j) {
+                    mbar_wait(&c.kf[j % ST], (j / ST) & 1, nullptr);
+                    mbar_wait(&c.vf[j % ST], (j / ST) & 1, nullptr);
+                }
+                if (items > 0)
+                    mbar_wait(&c.qf, (items - 1) & 1, nullptr);
+            }
+            __syncwarp();
+        } else if (warp == 1) {
+            // -------------------------------------------------------------------- MMA issuer
+            if (lane == 0) {
+                constexpr uint32_t idesc_s = idesc_bf16(128, KT, false, false);
+                constexpr uint32_t idesc_o = idesc_bf16(128, 128, false, true);
+                int kuse = 0, vuse = 0, items = 0;
+                uint32_t spend[2] = {0, 0};   // tiles of a q tile so far, all items
+                bool ok = true;
+                for (int idx = blockIdx.x; idx < total && ok; idx += gridDim.x) {
+                    const WItem it = item_of<NQ, KT>(c, p, idx);
+                    const int n = it.t1 - it.t0;
+                    if (n == 0)
+                        continue;
+                    ok = mbar_wait(&c.qf, items & 1, &c.abort);
+                    if (!ok)
+                        break;
+                    auto scores = [&](int a, int j, bool wait) -> bool {
+                        const int st = (kuse + j) % ST;
+                        if (wait && !mbar_wait(&c.kf[st], ((kuse + j) / ST) & 1, &c.abort))
+                            return false;
+                        tc_fence_after();
+                        const uint32_t ka = smem_u32(kv_smem + st * kStage), qa = smem_u32(smem + a * 2 * kHalfQ);
+                        const int buf = (spend[a] + j) % NS;
+#pragma unroll
+                        for (int kk = 0; kk < 8; ++kk)
+                            umma_bf16(s_col(a, buf),
+                                      smem_desc_sw128(qa + (kk >> 2) * kHalfQ + (kk & 3) * 32, 16, 1024),
+                                      smem_desc_sw128(ka + (kk >> 2) * kHalfKV + (kk & 3) * 32, 16, 1024),
+                                      idesc_s, kk > 0 ? 1u : 0u);
+                        umma_commit(&c.sf[a][buf]);
+                        return true;
+                    };
+                    auto scores_done = [&](int j) {
+                        umma_commit(&c.ke[(kuse + j) % ST]);
+                        if (j == n - 1)
+                            umma_commit(&c.qe);
+                    };
+                    for (int a = 0; a < NQ && ok; ++a)
+                        ok = scores(a, 0, a == 0);
+                    if (!ok)
+                        break;
+                    scores_done(0);
+                    for (int j = 0; j < n && ok; ++j) {
+                        // with two score buffers the next scores are computed ahead of the softmax
+                        if (NS == 2 && j + 1 < n) {
+                            for (int a = 0; a < NQ && ok; ++a)
+                                ok = scores(a, j + 1, a == 0);
+                            if (!ok)
+                                break;
+                            scores_done(j + 1);
+                        }
+                        const int st = (vuse + j) % ST;
+                        for (int a = 0; a < NQ && ok; ++a) {
+                            const int buf = (spend[a] + j) % NS;
+                            ok = mbar_wait(&c.pf[a][buf], ((spend[a] + j) / NS) & 1, &c.abort) &&
+                                 (j > 0 || mbar_wait(&c.oe[a], (items & 1) ^ 1, &c.abort)) &&
+                                 (a > 0 || mbar_wait(&c.vr[st], ((vuse + j) / ST) & 1, &c.abort));
+                            if (!ok)
+                                break;
+                            tc_fence_after();
+                            const uint32_t va = smem_u32(kv_smem + st * kStage + 2 * kHalfKV);
+#pragma unroll
+                            for (int part = 0; part < (TWO ? 2 : 1); ++part)
+#pragma unroll
+                                for (int kk = 0; kk < kBlocks; ++kk)
+                                    umma_bf16_ta(o_col(a), s_col(a, buf) + part * (KT / 2) + kk * 8,
+                                                 smem_desc_sw128(va + kk * 2048, kHalfKV, 1024), idesc_o,
+                                                 j > 0 || kk > 0 || part > 0 ? 1u : 0u);
+                            umma_commit(&c.od[a][buf]);
+                            if (a == NQ - 1)
+                                umma_commit(&c.ve[st]);
+                            if (NS == 1 && j + 1 < n) {
+                                ok = scores(a, j + 1, a == 0);
+                                if (ok && a == NQ - 1)
+                                    scores_done(j + 1);
+                            }
+                        }
+                    }
+                    kuse += n;
+                    vuse += n;
+                    for (int a = 0; a < NQ; ++a)
+                        spend[a] += n;
+                    ++items;
+                }
+                if (!ok)
+                    wfail(c, p.err);
+                umma_commit(&c.drain);
+                mbar_wait(&c.drain, 0, nullptr);
+            }
+            __syncwarp();
+        } else if (warp == 2) {
+            // ------------------------------------------------- V rows that nobody may see := 0
+            int use = 0;
+            bool ok = true;
+            for (int idx = blockIdx.x; idx < total && ok; idx += gridDim.x) {
+                const WItem it = item_of<NQ, KT>(c, p, idx);
+                const int last = it.p0 + it.np - 1;
+                for (int t = it.t0; t < it.t1; ++t, ++use) {
+                    const int st = use % ST;
+                    ok = mbar_wait(&c.vf[st], (use / ST) & 1, &c.abort);
+                    if (!__all_sync(0xffffffffu, ok)) {
+                        ok = false;
+                        break;
+                    }
+                    uint8_t *v = kv_smem + st * kStage + 2 * kHalfKV;
+                    bool wrote = false;
+#pragma unroll
+                    for (int i = 0; i < KT / 32; ++i) {
+                        const int r = i * 32 + lane, col = t * KT + r, blk = col >> 4;
+                        const int pos = col + (blk < it.sb ? 0 : it.base);
+                        // (blocks behind the list were filled with zeros)
+                        const bool seen = blk >= it.nb || (pos <= last && (pos < p.n_sink || pos >= it.lo));
+                        uint32_t m = __ballot_sync(0xffffffffu, !seen);
+                        wrote = wrote || m != 0;
+                        while (m) {
+                            const int rr = i * 32 + __ffs(m) - 1;
+                            m &= m - 1;
+                            if (lane < 16)
+                                reinterpret_cast<uint4 *>(v + (lane >> 3) * kHalfKV + rr * 128)[lane & 7] =
+                                    make_uint4(0, 0, 0, 0);
+                        }
+                    }
+                    if (wrote)
+                        fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(&c.vr[st]);
+                }
+            }
+            if (!ok && lane == 0)
+                wfail(c, p.err);
+        }
     }
     __syncwarp();
     tc_fence_before();
