@@ -155,8 +155,10 @@ __device__ __forceinline__ void load_chunk(const T *row, int shift, int vocab, i
 template <typename T>
 __global__ void __launch_bounds__(kBeamThreads, 4) beam_kernel(const BeamParams p)
 {
-    __shared__ float sh_x[kBeamWarps][kMaxBeams], sh_m[kBeamWarps], sh_s[kBeamWarps];
-    __shared__ int sh_v[kBeamWarps][kMaxBeams];
+    __shared__ float sh_x[kMaxBeams][kBeamWarps], sh_m[kBeamWarps], sh_s[kBeamWarps];
+    __shared__ int sh_v[kMaxBeams][kBeamWarps];
+    __shared__ float cand_x[kBeamWarps][32 * kLaneTok];   // a chunk's candidates, in any order
+    __shared__ int cand_v[kBeamWarps][32 * kLaneTok], n_cand[kBeamWarps];
     __shared__ float row_x[kMaxBeams][kMaxBeams], row_s[kMaxBeams][kMaxBeams];
     __shared__ int row_v[kMaxBeams][kMaxBeams];
     __shared__ uint8_t row_done[kMaxBeams];
@@ -207,40 +209,46 @@ __global__ void __launch_bounds__(kBeamThreads, 4) beam_kernel(const BeamParams 
                 for (int j = 0; j < kLaneTok; ++j)
                     s = x[j] == -CUDART_INF_F ? s : CUDART_NAN_F;
             }
-            // Tokens that beat the K-th best (in a warp's first chunk the list is empty): each
-            // lane offers its best, and again as long as some lane has another one.
+            // Tokens that beat the K-th best so far. A warp's first chunk starts the list with
+            // every lane's best; the others that still beat it go through shared memory.
             if (__any_sync(kAll, cm > best.tx || best.tv < 0)) {
-                uint32_t left = 0;      // tokens not offered yet
                 const int v0 = (c + lane) * V - shift;
-                // (positions only grow with j, so the first of equal logits is the lowest token)
+                // (tokens grow with j, so the first of equal logits is the lowest token)
                 auto token = [&](int j) { return v0 + 32 * V * (j / V) + j % V; };
-#pragma unroll
-                for (int j = 0; j < kLaneTok; ++j)
-                    left |= token(j) >= 0 && token(j) < p.vocab ? 1u << j : 0u;
-                for (;;) {
+                int taken = -1;
+                if (fresh) {
                     float cx = -CUDART_INF_F;
-                    int cj = -1;
 #pragma unroll
                     for (int j = kLaneTok - 1; j >= 0; --j) {
-                        if (((left >> j) & 1u) && x[j] >= cx) {
+                        if (x[j] >= cx && token(j) >= 0 && token(j) < p.vocab) {
                             cx = x[j];
-                            cj = j;
+                            taken = token(j);
                         }
                     }
-                    const int cv = cj < 0 ? -1 : token(cj);
-                    left &= cj < 0 ? 0u : ~(1u << cj);
-                    if (fresh)
-                        best.start(cx, cv, K, lane);
-                    else
-                        best.offer(cx, cv, K, lane);
+                    best.start(cx, taken, K, lane);
                     fresh = false;
-                    bool more = false;
-#pragma unroll
-                    for (int j = 0; j < kLaneTok; ++j)
-                        more = more || (((left >> j) & 1u) && better(x[j], token(j), best.tx, best.tv));
-                    if (!__any_sync(kAll, more))
-                        break;
                 }
+                if (lane == 0)
+                    n_cand[warp] = 0;
+                __syncwarp();
+#pragma unroll
+                for (int j = 0; j < kLaneTok; ++j) {
+                    if (x[j] >= best.tx) {
+                        const int v = token(j);
+                        if (v != taken && v >= 0 && v < p.vocab) {
+                            const int at = atomicAdd(&n_cand[warp], 1);
+                            cand_x[warp][at] = x[j];
+                            cand_v[warp][at] = v;
+                        }
+                    }
+                }
+                __syncwarp();
+                const int n = n_cand[warp];
+                for (int i = 0; i < n; i += 32) {
+                    const bool on = i + lane < n;
+                    best.offer(on ? cand_x[warp][i + lane] : 0.f, on ? cand_v[warp][i + lane] : -1, K, lane);
+                }
+                __syncwarp();
             }
         }
         // the warp's maximum and sum
@@ -256,17 +264,17 @@ __global__ void __launch_bounds__(kBeamThreads, 4) beam_kernel(const BeamParams 
             sh_m[warp] = wm;
             sh_s[warp] = ws;
         }
-        // the CTA's best: warps pair off
-#pragma unroll
-        for (int half = kBeamWarps / 2; half > 0; half >>= 1) {
-            if (warp >= half && warp < 2 * half && lane < K) {
-                sh_x[warp][lane] = best.x;
-                sh_v[warp][lane] = best.v;
-            }
-            __syncthreads();
-            if (warp < half)
-                best.offer(lane < K ? sh_x[warp + half][lane] : 0.f,
-                           lane < K ? sh_v[warp + half][lane] : -1, K, lane);
+        // the CTA's best: all warps' j-th before any (j + 1)-th, so that the first 32 settle most
+        if (lane < K) {
+            sh_x[lane][warp] = best.x;
+            sh_v[lane][warp] = best.v;
+        }
+        __syncthreads();
+        if (warp == 0) {
+            best.start((&sh_x[0][0])[lane], lane < K * kBeamWarps ? (&sh_v[0][0])[lane] : -1, K, lane);
+            for (int i = 32; i < K * kBeamWarps; i += 32)
+                best.offer((&sh_x[0][0])[i + lane], i + lane < K * kBeamWarps ? (&sh_v[0][0])[i + lane] : -1,
+                           K, lane);
         }
         const size_t part = static_cast<size_t>(row) * p.splits + split;
         if (warp == 0) {
@@ -283,8 +291,9 @@ __global__ void __launch_bounds__(kBeamThreads, 4) beam_kernel(const BeamParams 
             if (lane == 0)
                 p.part_stat[part] = make_float2(bm, bs);
             if (lane < K) {
-                p.part_x[part * K + lane] = best.x;
-                p.part_v[part * K + lane] = best.v;
+                const size_t at = (static_cast<size_t>(row) * K + lane) * p.splits + split;
+                p.part_x[at] = best.x;
+                p.part_v[at] = best.v;
             }
             __threadfence();
         }
@@ -304,6 +313,11 @@ __global__ void __launch_bounds__(kBeamThreads, 4) beam_kernel(const BeamParams 
         const int r = group * K + b;
         const float cum = p.cum[r], scale = p.rank_scale ? p.rank_scale[r] : 1.f;
         const bool fin = p.done && p.done[r];
+        // (requested together; a finished row's are not there and not used)
+        const size_t part = static_cast<size_t>(r) * p.splits, list = part * K;
+        const int n = p.splits * K;
+        const float cx = lane < n ? __ldcg(p.part_x + list + lane) : 0.f;
+        const int cv = lane < n ? __ldcg(p.part_v + list + lane) : -1;
         Best best;
         best.clear();
         float score = -CUDART_INF_F;
@@ -313,7 +327,6 @@ __global__ void __launch_bounds__(kBeamThreads, 4) beam_kernel(const BeamParams 
                 score = isfinite(cum) ? cum : -CUDART_INF_F;
             }
         } else {
-            const size_t part = static_cast<size_t>(r) * p.splits;
             float m = -CUDART_INF_F, s = 0.f;
             for (int i = lane; i < p.splits; i += 32) {
                 const float2 st = __ldcg(p.part_stat + part + i);
@@ -338,16 +351,14 @@ __global__ void __launch_bounds__(kBeamThreads, 4) beam_kernel(const BeamParams 
             if (dead) {
                 best.v = lane < K && lane < p.vocab ? lane : -1;
             } else {
-                float cx = lane < K ? __ldcg(p.part_x + part * K + lane) : 0.f;
-                int cv = lane < K ? __ldcg(p.part_v + part * K + lane) : -1;
-                for (int i = 0; i < p.splits; ++i) {
-                    const float ox = cx;
-                    const int ov = cv;
-                    if (i + 1 < p.splits && lane < K) {
-                        cx = __ldcg(p.part_x + (part + i + 1) * K + lane);
-                        cv = __ldcg(p.part_v + (part + i + 1) * K + lane);
-                    }
-                    best.offer(ox, ov, K, lane);
+                // all splits' j-th before any (j + 1)-th
+                for (int i = 0; i < n; i += 32) {
+                    const float ox = i == 0 ? cx : i + lane < n ? __ldcg(p.part_x + list + i + lane) : 0.f;
+                    const int ov = i == 0 ? cv : i + lane < n ? __ldcg(p.part_v + list + i + lane) : -1;
+                    if (i == 0)
+                        best.start(ox, ov, K, lane);
+                    else
+                        best.offer(ox, ov, K, lane);
                 }
                 score = cum + ((best.x - wm) - ls);
             }
@@ -366,9 +377,16 @@ __global__ void __launch_bounds__(kBeamThreads, 4) beam_kernel(const BeamParams 
     if (warp == 0) {
         Best best;
         best.clear();
-        for (int b = 0; b < K; ++b)
-            best.offer(lane < K ? row_x[b][lane] : 0.f,
-                       lane < K && row_v[b][lane] >= 0 ? b * kMaxBeams + lane : -1, K, lane);
+        // (place by place over the rows: the first 32 settle most)
+        for (int i = 0; i < K * K; i += 32) {
+            const int at = i + lane, j = at / K, b = at - j * K;
+            const bool on = at < K * K && row_v[min(b, kMaxBeams - 1)][min(j, kMaxBeams - 1)] >= 0;
+            const float ox = on ? row_x[b][j] : 0.f;
+            if (i == 0)
+                best.start(ox, on ? b * kMaxBeams + j : -1, K, lane);
+            else
+                best.offer(ox, on ? b * kMaxBeams + j : -1, K, lane);
+        }
         if (lane < K) {
             const int id = max(best.v, 0);   // (all places are filled unless a scale is not a number)
             const int b = id / kMaxBeams, j = id % kMaxBeams, o = group * K + lane;

@@ -208,7 +208,7 @@ struct BeamParams {
     uint8_t *done_out;
     int *tickets;               // [n_groups], zero between launches
     float2 *part_stat;          // [rows][splits]: maximum, sum of exp(x - maximum)
-    float *part_x;              // [rows][splits][n_beams] best logits, descending
+    float *part_x;              // [rows][n_beams][splits] best logits, descending over places
     int32_t *part_v;            // and their tokens (-1: none)
 };
 cudaError_t launch_beam_select(const BeamParams &p, cudaStream_t stream);
