@@ -157,6 +157,22 @@ __device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, u
         : "memory");
 }
 
+// Every lane waits; the answer is the same in all of them.
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort)
+{
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort)) != 0;
+}
+
+// A value that all lanes have, as one that the compiler knows to be uniform over the warp.
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __reduce_or_sync(0xffffffffu, v); }
+
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred P;\n\telect.sync _|P, 0xffffffff;\n\tselp.u32 %0, 1, 0, P;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
 // Bits [lo, hi) of word w of a column mask (columns 32 w .. 32 w + 31).
 __device__ __forceinline__ uint32_t span_bits(int lo, int hi, int w)
 {
@@ -395,8 +411,7 @@ __global__ void __launch_bounds__(128 + 128 * NQ, NQ == 1 ? 2 : 1)
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(&c.gs);
-            const bool good = mbar_wait(&c.gs, syncs++ & 1, &c.abort);
-            return __all_sync(0xffffffffu, good);
+            return warp_wait(&c.gs, syncs++ & 1, &c.abort);
         };
         const int rq = a * 128 + rowi;
         for (int idx = blockIdx.x; idx < total && ok; idx += gridDim.x) {
@@ -409,8 +424,7 @@ __global__ void __launch_bounds__(128 + 128 * NQ, NQ == 1 ? 2 : 1)
             float m = -CUDART_INF_F, l = 0.f;
             for (int t = it.t0; t < it.t1; ++t, ++done) {
                 const int buf = done % NS;
-                ok = mbar_wait(&c.sf[a][buf], (done / NS) & 1, &c.abort);
-                ok = __all_sync(0xffffffffu, ok);
+                ok = warp_wait(&c.sf[a][buf], (done / NS) & 1, &c.abort);
                 if (!ok)
                     break;
                 tc_fence_after();
@@ -454,8 +468,7 @@ __global__ void __launch_bounds__(128 + 128 * NQ, NQ == 1 ? 2 : 1)
                 const bool grow = (mn - m) * sc > 8.f;      // (from -inf: always, unless still -inf)
                 if (__any_sync(0xffffffffu, grow) && t > it.t0) {
                     const float alpha = grow ? ex2_approx((m - mn) * sc) : 1.f;
-                    ok = mbar_wait(&c.od[a][(done - 1) % NS], ((done - 1) / NS) & 1, &c.abort);
-                    ok = __all_sync(0xffffffffu, ok);
+                    ok = warp_wait(&c.od[a][(done - 1) % NS], ((done - 1) / NS) & 1, &c.abort);
                     if (!ok)
                         break;
                     tc_fence_after();
@@ -514,8 +527,7 @@ __global__ void __launch_bounds__(128 + 128 * NQ, NQ == 1 ? 2 : 1)
             // ------------------------------------------------------------------ epilogue
             const bool any = it.t1 > it.t0;
             if (any) {
-                ok = mbar_wait(&c.od[a][(done - 1) % NS], ((done - 1) / NS) & 1, &c.abort);
-                ok = __all_sync(0xffffffffu, ok);
+                ok = warp_wait(&c.od[a][(done - 1) % NS], ((done - 1) / NS) & 1, &c.abort);
                 if (!ok)
                     break;
                 tc_fence_after();
@@ -692,93 +704,102 @@ __global__ void __launch_bounds__(128 + 128 * NQ, NQ == 1 ? 2 : 1)
             __syncwarp();
         } else if (warp == 1) {
             // -------------------------------------------------------------------- MMA issuer
-            if (lane == 0) {
-                constexpr uint32_t idesc_s = idesc_bf16(128, KT, false, false);
-                constexpr uint32_t idesc_o = idesc_bf16(128, 128, false, true);
-                int kuse = 0, vuse = 0, items = 0;
-                uint32_t spend[2] = {0, 0};   // tiles of a q tile so far, all items
-                bool ok = true;
-                for (int idx = blockIdx.x; idx < total && ok; idx += gridDim.x) {
-                    const WItem it = item_of<NQ, KT>(c, p, idx);
-                    const int n = it.t1 - it.t0;
-                    if (n == 0)
-                        continue;
-                    ok = mbar_wait(&c.qf, items & 1, &c.abort);
+            // The whole warp runs this loop on values that are uniform over it (trip counts, stages,
+            // the tensor-memory base), and one elected lane issues: the descriptors then live in
+            // uniform registers, and an MMA costs two additions beside itself. Issued from one
+            // lane's own branch an MMA took 85-95 clocks (for 32-64 of work): the tensor core
+            // waited for its instructions.
+            constexpr uint32_t idesc_s = idesc_bf16(128, KT, false, false);
+            constexpr uint32_t idesc_o = idesc_bf16(128, 128, false, true);
+            const uint64_t dq0 = smem_desc_sw128(smem_u32(smem), 16, 1024);
+            const uint64_t dk0 = smem_desc_sw128(smem_u32(kv_smem), 16, 1024);
+            const uint64_t dv0 = smem_desc_sw128(smem_u32(kv_smem) + 2 * kHalfKV, kHalfKV, 1024);
+            const uint32_t tm = uniform(tmem), all = uniform(total);
+            uint32_t seq = 0, items = 0;      // tiles and items so far
+            bool ok = true;
+            // S of q tile A from the keys in stage st
+            auto scores = [&](int A, uint32_t st, uint32_t buf) {
+                const uint64_t dq = dq0 + A * (2 * kHalfQ / 16), dk = dk0 + st * (kStage / 16);
+                const uint32_t d = tm + A * (NS * KT + 128) + buf * KT;
+#pragma unroll
+                for (int kk = 0; kk < 8; ++kk)
+                    umma_bf16(d, dq + ((kk >> 2) * kHalfQ + (kk & 3) * 32) / 16,
+                              dk + ((kk >> 2) * kHalfKV + (kk & 3) * 32) / 16, idesc_s, kk > 0 ? 1u : 0u);
+                umma_commit(&c.sf[A][buf]);
+            };
+            auto products = [&](int A, uint32_t st, uint32_t buf, bool first) {
+                const uint64_t dv = dv0 + st * (kStage / 16);
+                const uint32_t d = tm + A * (NS * KT + 128) + NS * KT, w = tm + A * (NS * KT + 128) + buf * KT;
+#pragma unroll
+                for (int part = 0; part < (TWO ? 2 : 1); ++part)
+#pragma unroll
+                    for (int kk = 0; kk < kBlocks; ++kk)
+                        umma_bf16_ta(d, w + part * (KT / 2) + kk * 8, dv + kk * 128, idesc_o,
+                                     kk > 0 || part > 0 ? 1u : first ? 0u : 1u);
+                umma_commit(&c.od[A][buf]);
+            };
+            for (uint32_t idx = blockIdx.x; idx < all && ok; idx += gridDim.x) {
+                const WItem it = item_of<NQ, KT>(c, p, idx);
+                const uint32_t end = seq + uniform(it.t1 - it.t0);
+                if (seq == end)
+                    continue;
+                ok = warp_wait(&c.qf, items & 1, &c.abort);
+                // The scores of the first NS tiles, then tile by tile the product of a q tile and at
+                // once the scores that take over its buffer: NS tiles ahead of the softmax.
+                for (uint32_t t = seq; t < end && t < seq + NS && ok; ++t) {
+                    ok = warp_wait(&c.kf[t % ST], (t / ST) & 1, &c.abort);
                     if (!ok)
                         break;
-                    auto scores = [&](int a, int j, bool wait) -> bool {
-                        const int st = (kuse + j) % ST;
-                        if (wait && !mbar_wait(&c.kf[st], ((kuse + j) / ST) & 1, &c.abort))
-                            return false;
-                        tc_fence_after();
-                        const uint32_t ka = smem_u32(kv_smem + st * kStage), qa = smem_u32(smem + a * 2 * kHalfQ);
-                        const int buf = (spend[a] + j) % NS;
+                    tc_fence_after();
+                    if (elect_one()) {
 #pragma unroll
-                        for (int kk = 0; kk < 8; ++kk)
-                            umma_bf16(s_col(a, buf),
-                                      smem_desc_sw128(qa + (kk >> 2) * kHalfQ + (kk & 3) * 32, 16, 1024),
-                                      smem_desc_sw128(ka + (kk >> 2) * kHalfKV + (kk & 3) * 32, 16, 1024),
-                                      idesc_s, kk > 0 ? 1u : 0u);
-                        umma_commit(&c.sf[a][buf]);
-                        return true;
-                    };
-                    auto scores_done = [&](int j) {
-                        umma_commit(&c.ke[(kuse + j) % ST]);
-                        if (j == n - 1)
+                        for (int A = 0; A < NQ; ++A)
+                            scores(A, t % ST, t % NS);
+                        umma_commit(&c.ke[t % ST]);
+                        if (t + 1 == end)
                             umma_commit(&c.qe);
-                    };
-                    for (int a = 0; a < NQ && ok; ++a)
-                        ok = scores(a, 0, a == 0);
-                    if (!ok)
-                        break;
-                    scores_done(0);
-                    for (int j = 0; j < n && ok; ++j) {
-                        // with two score buffers the next scores are computed ahead of the softmax
-                        if (NS == 2 && j + 1 < n) {
-                            for (int a = 0; a < NQ && ok; ++a)
-                                ok = scores(a, j + 1, a == 0);
-                            if (!ok)
-                                break;
-                            scores_done(j + 1);
-                        }
-                        const int st = (vuse + j) % ST;
-                        for (int a = 0; a < NQ && ok; ++a) {
-                            const int buf = (spend[a] + j) % NS;
-                            ok = mbar_wait(&c.pf[a][buf], ((spend[a] + j) / NS) & 1, &c.abort) &&
-                                 (j > 0 || mbar_wait(&c.oe[a], (items & 1) ^ 1, &c.abort)) &&
-                                 (a > 0 || mbar_wait(&c.vr[st], ((vuse + j) / ST) & 1, &c.abort));
-                            if (!ok)
-                                break;
-                            tc_fence_after();
-                            const uint32_t va = smem_u32(kv_smem + st * kStage + 2 * kHalfKV);
+                    }
+                    __syncwarp();
+                }
+                const uint32_t begin = seq;
+                for (; seq < end && ok; ++seq) {
+                    const uint32_t st = seq % ST, buf = seq % NS, next = seq + NS;
+                    const bool more = next < end;
+                    ok = warp_wait(&c.vr[st], (seq / ST) & 1, &c.abort) &&
+                         (!more || warp_wait(&c.kf[next % ST], (next / ST) & 1, &c.abort));
 #pragma unroll
-                            for (int part = 0; part < (TWO ? 2 : 1); ++part)
-#pragma unroll
-                                for (int kk = 0; kk < kBlocks; ++kk)
-                                    umma_bf16_ta(o_col(a), s_col(a, buf) + part * (KT / 2) + kk * 8,
-                                                 smem_desc_sw128(va + kk * 2048, kHalfKV, 1024), idesc_o,
-                                                 j > 0 || kk > 0 || part > 0 ? 1u : 0u);
-                            umma_commit(&c.od[a][buf]);
-                            if (a == NQ - 1)
+                    for (int A = 0; A < NQ; ++A) {
+                        ok = ok && warp_wait(&c.pf[A][buf], (seq / NS) & 1, &c.abort) &&
+                             (seq > begin || warp_wait(&c.oe[A], (items & 1) ^ 1, &c.abort));
+                        if (!ok)
+                            break;
+                        tc_fence_after();
+                        if (elect_one()) {
+                            products(A, st, buf, seq == begin);
+                            if (A == NQ - 1)
                                 umma_commit(&c.ve[st]);
-                            if (NS == 1 && j + 1 < n) {
-                                ok = scores(a, j + 1, a == 0);
-                                if (ok && a == NQ - 1)
-                                    scores_done(j + 1);
+                            if (more) {
+                                scores(A, next % ST, buf);
+                                if (A == NQ - 1) {
+                                    umma_commit(&c.ke[next % ST]);
+                                    if (next + 1 == end)
+                                        umma_commit(&c.qe);
+                                }
                             }
                         }
+                        __syncwarp();
                     }
-                    kuse += n;
-                    vuse += n;
-                    for (int a = 0; a < NQ; ++a)
-                        spend[a] += n;
-                    ++items;
                 }
                 if (!ok)
-                    wfail(c, p.err);
-                umma_commit(&c.drain);
-                mbar_wait(&c.drain, 0, nullptr);
+                    break;
+                ++items;
             }
+            if (lane == 0 && !ok)
+                wfail(c, p.err);
+            if (elect_one())
+                umma_commit(&c.drain);
+            __syncwarp();
+            mbar_wait(&c.drain, 0, nullptr);
             __syncwarp();
         } else if (warp == 2) {
             // ------------------------------------------------- V rows that nobody may see := 0
@@ -789,11 +810,9 @@ __global__ void __launch_bounds__(128 + 128 * NQ, NQ == 1 ? 2 : 1)
                 const int last = it.p0 + it.np - 1;
                 for (int t = it.t0; t < it.t1; ++t, ++use) {
                     const int st = use % ST;
-                    ok = mbar_wait(&c.vf[st], (use / ST) & 1, &c.abort);
-                    if (!__all_sync(0xffffffffu, ok)) {
-                        ok = false;
+                    ok = warp_wait(&c.vf[st], (use / ST) & 1, &c.abort);
+                    if (!ok)
                         break;
-                    }
                     uint8_t *v = kv_smem + st * kStage + 2 * kHalfKV;
                     bool wrote = false;
 #pragma unroll
@@ -851,8 +870,8 @@ cudaError_t launch_window(const WindowParams &p, int n_qtiles, const CUtensorMap
                           cudaStream_t stream)
 {
     if (n_qtiles == 2)
-        return p.out_fp32 ? launch_one<2, 128, 2, 1, true>(p, tm_k, tm_v, tm_q, grid, stream)
-                          : launch_one<2, 128, 2, 1, false>(p, tm_k, tm_v, tm_q, grid, stream);
+        return p.out_fp32 ? launch_one<2, 64, 4, 2, true>(p, tm_k, tm_v, tm_q, grid, stream)
+                          : launch_one<2, 64, 4, 2, false>(p, tm_k, tm_v, tm_q, grid, stream);
     return p.out_fp32 ? launch_one<1, 64, 2, 2, true>(p, tm_k, tm_v, tm_q, grid, stream)
                       : launch_one<1, 64, 2, 2, false>(p, tm_k, tm_v, tm_q, grid, stream);
 }
