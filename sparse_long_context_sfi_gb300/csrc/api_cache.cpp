@@ -297,6 +297,7 @@ sfi_status sfi_window_attn(const sfi_kv_cache *kv, const void *q, void *out, int
     p.batch = kv->batch;
     p.n_kv_heads = kv->n_kv_heads;
     p.group = kv->n_q_heads / kv->n_kv_heads;
+    p.group_log2 = p.group == 8 ? 3 : p.group == 4 ? 2 : p.group == 2 ? 1 : 0;
     p.capacity = kv->capacity;
     p.page_size = kv->page_size;
     p.n_pages = kv->n_pages;

@@ -216,7 +216,7 @@ cudaError_t launch_beam_select(const BeamParams &p, cudaStream_t stream);
 // --------------------------------------------------------- attention with sinks and a window
 
 struct WindowParams {
-    int n_layers, batch, n_kv_heads, group;
+    int n_layers, batch, n_kv_heads, group, group_log2;
     int capacity, page_size, n_pages, max_pages, max_len;
     const int32_t *page_table;
     const int32_t *seq_len;

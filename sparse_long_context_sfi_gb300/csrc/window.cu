@@ -157,6 +157,26 @@ __device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, u
         : "memory");
 }
 
+// Polls until `done()` holds in every lane (a warp call; it may test several barriers, whose
+// latencies then overlap); gives up like mbar_wait. For the MMA warp, whose waits are on the
+// critical path and which has nothing else to do: a wait that is over costs it ~140 clocks.
+template <typename F>
+__device__ __forceinline__ bool warp_poll(F done, volatile int *abort)
+{
+    uint64_t t0 = 0;
+    for (uint32_t spins = 1;; ++spins) {
+        if (__all_sync(0xffffffffu, done()))
+            return true;
+        if ((spins & 255u) == 0u) {
+            const uint64_t now = global_timer_ns();
+            if (t0 == 0)
+                t0 = now;
+            if (__any_sync(0xffffffffu, *abort != 0 || now - t0 > kWaitTimeoutNs))
+                return false;
+        }
+    }
+}
+
 // Every lane waits; the answer is the same in all of them.
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort)
 {
@@ -188,7 +208,8 @@ struct WCtrl {
     uint64_t kf[kMaxStages], ke[kMaxStages], vf[kMaxStages], vr[kMaxStages], ve[kMaxStages];
     uint64_t qf, qe;
     uint64_t sf[2][2];          // [q tile][score buffer]: scores complete
-    uint64_t pf[2][2];          // weights stored (one arrival per softmax warp)
+    uint64_t pf[2][2];          // [q tile][score buffer, or half of the tile's columns with one buffer]:
+                                // weights stored (one arrival per softmax warp)
     // an O += P V complete; one per score buffer, because with two the softmax may be two
     // tiles ahead of the products, and one barrier's parity tells only one phase
     uint64_t od[2][2];
@@ -218,7 +239,7 @@ template <int NQ, int KT>
 __device__ __forceinline__ WItem item_of(const WCtrl &c, const WindowParams &p, int idx)
 {
     WItem it;
-    const int per = 128 * NQ / p.group;
+    const int per = (128 * NQ) >> p.group_log2;
     it.sp = idx % p.n_split;
     int q = idx / p.n_split;
     it.kvh = q % p.n_kv_heads;
@@ -312,13 +333,14 @@ __global__ void __launch_bounds__(128 + 128 * NQ, NQ == 1 ? 2 : 1)
 {
     constexpr int kHalfQ = 16384, kHalfKV = KT * 128, kStage = 4 * kHalfKV, kBlocks = KT / 16;
     constexpr uint32_t kCols = NQ == 1 ? 256 : 512;
+    constexpr int NH = NS == 1 ? 2 : 1;     // parts in which a tile's weights are handed over
     static_assert(NQ * (NS * KT + 128) <= static_cast<int>(kCols) && ST <= kMaxStages && NS <= 2);
     extern __shared__ uint8_t raw[];
     uint8_t *smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
     uint8_t *kv_smem = smem + NQ * 2 * kHalfQ;
     WCtrl &c = *reinterpret_cast<WCtrl *>(kv_smem + ST * kStage);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int G = p.group, per = 128 * NQ / G;
+    const int G = p.group, per = (128 * NQ) >> p.group_log2;
 
     if (tid < kWBars) {
         uint64_t *bar = reinterpret_cast<uint64_t *>(&c) + tid;
@@ -414,9 +436,26 @@ __global__ void __launch_bounds__(128 + 128 * NQ, NQ == 1 ? 2 : 1)
             return warp_wait(&c.gs, syncs++ & 1, &c.abort);
         };
         const int rq = a * 128 + rowi;
-        for (int idx = blockIdx.x; idx < total && ok; idx += gridDim.x) {
-            const WItem it = item_of<NQ, KT>(c, p, idx);
-            const int dp = rq / G, h = rq - dp * G;
+        // what the softmax needs of an item; the next one is worked out ahead
+        struct {
+            int p0, np, base, t0, t1, slot, sp;
+            uint32_t row0;              // row of out that the item's first position and head is
+        } it;
+        auto look = [&](int idx) {
+            const WItem w = item_of<NQ, KT>(c, p, idx);
+            it.p0 = w.p0;
+            it.np = w.np;
+            it.base = w.base;
+            it.t0 = w.t0;
+            it.t1 = w.t1;
+            it.slot = w.slot;
+            it.sp = w.sp;
+            it.row0 = static_cast<uint32_t>(w.layer * p.n_rows + w.r0) * (p.n_kv_heads * G) + w.kvh * G;
+        };
+        if (static_cast<int>(blockIdx.x) < total)
+            look(blockIdx.x);
+        for (int idx = blockIdx.x; idx < total; idx += gridDim.x) {
+            const int dp = rq >> p.group_log2, h = rq & (G - 1);
             const bool valid = dp < it.np;
             const int i = it.p0 + dp;                       // this row's position
             const int e1 = min(p.n_sink, i + 1);            // list columns [0, e1) and [a2, e2)
@@ -496,19 +535,40 @@ __global__ void __launch_bounds__(128 + 128 * NQ, NQ == 1 ? 2 : 1)
                         for (int x = 0; x < 16; ++x)
                             w[x] = r[TWO ? x : 0] = 0u;
                     } else {
+                        // in a rolling order, so that the exponentials of a pair issue between the
+                        // arithmetic of its neighbours
+                        uint64_t z = fma2(pack2(s[32 * q], s[32 * q + 1]), sc2, off2);
+                        float2 pp = make_float2(0.f, 0.f);
 #pragma unroll
-                        for (int x = 0; x < 16; ++x) {
-                            const float2 z = unpack2(fma2(pack2(s[32 * q + 2 * x], s[32 * q + 2 * x + 1]), sc2, off2));
-                            const float p0 = ex2_approx(z.x), p1 = ex2_approx(z.y);
-                            sum[x & 1] = add2(sum[x & 1], pack2(p0, p1));
-                            const __nv_bfloat162 hi = __floats2bfloat162_rn(p0, p1);
-                            w[x] = *reinterpret_cast<const uint32_t *>(&hi);
-                            if (TWO) {
-                                const float2 b = __bfloat1622float2(hi);
-                                const __nv_bfloat162 lo = __floats2bfloat162_rn(p0 - b.x, p1 - b.y);
-                                r[TWO ? x : 0] = *reinterpret_cast<const uint32_t *>(&lo);
+                        for (int x = 0; x <= 16; ++x) {
+                            const float2 zz = unpack2(z);
+                            float2 pn;
+                            if (x < 16)
+                                pn.x = ex2_approx(zz.x);
+                            if (x < 15)
+                                z = fma2(pack2(s[32 * q + 2 * x + 2], s[32 * q + 2 * x + 3]), sc2, off2);
+                            if (x > 0) {
+                                sum[x & 1] = add2(sum[x & 1], pack2(pp.x, pp.y));
+                                const __nv_bfloat162 hi = __floats2bfloat162_rn(pp.x, pp.y);
+                                w[x - 1] = *reinterpret_cast<const uint32_t *>(&hi);
+                                if (TWO) {
+                                    const float2 b = __bfloat1622float2(hi);
+                                    const __nv_bfloat162 lo = __floats2bfloat162_rn(pp.x - b.x, pp.y - b.y);
+                                    r[TWO ? x - 1 : 0] = *reinterpret_cast<const uint32_t *>(&lo);
+                                }
                             }
+                            if (x < 16)
+                                pn.y = ex2_approx(zz.y);
+                            pp = pn;
                         }
+                    }
+                    if (NH == 2 && q == KT / 64) {
+                        // the first half of the weights has been stored for a while: let its product go
+                        tmem_st_wait();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0)
+                            mbar_arrive(&c.pf[a][0]);
                     }
                     tmem_st16(sa + 16 * q, w);
                     if (TWO)
@@ -520,23 +580,24 @@ __global__ void __launch_bounds__(128 + 128 * NQ, NQ == 1 ? 2 : 1)
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0)
-                    mbar_arrive(&c.pf[a][buf]);
+                    mbar_arrive(&c.pf[a][NH == 2 ? 1 : buf]);
             }
             if (!ok)
                 break;
             // ------------------------------------------------------------------ epilogue
             const bool any = it.t1 > it.t0;
+            const uint32_t row0 = it.row0, my_row = row0 + dp * (p.n_kv_heads * G) + h;
+            const int nrows = it.np * G, slot = it.slot;
+            const size_t part = static_cast<size_t>(slot) * p.n_split + it.sp;
+            const float inv = p.n_split == 1 ? 1.f / l : 1.f;
+            // the next item is worked out while the last products run
+            if (idx + static_cast<int>(gridDim.x) < total)
+                look(idx + gridDim.x);
             if (any) {
                 ok = warp_wait(&c.od[a][(done - 1) % NS], ((done - 1) / NS) & 1, &c.abort);
                 if (!ok)
                     break;
                 tc_fence_after();
-            }
-            const size_t out_at = ((static_cast<size_t>(it.layer) * p.n_rows + it.r0 + dp) * p.n_kv_heads * G +
-                                   it.kvh * G + h) * kHeadDim;
-            const size_t part = static_cast<size_t>(it.slot) * p.n_split + it.sp;
-            const float inv = p.n_split == 1 ? 1.f / l : 1.f;
-            if (any) {
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
                     float o[64];
@@ -556,7 +617,7 @@ __global__ void __launch_bounds__(128 + 128 * NQ, NQ == 1 ? 2 : 1)
                         for (int x = 0; x < 64; ++x)
                             o[x] *= inv;
                         if (p.n_split == 1) {
-                            store_row<64>(p, out_at + 64 * q, o);
+                            store_row<64>(p, static_cast<size_t>(my_row) * kHeadDim + 64 * q, o);
                         } else {
                             float *w = p.parts + (part * p.part_rows + rq) * kHeadDim + 64 * q;
 #pragma unroll
@@ -574,18 +635,17 @@ __global__ void __launch_bounds__(128 + 128 * NQ, NQ == 1 ? 2 : 1)
                 if (!(ok = softmax_sync()))
                     break;
                 if (tid == 128)
-                    c.last = atomic_add_acq_rel_gpu(p.tickets + it.slot, 1) == p.n_split - 1;
+                    c.last = atomic_add_acq_rel_gpu(p.tickets + slot, 1) == p.n_split - 1;
                 if (!(ok = softmax_sync()))
                     break;
                 if (c.last != 0) {
                     if (tid == 128)
-                        p.tickets[it.slot] = 0;
+                        p.tickets[slot] = 0;
                     __threadfence();
                     // a thread per (row, dim): 128 dims, NQ rows at a time
                     const int d = (tid - 128) & 127;
-                    const int nrows = it.np * G;
                     for (int r = (tid - 128) >> 7; r < nrows; r += NQ) {
-                        const size_t p0 = static_cast<size_t>(it.slot) * p.n_split * p.part_rows + r;
+                        const size_t p0 = static_cast<size_t>(slot) * p.n_split * p.part_rows + r;
                         float M = -CUDART_INF_F;
                         for (int sp = 0; sp < p.n_split; ++sp)
                             M = fmaxf(M, __ldcg(p.part_ml + p0 + static_cast<size_t>(sp) * p.part_rows).x);
@@ -599,9 +659,9 @@ __global__ void __launch_bounds__(128 + 128 * NQ, NQ == 1 ? 2 : 1)
                                 den = fmaf(w, ml.y, den);
                             }
                         }
-                        const int dpr = r / G;
-                        const size_t o = ((static_cast<size_t>(it.layer) * p.n_rows + it.r0 + dpr) *
-                                              p.n_kv_heads * G + it.kvh * G + (r - dpr * G)) * kHeadDim + d;
+                        const int dpr = r >> p.group_log2;
+                        const size_t o = static_cast<size_t>(row0 + dpr * (p.n_kv_heads * G) + (r & (G - 1))) *
+                                             kHeadDim + d;
                         if (p.out_fp32)
                             static_cast<float *>(p.out)[o] = acc / den;
                         else
@@ -727,16 +787,19 @@ __global__ void __launch_bounds__(128 + 128 * NQ, NQ == 1 ? 2 : 1)
                               dk + ((kk >> 2) * kHalfKV + (kk & 3) * 32) / 16, idesc_s, kk > 0 ? 1u : 0u);
                 umma_commit(&c.sf[A][buf]);
             };
-            auto products = [&](int A, uint32_t st, uint32_t buf, bool first) {
+            auto products = [&](int A, uint32_t st, uint32_t buf, int half, bool first) {
                 const uint64_t dv = dv0 + st * (kStage / 16);
                 const uint32_t d = tm + A * (NS * KT + 128) + NS * KT, w = tm + A * (NS * KT + 128) + buf * KT;
 #pragma unroll
                 for (int part = 0; part < (TWO ? 2 : 1); ++part)
 #pragma unroll
-                    for (int kk = 0; kk < kBlocks; ++kk)
+                    for (int k2 = 0; k2 < kBlocks / NH; ++k2) {
+                        const int kk = half * (kBlocks / NH) + k2;
                         umma_bf16_ta(d, w + part * (KT / 2) + kk * 8, dv + kk * 128, idesc_o,
                                      kk > 0 || part > 0 ? 1u : first ? 0u : 1u);
-                umma_commit(&c.od[A][buf]);
+                    }
+                if (half == NH - 1)
+                    umma_commit(&c.od[A][buf]);
             };
             for (uint32_t idx = blockIdx.x; idx < all && ok; idx += gridDim.x) {
                 const WItem it = item_of<NQ, KT>(c, p, idx);
@@ -765,26 +828,43 @@ __global__ void __launch_bounds__(128 + 128 * NQ, NQ == 1 ? 2 : 1)
                 for (; seq < end && ok; ++seq) {
                     const uint32_t st = seq % ST, buf = seq % NS, next = seq + NS;
                     const bool more = next < end;
-                    ok = warp_wait(&c.vr[st], (seq / ST) & 1, &c.abort) &&
-                         (!more || warp_wait(&c.kf[next % ST], (next / ST) & 1, &c.abort));
 #pragma unroll
                     for (int A = 0; A < NQ; ++A) {
-                        ok = ok && warp_wait(&c.pf[A][buf], (seq / NS) & 1, &c.abort) &&
-                             (seq > begin || warp_wait(&c.oe[A], (items & 1) ^ 1, &c.abort));
+#pragma unroll
+                        for (int half = 0; half < NH; ++half) {
+                            ok = ok && warp_poll([&] {
+                                return mbar_test_wait(&c.pf[A][NH == 2 ? half : buf], (seq / NS) & 1) &&
+                                       (A > 0 || half > 0 || mbar_test_wait(&c.vr[st], (seq / ST) & 1)) &&
+                                       (seq > begin || half > 0 || mbar_test_wait(&c.oe[A], (items & 1) ^ 1));
+                            }, &c.abort);
+                            if (!ok)
+                                break;
+                            tc_fence_after();
+                            if (elect_one()) {
+                                products(A, st, buf, half, seq == begin);
+                                if (A == NQ - 1 && half == NH - 1)
+                                    umma_commit(&c.ve[st]);
+                            }
+                            __syncwarp();
+                        }
                         if (!ok)
                             break;
-                        tc_fence_after();
+                        if (!more)
+                            continue;
+                        // (asked only now: the product does not wait for keys that are on their way)
+                        if (A == 0) {
+                            ok = warp_poll([&] { return mbar_test_wait(&c.kf[next % ST], (next / ST) & 1); },
+                                           &c.abort);
+                            if (!ok)
+                                break;
+                            tc_fence_after();
+                        }
                         if (elect_one()) {
-                            products(A, st, buf, seq == begin);
-                            if (A == NQ - 1)
-                                umma_commit(&c.ve[st]);
-                            if (more) {
-                                scores(A, next % ST, buf);
-                                if (A == NQ - 1) {
-                                    umma_commit(&c.ke[next % ST]);
-                                    if (next + 1 == end)
-                                        umma_commit(&c.qe);
-                                }
+                            scores(A, next % ST, buf);
+                            if (A == NQ - 1) {
+                                umma_commit(&c.ke[next % ST]);
+                                if (next + 1 == end)
+                                    umma_commit(&c.qe);
                             }
                         }
                         __syncwarp();
@@ -870,8 +950,8 @@ cudaError_t launch_window(const WindowParams &p, int n_qtiles, const CUtensorMap
                           cudaStream_t stream)
 {
     if (n_qtiles == 2)
-        return p.out_fp32 ? launch_one<2, 64, 4, 2, true>(p, tm_k, tm_v, tm_q, grid, stream)
-                          : launch_one<2, 64, 4, 2, false>(p, tm_k, tm_v, tm_q, grid, stream);
+        return p.out_fp32 ? launch_one<2, 128, 2, 1, true>(p, tm_k, tm_v, tm_q, grid, stream)
+                          : launch_one<2, 128, 2, 1, false>(p, tm_k, tm_v, tm_q, grid, stream);
     return p.out_fp32 ? launch_one<1, 64, 2, 2, true>(p, tm_k, tm_v, tm_q, grid, stream)
                       : launch_one<1, 64, 2, 2, false>(p, tm_k, tm_v, tm_q, grid, stream);
 }
