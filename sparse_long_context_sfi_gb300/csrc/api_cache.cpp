@@ -82,7 +82,7 @@ sfi_status check_rows(const sfi_kv_cache *kv, const int32_t *row_start, int32_t 
     return SFI_OK;
 }
 
-// How sfi_window_attn runs with n_qtiles (1 or 2) 128-row q tiles per CTA.
+// How sfi_window_attn runs with items of `rows` operand rows (16, 128 or 256).
 struct WindowShape {
     int rows, slots;        // operand rows per item; CTAs that are resident at once
     long long items;        // bound of the items before splitting
@@ -90,12 +90,12 @@ struct WindowShape {
     int part_rows;
 };
 
-WindowShape window_shape(const sfi_kv_cache *kv, int n_rows, int max_rows, int n_qtiles)
+WindowShape window_shape(const sfi_kv_cache *kv, int n_rows, int max_rows, int rows)
 {
     WindowShape s;
     const int g = kv->n_q_heads / kv->n_kv_heads, sms = sm_count();
-    s.rows = 128 * n_qtiles;
-    s.slots = n_qtiles == 2 ? sms : 2 * sms;
+    s.rows = rows;
+    s.slots = rows == 256 ? sms : 2 * sms;
     const long long seqs = n_rows < kv->batch ? n_rows : kv->batch;
     const long long units = 1LL * kv->n_kv_heads * kv->n_layers;
     s.items = (1LL * n_rows * g / s.rows + seqs) * units;
@@ -107,12 +107,23 @@ WindowShape window_shape(const sfi_kv_cache *kv, int n_rows, int max_rows, int n
     return s;
 }
 
-// Sized for either q tile count and any split, so that it holds for every max_len and window.
+// The item size. 16 rows hold a single token's heads and leave room for a third stage. Two q
+// tiles (256 rows) halve the reads of K and V and keep the tensor core busy while the other
+// tile is in its softmax, but only one such CTA fits an SM: where the reach of a row is short,
+// an item is mostly start and end, which two CTAs of 128 rows overlap.
+int window_rows(const sfi_kv_cache *kv, int max_rows, int n_window)
+{
+    const long long all = 1LL * max_rows * (kv->n_q_heads / kv->n_kv_heads);
+    const int reach = n_window < kv->max_len ? n_window : kv->max_len;
+    return all <= 16 ? 16 : all > 128 && reach >= 512 ? 256 : 128;
+}
+
+// Sized for any item size and split, so that it holds for every max_len and window.
 size_t window_scratch(const sfi_kv_cache *kv, int n_rows, int max_rows, char *base, WindowParams *p)
 {
     size_t o = 0, items = 1, parts = 1;
-    for (int q = 1; q <= 2; ++q) {
-        const WindowShape s = window_shape(kv, n_rows, max_rows, q);
+    for (int rows : {16, 128, 256}) {
+        const WindowShape s = window_shape(kv, n_rows, max_rows, rows);
         const size_t n = s.most_split > 1 ? static_cast<size_t>(s.items) : 1;
         const size_t m = s.most_split > 1 ? n * s.most_split * s.part_rows : 1;
         items = n > items ? n : items;
@@ -287,17 +298,22 @@ sfi_status sfi_window_attn(const sfi_kv_cache *kv, const void *q, void *out, int
         return SFI_OK;
     if (!q || !out || !aligned16(q) || !aligned16(out))
         return SFI_ERR_INVALID_ARG;
+    const int rows = window_rows(kv, max_rows, n_window);
     CUtensorMap tk, tv, tq;
     if (!make_map(&tk, kv->k, cache_rows(kv), 16u) || !make_map(&tv, kv->v, cache_rows(kv), 16u) ||
         !make_chunk_map(&tq, q, static_cast<uint64_t>(kv->n_layers) * n_rows,
                         static_cast<uint32_t>(kv->n_q_heads),
-                        static_cast<uint32_t>(kv->n_q_heads / kv->n_kv_heads)))
+                        static_cast<uint32_t>(kv->n_q_heads / kv->n_kv_heads), rows == 16 ? 16u : 128u))
         return SFI_ERR_CUDA;
     p.n_layers = kv->n_layers;
     p.batch = kv->batch;
     p.n_kv_heads = kv->n_kv_heads;
     p.group = kv->n_q_heads / kv->n_kv_heads;
     p.group_log2 = p.group == 8 ? 3 : p.group == 4 ? 2 : p.group == 2 ? 1 : 0;
+    p.heads_log2 = -1;
+    for (int i = 0; i < 31; ++i)
+        if (kv->n_kv_heads == 1 << i)
+            p.heads_log2 = i;
     p.capacity = kv->capacity;
     p.page_size = kv->page_size;
     p.n_pages = kv->n_pages;
@@ -315,13 +331,11 @@ sfi_status sfi_window_attn(const sfi_kv_cache *kv, const void *q, void *out, int
     p.out_fp32 = out_fp32 ? 1 : 0;
     p.out_aligned32 = (reinterpret_cast<uintptr_t>(out) & 31u) == 0;
     p.err = kv->err;
-    const int g = p.group;
     const long long len = kv->max_len, reach = n_window < len ? n_window : len;
-    const int qtiles = 1LL * max_rows * g > 128 && reach >= 512 ? 2 : 1;
-    const WindowShape s = window_shape(kv, n_rows, max_rows, qtiles);
+    const WindowShape s = window_shape(kv, n_rows, max_rows, rows);
     // Fewer items than CTAs that fit: split their keys, four tiles at least to a split.
-    const int kt = qtiles == 2 ? 128 : 64;
-    const long long span = reach + s.rows / g < len ? reach + s.rows / g : len;
+    const int kt = rows == 256 ? 128 : 64;
+    const long long span = reach + rows / p.group < len ? reach + rows / p.group : len;
     const long long tiles = (span + n_sink + 32 + kt - 1) / kt;
     long long split = s.most_split < tiles / 4 ? s.most_split : tiles / 4;
     split = split < 1 ? 1 : split;
@@ -330,7 +344,7 @@ sfi_status sfi_window_attn(const sfi_kv_cache *kv, const void *q, void *out, int
     const long long all = s.items * split;
     const int grid = static_cast<int>(all < s.slots ? all : s.slots);
     p.scale_log2 = static_cast<float>(1.4426950408889634074 / std::sqrt(static_cast<double>(kHeadDim)));
-    return launch_status(launch_window(p, qtiles, tk, tv, tq, grid, as_stream(stream)));
+    return launch_status(launch_window(p, rows, tk, tv, tq, grid, as_stream(stream)));
 }
 
 sfi_status sfi_reorder(const sfi_kv_cache *kv, const sfi_page_pool *pool,

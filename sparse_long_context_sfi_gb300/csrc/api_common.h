@@ -49,16 +49,18 @@ inline bool make_map(CUtensorMap *m, const void *base, uint64_t rows, uint32_t b
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// The queries of a packed chunk as [rows][heads][128]; a box is one kv head's G heads of 128 / G
-// rows (128 operand rows, row-major by position), 64 columns, 128-byte swizzle.
-inline bool make_chunk_map(CUtensorMap *m, const void *base, uint64_t rows, uint32_t heads, uint32_t group)
+// The queries of a packed chunk as [rows][heads][128]; a box is one kv head's G heads of
+// box_rows / G rows (box_rows operand rows, by position, then head), 64 columns, 128-byte
+// swizzle.
+inline bool make_chunk_map(CUtensorMap *m, const void *base, uint64_t rows, uint32_t heads, uint32_t group,
+                           uint32_t box_rows)
 {
     EncodeTiledFn fn = encode_fn();
     if (!fn || rows == 0)
         return false;
     const cuuint64_t dims[3] = {static_cast<cuuint64_t>(kHeadDim), heads, rows};
     const cuuint64_t strides[2] = {kHeadDim * 2, static_cast<cuuint64_t>(heads) * kHeadDim * 2};
-    const cuuint32_t box[3] = {64, group, 128 / group};
+    const cuuint32_t box[3] = {64, group, box_rows / group};
     const cuuint32_t estr[3] = {1, 1, 1};
     return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box,
               estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,

@@ -217,6 +217,7 @@ cudaError_t launch_beam_select(const BeamParams &p, cudaStream_t stream);
 
 struct WindowParams {
     int n_layers, batch, n_kv_heads, group, group_log2;
+    int heads_log2;             // of n_kv_heads, -1 if it is no power of two
     int capacity, page_size, n_pages, max_pages, max_len;
     const int32_t *page_table;
     const int32_t *seq_len;
@@ -233,8 +234,8 @@ struct WindowParams {
     float *parts;               // [items][n_split][part_rows][128] unnormalised outputs
     float2 *part_ml;            // [items][n_split][part_rows] maximum (scaled by nothing), sum
 };
-// n_qtiles: 128-row q tiles per CTA, 1 (two CTAs per SM) or 2.
-cudaError_t launch_window(const WindowParams &p, int n_qtiles, const CUtensorMap &tm_k,
+// rows: operand rows per item, 256 (two q tiles), 128 or 16 (two CTAs per SM).
+cudaError_t launch_window(const WindowParams &p, int rows, const CUtensorMap &tm_k,
                           const CUtensorMap &tm_v, const CUtensorMap &tm_q, int grid,
                           cudaStream_t stream);
 

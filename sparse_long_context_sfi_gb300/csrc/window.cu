@@ -84,14 +84,11 @@ __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t *v)
         : "memory");
 }
 
-__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t *v)
+__device__ __forceinline__ void tmem_st8(uint32_t addr, const uint32_t *v)
 {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
-        "%11, %12, %13, %14, %15};" ::"r"(v[0]),
-        "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]),
-        "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(addr)
-        : "memory");
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::"r"(v[0]),
+                 "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(addr)
+                 : "memory");
 }
 
 // Two floats at a time (sm_100 has packed fp32 adds and multiply-adds).
@@ -235,16 +232,18 @@ struct WItem {
     int slot, sp;
 };
 
-template <int NQ, int KT>
+template <int ROWS, int KT, bool SPLIT>
 __device__ __forceinline__ WItem item_of(const WCtrl &c, const WindowParams &p, int idx)
 {
     WItem it;
-    const int per = (128 * NQ) >> p.group_log2;
-    it.sp = idx % p.n_split;
-    int q = idx / p.n_split;
-    it.kvh = q % p.n_kv_heads;
-    q /= p.n_kv_heads;
-    it.layer = q / c.tiles;
+    const int per = ROWS >> p.group_log2;
+    // (an integer division costs ~40 instructions: taken only where it says something)
+    int q = SPLIT ? idx / p.n_split : idx;
+    it.sp = SPLIT ? idx - q * p.n_split : 0;
+    const int qh = p.heads_log2 >= 0 ? q >> p.heads_log2 : q / p.n_kv_heads;
+    it.kvh = q - qh * p.n_kv_heads;
+    q = qh;
+    it.layer = p.n_layers == 1 ? 0 : q / c.tiles;
     // the last rows of a prompt first: they see the most keys
     const int t = c.tiles - 1 - (q - it.layer * c.tiles);
     int lo = 0, hi = p.batch;
@@ -266,8 +265,12 @@ __device__ __forceinline__ WItem item_of(const WCtrl &c, const WindowParams &p, 
     it.base = (lo_blk - it.sb) * 16;
     it.nb = it.sb + ((it.p0 + it.np - 1) >> 4) - lo_blk + 1;
     const int n = (it.nb + KT / 16 - 1) / (KT / 16);
-    it.t0 = static_cast<int>(static_cast<long long>(n) * it.sp / p.n_split);
-    it.t1 = static_cast<int>(static_cast<long long>(n) * (it.sp + 1) / p.n_split);
+    it.t0 = 0;
+    it.t1 = n;
+    if (SPLIT) {                // (tiles * splits stays far below 2^32: at most 2^27 positions of 64)
+        it.t0 = static_cast<int>(static_cast<uint32_t>(n) * it.sp / p.n_split);
+        it.t1 = static_cast<int>(static_cast<uint32_t>(n) * (it.sp + 1) / p.n_split);
+    }
     it.slot = (it.layer * c.tiles + t) * p.n_kv_heads + it.kvh;
     return it;
 }
@@ -322,16 +325,21 @@ __device__ __forceinline__ void store_row(const WindowParams &p, size_t at, cons
     }
 }
 
-template <int NQ, int KT, int ST>
-constexpr int window_smem() { return 1024 + NQ * 32768 + ST * KT * 512 + static_cast<int>(sizeof(WCtrl)); }
+template <int NQ, int KT, int ST, int QR>
+constexpr int window_smem() { return 1024 + NQ * QR * 256 + ST * KT * 512 + static_cast<int>(sizeof(WCtrl)); }
 
+// NQ q tiles of QR operand rows, KT keys per tile, ST stages of keys and values, NS score
+// buffers per q tile. QR 16 is for single tokens: the MMA still takes 128 rows, of which all
+// but the first 16 are whatever lies behind them in shared memory; they end in rows of S and O
+// that nobody reads, and the memory holds a third stage instead.
 // TWO: the weights enter the product with V as bf16 part and bf16 remainder (fp32 outputs).
-template <int NQ, int KT, int ST, int NS, bool TWO>
+// SPLIT: an item's keys over several CTAs (the joining code costs registers).
+template <int NQ, int KT, int ST, int NS, int QR, bool TWO, bool SPLIT>
 __global__ void __launch_bounds__(128 + 128 * NQ, NQ == 1 ? 2 : 1)
     window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                   const __grid_constant__ CUtensorMap tm_q, const WindowParams p)
 {
-    constexpr int kHalfQ = 16384, kHalfKV = KT * 128, kStage = 4 * kHalfKV, kBlocks = KT / 16;
+    constexpr int kRows = NQ * QR, kHalfQ = QR * 128, kHalfKV = KT * 128, kStage = 4 * kHalfKV, kBlocks = KT / 16;
     constexpr uint32_t kCols = NQ == 1 ? 256 : 512;
     constexpr int NH = NS == 1 ? 2 : 1;     // parts in which a tile's weights are handed over
     static_assert(NQ * (NS * KT + 128) <= static_cast<int>(kCols) && ST <= kMaxStages && NS <= 2);
@@ -340,7 +348,7 @@ __global__ void __launch_bounds__(128 + 128 * NQ, NQ == 1 ? 2 : 1)
     uint8_t *kv_smem = smem + NQ * 2 * kHalfQ;
     WCtrl &c = *reinterpret_cast<WCtrl *>(kv_smem + ST * kStage);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int G = p.group, per = (128 * NQ) >> p.group_log2;
+    const int G = p.group, per = kRows >> p.group_log2;
 
     if (tid < kWBars) {
         uint64_t *bar = reinterpret_cast<uint64_t *>(&c) + tid;
@@ -415,48 +423,147 @@ __global__ void __launch_bounds__(128 + 128 * NQ, NQ == 1 ? 2 : 1)
     auto s_col = [&](int a, int buf) { return tmem + a * (NS * KT + 128) + buf * KT; };
     auto o_col = [&](int a) { return tmem + a * (NS * KT + 128) + NS * KT; };
 
-    // Registers: the softmax keeps a whole score row; the first warpgroup gives up what it does
-    // not need (launched with 168 or 128 a thread: 384 * 168 = 256 * 216 + 128 * 72,
-    // 256 * 128 = 128 * 184 + 128 * 72).
+    // What softmax and epilogue need of an item.
+    struct Rows {
+        int p0, np, base, t0, t1, slot, sp;
+        uint32_t row0;              // row of out that the item's first position and head is
+    };
+    auto look = [&](int idx) {
+        const WItem w = item_of<kRows, KT, SPLIT>(c, p, idx);
+        Rows r;
+        r.p0 = w.p0;
+        r.np = w.np;
+        r.base = w.base;
+        r.t0 = w.t0;
+        r.t1 = w.t1;
+        r.slot = w.slot;
+        r.sp = w.sp;
+        r.row0 = static_cast<uint32_t>(w.layer * p.n_rows + w.r0) * (p.n_kv_heads * G) + w.kvh * G;
+        return r;
+    };
+    uint32_t syncs = 0;
+    constexpr int kOut0 = 128;      // the first softmax thread
+    auto out_sync = [&]() -> bool {
+        __syncwarp();
+        if (lane == 0)
+            mbar_arrive(&c.gs);
+        return warp_wait(&c.gs, syncs++ & 1, &c.abort);
+    };
+    // O of q tile a once its `done`-th tile's product is complete, divided and written (or left as
+    // a partial and joined); each thread a row. False if a wait ran out.
+    auto finish = [&](int a, const Rows &it, uint32_t done, float m, float l) -> bool {
+        const int quad = warp & 3, rq = a * 128 + quad * 32 + lane;
+        const uint32_t lane_addr = static_cast<uint32_t>(quad * 32) << 16;
+        const int dp = rq >> p.group_log2, h = rq & (G - 1), nrows = it.np * G;
+        const bool valid = rq < nrows, live = a * 128 + quad * 32 < nrows;
+        const size_t part = SPLIT ? static_cast<size_t>(it.slot) * p.n_split + it.sp : 0;
+        if (it.t1 > it.t0) {
+            const size_t my_row = it.row0 + dp * (p.n_kv_heads * G) + h;
+            const float inv = SPLIT ? 1.f : 1.f / l;
+            if (!warp_wait(&c.od[a][(done - 1) % NS], ((done - 1) / NS) & 1, &c.abort))
+                return false;
+            tc_fence_after();
+            constexpr int kCol = 32;    // columns at a time (registers)
+#pragma unroll
+            for (int q = 0; q < 128; q += kCol) {
+                float o[kCol];
+                if (live) {
+#pragma unroll
+                    for (int x = 0; x < kCol; x += 32)
+                        tmem_ld32(o_col(a) + lane_addr + q + x, o + x);
+#pragma unroll
+                    for (int x = 0; x < kCol; x += 32)
+                        tmem_landed(o + x);
+                }
+                if (q + kCol == 128) {
+                    // O is free for the next item
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(&c.oe[a]);
+                }
+                if (valid) {
+#pragma unroll
+                    for (int x = 0; x < kCol; ++x)
+                        o[x] *= inv;
+                    if (!SPLIT) {
+                        store_row<kCol>(p, my_row * kHeadDim + q, o);
+                    } else {
+                        float *w = p.parts + (part * p.part_rows + rq) * kHeadDim + q;
+#pragma unroll
+                        for (int x = 0; x < kCol; x += 8)
+                            st_global32(w + x, reinterpret_cast<const uint32_t *>(o + x));
+                    }
+                }
+            }
+        }
+        if (SPLIT) {
+            if (valid)
+                p.part_ml[part * p.part_rows + rq] = make_float2(m, l);
+            // every thread's partials before the ticket, the ticket before any read
+            __threadfence();
+            if (!out_sync())
+                return false;
+            if (tid == kOut0)
+                c.last = atomic_add_acq_rel_gpu(p.tickets + it.slot, 1) == p.n_split - 1;
+            if (!out_sync())
+                return false;
+            if (c.last != 0) {
+                if (tid == kOut0)
+                    p.tickets[it.slot] = 0;
+                __threadfence();
+                // a thread per (row, dim): 128 dims, NQ rows at a time; splits in order
+                const int d = (tid - kOut0) & 127;
+                for (int r = (tid - kOut0) >> 7; r < nrows; r += NQ) {
+                    const size_t p0 = static_cast<size_t>(it.slot) * p.n_split * p.part_rows + r;
+                    float M = -CUDART_INF_F;
+                    for (int sp = 0; sp < p.n_split; ++sp)
+                        M = fmaxf(M, __ldcg(p.part_ml + p0 + static_cast<size_t>(sp) * p.part_rows).x);
+                    float acc = 0.f, den = 0.f;
+                    for (int sp = 0; sp < p.n_split; ++sp) {
+                        const size_t at = p0 + static_cast<size_t>(sp) * p.part_rows;
+                        const float2 ml = __ldcg(p.part_ml + at);
+                        if (ml.y > 0.f) {
+                            const float w = ex2_approx((ml.x - M) * p.scale_log2);
+                            acc = fmaf(w, __ldcg(p.parts + at * kHeadDim + d), acc);
+                            den = fmaf(w, ml.y, den);
+                        }
+                    }
+                    const int dpr = r >> p.group_log2;
+                    const size_t o = static_cast<size_t>(it.row0 + dpr * (p.n_kv_heads * G) + (r & (G - 1))) *
+                                         kHeadDim + d;
+                    if (p.out_fp32)
+                        static_cast<float *>(p.out)[o] = acc / den;
+                    else
+                        static_cast<__nv_bfloat16 *>(p.out)[o] = __float2bfloat16_rn(acc / den);
+                }
+            }
+        }
+        return true;
+    };
+
+    // Registers (launched with 168 a thread, or 128 with two CTAs per SM): the softmax keeps a
+    // score row, the other roles give up what they do not need.
+    // 384 * 168 = 256 * 200 + 128 * 104; 256 * 128 = 128 * 184 + 128 * 72.
     if (warp >= 4) {
         if (NQ == 2)
-            asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
         else
             asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
         // ------------------------------------------------------------------------ softmax
         const int a = (warp - 4) >> 2, quad = warp & 3, rowi = quad * 32 + lane;
         const uint32_t lane_addr = static_cast<uint32_t>(quad * 32) << 16;
         const float sc = p.scale_log2;
-        uint32_t done = 0, syncs = 0;   // tiles so far, all items
+        uint32_t done = 0;              // tiles so far, all items
         bool ok = true;
-        auto softmax_sync = [&]() -> bool {
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive(&c.gs);
-            return warp_wait(&c.gs, syncs++ & 1, &c.abort);
-        };
         const int rq = a * 128 + rowi;
-        // what the softmax needs of an item; the next one is worked out ahead
-        struct {
-            int p0, np, base, t0, t1, slot, sp;
-            uint32_t row0;              // row of out that the item's first position and head is
-        } it;
-        auto look = [&](int idx) {
-            const WItem w = item_of<NQ, KT>(c, p, idx);
-            it.p0 = w.p0;
-            it.np = w.np;
-            it.base = w.base;
-            it.t0 = w.t0;
-            it.t1 = w.t1;
-            it.slot = w.slot;
-            it.sp = w.sp;
-            it.row0 = static_cast<uint32_t>(w.layer * p.n_rows + w.r0) * (p.n_kv_heads * G) + w.kvh * G;
-        };
+        Rows it;
         if (static_cast<int>(blockIdx.x) < total)
-            look(blockIdx.x);
+            it = look(blockIdx.x);
         for (int idx = blockIdx.x; idx < total; idx += gridDim.x) {
-            const int dp = rq >> p.group_log2, h = rq & (G - 1);
+            const int dp = rq >> p.group_log2;
             const bool valid = dp < it.np;
+            const bool live = a * 128 + quad * 32 < it.np * G;   // some row of the warp is valid
             const int i = it.p0 + dp;                       // this row's position
             const int e1 = min(p.n_sink, i + 1);            // list columns [0, e1) and [a2, e2)
             const int a2 = max(i - p.n_window + 1, 0) - it.base, e2 = i - it.base + 1;
@@ -467,40 +574,57 @@ __global__ void __launch_bounds__(128 + 128 * NQ, NQ == 1 ? 2 : 1)
                 if (!ok)
                     break;
                 tc_fence_after();
-                float s[KT];
-                const uint32_t sa = s_col(a, buf) + lane_addr;
-#pragma unroll
-                for (int q = 0; q < KT / 32; ++q)
-                    tmem_ld32(sa + 32 * q, s + 32 * q);
-#pragma unroll
-                for (int q = 0; q < KT / 32; ++q)
-                    tmem_landed(s + 32 * q);
-                const int c0 = t * KT;
-                const bool whole = a2 <= c0 && e2 >= c0 + KT;
-                uint32_t hidden = 0;        // 32-column chunks that no row of the warp sees
-                if (!__all_sync(0xffffffffu, whole)) {
-#pragma unroll
-                    for (int w = 0; w < KT / 32; ++w) {
-                        const uint32_t see = span_bits(0, e1 - c0, w) | span_bits(a2 - c0, e2 - c0, w);
-                        if (!__any_sync(0xffffffffu, valid && see != 0u)) {
-                            hidden |= 1u << w;
-                        } else if (!__all_sync(0xffffffffu, see == 0xffffffffu)) {
-#pragma unroll
-                            for (int x = 0; x < 32; ++x)
-                                s[32 * w + x] = (see >> x) & 1u ? s[32 * w + x] : -CUDART_INF_F;
-                        }
+                if (!live) {
+                    // (the product takes what lies there, into rows that nobody reads)
+                    if (lane == 0) {
+                        if (NH == 2)
+                            mbar_arrive(&c.pf[a][0]);
+                        mbar_arrive(&c.pf[a][NH == 2 ? 1 : buf]);
                     }
+                    continue;
                 }
+                const uint32_t sa = s_col(a, buf) + lane_addr;
+                const int c0 = t * KT;
+                const bool whole = __all_sync(0xffffffffu, a2 <= c0 && e2 >= c0 + KT);
+                // 64 columns of scores stay in registers from the maximum to the weights; of a
+                // 128-column tile the other 64 are looked at first and read again later, which
+                // costs less than the registers of a whole row (spills go to L2 here: shared
+                // memory leaves next to no L1).
+                constexpr int kC = KT / 32;
+                float s[64];
+                uint32_t hidden = 0;        // 32-column chunks that no row of the warp sees
+                // chunk q, its columns that the row does not see at -inf
+                auto mask = [&](float *v, int q) {
+                    const uint32_t see = span_bits(0, e1 - c0, q) | span_bits(a2 - c0, e2 - c0, q);
+                    if (!__any_sync(0xffffffffu, valid && see != 0u)) {
+                        hidden |= 1u << q;
+                    } else if (!__all_sync(0xffffffffu, see == 0xffffffffu)) {
+#pragma unroll
+                        for (int x = 0; x < 32; ++x)
+                            v[x] = (see >> x) & 1u ? v[x] : -CUDART_INF_F;
+                    }
+                };
                 float mx[4] = {m, m, m, m};
 #pragma unroll
-                for (int w = 0; w < KT / 32; ++w) {
-                    if ((hidden >> w) & 1u)
-                        continue;
+                for (int q0 = kC - 2; q0 >= 0; q0 -= 2) {
+                    tmem_ld32(sa + 32 * q0, s);
+                    tmem_ld32(sa + 32 * q0 + 32, s + 32);
+                    tmem_landed(s);
+                    tmem_landed(s + 32);
+                    if (!whole) {
+                        mask(s, q0);
+                        mask(s + 32, q0 + 1);
+                    }
 #pragma unroll
-                    for (int x = 0; x < 32; x += 8) {
+                    for (int q = 0; q < 2; ++q) {
+                        if ((hidden >> (q0 + q)) & 1u)
+                            continue;
 #pragma unroll
-                        for (int y = 0; y < 4; ++y)
-                            mx[y] = max3(mx[y], s[32 * w + x + 2 * y], s[32 * w + x + 2 * y + 1]);
+                        for (int x = 0; x < 32; x += 8) {
+#pragma unroll
+                            for (int y = 0; y < 4; ++y)
+                                mx[y] = max3(mx[y], s[32 * q + x + 2 * y], s[32 * q + x + 2 * y + 1]);
+                        }
                     }
                 }
                 const float mn = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
@@ -527,52 +651,53 @@ __global__ void __launch_bounds__(128 + 128 * NQ, NQ == 1 ? 2 : 1)
                 const float off = m == -CUDART_INF_F ? 0.f : -m * sc;
                 const uint64_t sc2 = pack2(sc, sc), off2 = pack2(off, off);
                 uint64_t sum[2] = {0, 0};
+                // weights of chunk q over the first 16 columns of its scores, the remainders (TWO)
+                // over the other 16; 16 keys at a time
 #pragma unroll
-                for (int q = 0; q < KT / 32; ++q) {
-                    uint32_t w[16], r[TWO ? 16 : 1];
-                    if ((hidden >> q) & 1u) {
+                for (int q = 0; q < kC; ++q) {
+                    float *v = s + 32 * (q & 1);
+                    if (q >= 2) {
+                        tmem_landed(v);
+                        if (!whole)
+                            mask(v, q);
+                    }
 #pragma unroll
-                        for (int x = 0; x < 16; ++x)
-                            w[x] = r[TWO ? x : 0] = 0u;
-                    } else {
-                        // in a rolling order, so that the exponentials of a pair issue between the
-                        // arithmetic of its neighbours
-                        uint64_t z = fma2(pack2(s[32 * q], s[32 * q + 1]), sc2, off2);
-                        float2 pp = make_float2(0.f, 0.f);
+                    for (int part = 0; part < 2; ++part) {
+                        uint32_t w[8], r[TWO ? 8 : 1];
+                        if ((hidden >> q) & 1u) {
 #pragma unroll
-                        for (int x = 0; x <= 16; ++x) {
-                            const float2 zz = unpack2(z);
-                            float2 pn;
-                            if (x < 16)
-                                pn.x = ex2_approx(zz.x);
-                            if (x < 15)
-                                z = fma2(pack2(s[32 * q + 2 * x + 2], s[32 * q + 2 * x + 3]), sc2, off2);
-                            if (x > 0) {
-                                sum[x & 1] = add2(sum[x & 1], pack2(pp.x, pp.y));
-                                const __nv_bfloat162 hi = __floats2bfloat162_rn(pp.x, pp.y);
-                                w[x - 1] = *reinterpret_cast<const uint32_t *>(&hi);
+                            for (int x = 0; x < 8; ++x)
+                                w[x] = r[TWO ? x : 0] = 0u;
+                        } else {
+#pragma unroll
+                            for (int x = 0; x < 8; ++x) {
+                                const float2 z = unpack2(fma2(pack2(v[16 * part + 2 * x], v[16 * part + 2 * x + 1]), sc2, off2));
+                                const float p0 = ex2_approx(z.x), p1 = ex2_approx(z.y);
+                                sum[x & 1] = add2(sum[x & 1], pack2(p0, p1));
+                                const __nv_bfloat162 hi = __floats2bfloat162_rn(p0, p1);
+                                w[x] = *reinterpret_cast<const uint32_t *>(&hi);
                                 if (TWO) {
                                     const float2 b = __bfloat1622float2(hi);
-                                    const __nv_bfloat162 lo = __floats2bfloat162_rn(pp.x - b.x, pp.y - b.y);
-                                    r[TWO ? x - 1 : 0] = *reinterpret_cast<const uint32_t *>(&lo);
+                                    const __nv_bfloat162 lo = __floats2bfloat162_rn(p0 - b.x, p1 - b.y);
+                                    r[TWO ? x : 0] = *reinterpret_cast<const uint32_t *>(&lo);
                                 }
                             }
-                            if (x < 16)
-                                pn.y = ex2_approx(zz.y);
-                            pp = pn;
                         }
+                        if (NH == 2 && q == kC / 2 && part == 1) {
+                            // the first half of the weights has been stored for a while: let its
+                            // product go
+                            tmem_st_wait();
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0)
+                                mbar_arrive(&c.pf[a][0]);
+                        }
+                        tmem_st8(sa + 32 * q + 8 * part, w);
+                        if (TWO)
+                            tmem_st8(sa + 32 * q + 16 + 8 * part, r);
                     }
-                    if (NH == 2 && q == KT / 64) {
-                        // the first half of the weights has been stored for a while: let its product go
-                        tmem_st_wait();
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0)
-                            mbar_arrive(&c.pf[a][0]);
-                    }
-                    tmem_st16(sa + 16 * q, w);
-                    if (TWO)
-                        tmem_st16(sa + KT / 2 + 16 * q, r);
+                    if (q + 2 < kC)
+                        tmem_ld32(sa + 32 * q + 64, v);
                 }
                 const float2 sums = unpack2(add2(sum[0], sum[1]));
                 l += sums.x + sums.y;
@@ -584,102 +709,27 @@ __global__ void __launch_bounds__(128 + 128 * NQ, NQ == 1 ? 2 : 1)
             }
             if (!ok)
                 break;
-            // ------------------------------------------------------------------ epilogue
-            const bool any = it.t1 > it.t0;
-            const uint32_t row0 = it.row0, my_row = row0 + dp * (p.n_kv_heads * G) + h;
-            const int nrows = it.np * G, slot = it.slot;
-            const size_t part = static_cast<size_t>(slot) * p.n_split + it.sp;
-            const float inv = p.n_split == 1 ? 1.f / l : 1.f;
             // the next item is worked out while the last products run
+            const Rows now = it;
             if (idx + static_cast<int>(gridDim.x) < total)
-                look(idx + gridDim.x);
-            if (any) {
-                ok = warp_wait(&c.od[a][(done - 1) % NS], ((done - 1) / NS) & 1, &c.abort);
-                if (!ok)
-                    break;
-                tc_fence_after();
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    float o[64];
-                    tmem_ld32(o_col(a) + lane_addr + 64 * q, o);
-                    tmem_ld32(o_col(a) + lane_addr + 64 * q + 32, o + 32);
-                    tmem_landed(o);
-                    tmem_landed(o + 32);
-                    if (q == 1) {
-                        // O is free for the next item
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0)
-                            mbar_arrive(&c.oe[a]);
-                    }
-                    if (valid) {
-#pragma unroll
-                        for (int x = 0; x < 64; ++x)
-                            o[x] *= inv;
-                        if (p.n_split == 1) {
-                            store_row<64>(p, static_cast<size_t>(my_row) * kHeadDim + 64 * q, o);
-                        } else {
-                            float *w = p.parts + (part * p.part_rows + rq) * kHeadDim + 64 * q;
-#pragma unroll
-                            for (int x = 0; x < 64; x += 8)
-                                st_global32(w + x, reinterpret_cast<const uint32_t *>(o + x));
-                        }
-                    }
-                }
-            }
-            if (p.n_split > 1) {
-                if (valid)
-                    p.part_ml[part * p.part_rows + rq] = make_float2(m, l);
-                // every softmax thread's partials before the ticket, the ticket before any read
-                __threadfence();
-                if (!(ok = softmax_sync()))
-                    break;
-                if (tid == 128)
-                    c.last = atomic_add_acq_rel_gpu(p.tickets + slot, 1) == p.n_split - 1;
-                if (!(ok = softmax_sync()))
-                    break;
-                if (c.last != 0) {
-                    if (tid == 128)
-                        p.tickets[slot] = 0;
-                    __threadfence();
-                    // a thread per (row, dim): 128 dims, NQ rows at a time
-                    const int d = (tid - 128) & 127;
-                    for (int r = (tid - 128) >> 7; r < nrows; r += NQ) {
-                        const size_t p0 = static_cast<size_t>(slot) * p.n_split * p.part_rows + r;
-                        float M = -CUDART_INF_F;
-                        for (int sp = 0; sp < p.n_split; ++sp)
-                            M = fmaxf(M, __ldcg(p.part_ml + p0 + static_cast<size_t>(sp) * p.part_rows).x);
-                        float acc = 0.f, den = 0.f;
-                        for (int sp = 0; sp < p.n_split; ++sp) {
-                            const size_t at = p0 + static_cast<size_t>(sp) * p.part_rows;
-                            const float2 ml = __ldcg(p.part_ml + at);
-                            if (ml.y > 0.f) {
-                                const float w = ex2_approx((ml.x - M) * sc);
-                                acc = fmaf(w, __ldcg(p.parts + at * kHeadDim + d), acc);
-                                den = fmaf(w, ml.y, den);
-                            }
-                        }
-                        const int dpr = r >> p.group_log2;
-                        const size_t o = static_cast<size_t>(row0 + dpr * (p.n_kv_heads * G) + (r & (G - 1))) *
-                                             kHeadDim + d;
-                        if (p.out_fp32)
-                            static_cast<float *>(p.out)[o] = acc / den;
-                        else
-                            static_cast<__nv_bfloat16 *>(p.out)[o] = __float2bfloat16_rn(acc / den);
-                    }
-                }
-            }
+                it = look(idx + gridDim.x);
+            ok = finish(a, now, done, m, l);
+            if (!ok)
+                break;
         }
         if (!ok && lane == 0)
             wfail(c, p.err);
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        if (NQ == 2)
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+        else
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         if (warp == 0) {
             // ------------------------------------------------------------------ TMA producer
             int use = 0, items = 0;
             bool ok = true;
             for (int idx = blockIdx.x; idx < total && ok; idx += gridDim.x) {
-                const WItem it = item_of<NQ, KT>(c, p, idx);
+                const WItem it = item_of<kRows, KT, SPLIT>(c, p, idx);
                 if (it.t0 == it.t1)
                     continue;
                 const long long unit = p.page_size
@@ -723,13 +773,13 @@ __global__ void __launch_bounds__(128 + 128 * NQ, NQ == 1 ? 2 : 1)
                         // the queries behind the first keys: they wait for the last item's scores
                         ok = mbar_wait(&c.qe, (items & 1) ^ 1, &c.abort);
                         if (ok) {
-                            mbar_arrive_expect_tx(&c.qf, NQ * 32768);
+                            mbar_arrive_expect_tx(&c.qf, NQ * 2 * kHalfQ);
 #pragma unroll
                             for (int a = 0; a < NQ; ++a)
 #pragma unroll
                                 for (int h = 0; h < 2; ++h)
                                     tma_load_3d(smem + (2 * a + h) * kHalfQ, &tm_q, &c.qf, 64 * h, it.kvh * G,
-                                                it.layer * p.n_rows + it.r0 + a * (128 / G));
+                                                it.layer * p.n_rows + it.r0 + a * (QR / G));
                         }
                     }
                     if (!have_q) {
@@ -795,14 +845,15 @@ __global__ void __launch_bounds__(128 + 128 * NQ, NQ == 1 ? 2 : 1)
 #pragma unroll
                     for (int k2 = 0; k2 < kBlocks / NH; ++k2) {
                         const int kk = half * (kBlocks / NH) + k2;
-                        umma_bf16_ta(d, w + part * (KT / 2) + kk * 8, dv + kk * 128, idesc_o,
+                        umma_bf16_ta(d, w + (kk >> 1) * 32 + part * 16 + (kk & 1) * 8, dv + kk * 128,
+                                     idesc_o,
                                      kk > 0 || part > 0 ? 1u : first ? 0u : 1u);
                     }
                 if (half == NH - 1)
                     umma_commit(&c.od[A][buf]);
             };
             for (uint32_t idx = blockIdx.x; idx < all && ok; idx += gridDim.x) {
-                const WItem it = item_of<NQ, KT>(c, p, idx);
+                const WItem it = item_of<kRows, KT, SPLIT>(c, p, idx);
                 const uint32_t end = seq + uniform(it.t1 - it.t0);
                 if (seq == end)
                     continue;
@@ -886,7 +937,7 @@ __global__ void __launch_bounds__(128 + 128 * NQ, NQ == 1 ? 2 : 1)
             int use = 0;
             bool ok = true;
             for (int idx = blockIdx.x; idx < total && ok; idx += gridDim.x) {
-                const WItem it = item_of<NQ, KT>(c, p, idx);
+                const WItem it = item_of<kRows, KT, SPLIT>(c, p, idx);
                 const int last = it.p0 + it.np - 1;
                 for (int t = it.t0; t < it.t1; ++t, ++use) {
                     const int st = use % ST;
@@ -931,29 +982,40 @@ __global__ void __launch_bounds__(128 + 128 * NQ, NQ == 1 ? 2 : 1)
     }
 }
 
-template <int NQ, int KT, int ST, int NS, bool TWO>
+template <int NQ, int KT, int ST, int NS, int QR, bool TWO, bool SPLIT>
 cudaError_t launch_one(const WindowParams &p, const CUtensorMap &tm_k, const CUtensorMap &tm_v,
                        const CUtensorMap &tm_q, int grid, cudaStream_t stream)
 {
-    auto *kern = window_kernel<NQ, KT, ST, NS, TWO>;
-    constexpr int smem = window_smem<NQ, KT, ST>();
+    auto *kern = window_kernel<NQ, KT, ST, NS, QR, TWO, SPLIT>;
+    constexpr int smem = window_smem<NQ, KT, ST, QR>();
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e == cudaSuccess)
         e = launch_pdl(kern, dim3(grid), dim3(128 + 128 * NQ), smem, stream, tm_k, tm_v, tm_q, p);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
+template <int NQ, int KT, int ST, int NS, int QR>
+cudaError_t launch_form(const WindowParams &p, const CUtensorMap &tm_k, const CUtensorMap &tm_v,
+                        const CUtensorMap &tm_q, int grid, cudaStream_t stream)
+{
+    if (p.n_split > 1)
+        return p.out_fp32 ? launch_one<NQ, KT, ST, NS, QR, true, true>(p, tm_k, tm_v, tm_q, grid, stream)
+                          : launch_one<NQ, KT, ST, NS, QR, false, true>(p, tm_k, tm_v, tm_q, grid, stream);
+    return p.out_fp32 ? launch_one<NQ, KT, ST, NS, QR, true, false>(p, tm_k, tm_v, tm_q, grid, stream)
+                      : launch_one<NQ, KT, ST, NS, QR, false, false>(p, tm_k, tm_v, tm_q, grid, stream);
+}
+
 }  // namespace
 
-cudaError_t launch_window(const WindowParams &p, int n_qtiles, const CUtensorMap &tm_k,
+cudaError_t launch_window(const WindowParams &p, int rows, const CUtensorMap &tm_k,
                           const CUtensorMap &tm_v, const CUtensorMap &tm_q, int grid,
                           cudaStream_t stream)
 {
-    if (n_qtiles == 2)
-        return p.out_fp32 ? launch_one<2, 128, 2, 1, true>(p, tm_k, tm_v, tm_q, grid, stream)
-                          : launch_one<2, 128, 2, 1, false>(p, tm_k, tm_v, tm_q, grid, stream);
-    return p.out_fp32 ? launch_one<1, 64, 2, 2, true>(p, tm_k, tm_v, tm_q, grid, stream)
-                      : launch_one<1, 64, 2, 2, false>(p, tm_k, tm_v, tm_q, grid, stream);
+    if (rows == 256)
+        return launch_form<2, 128, 2, 1, 128>(p, tm_k, tm_v, tm_q, grid, stream);
+    if (rows == 16)
+        return launch_form<1, 64, 3, 2, 16>(p, tm_k, tm_v, tm_q, grid, stream);
+    return launch_form<1, 64, 2, 2, 128>(p, tm_k, tm_v, tm_q, grid, stream);
 }
 
 }  // namespace sfi
