@@ -543,13 +543,10 @@ __global__ void __launch_bounds__(128 + 128 * NQ, NQ == 1 ? 2 : 1)
     };
 
     // Registers (launched with 168 a thread, or 128 with two CTAs per SM): the softmax keeps a
-    // score row, the other roles give up what they do not need.
-    // 384 * 168 = 256 * 200 + 128 * 104; 256 * 128 = 128 * 184 + 128 * 72.
+    // score row, the other roles give up what they do not need. 384 * 168 = 256 * 208 + 128 * 88
+    // = 256 * 200 + 128 * 104; 256 * 128 = 128 * 192 + 128 * 64.
     if (warp >= 4) {
-        if (NQ == 2)
-            asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
-        else
-            asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(NQ == 1 ? 192 : TWO ? 200 : 208));
         // ------------------------------------------------------------------------ softmax
         const int a = (warp - 4) >> 2, quad = warp & 3, rowi = quad * 32 + lane;
         const uint32_t lane_addr = static_cast<uint32_t>(quad * 32) << 16;
@@ -709,21 +706,23 @@ __global__ void __launch_bounds__(128 + 128 * NQ, NQ == 1 ? 2 : 1)
             }
             if (!ok)
                 break;
-            // the next item is worked out while the last products run
+            // The next item is worked out while the last products run; where that would cost spills
+            // (one tile of 128 rows), afterwards.
+            constexpr bool kAhead = NQ == 2 || QR == 16;
+            const bool more = idx + static_cast<int>(gridDim.x) < total;
             const Rows now = it;
-            if (idx + static_cast<int>(gridDim.x) < total)
+            if (kAhead && more)
                 it = look(idx + gridDim.x);
             ok = finish(a, now, done, m, l);
             if (!ok)
                 break;
+            if (!kAhead && more)
+                it = look(idx + gridDim.x);
         }
         if (!ok && lane == 0)
             wfail(c, p.err);
     } else {
-        if (NQ == 2)
-            asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
-        else
-            asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(NQ == 1 ? 64 : TWO ? 104 : 88));
         if (warp == 0) {
             // ------------------------------------------------------------------ TMA producer
             int use = 0, items = 0;
