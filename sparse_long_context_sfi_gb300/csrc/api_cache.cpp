@@ -48,7 +48,7 @@ sfi_status check_pool(const sfi_kv_cache *kv, const sfi_page_pool *pool)
 size_t page_scratch(const sfi_kv_cache *kv, char *base, PageScratch *s)
 {
     const size_t pages = static_cast<size_t>(kv->n_pages) * sizeof(int32_t);
-    const int words = (kv->max_pages_per_seq + 31) / 32;
+    const int words = (kv->max_pages_per_seq + 31) / 32 + 1;   // a range may start inside a word
     size_t o = 0;
     auto take = [&](size_t bytes) {
         char *at = base + o;
@@ -57,11 +57,12 @@ size_t page_scratch(const sfi_kv_cache *kv, char *base, PageScratch *s)
     };
     s->list = static_cast<int32_t *>(take(pages));
     s->movers = static_cast<int32_t *>(take(pages));
-    s->remap = static_cast<int32_t *>(take(pages));
-    s->n_moves = static_cast<int32_t *>(take(sizeof(int32_t)));
-    s->marks = static_cast<uint32_t *>(take(static_cast<size_t>(kv->batch) * words * sizeof(uint32_t)));
+    s->rank = static_cast<int32_t *>(take(pages));
+    s->n_moves = static_cast<int32_t *>(take(2 * sizeof(int32_t)));
+    const size_t tasks = static_cast<size_t>(kv->batch) * words;
+    s->marks = static_cast<uint32_t *>(take(tasks * sizeof(uint32_t)));
+    s->counts = static_cast<int32_t *>(take((tasks + 1) * sizeof(int32_t)));
     s->copies = static_cast<int4 *>(take(static_cast<size_t>(kv->batch) * sizeof(int4)));
-    s->words = words;
     return o;
 }
 
@@ -385,6 +386,7 @@ sfi_status sfi_reorder(const sfi_kv_cache *kv, const sfi_page_pool *pool,
         part(3, mem->rows, kv->n_layers, kv->n_kv_heads, nullptr);
     }
     part(4, kv->seq_len, 1, 1, nullptr);
+    // the rows first: the matrices say how many rows there are
     cudaError_t e = cudaSuccess;
     if (mem)
         e = launch_reorder_rows(p, mem->kc, mem->vc, kv->n_layers, budget->n_sink + budget->n_select,

@@ -75,113 +75,176 @@ __device__ __forceinline__ int warp_prefix(int v, int *sh, int &total)
     return mine;
 }
 
-// One CTA: (A) a warp per sequence marks the entries that need a page, (B) the lowest free
-// pages are listed, (C) a warp per sequence hands them out. The marks are kept because the
-// sharing rule reads other sequences' entries, which (C) changes.
+// Inclusive prefix sums over the warp.
+__device__ __forceinline__ int warp_scan(int x)
+{
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(kFull, x, o);
+        if (lane >= o)
+            x += y;
+    }
+    return x;
+}
+
+// One CTA. A task is 32 columns of one sequence's range; tasks are numbered by sequence, then
+// position, so that the running count of entries that need a page, over tasks, is the order in
+// which pages are handed out. (A) a warp per task marks its entries, four tasks in flight;
+// (B) the marks are counted; (C) the lowest free pages are listed; (D) a warp per task hands
+// them out. The marks are kept because the sharing rule of (A) reads other sequences' entries,
+// which (D) changes. What is left is latency: about eight dependent round trips to L2.
+constexpr int kTasksInSmem = 1024, kListInSmem = 2048;
+
 __global__ void __launch_bounds__(kPlanThreads) reserve_kernel(const PageParams p,
                                                                const int32_t *n_new, uint8_t *ok,
                                                                const PageScratch s)
 {
-    __shared__ int first[kMaxBatch], last[kMaxBatch], need[kMaxBatch], base[kMaxBatch];
-    __shared__ int sh[32], sh_total;
+    __shared__ int first[kMaxBatch], last[kMaxBatch], task0[kMaxBatch + 1];
+    __shared__ int8_t state[kMaxBatch];     // 0: to be served, -1: refused or not active
+    __shared__ uint8_t tail[kMaxBatch];     // rows in the current page
+    __shared__ uint32_t sh_marks[kTasksInSmem];
+    __shared__ int sh_count[kTasksInSmem + 1], sh_list[kListInSmem], sh[32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     pdl_wait();
-    for (int b = tid; b < p.batch; b += kPlanThreads) {
+    // the first chunk's counts are asked for at once: nothing before (D) changes them
+    int held[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+        held[i] = warp * 512 + lane + 32 * i < p.n_pages ? p.refs[warp * 512 + lane + 32 * i] : 1;
+    if (tid < p.batch) {
+        const int b = tid;
         const bool on = !p.active || p.active[b];
         const int L = p.seq_len[b], n = n_new ? n_new[b] : 1;
-        int f = 0, l = -1, state = on ? 0 : -1;
+        int f = 0, l = -1, st = on ? 0 : -1;
         if (on && (L < 0 || L > p.max_len)) {
             raise_error(p.err, 0x8u);  // SFI_DEVERR_LENGTH
-            state = -1;
+            st = -1;
         } else if (on && n > 0) {
             if (n > p.capacity - L) {
                 raise_error(p.err, 0x2u);  // SFI_DEVERR_CAPACITY
-                state = -1;
+                st = -1;
             } else {
                 f = L >> 4;
                 l = (L + n - 1) >> 4;
-                const int e = (L & 15) ? p.table[static_cast<size_t>(b) * p.max_pages + f] : 0;
-                if (e < 0 || e >= p.n_pages) {
-                    raise_error(p.err, 0x1u);  // SFI_DEVERR_PAGE_RANGE
-                    state = -1;
-                    l = -1;
-                }
             }
         }
         first[b] = f;
         last[b] = l;
-        need[b] = state;
-    }
-    __syncthreads();
-    // (A)
-    for (int b = warp; b < p.batch; b += 32) {
-        const int32_t *row = p.table + static_cast<size_t>(b) * p.max_pages;
-        int count = 0;
-        for (int c0 = first[b]; c0 <= last[b]; c0 += 32) {
-            const int c = c0 + lane;
-            bool want = false;
-            int e = -1, holders = 0;
-            if (c <= last[b]) {
-                e = row[c];
-                want = e < 0;
-                if (e >= p.n_pages) {
-                    raise_error(p.err, 0x1u);
-                    want = true;   // a bad entry ahead is replaced
-                } else if (e >= 0) {
-                    holders = p.refs[e];
-                }
-            }
-            // shared pages (as a rule one per sequence, its current page): the warp counts the
-            // earlier sequences that reserve on the same page
-            for (uint32_t sh_m = __ballot_sync(kFull, holders > 1); sh_m != 0; sh_m &= sh_m - 1) {
-                const int src = __ffs(sh_m) - 1, page = __shfl_sync(kFull, e, src), col = c0 + src;
-                int before = 0;
-                for (int o = lane; o < b; o += 32)
-                    before += (col >= first[o] && col <= last[o] &&
-                               p.table[static_cast<size_t>(o) * p.max_pages + col] == page);
-                before = __reduce_add_sync(kFull, before);
-                if (lane == src)
-                    want = holders - before > 1;
-            }
-            const uint32_t m = __ballot_sync(kFull, want);
-            if (lane == 0)
-                s.marks[static_cast<size_t>(b) * s.words + ((c0 - first[b]) >> 5)] = m;
-            count += __popc(m);
-        }
-        if (lane == 0 && need[b] == 0)
-            need[b] = count;
+        tail[b] = static_cast<uint8_t>(L & 15);
+        state[b] = static_cast<int8_t>(st);
+        s.copies[b] = make_int4(0, 0, 0, 0);    // page to, page from, rows
     }
     __syncthreads();
     if (warp == 0) {
         int run = 0;
         for (int b0 = 0; b0 < p.batch; b0 += 32) {
-            const int v = b0 + lane < p.batch ? max(0, need[b0 + lane]) : 0;
-            int x = v;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int y = __shfl_up_sync(kFull, x, o);
-                if (lane >= o)
-                    x += y;
-            }
-            if (b0 + lane < p.batch)
-                base[b0 + lane] = run + x - v;
+            const int b = b0 + lane;
+            const int v = b < p.batch && last[b] >= first[b] ? ((last[b] - first[b]) >> 5) + 1 : 0;
+            const int x = warp_scan(v);
+            if (b < p.batch)
+                task0[b] = run + x - v;
             run += __shfl_sync(kFull, x, 31);
         }
         if (lane == 0)
-            sh_total = run;
+            task0[p.batch] = run;
     }
     __syncthreads();
-    const int total = sh_total;
-    // (B) each warp takes 512 consecutive pages of a chunk of 16384
+    const int tasks = task0[p.batch];
+    uint32_t *marks = tasks <= kTasksInSmem ? sh_marks : s.marks;
+    int *count = tasks <= kTasksInSmem ? sh_count : s.counts;
+    // the sequence of a task: the last b with task0[b] <= t
+    auto owner = [&](int t) {
+        int lo = 0, hi = p.batch;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (task0[mid] <= t)
+                lo = mid;
+            else
+                hi = mid;
+        }
+        return lo;
+    };
+    // (A)
+    for (int t0 = warp; t0 < tasks; t0 += 128) {      // tasks t0, t0 + 32, t0 + 64, t0 + 96
+        int b[4], c0[4], e[4], holders[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            b[q] = t0 + 32 * q < tasks ? owner(t0 + 32 * q) : -1;
+            c0[q] = b[q] < 0 ? 0 : first[b[q]] + 32 * (t0 + 32 * q - task0[b[q]]);
+            e[q] = b[q] >= 0 && c0[q] + lane <= last[b[q]]
+                       ? p.table[static_cast<size_t>(b[q]) * p.max_pages + c0[q] + lane]
+                       : 0x7fffffff;
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            holders[q] = e[q] >= 0 && e[q] < p.n_pages ? p.refs[e[q]] : 0;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            if (b[q] < 0)
+                continue;
+            const bool in = c0[q] + lane <= last[b[q]];
+            bool want = in && (e[q] < 0 || e[q] >= p.n_pages);   // (a bad entry ahead is replaced)
+            if (in && e[q] >= p.n_pages)
+                raise_error(p.err, 0x1u);
+            // shared pages (as a rule one per sequence, its current page): the warp counts the
+            // earlier sequences that reserve on the same page
+            for (uint32_t sm = __ballot_sync(kFull, holders[q] > 1); sm != 0; sm &= sm - 1) {
+                const int src = __ffs(sm) - 1, page = __shfl_sync(kFull, e[q], src), col = c0[q] + src;
+                int before = 0;
+                for (int o = lane; o < b[q]; o += 32)
+                    before += (col >= first[o] && col <= last[o] &&
+                               p.table[static_cast<size_t>(o) * p.max_pages + col] == page);
+                before = __reduce_add_sync(kFull, before);
+                if (lane == src)
+                    want = holders[q] - before > 1;
+            }
+            const uint32_t m = __ballot_sync(kFull, want);
+            if (lane == 0) {
+                marks[t0 + 32 * q] = m;
+                // a current page that holds rows has to be there
+                if (c0[q] == first[b[q]] && tail[b[q]] && (e[q] < 0 || e[q] >= p.n_pages)) {
+                    raise_error(p.err, 0x1u);  // SFI_DEVERR_PAGE_RANGE
+                    state[b[q]] = -1;
+                }
+            }
+        }
+    }
+    __syncthreads();
+    // (B)
+    int total = 0;
+    for (int t0 = 0; t0 < tasks; t0 += kPlanThreads) {
+        const int t = t0 + tid;
+        int v = 0;
+        if (t < tasks) {
+            if (state[owner(t)] != 0)
+                marks[t] = 0;       // refused: nothing is handed out
+            v = __popc(marks[t]);
+        }
+        const int x = warp_scan(v);
+        int sum;
+        const int before = warp_prefix(__shfl_sync(kFull, x, 31), sh, sum);
+        if (t < tasks)
+            count[t] = total + before + x - v;
+        total += sum;
+    }
+    if (tid == 0)
+        count[tasks] = total;
+    int32_t *list = total <= kListInSmem ? sh_list : s.list;
+    // (C) each warp takes 512 consecutive pages of a chunk of 16384
     int found = 0;
     for (int chunk = 0; chunk < p.n_pages && found < total; chunk += 16384) {
         const int at = chunk + warp * 512 + lane;
+        if (chunk > 0) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                held[i] = at + 32 * i < p.n_pages ? p.refs[at + 32 * i] : 1;
+        }
         uint32_t bits[16];
         int mine = 0;
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-            const int id = at + 32 * i;
-            bits[i] = __ballot_sync(kFull, id < p.n_pages && p.refs[id] == 0);
+            bits[i] = __ballot_sync(kFull, held[i] == 0);
             mine += __popc(bits[i]);
         }
         int sum;
@@ -190,43 +253,38 @@ __global__ void __launch_bounds__(kPlanThreads) reserve_kernel(const PageParams 
         for (int i = 0; i < 16; ++i) {
             const int k = pos + __popc(bits[i] & ((1u << lane) - 1u));
             if (((bits[i] >> lane) & 1u) && k < total)
-                s.list[k] = at + 32 * i;
+                list[k] = at + 32 * i;
             pos += __popc(bits[i]);
         }
         found += sum;
     }
     __syncthreads();
-    // (C)
-    for (int b = warp; b < p.batch; b += 32) {
-        const bool fits = need[b] <= 0 || base[b] + need[b] <= found;
-        int4 copy = make_int4(0, 0, 0, 0);   // page to, page from, rows
-        if (need[b] > 0 && fits) {
-            int32_t *row = p.table + static_cast<size_t>(b) * p.max_pages;
-            int k = base[b];
-            const int rows = p.seq_len[b] & 15;
-            for (int c0 = first[b]; c0 <= last[b]; c0 += 32) {
-                const uint32_t m = s.marks[static_cast<size_t>(b) * s.words + ((c0 - first[b]) >> 5)];
-                if ((m >> lane) & 1u) {
-                    const int c = c0 + lane, old = row[c];
-                    const int page = s.list[k + __popc(m & ((1u << lane) - 1u))];
-                    row[c] = page;
-                    p.refs[page] = 1;
-                    if (old >= 0 && old < p.n_pages) {
-                        atomicSub(p.refs + old, 1);
-                        if (c == first[b])
-                            copy = make_int4(page, old, rows, 0);
-                    }
-                }
-                k += __popc(m);
-            }
+    // (D)
+    for (int t = warp; t < tasks; t += 32) {
+        const uint32_t m = marks[t];
+        if (m == 0)
+            continue;
+        const int b = owner(t);
+        if (count[task0[b + 1]] > found || !((m >> lane) & 1u))
+            continue;
+        const int c = first[b] + 32 * (t - task0[b]) + lane;
+        int32_t *entry = p.table + static_cast<size_t>(b) * p.max_pages + c;
+        const int page = list[count[t] + __popc(m & ((1u << lane) - 1u))], old = *entry;
+        *entry = page;
+        p.refs[page] = 1;
+        if (old >= 0 && old < p.n_pages) {
+            atomicSub(p.refs + old, 1);
+            if (c == first[b])
+                s.copies[b] = make_int4(page, old, tail[b], 0);
         }
-        if (lane == 0) {
-            if (!fits)
-                raise_error(p.err, 0x10u);  // SFI_DEVERR_POOL
-            s.copies[b] = copy;   // (lane 0 holds column first[b])
-            if (ok)
-                ok[b] = need[b] >= 0 && fits ? 1 : 0;
-        }
+    }
+    if (tid < p.batch) {
+        const int upto = count[task0[tid + 1]];
+        const bool fits = upto == count[task0[tid]] || upto <= found;
+        if (!fits)
+            raise_error(p.err, 0x10u);  // SFI_DEVERR_POOL
+        if (ok)
+            ok[tid] = state[tid] == 0 && fits ? 1 : 0;
     }
 }
 
@@ -252,7 +310,7 @@ __global__ void __launch_bounds__(256) copy_rows_kernel(const PageParams p, cons
 // ------------------------------------------------------------------------------ compaction
 
 // One CTA: U = pages in use, the free ids below U and the used ids from U on, both ascending,
-// paired; remap[id] is where a page ends up.
+// so that the i-th of one goes to the i-th of the other; rank[id] is that i for a used id.
 __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const PageParams p,
                                                                     int32_t *n_used,
                                                                     const PageScratch s)
@@ -260,61 +318,69 @@ __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const PagePa
     __shared__ int sh[32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     pdl_wait();
+    // occupancy of a chunk of 16384 pages, a warp 512 of them; the first chunk's is kept
+    auto occupied = [&](int chunk, uint32_t *bits) {
+        const int at = chunk + warp * 512 + lane;
+        int held[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            held[i] = at + 32 * i < p.n_pages ? p.refs[at + 32 * i] : 0;
+        int mine = 0;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            bits[i] = __ballot_sync(kFull, held[i] != 0);
+            mine += __popc(bits[i]);
+        }
+        return mine;
+    };
+    uint32_t bits[16];
     int used = 0, sum;
-    for (int id = tid; id < p.n_pages; id += kPlanThreads)
-        used += p.refs[id] != 0;
-    used = __reduce_add_sync(kFull, used);
+    for (int chunk = (p.n_pages - 1) / 16384 * 16384; chunk >= 0; chunk -= 16384)
+        used += occupied(chunk, bits);      // (the first chunk last: its bits stay)
     warp_prefix(used, sh, sum);
     const int U = sum;
     int holes = 0, movers = 0;
     for (int chunk = 0; chunk < p.n_pages; chunk += 16384) {
-        const int at = chunk + warp * 512 + lane;
-        uint32_t bits[16];
+        if (chunk > 0)
+            occupied(chunk, bits);
+        const int at0 = chunk + warp * 512;
         int mine = 0;
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-            const int id = at + 32 * i;
-            const bool in = id < p.n_pages;
-            const bool full = in && p.refs[id] != 0;
-            if (in)
-                s.remap[id] = id;
             // below U the free ids count, from U on the used ones
-            bits[i] = __ballot_sync(kFull, in && (id < U ? !full : full));
-            const uint32_t below = __ballot_sync(kFull, id < U);
+            const int left = U - (at0 + 32 * i);
+            const uint32_t below = left >= 32 ? kFull : left <= 0 ? 0u : (1u << left) - 1u;
+            bits[i] = (~bits[i] & below) | (bits[i] & ~below);
             mine += __popc(bits[i] & below) + (__popc(bits[i] & ~below) << 16);
         }
         // both counts of a chunk in one word: at most 16384 each
-        int pos = warp_prefix(mine, sh, sum);
+        const int pos = warp_prefix(mine, sh, sum);
         int h = holes + (pos & 0xffff), m = movers + (pos >> 16);
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-            const int id = at + 32 * i;
-            const uint32_t below = __ballot_sync(kFull, id < U);
+            const int left = U - (at0 + 32 * i), id = at0 + 32 * i + lane;
+            const uint32_t below = left >= 32 ? kFull : left <= 0 ? 0u : (1u << left) - 1u;
             const uint32_t hb = bits[i] & below, mb = bits[i] & ~below, lower = (1u << lane) - 1u;
             if ((hb >> lane) & 1u)
                 s.list[h + __popc(hb & lower)] = id;
-            if ((mb >> lane) & 1u)
+            if ((mb >> lane) & 1u) {
                 s.movers[m + __popc(mb & lower)] = id;
+                s.rank[id] = m + __popc(mb & lower);
+            }
             h += __popc(hb);
             m += __popc(mb);
         }
         holes += sum & 0xffff;
         movers += sum >> 16;
     }
-    __syncthreads();
-    for (int i = tid; i < movers; i += kPlanThreads) {
-        const int from = s.movers[i], to = s.list[i];
-        s.remap[from] = to;
-        p.refs[to] = p.refs[from];
-        p.refs[from] = 0;
-    }
     if (tid == 0) {
         *n_used = U;
-        *s.n_moves = movers;
+        s.n_moves[0] = movers;
+        s.n_moves[1] = U;
     }
 }
 
-// Tables through the remap, and the moved pages: one 4 KB piece (a head's page) per warp step.
+// Tables, counts and the moved pages: one 4 KB piece (a head's page) per warp step.
 __global__ void __launch_bounds__(256) compact_move_kernel(const PageParams p, const PageScratch s,
                                                            uint4 *k, uint4 *v, int n_layers)
 {
@@ -322,15 +388,21 @@ __global__ void __launch_bounds__(256) compact_move_kernel(const PageParams p, c
     const long long threads = static_cast<long long>(gridDim.x) * 256;
     const long long t0 = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
     const long long entries = static_cast<long long>(p.batch) * p.max_pages;
+    const int moves = s.n_moves[0], U = s.n_moves[1];
+    for (long long i = t0; i < moves; i += threads) {
+        const int from = s.movers[i], to = s.list[i];
+        p.refs[to] = p.refs[from];
+        p.refs[from] = 0;
+    }
     for (long long i = t0; i < entries; i += threads) {
         const int e = p.table[i];
         if (e >= p.n_pages)
             raise_error(p.err, 0x1u);
-        else if (e >= 0)
-            p.table[i] = s.remap[e];
+        else if (e >= U)
+            p.table[i] = s.list[s.rank[e]];
     }
     const int lane = threadIdx.x & 31;
-    const long long pieces = static_cast<long long>(*s.n_moves) * n_layers * 2 * p.n_kv_heads;
+    const long long pieces = static_cast<long long>(moves) * n_layers * 2 * p.n_kv_heads;
     const size_t layer = static_cast<size_t>(p.n_pages) * p.n_kv_heads * 256;
     for (long long w = t0 >> 5; w < pieces; w += threads >> 5) {
         const int head = static_cast<int>(w % p.n_kv_heads);
@@ -449,7 +521,9 @@ __global__ void __launch_bounds__(256) append_chunk_kernel(const ChunkParams p,
     }
 }
 
-// The lengths after the rows: a warp per sequence, which first looks over the chunk's pages.
+// The lengths after the rows: a warp per sequence, which first looks over the chunk's pages. (A
+// cluster of CTAs per sequence that wrote the rows and then advanced the length in one launch
+// took 9.3 us for 32 sequences of 1 to 40 rows in four layers; the two launches take 7.)
 __global__ void __launch_bounds__(1024) advance_kernel(const ChunkParams p)
 {
     pdl_trigger();
@@ -507,6 +581,47 @@ __device__ __forceinline__ int moved_list(const int32_t *src, int batch, int2 *m
     return *count;
 }
 
+// The int32 matrices [layers][batch][cols] of a sequence's state, permuted over the batch, 32
+// columns per CTA: page table (with its reference counts), selections, counts, lengths.
+__global__ void __launch_bounds__(256) reorder_ints_kernel(const ReorderParams p)
+{
+    extern __shared__ int held[];
+    __shared__ int2 mv[kMaxBatch];
+    __shared__ int n_mv;
+    pdl_wait();
+    const int n = moved_list(p.src, p.batch, mv, &n_mv, p.err, blockIdx.x == 0);
+    int part = 0, slice = blockIdx.x;
+    while (slice >= p.ints[part].slices)
+        slice -= p.ints[part++].slices;
+    const ReorderInts &a = p.ints[part];
+    const int per_layer = (a.cols + 31) / 32;
+    const int layer = slice / per_layer, c0 = (slice - layer * per_layer) * 32;
+    int32_t *t = a.data + static_cast<size_t>(layer) * p.batch * a.cols;
+    const int lane = threadIdx.x & 31, c = c0 + lane;
+    if (c < a.cols)
+        for (int i = threadIdx.x >> 5; i < n; i += 8)
+            held[i * 32 + lane] = t[static_cast<size_t>(mv[i].y) * a.cols + c];
+    __syncthreads();
+    if (c >= a.cols)
+        return;
+    for (int i = threadIdx.x >> 5; i < n; i += 8) {
+        int32_t *e = t + static_cast<size_t>(mv[i].x) * a.cols + c;
+        const int now = held[i * 32 + lane];
+        if (a.refs) {
+            const int was = *e;
+            if (was != now) {
+                if (now >= p.n_pages || was >= p.n_pages)
+                    raise_error(p.err, 0x1u);  // SFI_DEVERR_PAGE_RANGE
+                if (now >= 0 && now < p.n_pages)
+                    atomicAdd(a.refs + now, 1);
+                if (was >= 0 && was < p.n_pages)
+                    atomicSub(a.refs + was, 1);
+            }
+        }
+        *e = now;
+    }
+}
+
 // Bulk rows, [layers][batch][heads][rows_per_head] of 256 bytes, permuted over the batch in
 // place. A CTA holds the same few rows of one head of every moving sequence: each of its
 // threads reads its 16-byte pieces of them into registers, all at once, and writes them after
@@ -550,47 +665,6 @@ __global__ void __launch_bounds__(256) reorder_rows_kernel(const ReorderParams p
             t[mv[m0 + q * step].x * stride + col] = x[q];
 }
 
-// The int32 matrices [layers][batch][cols] of a sequence's state, permuted the same way, 32
-// columns per CTA: page table (with its reference counts), selections, counts, lengths.
-__global__ void __launch_bounds__(256) reorder_ints_kernel(const ReorderParams p)
-{
-    extern __shared__ int held[];
-    __shared__ int2 mv[kMaxBatch];
-    __shared__ int n_mv;
-    pdl_wait();
-    const int n = moved_list(p.src, p.batch, mv, &n_mv, p.err, blockIdx.x == 0);
-    int part = 0, slice = blockIdx.x;
-    while (slice >= p.ints[part].slices)
-        slice -= p.ints[part++].slices;
-    const ReorderInts &a = p.ints[part];
-    const int per_layer = (a.cols + 31) / 32;
-    const int layer = slice / per_layer, c0 = (slice - layer * per_layer) * 32;
-    int32_t *t = a.data + static_cast<size_t>(layer) * p.batch * a.cols;
-    const int lane = threadIdx.x & 31, c = c0 + lane;
-    if (c < a.cols)
-        for (int i = threadIdx.x >> 5; i < n; i += 8)
-            held[i * 32 + lane] = t[static_cast<size_t>(mv[i].y) * a.cols + c];
-    __syncthreads();
-    if (c >= a.cols)
-        return;
-    for (int i = threadIdx.x >> 5; i < n; i += 8) {
-        int32_t *e = t + static_cast<size_t>(mv[i].x) * a.cols + c;
-        const int now = held[i * 32 + lane];
-        if (a.refs) {
-            const int was = *e;
-            if (was != now) {
-                if (now >= p.n_pages || was >= p.n_pages)
-                    raise_error(p.err, 0x1u);  // SFI_DEVERR_PAGE_RANGE
-                if (now >= 0 && now < p.n_pages)
-                    atomicAdd(a.refs + now, 1);
-                if (was >= 0 && was < p.n_pages)
-                    atomicSub(a.refs + was, 1);
-            }
-        }
-        *e = now;
-    }
-}
-
 }  // namespace
 
 cudaError_t launch_drop_pages(const PageParams &p, int evict, int n_sink, int n_window,
@@ -625,20 +699,16 @@ cudaError_t launch_pages_compact(const PageParams &p, int32_t *n_used, const Pag
 cudaError_t launch_append_chunk(const ChunkParams &p, const void *k_new, const void *v_new, void *k,
                                 void *v, int n_layers, cudaStream_t stream)
 {
-    cudaError_t e = cudaSuccess;
-    if (p.n_rows > 0)
-        e = launch_pdl(append_chunk_kernel, dim3((p.n_rows + kChunkRows - 1) / kChunkRows, n_layers),
-                       dim3(256), 0, stream, p, static_cast<const uint4 *>(k_new),
-                       static_cast<const uint4 *>(v_new), static_cast<uint4 *>(k),
-                       static_cast<uint4 *>(v));
+    cudaError_t e = launch_pdl(append_chunk_kernel, dim3((p.n_rows + kChunkRows - 1) / kChunkRows, n_layers),
+                   dim3(256), 0, stream, p, static_cast<const uint4 *>(k_new),
+                   static_cast<const uint4 *>(v_new), static_cast<uint4 *>(k), static_cast<uint4 *>(v));
     if (e == cudaSuccess)
         e = launch_pdl(advance_kernel, dim3(1), dim3(1024), 0, stream, p);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 cudaError_t launch_reorder_rows(const ReorderParams &p, void *k, void *v, int n_layers,
-                                int rows_per_head, const int32_t *rows, int rows_by_unit,
-                                cudaStream_t stream)
+                                int rows_per_head, const int32_t *rows, int rows_by_unit, cudaStream_t stream)
 {
     // pieces per sequence and CTA: a power of two such that the batch fits the threads' registers
     // (8 each, 16 from batch 129 on); at most 256, at least one row

@@ -151,11 +151,11 @@ struct PageParams {
 struct PageScratch {
     int32_t *list;              // free pages, ascending [n_pages]
     int32_t *movers;            // pages that move [n_pages]
-    int32_t *remap;             // where each page ends up [n_pages]
-    int32_t *n_moves;
-    uint32_t *marks;            // entries that need a page, bit per column [batch][words]
+    int32_t *rank;              // their place among those [n_pages]
+    int32_t *n_moves;           // pages that move, pages in use
+    uint32_t *marks;            // entries that need a page, a bit each [batch * words]
+    int32_t *counts;            // and how many before [batch * words + 1]
     int4 *copies;               // page to, page from, rows [batch]
-    int words;
 };
 
 struct ChunkParams {
