@@ -9,6 +9,11 @@
 // inserted one by one, the chunk from its end, so that neither ascending nor descending logits
 // insert every token. Warps of a CTA, the CTAs of a row (splits) and the rows of a group are
 // joined by the same insertion; the last CTA of a group does the last two.
+//
+// Issue slots bound it (a token's share at the copy rate is ~22 of fp32, ~11 of bf16), so the
+// sums are kept relative to R = fl(max * log2 e): exp(x) / 2^R = 2^(x log2 e - R) is then one
+// exact-product multiply-add and an exponential per token, whatever the size of the logits,
+// and only the scores of the chosen few are formed from R, in double.
 #include "sfi_device.cuh"
 
 #include <math_constants.h>
@@ -21,12 +26,43 @@ constexpr int kBeamWarps = kBeamThreads / 32;
 constexpr int kLaneTok = 16;                 // tokens per lane and chunk
 constexpr uint32_t kAll = 0xffffffffu;
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLowest = -0x1p126f;         // logits below it are masks (a power of two, so that its
+                                             // product with kLog2e is exact)
 
 // a before b: higher logit, then lower token (empty places, v < 0, last)
 __device__ __forceinline__ bool better(float xa, int va, float xb, int vb)
 {
     // (unsigned: an empty place, -1, is behind every token)
     return xa > xb || (xa == xb && static_cast<uint32_t>(va) < static_cast<uint32_t>(vb));
+}
+
+// Two floats at a time (sm_100 has packed fp32 adds and multiply-adds).
+__device__ __forceinline__ uint64_t pack2(float a, float b)
+{
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+    return d;
+}
+
+__device__ __forceinline__ float2 unpack2(uint64_t v)
+{
+    float2 f;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
+    return f;
+}
+
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
 }
 
 __device__ __forceinline__ float ex2(float x)
@@ -159,6 +195,7 @@ __global__ void __launch_bounds__(kBeamThreads, 4) beam_kernel(const BeamParams 
     __shared__ int sh_v[kMaxBeams][kBeamWarps];
     __shared__ float cand_x[kBeamWarps][32 * kLaneTok];   // a chunk's candidates, in any order
     __shared__ int cand_v[kBeamWarps][32 * kLaneTok], n_cand[kBeamWarps];
+    __shared__ volatile float top[kBeamWarps];
     __shared__ float row_x[kMaxBeams][kMaxBeams], row_s[kMaxBeams][kMaxBeams];
     __shared__ int row_v[kMaxBeams][kMaxBeams];
     __shared__ uint8_t row_done[kMaxBeams];
@@ -166,7 +203,10 @@ __global__ void __launch_bounds__(kBeamThreads, 4) beam_kernel(const BeamParams 
     constexpr int V = Chunk<T>::kV;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int K = p.n_beams, row = blockIdx.y, split = blockIdx.x, group = row / K;
+    if (tid < kBeamWarps)
+        top[tid] = -CUDART_INF_F;
     pdl_wait();
+    __syncthreads();
     if (!(p.done && p.done[row])) {
         const T *x0 = static_cast<const T *>(p.logits) + static_cast<size_t>(row) * p.row_stride;
         const int shift = static_cast<int>((reinterpret_cast<uintptr_t>(x0) & 15u) / sizeof(T));
@@ -175,7 +215,7 @@ __global__ void __launch_bounds__(kBeamThreads, 4) beam_kernel(const BeamParams 
         Best best;
         best.clear();
         bool fresh = true;          // (the same in every lane, as is all that decides a branch here)
-        float m = -CUDART_INF_F, s = 0.f;
+        float R = -CUDART_INF_F, s = 0.f;
         int c = (split * kBeamWarps + warp) * kStep;
         const int stride = p.splits * kBeamWarps * kStep;
         uint4 w[kLaneTok / V];
@@ -188,30 +228,48 @@ __global__ void __launch_bounds__(kBeamThreads, 4) beam_kernel(const BeamParams 
                 Chunk<T>::unpack(w[i], x + V * i);
             if (c + stride < pieces)
                 load_chunk(x0, shift, p.vocab, c + stride, lane, w);
-            float cm = x[0];
+            float cm = -CUDART_INF_F;       // (fmaxf drops NaN)
 #pragma unroll
-            for (int j = 1; j < kLaneTok; ++j)
+            for (int j = 0; j < kLaneTok; ++j)
                 cm = fmaxf(cm, x[j]);
-            // sum of exp(x - m), the lane's own running maximum
-            const float mn = fmaxf(m, cm);
-            if (mn > -CUDART_INF_F) {
-                float a0 = 0.f, a1 = 0.f;
+            // sum of 2^(x log2 e - R), R the lane's own running reference
+            const float rn = fmaxf(R, cm > -CUDART_INF_F ? fmaxf(cm, kLowest) * kLog2e : -CUDART_INF_F);
+            if (rn > kLowest * 0.5f) {
+                const uint64_t c2 = pack2(kLog2e, kLog2e), r2 = pack2(-rn, -rn);
+                uint64_t acc = 0;
 #pragma unroll
                 for (int j = 0; j < kLaneTok; j += 2) {
-                    a0 += ex2((x[j] - mn) * kLog2e);
-                    a1 += ex2((x[j + 1] - mn) * kLog2e);
+                    const float2 z = unpack2(fma2(pack2(x[j], x[j + 1]), c2, r2));
+                    acc = add2(acc, pack2(ex2(z.x), ex2(z.y)));
                 }
-                s = (m > -CUDART_INF_F ? s * ex2((m - mn) * kLog2e) : s) + (a0 + a1);
-                m = mn;
+                const float2 a = unpack2(acc);
+                s = (R > -CUDART_INF_F ? s * ex2(R - rn) : s) + (a.x + a.y);
+                R = rn;
             } else {
-                // nothing but -inf, or NaN, which has to show in the sum
+                // nothing but -inf and masks of the type's lowest value (which count alike, and only
+                // where there is nothing else), or NaN, which has to show in the sum
+                s = R > -CUDART_INF_F ? s * ex2(R - rn) : s;
+                R = rn;
 #pragma unroll
                 for (int j = 0; j < kLaneTok; ++j)
-                    s = x[j] == -CUDART_INF_F ? s : CUDART_NAN_F;
+                    s += x[j] > -CUDART_INF_F ? ex2(fmaf(fmaxf(x[j], kLowest), kLog2e, -rn))
+                                              : x[j] == x[j] ? 0.f : CUDART_NAN_F;
             }
             // Tokens that beat the K-th best so far. A warp's first chunk starts the list with
             // every lane's best; the others that still beat it go through shared memory.
-            if (__any_sync(kAll, cm > best.tx || best.tv < 0)) {
+            // What all warps of the CTA hold bounds it too: top[w] is the ceil(K / 8)-th best of warp
+            // w, so at least K tokens are as high as the lowest of them (read without a barrier: an
+            // older value is only a weaker bound).
+            bool look = __any_sync(kAll, cm > best.tx || best.tv < 0);
+            float floor = -CUDART_INF_F;
+            if (look) {
+                floor = top[lane & (kBeamWarps - 1)];
+#pragma unroll
+                for (int o = 1; o < kBeamWarps; o <<= 1)
+                    floor = fminf(floor, __shfl_xor_sync(kAll, floor, o));
+                look = __any_sync(kAll, cm >= floor && (cm > best.tx || best.tv < 0));
+            }
+            if (look) {
                 const int v0 = (c + lane) * V - shift;
                 // (tokens grow with j, so the first of equal logits is the lowest token)
                 auto token = [&](int j) { return v0 + 32 * V * (j / V) + j % V; };
@@ -231,9 +289,10 @@ __global__ void __launch_bounds__(kBeamThreads, 4) beam_kernel(const BeamParams 
                 if (lane == 0)
                     n_cand[warp] = 0;
                 __syncwarp();
+                floor = fmaxf(floor, best.tx);
 #pragma unroll
                 for (int j = 0; j < kLaneTok; ++j) {
-                    if (x[j] >= best.tx) {
+                    if (x[j] >= floor) {
                         const int v = token(j);
                         if (v != taken && v >= 0 && v < p.vocab) {
                             const int at = atomicAdd(&n_cand[warp], 1);
@@ -248,15 +307,17 @@ __global__ void __launch_bounds__(kBeamThreads, 4) beam_kernel(const BeamParams 
                     const bool on = i + lane < n;
                     best.offer(on ? cand_x[warp][i + lane] : 0.f, on ? cand_v[warp][i + lane] : -1, K, lane);
                 }
+                if (lane == (K - 1) / kBeamWarps)
+                    top[warp] = best.x;
                 __syncwarp();
             }
         }
-        // the warp's maximum and sum
-        float wm = m;
+        // the warp's reference and sum
+        float wm = R;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1)
             wm = fmaxf(wm, __shfl_xor_sync(kAll, wm, o));
-        float ws = s == 0.f ? 0.f : wm > -CUDART_INF_F ? s * ex2((m - wm) * kLog2e) : s;
+        float ws = s == 0.f ? 0.f : wm > -CUDART_INF_F ? s * ex2(R - wm) : s;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1)
             ws += __shfl_xor_sync(kAll, ws, o);
@@ -284,7 +345,7 @@ __global__ void __launch_bounds__(kBeamThreads, 4) beam_kernel(const BeamParams 
             for (int o = 16; o > 0; o >>= 1)
                 bm = fmaxf(bm, __shfl_xor_sync(kAll, bm, o));
             float bs = lane < kBeamWarps ? sh_s[lane] : 0.f;
-            bs = bs == 0.f ? 0.f : bm > -CUDART_INF_F ? bs * ex2((mine - bm) * kLog2e) : bs;
+            bs = bs == 0.f ? 0.f : bm > -CUDART_INF_F ? bs * ex2(mine - bm) : bs;
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1)
                 bs += __shfl_xor_sync(kAll, bs, o);
@@ -332,8 +393,8 @@ __global__ void __launch_bounds__(kBeamThreads, 4) beam_kernel(const BeamParams 
                 const float2 st = __ldcg(p.part_stat + part + i);
                 const float mn = fmaxf(m, st.x);
                 if (st.y != 0.f) {
-                    const float add = mn > -CUDART_INF_F ? st.y * ex2((st.x - mn) * kLog2e) : st.y;
-                    s = (s != 0.f && mn > -CUDART_INF_F ? s * ex2((m - mn) * kLog2e) : s) + add;
+                    const float add = mn > -CUDART_INF_F ? st.y * ex2(st.x - mn) : st.y;
+                    s = (s != 0.f && mn > -CUDART_INF_F ? s * ex2(m - mn) : s) + add;
                     m = mn;
                 }
             }
@@ -341,11 +402,10 @@ __global__ void __launch_bounds__(kBeamThreads, 4) beam_kernel(const BeamParams 
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1)
                 wm = fmaxf(wm, __shfl_xor_sync(kAll, wm, o));
-            s = s == 0.f ? 0.f : wm > -CUDART_INF_F ? s * ex2((m - wm) * kLog2e) : s;
+            s = s == 0.f ? 0.f : wm > -CUDART_INF_F ? s * ex2(m - wm) : s;
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1)
                 s += __shfl_xor_sync(kAll, s, o);
-            // maximum and log of the sum stay apart: their sum would round at |m|
             const float ls = logf(s);
             const bool dead = !isfinite(wm) || !isfinite(ls) || !isfinite(cum);
             if (dead) {
@@ -360,7 +420,11 @@ __global__ void __launch_bounds__(kBeamThreads, 4) beam_kernel(const BeamParams 
                     else
                         best.offer(ox, ov, K, lane);
                 }
-                score = cum + ((best.x - wm) - ls);
+                // x - R / kLog2e in double: in fp32 it would round at the size of the logits
+                if (best.v >= 0) {
+                    const double bx = wm > kLowest * 0.5f ? best.x : fmaxf(best.x, kLowest);
+                    score = static_cast<float>(bx - wm / static_cast<double>(kLog2e) - ls + cum);
+                }
             }
         }
         if (lane < K) {

@@ -127,6 +127,41 @@ def test_lowest_finite_logits():
     check(o, x, cum, 2)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_rows_masked_with_the_lowest_value(dtype):
+    """A row of nothing but the type's lowest value is uniform; beside a real logit such a
+    token keeps its own (hopeless, finite) score."""
+    x = torch.full((6, 9001), torch.finfo(dtype).min, device="cuda", dtype=dtype)
+    x[3, 4000], x[4, 17], x[4, 18], x[5, 9000] = 2.0, 1.0, 0.5, -3.0
+    cum = torch.tensor([-1.0, -2.0, -3.0, -1.0, -1.5, -40.0], device="cuda")
+    o = run(x, cum, 3)
+    check(o, x, cum, 3)
+    x[3:, :] = torch.finfo(dtype).min
+    x[3, 4000] = 2.0
+    cum[4:] = -float("inf")
+    o = run(x, cum, 3)
+    check(o, x, cum, 3)
+
+
+def test_large_logits_keep_their_differences():
+    g = torch.Generator(device="cuda").manual_seed(8)
+    x = 20000 + torch.randn((8, 5000), generator=g, device="cuda")
+    x[4:] -= 40000
+    cum = -torch.rand(8, generator=g, device="cuda")
+    o = run(x, cum, 4)
+    check(o, x, cum, 4)
+
+
+def test_sorted_logits():
+    """Ascending and descending logits: every chunk beats the ones before it, or none does."""
+    x = torch.arange(40000, device="cuda", dtype=torch.float32).repeat(4, 1) * 1e-3
+    x[2:] = x[2:].flip(1)
+    cum = -torch.arange(4, device="cuda", dtype=torch.float32)
+    for beams in (1, 4):
+        o = run(x, cum, beams)
+        check(o, x, cum, beams)
+
+
 def test_repeatable_and_captured():
     g = torch.Generator(device="cuda").manual_seed(5)
     x = torch.randn((16, 40000), generator=g, device="cuda")
