@@ -201,6 +201,18 @@ __device__ __forceinline__ uint32_t span_bits(int lo, int hi, int w)
 
 constexpr int kMaxStages = 4;
 
+// An item as the producer works it out and the other roles read it.
+struct WItem {
+    int b, layer, kvh;
+    int r0, np, p0;             // first packed row, positions, first position
+    int lo;                     // first position of the joint window
+    int sb, nb, base;           // sink blocks, all blocks; position = list column + base behind the sinks
+    int t0, t1;                 // tiles of this split
+    int slot, sp;
+    uint32_t row0;              // row of out that the first position and head is
+};
+constexpr int kItemRing = 4;
+
 struct WCtrl {
     uint64_t kf[kMaxStages], ke[kMaxStages], vf[kMaxStages], vr[kMaxStages], ve[kMaxStages];
     uint64_t qf, qe;
@@ -211,6 +223,8 @@ struct WCtrl {
     // tiles ahead of the products, and one barrier's parity tells only one phase
     uint64_t od[2][2];
     uint64_t oe[2];             // O read out (one arrival per softmax warp)
+    uint64_t itf[kItemRing];    // items[i] written
+    uint64_t ite[kItemRing];    // and read (one arrival per reading warp)
     uint64_t drain;
     uint64_t gs;                // all softmax warps (splits only)
     uint32_t tmem;
@@ -220,17 +234,9 @@ struct WCtrl {
     int tiles;                  // q tiles (of 128 NQ rows) of one layer and kv head
     int pre[kMaxBatch + 1];     // q tiles before each sequence
     int len[kMaxBatch], cnt[kMaxBatch], start[kMaxBatch];
+    WItem items[kItemRing];
 };
 constexpr int kWBars = static_cast<int>((offsetof(WCtrl, tmem)) / sizeof(uint64_t));
-
-struct WItem {
-    int b, layer, kvh;
-    int r0, np, p0;             // first packed row, positions, first position
-    int lo;                     // first position of the joint window
-    int sb, nb, base;           // sink blocks, all blocks; position = list column + base behind the sinks
-    int t0, t1;                 // tiles of this split
-    int slot, sp;
-};
 
 template <int ROWS, int KT, bool SPLIT>
 __device__ __forceinline__ WItem item_of(const WCtrl &c, const WindowParams &p, int idx)
@@ -272,6 +278,7 @@ __device__ __forceinline__ WItem item_of(const WCtrl &c, const WindowParams &p, 
         it.t1 = static_cast<int>(static_cast<uint32_t>(n) * (it.sp + 1) / p.n_split);
     }
     it.slot = (it.layer * c.tiles + t) * p.n_kv_heads + it.kvh;
+    it.row0 = (static_cast<uint32_t>(it.layer * p.n_rows + it.r0) * p.n_kv_heads + it.kvh) << p.group_log2;
     return it;
 }
 
@@ -290,10 +297,10 @@ __device__ __forceinline__ void st_global32(void *p, const uint32_t *w)
 
 // N (32 or 64) output values of one row, a thread per row: in 32-byte pieces, whole sectors,
 // where the output is aligned to them.
-template <int N>
+template <int N, bool FP32>
 __device__ __forceinline__ void store_row(const WindowParams &p, size_t at, const float *v)
 {
-    if (p.out_fp32) {
+    if constexpr (FP32) {
         float *o = static_cast<float *>(p.out) + at;
 #pragma unroll
         for (int i = 0; i < N; i += 8) {
@@ -354,8 +361,9 @@ __global__ void __launch_bounds__(128 + 128 * NQ, NQ == 1 ? 2 : 1)
         uint64_t *bar = reinterpret_cast<uint64_t *>(&c) + tid;
         const int off = tid * 8;
         const bool four = (off >= static_cast<int>(offsetof(WCtrl, pf)) && off < static_cast<int>(offsetof(WCtrl, od))) ||
-                          (off >= static_cast<int>(offsetof(WCtrl, oe)) && off < static_cast<int>(offsetof(WCtrl, drain)));
-        mbar_init(bar, off == static_cast<int>(offsetof(WCtrl, gs)) ? 4 * NQ : four ? 4 : 1);
+                          (off >= static_cast<int>(offsetof(WCtrl, oe)) && off < static_cast<int>(offsetof(WCtrl, itf)));
+        const bool readers = off >= static_cast<int>(offsetof(WCtrl, ite)) && off < static_cast<int>(offsetof(WCtrl, drain));
+        mbar_init(bar, off == static_cast<int>(offsetof(WCtrl, gs)) ? 4 * NQ : readers ? 4 * NQ + 2 : four ? 4 : 1);
         mbar_fence_init();
     }
     if (warp == 1) {
@@ -423,23 +431,16 @@ __global__ void __launch_bounds__(128 + 128 * NQ, NQ == 1 ? 2 : 1)
     auto s_col = [&](int a, int buf) { return tmem + a * (NS * KT + 128) + buf * KT; };
     auto o_col = [&](int a) { return tmem + a * (NS * KT + 128) + NS * KT; };
 
-    // What softmax and epilogue need of an item.
-    struct Rows {
-        int p0, np, base, t0, t1, slot, sp;
-        uint32_t row0;              // row of out that the item's first position and head is
-    };
-    auto look = [&](int idx) {
-        const WItem w = item_of<kRows, KT, SPLIT>(c, p, idx);
-        Rows r;
-        r.p0 = w.p0;
-        r.np = w.np;
-        r.base = w.base;
-        r.t0 = w.t0;
-        r.t1 = w.t1;
-        r.slot = w.slot;
-        r.sp = w.sp;
-        r.row0 = static_cast<uint32_t>(w.layer * p.n_rows + w.r0) * (p.n_kv_heads * G) + w.kvh * G;
-        return r;
+    // The n-th item of this CTA, for the roles other than the producer: what they do not use of it
+    // is never read. False if the wait ran out.
+    auto next_item = [&](uint32_t n, WItem &it) -> bool {
+        if (!warp_wait(&c.itf[n % kItemRing], (n / kItemRing) & 1, &c.abort))
+            return false;
+        it = c.items[n % kItemRing];
+        __syncwarp();
+        if (lane == 0)
+            mbar_arrive(&c.ite[n % kItemRing]);
+        return true;
     };
     uint32_t syncs = 0;
     constexpr int kOut0 = 128;      // the first softmax thread
@@ -451,7 +452,7 @@ __global__ void __launch_bounds__(128 + 128 * NQ, NQ == 1 ? 2 : 1)
     };
     // O of q tile a once its `done`-th tile's product is complete, divided and written (or left as
     // a partial and joined); each thread a row. False if a wait ran out.
-    auto finish = [&](int a, const Rows &it, uint32_t done, float m, float l) -> bool {
+    auto finish = [&](int a, const WItem &it, uint32_t done, float m, float l) -> bool {
         const int quad = warp & 3, rq = a * 128 + quad * 32 + lane;
         const uint32_t lane_addr = static_cast<uint32_t>(quad * 32) << 16;
         const int dp = rq >> p.group_log2, h = rq & (G - 1), nrows = it.np * G;
@@ -463,38 +464,41 @@ __global__ void __launch_bounds__(128 + 128 * NQ, NQ == 1 ? 2 : 1)
             if (!warp_wait(&c.od[a][(done - 1) % NS], ((done - 1) / NS) & 1, &c.abort))
                 return false;
             tc_fence_after();
-            constexpr int kCol = 32;    // columns at a time (registers)
+            auto release = [&] {        // O is free for the next item
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&c.oe[a]);
+            };
+            if (live) {
+                // (the arrays inside the branch: defined on one path only, they would count as live
+                // around the whole loop over items)
+                float o[2][32];         // 32 columns at a time, the next ones on their way
+                tmem_ld32(o_col(a) + lane_addr, o[0]);
 #pragma unroll
-            for (int q = 0; q < 128; q += kCol) {
-                float o[kCol];
-                if (live) {
+                for (int q = 0; q < 4; ++q) {
+                    float *v = o[q & 1];
+                    tmem_landed(v);
+                    if (q < 3)
+                        tmem_ld32(o_col(a) + lane_addr + 32 * q + 32, o[(q + 1) & 1]);
+                    else
+                        release();
+                    if (valid) {
 #pragma unroll
-                    for (int x = 0; x < kCol; x += 32)
-                        tmem_ld32(o_col(a) + lane_addr + q + x, o + x);
+                        for (int x = 0; x < 32; ++x)
+                            v[x] *= inv;
+                        if (!SPLIT) {
+                            store_row<32, TWO>(p, my_row * kHeadDim + 32 * q, v);
+                        } else {
+                            float *w = p.parts + (part * p.part_rows + rq) * kHeadDim + 32 * q;
 #pragma unroll
-                    for (int x = 0; x < kCol; x += 32)
-                        tmem_landed(o + x);
-                }
-                if (q + kCol == 128) {
-                    // O is free for the next item
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0)
-                        mbar_arrive(&c.oe[a]);
-                }
-                if (valid) {
-#pragma unroll
-                    for (int x = 0; x < kCol; ++x)
-                        o[x] *= inv;
-                    if (!SPLIT) {
-                        store_row<kCol>(p, my_row * kHeadDim + q, o);
-                    } else {
-                        float *w = p.parts + (part * p.part_rows + rq) * kHeadDim + q;
-#pragma unroll
-                        for (int x = 0; x < kCol; x += 8)
-                            st_global32(w + x, reinterpret_cast<const uint32_t *>(o + x));
+                            for (int x = 0; x < 32; x += 8)
+                                st_global32(w + x, reinterpret_cast<const uint32_t *>(v + x));
+                        }
                     }
                 }
+            } else {
+                release();
             }
         }
         if (SPLIT) {
@@ -532,7 +536,7 @@ __global__ void __launch_bounds__(128 + 128 * NQ, NQ == 1 ? 2 : 1)
                     const int dpr = r >> p.group_log2;
                     const size_t o = static_cast<size_t>(it.row0 + dpr * (p.n_kv_heads * G) + (r & (G - 1))) *
                                          kHeadDim + d;
-                    if (p.out_fp32)
+                    if (TWO)
                         static_cast<float *>(p.out)[o] = acc / den;
                     else
                         static_cast<__nv_bfloat16 *>(p.out)[o] = __float2bfloat16_rn(acc / den);
@@ -554,10 +558,12 @@ __global__ void __launch_bounds__(128 + 128 * NQ, NQ == 1 ? 2 : 1)
         uint32_t done = 0;              // tiles so far, all items
         bool ok = true;
         const int rq = a * 128 + rowi;
-        Rows it;
-        if (static_cast<int>(blockIdx.x) < total)
-            it = look(blockIdx.x);
-        for (int idx = blockIdx.x; idx < total; idx += gridDim.x) {
+        uint32_t nth = 0;
+        for (int idx = blockIdx.x; idx < total; idx += gridDim.x, ++nth) {
+            WItem it;
+            ok = next_item(nth, it);
+            if (!ok)
+                break;
             const int dp = rq >> p.group_log2;
             const bool valid = dp < it.np;
             const bool live = a * 128 + quad * 32 < it.np * G;   // some row of the warp is valid
@@ -706,18 +712,9 @@ __global__ void __launch_bounds__(128 + 128 * NQ, NQ == 1 ? 2 : 1)
             }
             if (!ok)
                 break;
-            // The next item is worked out while the last products run; where that would cost spills
-            // (one tile of 128 rows), afterwards.
-            constexpr bool kAhead = NQ == 2 || QR == 16;
-            const bool more = idx + static_cast<int>(gridDim.x) < total;
-            const Rows now = it;
-            if (kAhead && more)
-                it = look(idx + gridDim.x);
-            ok = finish(a, now, done, m, l);
+            ok = finish(a, it, done, m, l);
             if (!ok)
                 break;
-            if (!kAhead && more)
-                it = look(idx + gridDim.x);
         }
         if (!ok && lane == 0)
             wfail(c, p.err);
@@ -727,8 +724,17 @@ __global__ void __launch_bounds__(128 + 128 * NQ, NQ == 1 ? 2 : 1)
             // ------------------------------------------------------------------ TMA producer
             int use = 0, items = 0;
             bool ok = true;
-            for (int idx = blockIdx.x; idx < total && ok; idx += gridDim.x) {
+            uint32_t nth = 0;
+            for (int idx = blockIdx.x; idx < total && ok; idx += gridDim.x, ++nth) {
                 const WItem it = item_of<kRows, KT, SPLIT>(c, p, idx);
+                ok = warp_wait(&c.ite[nth % kItemRing], ((nth / kItemRing) & 1) ^ 1, &c.abort);
+                if (!ok)
+                    break;
+                if (lane == 0) {
+                    c.items[nth % kItemRing] = it;
+                    mbar_arrive(&c.itf[nth % kItemRing]);
+                }
+                __syncwarp();
                 if (it.t0 == it.t1)
                     continue;
                 const long long unit = p.page_size
@@ -824,7 +830,7 @@ __global__ void __launch_bounds__(128 + 128 * NQ, NQ == 1 ? 2 : 1)
             const uint64_t dk0 = smem_desc_sw128(smem_u32(kv_smem), 16, 1024);
             const uint64_t dv0 = smem_desc_sw128(smem_u32(kv_smem) + 2 * kHalfKV, kHalfKV, 1024);
             const uint32_t tm = uniform(tmem), all = uniform(total);
-            uint32_t seq = 0, items = 0;      // tiles and items so far
+            uint32_t seq = 0, items = 0, nth = 0;     // tiles, items with tiles and items so far
             bool ok = true;
             // S of q tile A from the keys in stage st
             auto scores = [&](int A, uint32_t st, uint32_t buf) {
@@ -852,7 +858,10 @@ __global__ void __launch_bounds__(128 + 128 * NQ, NQ == 1 ? 2 : 1)
                     umma_commit(&c.od[A][buf]);
             };
             for (uint32_t idx = blockIdx.x; idx < all && ok; idx += gridDim.x) {
-                const WItem it = item_of<kRows, KT, SPLIT>(c, p, idx);
+                WItem it;
+                ok = next_item(nth++, it);
+                if (!ok)
+                    break;
                 const uint32_t end = seq + uniform(it.t1 - it.t0);
                 if (seq == end)
                     continue;
@@ -934,9 +943,13 @@ __global__ void __launch_bounds__(128 + 128 * NQ, NQ == 1 ? 2 : 1)
         } else if (warp == 2) {
             // ------------------------------------------------- V rows that nobody may see := 0
             int use = 0;
+            uint32_t nth = 0;
             bool ok = true;
             for (int idx = blockIdx.x; idx < total && ok; idx += gridDim.x) {
-                const WItem it = item_of<kRows, KT, SPLIT>(c, p, idx);
+                WItem it;
+                ok = next_item(nth++, it);
+                if (!ok)
+                    break;
                 const int last = it.p0 + it.np - 1;
                 for (int t = it.t0; t < it.t1; ++t, ++use) {
                     const int st = use % ST;
