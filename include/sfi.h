@@ -452,7 +452,7 @@ sfi_status sfi_pages_compact(const sfi_kv_cache *kv, const sfi_page_pool *pool, 
  * int32 [batch + 1], ascending). n_rows bounds row_start[batch] and max_rows every sequence's
  * count; rows behind row_start[batch] are not touched. row_start == NULL: one row each
  * (n_rows == batch). A sequence whose rows run backwards, past n_rows or past max_rows is
- * skipped (SFI_DEVERR_ROWS).
+ * skipped (SFI_DEVERR_ROWS); so are, in sfi_window_attn, sequences beyond n_rows rows in all.
  *
  * sfi_append_chunk writes a chunk of new tokens (a prompt or a part of one):
  * k_new, v_new: bf16 [n_layers][n_rows][n_kv_heads][128]. Row i of an active sequence goes to
@@ -476,7 +476,8 @@ sfi_status sfi_append_chunk(const sfi_kv_cache *kv, const void *k_new, const voi
  *   out  [n_layers][n_rows][n_q_heads][128], fp32 if out_fp32 else bf16; rows of inactive or
  *        skipped sequences and rows behind row_start[batch] are not written
  * Cache rows that no row of the call attends to are never looked at (their pages may be
- * missing, their contents may be anything). Softmax weights enter the product with V as bf16;
+ * missing, their contents may be anything); a V row that some row attends to has to be finite,
+ * because its neighbours in the chunk meet it with a weight of zero. Softmax weights enter the product with V as bf16;
  * with out_fp32 as bf16 part and bf16 remainder. n_sink >= 0, n_window >= 1. A sequence longer
  * than max_len, or with more rows than its length, is skipped (SFI_DEVERR_LENGTH).
  *   ws   workspace of at least sfi_window_workspace_bytes(), 256-byte aligned and initialised
@@ -520,7 +521,7 @@ sfi_status sfi_reorder(const sfi_kv_cache *kv, const sfi_page_pool *pool,
  *   cum_out     fp32 [rows]: their scores s; done_out: uint8 [rows] or NULL: done[parent], or
  *               token == eos. Outputs must not overlap the inputs.
  * eos < 0: no token ends a beam (done must be NULL then). 1 <= n_beams <= 16, else
- * SFI_ERR_UNSUPPORTED; n_groups * n_beams <= 65535; vocab < 2^31 / n_beams.
+ * SFI_ERR_UNSUPPORTED; n_groups * n_beams <= 65535; vocab <= 2^30 / n_beams.
  */
 typedef struct sfi_beam {
     int32_t n_groups, n_beams, vocab, logits_fp32;

@@ -147,7 +147,7 @@ sfi_status check_beam(const sfi_beam *b)
         b->eos >= b->vocab)
         return SFI_ERR_INVALID_ARG;
     if (b->n_beams > kMaxBeams || 1LL * b->n_groups * b->n_beams > 65535 ||
-        1LL * b->vocab * b->n_beams >= (1LL << 31))
+        1LL * b->vocab * b->n_beams > (1LL << 30))
         return SFI_ERR_UNSUPPORTED;
     return SFI_OK;
 }
@@ -413,7 +413,8 @@ sfi_status sfi_beam_select(const sfi_beam *beam, void *ws, size_t ws_bytes, void
     if (st != SFI_OK)
         return st;
     if (!beam->logits || !beam->cum || !beam->parent || !beam->token || !beam->cum_out ||
-        (beam->done && beam->eos < 0))
+        (beam->done && beam->eos < 0) ||
+        (reinterpret_cast<uintptr_t>(beam->logits) & (beam->logits_fp32 ? 3u : 1u)))
         return SFI_ERR_INVALID_ARG;
     BeamParams p;
     std::memset(&p, 0, sizeof p);

@@ -403,9 +403,25 @@ __global__ void __launch_bounds__(128 + 128 * NQ, NQ == 1 ? 2 : 1)
     }
     __syncthreads();
     if (warp == 0) {
+        // Sequences whose rows overlap (a row_start that runs backwards somewhere) must not make more
+        // items than the rows can hold: behind n_rows rows in all, the others are skipped.
         int run = 0;
+        long long rows = 0;
         for (int b0 = 0; b0 < p.batch; b0 += 32) {
             const int b = b0 + lane;
+            long long upto = b < p.batch ? c.cnt[b] : 0;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long y = __shfl_up_sync(0xffffffffu, upto, o);
+                if (lane >= o)
+                    upto += y;
+            }
+            if (b < p.batch && c.cnt[b] > 0 && rows + upto > p.n_rows) {
+                c.cnt[b] = 0;
+                if (blockIdx.x == 0)
+                    raise_error(p.err, 0x20u);  // SFI_DEVERR_ROWS
+            }
+            rows += __shfl_sync(0xffffffffu, upto, 31);
             const int v = b < p.batch ? (c.cnt[b] + per - 1) / per : 0;
             int x = v;
 #pragma unroll
@@ -653,7 +669,7 @@ __global__ void __launch_bounds__(128 + 128 * NQ, NQ == 1 ? 2 : 1)
                 m = grow ? mn : m;
                 const float off = m == -CUDART_INF_F ? 0.f : -m * sc;
                 const uint64_t sc2 = pack2(sc, sc), off2 = pack2(off, off);
-                uint64_t sum[2] = {0, 0};
+                uint64_t sum = 0;
                 // weights of chunk q over the first 16 columns of its scores, the remainders (TWO)
                 // over the other 16; 16 keys at a time
 #pragma unroll
@@ -676,7 +692,7 @@ __global__ void __launch_bounds__(128 + 128 * NQ, NQ == 1 ? 2 : 1)
                             for (int x = 0; x < 8; ++x) {
                                 const float2 z = unpack2(fma2(pack2(v[16 * part + 2 * x], v[16 * part + 2 * x + 1]), sc2, off2));
                                 const float p0 = ex2_approx(z.x), p1 = ex2_approx(z.y);
-                                sum[x & 1] = add2(sum[x & 1], pack2(p0, p1));
+                                sum = add2(sum, pack2(p0, p1));
                                 const __nv_bfloat162 hi = __floats2bfloat162_rn(p0, p1);
                                 w[x] = *reinterpret_cast<const uint32_t *>(&hi);
                                 if (TWO) {
@@ -702,7 +718,7 @@ __global__ void __launch_bounds__(128 + 128 * NQ, NQ == 1 ? 2 : 1)
                     if (q + 2 < kC)
                         tmem_ld32(sa + 32 * q + 64, v);
                 }
-                const float2 sums = unpack2(add2(sum[0], sum[1]));
+                const float2 sums = unpack2(sum);
                 l += sums.x + sums.y;
                 tmem_st_wait();
                 tc_fence_before();

@@ -140,5 +140,8 @@ def test_beam_pointers_refused(lib):
                        **{n: DUMMY for n in names})
     assert lib.sfi_beam_select(C.byref(beam), DUMMY, 1 << 30, None) == sfi.SFI_ERR_INVALID_ARG
     beam.done = None
+    beam.logits = DUMMY + 1
+    assert lib.sfi_beam_select(C.byref(beam), DUMMY, 1 << 30, None) == sfi.SFI_ERR_INVALID_ARG
+    beam.logits = DUMMY
     for ws, n in ((None, 1 << 30), (DUMMY + 64, 1 << 30), (DUMMY, 0)):
         assert lib.sfi_beam_select(C.byref(beam), ws, n, None) == sfi.SFI_ERR_WORKSPACE

@@ -53,7 +53,7 @@ def check(o, x, cum, n_beams, done=None, scale=None, eos=2, done_out=True):
     np.testing.assert_array_equal(c(o["token"]), t)
     got, fin = c(o["cum"]).astype(np.float64), np.isfinite(s)
     np.testing.assert_array_equal(got[~fin], s[~fin])
-    assert (np.abs(got - s)[fin] <= 1e-5 + 2.0 ** -20 * np.abs(s[fin])).all()
+    assert (np.abs(got[fin] - s[fin]) <= 1e-5 + 2.0 ** -20 * np.abs(s[fin])).all()
     np.testing.assert_array_equal(c(o["done"]), f if done_out else 9)
 
 

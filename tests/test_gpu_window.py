@@ -199,6 +199,66 @@ def test_bad_inputs_are_reported_and_skipped():
     assert torch.isfinite(c.out[:, 50:180].float()).all()
 
 
+@pytest.mark.parametrize("fp32", [True, False])
+def test_output_aligned_to_16_bytes_only(fp32):
+    c = Case([300, 140], [150, 1], 8, 2, paged=True)
+    c.run(4, 64, fp32)
+    want = c.out.clone()
+    flat = torch.full((c.out.numel() + 8,), -7.0, dtype=c.out.dtype, device="cuda")
+    at = 4 if fp32 else 8
+    out = flat[at:at + c.out.numel()].view(c.out.shape)
+    assert out.data_ptr() % 32 == 16
+    sfi.sfi_window_attn(c.kv, c.q, out, fp32, c.row_start, c.total, max(c.rows), 4, 64, c.ws, c.ws.numel())
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and (flat[:at] == -7.0).all() and (flat[at + out.numel():] == -7.0).all()
+
+
+def test_overlapping_rows_stay_in_bounds():
+    """A row_start that runs backwards: what is skipped is reported, rows of sound sequences in
+    front of it are right, and no other memory is touched."""
+    c = Case([3000, 2000, 2500], [2, 2, 2], 8, 2)
+    c.row_start = torch.tensor([0, 2, 0, 2], dtype=torch.int32, device="cuda")
+    c.n_rows, c.total = 2, 2
+    c.run(4, 2048, max_rows=2)
+    torch.cuda.synchronize()
+    assert int(c.err[0]) == sfi.SFI_DEVERR_ROWS
+    q, k, v = (t.double().cpu().numpy() for t in (c.q, c.flat_k, c.flat_v))
+    o, mag = window_attention(q[0, :2], k[0, 0, :, :3000], v[0, 0, :, :3000], 3000, 4, 2048)
+    assert (np.abs(c.out[0, :2].double().cpu().numpy() - o) <= 1e-4 * mag).all()
+
+
+def test_cache_beyond_32_bit_offsets():
+    """Rows whose byte offset passes 2^32 and whose element offset passes 2^31."""
+    cap, hkv, n = 1 << 21, 4, 1000
+    k = torch.zeros((1, 3, hkv, cap, D), dtype=torch.bfloat16, device="cuda")
+    v = torch.zeros_like(k)
+    assert k.numel() > 1 << 31
+    length = torch.tensor([0, 0, cap - n - 3], dtype=torch.int32, device="cuda")
+    err = torch.zeros(4, dtype=torch.int32, device="cuda")
+    kv = sfi.SfiKvCache(n_layers=1, batch=3, n_q_heads=8, n_kv_heads=hkv, head_dim=D, capacity=cap,
+                        max_len=cap, k=k.data_ptr(), v=v.data_ptr(), seq_len=length.data_ptr(),
+                        err=err.data_ptr())
+    g = torch.Generator(device="cuda").manual_seed(1)
+    rnd = lambda *s: torch.randn(s, generator=g, device="cuda").to(torch.bfloat16)
+    q, kn, vn = rnd(1, n, 8, D), rnd(1, n, hkv, D), rnd(1, n, hkv, D)
+    start = torch.tensor([0, 0, 0, n], dtype=torch.int32, device="cuda")
+    sfi.sfi_append_chunk(kv, kn, vn, start, n, n)
+    assert torch.equal(k[0, 2, :, cap - n - 3:cap - 3], kn[0].transpose(0, 1))
+    out = torch.zeros((1, n, 8, D), device="cuda")
+    nb = sfi.sfi_window_workspace_bytes(kv, n, n, 0, 200)
+    ws = torch.empty(nb, dtype=torch.uint8, device="cuda")
+    sfi.sfi_workspace_init(ws, nb)
+    sfi.sfi_window_attn(kv, q, out, True, start, n, n, 0, 200, ws, nb)
+    torch.cuda.synchronize()
+    assert int(err[0]) == 0
+    # rows from 200 on see new rows alone
+    o, mag = window_attention(q[0].double().cpu().numpy(), kn[0].transpose(0, 1).double().cpu().numpy(),
+                              vn[0].transpose(0, 1).double().cpu().numpy(), n, 0, 200)
+    assert (np.abs(out[0, 200:].double().cpu().numpy() - o[200:]) <= 1e-4 * mag[200:]).all()
+    del k, v
+    torch.cuda.empty_cache()
+
+
 def test_repeatable_and_captured():
     """The same call gives the same bits: again, on another stream, and replayed from a graph
     whose inputs changed in place; and the workspace is ready for the next call."""
