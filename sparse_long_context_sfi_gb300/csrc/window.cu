@@ -84,11 +84,14 @@ __device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t *v)
         : "memory");
 }
 
-__device__ __forceinline__ void tmem_st8(uint32_t addr, const uint32_t *v)
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t *v)
 {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::"r"(v[0]),
-                 "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(addr)
-                 : "memory");
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+        "%11, %12, %13, %14, %15};" ::"r"(v[0]),
+        "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]),
+        "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(addr)
+        : "memory");
 }
 
 // Two floats at a time (sm_100 has packed fp32 adds and multiply-adds).
@@ -671,7 +674,8 @@ __global__ void __launch_bounds__(128 + 128 * NQ, NQ == 1 ? 2 : 1)
                 const uint64_t sc2 = pack2(sc, sc), off2 = pack2(off, off);
                 uint64_t sum = 0;
                 // weights of chunk q over the first 16 columns of its scores, the remainders (TWO)
-                // over the other 16; 16 keys at a time
+                // over the other 16. (Stores of 16 columns: with 8 the 8K chunk under a window of 4096 took
+                // 417 us, with 16 397, with 32 no less.)
 #pragma unroll
                 for (int q = 0; q < kC; ++q) {
                     float *v = s + 32 * (q & 1);
@@ -680,41 +684,38 @@ __global__ void __launch_bounds__(128 + 128 * NQ, NQ == 1 ? 2 : 1)
                         if (!whole)
                             mask(v, q);
                     }
+                    uint32_t w[16], r[TWO ? 16 : 1];
+                    if ((hidden >> q) & 1u) {
 #pragma unroll
-                    for (int part = 0; part < 2; ++part) {
-                        uint32_t w[8], r[TWO ? 8 : 1];
-                        if ((hidden >> q) & 1u) {
+                        for (int x = 0; x < 16; ++x)
+                            w[x] = r[TWO ? x : 0] = 0u;
+                    } else {
 #pragma unroll
-                            for (int x = 0; x < 8; ++x)
-                                w[x] = r[TWO ? x : 0] = 0u;
-                        } else {
-#pragma unroll
-                            for (int x = 0; x < 8; ++x) {
-                                const float2 z = unpack2(fma2(pack2(v[16 * part + 2 * x], v[16 * part + 2 * x + 1]), sc2, off2));
-                                const float p0 = ex2_approx(z.x), p1 = ex2_approx(z.y);
-                                sum = add2(sum, pack2(p0, p1));
-                                const __nv_bfloat162 hi = __floats2bfloat162_rn(p0, p1);
-                                w[x] = *reinterpret_cast<const uint32_t *>(&hi);
-                                if (TWO) {
-                                    const float2 b = __bfloat1622float2(hi);
-                                    const __nv_bfloat162 lo = __floats2bfloat162_rn(p0 - b.x, p1 - b.y);
-                                    r[TWO ? x : 0] = *reinterpret_cast<const uint32_t *>(&lo);
-                                }
+                        for (int x = 0; x < 16; ++x) {
+                            const float2 z = unpack2(fma2(pack2(v[2 * x], v[2 * x + 1]), sc2, off2));
+                            const float p0 = ex2_approx(z.x), p1 = ex2_approx(z.y);
+                            sum = add2(sum, pack2(p0, p1));
+                            const __nv_bfloat162 hi = __floats2bfloat162_rn(p0, p1);
+                            w[x] = *reinterpret_cast<const uint32_t *>(&hi);
+                            if (TWO) {
+                                const float2 b = __bfloat1622float2(hi);
+                                const __nv_bfloat162 lo = __floats2bfloat162_rn(p0 - b.x, p1 - b.y);
+                                r[TWO ? x : 0] = *reinterpret_cast<const uint32_t *>(&lo);
                             }
                         }
-                        if (NH == 2 && q == kC / 2 && part == 1) {
-                            // the first half of the weights has been stored for a while: let its
-                            // product go
-                            tmem_st_wait();
-                            tc_fence_before();
-                            __syncwarp();
-                            if (lane == 0)
-                                mbar_arrive(&c.pf[a][0]);
-                        }
-                        tmem_st8(sa + 32 * q + 8 * part, w);
-                        if (TWO)
-                            tmem_st8(sa + 32 * q + 16 + 8 * part, r);
                     }
+                    if (NH == 2 && q == kC / 2) {
+                        // the first half of the weights has been stored for a while: let its
+                        // product go
+                        tmem_st_wait();
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0)
+                            mbar_arrive(&c.pf[a][0]);
+                    }
+                    tmem_st16(sa + 32 * q, w);
+                    if (TWO)
+                        tmem_st16(sa + 32 * q + 16, r);
                     if (q + 2 < kC)
                         tmem_ld32(sa + 32 * q + 64, v);
                 }
