@@ -477,9 +477,10 @@ sfi_status sfi_append_chunk(const sfi_kv_cache *kv, const void *k_new, const voi
  *        skipped sequences and rows behind row_start[batch] are not written
  * Cache rows that no row of the call attends to are never looked at (their pages may be
  * missing, their contents may be anything); a V row that some row attends to has to be finite,
- * because its neighbours in the chunk meet it with a weight of zero. Softmax weights enter the product with V as bf16;
- * with out_fp32 as bf16 part and bf16 remainder. n_sink >= 0, n_window >= 1. A sequence longer
- * than max_len, or with more rows than its length, is skipped (SFI_DEVERR_LENGTH).
+ * because its neighbours in the chunk meet it with a weight of zero. Softmax weights
+ * enter the product with V as bf16, with out_fp32 in three bf16 parts (24 bits). n_sink >= 0,
+ * n_window >= 1. A sequence longer than max_len, or with more rows than its length, is skipped
+ * (SFI_DEVERR_LENGTH).
  *   ws   workspace of at least sfi_window_workspace_bytes(), 256-byte aligned and initialised
  *        (sfi_workspace_init, once); calls sharing it must not overlap.
  */

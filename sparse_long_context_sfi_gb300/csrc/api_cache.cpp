@@ -91,12 +91,12 @@ struct WindowShape {
     int part_rows;
 };
 
-WindowShape window_shape(const sfi_kv_cache *kv, int n_rows, int max_rows, int rows)
+WindowShape window_shape(const sfi_kv_cache *kv, int n_rows, int max_rows, int rows, bool fp32)
 {
     WindowShape s;
     const int g = kv->n_q_heads / kv->n_kv_heads, sms = sm_count();
     s.rows = rows;
-    s.slots = rows == 256 ? sms : 2 * sms;
+    s.slots = rows == 256 || fp32 ? sms : 2 * sms;
     const long long seqs = n_rows < kv->batch ? n_rows : kv->batch;
     const long long units = 1LL * kv->n_kv_heads * kv->n_layers;
     s.items = (1LL * n_rows * g / s.rows + seqs) * units;
@@ -111,12 +111,13 @@ WindowShape window_shape(const sfi_kv_cache *kv, int n_rows, int max_rows, int r
 // The item size. 16 rows hold a single token's heads and leave room for a third stage. Two q
 // tiles (256 rows) halve the reads of K and V and keep the tensor core busy while the other
 // tile is in its softmax, but only one such CTA fits an SM: where the reach of a row is short,
-// an item is mostly start and end, which two CTAs of 128 rows overlap.
-int window_rows(const sfi_kv_cache *kv, int max_rows, int n_window)
+// an item is mostly start and end, which two CTAs of 128 rows overlap. fp32 outputs take the
+// tensor memory of a second q tile, and of a second CTA, for themselves.
+int window_rows(const sfi_kv_cache *kv, int max_rows, int n_window, bool fp32)
 {
     const long long all = 1LL * max_rows * (kv->n_q_heads / kv->n_kv_heads);
     const int reach = n_window < kv->max_len ? n_window : kv->max_len;
-    return all <= 16 ? 16 : all > 128 && reach >= 512 ? 256 : 128;
+    return all <= 16 ? 16 : all > 128 && reach >= 512 && !fp32 ? 256 : 128;
 }
 
 // Sized for any item size and split, so that it holds for every max_len and window.
@@ -124,7 +125,7 @@ size_t window_scratch(const sfi_kv_cache *kv, int n_rows, int max_rows, char *ba
 {
     size_t o = 0, items = 1, parts = 1;
     for (int rows : {16, 128, 256}) {
-        const WindowShape s = window_shape(kv, n_rows, max_rows, rows);
+        const WindowShape s = window_shape(kv, n_rows, max_rows, rows, false);
         const size_t n = s.most_split > 1 ? static_cast<size_t>(s.items) : 1;
         const size_t m = s.most_split > 1 ? n * s.most_split * s.part_rows : 1;
         items = n > items ? n : items;
@@ -299,7 +300,8 @@ sfi_status sfi_window_attn(const sfi_kv_cache *kv, const void *q, void *out, int
         return SFI_OK;
     if (!q || !out || !aligned16(q) || !aligned16(out))
         return SFI_ERR_INVALID_ARG;
-    const int rows = window_rows(kv, max_rows, n_window);
+    const bool fp32 = out_fp32 != 0;
+    const int rows = window_rows(kv, max_rows, n_window, fp32);
     CUtensorMap tk, tv, tq;
     if (!make_map(&tk, kv->k, cache_rows(kv), 16u) || !make_map(&tv, kv->v, cache_rows(kv), 16u) ||
         !make_chunk_map(&tq, q, static_cast<uint64_t>(kv->n_layers) * n_rows,
@@ -333,7 +335,7 @@ sfi_status sfi_window_attn(const sfi_kv_cache *kv, const void *q, void *out, int
     p.out_aligned32 = (reinterpret_cast<uintptr_t>(out) & 31u) == 0;
     p.err = kv->err;
     const long long len = kv->max_len, reach = n_window < len ? n_window : len;
-    const WindowShape s = window_shape(kv, n_rows, max_rows, rows);
+    const WindowShape s = window_shape(kv, n_rows, max_rows, rows, fp32);
     // Fewer items than CTAs that fit: split their keys, four tiles at least to a split.
     const int kt = rows == 256 ? 128 : 64;
     const long long span = reach + rows / p.group < len ? reach + rows / p.group : len;

@@ -39,6 +39,11 @@ __device__ __forceinline__ float ex2_approx(float x)
     return y;
 }
 
+// fp32 outputs: tiles summed by the tensor core before O moves to M. Error (2-norm) and time of a
+// token of 32 sequences under a window of 4096: every tile 4.9e-7, 238 us; 2 6.6e-7, 194 us;
+// 4 1.1e-6, 189 us; never 1.0e-5.
+constexpr int kFlush = 2;
+
 // 32 tensor-memory columns of this thread's lane; the values are there after tmem_landed.
 __device__ __forceinline__ void tmem_ld32(uint32_t addr, float *v)
 {
@@ -342,17 +347,24 @@ constexpr int window_smem() { return 1024 + NQ * QR * 256 + ST * KT * 512 + stat
 // buffers per q tile. QR 16 is for single tokens: the MMA still takes 128 rows, of which all
 // but the first 16 are whatever lies behind them in shared memory; they end in rows of S and O
 // that nobody reads, and the memory holds a third stage instead.
-// TWO: the weights enter the product with V as bf16 part and bf16 remainder (fp32 outputs).
+// F32 (fp32 outputs): the weights enter the product with V in three bf16 parts, 24 bits, and O
+// is moved every kFlush tiles to a second accumulator M with ordinary additions: the tensor
+// core's own additions do not round to nearest, and 520 of them in a row (two parts, a window of
+// 4096) had left outputs 1.0e-5 off (2-norm). Tensor memory then holds one CTA per SM. A bf16
+// output rounds at 2^-8 and needs neither.
 // SPLIT: an item's keys over several CTAs (the joining code costs registers).
-template <int NQ, int KT, int ST, int NS, int QR, bool TWO, bool SPLIT>
-__global__ void __launch_bounds__(128 + 128 * NQ, NQ == 1 ? 2 : 1)
+template <int NQ, int KT, int ST, int NS, int QR, bool F32, bool SPLIT>
+__global__ void __launch_bounds__(128 + 128 * NQ, NQ == 1 && !F32 ? 2 : 1)
     window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                   const __grid_constant__ CUtensorMap tm_q, const WindowParams p)
 {
     constexpr int kRows = NQ * QR, kHalfQ = QR * 128, kHalfKV = KT * 128, kStage = 4 * kHalfKV, kBlocks = KT / 16;
-    constexpr uint32_t kCols = NQ == 1 ? 256 : 512;
+    constexpr uint32_t kCols = NQ == 1 && !F32 ? 256 : 512;
+    constexpr int kSW = F32 ? KT + KT / 2 : KT;     // columns of a score buffer
+    constexpr int kQTile = NS * kSW + (F32 ? 256 : 128);     // and of a q tile with O (and M)
     constexpr int NH = NS == 1 ? 2 : 1;     // parts in which a tile's weights are handed over
-    static_assert(NQ * (NS * KT + 128) <= static_cast<int>(kCols) && ST <= kMaxStages && NS <= 2);
+    static_assert(NQ * kQTile <= static_cast<int>(kCols) && ST <= kMaxStages && NS <= 2);
+    static_assert(!F32 || NQ == 1);
     extern __shared__ uint8_t raw[];
     uint8_t *smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
     uint8_t *kv_smem = smem + NQ * 2 * kHalfQ;
@@ -447,8 +459,8 @@ __global__ void __launch_bounds__(128 + 128 * NQ, NQ == 1 ? 2 : 1)
     tc_fence_after();
     const uint32_t tmem = c.tmem;
     const int total = c.total;
-    auto s_col = [&](int a, int buf) { return tmem + a * (NS * KT + 128) + buf * KT; };
-    auto o_col = [&](int a) { return tmem + a * (NS * KT + 128) + NS * KT; };
+    auto s_col = [&](int a, int buf) { return tmem + a * kQTile + buf * kSW; };
+    auto o_col = [&](int a) { return tmem + a * kQTile + NS * kSW; };
 
     // The n-th item of this CTA, for the roles other than the producer: what they do not use of it
     // is never read. False if the wait ran out.
@@ -498,6 +510,16 @@ __global__ void __launch_bounds__(128 + 128 * NQ, NQ == 1 ? 2 : 1)
                 for (int q = 0; q < 4; ++q) {
                     float *v = o[q & 1];
                     tmem_landed(v);
+                    if constexpr (F32) {
+                        if (it.t1 - it.t0 > kFlush) {
+                            float mm[32];
+                            tmem_ld32(o_col(a) + 128 + lane_addr + 32 * q, mm);
+                            tmem_landed(mm);
+#pragma unroll
+                            for (int x = 0; x < 32; ++x)
+                                v[x] += mm[x];
+                        }
+                    }
                     if (q < 3)
                         tmem_ld32(o_col(a) + lane_addr + 32 * q + 32, o[(q + 1) & 1]);
                     else
@@ -507,7 +529,7 @@ __global__ void __launch_bounds__(128 + 128 * NQ, NQ == 1 ? 2 : 1)
                         for (int x = 0; x < 32; ++x)
                             v[x] *= inv;
                         if (!SPLIT) {
-                            store_row<32, TWO>(p, my_row * kHeadDim + 32 * q, v);
+                            store_row<32, F32>(p, my_row * kHeadDim + 32 * q, v);
                         } else {
                             float *w = p.parts + (part * p.part_rows + rq) * kHeadDim + 32 * q;
 #pragma unroll
@@ -555,7 +577,7 @@ __global__ void __launch_bounds__(128 + 128 * NQ, NQ == 1 ? 2 : 1)
                     const int dpr = r >> p.group_log2;
                     const size_t o = static_cast<size_t>(it.row0 + dpr * (p.n_kv_heads * G) + (r & (G - 1))) *
                                          kHeadDim + d;
-                    if (TWO)
+                    if (F32)
                         static_cast<float *>(p.out)[o] = acc / den;
                     else
                         static_cast<__nv_bfloat16 *>(p.out)[o] = __float2bfloat16_rn(acc / den);
@@ -566,10 +588,11 @@ __global__ void __launch_bounds__(128 + 128 * NQ, NQ == 1 ? 2 : 1)
     };
 
     // Registers (launched with 168 a thread, or 128 with two CTAs per SM): the softmax keeps a
-    // score row, the other roles give up what they do not need. 384 * 168 = 256 * 208 + 128 * 88
-    // = 256 * 200 + 128 * 104; 256 * 128 = 128 * 192 + 128 * 64.
+    // score row, the other roles give up what they do not need. 384 * 168 = 256 * 208 + 128 * 88;
+    // 256 * 128 = 128 * 192 + 128 * 64. (With F32 everybody has enough.)
     if (warp >= 4) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(NQ == 1 ? 192 : TWO ? 200 : 208));
+        if constexpr (!F32)
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(NQ == 1 ? 192 : 208));
         // ------------------------------------------------------------------------ softmax
         const int a = (warp - 4) >> 2, quad = warp & 3, rowi = quad * 32 + lane;
         const uint32_t lane_addr = static_cast<uint32_t>(quad * 32) << 16;
@@ -651,30 +674,59 @@ __global__ void __launch_bounds__(128 + 128 * NQ, NQ == 1 ? 2 : 1)
                 }
                 const float mn = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
                 const bool grow = (mn - m) * sc > 8.f;      // (from -inf: always, unless still -inf)
-                if (__any_sync(0xffffffffu, grow) && t > it.t0) {
+                const int nth_tile = t - it.t0;
+                const bool flush = F32 && nth_tile > 0 && nth_tile % kFlush == 0;
+                if (flush || (__any_sync(0xffffffffu, grow) && nth_tile > 0)) {
+                    // O (and M) to the new maximum, O into M
                     const float alpha = grow ? ex2_approx((m - mn) * sc) : 1.f;
                     ok = warp_wait(&c.od[a][(done - 1) % NS], ((done - 1) / NS) & 1, &c.abort);
                     if (!ok)
                         break;
                     tc_fence_after();
                     l *= alpha;
+                    const bool has_m = F32 && nth_tile > kFlush;    // M holds something
+#pragma unroll(F32 ? 1 : 4)
+                    for (int q = 0; q < 4; ++q) {
+                        const uint32_t oa = o_col(a) + lane_addr + 32 * q;
+                        float o[32], mm[F32 ? 32 : 1];
+                        tmem_ld32(oa, o);
+                        if constexpr (F32) {
+                            if (has_m)
+                                tmem_ld32(oa + 128, mm);
+                            else
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {   // (rare: kept short of registers)
-                        float o[32];
-                        tmem_ld32(o_col(a) + lane_addr + 32 * q, o);
+                                for (int x = 0; x < 32; ++x)
+                                    mm[x] = 0.f;
+                            tmem_landed(mm);
+                        }
                         tmem_landed(o);
+                        if (flush) {
 #pragma unroll
-                        for (int x = 0; x < 32; ++x)
-                            o[x] *= alpha;
-                        tmem_st32(o_col(a) + lane_addr + 32 * q, reinterpret_cast<const uint32_t *>(o));
+                            for (int x = 0; x < 32; ++x)
+                                o[x] = (o[x] + mm[F32 ? x : 0]) * alpha;
+                            tmem_st32(oa + 128, reinterpret_cast<const uint32_t *>(o));
+                        } else {
+#pragma unroll
+                            for (int x = 0; x < 32; ++x)
+                                o[x] *= alpha;
+                            tmem_st32(oa, reinterpret_cast<const uint32_t *>(o));
+                            if constexpr (F32) {
+                                if (has_m) {
+#pragma unroll
+                                    for (int x = 0; x < 32; ++x)
+                                        mm[x] *= alpha;
+                                    tmem_st32(oa + 128, reinterpret_cast<const uint32_t *>(mm));
+                                }
+                            }
+                        }
                     }
                 }
                 m = grow ? mn : m;
                 const float off = m == -CUDART_INF_F ? 0.f : -m * sc;
                 const uint64_t sc2 = pack2(sc, sc), off2 = pack2(off, off);
                 uint64_t sum = 0;
-                // weights of chunk q over the first 16 columns of its scores, the remainders (TWO)
-                // over the other 16. (Stores of 16 columns: with 8 the 8K chunk under a window of 4096 took
+                // Weights of chunk q over the first 16 columns of its scores; with F32 their remainders
+                // over the other 16, and what those leave behind the scores. (Stores of 16 columns: with 8 the 8K chunk under a window of 4096 took
                 // 417 us, with 16 397, with 32 no less.)
 #pragma unroll
                 for (int q = 0; q < kC; ++q) {
@@ -684,11 +736,11 @@ __global__ void __launch_bounds__(128 + 128 * NQ, NQ == 1 ? 2 : 1)
                         if (!whole)
                             mask(v, q);
                     }
-                    uint32_t w[16], r[TWO ? 16 : 1];
+                    uint32_t w[16], r[F32 ? 16 : 1], r2[F32 ? 16 : 1];
                     if ((hidden >> q) & 1u) {
 #pragma unroll
                         for (int x = 0; x < 16; ++x)
-                            w[x] = r[TWO ? x : 0] = 0u;
+                            w[x] = r[F32 ? x : 0] = r2[F32 ? x : 0] = 0u;
                     } else {
 #pragma unroll
                         for (int x = 0; x < 16; ++x) {
@@ -697,10 +749,15 @@ __global__ void __launch_bounds__(128 + 128 * NQ, NQ == 1 ? 2 : 1)
                             sum = add2(sum, pack2(p0, p1));
                             const __nv_bfloat162 hi = __floats2bfloat162_rn(p0, p1);
                             w[x] = *reinterpret_cast<const uint32_t *>(&hi);
-                            if (TWO) {
+                            if (F32) {
+                                // (both differences are exact)
                                 const float2 b = __bfloat1622float2(hi);
-                                const __nv_bfloat162 lo = __floats2bfloat162_rn(p0 - b.x, p1 - b.y);
-                                r[TWO ? x : 0] = *reinterpret_cast<const uint32_t *>(&lo);
+                                const float d0 = p0 - b.x, d1 = p1 - b.y;
+                                const __nv_bfloat162 lo = __floats2bfloat162_rn(d0, d1);
+                                const float2 e = __bfloat1622float2(lo);
+                                const __nv_bfloat162 rest = __floats2bfloat162_rn(d0 - e.x, d1 - e.y);
+                                r[F32 ? x : 0] = *reinterpret_cast<const uint32_t *>(&lo);
+                                r2[F32 ? x : 0] = *reinterpret_cast<const uint32_t *>(&rest);
                             }
                         }
                     }
@@ -714,8 +771,10 @@ __global__ void __launch_bounds__(128 + 128 * NQ, NQ == 1 ? 2 : 1)
                             mbar_arrive(&c.pf[a][0]);
                     }
                     tmem_st16(sa + 32 * q, w);
-                    if (TWO)
+                    if (F32) {
                         tmem_st16(sa + 32 * q + 16, r);
+                        tmem_st16(sa + KT + 16 * q, r2);
+                    }
                     if (q + 2 < kC)
                         tmem_ld32(sa + 32 * q + 64, v);
                 }
@@ -736,7 +795,8 @@ __global__ void __launch_bounds__(128 + 128 * NQ, NQ == 1 ? 2 : 1)
         if (!ok && lane == 0)
             wfail(c, p.err);
     } else {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(NQ == 1 ? 64 : TWO ? 104 : 88));
+        if constexpr (!F32)
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(NQ == 1 ? 64 : 88));
         if (warp == 0) {
             // ------------------------------------------------------------------ TMA producer
             int use = 0, items = 0;
@@ -852,7 +912,7 @@ __global__ void __launch_bounds__(128 + 128 * NQ, NQ == 1 ? 2 : 1)
             // S of q tile A from the keys in stage st
             auto scores = [&](int A, uint32_t st, uint32_t buf) {
                 const uint64_t dq = dq0 + A * (2 * kHalfQ / 16), dk = dk0 + st * (kStage / 16);
-                const uint32_t d = tm + A * (NS * KT + 128) + buf * KT;
+                const uint32_t d = tm + A * kQTile + buf * kSW;
 #pragma unroll
                 for (int kk = 0; kk < 8; ++kk)
                     umma_bf16(d, dq + ((kk >> 2) * kHalfQ + (kk & 3) * 32) / 16,
@@ -861,13 +921,14 @@ __global__ void __launch_bounds__(128 + 128 * NQ, NQ == 1 ? 2 : 1)
             };
             auto products = [&](int A, uint32_t st, uint32_t buf, int half, bool first) {
                 const uint64_t dv = dv0 + st * (kStage / 16);
-                const uint32_t d = tm + A * (NS * KT + 128) + NS * KT, w = tm + A * (NS * KT + 128) + buf * KT;
+                const uint32_t d = tm + A * kQTile + NS * kSW, w = tm + A * kQTile + buf * kSW;
 #pragma unroll
-                for (int part = 0; part < (TWO ? 2 : 1); ++part)
+                for (int part = 0; part < (F32 ? 3 : 1); ++part)
 #pragma unroll
                     for (int k2 = 0; k2 < kBlocks / NH; ++k2) {
                         const int kk = half * (kBlocks / NH) + k2;
-                        umma_bf16_ta(d, w + (kk >> 1) * 32 + part * 16 + (kk & 1) * 8, dv + kk * 128,
+                        umma_bf16_ta(d, part == 2 ? w + KT + kk * 8 : w + (kk >> 1) * 32 + part * 16 + (kk & 1) * 8,
+                                     dv + kk * 128,
                                      idesc_o,
                                      kk > 0 || part > 0 ? 1u : first ? 0u : 1u);
                     }
@@ -917,7 +978,7 @@ __global__ void __launch_bounds__(128 + 128 * NQ, NQ == 1 ? 2 : 1)
                                 break;
                             tc_fence_after();
                             if (elect_one()) {
-                                products(A, st, buf, half, seq == begin);
+                                products(A, st, buf, half, F32 ? (seq - begin) % kFlush == 0 : seq == begin);
                                 if (A == NQ - 1 && half == NH - 1)
                                     umma_commit(&c.ve[st]);
                             }
@@ -1011,11 +1072,11 @@ __global__ void __launch_bounds__(128 + 128 * NQ, NQ == 1 ? 2 : 1)
     }
 }
 
-template <int NQ, int KT, int ST, int NS, int QR, bool TWO, bool SPLIT>
+template <int NQ, int KT, int ST, int NS, int QR, bool F32, bool SPLIT>
 cudaError_t launch_one(const WindowParams &p, const CUtensorMap &tm_k, const CUtensorMap &tm_v,
                        const CUtensorMap &tm_q, int grid, cudaStream_t stream)
 {
-    auto *kern = window_kernel<NQ, KT, ST, NS, QR, TWO, SPLIT>;
+    auto *kern = window_kernel<NQ, KT, ST, NS, QR, F32, SPLIT>;
     constexpr int smem = window_smem<NQ, KT, ST, QR>();
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e == cudaSuccess)
@@ -1023,15 +1084,12 @@ cudaError_t launch_one(const WindowParams &p, const CUtensorMap &tm_k, const CUt
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-template <int NQ, int KT, int ST, int NS, int QR>
+template <int NQ, int KT, int ST, int NS, int QR, bool F32>
 cudaError_t launch_form(const WindowParams &p, const CUtensorMap &tm_k, const CUtensorMap &tm_v,
                         const CUtensorMap &tm_q, int grid, cudaStream_t stream)
 {
-    if (p.n_split > 1)
-        return p.out_fp32 ? launch_one<NQ, KT, ST, NS, QR, true, true>(p, tm_k, tm_v, tm_q, grid, stream)
-                          : launch_one<NQ, KT, ST, NS, QR, false, true>(p, tm_k, tm_v, tm_q, grid, stream);
-    return p.out_fp32 ? launch_one<NQ, KT, ST, NS, QR, true, false>(p, tm_k, tm_v, tm_q, grid, stream)
-                      : launch_one<NQ, KT, ST, NS, QR, false, false>(p, tm_k, tm_v, tm_q, grid, stream);
+    return p.n_split > 1 ? launch_one<NQ, KT, ST, NS, QR, F32, true>(p, tm_k, tm_v, tm_q, grid, stream)
+                         : launch_one<NQ, KT, ST, NS, QR, F32, false>(p, tm_k, tm_v, tm_q, grid, stream);
 }
 
 }  // namespace
@@ -1040,11 +1098,13 @@ cudaError_t launch_window(const WindowParams &p, int rows, const CUtensorMap &tm
                           const CUtensorMap &tm_v, const CUtensorMap &tm_q, int grid,
                           cudaStream_t stream)
 {
-    if (rows == 256)
-        return launch_form<2, 128, 2, 1, 128>(p, tm_k, tm_v, tm_q, grid, stream);
+    if (rows == 256)        // (bf16 outputs only)
+        return launch_form<2, 128, 2, 1, 128, false>(p, tm_k, tm_v, tm_q, grid, stream);
     if (rows == 16)
-        return launch_form<1, 64, 3, 2, 16>(p, tm_k, tm_v, tm_q, grid, stream);
-    return launch_form<1, 64, 2, 2, 128>(p, tm_k, tm_v, tm_q, grid, stream);
+        return p.out_fp32 ? launch_form<1, 64, 4, 2, 16, true>(p, tm_k, tm_v, tm_q, grid, stream)
+                          : launch_form<1, 64, 3, 2, 16, false>(p, tm_k, tm_v, tm_q, grid, stream);
+    return p.out_fp32 ? launch_form<1, 64, 4, 2, 128, true>(p, tm_k, tm_v, tm_q, grid, stream)
+                      : launch_form<1, 64, 2, 2, 128, false>(p, tm_k, tm_v, tm_q, grid, stream);
 }
 
 }  // namespace sfi

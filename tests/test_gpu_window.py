@@ -146,6 +146,20 @@ def test_one_row_among_long_history():
         c.check(64, window)
 
 
+def test_fp32_sums_over_a_long_window():
+    """The tensor core's own sums do not round to nearest; over 8000 keys the fp32 outputs stay
+    within 2e-6 of the definition in the 2-norm (a single chain of such sums had 1e-5 there)."""
+    c = Case([9000, 8200], [3, 130], 8, 2, seed=2)
+    c.run(4, 8000)
+    c.check(4, 8000)
+    q, k, v = (t.double().cpu().numpy() for t in (c.q, c.flat_k, c.flat_v))
+    for b, (n, m) in enumerate(zip(c.lens, c.rows)):
+        r0, r1 = c.starts[b], c.starts[b + 1]
+        o, _ = window_attention(q[0, r0:r1], k[0, b, :, :n], v[0, b, :, :n], n, 4, 8000)
+        d = c.out[0, r0:r1].double().cpu().numpy() - o
+        assert np.linalg.norm(d) <= 2e-6 * np.linalg.norm(o)
+
+
 def test_layers_and_inactive_sequences():
     c = Case([500, 320, 640], [90, 320, 1], 8, 2, paged=True, layers=3)
     active = torch.tensor([1, 0, 1], dtype=torch.uint8, device="cuda")
