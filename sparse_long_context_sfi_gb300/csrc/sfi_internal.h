@@ -232,7 +232,7 @@ struct WindowParams {
     int part_rows;              // operand rows kept per item and split
     int *tickets;               // [items], zero between launches
     float *parts;               // [items][n_split][part_rows][128] unnormalised outputs
-    float2 *part_ml;            // [items][n_split][part_rows] maximum (scaled by nothing), sum
+    float2 *part_ml;            // [items][n_split][part_rows] maximum (of unscaled logits), sum
 };
 // rows: operand rows per item, 256 (two q tiles), 128 or 16 (two CTAs per SM).
 cudaError_t launch_window(const WindowParams &p, int rows, const CUtensorMap &tm_k,

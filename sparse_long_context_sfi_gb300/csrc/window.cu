@@ -4,25 +4,38 @@
 // A row at position i of query head h sees keys j <= i with j < n_sink or j > i - n_window:
 //     z_ij = q_i . k_j / sqrt(128),  o_i = sum_j exp(z_ij - m_i) v_j / sum_j exp(z_ij - m_i).
 //
-// An item is 128 * NQ operand rows of one (layer, sequence, kv head): 128 NQ / G positions of
-// all G query heads that share the head's keys, so one read of a K/V row serves the group.
-// The keys that any of its rows sees are a list of 16-position blocks (a cache page each):
-// the sink blocks, then the blocks of the joint window; a tile is KT / 16 consecutive entries
-// of the list, so few sinks share a tile with the window instead of costing one.
+// An item is 256, 128 or 16 operand rows of one (layer, sequence, kv head): its positions times
+// the G query heads that share the head's keys, so one read of a K/V row serves the group. The
+// keys that any of its rows sees are a list of 16-position blocks (a cache page each): the sink
+// blocks, then the blocks of the joint window; a tile is KT / 16 consecutive entries of the
+// list, so few sinks share a tile with the window instead of costing one.
 //
 // One CTA, roles by warp:
-//   0      TMA: the item's queries, then K and V of every tile (16-row boxes)
+//   0      works the items out for all roles; TMA: the item's queries, then K and V of every
+//          tile (16-row boxes)
 //   1      MMA: S = Q K^T and O += P V per q tile (M = 128), P read from tensor memory
 //   2      zeroes the V rows of a landed tile that no row of the item may see (a zero weight
 //          would not cancel a NaN)
-//   4-7    softmax of q tile 0, one row per thread; 8-11 of q tile 1
+//   4-7    softmax and output of q tile 0, one row per thread; 8-11 of q tile 1
 // Tensor memory: per q tile NS score buffers of KT columns, each overwritten by its weights,
 // and 128 columns of O. The running maximum is only moved (and O rescaled) when it grows by
-// more than 2^8, so that most tiles leave O alone; weights up to 2^8 are as exact in floating
-// point as weights up to 1.
+// more than 2^8, so that most tiles leave O alone (an 8K chunk: 491 us with every growth, 417
+// without); weights up to 2^8 are as exact in floating point as weights up to 1.
 //
 // Few rows and a long window: the tiles of an item are split over n_split items, whose
 // unnormalised outputs, maxima and sums the last one to finish joins, in split order.
+//
+// What bounds it (GB300, copy rate 6.78 TB/s, bf16 products 1.90 PFLOP/s measured):
+//   256 rows, 8K of 32K rows, window 4096: 397 us, 1.39 PFLOP/s. Per 128 keys the tensor core has
+//     2048 clocks of work for the two q tiles and the cycle takes ~3300: scores, softmax and
+//     products of one tile are a chain (tensor memory holds one score buffer per q tile beside
+//     two O), which the other q tile only partly fills. 64-key tiles with two buffers break
+//     the chain, but their products are smaller: 512 us.
+//   128 rows, 4 x 32K rows, window 64: 473 us, 5.7 TB/s of the 2.7 GB it has to move. The four
+//     softmax warps of each of an SM's two CTAs are busy throughout (two tiles, then the output).
+//   16 rows, 32 tokens, window 4096, pages: 88 us, 6.1 TB/s. HBM.
+// Registers that spill are the first thing to look at here: shared memory leaves next to no L1,
+// so a spill is a trip to L2 (a form that spilled took twice the time).
 #include "sfi_device.cuh"
 
 #include <math_constants.h>

@@ -3,8 +3,8 @@
 Tolerances, from the arithmetic: a weight's relative error is at most its logit's absolute
 error (fp32 sums of 128 bf16 products and one fp32 scaling, logits below 64 here: under
 2^-16) plus the exponential's 2^-22, twice for the normalisation: under 1e-4 / 2 in all with
-the output's fp32 sum. A bf16 weight adds half a step, 2^-8; bf16 part and remainder add
-2^-16. So an output is off by at most (1e-4 + [bf16: 2^-8]) * sum_j w_j |v_j|, and a bf16
+the output's fp32 sum. A bf16 weight adds half a step, 2^-8; one in three bf16 parts (fp32 outputs)
+adds 2^-24. So an output is off by at most (1e-4 + [bf16: 2^-8]) * sum_j w_j |v_j|, and a bf16
 output by 2^-8 |o| more."""
 import numpy as np
 import pytest
