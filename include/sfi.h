@@ -415,7 +415,8 @@ size_t sfi_pages_workspace_bytes(const sfi_kv_cache *kv);
  * last keeps it if nobody else holds it). seq_len is not changed.
  * A sequence that does not fit its capacity (SFI_DEVERR_CAPACITY), whose current page is
  * missing (SFI_DEVERR_PAGE_RANGE), or that the free pages do not cover, counted in order of
- * sequence (SFI_DEVERR_POOL, it and every later one that needs a page), is left as it was.
+ * sequence (SFI_DEVERR_POOL, it and every later one that needs a page or that page to itself),
+ * is left as it was.
  *   ok  optional device uint8 [batch]: 1 for the active sequences whose positions are
  *       writable, else 0; may be given as `active` to the calls that write them.
  */
@@ -441,7 +442,8 @@ sfi_status sfi_pages_evict(const sfi_kv_cache *kv, const sfi_page_pool *pool, in
  * Move the pages in use to the front of the pool: with U pages in use, the i-th used page
  * with id >= U (ascending) moves to the i-th free id below U, in every layer, and table and
  * refs follow, so that pages [U, n_pages) are free and the pool can be cut to any n_pages >=
- * U. n_used: device int32, receives U. The contents of pages left behind are not cleared.
+ * U. n_used: device int32, receives U. The contents of pages left behind are not cleared. A
+ * table entry whose page counts as free (SFI_DEVERR_REFS) stays as it is.
  */
 sfi_status sfi_pages_compact(const sfi_kv_cache *kv, const sfi_page_pool *pool, int32_t *n_used,
                              void *ws, size_t ws_bytes, void *stream);
@@ -482,7 +484,7 @@ sfi_status sfi_append_chunk(const sfi_kv_cache *kv, const void *k_new, const voi
  * n_window >= 1. A sequence longer than max_len, or with more rows than its length, is skipped
  * (SFI_DEVERR_LENGTH).
  *   ws   workspace of at least sfi_window_workspace_bytes(), 256-byte aligned and initialised
- *        (sfi_workspace_init, once); calls sharing it must not overlap.
+ *        (sfi_workspace_init, once); calls of any shape may share it, but must not overlap.
  */
 sfi_status sfi_window_attn(const sfi_kv_cache *kv, const void *q, void *out, int32_t out_fp32,
                            const int32_t *row_start, int32_t n_rows, int32_t max_rows,
@@ -520,7 +522,8 @@ sfi_status sfi_reorder(const sfi_kv_cache *kv, const sfi_page_pool *pool,
  *   parent, token  int32 [rows]: the kept candidates, best first; parent as a row, ready to be
  *               sfi_reorder's src
  *   cum_out     fp32 [rows]: their scores s; done_out: uint8 [rows] or NULL: done[parent], or
- *               token == eos. Outputs must not overlap the inputs.
+ *               token == eos. cum_out may be cum and done_out may be done; otherwise outputs
+ *               do not overlap inputs.
  * eos < 0: no token ends a beam (done must be NULL then). 1 <= n_beams <= 16, else
  * SFI_ERR_UNSUPPORTED; n_groups * n_beams <= 65535; vocab <= 2^30 / n_beams.
  */
@@ -540,7 +543,7 @@ typedef struct sfi_beam {
 } sfi_beam;
 
 /* Workspace of sfi_beam_select (256-byte aligned, initialised once with sfi_workspace_init;
- * calls sharing it must not overlap). 0 on invalid arguments. */
+ * calls of any shape may share it, but must not overlap). 0 on invalid arguments. */
 size_t sfi_beam_workspace_bytes(const sfi_beam *beam);
 sfi_status sfi_beam_select(const sfi_beam *beam, void *ws, size_t ws_bytes, void *stream);
 

@@ -120,23 +120,27 @@ int window_rows(const sfi_kv_cache *kv, int max_rows, int n_window, bool fp32)
     return all <= 16 ? 16 : all > 128 && reach >= 512 && !fp32 ? 256 : 128;
 }
 
-// Sized for any item size and split, so that it holds for every max_len and window.
+// Sized for any item size and split, so that it holds for every max_len and window. The tickets
+// come first and their room does not depend on the call, so that calls of other shapes on the
+// same workspace find them as this one leaves them, zero: items are split only if at least two
+// CTAs are left for each, and the bound of their number is at most twice the likely one, so no
+// more are split than CTAs fit, two to an SM.
 size_t window_scratch(const sfi_kv_cache *kv, int n_rows, int max_rows, char *base, WindowParams *p)
 {
-    size_t o = 0, items = 1, parts = 1;
+    size_t o = 0, parts = 1;
     for (int rows : {16, 128, 256}) {
         const WindowShape s = window_shape(kv, n_rows, max_rows, rows, false);
-        const size_t n = s.most_split > 1 ? static_cast<size_t>(s.items) : 1;
-        const size_t m = s.most_split > 1 ? n * s.most_split * s.part_rows : 1;
-        items = n > items ? n : items;
+        const size_t m = s.most_split > 1 ? static_cast<size_t>(s.items) * s.most_split * s.part_rows : 1;
         parts = m > parts ? m : parts;
     }
+    const int sms = sm_count();
+    const size_t tickets = 2 * static_cast<size_t>(sms > 0 ? sms : 1);
     auto take = [&](size_t bytes) {
         char *at = base + o;
         o = align256(o + bytes);
         return static_cast<void *>(at);
     };
-    p->tickets = static_cast<int *>(take(items * sizeof(int)));
+    p->tickets = static_cast<int *>(take(tickets * sizeof(int)));
     p->part_ml = static_cast<float2 *>(take(parts * sizeof(float2)));
     p->parts = static_cast<float *>(take(parts * kHeadDim * sizeof(float)));
     return o;
@@ -174,7 +178,8 @@ size_t beam_scratch(const sfi_beam *b, char *base, BeamParams *p)
         return static_cast<void *>(at);
     };
     p->splits = beam_splits(b);
-    p->tickets = static_cast<int *>(take(b->n_groups * sizeof(int)));
+    // (room for the most groups, so that calls of other shapes leave the tickets zero)
+    p->tickets = static_cast<int *>(take(65536 * sizeof(int)));
     p->part_stat = static_cast<float2 *>(take(rows * p->splits * sizeof(float2)));
     p->part_x = static_cast<float *>(take(rows * p->splits * b->n_beams * sizeof(float)));
     p->part_v = static_cast<int32_t *>(take(rows * p->splits * b->n_beams * sizeof(int32_t)));

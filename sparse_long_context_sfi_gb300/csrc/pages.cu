@@ -105,6 +105,7 @@ __global__ void __launch_bounds__(kPlanThreads) reserve_kernel(const PageParams 
                                                                const PageScratch s)
 {
     __shared__ int first[kMaxBatch], last[kMaxBatch], task0[kMaxBatch + 1];
+    __shared__ int lean[kMaxBatch];         // the last sequence that has to leave a page for this one
     __shared__ int8_t state[kMaxBatch];     // 0: to be served, -1: refused or not active
     __shared__ uint8_t tail[kMaxBatch];     // rows in the current page
     __shared__ uint32_t sh_marks[kTasksInSmem];
@@ -135,6 +136,7 @@ __global__ void __launch_bounds__(kPlanThreads) reserve_kernel(const PageParams 
         }
         first[b] = f;
         last[b] = l;
+        lean[b] = -1;
         tail[b] = static_cast<uint8_t>(L & 15);
         state[b] = static_cast<int8_t>(st);
         s.copies[b] = make_int4(0, 0, 0, 0);    // page to, page from, rows
@@ -192,16 +194,25 @@ __global__ void __launch_bounds__(kPlanThreads) reserve_kernel(const PageParams 
             if (in && e[q] >= p.n_pages)
                 raise_error(p.err, 0x1u);
             // shared pages (as a rule one per sequence, its current page): the warp counts the
-            // earlier sequences that reserve on the same page
+            // earlier sequences that reserve on the same page (and whose current page is there)
             for (uint32_t sm = __ballot_sync(kFull, holders[q] > 1); sm != 0; sm &= sm - 1) {
                 const int src = __ffs(sm) - 1, page = __shfl_sync(kFull, e[q], src), col = c0[q] + src;
-                int before = 0;
-                for (int o = lane; o < b[q]; o += 32)
-                    before += (col >= first[o] && col <= last[o] &&
-                               p.table[static_cast<size_t>(o) * p.max_pages + col] == page);
+                int before = 0, leaver = -1;
+                for (int o = lane; o < b[q]; o += 32) {
+                    const int32_t *row = p.table + static_cast<size_t>(o) * p.max_pages;
+                    if (col >= first[o] && col <= last[o] && row[col] == page &&
+                        (col == first[o] || !tail[o] || (row[first[o]] >= 0 && row[first[o]] < p.n_pages))) {
+                        ++before;
+                        leaver = o;
+                    }
+                }
                 before = __reduce_add_sync(kFull, before);
-                if (lane == src)
+                leaver = __reduce_max_sync(kFull, leaver);
+                if (lane == src) {
                     want = holders[q] - before > 1;
+                    if (!want)
+                        atomicMax(lean + b[q], leaver);
+                }
             }
             const uint32_t m = __ballot_sync(kFull, want);
             if (lane == 0) {
@@ -284,7 +295,10 @@ __global__ void __launch_bounds__(kPlanThreads) reserve_kernel(const PageParams 
     }
     if (tid < p.batch) {
         const int upto = count[task0[tid + 1]];
-        const bool fits = upto == count[task0[tid]] || upto <= found;
+        // (a page that this sequence keeps because the others leave it: pages run out in order, so
+        // that if the last of them is served all are)
+        const bool fits = (upto == count[task0[tid]] || upto <= found) &&
+                          (lean[tid] < 0 || count[task0[lean[tid] + 1]] <= found);
         if (!fits)
             raise_error(p.err, 0x10u);  // SFI_DEVERR_POOL
         if (ok)
@@ -402,8 +416,14 @@ __global__ void __launch_bounds__(256) compact_move_kernel(const PageParams p, c
         const int e = p.table[i];
         if (e >= p.n_pages)
             raise_error(p.err, 0x1u);
-        else if (e >= U)
-            p.table[i] = s.list[s.rank[e]];
+        else if (e >= U) {
+            // (an entry whose page counts as free has no rank)
+            const int r = s.rank[e];
+            if (r >= 0 && r < moves && s.movers[r] == e)
+                p.table[i] = s.list[r];
+            else
+                raise_error(p.err, 0x80u);  // SFI_DEVERR_REFS
+        }
     }
     const int lane = threadIdx.x & 31;
     const long long pieces = static_cast<long long>(moves) * n_layers * 2 * p.n_kv_heads;
@@ -650,14 +670,14 @@ __global__ void __launch_bounds__(256) reorder_rows_kernel(const ReorderParams p
     const long long stride = static_cast<long long>(p.n_kv_heads) * rows_per_head * 16;
     uint4 *t = (blockIdx.z ? v : k) + static_cast<long long>(layer) * p.batch * stride +
                static_cast<long long>(head) * rows_per_head * 16;
-    const int col = (static_cast<int>(blockIdx.x) << cols_log2) + (threadIdx.x & ((1 << cols_log2) - 1));
+    const uint32_t col = (blockIdx.x << cols_log2) + (threadIdx.x & ((1u << cols_log2) - 1u));
     const int m0 = threadIdx.x >> cols_log2, step = 256 >> cols_log2;
     uint4 x[kPieces];
     uint32_t live = 0;
 #pragma unroll
     for (int q = 0; q < kPieces; ++q) {
         const int i = m0 + q * step;
-        if (i < n && (col >> 4) < min(have[i], rows_per_head)) {
+        if (i < n && static_cast<int>(col >> 4) < min(have[i], rows_per_head)) {
             live |= 1u << q;
             x[q] = t[mv[i].y * stride + col];
         }

@@ -21,6 +21,14 @@ from . import (SfiBeam, SfiBudget, SfiDecodePlan, SfiKvCache, SfiPagePool, SfiSp
                sfi_workspace_bytes, sfi_workspace_init)
 
 
+def _torch_stream(stream):
+    """The torch stream behind a `stream` argument (None: the current one). Tensors made for a call
+    are allocated on the stream that uses them, so that their memory is reused in its order."""
+    if stream is None:
+        return torch.cuda.current_stream()
+    return torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream
+
+
 class SfiState:
     def __init__(self, cfg, len0, device="cuda", page_table=None, n_pages=0, capacity=None):
         self.cfg = cfg
@@ -193,18 +201,20 @@ class SfiState:
         sfi_decode_run(self.kv, self.budget, self.mem, plan, self.ws, self.ws_bytes, stream=stream)
 
     # -- prompts, pages and beams ------------------------------------------------------------
-    def pool(self) -> SfiPagePool:
+    def pool(self, stream=None) -> SfiPagePool:
         """The page pool behind the table (made on first use: every entry the table holds then
         counts as one reference)."""
         if getattr(self, "_pool", None) is None:
             if self.page_table is None:
                 raise ValueError("a contiguous cache has no pages")
-            held = self.page_table[self.page_table >= 0]
-            self.page_refs = torch.bincount(held.long(), minlength=self.n_pages).to(torch.int32)
-            self._pool = SfiPagePool(page_table=self.page_table.data_ptr(),
-                                     refs=self.page_refs.data_ptr())
-            self._pages_bytes = sfi_pages_workspace_bytes(self.kv)
-            self._pages_ws = torch.empty(self._pages_bytes, dtype=torch.uint8, device=self.device)
+            with torch.cuda.stream(_torch_stream(stream)):
+                held = self.page_table[self.page_table >= 0]
+                self.page_refs = torch.bincount(held.long(), minlength=self.n_pages).to(torch.int32)
+                self._pool = SfiPagePool(page_table=self.page_table.data_ptr(),
+                                         refs=self.page_refs.data_ptr())
+                self._pages_bytes = sfi_pages_workspace_bytes(self.kv)
+                self._pages_ws = torch.empty(self._pages_bytes, dtype=torch.uint8, device=self.device)
+                self._pages_ok = torch.empty(self.cfg.batch, dtype=torch.uint8, device=self.device)
         return self._pool
 
     def _bound(self):
@@ -213,24 +223,30 @@ class SfiState:
         return self.kv
 
     def reserve(self, n_new=None, active=None, ok=None, stream=None):
-        """Pages for the next n_new[b] positions (device int32 [B]; None: one each)."""
-        pool = self.pool()
+        """Pages for the next n_new[b] positions (device int32 [B]; None: one each). Returns `ok`
+        (device uint8 [B], its own unless given): 1 for the active sequences that may write
+        them, to be given as `active` to the calls that do."""
+        pool = self.pool(stream)
+        ok = self._pages_ok if ok is None else ok
         sfi_pages_reserve(self._bound(), pool, n_new, self._pages_ws, self._pages_bytes,
                           active=active, ok=ok, stream=stream)
+        return ok
 
     def evict(self, n_window=None, active=None, stream=None):
         """Give up the pages outside the sinks and the recent window."""
-        sfi_pages_evict(self._bound(), self.pool(), self.cfg.n_sink,
+        sfi_pages_evict(self._bound(), self.pool(stream), self.cfg.n_sink,
                         self.cfg.n_window if n_window is None else n_window, active=active,
                         stream=stream)
 
     def release(self, active=None, stream=None):
         """Give up all pages of the active sequences; their lengths become 0."""
-        sfi_pages_release(self._bound(), self.pool(), active=active, stream=stream)
+        sfi_pages_release(self._bound(), self.pool(stream), active=active, stream=stream)
 
     def compact_pages(self, stream=None):
         """Move the pages in use to the front of the pool; returns their number (device int32)."""
-        pool, used = self.pool(), torch.empty(1, dtype=torch.int32, device=self.device)
+        pool = self.pool(stream)
+        with torch.cuda.stream(_torch_stream(stream)):
+            used = torch.empty(1, dtype=torch.int32, device=self.device)
         sfi_pages_compact(self._bound(), pool, used, self._pages_ws, self._pages_bytes, stream=stream)
         return used
 
@@ -238,19 +254,22 @@ class SfiState:
         """One chunk of a prompt: rows[b] (host) new tokens of every sequence, packed in order of
         sequence. Reserves their pages (paged cache), appends k_new/v_new [Ly][n][Hkv][D] and
         attends q [Ly][n][Hq][D] under the sinks and a window of n_window (default: the
-        budget's) into out [Ly][n][Hq][D]."""
+        budget's) into out [Ly][n][Hq][D]. A sequence whose pages the pool does not cover is
+        left out (its rows of out, too), and the error word says so."""
         rows = np.asarray(rows, dtype=np.int32)
         start = np.concatenate([[0], np.cumsum(rows)]).astype(np.int32)
         n, most = int(q.shape[1]), int(rows.max())
         if n < start[-1] or tuple(out.shape) != tuple(q.shape):
             raise ValueError("q and out hold the rows of every sequence")
         window = self.cfg.n_window if n_window is None else n_window
-        dev = torch.from_numpy(start).to(self.device)
-        if self.page_table is not None:
-            self.reserve(torch.from_numpy(rows).to(self.device), stream=stream)
-        sfi_append_chunk(self._bound(), k_new, v_new, dev, n, most, stream=stream)
+        active = None
+        with torch.cuda.stream(_torch_stream(stream)):
+            dev = torch.from_numpy(start).to(self.device)
+            if self.page_table is not None:
+                active = self.reserve(torch.from_numpy(rows).to(self.device), stream=stream)
+        sfi_append_chunk(self._bound(), k_new, v_new, dev, n, most, active=active, stream=stream)
         self.len0 = self.len0 + rows
-        self._window(q, out, out_fp32, dev, n, most, window, stream)
+        self._window(q, out, out_fp32, dev, n, most, window, stream, active)
 
     def window_step(self, q, k_new, v_new, out, out_fp32=True, n_window=None, active=None,
                     stream=None):
@@ -258,7 +277,7 @@ class SfiState:
         packed memory): q/out [Ly][B][Hq][D], k_new/v_new [Ly][B][Hkv][D]."""
         window = self.cfg.n_window if n_window is None else n_window
         if self.page_table is not None:
-            self.reserve(active=active, stream=stream)
+            active = self.reserve(active=active, stream=stream)
         sfi_append_chunk(self._bound(), k_new, v_new, None, self.cfg.batch, 1, active=active,
                          stream=stream)
         self.t += 1
@@ -268,7 +287,8 @@ class SfiState:
         kv = self._bound()
         need = sfi_window_workspace_bytes(kv, n, most, self.cfg.n_sink, window)
         if getattr(self, "_window_ws", None) is None or self._window_ws.numel() < need:
-            self._window_ws = torch.empty(need, dtype=torch.uint8, device=self.device)
+            with torch.cuda.stream(_torch_stream(stream)):
+                self._window_ws = torch.empty(need, dtype=torch.uint8, device=self.device)
             sfi_workspace_init(self._window_ws, need, stream=stream)
         sfi_window_attn(kv, q, out, out_fp32, start, n, most, self.cfg.n_sink, window,
                         self._window_ws, self._window_ws.numel(), active=active, stream=stream)
@@ -276,7 +296,7 @@ class SfiState:
     def reorder(self, src, stream=None):
         """Every sequence b takes over the state of sequence src[b] (device int32 [B]): table,
         length, packed memory. Forked sequences share their pages until they are reserved."""
-        pool = self.pool() if self.page_table is not None else None
+        pool = self.pool(stream) if self.page_table is not None else None
         sfi_reorder(self._bound(), src, pool=pool, budget=self.budget, mem=self.mem, stream=stream)
         self.len0 = np.full_like(self.len0, self.len0.max())   # a bound; src stays on the device
 
@@ -294,30 +314,28 @@ class BeamSearch:
         self.done = torch.zeros(rows, dtype=torch.uint8, **dev)
         self.parent = torch.zeros(rows, dtype=torch.int32, **dev)
         self.token = torch.zeros(rows, dtype=torch.int32, **dev)
-        self._next = torch.empty_like(self.cum), torch.empty_like(self.done)
         self._ws = None
 
     def select(self, logits, rank_scale=None, stream=None):
         """logits [rows][vocab] (bf16 or fp32, rows may be strided): keeps the best beams; returns
-        (parent, token), cum and done are updated."""
+        (parent, token); cum and done are updated in place, so that a captured selection can
+        be replayed."""
         if logits.shape != (self.n_groups * self.n_beams, self.vocab) or logits.stride(1) != 1:
             raise ValueError("logits are [rows][vocab] with contiguous rows")
         if logits.dtype not in (torch.bfloat16, torch.float32):
             raise ValueError("logits are bf16 or fp32")
-        cum, done = self._next
         beam = SfiBeam(
             n_groups=self.n_groups, n_beams=self.n_beams, vocab=self.vocab,
             logits_fp32=1 if logits.dtype == torch.float32 else 0, row_stride=logits.stride(0),
             eos=self.eos, logits=logits.data_ptr(), cum=self.cum.data_ptr(),
             done=self.done.data_ptr() if self.eos >= 0 else None,
             rank_scale=None if rank_scale is None else rank_scale.data_ptr(),
-            parent=self.parent.data_ptr(), token=self.token.data_ptr(), cum_out=cum.data_ptr(),
-            done_out=done.data_ptr())
-        if self._ws is None:
-            self._ws = torch.empty(sfi_beam_workspace_bytes(beam), dtype=torch.uint8,
-                                   device=self.cum.device)
+            parent=self.parent.data_ptr(), token=self.token.data_ptr(),
+            cum_out=self.cum.data_ptr(), done_out=self.done.data_ptr())
+        need = sfi_beam_workspace_bytes(beam)
+        if self._ws is None or self._ws.numel() < need:
+            with torch.cuda.stream(_torch_stream(stream)):
+                self._ws = torch.empty(need, dtype=torch.uint8, device=self.cum.device)
             sfi_workspace_init(self._ws, self._ws.numel(), stream=stream)
         sfi_beam_select(beam, self._ws, self._ws.numel(), stream=stream)
-        self._next = self.cum, self.done
-        self.cum, self.done = cum, done
         return self.parent, self.token

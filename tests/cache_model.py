@@ -32,18 +32,21 @@ class PoolModel:
                 self.err |= 0x1
                 continue
             spans[b] = range(length // PAGE, (length + n - 1) // PAGE + 1)
+        leans = {}                      # the last sequence that leaves a page to this one
         for b in spans:
             wants[b] = []
             for c in spans[b]:
                 e = self.table[b, c]
-                before = sum(1 for o in spans if o < b and c in spans[o] and self.table[o, c] == e)
-                if e < 0 or (self.refs[e] > 1 and self.refs[e] - before > 1):
+                before = [o for o in spans if o < b and c in spans[o] and self.table[o, c] == e]
+                if e < 0 or (self.refs[e] > 1 and self.refs[e] - len(before) > 1):
                     wants[b].append(c)
+                elif before and self.refs[e] > 1:
+                    leans.setdefault(b, set()).update(before)
         free = [int(i) for i in np.flatnonzero(self.refs == 0)]
         used = 0
         for b in spans:
             used += len(wants[b])
-            if wants[b] and used > len(free):
+            if (wants[b] and used > len(free)) or any(not ok[o] for o in leans.get(b, ())):
                 self.err |= 0x10
                 continue
             ok[b] = 1

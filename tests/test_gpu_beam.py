@@ -162,6 +162,36 @@ def test_sorted_logits():
         check(o, x, cum, beams)
 
 
+def test_selections_of_other_shapes_share_a_workspace():
+    ws = torch.empty(4 << 20, dtype=torch.uint8, device="cuda")
+    sfi.sfi_workspace_init(ws, ws.numel())
+    g = torch.Generator(device="cuda").manual_seed(6)
+    for groups, beams, vocab in ((1, 4, 40000), (64, 4, 9001), (3, 16, 128001), (200, 2, 700), (1, 4, 40000)):
+        x = torch.randn((groups * beams, vocab), generator=g, device="cuda")
+        cum = -torch.rand(groups * beams, generator=g, device="cuda")
+        check(run(x, cum, beams, ws=ws), x, cum, beams)
+
+
+def test_scores_in_place():
+    """cum_out = cum and done_out = done."""
+    g = torch.Generator(device="cuda").manual_seed(9)
+    x = torch.randn((12, 60001), generator=g, device="cuda") * 2
+    cum = -torch.rand(12, generator=g, device="cuda")
+    done = torch.zeros(12, dtype=torch.uint8, device="cuda")
+    done[[1, 6, 7]] = 1
+    want = run(x, cum, 4, done)
+    parent, token = (torch.zeros(12, dtype=torch.int32, device="cuda") for _ in "pt")
+    beam = sfi.SfiBeam(n_groups=3, n_beams=4, vocab=60001, logits_fp32=1, row_stride=60001, eos=2,
+                       logits=x.data_ptr(), cum=cum.data_ptr(), done=done.data_ptr(),
+                       rank_scale=None, parent=parent.data_ptr(), token=token.data_ptr(),
+                       cum_out=cum.data_ptr(), done_out=done.data_ptr())
+    ws = want["keep"][1]
+    sfi.sfi_beam_select(beam, ws, ws.numel())
+    torch.cuda.synchronize()
+    assert torch.equal(parent, want["parent"]) and torch.equal(token, want["token"])
+    assert torch.equal(cum, want["cum"]) and torch.equal(done, want["done"])
+
+
 def test_repeatable_and_captured():
     g = torch.Generator(device="cuda").manual_seed(5)
     x = torch.randn((16, 40000), generator=g, device="cuda")

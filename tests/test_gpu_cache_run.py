@@ -181,6 +181,66 @@ def test_two_states_at_once():
     assert torch.equal(outs[0], outs[1])     # the same seeds: the same bits
 
 
+def test_exhausted_pool_leaves_the_others_alone():
+    """Three beams on one page and no page to copy to: the step leaves them as they are and serves
+    the sequence that needs none."""
+    lp = Loop(True)
+    st = lp.st
+    lp.prefill([60, 0, 0, 1200 // 8, 0, 0], 64)
+    lp.reorder(torch.tensor([0, 0, 0, 3, 4, 5], dtype=torch.int32, device="cuda"))
+    st.page_refs[st.page_refs == 0] = 7                 # (nothing is free)
+    before = st.k.clone()
+    q, k, v = lp.rnd(2, 6, 8, D), lp.rnd(2, 6, 2, D), lp.rnd(2, 6, 2, D)
+    out = torch.full((2, 6, 8, D), -7.0, device="cuda")
+    st.window_step(q, k, v, out, n_window=64)
+    torch.cuda.synchronize()
+    assert int(st.err[0]) == sfi.SFI_DEVERR_POOL
+    assert st.seq_len.tolist() == [60, 60, 60, 151, 0, 0]
+    page = int(st.page_table[3, 150 // 16])
+    assert torch.equal(st.k[:, page, :, 150 % 16], k[:, 3])
+    before[:, page, :, 150 % 16] = k[:, 3]
+    assert torch.equal(st.k, before)
+    assert (out[:, [0, 1, 2, 4, 5]] == -7.0).all() and (out[:, 3] != -7.0).all()
+
+
+def test_captured_beam_step():
+    """A captured step (select, reorder, reserve) replayed: the same beams as eager steps."""
+    def setup():
+        lp, beam = Loop(True), BeamSearch(2, 3, 500, eos=7)
+        lp.prefill([60, 0, 0, 33, 0, 0], 64)
+        lp.reorder(torch.tensor([0, 0, 0, 3, 3, 3], dtype=torch.int32, device="cuda"))
+        return lp, beam
+
+    def step(lp, beam, logits, out, q, kv):
+        parent, token = beam.select(logits)
+        lp.st.reorder(parent)
+        lp.st.window_step(q, kv, kv, out, n_window=64)
+
+    g = torch.Generator(device="cuda").manual_seed(1)
+    many = torch.randn((5, 6, 500), generator=g, device="cuda") * 2
+    q = torch.randn((2, 6, 8, D), generator=g, device="cuda").to(torch.bfloat16)
+    kv = torch.randn((2, 6, 2, D), generator=g, device="cuda").to(torch.bfloat16)
+    outs = []
+    for captured in (False, True):
+        lp, beam = setup()
+        out, logits = torch.zeros((2, 6, 8, D), device="cuda"), many[0].clone()
+        step(lp, beam, logits, out, q, kv)              # (workspaces are made here)
+        if captured:
+            torch.cuda.synchronize()
+            lp.st.len0 = lp.st.len0 + 8                 # a bound for the steps to come
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph):
+                step(lp, beam, logits, out, q, kv)
+        for t in range(1, 5):
+            logits.copy_(many[t])
+            graph.replay() if captured else step(lp, beam, logits, out, q, kv)
+        torch.cuda.synchronize()
+        assert int(lp.st.err[0]) == 0
+        outs.append((out, beam.parent, beam.token, beam.cum, beam.done, lp.st.seq_len, lp.st.page_table))
+    for a, b in zip(*outs):
+        assert torch.equal(a, b)
+
+
 def test_engine_refuses():
     lp = Loop(False)
     with pytest.raises(ValueError):

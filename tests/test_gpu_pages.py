@@ -83,6 +83,10 @@ class Pool:
         sfi.sfi_reorder(self.kv, torch.tensor(src, dtype=torch.int32, device="cuda"), pool=self.pool)
         self.model.reorder(np.array(src))
 
+    def release(self, mask):
+        sfi.sfi_pages_release(self.kv, self.pool, active=self.mask(mask))
+        self.model.release(mask)
+
     def compact(self):
         n = torch.full((1,), -1, dtype=torch.int32, device="cuda")
         sfi.sfi_pages_compact(self.kv, self.pool, n, self.ws, self.nb)
@@ -143,6 +147,24 @@ def test_pool_exhausted_and_capacity():
     p.check()
 
 
+def test_last_holder_of_a_page_when_the_others_are_refused():
+    """With no page left to copy to, the first holders stay on the shared page, so the last one
+    may not write there either; a sequence that needs nothing is served all the same."""
+    p = Pool(4, 4, 4)
+    p.reserve([20, 0, 0, 17])
+    p.append([20, 0, 0, 17])
+    p.reorder([0, 0, 0, 3])
+    ok = p.reserve()
+    assert p.model.err == sfi.SFI_DEVERR_POOL and ok.tolist() == [0, 0, 0, 1]
+    p.check()
+    p.release([0, 0, 0, 1])
+    ok = p.reserve(mask=[1, 1, 1, 0])   # two pages: both copies, and the last keeps the page
+    assert ok.tolist() == [1, 1, 1, 0]
+    p.check()
+    p.append([1, 1, 1, 0])
+    p.check()
+
+
 def test_release_and_evict():
     p = Pool(5, 30, 200)
     p.reserve([400, 100, 480, 33, 0])
@@ -170,6 +192,18 @@ def test_counts_that_disagree_are_reported():
     torch.cuda.synchronize()
     assert int(p.err[0]) == sfi.SFI_DEVERR_REFS | sfi.SFI_DEVERR_PAGE_RANGE
     assert (p.refs == 0).all() and (p.table == -1).all()
+
+
+def test_compact_reports_entries_of_free_pages():
+    """An entry whose page counts as free is reported and stays; the others follow their pages."""
+    p = Pool(2, 6, 40)
+    p.table[0, :3] = torch.tensor([30, 39, 12], dtype=torch.int32)
+    p.refs[30] = p.refs[12] = 1                      # 39 is held by the table alone
+    n = torch.zeros(1, dtype=torch.int32, device="cuda")
+    sfi.sfi_pages_compact(p.kv, p.pool, n, p.ws, p.nb)
+    torch.cuda.synchronize()
+    assert int(n[0]) == 2 and int(p.err[0]) == sfi.SFI_DEVERR_REFS
+    assert p.table[0, :3].tolist() == [1, 39, 0] and p.refs.sum() == 2
 
 
 @pytest.mark.parametrize("layers,hkv", [(1, 2), (3, 1)])

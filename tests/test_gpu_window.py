@@ -273,6 +273,19 @@ def test_cache_beyond_32_bit_offsets():
     torch.cuda.empty_cache()
 
 
+def test_calls_of_other_shapes_share_a_workspace():
+    """Split items of a small call, then of a larger one whose tickets reach further, and back."""
+    small = Case([4000], [1], tail=0)
+    large = Case([4000] * 16, [1] * 16, hkv=8, hq=16, tail=0, seed=1)
+    chunk = Case([3000, 2000], [9, 40], seed=2)
+    nb = max(sfi.sfi_window_workspace_bytes(c.kv, c.total, max(c.rows), 4, 4096) for c in (small, large, chunk))
+    ws = torch.empty(nb, dtype=torch.uint8, device="cuda")
+    sfi.sfi_workspace_init(ws, nb)
+    for c in (small, chunk, large, small, large, chunk):
+        c.run(4, 4096, ws=ws)
+        c.check(4, 4096)
+
+
 def test_repeatable_and_captured():
     """The same call gives the same bits: again, on another stream, and replayed from a graph
     whose inputs changed in place; and the workspace is ready for the next call."""
