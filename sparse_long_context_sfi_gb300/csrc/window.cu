@@ -26,13 +26,16 @@
 // unnormalised outputs, maxima and sums the last one to finish joins, in split order.
 //
 // What bounds it (GB300, copy rate 6.78 TB/s, bf16 products 1.90 PFLOP/s measured):
-//   256 rows, 8K of 32K rows, window 4096: 397 us, 1.39 PFLOP/s. Per 128 keys the tensor core has
-//     2048 clocks of work for the two q tiles and the cycle takes ~3300: scores, softmax and
-//     products of one tile are a chain (tensor memory holds one score buffer per q tile beside
-//     two O), which the other q tile only partly fills. 64-key tiles with two buffers break
-//     the chain, but their products are smaller: 512 us.
-//   128 rows, 4 x 32K rows, window 64: 473 us, 5.7 TB/s of the 2.7 GB it has to move. The four
-//     softmax warps of each of an SM's two CTAs are busy throughout (two tiles, then the output).
+//   256 rows, 8K of 32K rows, window 4096: 395 us, 1.39 PFLOP/s. Per 128 keys a q tile's softmax
+//     (~2000 clocks), the hand-over of its weights (~370) and their product with the next scores
+//     (~1030) are a chain of ~3400, as tensor memory has one score buffer per q tile beside two O;
+//     the other q tile fits between, so the tensor core has 2048 clocks of work in 3400 (without
+//     the softmax it would take 328 us). An item's start and end cost ~5600 more. Tried: 64-key
+//     tiles with two buffers (512 us: smaller products), two threads per score row (429: they
+//     share a scheduler, and the weights are handed over later), an MMA warp per q tile (533:
+//     the q tiles fall into step), warps of their own for the output (404).
+//   128 rows, 4 x 32K rows, window 64: 450 us, 6.0 TB/s of the 2.7 GB it has to move. Its output:
+//     335 us without the stores, the same with the softmax left out.
 //   16 rows, 32 tokens, window 4096, pages: 88 us, 6.1 TB/s. HBM.
 // Registers that spill are the first thing to look at here: shared memory leaves next to no L1,
 // so a spill is a trip to L2 (a form that spilled took twice the time).
@@ -316,7 +319,7 @@ __device__ __forceinline__ void st_global32(void *p, const uint32_t *w)
                  : "memory");
 }
 
-// N (32 or 64) output values of one row, a thread per row: in 32-byte pieces, whole sectors,
+// N output values of one row, a thread per row: in 32-byte pieces, whole sectors,
 // where the output is aligned to them.
 template <int N, bool FP32>
 __device__ __forceinline__ void store_row(const WindowParams &p, size_t at, const float *v)
@@ -349,6 +352,44 @@ __device__ __forceinline__ void store_row(const WindowParams &p, size_t at, cons
                 *reinterpret_cast<uint4 *>(o + i) = make_uint4(w[0], w[1], w[2], w[3]);
                 *reinterpret_cast<uint4 *>(o + i + 8) = make_uint4(w[4], w[5], w[6], w[7]);
             }
+        }
+    }
+}
+
+// 128 bytes of each of a warp's 32 rows, a thread per row, in four pieces of 32 bytes: the pieces
+// are transposed among each four lanes, so that a store instruction covers whole lines of 8 rows
+// instead of a sector of each of 32. `at` says where (in bytes) the piece of a row belongs, or
+// a negative number for rows that are not written. For the form whose time is its output: four
+// 32K prompts under a window of 64 take 450 us, with store_row 472 (and 335 with no store at
+// all). With two q tiles the transposition costs the tile loop more than it gives (an 8K chunk
+// under a window of 4096: 414 us against 395), with one token it is only latency.
+template <typename At>
+__device__ __forceinline__ void store_lines(const WindowParams &p, uint32_t *w, int lane, At at)
+{
+#pragma unroll
+    for (int step = 1; step <= 2; ++step) {
+        const bool upper = (lane & step) != 0;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            // pieces (0, 1) and (2, 3), then (0, 2) and (1, 3)
+            const int lo = step == 1 ? (i >> 3) * 16 + (i & 7) : i, hi = lo + 8 * step;
+            const uint32_t got = __shfl_xor_sync(0xffffffffu, upper ? w[lo] : w[hi], step);
+            w[lo] = upper ? got : w[lo];
+            w[hi] = upper ? w[hi] : got;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const long long to = at(i);
+        if (to < 0)
+            continue;
+        uint8_t *o = static_cast<uint8_t *>(p.out) + to + 32 * (lane & 3);
+        const uint32_t *v = w + 8 * i;
+        if (p.out_aligned32) {
+            st_global32(o, v);
+        } else {
+            reinterpret_cast<uint4 *>(o)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+            reinterpret_cast<uint4 *>(o)[1] = make_uint4(v[4], v[5], v[6], v[7]);
         }
     }
 }
@@ -518,6 +559,8 @@ __global__ void __launch_bounds__(128 + 128 * NQ, NQ == 1 && !F32 ? 2 : 1)
                 // (the arrays inside the branch: defined on one path only, they would count as live
                 // around the whole loop over items)
                 float o[2][32];         // 32 columns at a time, the next ones on their way
+                constexpr bool kLines = NQ == 1 && QR == 128 && !F32;
+                uint32_t line[kLines ? 32 : 1];     // 128 bytes of the row
                 tmem_ld32(o_col(a) + lane_addr, o[0]);
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
@@ -537,18 +580,28 @@ __global__ void __launch_bounds__(128 + 128 * NQ, NQ == 1 && !F32 ? 2 : 1)
                         tmem_ld32(o_col(a) + lane_addr + 32 * q + 32, o[(q + 1) & 1]);
                     else
                         release();
-                    if (valid) {
+                    if constexpr (!SPLIT && kLines) {
+#pragma unroll
+                        for (int x = 0; x < 16; ++x) {
+                            const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * x] * inv, v[2 * x + 1] * inv);
+                            line[16 * (q & 1) + x] = *reinterpret_cast<const uint32_t *>(&b);
+                        }
+                        if (q & 1)
+                            store_lines(p, line, lane, [&](int i) -> long long {
+                                const int r = (rq & ~3) + i;
+                                const uint32_t row = it.row0 + (r >> p.group_log2) * (p.n_kv_heads * G) + (r & (G - 1));
+                                return r < nrows ? static_cast<long long>(row) * 256 + 64 * (q - 1) : -1;
+                            });
+                    } else if (valid && !SPLIT) {
 #pragma unroll
                         for (int x = 0; x < 32; ++x)
                             v[x] *= inv;
-                        if (!SPLIT) {
-                            store_row<32, F32>(p, my_row * kHeadDim + 32 * q, v);
-                        } else {
-                            float *w = p.parts + (part * p.part_rows + rq) * kHeadDim + 32 * q;
+                        store_row<32, F32>(p, my_row * kHeadDim + 32 * q, v);
+                    } else if (valid) {
+                        float *w = p.parts + (part * p.part_rows + rq) * kHeadDim + 32 * q;
 #pragma unroll
-                            for (int x = 0; x < 32; x += 8)
-                                st_global32(w + x, reinterpret_cast<const uint32_t *>(v + x));
-                        }
+                        for (int x = 0; x < 32; x += 8)
+                            st_global32(w + x, reinterpret_cast<const uint32_t *>(v + x));
                     }
                 }
             } else {
