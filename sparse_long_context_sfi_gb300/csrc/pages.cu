@@ -6,8 +6,9 @@
 // runs on the whole GPU. A page of one layer and tensor is n_kv_heads * 4 KB, contiguous.
 //
 // Measured (GB300, copy rate 6.78 TB/s): rows of four 8K chunks 38 us (7.0 TB/s of read and
-// written bytes), a quarter of a 16K-page pool moved in 77 us (7.0 TB/s), packed memory of 8
-// sequences to 24 others 21 us; the one-CTA plans take 5 to 8 us, round trips to L2.
+// written bytes), a quarter of a 16K-page pool moved in 77 us (7.0 TB/s); 8 sequences with
+// their packed memory (31 MB) forked to 24 others in 27.7 us with tables and counts (29.4 when each
+// copy read its source); the one-CTA plans take 5 to 8 us, round trips to L2.
 //
 // Kernels here that write what a fast step may read before its own wait (packed memory, `ok`
 // masks) let no dependent start early; the others start theirs at entry.
@@ -650,43 +651,63 @@ __global__ void __launch_bounds__(256) reorder_ints_kernel(const ReorderParams p
 // place. A CTA holds the same few rows of one head of every moving sequence: each of its
 // threads reads its 16-byte pieces of them into registers, all at once, and writes them after
 // a barrier, so that no other CTA and no scratch is involved. A row moves if it is below the
-// source's row count. kPieces: pieces per thread, enough for a whole batch that moves.
+// source's row count. kPieces: pieces per thread, enough for a whole batch that moves. The
+// moves are sorted by source and a thread takes consecutive ones, so that a source of several
+// copies (a fork) is read once per thread and not once per copy.
 template <int kPieces>
 __global__ void __launch_bounds__(256) reorder_rows_kernel(const ReorderParams p, uint4 *k, uint4 *v,
                                                            int rows_per_head, const int32_t *rows,
                                                            int rows_by_unit, int cols_log2)
 {
-    __shared__ int2 mv[kMaxBatch];
+    __shared__ int2 listed[kMaxBatch], mv[kMaxBatch];
     __shared__ int have[kMaxBatch];
     __shared__ int n_mv;
     pdl_wait();
-    const int n = moved_list(p.src, p.batch, mv, &n_mv, p.err, false);
+    const int n = moved_list(p.src, p.batch, listed, &n_mv, p.err, false);
     const int layer = blockIdx.y / p.n_kv_heads, head = blockIdx.y - layer * p.n_kv_heads;
-    for (int i = threadIdx.x; i < n; i += 256)
-        have[i] = rows_by_unit
-                      ? rows[(static_cast<long long>(layer) * p.batch + mv[i].y) * p.n_kv_heads + head]
-                      : rows[mv[i].y];
+    if (static_cast<int>(threadIdx.x) < n) {    // (at most one each)
+        const int2 me = listed[threadIdx.x];
+        const int count = rows_by_unit
+                              ? rows[(static_cast<long long>(layer) * p.batch + me.y) * p.n_kv_heads + head]
+                              : rows[me.y];
+        int at = 0;
+        for (int i = 0; i < n; ++i) {
+            const int y = listed[i].y;
+            at += y < me.y || (y == me.y && i < static_cast<int>(threadIdx.x));
+        }
+        mv[at] = me;
+        have[at] = count;
+    }
     __syncthreads();
     const long long stride = static_cast<long long>(p.n_kv_heads) * rows_per_head * 16;
     uint4 *t = (blockIdx.z ? v : k) + static_cast<long long>(layer) * p.batch * stride +
                static_cast<long long>(head) * rows_per_head * 16;
     const uint32_t col = (blockIdx.x << cols_log2) + (threadIdx.x & ((1u << cols_log2) - 1u));
-    const int m0 = threadIdx.x >> cols_log2, step = 256 >> cols_log2;
+    // (at most kPieces each: the batch times the columns is at most 256 kPieces)
+    const int groups = 256 >> cols_log2, per = (n + groups - 1) / groups;
+    const int m0 = (threadIdx.x >> cols_log2) * per;
     uint4 x[kPieces];
-    uint32_t live = 0;
+    uint32_t live = 0, same = 0;
 #pragma unroll
     for (int q = 0; q < kPieces; ++q) {
-        const int i = m0 + q * step;
-        if (i < n && static_cast<int>(col >> 4) < min(have[i], rows_per_head)) {
+        const int i = m0 + q;
+        if (q < per && i < n && static_cast<int>(col >> 4) < min(have[i], rows_per_head)) {
             live |= 1u << q;
-            x[q] = t[mv[i].y * stride + col];
+            if (q > 0 && mv[i - 1].y == mv[i].y)
+                same |= 1u << q;
+            else
+                x[q] = t[mv[i].y * stride + col];
         }
     }
+#pragma unroll
+    for (int q = 1; q < kPieces; ++q)
+        if ((same >> q) & 1u)
+            x[q] = x[q - 1];
     __syncthreads();
 #pragma unroll
     for (int q = 0; q < kPieces; ++q)
         if ((live >> q) & 1u)
-            t[mv[m0 + q * step].x * stride + col] = x[q];
+            t[mv[m0 + q].x * stride + col] = x[q];
 }
 
 }  // namespace
