@@ -26,7 +26,7 @@
 // unnormalised outputs, maxima and sums the last one to finish joins, in split order.
 //
 // What bounds it (GB300, copy rate 6.78 TB/s, bf16 products 1.90 PFLOP/s measured):
-//   256 rows, 8K of 32K rows, window 4096: 395 us, 1.39 PFLOP/s. Per 128 keys a q tile's softmax
+//   256 rows, 8K of 32K rows, window 4096: 396 us, 1.39 PFLOP/s. Per 128 keys a q tile's softmax
 //     (~2000 clocks), the hand-over of its weights (~370) and their product with the next scores
 //     (~1030) are a chain of ~3400, as tensor memory has one score buffer per q tile beside two O;
 //     the other q tile fits between, so the tensor core has 2048 clocks of work in 3400 (without
@@ -34,8 +34,8 @@
 //     tiles with two buffers (512 us: smaller products), two threads per score row (429: they
 //     share a scheduler, and the weights are handed over later), an MMA warp per q tile (533:
 //     the q tiles fall into step), warps of their own for the output (404).
-//   128 rows, 4 x 32K rows, window 64: 450 us, 6.0 TB/s of the 2.7 GB it has to move. Its output:
-//     335 us without the stores, the same with the softmax left out.
+//   128 rows, 4 x 32K rows, window 64: 444 us, 6.0 TB/s of the 2.7 GB it has to move: 335 us
+//     without the stores, no less with the softmax left out, 446 with stores through TMA.
 //   16 rows, 32 tokens, window 4096, pages: 88 us, 6.1 TB/s. HBM.
 // Registers that spill are the first thing to look at here: shared memory leaves next to no L1,
 // so a spill is a trip to L2 (a form that spilled took twice the time).
@@ -654,11 +654,11 @@ __global__ void __launch_bounds__(128 + 128 * NQ, NQ == 1 && !F32 ? 2 : 1)
     };
 
     // Registers (launched with 168 a thread, or 128 with two CTAs per SM): the softmax keeps a
-    // score row, the other roles give up what they do not need. 384 * 168 = 256 * 208 + 128 * 88;
+    // score row, the other roles give up what they do not need. 384 * 168 = 256 * 184 + 128 * 136;
     // 256 * 128 = 128 * 192 + 128 * 64. (With F32 everybody has enough.)
     if (warp >= 4) {
         if constexpr (!F32)
-            asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(NQ == 1 ? 192 : 208));
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(NQ == 1 ? 192 : 184));
         // ------------------------------------------------------------------------ softmax
         const int a = (warp - 4) >> 2, quad = warp & 3, rowi = quad * 32 + lane;
         const uint32_t lane_addr = static_cast<uint32_t>(quad * 32) << 16;
@@ -862,7 +862,7 @@ __global__ void __launch_bounds__(128 + 128 * NQ, NQ == 1 && !F32 ? 2 : 1)
             wfail(c, p.err);
     } else {
         if constexpr (!F32)
-            asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(NQ == 1 ? 64 : 88));
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(NQ == 1 ? 64 : 136));
         if (warp == 0) {
             // ------------------------------------------------------------------ TMA producer
             int use = 0, items = 0;
@@ -1010,49 +1010,37 @@ __global__ void __launch_bounds__(128 + 128 * NQ, NQ == 1 && !F32 ? 2 : 1)
                 if (seq == end)
                     continue;
                 ok = warp_wait(&c.qf, items & 1, &c.abort);
-                // The scores of the first NS tiles, then tile by tile the product of a q tile and at
-                // once the scores that take over its buffer: NS tiles ahead of the softmax.
-                for (uint32_t t = seq; t < end && t < seq + NS && ok; ++t) {
-                    ok = warp_wait(&c.kf[t % ST], (t / ST) & 1, &c.abort);
-                    if (!ok)
-                        break;
-                    tc_fence_after();
-                    if (elect_one()) {
-#pragma unroll
-                        for (int A = 0; A < NQ; ++A)
-                            scores(A, t % ST, t % NS);
-                        umma_commit(&c.ke[t % ST]);
-                        if (t + 1 == end)
-                            umma_commit(&c.qe);
-                    }
-                    __syncwarp();
-                }
+                // Steps: the product of a tile and at once the scores that take over its buffer, NS tiles
+                // ahead of the softmax; the first NS steps have no product yet. (One copy of this code:
+                // with one of its own for an item's first scores, four 32K prompts under a window of 64
+                // take 450 us, so 444.)
                 const uint32_t begin = seq;
-                for (; seq < end && ok; ++seq) {
-                    const uint32_t st = seq % ST, buf = seq % NS, next = seq + NS;
-                    const bool more = next < end;
+                for (uint32_t next = seq; next < end + NS && ok; ++next) {
+                    const uint32_t st = seq % ST, buf = next % NS;
 #pragma unroll
                     for (int A = 0; A < NQ; ++A) {
+                        if (next >= begin + NS) {
 #pragma unroll
-                        for (int half = 0; half < NH; ++half) {
-                            ok = ok && warp_poll([&] {
-                                return mbar_test_wait(&c.pf[A][NH == 2 ? half : buf], (seq / NS) & 1) &&
-                                       (A > 0 || half > 0 || mbar_test_wait(&c.vr[st], (seq / ST) & 1)) &&
-                                       (seq > begin || half > 0 || mbar_test_wait(&c.oe[A], (items & 1) ^ 1));
-                            }, &c.abort);
+                            for (int half = 0; half < NH; ++half) {
+                                ok = ok && warp_poll([&] {
+                                    return mbar_test_wait(&c.pf[A][NH == 2 ? half : buf], (seq / NS) & 1) &&
+                                           (A > 0 || half > 0 || mbar_test_wait(&c.vr[st], (seq / ST) & 1)) &&
+                                           (seq > begin || half > 0 || mbar_test_wait(&c.oe[A], (items & 1) ^ 1));
+                                }, &c.abort);
+                                if (!ok)
+                                    break;
+                                tc_fence_after();
+                                if (elect_one()) {
+                                    products(A, st, buf, half, F32 ? (seq - begin) % kFlush == 0 : seq == begin);
+                                    if (A == NQ - 1 && half == NH - 1)
+                                        umma_commit(&c.ve[st]);
+                                }
+                                __syncwarp();
+                            }
                             if (!ok)
                                 break;
-                            tc_fence_after();
-                            if (elect_one()) {
-                                products(A, st, buf, half, F32 ? (seq - begin) % kFlush == 0 : seq == begin);
-                                if (A == NQ - 1 && half == NH - 1)
-                                    umma_commit(&c.ve[st]);
-                            }
-                            __syncwarp();
                         }
-                        if (!ok)
-                            break;
-                        if (!more)
+                        if (next >= end)
                             continue;
                         // (asked only now: the product does not wait for keys that are on their way)
                         if (A == 0) {
@@ -1072,6 +1060,8 @@ __global__ void __launch_bounds__(128 + 128 * NQ, NQ == 1 && !F32 ? 2 : 1)
                         }
                         __syncwarp();
                     }
+                    if (next >= begin + NS)
+                        ++seq;
                 }
                 if (!ok)
                     break;
