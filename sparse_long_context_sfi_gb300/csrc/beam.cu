@@ -75,6 +75,15 @@ __device__ __forceinline__ float ex2(float x)
     return y;
 }
 
+// An integer that orders like the float (and back), for the warp's integer reductions.
+__device__ __forceinline__ int order(float x)
+{
+    const int i = __float_as_int(x);
+    return i ^ ((i >> 31) & 0x7fffffff);
+}
+
+__device__ __forceinline__ float unorder(int i) { return __int_as_float(i ^ ((i >> 31) & 0x7fffffff)); }
+
 // The warp's K best so far: lane j holds the j-th, lanes from K on hold nothing.
 struct Best {
     float x;
@@ -196,9 +205,10 @@ __global__ void __launch_bounds__(kBeamThreads, 4) beam_kernel(const BeamParams 
 {
     __shared__ float sh_x[kMaxBeams][kBeamWarps], sh_m[kBeamWarps], sh_s[kBeamWarps];
     __shared__ int sh_v[kMaxBeams][kBeamWarps];
-    __shared__ float cand_x[kBeamWarps][32 * kLaneTok];   // a chunk's candidates, in any order
-    __shared__ int cand_v[kBeamWarps][32 * kLaneTok], n_cand[kBeamWarps];
-    __shared__ volatile float top[kBeamWarps];
+    // candidates that wait to be inserted, in any order: fewer than 32 and a chunk's
+    __shared__ float cand_x[kBeamWarps][32 * kLaneTok + 32];
+    __shared__ int cand_v[kBeamWarps][32 * kLaneTok + 32], n_cand[kBeamWarps];
+    __shared__ volatile int top[kBeamWarps];        // (as order())
     __shared__ float row_x[kMaxBeams][kMaxBeams], row_s[kMaxBeams][kMaxBeams];
     __shared__ int row_v[kMaxBeams][kMaxBeams];
     __shared__ uint8_t row_done[kMaxBeams];
@@ -206,8 +216,10 @@ __global__ void __launch_bounds__(kBeamThreads, 4) beam_kernel(const BeamParams 
     constexpr int V = Chunk<T>::kV;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int K = p.n_beams, row = blockIdx.y, split = blockIdx.x, group = row / K;
-    if (tid < kBeamWarps)
-        top[tid] = -CUDART_INF_F;
+    if (tid < kBeamWarps) {
+        top[tid] = order(-CUDART_INF_F);
+        n_cand[tid] = 0;
+    }
     pdl_wait();
     __syncthreads();
     if (!(p.done && p.done[row])) {
@@ -218,6 +230,22 @@ __global__ void __launch_bounds__(kBeamThreads, 4) beam_kernel(const BeamParams 
         Best best;
         best.clear();
         bool fresh = true;          // (the same in every lane, as is all that decides a branch here)
+        int mine = order(-CUDART_INF_F);    // the warp's highest logit
+        // the candidates that wait go into the list
+        auto insert_waiting = [&] {
+            __syncwarp();
+            const int n = n_cand[warp];
+            for (int i = 0; i < n; i += 32) {
+                const bool on = i + lane < n;
+                best.offer(on ? cand_x[warp][i + lane] : 0.f, on ? cand_v[warp][i + lane] : -1, K, lane);
+            }
+            __syncwarp();
+            if (lane == 0)
+                n_cand[warp] = 0;
+            if (K > kBeamWarps && lane == (K - 1) / kBeamWarps)
+                top[warp] = order(best.x);
+            __syncwarp();
+        };
         float R = -CUDART_INF_F, s = 0.f;
         int c = (split * kBeamWarps + warp) * kStep;
         const int stride = p.splits * kBeamWarps * kStep;
@@ -259,23 +287,22 @@ __global__ void __launch_bounds__(kBeamThreads, 4) beam_kernel(const BeamParams 
                                               : x[j] == x[j] ? 0.f : CUDART_NAN_F;
             }
             // Tokens that beat the K-th best so far. A warp's first chunk starts the list with
-            // every lane's best; the others that still beat it go through shared memory.
-            // What all warps of the CTA hold bounds it too: top[w] is the ceil(K / 8)-th best of warp
-            // w, so at least K tokens are as high as the lowest of them (read without a barrier: an
-            // older value is only a weaker bound).
-            bool look = __any_sync(kAll, cm > best.tx || best.tv < 0);
-            float floor = -CUDART_INF_F;
-            if (look) {
-                floor = top[lane & (kBeamWarps - 1)];
-#pragma unroll
-                for (int o = 1; o < kBeamWarps; o <<= 1)
-                    floor = fminf(floor, __shfl_xor_sync(kAll, floor, o));
-                look = __any_sync(kAll, cm >= floor && (cm > best.tx || best.tv < 0));
-            }
-            if (look) {
+            // every lane's best; the others that may still beat it wait in shared memory until there
+            // are 32 of them or the row ends (inserted chunk by chunk, each a chain of shuffles, they
+            // took 9 of 35 us in 256 rows of 128001 tokens).
+            // What all warps of the CTA hold is a bound, too: top[w] is the ceil(K / 8)-th best that
+            // warp w has seen, so at least K tokens are as high as the lowest of them (read without
+            // a barrier: an older value is only a weaker bound).
+            const float floor = unorder(__reduce_min_sync(kAll, top[lane & (kBeamWarps - 1)]));
+            if (__any_sync(kAll, cm >= floor && (cm > best.tx || best.tv < 0))) {
                 const int v0 = (c + lane) * V - shift;
                 // (tokens grow with j, so the first of equal logits is the lowest token)
                 auto token = [&](int j) { return v0 + 32 * V * (j / V) + j % V; };
+                if (K <= kBeamWarps) {
+                    mine = max(mine, __reduce_max_sync(kAll, order(cm)));
+                    if (lane == 0)
+                        top[warp] = mine;
+                }
                 int taken = -1;
                 if (fresh) {
                     float cx = -CUDART_INF_F;
@@ -287,15 +314,11 @@ __global__ void __launch_bounds__(kBeamThreads, 4) beam_kernel(const BeamParams 
                         }
                     }
                     best.start(cx, taken, K, lane);
-                    fresh = false;
                 }
-                if (lane == 0)
-                    n_cand[warp] = 0;
-                __syncwarp();
-                floor = fmaxf(floor, best.tx);
+                const float least = fmaxf(floor, best.tx);
 #pragma unroll
                 for (int j = 0; j < kLaneTok; ++j) {
-                    if (x[j] >= floor) {
+                    if (x[j] >= least) {
                         const int v = token(j);
                         if (v != taken && v >= 0 && v < p.vocab) {
                             const int at = atomicAdd(&n_cand[warp], 1);
@@ -305,16 +328,12 @@ __global__ void __launch_bounds__(kBeamThreads, 4) beam_kernel(const BeamParams 
                     }
                 }
                 __syncwarp();
-                const int n = n_cand[warp];
-                for (int i = 0; i < n; i += 32) {
-                    const bool on = i + lane < n;
-                    best.offer(on ? cand_x[warp][i + lane] : 0.f, on ? cand_v[warp][i + lane] : -1, K, lane);
-                }
-                if (lane == (K - 1) / kBeamWarps)
-                    top[warp] = best.x;
-                __syncwarp();
+                if (fresh || n_cand[warp] >= 32)
+                    insert_waiting();
+                fresh = false;
             }
         }
+        insert_waiting();
         // the warp's reference and sum
         float wm = R;
 #pragma unroll
