@@ -5,9 +5,10 @@
 // logit are all that its group can need. The logits are read once (the floor: their bytes);
 // every warp takes 512-token chunks of its row, 16 tokens per lane in registers, the next
 // chunk's loads in flight. The best tokens so far lie sorted in the warp's lanes, and a chunk
-// whose maximum is below the last of them costs one comparison per lane; the others are
-// inserted one by one, the chunk from its end, so that neither ascending nor descending logits
-// insert every token. Warps of a CTA, the CTAs of a row (splits) and the rows of a group are
+// whose maximum is below the last of them, or below a bound that the CTA's warps share, costs a
+// comparison per lane; tokens that may enter the list wait in shared memory and are inserted
+// together, from the last one, so that neither ascending nor descending logits insert every
+// token. Warps of a CTA, the CTAs of a row (splits) and the rows of a group are
 // joined by the same insertion; the last CTA of a group does the last two.
 //
 // Issue slots bound it (a token's share at the copy rate is ~22 of fp32, ~11 of bf16), so the
@@ -15,8 +16,9 @@
 // exact-product multiply-add and an exponential per token, whatever the size of the logits,
 // and only the scores of the chosen few are formed from R, in double.
 //
-// 256 rows of 128001 fp32 logits: 35 us, 3.8 TB/s (floor 19 us; issue slots, 52 % of them
-// active, and 512 CTAs over 152 SMs); 4 rows of 32000 bf16: 8.6 us, launch and round trips.
+// 256 rows of 128001 fp32 logits: 32.8 us, 4.0 TB/s (floor 19 us). Without any list it takes
+// 21.6 us, with the first chunk's alone 26; the rest is tests, waiting tokens and insertions.
+// 4 rows of 32000 bf16: 8.5 us, launch and round trips.
 #include "sfi_device.cuh"
 
 #include <math_constants.h>
