@@ -233,13 +233,14 @@ __global__ void __launch_bounds__(kBeamThreads, 4) beam_kernel(const BeamParams 
         best.clear();
         bool fresh = true;          // (the same in every lane, as is all that decides a branch here)
         int mine = order(-CUDART_INF_F);    // the warp's highest logit
-        // the candidates that wait go into the list
+        // the candidates that wait go into the list, without those that the CTA's bound has passed
         auto insert_waiting = [&] {
             __syncwarp();
             const int n = n_cand[warp];
+            const float floor = unorder(__reduce_min_sync(kAll, top[lane & (kBeamWarps - 1)]));
             for (int i = 0; i < n; i += 32) {
-                const bool on = i + lane < n;
-                best.offer(on ? cand_x[warp][i + lane] : 0.f, on ? cand_v[warp][i + lane] : -1, K, lane);
+                const float cx = i + lane < n ? cand_x[warp][i + lane] : -CUDART_INF_F;
+                best.offer(cx, i + lane < n && cx >= floor ? cand_v[warp][i + lane] : -1, K, lane);
             }
             __syncwarp();
             if (lane == 0)
