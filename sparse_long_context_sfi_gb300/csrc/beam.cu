@@ -16,8 +16,9 @@
 // exact-product multiply-add and an exponential per token, whatever the size of the logits,
 // and only the scores of the chosen few are formed from R, in double.
 //
-// 256 rows of 128001 fp32 logits: 32.8 us, 4.0 TB/s (floor 19 us). Without any list it takes
-// 21.6 us, with the first chunk's alone 26; the rest is tests, waiting tokens and insertions.
+// 256 rows of 128001 fp32 logits: 31.3 us, 4.2 TB/s (floor 19 us). Without any list it takes
+// 21.6 us, with the first chunk's alone 26; the rest is tests, waiting tokens and insertions. (304
+// rows, which fill the GPU, take no longer than 256, whose 512 CTAs leave some SMs a quarter idle.)
 // 4 rows of 32000 bf16: 8.5 us, launch and round trips.
 #include "sfi_device.cuh"
 
