@@ -479,7 +479,8 @@ sfi_status sfi_append_chunk(const sfi_kv_cache *kv, const void *k_new, const voi
  *        skipped sequences and rows behind row_start[batch] are not written
  * Cache rows that no row of the call attends to are never looked at (their pages may be
  * missing, their contents may be anything); a V row that some row attends to has to be finite,
- * because its neighbours in the chunk meet it with a weight of zero. Softmax weights
+ * because its neighbours in the chunk meet it with a weight of zero. A K row that is not a
+ * number makes the rows that attend to it NaN, and no others. Softmax weights
  * enter the product with V as bf16, with out_fp32 in three bf16 parts (24 bits). n_sink >= 0,
  * n_window >= 1. A sequence longer than max_len, or with more rows than its length, is skipped
  * (SFI_DEVERR_LENGTH).

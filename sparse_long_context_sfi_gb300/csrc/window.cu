@@ -634,7 +634,8 @@ __global__ void __launch_bounds__(128 + 128 * NQ, NQ == 1 && !F32 ? 2 : 1)
                     for (int sp = 0; sp < p.n_split; ++sp) {
                         const size_t at = p0 + static_cast<size_t>(sp) * p.part_rows;
                         const float2 ml = __ldcg(p.part_ml + at);
-                        if (ml.y > 0.f) {
+                        // (a split that saw nothing left no outputs; one whose sum is not a number did)
+                        if (ml.y != 0.f) {
                             const float w = ex2_approx((ml.x - M) * p.scale_log2);
                             acc = fmaf(w, __ldcg(p.parts + at * kHeadDim + d), acc);
                             den = fmaf(w, ml.y, den);
