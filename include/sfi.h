@@ -453,8 +453,9 @@ sfi_status sfi_pages_compact(const sfi_kv_cache *kv, const sfi_page_pool *pool, 
  * packed: sequence b owns rows [row_start[b], row_start[b + 1]) of [n_rows] (row_start: device
  * int32 [batch + 1], ascending). n_rows bounds row_start[batch] and max_rows every sequence's
  * count; rows behind row_start[batch] are not touched. row_start == NULL: one row each
- * (n_rows == batch). A sequence whose rows run backwards, past n_rows or past max_rows is
- * skipped (SFI_DEVERR_ROWS); so are, in sfi_window_attn, sequences beyond n_rows rows in all.
+ * (n_rows == batch). A sequence whose rows run backwards, past n_rows or past max_rows, or
+ * start before an earlier entry of row_start (they would be another's rows, too), is skipped by
+ * both calls (SFI_DEVERR_ROWS).
  *
  * sfi_append_chunk writes a chunk of new tokens (a prompt or a part of one):
  * k_new, v_new: bf16 [n_layers][n_rows][n_kv_heads][128]. Row i of an active sequence goes to

@@ -450,16 +450,23 @@ __global__ void __launch_bounds__(256) compact_move_kernel(const PageParams p, c
 
 // --------------------------------------------------------------------------- chunk appends
 
-// Whether sequence b's chunk is sound: rows within bounds, room in the cache.
-__device__ __forceinline__ bool chunk_ok(const ChunkParams &p, int b, int &r0, int &n, int &L,
+// Whether sequence b's chunk is sound: rows within bounds and no other's, room in the cache. A
+// warp call, every lane the same b. Where the starts run backwards somewhere, rows belong to the
+// first sequence that claims them: one that begins before an earlier start is left out.
+__device__ __forceinline__ bool chunk_ok(const ChunkParams &p, int b, int lane, int &r0, int &n, int &L,
                                          bool report)
 {
     r0 = p.row_start ? p.row_start[b] : b;
     const int r1 = p.row_start ? p.row_start[b + 1] : b + 1;
     n = r1 - r0;
     L = p.pg.seq_len[b];
+    bool owned = true;
+    if (p.row_start)
+        for (int i = lane; i < b; i += 32)
+            owned = owned && p.row_start[i] <= r0;
+    owned = __all_sync(kFull, owned) != 0;
     uint32_t bad = 0;
-    if (r0 < 0 || n < 0 || r1 > p.n_rows || n > p.max_rows)
+    if (r0 < 0 || n < 0 || r1 > p.n_rows || n > p.max_rows || (n > 0 && !owned))
         bad = 0x20u;  // SFI_DEVERR_ROWS
     else if (L < 0 || L > p.pg.max_len)
         bad = 0x8u;   // SFI_DEVERR_LENGTH
@@ -473,23 +480,24 @@ __device__ __forceinline__ bool chunk_ok(const ChunkParams &p, int b, int &r0, i
 constexpr int kChunkRows = 8;   // rows per CTA
 
 // The cache row of (layer 0, head 0) for packed row r, -1 where it is not written. One warp,
-// every lane the same r: the row's sequence is the last b with row_start[b] <= r, found by
-// counting, so that the starts are read in one round trip.
+// every lane the same r: the row's sequence is the one before the first start behind r, found
+// in one round trip (a sound sequence's own rows are in front of every later start that counts).
 __device__ __forceinline__ long long chunk_dst(const ChunkParams &p, int r, int lane)
 {
     int b = r;
     if (r >= p.n_rows)
         return -1;
     if (p.row_start) {
-        int at = 0;
+        int behind = p.pg.batch + 1;
         for (int i = lane; i <= p.pg.batch; i += 32)
-            at += p.row_start[i] <= r;
-        b = __reduce_add_sync(kFull, at) - 1;
+            if (p.row_start[i] > r)
+                behind = min(behind, i);
+        b = __reduce_min_sync(kFull, behind) - 1;
         if (b < 0 || b >= p.pg.batch)
             return -1;
     }
     int s0, n, L;
-    if ((p.pg.active && !p.pg.active[b]) || !chunk_ok(p, b, s0, n, L, false) || r < s0 || r >= s0 + n)
+    if ((p.pg.active && !p.pg.active[b]) || !chunk_ok(p, b, lane, s0, n, L, false) || r < s0 || r >= s0 + n)
         return -1;
     const int pos = L + r - s0;
     if (p.pg.page_size == 0)
@@ -558,7 +566,7 @@ __global__ void __launch_bounds__(1024) advance_kernel(const ChunkParams p)
         if (p.pg.active && !p.pg.active[b])
             continue;
         int s0, n, L;
-        if (!chunk_ok(p, b, s0, n, L, lane == 0))
+        if (!chunk_ok(p, b, lane, s0, n, L, lane == 0))
             continue;
         bool good = true;
         if (p.pg.page_size != 0 && n > 0) {

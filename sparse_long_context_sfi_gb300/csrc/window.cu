@@ -43,6 +43,7 @@
 
 #include <math_constants.h>
 
+#include <climits>
 #include <cstddef>
 
 namespace sfi {
@@ -455,15 +456,12 @@ __global__ void __launch_bounds__(128 + 128 * NQ, NQ == 1 && !F32 ? 2 : 1)
         if (p.active && !p.active[b]) {
             n = 0;
         } else {
-            uint32_t bad = 0;
-            if (s0 < 0 || n < 0 || s1 > p.n_rows || n > p.max_rows)
-                bad = 0x20u;  // SFI_DEVERR_ROWS
-            else if (L < n || L > p.max_len)
-                bad = 0x8u;   // SFI_DEVERR_LENGTH
-            if (bad) {
+            if (s0 < 0 || n < 0 || s1 > p.n_rows || n > p.max_rows) {
                 n = 0;
                 if (blockIdx.x == 0)
-                    raise_error(p.err, bad);
+                    raise_error(p.err, 0x20u);  // SFI_DEVERR_ROWS
+            } else if (L < n || L > p.max_len) {
+                n = -1 - n;     // (told below, if its rows are its own)
             }
         }
         c.cnt[b] = n;
@@ -472,26 +470,28 @@ __global__ void __launch_bounds__(128 + 128 * NQ, NQ == 1 && !F32 ? 2 : 1)
     }
     __syncthreads();
     if (warp == 0) {
-        // Sequences whose rows overlap (a row_start that runs backwards somewhere) must not make more
-        // items than the rows can hold: behind n_rows rows in all, the others are skipped.
-        int run = 0;
-        long long rows = 0;
+        // Where row_start runs backwards somewhere, rows belong to the first sequence that claims
+        // them: one that begins before an earlier start is skipped (so that there are never more
+        // items than the rows can hold).
+        int run = 0, high = INT_MIN;
         for (int b0 = 0; b0 < p.batch; b0 += 32) {
             const int b = b0 + lane;
-            long long upto = b < p.batch ? c.cnt[b] : 0;
+            const int s0 = b < p.batch ? c.start[b] : INT_MIN;
+            int upto = s0;
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const long long y = __shfl_up_sync(0xffffffffu, upto, o);
-                if (lane >= o)
-                    upto += y;
-            }
-            if (b < p.batch && c.cnt[b] > 0 && rows + upto > p.n_rows) {
-                c.cnt[b] = 0;
+            for (int o = 1; o < 32; o <<= 1)
+                upto = max(upto, __shfl_up_sync(0xffffffffu, upto, o));
+            int n = b < p.batch ? c.cnt[b] : 0;
+            const uint32_t bad = n != 0 && n != -1 && max(high, upto) > s0 ? 0x20u  // SFI_DEVERR_ROWS
+                                 : n < 0                                   ? 0x8u   // SFI_DEVERR_LENGTH
+                                                                           : 0u;
+            if (bad) {
+                c.cnt[b] = n = 0;
                 if (blockIdx.x == 0)
-                    raise_error(p.err, 0x20u);  // SFI_DEVERR_ROWS
+                    raise_error(p.err, bad);
             }
-            rows += __shfl_sync(0xffffffffu, upto, 31);
-            const int v = b < p.batch ? (c.cnt[b] + per - 1) / per : 0;
+            high = max(high, __shfl_sync(0xffffffffu, upto, 31));
+            const int v = (n + per - 1) / per;
             int x = v;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
