@@ -13,8 +13,8 @@
 //
 // Issue slots bound it (a token's share at the copy rate is ~22 of fp32, ~11 of bf16), so the
 // sums are kept relative to R = fl(max * log2 e): exp(x) / 2^R = 2^(x log2 e - R) is then one
-// exact-product multiply-add and an exponential per token, whatever the size of the logits,
-// and only the scores of the chosen few are formed from R, in double.
+// exact-product multiply-add and an exponential per token, for logits up to 2^29 (beyond: see
+// reference()), and only the scores of the chosen few are formed from R, in double.
 //
 // 256 rows of 128001 fp32 logits: 31.3 us, 4.2 TB/s (floor 19 us). Without any list it takes
 // 21.6 us, with the first chunk's alone 26; the rest is tests, waiting tokens and insertions. (304
@@ -32,8 +32,18 @@ constexpr int kBeamWarps = kBeamThreads / 32;
 constexpr int kLaneTok = 16;                 // tokens per lane and chunk
 constexpr uint32_t kAll = 0xffffffffu;
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLowest = -0x1p126f;         // logits below it are masks (a power of two, so that its
-                                             // product with kLog2e is exact)
+constexpr float kLarge = 0x1p29f;            // logits of this size and beyond: see reference()
+constexpr float kLog2e4 = 0.25f * kLog2e;
+
+// What a logit is measured from, in units of 2^4 (by which exp(x) is 2^(x log2 e - 4 R)). Below
+// kLarge R = fl(x log2 e) / 4; x log2 e is off from it by 2^5 at most, so that the power stays in
+// range. From kLarge on two different logits are at least 64 apart, and in a row's sum only those
+// equal to the largest are left (the next has e^-64 of its weight or less): there it is enough that
+// R = x / 2 is exact, and above (or, negative, below) all the others.
+__device__ __forceinline__ float reference(float x)
+{
+    return fabsf(x) < kLarge ? x * kLog2e4 : 0.5f * x;
+}
 
 // a before b: higher logit, then lower token (empty places, v < 0, last)
 __device__ __forceinline__ bool better(float xa, int va, float xb, int vb)
@@ -77,6 +87,9 @@ __device__ __forceinline__ float ex2(float x)
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+
+// What a term relative to reference a counts relative to b.
+__device__ __forceinline__ float apart(float a, float b) { return ex2(4.f * (a - b)); }
 
 // An integer that orders like the float (and back), for the warp's integer reductions.
 __device__ __forceinline__ int order(float x)
@@ -267,10 +280,10 @@ __global__ void __launch_bounds__(kBeamThreads, 4) beam_kernel(const BeamParams 
 #pragma unroll
             for (int j = 0; j < kLaneTok; ++j)
                 cm = fmaxf(cm, x[j]);
-            // sum of 2^(x log2 e - R), R the lane's own running reference
-            const float rn = fmaxf(R, cm > -CUDART_INF_F ? fmaxf(cm, kLowest) * kLog2e : -CUDART_INF_F);
-            if (rn > kLowest * 0.5f) {
-                const uint64_t c2 = pack2(kLog2e, kLog2e), r2 = pack2(-rn, -rn);
+            // sum of 2^(x log2 e - 4 R), R the lane's own running reference
+            const float rn = fmaxf(R, cm * kLog2e4);
+            if (fabsf(rn) < kLarge * kLog2e4) {
+                const uint64_t c2 = pack2(kLog2e, kLog2e), r2 = pack2(-4.f * rn, -4.f * rn);
                 uint64_t acc = 0;
 #pragma unroll
                 for (int j = 0; j < kLaneTok; j += 2) {
@@ -278,17 +291,17 @@ __global__ void __launch_bounds__(kBeamThreads, 4) beam_kernel(const BeamParams 
                     acc = add2(acc, pack2(ex2(z.x), ex2(z.y)));
                 }
                 const float2 a = unpack2(acc);
-                s = (R > -CUDART_INF_F ? s * ex2(R - rn) : s) + (a.x + a.y);
+                s = (R > -CUDART_INF_F ? s * apart(R, rn) : s) + (a.x + a.y);
                 R = rn;
             } else {
-                // nothing but -inf and masks of the type's lowest value (which count alike, and only
-                // where there is nothing else), or NaN, which has to show in the sum
-                s = R > -CUDART_INF_F ? s * ex2(R - rn) : s;
-                R = rn;
+                // a largest logit from kLarge on, of either sign, or -inf alone, or NaN or +inf, which
+                // have to show in the sum
+                const float rm = cm > -CUDART_INF_F ? fmaxf(R, reference(cm)) : R;
+                s = R > -CUDART_INF_F ? s * apart(R, rm) : s;
+                R = rm;
 #pragma unroll
                 for (int j = 0; j < kLaneTok; ++j)
-                    s += x[j] > -CUDART_INF_F ? ex2(fmaf(fmaxf(x[j], kLowest), kLog2e, -rn))
-                                              : x[j] == x[j] ? 0.f : CUDART_NAN_F;
+                    s += x[j] > -CUDART_INF_F ? apart(reference(x[j]), rm) : x[j] == x[j] ? 0.f : CUDART_NAN_F;
             }
             // Tokens that beat the K-th best so far. A warp's first chunk starts the list with
             // every lane's best; the others that may still beat it wait in shared memory until there
@@ -343,7 +356,7 @@ __global__ void __launch_bounds__(kBeamThreads, 4) beam_kernel(const BeamParams 
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1)
             wm = fmaxf(wm, __shfl_xor_sync(kAll, wm, o));
-        float ws = s == 0.f ? 0.f : wm > -CUDART_INF_F ? s * ex2(R - wm) : s;
+        float ws = s == 0.f ? 0.f : wm > -CUDART_INF_F ? s * apart(R, wm) : s;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1)
             ws += __shfl_xor_sync(kAll, ws, o);
@@ -371,7 +384,7 @@ __global__ void __launch_bounds__(kBeamThreads, 4) beam_kernel(const BeamParams 
             for (int o = 16; o > 0; o >>= 1)
                 bm = fmaxf(bm, __shfl_xor_sync(kAll, bm, o));
             float bs = lane < kBeamWarps ? sh_s[lane] : 0.f;
-            bs = bs == 0.f ? 0.f : bm > -CUDART_INF_F ? bs * ex2(mine - bm) : bs;
+            bs = bs == 0.f ? 0.f : bm > -CUDART_INF_F ? bs * apart(mine, bm) : bs;
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1)
                 bs += __shfl_xor_sync(kAll, bs, o);
@@ -419,8 +432,8 @@ __global__ void __launch_bounds__(kBeamThreads, 4) beam_kernel(const BeamParams 
                 const float2 st = __ldcg(p.part_stat + part + i);
                 const float mn = fmaxf(m, st.x);
                 if (st.y != 0.f) {
-                    const float add = mn > -CUDART_INF_F ? st.y * ex2(st.x - mn) : st.y;
-                    s = (s != 0.f && mn > -CUDART_INF_F ? s * ex2(m - mn) : s) + add;
+                    const float add = mn > -CUDART_INF_F ? st.y * apart(st.x, mn) : st.y;
+                    s = (s != 0.f && mn > -CUDART_INF_F ? s * apart(m, mn) : s) + add;
                     m = mn;
                 }
             }
@@ -428,7 +441,7 @@ __global__ void __launch_bounds__(kBeamThreads, 4) beam_kernel(const BeamParams 
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1)
                 wm = fmaxf(wm, __shfl_xor_sync(kAll, wm, o));
-            s = s == 0.f ? 0.f : wm > -CUDART_INF_F ? s * ex2(m - wm) : s;
+            s = s == 0.f ? 0.f : wm > -CUDART_INF_F ? s * apart(m, wm) : s;
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1)
                 s += __shfl_xor_sync(kAll, s, o);
@@ -446,10 +459,12 @@ __global__ void __launch_bounds__(kBeamThreads, 4) beam_kernel(const BeamParams 
                     else
                         best.offer(ox, ov, K, lane);
                 }
-                // x - R / kLog2e in double: in fp32 it would round at the size of the logits
+                // x - 4 R / kLog2e in double: in fp32 it would round at the size of the logits. From
+                // kLarge on the largest logit, the list's first, stands for its reference.
+                const float first = __shfl_sync(kAll, best.x, 0);
                 if (best.v >= 0) {
-                    const double bx = wm > kLowest * 0.5f ? best.x : fmaxf(best.x, kLowest);
-                    score = static_cast<float>(bx - wm / static_cast<double>(kLog2e) - ls + cum);
+                    const double ref = fabsf(wm) < kLarge * kLog2e4 ? wm / static_cast<double>(kLog2e4) : first;
+                    score = static_cast<float>(best.x - ref - ls + cum);
                 }
             }
         }

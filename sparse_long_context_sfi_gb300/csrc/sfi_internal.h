@@ -207,7 +207,7 @@ struct BeamParams {
     float *cum_out;
     uint8_t *done_out;
     int *tickets;               // [n_groups], zero between launches
-    float2 *part_stat;          // [rows][splits]: reference R, sum of 2^(x log2 e - R)
+    float2 *part_stat;          // [rows][splits]: reference R, sum of 2^(x log2 e - 4 R)
     float *part_x;              // [rows][n_beams][splits] best logits, descending over places
     int32_t *part_v;            // and their tokens (-1: none)
 };
