@@ -29,6 +29,12 @@ def _torch_stream(stream):
     return torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream
 
 
+def _capturing(stream):
+    """Whether the call is being captured into a graph."""
+    with torch.cuda.stream(_torch_stream(stream)):
+        return torch.cuda.is_current_stream_capturing()
+
+
 class SfiState:
     def __init__(self, cfg, len0, device="cuda", page_table=None, n_pages=0, capacity=None):
         self.cfg = cfg
@@ -77,6 +83,7 @@ class SfiState:
         self.ws = torch.empty(self.ws_bytes, dtype=torch.uint8, device=self.device)
         sfi_workspace_init(self.ws, self.ws_bytes)
         self.t = 0
+        self._replayed = False      # a captured step may have advanced the lengths unseen
 
     # -- host bookkeeping -------------------------------------------------------------------
     def reset_lengths(self):
@@ -217,9 +224,18 @@ class SfiState:
                 self._pages_ok = torch.empty(self.cfg.batch, dtype=torch.uint8, device=self.device)
         return self._pool
 
-    def _bound(self):
-        """Host bound of every length, for the descriptor."""
-        self.kv.max_len = min(self.capacity, int(self.len0.max()) + self.t)
+    def _whole(self):
+        """The descriptor for calls that launch the same whatever the lengths are."""
+        self.kv.max_len = self.capacity
+        return self.kv
+
+    def _bound(self, stream):
+        """The descriptor with the host's bound of every length, by which a call is sized. A graph
+        is replayed at lengths that the host does not see: its calls, and all after it, are
+        sized by the capacity."""
+        self._replayed = self._replayed or _capturing(stream)
+        self.kv.max_len = (self.capacity if self._replayed else
+                           min(self.capacity, int(self.len0.max()) + self.t))
         return self.kv
 
     def reserve(self, n_new=None, active=None, ok=None, stream=None):
@@ -228,26 +244,26 @@ class SfiState:
         them, to be given as `active` to the calls that do."""
         pool = self.pool(stream)
         ok = self._pages_ok if ok is None else ok
-        sfi_pages_reserve(self._bound(), pool, n_new, self._pages_ws, self._pages_bytes,
+        sfi_pages_reserve(self._whole(), pool, n_new, self._pages_ws, self._pages_bytes,
                           active=active, ok=ok, stream=stream)
         return ok
 
     def evict(self, n_window=None, active=None, stream=None):
         """Give up the pages outside the sinks and the recent window."""
-        sfi_pages_evict(self._bound(), self.pool(stream), self.cfg.n_sink,
+        sfi_pages_evict(self._whole(), self.pool(stream), self.cfg.n_sink,
                         self.cfg.n_window if n_window is None else n_window, active=active,
                         stream=stream)
 
     def release(self, active=None, stream=None):
         """Give up all pages of the active sequences; their lengths become 0."""
-        sfi_pages_release(self._bound(), self.pool(stream), active=active, stream=stream)
+        sfi_pages_release(self._whole(), self.pool(stream), active=active, stream=stream)
 
     def compact_pages(self, stream=None):
         """Move the pages in use to the front of the pool; returns their number (device int32)."""
         pool = self.pool(stream)
         with torch.cuda.stream(_torch_stream(stream)):
             used = torch.empty(1, dtype=torch.int32, device=self.device)
-        sfi_pages_compact(self._bound(), pool, used, self._pages_ws, self._pages_bytes, stream=stream)
+        sfi_pages_compact(self._whole(), pool, used, self._pages_ws, self._pages_bytes, stream=stream)
         return used
 
     def prefill(self, q, k_new, v_new, rows, out, out_fp32=False, n_window=None, stream=None):
@@ -267,7 +283,7 @@ class SfiState:
             dev = torch.from_numpy(start).to(self.device)
             if self.page_table is not None:
                 active = self.reserve(torch.from_numpy(rows).to(self.device), stream=stream)
-        sfi_append_chunk(self._bound(), k_new, v_new, dev, n, most, active=active, stream=stream)
+        sfi_append_chunk(self._whole(), k_new, v_new, dev, n, most, active=active, stream=stream)
         self.len0 = self.len0 + rows
         self._window(q, out, out_fp32, dev, n, most, window, stream, active)
 
@@ -278,13 +294,13 @@ class SfiState:
         window = self.cfg.n_window if n_window is None else n_window
         if self.page_table is not None:
             active = self.reserve(active=active, stream=stream)
-        sfi_append_chunk(self._bound(), k_new, v_new, None, self.cfg.batch, 1, active=active,
+        sfi_append_chunk(self._whole(), k_new, v_new, None, self.cfg.batch, 1, active=active,
                          stream=stream)
         self.t += 1
         self._window(q, out, out_fp32, None, self.cfg.batch, 1, window, stream, active)
 
     def _window(self, q, out, out_fp32, start, n, most, window, stream, active=None):
-        kv = self._bound()
+        kv = self._bound(stream)
         need = sfi_window_workspace_bytes(kv, n, most, self.cfg.n_sink, window)
         if getattr(self, "_window_ws", None) is None or self._window_ws.numel() < need:
             with torch.cuda.stream(_torch_stream(stream)):
@@ -297,7 +313,7 @@ class SfiState:
         """Every sequence b takes over the state of sequence src[b] (device int32 [B]): table,
         length, packed memory. Forked sequences share their pages until they are reserved."""
         pool = self.pool(stream) if self.page_table is not None else None
-        sfi_reorder(self._bound(), src, pool=pool, budget=self.budget, mem=self.mem, stream=stream)
+        sfi_reorder(self._whole(), src, pool=pool, budget=self.budget, mem=self.mem, stream=stream)
         self.len0 = np.full_like(self.len0, self.len0.max())   # a bound; src stays on the device
 
 
