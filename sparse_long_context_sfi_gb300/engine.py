@@ -83,12 +83,21 @@ class SfiState:
         self.ws = torch.empty(self.ws_bytes, dtype=torch.uint8, device=self.device)
         sfi_workspace_init(self.ws, self.ws_bytes)
         self.t = 0
+        self._upto = self.len0.copy()   # host bound of every length (len0: the lengths at the start)
+        self._off_course = False    # lengths that are no longer len0 and the steps since
         self._replayed = False      # a captured step may have advanced the lengths unseen
 
     # -- host bookkeeping -------------------------------------------------------------------
     def reset_lengths(self):
+        """Every sequence at its length of the start again."""
         self.seq_len.copy_(torch.from_numpy(self.len0.astype(np.int32)))
+        self._upto = self.len0.copy()
+        self._off_course = False
         self.t = 0
+
+    def _grown(self, rows):
+        """The host's bounds after `rows` further rows (of each sequence, or of all)."""
+        self._upto = np.minimum(self._upto + rows, self.capacity)
 
     def schedule(self, masks: np.ndarray) -> np.ndarray:
         """Slow flags [steps][B] from per-sequence boundary masks [B][steps]."""
@@ -108,7 +117,7 @@ class SfiState:
         driver); otherwise every row is appended first and the fast step is
         sfi_sparse_decode_attn."""
         kv = self.kv
-        bound = int(self.len0.max()) + self.t
+        bound = int(self._upto.max())
         slow_b = np.asarray(slow_b, bool)
         mixed = slow_b.any() and not slow_b.all()
         if mixed:
@@ -136,6 +145,7 @@ class SfiState:
             else:
                 sfi_sparse_decode_attn(kv, self.mem, self.budget, q, out, out_fp32, self.ws,
                                        self.ws_bytes, active=a_fast, stream=stream)
+        self._grown(1)
         self.t += 1
         return mixed and (a_slow, a_fast)
 
@@ -184,7 +194,7 @@ class SfiState:
             v_new=v_new.data_ptr(), out=out.data_ptr(), out_fp32=1 if out_fp32 else 0,
             out_per_step=1 if out_per_step else 0, scores_f=self.scores.data_ptr(),
             masks=None if masks is None else masks.data_ptr(),
-            len_start=int(self.len0.max()) + t0, dense_only=1 if dense_only else 0)
+            len_start=int(self._upto.max() if self._off_course else self.len0.max() + t0), dense_only=1 if dense_only else 0)
         if pipeline or concurrent:
             side, fork, join = self.side_stream()
             plan.side_stream, plan.fork_event, plan.join_event = (side.cuda_stream, fork.cuda_event,
@@ -205,7 +215,18 @@ class SfiState:
         return plan
 
     def run(self, plan: SfiDecodePlan, stream=None):
+        """Issue a plan. Steps [t0, t1) start at the lengths of the start and t0 rows, or where
+        prompts, windowed steps and reordering have left the lengths since."""
+        steps = plan.n_steps
+        if self._off_course:
+            plan = SfiDecodePlan.from_buffer_copy(plan)     # (its arrays are the caller's)
+            plan.len_start = int(self._upto.max())
         sfi_decode_run(self.kv, self.budget, self.mem, plan, self.ws, self.ws_bytes, stream=stream)
+        if self._off_course:
+            self._grown(steps)
+        else:
+            at = self.len0 - self.len0.max() + plan.len_start + steps
+            self._upto = np.minimum(np.maximum(self._upto, at), self.capacity)
 
     # -- prompts, pages and beams ------------------------------------------------------------
     def pool(self, stream=None) -> SfiPagePool:
@@ -234,8 +255,7 @@ class SfiState:
         is replayed at lengths that the host does not see: its calls, and all after it, are
         sized by the capacity."""
         self._replayed = self._replayed or _capturing(stream)
-        self.kv.max_len = (self.capacity if self._replayed else
-                           min(self.capacity, int(self.len0.max()) + self.t))
+        self.kv.max_len = self.capacity if self._replayed else int(self._upto.max())
         return self.kv
 
     def reserve(self, n_new=None, active=None, ok=None, stream=None):
@@ -284,7 +304,8 @@ class SfiState:
             if self.page_table is not None:
                 active = self.reserve(torch.from_numpy(rows).to(self.device), stream=stream)
         sfi_append_chunk(self._whole(), k_new, v_new, dev, n, most, active=active, stream=stream)
-        self.len0 = self.len0 + rows
+        self._grown(rows)
+        self._off_course = True
         self._window(q, out, out_fp32, dev, n, most, window, stream, active)
 
     def window_step(self, q, k_new, v_new, out, out_fp32=True, n_window=None, active=None,
@@ -296,7 +317,8 @@ class SfiState:
             active = self.reserve(active=active, stream=stream)
         sfi_append_chunk(self._whole(), k_new, v_new, None, self.cfg.batch, 1, active=active,
                          stream=stream)
-        self.t += 1
+        self._grown(1)
+        self._off_course = True
         self._window(q, out, out_fp32, None, self.cfg.batch, 1, window, stream, active)
 
     def _window(self, q, out, out_fp32, start, n, most, window, stream, active=None):
@@ -314,7 +336,8 @@ class SfiState:
         length, packed memory. Forked sequences share their pages until they are reserved."""
         pool = self.pool(stream) if self.page_table is not None else None
         sfi_reorder(self._whole(), src, pool=pool, budget=self.budget, mem=self.mem, stream=stream)
-        self.len0 = np.full_like(self.len0, self.len0.max())   # a bound; src stays on the device
+        self._upto = np.full_like(self._upto, self._upto.max())     # (src stays on the device)
+        self._off_course = True
 
 
 class BeamSearch:

@@ -11,6 +11,48 @@ from tests.test_gpu_cache_run import D, Loop, built  # noqa: F401  (built: the m
 pytestmark = pytest.mark.gpu
 
 
+def forget(lp):
+    lp.k = [np.zeros((lp.layers, 2, 0, D)) for _ in range(lp.batch)]
+    lp.v = [np.zeros((lp.layers, 2, 0, D)) for _ in range(lp.batch)]
+
+
+def by_run(lp):
+    """The loop's slow and fast steps through make_plan and run."""
+    st = lp.st
+    st.step = lambda q, k, v, slow, out: st.run(st.make_plan(
+        np.asarray(slow, np.uint8)[None], q[None], k[None], v[None], out[None]))
+
+
+@pytest.mark.parametrize("paged", [False, True])
+def test_runs_between_the_other_calls(paged):
+    lp = Loop(paged)
+    by_run(lp)
+    lp.prefill([100, 40, 60, 77, 30, 50], 64)
+    lp.step("slow")
+    lp.step("window", window=48)
+    lp.step("fast")
+    lp.step("fast")
+    lp.step("window", window=48)
+    lp.prefill([10, 0, 1, 0, 33, 2], 64)
+    lp.reorder(torch.tensor([1, 1, 2, 0, 3, 3], dtype=torch.int32, device="cuda"))
+    for kind in ("slow", "fast", "window", "slow"):
+        lp.step(kind, window=48)
+
+
+@pytest.mark.parametrize("paged", [False, True])
+def test_reset_lengths_puts_back_the_first_lengths(paged):
+    lp = Loop(paged)
+    lp.prefill([100, 0, 0, 77, 0, 0], 64)
+    lp.reorder(torch.tensor([0, 0, 0, 3, 3, 3], dtype=torch.int32, device="cuda"))
+    lp.st.reset_lengths()
+    assert lp.st.seq_len.tolist() == [0] * 6
+    if paged:
+        lp.st.release()
+    forget(lp)
+    lp.prefill([10, 20, 30, 40, 50, 60], 64)
+    lp.step("slow")
+
+
 def test_a_captured_step_is_replayed_at_lengths_that_the_host_has_not_seen():
     """And so is the eager step behind it."""
     lp = Loop(True)
