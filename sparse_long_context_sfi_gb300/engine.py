@@ -31,6 +31,8 @@ def _torch_stream(stream):
 
 def _capturing(stream):
     """Whether the call is being captured into a graph."""
+    if stream is None:
+        return torch.cuda.is_current_stream_capturing()
     with torch.cuda.stream(_torch_stream(stream)):
         return torch.cuda.is_current_stream_capturing()
 
@@ -99,6 +101,20 @@ class SfiState:
         """The host's bounds after `rows` further rows (of each sequence, or of all)."""
         self._upto = np.minimum(self._upto + rows, self.capacity)
 
+    def _longest(self, more, stream):
+        """Host bound of every length before `more` further rows each. Where it would leave no room
+        for them the lengths themselves are read: which sequences a mask released, a reserve
+        refused or a map reordered is known to the device alone."""
+        capturing = _capturing(stream)
+        if self._off_course:
+            self._replayed = self._replayed or capturing
+        if self._replayed:
+            return self.capacity - more
+        if int(self._upto.max()) + more > self.capacity and not capturing:
+            with torch.cuda.stream(_torch_stream(stream)):
+                self._upto = self.seq_len.cpu().numpy().astype(np.int64)
+        return int(self._upto.max())
+
     def schedule(self, masks: np.ndarray) -> np.ndarray:
         """Slow flags [steps][B] from per-sequence boundary masks [B][steps]."""
         return np.stack([sfi_schedule(masks[b], self.cfg.t_max) for b in range(self.cfg.batch)], 1)
@@ -117,7 +133,7 @@ class SfiState:
         driver); otherwise every row is appended first and the fast step is
         sfi_sparse_decode_attn."""
         kv = self.kv
-        bound = int(self._upto.max())
+        bound = self._longest(1, stream)
         slow_b = np.asarray(slow_b, bool)
         mixed = slow_b.any() and not slow_b.all()
         if mixed:
@@ -146,6 +162,7 @@ class SfiState:
                 sfi_sparse_decode_attn(kv, self.mem, self.budget, q, out, out_fp32, self.ws,
                                        self.ws_bytes, active=a_fast, stream=stream)
         self._grown(1)
+        self._replayed = self._replayed or _capturing(stream)
         self.t += 1
         return mixed and (a_slow, a_fast)
 
@@ -220,7 +237,7 @@ class SfiState:
         steps = plan.n_steps
         if self._off_course:
             plan = SfiDecodePlan.from_buffer_copy(plan)     # (its arrays are the caller's)
-            plan.len_start = int(self._upto.max())
+            plan.len_start = self._longest(steps, stream)
         sfi_decode_run(self.kv, self.budget, self.mem, plan, self.ws, self.ws_bytes, stream=stream)
         if self._off_course:
             self._grown(steps)
@@ -277,6 +294,9 @@ class SfiState:
     def release(self, active=None, stream=None):
         """Give up all pages of the active sequences; their lengths become 0."""
         sfi_pages_release(self._whole(), self.pool(stream), active=active, stream=stream)
+        if active is None and not _capturing(stream):
+            self._upto = np.zeros_like(self._upto)
+        self._off_course = True
 
     def compact_pages(self, stream=None):
         """Move the pages in use to the front of the pool; returns their number (device int32)."""

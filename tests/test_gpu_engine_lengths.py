@@ -23,6 +23,30 @@ def by_run(lp):
         np.asarray(slow, np.uint8)[None], q[None], k[None], v[None], out[None]))
 
 
+@pytest.mark.parametrize("native", [False, True])
+def test_slots_are_used_again(native):
+    """Released sequences start over: more tokens in all than a slot holds (320)."""
+    lp = Loop(True)
+    if native:
+        by_run(lp)
+    for _ in range(4):
+        lp.prefill([180, 20, 33, 200, 40, 21], 64)
+        lp.step("slow")
+        lp.step("window", window=48)
+        lp.step("fast")
+        lp.st.release()
+        forget(lp)
+    # and some of them: the others go on
+    lp.prefill([30, 20, 30, 20, 30, 20], 64)
+    for t in range(8):
+        lp.prefill([50, 0, 50, 0, 50, 0], 64)
+        lp.step("slow" if t % 2 == 0 else "window", window=32)
+        mask = torch.tensor([1, 0, 1, 0, 1, 0], dtype=torch.uint8, device="cuda")
+        lp.st.release(active=mask)
+        for b in (0, 2, 4):
+            lp.k[b], lp.v[b] = (np.zeros((lp.layers, 2, 0, D)) for _ in "kv")
+
+
 @pytest.mark.parametrize("paged", [False, True])
 def test_runs_between_the_other_calls(paged):
     lp = Loop(paged)
@@ -72,3 +96,24 @@ def test_a_captured_step_is_replayed_at_lengths_that_the_host_has_not_seen():
     torch.cuda.synchronize()
     assert int(lp.st.err[0]) == 0 and lp.st.seq_len.tolist() == [k.shape[2] for k in lp.k]
     lp.step("window", window=200)
+    lp.step("slow")
+    lp.step("fast")
+    by_run(lp)
+    lp.step("slow")
+    lp.step("fast")
+
+
+def test_captured_release():
+    """A release that is only captured leaves the lengths, and their bounds, as they are."""
+    lp = Loop(True)
+    lp.prefill([60, 20, 30, 33, 40, 50], 64)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        lp.st.release()
+    lp.step("slow")
+    lp.step("fast")
+    graph.replay()
+    forget(lp)
+    lp.prefill([60, 20, 30, 33, 40, 50], 64)
+    lp.step("window", window=64)
+    lp.step("slow")
