@@ -37,6 +37,27 @@ def _capturing(stream):
         return torch.cuda.is_current_stream_capturing()
 
 
+class _Workspace:
+    """A workspace that calls of any shape share, one after the other. What a larger one replaces is
+    kept: a captured graph goes on using it. A capture that finds none has one to itself, for its
+    clearing is part of the graph and not done yet for anybody else."""
+
+    def __init__(self, device):
+        self.device, self.now, self.kept = device, None, []
+
+    def get(self, need, stream):
+        if self.now is not None and self.now.numel() >= need:
+            return self.now
+        size = need if self.now is None else max(need, 2 * self.now.numel())
+        with torch.cuda.stream(_torch_stream(stream)):
+            ws = torch.empty(size, dtype=torch.uint8, device=self.device)
+        sfi_workspace_init(ws, size, stream=stream)
+        self.kept.append(ws)
+        if not _capturing(stream):
+            self.now = ws
+        return ws
+
+
 class SfiState:
     def __init__(self, cfg, len0, device="cuda", page_table=None, n_pages=0, capacity=None):
         self.cfg = cfg
@@ -86,6 +107,7 @@ class SfiState:
         sfi_workspace_init(self.ws, self.ws_bytes)
         self.t = 0
         self._upto = self.len0.copy()   # host bound of every length (len0: the lengths at the start)
+        self._window_ws = _Workspace(self.device)
         self._off_course = False    # lengths that are no longer len0 and the steps since
         self._replayed = False      # a captured step may have advanced the lengths unseen
 
@@ -343,13 +365,9 @@ class SfiState:
 
     def _window(self, q, out, out_fp32, start, n, most, window, stream, active=None):
         kv = self._bound(stream)
-        need = sfi_window_workspace_bytes(kv, n, most, self.cfg.n_sink, window)
-        if getattr(self, "_window_ws", None) is None or self._window_ws.numel() < need:
-            with torch.cuda.stream(_torch_stream(stream)):
-                self._window_ws = torch.empty(need, dtype=torch.uint8, device=self.device)
-            sfi_workspace_init(self._window_ws, need, stream=stream)
-        sfi_window_attn(kv, q, out, out_fp32, start, n, most, self.cfg.n_sink, window,
-                        self._window_ws, self._window_ws.numel(), active=active, stream=stream)
+        ws = self._window_ws.get(sfi_window_workspace_bytes(kv, n, most, self.cfg.n_sink, window), stream)
+        sfi_window_attn(kv, q, out, out_fp32, start, n, most, self.cfg.n_sink, window, ws, ws.numel(),
+                        active=active, stream=stream)
 
     def reorder(self, src, stream=None):
         """Every sequence b takes over the state of sequence src[b] (device int32 [B]): table,
@@ -373,7 +391,7 @@ class BeamSearch:
         self.done = torch.zeros(rows, dtype=torch.uint8, **dev)
         self.parent = torch.zeros(rows, dtype=torch.int32, **dev)
         self.token = torch.zeros(rows, dtype=torch.int32, **dev)
-        self._ws = None
+        self._ws = _Workspace(self.cum.device)
 
     def select(self, logits, rank_scale=None, stream=None):
         """logits [rows][vocab] (bf16 or fp32, rows may be strided): keeps the best beams; returns
@@ -391,10 +409,6 @@ class BeamSearch:
             rank_scale=None if rank_scale is None else rank_scale.data_ptr(),
             parent=self.parent.data_ptr(), token=self.token.data_ptr(),
             cum_out=self.cum.data_ptr(), done_out=self.done.data_ptr())
-        need = sfi_beam_workspace_bytes(beam)
-        if self._ws is None or self._ws.numel() < need:
-            with torch.cuda.stream(_torch_stream(stream)):
-                self._ws = torch.empty(need, dtype=torch.uint8, device=self.cum.device)
-            sfi_workspace_init(self._ws, self._ws.numel(), stream=stream)
-        sfi_beam_select(beam, self._ws, self._ws.numel(), stream=stream)
+        ws = self._ws.get(sfi_beam_workspace_bytes(beam), stream)
+        sfi_beam_select(beam, ws, ws.numel(), stream=stream)
         return self.parent, self.token
