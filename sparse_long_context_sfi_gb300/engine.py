@@ -332,36 +332,54 @@ class SfiState:
         """One chunk of a prompt: rows[b] (host) new tokens of every sequence, packed in order of
         sequence. Reserves their pages (paged cache), appends k_new/v_new [Ly][n][Hkv][D] and
         attends q [Ly][n][Hq][D] under the sinks and a window of n_window (default: the
-        budget's) into out [Ly][n][Hq][D]. A sequence whose pages the pool does not cover is
-        left out (its rows of out, too), and the error word says so."""
+        budget's) into out [Ly][n][Hq][D]. A sequence that does not fit its capacity, or whose
+        pages the pool does not cover, is left out (its rows of out, too), and the error word
+        says so."""
         rows = np.asarray(rows, dtype=np.int32)
         start = np.concatenate([[0], np.cumsum(rows)]).astype(np.int32)
         n, most = int(q.shape[1]), int(rows.max())
         if n < start[-1] or tuple(out.shape) != tuple(q.shape):
             raise ValueError("q and out hold the rows of every sequence")
         window = self.cfg.n_window if n_window is None else n_window
-        active = None
         with torch.cuda.stream(_torch_stream(stream)):
             dev = torch.from_numpy(start).to(self.device)
             if self.page_table is not None:
-                active = self.reserve(torch.from_numpy(rows).to(self.device), stream=stream)
+                active = served = self.reserve(torch.from_numpy(rows).to(self.device), stream=stream)
+            else:
+                active, served = None, self._fitting(rows, None, stream)
         sfi_append_chunk(self._whole(), k_new, v_new, dev, n, most, active=active, stream=stream)
         self._grown(rows)
         self._off_course = True
-        self._window(q, out, out_fp32, dev, n, most, window, stream, active)
+        self._window(q, out, out_fp32, dev, n, most, window, stream, served)
 
     def window_step(self, q, k_new, v_new, out, out_fp32=True, n_window=None, active=None,
                     stream=None):
         """One new token each, attended under the sinks and a window straight from the cache (no
-        packed memory): q/out [Ly][B][Hq][D], k_new/v_new [Ly][B][Hkv][D]."""
+        packed memory): q/out [Ly][B][Hq][D], k_new/v_new [Ly][B][Hkv][D]. A sequence without
+        room is left out, as by prefill."""
         window = self.cfg.n_window if n_window is None else n_window
         if self.page_table is not None:
-            active = self.reserve(active=active, stream=stream)
+            active = served = self.reserve(active=active, stream=stream)
+        else:
+            served = self._fitting(1, active, stream)
         sfi_append_chunk(self._whole(), k_new, v_new, None, self.cfg.batch, 1, active=active,
                          stream=stream)
         self._grown(1)
         self._off_course = True
-        self._window(q, out, out_fp32, None, self.cfg.batch, 1, window, stream, active)
+        self._window(q, out, out_fp32, None, self.cfg.batch, 1, window, stream, served)
+
+    def _fitting(self, rows, active, stream):
+        """Which of the active sequences of a contiguous cache have room for `rows` more (host int or
+        [B]): what the append takes and the attention may look at. `active` itself where the
+        host's bounds say that all have."""
+        if not (self._replayed or _capturing(stream)) and (self._upto + rows).max() <= self.capacity:
+            return active
+        with torch.cuda.stream(_torch_stream(stream)):
+            more = rows if isinstance(rows, int) else torch.from_numpy(rows).to(self.device)
+            fits = self.seq_len + more <= self.capacity
+            if active is not None:
+                fits &= active != 0
+            return fits.view(torch.uint8)
 
     def _window(self, q, out, out_fp32, start, n, most, window, stream, active=None):
         kv = self._bound(stream)

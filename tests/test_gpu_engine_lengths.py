@@ -117,3 +117,54 @@ def test_captured_release():
     lp.prefill([60, 20, 30, 33, 40, 50], 64)
     lp.step("window", window=64)
     lp.step("slow")
+
+
+@pytest.mark.parametrize("out_fp32", [False, True])
+def test_a_full_sequence_is_left_out(out_fp32):
+    """A contiguous cache: what does not fit its capacity is not attended either; the others are."""
+    lp = Loop(False)
+    lp.prefill([320, 0, 0, 100, 318, 0], 64)
+    st = lp.st
+    dt = torch.float32 if out_fp32 else torch.bfloat16
+    q, k, v = lp.rnd(2, 10, 8, D), lp.rnd(2, 10, 2, D), lp.rnd(2, 10, 2, D)
+    out = torch.full((2, 10, 8, D), -7.0, dtype=dt, device="cuda")
+    st.prefill(q, k, v, [1, 0, 0, 5, 3, 0], out, out_fp32=out_fp32, n_window=64)
+    torch.cuda.synchronize()
+    assert int(st.err[0]) == sfi.SFI_DEVERR_CAPACITY
+    assert st.seq_len.tolist() == [320, 0, 0, 105, 318, 0]
+    assert (out[:, 0] == -7.0).all() and (out[:, 6:] == -7.0).all()
+    assert (out[:, 1:6] != -7.0).any(-1).all()
+    q, k, v = lp.rnd(2, 6, 8, D), lp.rnd(2, 6, 2, D), lp.rnd(2, 6, 2, D)
+    for mask in (None, [1, 1, 0, 1, 1, 0]):
+        out = torch.full((2, 6, 8, D), -7.0, dtype=dt, device="cuda")
+        before = st.seq_len.tolist()
+        st.err.zero_()
+        st.window_step(q, k, v, out, out_fp32=out_fp32, n_window=64,
+                       active=None if mask is None else torch.tensor(mask, dtype=torch.uint8, device="cuda"))
+        torch.cuda.synchronize()
+        assert int(st.err[0]) == sfi.SFI_DEVERR_CAPACITY
+        on = [b for b in range(6) if b != 0 and (mask is None or mask[b])]
+        assert st.seq_len.tolist() == [n + (b in on) for b, n in enumerate(before)]
+        for b in range(6):
+            assert (out[:, b] != -7.0).any(-1).all() if b in on else (out[:, b] == -7.0).all()
+
+
+def test_a_sequence_that_fills_up_in_a_replayed_step():
+    """The replays beyond its capacity leave the full sequence's output alone and serve the others."""
+    lp = Loop(False)
+    lp.prefill([318, 20, 1, 33, 40, 50], 64)
+    q, kv = lp.rnd(2, 6, 8, D), lp.rnd(2, 6, 2, D)
+    out = torch.zeros((2, 6, 8, D), device="cuda")
+    lp.st.window_step(q, kv, kv, out, n_window=64)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        lp.st.window_step(q, kv, kv, out, n_window=64)
+    for t in range(3):
+        out.fill_(-7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert int(lp.st.err[0]) == (sfi.SFI_DEVERR_CAPACITY if t else 0)
+        assert lp.st.seq_len.tolist() == [320] + [n + 2 + t for n in (20, 1, 33, 40, 50)]
+        assert (out[:, 0] == -7.0).all() if t else (out[:, 0] != -7.0).any()
+        assert (out[:, 1:] != -7.0).any(-1).all()
