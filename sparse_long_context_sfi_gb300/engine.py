@@ -149,23 +149,34 @@ class SfiState:
 
     # -- one decode step through the individual calls -----------------------------------------
     def step(self, q, k_new, v_new, slow_b: np.ndarray, out, out_fp32=True, stream=None,
-             fused=True):
+             fused=True, active=None):
         """q [Ly][B][Hq][D] bf16, k_new/v_new [Ly][B][Hkv][D] bf16 (device); slow_b [B] bool.
         fused: the fast sequences' append runs inside sfi_fast_decode_step (as in the native
         driver); otherwise every row is appended first and the fast step is
-        sfi_sparse_decode_attn."""
+        sfi_sparse_decode_attn. active: device uint8 [B], e.g. from reserve: the others are left as
+        they are (their rows of out, too)."""
+        return self._step(q, k_new, v_new, slow_b, None, active, out, out_fp32, stream, fused)
+
+    def _step(self, q, k_new, v_new, slow_b, masks, active, out, out_fp32, stream, fused):
+        """masks: slow_b and its complement on the device, if they are there already."""
         kv = self.kv
         bound = self._longest(1, stream)
         slow_b = np.asarray(slow_b, bool)
         mixed = slow_b.any() and not slow_b.all()
+        a_slow = a_fast = active
+        if active is not None:
+            bound = min(bound, self.capacity - 1)       # (what is full is not active)
         if mixed:
-            m = torch.from_numpy(np.stack([slow_b, ~slow_b]).astype(np.uint8)).to(self.device)
+            m = masks
+            if m is None:
+                m = torch.from_numpy(np.stack([slow_b, ~slow_b]).astype(np.uint8)).to(self.device)
+            if active is not None:
+                with torch.cuda.stream(_torch_stream(stream)):
+                    m = ((m != 0) & (active != 0)).view(torch.uint8)
             a_slow, a_fast = m[0], m[1]
-        else:
-            a_slow = a_fast = None
         kv.max_len = bound
         if not fused:
-            sfi_append_kv(kv, k_new, v_new, stream=stream)
+            sfi_append_kv(kv, k_new, v_new, active=active, stream=stream)
         elif slow_b.any():
             sfi_append_kv(kv, k_new, v_new, active=a_slow, stream=stream)
         kv.max_len = bound + 1
@@ -183,10 +194,13 @@ class SfiState:
             else:
                 sfi_sparse_decode_attn(kv, self.mem, self.budget, q, out, out_fp32, self.ws,
                                        self.ws_bytes, active=a_fast, stream=stream)
+        self._stepped(stream)
+        return mixed and (a_slow, a_fast)
+
+    def _stepped(self, stream):
         self._grown(1)
         self._replayed = self._replayed or _capturing(stream)
         self.t += 1
-        return mixed and (a_slow, a_fast)
 
     # -- a whole run through the native driver --------------------------------------------------
     def side_stream(self, priority=0):
@@ -253,9 +267,13 @@ class SfiState:
         plan._keep = (slow, masks, q, k_new, v_new, out, ev_arr, events)
         return plan
 
-    def run(self, plan: SfiDecodePlan, stream=None):
+    def run(self, plan: SfiDecodePlan, stream=None, active=None):
         """Issue a plan. Steps [t0, t1) start at the lengths of the start and t0 rows, or where
-        prompts, windowed steps and reordering have left the lengths since."""
+        prompts, windowed steps and reordering have left the lengths since. active (device uint8
+        [B], for all steps; not with events): the other sequences are left as they are; the steps
+        are then issued one by one, on `stream` alone."""
+        if active is not None:
+            return self._run_active(plan, active, stream)
         steps = plan.n_steps
         if self._off_course:
             plan = SfiDecodePlan.from_buffer_copy(plan)     # (its arrays are the caller's)
@@ -266,6 +284,24 @@ class SfiState:
         else:
             at = self.len0 - self.len0.max() + plan.len_start + steps
             self._upto = np.minimum(np.maximum(self._upto, at), self.capacity)
+
+    def _run_active(self, plan, active, stream):
+        slow, masks, q, k_new, v_new, out, _, events = plan._keep
+        if events is not None:
+            raise ValueError("a plan with events runs with all sequences")
+        out_fp32 = bool(plan.out_fp32)
+        for t in range(plan.n_steps):
+            o = out[t] if plan.out_per_step else out
+            if not plan.dense_only:
+                self._step(q[t], k_new[t], v_new[t], slow[t], None if masks is None else masks[t], active,
+                           o, out_fp32, stream, True)
+                continue
+            self.kv.max_len = min(self._longest(1, stream), self.capacity - 1)
+            sfi_append_kv(self.kv, k_new[t], v_new[t], active=active, stream=stream)
+            self.kv.max_len += 1
+            sfi_dense_decode_attn(self.kv, q[t], o, out_fp32, None, self.ws, self.ws_bytes, active=active,
+                                  stream=stream)
+            self._stepped(stream)
 
     # -- prompts, pages and beams ------------------------------------------------------------
     def pool(self, stream=None) -> SfiPagePool:
