@@ -29,6 +29,20 @@ def _torch_stream(stream):
     return torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream
 
 
+def _want(name, t, dtypes, shape, device):
+    """Refuses a tensor that the kernels, which get its address alone, would read or write wrongly."""
+    dtypes = dtypes if isinstance(dtypes, tuple) else (dtypes,)
+    if (not isinstance(t, torch.Tensor) or t.dtype not in dtypes or tuple(t.shape) != tuple(shape) or
+            not t.is_contiguous() or t.device.type != device.type or
+            (device.index is not None and t.device.index != device.index)):
+        have = (f"{t.dtype} {tuple(t.shape)} on {t.device}" if isinstance(t, torch.Tensor) else type(t).__name__)
+        raise ValueError(f"{name}: contiguous {' or '.join(map(str, dtypes))} {tuple(shape)} on {device}"
+                         f" wanted, not {have}")
+
+
+_MASK = (torch.uint8, torch.bool)
+
+
 def _capturing(stream):
     """Whether the call is being captured into a graph."""
     if stream is None:
@@ -164,6 +178,7 @@ class SfiState:
         slow_b = np.asarray(slow_b, bool)
         mixed = slow_b.any() and not slow_b.all()
         a_slow = a_fast = active
+        self._masked(active)
         if active is not None:
             bound = min(bound, self.capacity - 1)       # (what is full is not active)
         if mixed:
@@ -289,6 +304,7 @@ class SfiState:
         slow, masks, q, k_new, v_new, out, _, events = plan._keep
         if events is not None:
             raise ValueError("a plan with events runs with all sequences")
+        self._masked(active)
         out_fp32 = bool(plan.out_fp32)
         for t in range(plan.n_steps):
             o = out[t] if plan.out_per_step else out
@@ -337,6 +353,11 @@ class SfiState:
         """Pages for the next n_new[b] positions (device int32 [B]; None: one each). Returns `ok`
         (device uint8 [B], its own unless given): 1 for the active sequences that may write
         them, to be given as `active` to the calls that do."""
+        self._masked(active)
+        if n_new is not None:
+            _want("n_new", n_new, torch.int32, (self.cfg.batch,), self.device)
+        if ok is not None:
+            _want("ok", ok, torch.uint8, (self.cfg.batch,), self.device)
         pool = self.pool(stream)
         ok = self._pages_ok if ok is None else ok
         sfi_pages_reserve(self._whole(), pool, n_new, self._pages_ws, self._pages_bytes,
@@ -345,12 +366,14 @@ class SfiState:
 
     def evict(self, n_window=None, active=None, stream=None):
         """Give up the pages outside the sinks and the recent window."""
+        self._masked(active)
         sfi_pages_evict(self._whole(), self.pool(stream), self.cfg.n_sink,
                         self.cfg.n_window if n_window is None else n_window, active=active,
                         stream=stream)
 
     def release(self, active=None, stream=None):
         """Give up all pages of the active sequences; their lengths become 0."""
+        self._masked(active)
         sfi_pages_release(self._whole(), self.pool(stream), active=active, stream=stream)
         if active is None and not _capturing(stream):
             self._upto = np.zeros_like(self._upto)
@@ -372,10 +395,13 @@ class SfiState:
         pages the pool does not cover, is left out (its rows of out, too), and the error word
         says so."""
         rows = np.asarray(rows, dtype=np.int32)
+        if rows.shape != (self.cfg.batch,) or (rows < 0).any() or q.dim() != 4:
+            raise ValueError("rows: a count for every sequence; q: [Ly][n][Hq][D]")
         start = np.concatenate([[0], np.cumsum(rows)]).astype(np.int32)
         n, most = int(q.shape[1]), int(rows.max())
         if n < start[-1] or tuple(out.shape) != tuple(q.shape):
             raise ValueError("q and out hold the rows of every sequence")
+        self._chunk(n, q, k_new, v_new, out, out_fp32)
         window = self.cfg.n_window if n_window is None else n_window
         with torch.cuda.stream(_torch_stream(stream)):
             dev = torch.from_numpy(start).to(self.device)
@@ -394,6 +420,8 @@ class SfiState:
         packed memory): q/out [Ly][B][Hq][D], k_new/v_new [Ly][B][Hkv][D]. A sequence without
         room is left out, as by prefill."""
         window = self.cfg.n_window if n_window is None else n_window
+        self._masked(active)
+        self._chunk(self.cfg.batch, q, k_new, v_new, out, out_fp32)
         if self.page_table is not None:
             active = served = self.reserve(active=active, stream=stream)
         else:
@@ -403,6 +431,18 @@ class SfiState:
         self._grown(1)
         self._off_course = True
         self._window(q, out, out_fp32, None, self.cfg.batch, 1, window, stream, served)
+
+    def _masked(self, active):
+        if active is not None:
+            _want("active", active, _MASK, (self.cfg.batch,), self.device)
+
+    def _chunk(self, n, q, k_new, v_new, out, out_fp32):
+        """The arrays of a chunk of n rows."""
+        c, dev = self.cfg, self.device
+        _want("q", q, torch.bfloat16, (c.n_layers, n, c.n_q_heads, c.head_dim), dev)
+        _want("k_new", k_new, torch.bfloat16, (c.n_layers, n, c.n_kv_heads, c.head_dim), dev)
+        _want("v_new", v_new, torch.bfloat16, (c.n_layers, n, c.n_kv_heads, c.head_dim), dev)
+        _want("out", out, torch.float32 if out_fp32 else torch.bfloat16, q.shape, dev)
 
     def _fitting(self, rows, active, stream):
         """Which of the active sequences of a contiguous cache have room for `rows` more (host int or
@@ -426,6 +466,7 @@ class SfiState:
     def reorder(self, src, stream=None):
         """Every sequence b takes over the state of sequence src[b] (device int32 [B]): table,
         length, packed memory. Forked sequences share their pages until they are reserved."""
+        _want("src", src, torch.int32, (self.cfg.batch,), self.device)
         pool = self.pool(stream) if self.page_table is not None else None
         sfi_reorder(self._whole(), src, pool=pool, budget=self.budget, mem=self.mem, stream=stream)
         self._upto = np.full_like(self._upto, self._upto.max())     # (src stays on the device)
@@ -455,6 +496,10 @@ class BeamSearch:
             raise ValueError("logits are [rows][vocab] with contiguous rows")
         if logits.dtype not in (torch.bfloat16, torch.float32):
             raise ValueError("logits are bf16 or fp32")
+        if logits.device != self.cum.device:
+            raise ValueError(f"logits are on {logits.device}, the beams on {self.cum.device}")
+        if rank_scale is not None:
+            _want("rank_scale", rank_scale, torch.float32, self.cum.shape, self.cum.device)
         beam = SfiBeam(
             n_groups=self.n_groups, n_beams=self.n_beams, vocab=self.vocab,
             logits_fp32=1 if logits.dtype == torch.float32 else 0, row_stride=logits.stride(0),
