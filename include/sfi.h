@@ -482,8 +482,10 @@ sfi_status sfi_append_chunk(const sfi_kv_cache *kv, const void *k_new, const voi
  * missing, their contents may be anything); a V row that some row attends to has to be finite,
  * because its neighbours in the chunk meet it with a weight of zero. A K row that is not a
  * number makes the rows that attend to it NaN, and no others. Softmax weights
- * enter the product with V as bf16, with out_fp32 in three bf16 parts (24 bits). n_sink >= 0,
- * n_window >= 1. A sequence longer than max_len, or with more rows than its length, is skipped
+ * enter the product with V in bf16 parts: with out_fp32 three (24 bits), else two (16 bits) in
+ * calls of at most 16 / group rows per sequence (max_rows), as in the decode steps, and one in
+ * calls of more: bf16 outputs are then off by up to 2^-8 sum_j w_j |v_j| beside their own rounding.
+ * n_sink >= 0, n_window >= 1. A sequence longer than max_len, or with more rows than its length, is skipped
  * (SFI_DEVERR_LENGTH).
  *   ws   workspace of at least sfi_window_workspace_bytes(), 256-byte aligned and initialised
  *        (sfi_workspace_init, once); calls of any shape may share it, but must not overlap.

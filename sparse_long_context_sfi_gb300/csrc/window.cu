@@ -402,13 +402,18 @@ constexpr int window_smem() { return 1024 + NQ * QR * 256 + ST * KT * 512 + stat
 // buffers per q tile. QR 16 is for single tokens: the MMA still takes 128 rows, of which all
 // but the first 16 are whatever lies behind them in shared memory; they end in rows of S and O
 // that nobody reads, and the memory holds a third stage instead.
-// F32 (fp32 outputs): the weights enter the product with V in three bf16 parts, 24 bits, and O
-// is moved every kFlush tiles to a second accumulator M with ordinary additions: the tensor
-// core's own additions do not round to nearest, and 520 of them in a row (two parts, a window of
-// 4096) had left outputs 1.0e-5 off (2-norm). Tensor memory then holds one CTA per SM. A bf16
-// output rounds at 2^-8 and needs neither.
+// PARTS: the bf16 parts in which a weight enters the product with V. Single tokens have two, 16
+// bits, as in the decode kernels (one token of 32 sequences under a window of 4096: 92 us, with one
+// part 87): an output near zero is then off by its own rounding alone. In a chunk's bf16 outputs
+// the second part costs more than it gives: four 32K prompts under a window of 64 take 518 us with
+// it and 446 without, an 8K chunk under 4096 617 and 412, and the error (2-norm) falls from 2.3e-3 to
+// the output's own rounding, 1.7e-3; fp32 outputs are there for who needs more.
+// F32 (fp32 outputs): three parts, 24 bits, and O is moved every kFlush tiles to a second
+// accumulator M with ordinary additions: the tensor core's own additions do not round to nearest,
+// and 520 of them in a row (two parts, a window of 4096) had left outputs 1.0e-5 off (2-norm). Tensor
+// memory then holds one CTA per SM. A bf16 output rounds at 2^-8 and does not need M.
 // SPLIT: an item's keys over several CTAs (the joining code costs registers).
-template <int NQ, int KT, int ST, int NS, int QR, bool F32, bool SPLIT>
+template <int NQ, int KT, int ST, int NS, int QR, int PARTS, bool F32, bool SPLIT>
 __global__ void __launch_bounds__(128 + 128 * NQ, NQ == 1 && !F32 ? 2 : 1)
     window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                   const __grid_constant__ CUtensorMap tm_q, const WindowParams p)
@@ -420,6 +425,7 @@ __global__ void __launch_bounds__(128 + 128 * NQ, NQ == 1 && !F32 ? 2 : 1)
     constexpr int NH = NS == 1 ? 2 : 1;     // parts in which a tile's weights are handed over
     static_assert(NQ * kQTile <= static_cast<int>(kCols) && ST <= kMaxStages && NS <= 2);
     static_assert(!F32 || NQ == 1);
+    static_assert((PARTS == 3) == F32 && PARTS >= 1 && PARTS <= 3);
     extern __shared__ uint8_t raw[];
     uint8_t *smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
     uint8_t *kv_smem = smem + NQ * 2 * kHalfQ;
@@ -792,9 +798,9 @@ __global__ void __launch_bounds__(128 + 128 * NQ, NQ == 1 && !F32 ? 2 : 1)
                 const float off = m == -CUDART_INF_F ? 0.f : -m * sc;
                 const uint64_t sc2 = pack2(sc, sc), off2 = pack2(off, off);
                 uint64_t sum = 0;
-                // Weights of chunk q over the first 16 columns of its scores; with F32 their remainders
-                // over the other 16, and what those leave behind the scores. (Stores of 16 columns: with 8 the 8K chunk under a window of 4096 took
-                // 417 us, with 16 397, with 32 no less.)
+                // Weights of chunk q over the first 16 columns of its scores; their remainders over the
+                // other 16, and what those leave behind the scores. (Stores of 16 columns: with 8 the
+                // 8K chunk under a window of 4096 took 417 us, with 16 397, with 32 no less.)
 #pragma unroll
                 for (int q = 0; q < kC; ++q) {
                     float *v = s + 32 * (q & 1);
@@ -803,11 +809,11 @@ __global__ void __launch_bounds__(128 + 128 * NQ, NQ == 1 && !F32 ? 2 : 1)
                         if (!whole)
                             mask(v, q);
                     }
-                    uint32_t w[16], r[F32 ? 16 : 1], r2[F32 ? 16 : 1];
+                    uint32_t w[16], r[PARTS > 1 ? 16 : 1], r2[PARTS > 2 ? 16 : 1];
                     if ((hidden >> q) & 1u) {
 #pragma unroll
                         for (int x = 0; x < 16; ++x)
-                            w[x] = r[F32 ? x : 0] = r2[F32 ? x : 0] = 0u;
+                            w[x] = r[PARTS > 1 ? x : 0] = r2[PARTS > 2 ? x : 0] = 0u;
                     } else {
 #pragma unroll
                         for (int x = 0; x < 16; ++x) {
@@ -816,15 +822,17 @@ __global__ void __launch_bounds__(128 + 128 * NQ, NQ == 1 && !F32 ? 2 : 1)
                             sum = add2(sum, pack2(p0, p1));
                             const __nv_bfloat162 hi = __floats2bfloat162_rn(p0, p1);
                             w[x] = *reinterpret_cast<const uint32_t *>(&hi);
-                            if (F32) {
-                                // (both differences are exact)
+                            if (PARTS > 1) {
+                                // (the differences are exact)
                                 const float2 b = __bfloat1622float2(hi);
                                 const float d0 = p0 - b.x, d1 = p1 - b.y;
                                 const __nv_bfloat162 lo = __floats2bfloat162_rn(d0, d1);
-                                const float2 e = __bfloat1622float2(lo);
-                                const __nv_bfloat162 rest = __floats2bfloat162_rn(d0 - e.x, d1 - e.y);
-                                r[F32 ? x : 0] = *reinterpret_cast<const uint32_t *>(&lo);
-                                r2[F32 ? x : 0] = *reinterpret_cast<const uint32_t *>(&rest);
+                                r[PARTS > 1 ? x : 0] = *reinterpret_cast<const uint32_t *>(&lo);
+                                if (PARTS > 2) {
+                                    const float2 e = __bfloat1622float2(lo);
+                                    const __nv_bfloat162 rest = __floats2bfloat162_rn(d0 - e.x, d1 - e.y);
+                                    r2[PARTS > 2 ? x : 0] = *reinterpret_cast<const uint32_t *>(&rest);
+                                }
                             }
                         }
                     }
@@ -838,10 +846,10 @@ __global__ void __launch_bounds__(128 + 128 * NQ, NQ == 1 && !F32 ? 2 : 1)
                             mbar_arrive(&c.pf[a][0]);
                     }
                     tmem_st16(sa + 32 * q, w);
-                    if (F32) {
+                    if (PARTS > 1)
                         tmem_st16(sa + 32 * q + 16, r);
+                    if (PARTS > 2)
                         tmem_st16(sa + KT + 16 * q, r2);
-                    }
                     if (q + 2 < kC)
                         tmem_ld32(sa + 32 * q + 64, v);
                 }
@@ -990,7 +998,7 @@ __global__ void __launch_bounds__(128 + 128 * NQ, NQ == 1 && !F32 ? 2 : 1)
                 const uint64_t dv = dv0 + st * (kStage / 16);
                 const uint32_t d = tm + A * kQTile + NS * kSW, w = tm + A * kQTile + buf * kSW;
 #pragma unroll
-                for (int part = 0; part < (F32 ? 3 : 1); ++part)
+                for (int part = 0; part < PARTS; ++part)
 #pragma unroll
                     for (int k2 = 0; k2 < kBlocks / NH; ++k2) {
                         const int kk = half * (kBlocks / NH) + k2;
@@ -1129,11 +1137,11 @@ __global__ void __launch_bounds__(128 + 128 * NQ, NQ == 1 && !F32 ? 2 : 1)
     }
 }
 
-template <int NQ, int KT, int ST, int NS, int QR, bool F32, bool SPLIT>
+template <int NQ, int KT, int ST, int NS, int QR, int PARTS, bool F32, bool SPLIT>
 cudaError_t launch_one(const WindowParams &p, const CUtensorMap &tm_k, const CUtensorMap &tm_v,
                        const CUtensorMap &tm_q, int grid, cudaStream_t stream)
 {
-    auto *kern = window_kernel<NQ, KT, ST, NS, QR, F32, SPLIT>;
+    auto *kern = window_kernel<NQ, KT, ST, NS, QR, PARTS, F32, SPLIT>;
     constexpr int smem = window_smem<NQ, KT, ST, QR>();
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e == cudaSuccess)
@@ -1141,12 +1149,12 @@ cudaError_t launch_one(const WindowParams &p, const CUtensorMap &tm_k, const CUt
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-template <int NQ, int KT, int ST, int NS, int QR, bool F32>
+template <int NQ, int KT, int ST, int NS, int QR, int PARTS, bool F32>
 cudaError_t launch_form(const WindowParams &p, const CUtensorMap &tm_k, const CUtensorMap &tm_v,
                         const CUtensorMap &tm_q, int grid, cudaStream_t stream)
 {
-    return p.n_split > 1 ? launch_one<NQ, KT, ST, NS, QR, F32, true>(p, tm_k, tm_v, tm_q, grid, stream)
-                         : launch_one<NQ, KT, ST, NS, QR, F32, false>(p, tm_k, tm_v, tm_q, grid, stream);
+    return p.n_split > 1 ? launch_one<NQ, KT, ST, NS, QR, PARTS, F32, true>(p, tm_k, tm_v, tm_q, grid, stream)
+                         : launch_one<NQ, KT, ST, NS, QR, PARTS, F32, false>(p, tm_k, tm_v, tm_q, grid, stream);
 }
 
 }  // namespace
@@ -1156,12 +1164,12 @@ cudaError_t launch_window(const WindowParams &p, int rows, const CUtensorMap &tm
                           cudaStream_t stream)
 {
     if (rows == 256)        // (bf16 outputs only)
-        return launch_form<2, 128, 2, 1, 128, false>(p, tm_k, tm_v, tm_q, grid, stream);
+        return launch_form<2, 128, 2, 1, 128, 1, false>(p, tm_k, tm_v, tm_q, grid, stream);
     if (rows == 16)
-        return p.out_fp32 ? launch_form<1, 64, 4, 2, 16, true>(p, tm_k, tm_v, tm_q, grid, stream)
-                          : launch_form<1, 64, 3, 2, 16, false>(p, tm_k, tm_v, tm_q, grid, stream);
-    return p.out_fp32 ? launch_form<1, 64, 4, 2, 128, true>(p, tm_k, tm_v, tm_q, grid, stream)
-                      : launch_form<1, 64, 2, 2, 128, false>(p, tm_k, tm_v, tm_q, grid, stream);
+        return p.out_fp32 ? launch_form<1, 64, 4, 2, 16, 3, true>(p, tm_k, tm_v, tm_q, grid, stream)
+                          : launch_form<1, 64, 3, 2, 16, 2, false>(p, tm_k, tm_v, tm_q, grid, stream);
+    return p.out_fp32 ? launch_form<1, 64, 4, 2, 128, 3, true>(p, tm_k, tm_v, tm_q, grid, stream)
+                      : launch_form<1, 64, 2, 2, 128, 1, false>(p, tm_k, tm_v, tm_q, grid, stream);
 }
 
 }  // namespace sfi

@@ -1,7 +1,10 @@
-"""Windowed attention where values go to the edge: keys that are not numbers."""
+"""Windowed attention where values go to the edge: keys that are not numbers, weights that nearly
+cancel."""
+import numpy as np
 import pytest
 import torch
 
+from tests.cache_model import window_attention
 from tests.test_gpu_window import NAN, Case, built  # noqa: F401  (built: the module's fixture)
 
 pytestmark = pytest.mark.gpu
@@ -31,3 +34,22 @@ def test_nan_key_shows_in_the_rows_that_see_it(at, window, paged, fp32):
         assert torch.isnan(out[4:]).all() if s else torch.equal(c.out[0, row, 4:], clean[0, row, 4:]), row
         assert torch.equal(c.out[0, row, :4], clean[0, row, :4]), row
     assert any(seen)
+
+
+@pytest.mark.parametrize("paged", [False, True])
+@pytest.mark.parametrize("group,rows", [(1, 1), (1, 16), (2, 5), (4, 1), (4, 4), (8, 2)])
+@pytest.mark.parametrize("window", [16, 300, 4096])
+def test_bf16_outputs_of_few_rows_round_once(group, rows, window, paged):
+    """Items of up to 16 operand rows hold their weights in two bf16 parts: half a step of the first,
+    2^-8, and of the second, 2^-8 of that, leave 2^-16, which the 1e-4 of fp32 outputs covers;
+    beside it an output is off by its own rounding, half a step of 2^-8, and no more."""
+    lens = [4001, rows, 16, 2500, 127, 129]
+    c = Case(lens, [rows] * len(lens), 2 * group, 2, paged=paged, seed=rows)
+    c.run(4, window, False)
+    torch.cuda.synchronize()
+    got = c.out.double().cpu().numpy()
+    q, k, v = (t.double().cpu().numpy() for t in (c.q, c.flat_k, c.flat_v))
+    for b, n in enumerate(lens):
+        r0, r1 = c.starts[b], c.starts[b + 1]
+        o, mag = window_attention(q[0, r0:r1], k[0, b, :, :n], v[0, b, :, :n], n, 4, window)
+        assert (np.abs(got[0, r0:r1] - o) <= 1e-4 * mag + 2.0 ** -8 * np.abs(o)).all(), b
