@@ -33,14 +33,26 @@ def _want(name, t, dtypes, shape, device):
     """Refuses a tensor that the kernels, which get its address alone, would read or write wrongly."""
     dtypes = dtypes if isinstance(dtypes, tuple) else (dtypes,)
     if (not isinstance(t, torch.Tensor) or t.dtype not in dtypes or tuple(t.shape) != tuple(shape) or
-            not t.is_contiguous() or t.device.type != device.type or
-            (device.index is not None and t.device.index != device.index)):
+            not t.is_contiguous() or t.device != device):
         have = (f"{t.dtype} {tuple(t.shape)} on {t.device}" if isinstance(t, torch.Tensor) else type(t).__name__)
         raise ValueError(f"{name}: contiguous {' or '.join(map(str, dtypes))} {tuple(shape)} on {device}"
                          f" wanted, not {have}")
 
 
 _MASK = (torch.uint8, torch.bool)
+
+
+def _at(device):
+    """`device` with its number: a kernel runs on the current device, whatever its arrays are on."""
+    device = torch.device(device)
+    if device.type == "cuda" and device.index is None:
+        device = torch.device("cuda", torch.cuda.current_device())
+    return device
+
+
+def _here(device):
+    if device.type == "cuda" and device.index != torch.cuda.current_device():
+        raise ValueError(f"the state is on {device}, which is not the current device")
 
 
 def _capturing(stream):
@@ -75,7 +87,7 @@ class _Workspace:
 class SfiState:
     def __init__(self, cfg, len0, device="cuda", page_table=None, n_pages=0, capacity=None):
         self.cfg = cfg
-        self.device = torch.device(device)
+        self.device = _at(device)
         B, Ly, Hkv, Hq, D = cfg.batch, cfg.n_layers, cfg.n_kv_heads, cfg.n_q_heads, cfg.head_dim
         self.len0 = np.asarray(len0, dtype=np.int64)
         self.capacity = capacity or int(self.len0.max()) + cfg.steps
@@ -173,6 +185,7 @@ class SfiState:
 
     def _step(self, q, k_new, v_new, slow_b, masks, active, out, out_fp32, stream, fused):
         """masks: slow_b and its complement on the device, if they are there already."""
+        _here(self.device)
         kv = self.kv
         bound = self._longest(1, stream)
         slow_b = np.asarray(slow_b, bool)
@@ -289,6 +302,7 @@ class SfiState:
         are then issued one by one, on `stream` alone."""
         if active is not None:
             return self._run_active(plan, active, stream)
+        _here(self.device)
         steps = plan.n_steps
         if self._off_course:
             plan = SfiDecodePlan.from_buffer_copy(plan)     # (its arrays are the caller's)
@@ -323,6 +337,7 @@ class SfiState:
     def pool(self, stream=None) -> SfiPagePool:
         """The page pool behind the table (made on first use: every entry the table holds then
         counts as one reference)."""
+        _here(self.device)
         if getattr(self, "_pool", None) is None:
             if self.page_table is None:
                 raise ValueError("a contiguous cache has no pages")
@@ -338,6 +353,7 @@ class SfiState:
 
     def _whole(self):
         """The descriptor for calls that launch the same whatever the lengths are."""
+        _here(self.device)
         self.kv.max_len = self.capacity
         return self.kv
 
@@ -393,7 +409,7 @@ class SfiState:
         attends q [Ly][n][Hq][D] under the sinks and a window of n_window (default: the
         budget's) into out [Ly][n][Hq][D]. A sequence that does not fit its capacity, or whose
         pages the pool does not cover, is left out (its rows of out, too), and the error word
-        says so."""
+        says so. Copies rows to the device, so it cannot be captured."""
         rows = np.asarray(rows, dtype=np.int32)
         if rows.shape != (self.cfg.batch,) or (rows < 0).any() or q.dim() != 4:
             raise ValueError("rows: a count for every sequence; q: [Ly][n][Hq][D]")
@@ -429,6 +445,7 @@ class SfiState:
         sfi_append_chunk(self._whole(), k_new, v_new, None, self.cfg.batch, 1, active=active,
                          stream=stream)
         self._grown(1)
+        self.t += 1
         self._off_course = True
         self._window(q, out, out_fp32, None, self.cfg.batch, 1, window, stream, served)
 
@@ -480,7 +497,7 @@ class BeamSearch:
     def __init__(self, n_groups, n_beams, vocab, eos=-1, device="cuda"):
         self.n_groups, self.n_beams, self.vocab, self.eos = n_groups, n_beams, vocab, eos
         rows = n_groups * n_beams
-        dev = dict(device=torch.device(device))
+        dev = dict(device=_at(device))
         self.cum = torch.full((rows,), -float("inf"), dtype=torch.float32, **dev)
         self.cum[::n_beams] = 0.0
         self.done = torch.zeros(rows, dtype=torch.uint8, **dev)
@@ -498,6 +515,7 @@ class BeamSearch:
             raise ValueError("logits are bf16 or fp32")
         if logits.device != self.cum.device:
             raise ValueError(f"logits are on {logits.device}, the beams on {self.cum.device}")
+        _here(self.cum.device)
         if rank_scale is not None:
             _want("rank_scale", rank_scale, torch.float32, self.cum.shape, self.cum.device)
         beam = SfiBeam(

@@ -94,3 +94,18 @@ def test_beam_arrays():
                           (x, torch.ones(3)), (x, torch.ones((4, 2))[:, 0])):
         with pytest.raises(ValueError):
             beam.select(logits, rank_scale=scale)
+
+
+def test_another_device_than_the_current_one(monkeypatch):
+    """Kernels run on the current device: a state on another one refuses (the devices are made up)."""
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    st = state()
+    st.device, st._pool = torch.device("cuda", 1), None
+    with pytest.raises(ValueError, match="not the current device"):
+        st.reserve()
+    with pytest.raises(ValueError, match="not the current device"):
+        st.step(None, None, None, [True] * B, None)
+    with pytest.raises(ValueError, match="not the current device"):
+        st.run(None)
+    with pytest.raises(ValueError):
+        st.reorder(torch.zeros(B, dtype=torch.int32))
