@@ -111,8 +111,11 @@ WindowShape window_shape(const sfi_kv_cache *kv, int n_rows, int max_rows, int r
 // The item size. 16 rows hold a single token's heads and leave room for a third stage. Two q
 // tiles (256 rows) halve the reads of K and V and keep the tensor core busy while the other
 // tile is in its softmax, but only one such CTA fits an SM: where the reach of a row is short,
-// an item is mostly start and end, which two CTAs of 128 rows overlap. fp32 outputs take the
-// tensor memory of a second q tile, and of a second CTA, for themselves.
+// an item is mostly start and end, which two CTAs of 128 rows overlap. Measured, us of 128 and of
+// 256 rows: an 8K chunk of 32 heads, window 64: 37, 50; 256: 62, 64; 384: 77, 75; 512: 91, 86; 1024: 149,
+// 130. Eight ragged paged prompts of 64 heads, 256: 129, 139; 384: 163, 160; 512: 197, 184; 1024: 334,
+// 287. (The two meet between 256 and 384.) fp32 outputs take the tensor memory of a second q
+// tile, and of a second CTA, for themselves.
 int window_rows(const sfi_kv_cache *kv, int max_rows, int n_window, bool fp32)
 {
     const long long all = 1LL * max_rows * (kv->n_q_heads / kv->n_kv_heads);

@@ -26,17 +26,21 @@
 // unnormalised outputs, maxima and sums the last one to finish joins, in split order.
 //
 // What bounds it (GB300, copy rate 6.78 TB/s, bf16 products 1.90 PFLOP/s measured):
-//   256 rows, 8K of 32K rows, window 4096: 396 us, 1.39 PFLOP/s. Per 128 keys a q tile's softmax
+//   256 rows, 8K of 32K rows, window 4096: 414 us, 1.33 PFLOP/s (397 in a replayed graph, as are the
+//     other figures of this form here). Per 128 keys a q tile's softmax
 //     (~2000 clocks), the hand-over of its weights (~370) and their product with the next scores
-//     (~1030) are a chain of ~3400, as tensor memory has one score buffer per q tile beside two O;
+//     (~1030) are a chain of ~3400, as tensor memory has one score buffer per q tile beside two O
+//     (half of whose columns hold nothing while it holds weights: the next scores do not use them);
 //     the other q tile fits between, so the tensor core has 2048 clocks of work in 3400 (without
 //     the softmax it would take 328 us). An item's start and end cost ~5600 more. Tried: 64-key
 //     tiles with two buffers (512 us: smaller products), two threads per score row (429: they
 //     share a scheduler, and the weights are handed over later), an MMA warp per q tile (533:
 //     the q tiles fall into step), warps of their own for the output (404).
-//   128 rows, 4 x 32K rows, window 64: 444 us, 6.0 TB/s of the 2.7 GB it has to move: 335 us
+//   128 rows, 4 x 32K rows, window 64: 446 us, 6.0 TB/s of the 2.7 GB it has to move: 335 us
 //     without the stores, no less with the softmax left out, 446 with stores through TMA.
-//   16 rows, 32 tokens, window 4096, pages: 88 us, 6.1 TB/s. HBM.
+//   16 rows, 32 tokens, window 4096, pages: 92 us, 5.9 TB/s. HBM.
+//   fp32 outputs: the chunk 1333 us, the prompts 1133, the tokens 186 to 194: one CTA per SM, three
+//     products per tile and O into M every second one; of 16 rows one softmax warp is live.
 // Registers that spill are the first thing to look at here: shared memory leaves next to no L1,
 // so a spill is a trip to L2 (a form that spilled took twice the time).
 #include "sfi_device.cuh"
