@@ -135,7 +135,7 @@ class SfiState:
         self._upto = self.len0.copy()   # host bound of every length (len0: the lengths at the start)
         self._window_ws = _Workspace(self.device)
         self._off_course = False    # lengths that are no longer len0 and the steps since
-        self._replayed = False      # a captured step may have advanced the lengths unseen
+        self._replayed = False      # a captured call may have changed the lengths unseen
 
     # -- host bookkeeping -------------------------------------------------------------------
     def reset_lengths(self):
@@ -315,6 +315,7 @@ class SfiState:
             self._upto = np.minimum(np.maximum(self._upto, at), self.capacity)
 
     def _run_active(self, plan, active, stream):
+        _here(self.device)
         slow, masks, q, k_new, v_new, out, _, events = plan._keep
         if events is not None:
             raise ValueError("a plan with events runs with all sequences")
@@ -487,6 +488,7 @@ class SfiState:
         pool = self.pool(stream) if self.page_table is not None else None
         sfi_reorder(self._whole(), src, pool=pool, budget=self.budget, mem=self.mem, stream=stream)
         self._upto = np.full_like(self._upto, self._upto.max())     # (src stays on the device)
+        self._replayed = self._replayed or _capturing(stream)
         self._off_course = True
 
 

@@ -168,3 +168,23 @@ def test_a_sequence_that_fills_up_in_a_replayed_step():
         assert lp.st.seq_len.tolist() == [320] + [n + 2 + t for n in (20, 1, 33, 40, 50)]
         assert (out[:, 0] == -7.0).all() if t else (out[:, 0] != -7.0).any()
         assert (out[:, 1:] != -7.0).any(-1).all()
+
+
+def test_lengths_that_a_replayed_reorder_exchanged():
+    """A full slot's length has moved to another sequence, which is then the one that is left out."""
+    lp = Loop(False)
+    lp.prefill([20, 21, 22, 23, 24, 25], 64)
+    src = torch.tensor([1, 0, 2, 3, 4, 5], dtype=torch.int32, device="cuda")
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        lp.st.reorder(src)
+    lp.prefill([0, 290, 0, 0, 0, 0], 64)
+    graph.replay()
+    q, k, v = lp.rnd(2, 60, 8, D), lp.rnd(2, 60, 2, D), lp.rnd(2, 60, 2, D)
+    out = torch.full((2, 60, 8, D), -7.0, device="cuda")
+    lp.st.prefill(q, k, v, [30, 30, 0, 0, 0, 0], out, out_fp32=True, n_window=64)
+    torch.cuda.synchronize()
+    assert int(lp.st.err[0]) == sfi.SFI_DEVERR_CAPACITY
+    assert lp.st.seq_len.tolist() == [311, 50, 22, 23, 24, 25]
+    assert (out[:, :30] == -7.0).all() and (out[:, 30:] != -7.0).any(-1).all()
