@@ -337,11 +337,13 @@ class SfiState:
     # -- prompts, pages and beams ------------------------------------------------------------
     def pool(self, stream=None) -> SfiPagePool:
         """The page pool behind the table (made on first use: every entry the table holds then
-        counts as one reference)."""
+        counts as one reference; not in a capture, as the entries are counted on the way)."""
         _here(self.device)
         if getattr(self, "_pool", None) is None:
             if self.page_table is None:
                 raise ValueError("a contiguous cache has no pages")
+            if _capturing(stream):
+                raise ValueError("the page pool is made by a first call outside the capture")
             with torch.cuda.stream(_torch_stream(stream)):
                 held = self.page_table[self.page_table >= 0]
                 self.page_refs = torch.bincount(held.long(), minlength=self.n_pages).to(torch.int32)

@@ -188,3 +188,14 @@ def test_lengths_that_a_replayed_reorder_exchanged():
     assert int(lp.st.err[0]) == sfi.SFI_DEVERR_CAPACITY
     assert lp.st.seq_len.tolist() == [311, 50, 22, 23, 24, 25]
     assert (out[:, :30] == -7.0).all() and (out[:, 30:] != -7.0).any(-1).all()
+
+
+def test_the_pool_is_not_made_in_a_capture():
+    lp = Loop(True)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        with pytest.raises(ValueError):
+            lp.st.reserve()
+    lp.prefill([60, 20, 30, 33, 40, 50], 64)
+    lp.step("slow")
