@@ -14,6 +14,9 @@
  *   around it    sfi_append_chunk, sfi_window_attn   a prompt into the cache, and its attention
  *                sfi_pages_reserve, _release, _evict, _compact   the pages of a paged cache
  *                sfi_beam_select, sfi_reorder        beam search, and forking sequences
+ *                sfi_rope_apply, sfi_rope_append     rotary positions of queries and keys
+ *                sfi_cross_attn                      attention to an encoder's states
+ *                sfi_score_tokens                    log probabilities of given tokens
  *
  * Conventions for every call:
  *   - All tensors are device memory owned by the caller; the library never allocates.
@@ -469,6 +472,97 @@ sfi_status sfi_append_chunk(const sfi_kv_cache *kv, const void *k_new, const voi
                             const uint8_t *active, void *stream);
 
 /*
+ * Rotary positions. Queries and keys are turned by their position before the cache's calls get
+ * them. With f_i radians per position, dimensions (a, b) of pair i < rot_dim / 2 of a head become
+ *     y_a = c (x_a cos(P f_i) - x_b sin(P f_i)),  y_b = c (x_b cos(P f_i) + x_a sin(P f_i))
+ * at position P, where (a, b) = (i, i + rot_dim / 2), or (2 i, 2 i + 1) if interleaved; dimensions
+ * from rot_dim on stay as they are. With q_norm (k_norm) given, every query (key) head is first
+ * normed, all 128 dimensions: x <- x * w / sqrt(mean(x^2) + norm_eps). Computed in fp32, rounded
+ * once. (Without norms, the gradient of the inputs is the same call on the gradient of the
+ * outputs with the positions negated.)
+ *   rot_dim    even, 2..128
+ *   amplitude  c
+ *   turns      device uint64 [rot_dim / 2]: f_i / (2 pi) mod 1 in units of 2^-64, which makes the
+ *              angle at any position exact to 2^-25 turns; sfi_rope_turns makes them
+ *   q_norm, k_norm  bf16 [128] on the device, 16-byte aligned, or NULL; norm_eps > 0 with either
+ */
+typedef struct sfi_rope {
+    int32_t rot_dim, interleaved;
+    float amplitude, norm_eps;
+    const uint64_t *turns;
+    const void *q_norm;
+    const void *k_norm;
+} sfi_rope;
+
+/*
+ * The frequencies, host only: f_i = base^(-2 i / rot_dim), for contexts `factor` times longer than
+ * original_len changed by
+ *   SFI_ROPE_PLAIN   nothing
+ *   SFI_ROPE_LINEAR  f_i / factor
+ *   SFI_ROPE_BASE    base replaced by base * factor^(rot_dim / (rot_dim - 2)) (rot_dim > 2)
+ *   SFI_ROPE_RAMP    f_i (1 - g_i) + f_i / factor * g_i, g_i = (i - first) / max(last - first, 0.001)
+ *                    clamped to [0, 1], where dim(t) = rot_dim ln(original_len / (2 pi t)) / (2 ln base),
+ *                    first = max(0, floor(dim(high))), last = min(rot_dim - 1, ceil(dim(low)));
+ *                    amplitude 0.1 ln(factor) + 1
+ *   SFI_ROPE_SMOOTH  f_i g_i + f_i / factor * (1 - g_i), g_i = (original_len f_i / (2 pi) - low) /
+ *                    (high - low) clamped to [0, 1]
+ * low and high are turns over original_len (0 < low < high). amplitude is 1 where nothing else is
+ * said. turns: host uint64 [rot_dim / 2]; amplitude: host float. base > 1, factor >= 1.
+ */
+#define SFI_ROPE_PLAIN 0
+#define SFI_ROPE_LINEAR 1
+#define SFI_ROPE_BASE 2
+#define SFI_ROPE_RAMP 3
+#define SFI_ROPE_SMOOTH 4
+
+typedef struct sfi_rope_scaling {
+    int32_t kind;
+    int32_t reserved;           /* 0 */
+    double base, factor, original_len, low, high;
+} sfi_rope_scaling;
+
+sfi_status sfi_rope_turns(int32_t rot_dim, const sfi_rope_scaling *scaling, uint64_t *turns,
+                          float *amplitude);
+
+/*
+ * Rows of new tokens on their way to the cache, packed as those of a chunk (row_start, n_rows,
+ * max_rows as for sfi_append_chunk).
+ *   q, k, v    bf16 [n_layers][n_rows] rows of n_q_heads (n_kv_heads) heads of 128, q_stride (k_stride,
+ *              v_stride) elements from row to row, layers n_rows rows apart: rows of one fused
+ *              projection, or packed. Strides are multiples of 8, at least a row's heads.
+ *   q_out, k_out  bf16, packed: [n_layers][n_rows][heads][128]. q_out may be q, and k_out k, where
+ *              that is packed, too; no other overlap.
+ *   pos        device int32 [n_rows], or NULL: the positions by which rows are turned (any value).
+ *              NULL: row i of sequence b at seq_len[b] + i.
+ *
+ * sfi_rope_apply turns q into q_out and k into k_out (either pair may be NULL) and touches neither
+ * the cache nor the lengths: for the calls that append on their own (sfi_fast_decode_step,
+ * sfi_decode_run). v is not read. Rows of inactive sequences and of skipped ones (SFI_DEVERR_ROWS, or
+ * without pos SFI_DEVERR_LENGTH) are not written.
+ *
+ * sfi_rope_append turns q into q_out (the pair may be NULL) and appends the turned k, and v, as
+ * sfi_append_chunk does: at position seq_len[b] + i whatever pos says, with its errors; then the
+ * lengths advance. k_out must be NULL. Of a sequence that is skipped there nothing is written;
+ * of one that lacks a page q_out is.
+ */
+typedef struct sfi_rope_rows {
+    const void *q;
+    void *q_out;
+    const void *k;
+    void *k_out;
+    const void *v;
+    int64_t q_stride, k_stride, v_stride;
+    const int32_t *pos;
+} sfi_rope_rows;
+
+sfi_status sfi_rope_apply(const sfi_kv_cache *kv, const sfi_rope *rope, const sfi_rope_rows *rows,
+                          const int32_t *row_start, int32_t n_rows, int32_t max_rows,
+                          const uint8_t *active, void *stream);
+sfi_status sfi_rope_append(const sfi_kv_cache *kv, const sfi_rope *rope, const sfi_rope_rows *rows,
+                           const int32_t *row_start, int32_t n_rows, int32_t max_rows,
+                           const uint8_t *active, void *stream);
+
+/*
  * Attention of a chunk under the sinks and the sliding window of the sparse state (summary
  * 2A), with nothing packed: the prompt's form of the fast step, and for one row per sequence
  * its single-token form. The rows of an active sequence are its last positions, already in
@@ -496,6 +590,24 @@ sfi_status sfi_window_attn(const sfi_kv_cache *kv, const void *q, void *out, int
                            size_t ws_bytes, void *stream);
 size_t sfi_window_workspace_bytes(const sfi_kv_cache *kv, int32_t n_rows, int32_t max_rows,
                                   int32_t n_sink, int32_t n_window);
+
+/*
+ * Attention to an encoder's states: kv is a cache of its own that holds them (keys and values written
+ * by sfi_append_chunk, say), one sequence for each encoder input, and every row of sequence e sees
+ * all seq_len[e] positions, whatever its own position is:
+ *     z_hj = q_h . k_j / sqrt(128),  o_h = sum_j softmax_j(z_h) v_j  over j < seq_len[e]
+ * and 0 where seq_len[e] is 0. Rows have no position, so those of a prompt's chunk, of its beams and of
+ * its beams' drafts are rows of one sequence alike, which read the states once: with beams adjacent,
+ * sfi_reorder of the decoder's cache within a prompt leaves this cache as it is.
+ *   q, out, out_fp32, row_start, n_rows, max_rows, active, ws: as for sfi_window_attn, with its rows
+ * that are not written, its errors (but for rows and lengths, which have nothing to do with each
+ * other) and its softmax weights in bf16 parts: three with out_fp32, else two in calls of at most
+ * 16 / group rows per sequence and one in calls of more.
+ */
+sfi_status sfi_cross_attn(const sfi_kv_cache *kv, const void *q, void *out, int32_t out_fp32,
+                          const int32_t *row_start, int32_t n_rows, int32_t max_rows,
+                          const uint8_t *active, void *ws, size_t ws_bytes, void *stream);
+size_t sfi_cross_workspace_bytes(const sfi_kv_cache *kv, int32_t n_rows, int32_t max_rows);
 
 /*
  * Sequence b takes over the state of sequence src[b] (src: device int32 [batch]; src[b] == b
@@ -550,6 +662,37 @@ typedef struct sfi_beam {
  * calls of any shape may share it, but must not overlap). 0 on invalid arguments. */
 size_t sfi_beam_workspace_bytes(const sfi_beam *beam);
 sfi_status sfi_beam_select(const sfi_beam *beam, void *ws, size_t ws_bytes, void *stream);
+
+/*
+ * Log probabilities of given tokens. For every row r with x = logits[r], lse = log sum_w exp(x[w]):
+ *   logprob[r]   fp32: x[t] - lse of the row's token t = token[r]
+ *   rank[r]      int32 or NULL: how many tokens come before t, by logit, then lowest token (0: the best)
+ *   entropy[r]   fp32 or NULL: -sum_w p_w log p_w, p = exp(x - lse); tokens of -inf add nothing
+ *   top_token, top_logprob  int32, fp32 [n_rows][n_top]: the first n_top tokens in that order and
+ *                their x - lse (both given if n_top > 0, else not written)
+ * A token below 0 stands for none (padding): logprob 0 and rank -1; one from vocab on gets NaN and rank
+ * -1. A row without a distribution (a NaN or +inf logit, or -inf alone) gets NaN for every number,
+ * rank -1 and top tokens -1. Sums of terms in fp32, relative to the row's highest logit.
+ *   logits       bf16, or fp32 if logits_fp32: [n_rows] of vocab, row_stride elements apart
+ *   token        device int32 [n_rows] or NULL: no token (logprob and rank must be NULL then)
+ * 0 <= n_top <= 32 (else SFI_ERR_UNSUPPORTED) and n_top <= vocab; vocab <= 2^30; n_rows >= 0.
+ */
+typedef struct sfi_scoring {
+    int32_t n_rows, vocab, logits_fp32, n_top;
+    int64_t row_stride;
+    const void *logits;
+    const int32_t *token;
+    float *logprob;
+    int32_t *rank;
+    float *entropy;
+    int32_t *top_token;
+    float *top_logprob;
+} sfi_scoring;
+
+/* Workspace of sfi_score_tokens (256-byte aligned, initialised once with sfi_workspace_init; calls of
+ * any shape may share it, but must not overlap). 0 on invalid arguments. */
+size_t sfi_scoring_workspace_bytes(const sfi_scoring *scoring);
+sfi_status sfi_score_tokens(const sfi_scoring *scoring, void *ws, size_t ws_bytes, void *stream);
 
 /* Copy the device error word to *bits (synchronises `stream`). Returns SFI_OK when it is
  * zero, SFI_ERR_DEVICE when any bit is set. */

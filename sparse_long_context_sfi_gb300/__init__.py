@@ -41,6 +41,8 @@ ENTRY_POINTS = (
     "sfi_pages_workspace_bytes", "sfi_pages_reserve", "sfi_pages_release", "sfi_pages_evict",
     "sfi_pages_compact", "sfi_append_chunk", "sfi_window_attn", "sfi_window_workspace_bytes",
     "sfi_reorder", "sfi_beam_workspace_bytes", "sfi_beam_select",
+    "sfi_rope_turns", "sfi_rope_apply", "sfi_rope_append", "sfi_cross_workspace_bytes",
+    "sfi_cross_attn", "sfi_scoring_workspace_bytes", "sfi_score_tokens",
 )
 
 
@@ -88,6 +90,31 @@ class SfiBeam(C.Structure):
                 ("token", C.c_void_p), ("cum_out", C.c_void_p), ("done_out", C.c_void_p)]
 
 
+class SfiRope(C.Structure):
+    _fields_ = [("rot_dim", C.c_int32), ("interleaved", C.c_int32), ("amplitude", C.c_float),
+                ("norm_eps", C.c_float), ("turns", C.c_void_p), ("q_norm", C.c_void_p),
+                ("k_norm", C.c_void_p)]
+
+
+class SfiRopeScaling(C.Structure):
+    _fields_ = [("kind", C.c_int32), ("reserved", C.c_int32), ("base", C.c_double),
+                ("factor", C.c_double), ("original_len", C.c_double), ("low", C.c_double),
+                ("high", C.c_double)]
+
+
+class SfiRopeRows(C.Structure):
+    _fields_ = [("q", C.c_void_p), ("q_out", C.c_void_p), ("k", C.c_void_p), ("k_out", C.c_void_p),
+                ("v", C.c_void_p), ("q_stride", C.c_int64), ("k_stride", C.c_int64),
+                ("v_stride", C.c_int64), ("pos", C.c_void_p)]
+
+
+class SfiScoring(C.Structure):
+    _fields_ = [("n_rows", C.c_int32), ("vocab", C.c_int32), ("logits_fp32", C.c_int32),
+                ("n_top", C.c_int32), ("row_stride", C.c_int64), ("logits", C.c_void_p),
+                ("token", C.c_void_p), ("logprob", C.c_void_p), ("rank", C.c_void_p),
+                ("entropy", C.c_void_p), ("top_token", C.c_void_p), ("top_logprob", C.c_void_p)]
+
+
 class SfiError(RuntimeError):
     def __init__(self, fn: str, status: int):
         self.status = status
@@ -106,7 +133,7 @@ def lib():
         l = C.CDLL(LIB_PATH)
         P, I32, SZ = C.c_void_p, C.c_int32, C.c_size_t
         KV, BD, MEM = C.POINTER(SfiKvCache), C.POINTER(SfiBudget), C.POINTER(SfiSparseMem)
-        PP = C.POINTER(SfiPagePool)
+        PP, RP, RR = C.POINTER(SfiPagePool), C.POINTER(SfiRope), C.POINTER(SfiRopeRows)
         sig = {
             "sfi_status_string": (C.c_char_p, [C.c_int]),
             "sfi_version": (C.c_char_p, []),
@@ -138,6 +165,13 @@ def lib():
             "sfi_reorder": (C.c_int, [KV, PP, BD, MEM, P, P]),
             "sfi_beam_workspace_bytes": (SZ, [C.POINTER(SfiBeam)]),
             "sfi_beam_select": (C.c_int, [C.POINTER(SfiBeam), P, SZ, P]),
+            "sfi_rope_turns": (C.c_int, [I32, C.POINTER(SfiRopeScaling), P, C.POINTER(C.c_float)]),
+            "sfi_rope_apply": (C.c_int, [KV, RP, RR, P, I32, I32, P, P]),
+            "sfi_rope_append": (C.c_int, [KV, RP, RR, P, I32, I32, P, P]),
+            "sfi_cross_workspace_bytes": (SZ, [KV, I32, I32]),
+            "sfi_cross_attn": (C.c_int, [KV, P, P, I32, P, I32, I32, P, P, SZ, P]),
+            "sfi_scoring_workspace_bytes": (SZ, [C.POINTER(SfiScoring)]),
+            "sfi_score_tokens": (C.c_int, [C.POINTER(SfiScoring), P, SZ, P]),
         }
         for name, (res, args) in sig.items():
             f = getattr(l, name)
@@ -401,3 +435,68 @@ def sfi_beam_workspace_bytes(beam: SfiBeam) -> int:
 def sfi_beam_select(beam: SfiBeam, ws, ws_bytes: int, stream=None):
     _check("sfi_beam_select", lib().sfi_beam_select(C.byref(beam), _ptr(ws), ws_bytes,
                                                     _stream(stream)))
+
+
+# -------------------------------- rotary positions, an encoder's states, log probabilities
+
+ROPE_SCALINGS = ("none", "linear", "base", "ramp", "smooth")
+
+
+def sfi_rope_turns(rot_dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+                   original_len: float = 0.0, low: float = 1.0, high: float = 32.0):
+    """The frequencies of rotary positions as SfiRope takes them (uint64, numpy: to be copied to the
+    device) and the amplitude; scaling: one of ROPE_SCALINGS."""
+    import numpy as np
+    if scaling not in ROPE_SCALINGS:
+        raise ValueError(f"scaling is one of {ROPE_SCALINGS}, not {scaling!r}")
+    turns = np.zeros(max(1, rot_dim // 2), dtype=np.uint64)
+    sc = SfiRopeScaling(kind=ROPE_SCALINGS.index(scaling), base=base, factor=factor,
+                        original_len=original_len, low=low, high=high)
+    amplitude = C.c_float(0.0)
+    _check("sfi_rope_turns", lib().sfi_rope_turns(rot_dim, C.byref(sc), turns.ctypes.data,
+                                                  C.byref(amplitude)))
+    return turns, amplitude.value
+
+
+def sfi_rope_apply(kv: SfiKvCache, rope: SfiRope, rows: SfiRopeRows, row_start, n_rows: int,
+                   max_rows: int, active=None, stream=None):
+    """Queries and keys turned to their positions (packed rows; row_start None: one each)."""
+    _check("sfi_rope_apply", lib().sfi_rope_apply(
+        C.byref(kv), C.byref(rope), C.byref(rows), _ptr(row_start), n_rows, max_rows, _ptr(active),
+        _stream(stream)))
+
+
+def sfi_rope_append(kv: SfiKvCache, rope: SfiRope, rows: SfiRopeRows, row_start, n_rows: int,
+                    max_rows: int, active=None, stream=None):
+    """Queries turned; turned keys, and values, appended to the cache (sfi_append_chunk)."""
+    _check("sfi_rope_append", lib().sfi_rope_append(
+        C.byref(kv), C.byref(rope), C.byref(rows), _ptr(row_start), n_rows, max_rows, _ptr(active),
+        _stream(stream)))
+
+
+def sfi_cross_workspace_bytes(kv: SfiKvCache, n_rows: int, max_rows: int) -> int:
+    n = lib().sfi_cross_workspace_bytes(C.byref(kv), n_rows, max_rows)
+    if n == 0:
+        raise SfiError("sfi_cross_workspace_bytes", SFI_ERR_INVALID_ARG)
+    return n
+
+
+def sfi_cross_attn(kv: SfiKvCache, q, out, out_fp32: bool, row_start, n_rows: int, max_rows: int, ws,
+                   ws_bytes: int, active=None, stream=None):
+    """Attention of packed rows to all positions of their sequence in `kv`, an encoder's states."""
+    _check("sfi_cross_attn", lib().sfi_cross_attn(
+        C.byref(kv), _ptr(q), _ptr(out), 1 if out_fp32 else 0, _ptr(row_start), n_rows, max_rows,
+        _ptr(active), _ptr(ws), ws_bytes, _stream(stream)))
+
+
+def sfi_scoring_workspace_bytes(scoring: SfiScoring) -> int:
+    n = lib().sfi_scoring_workspace_bytes(C.byref(scoring))
+    if n == 0:
+        raise SfiError("sfi_scoring_workspace_bytes", SFI_ERR_INVALID_ARG)
+    return n
+
+
+def sfi_score_tokens(scoring: SfiScoring, ws, ws_bytes: int, stream=None):
+    """Log probabilities, ranks, entropies and best tokens of rows of logits."""
+    _check("sfi_score_tokens", lib().sfi_score_tokens(C.byref(scoring), _ptr(ws), ws_bytes,
+                                                      _stream(stream)))

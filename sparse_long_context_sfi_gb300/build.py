@@ -26,8 +26,8 @@ SYNTH_LIB = os.path.join(ROOT, "synth", "libsynth.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 COMMON = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
           "--expt-relaxed-constexpr", "-I", INCLUDE, "-I", CSRC]
-SOURCES = ["attn.cu", "select.cu", "refine.cu", "kvops.cu", "pages.cu", "beam.cu", "window.cu",
-           "api.cpp", "api_cache.cpp"]
+SOURCES = ["window.cu", "cross.cu", "score.cu", "attn.cu", "select.cu", "rope.cu", "refine.cu", "kvops.cu",
+           "pages.cu", "beam.cu", "api.cpp", "api_cache.cpp"]
 
 
 def nvcc() -> str:

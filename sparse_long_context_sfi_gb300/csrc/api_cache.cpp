@@ -1,9 +1,11 @@
 // api_cache.cpp -- the extern "C" entry points of include/sfi.h that keep the cache around the
-// decode path: pages, prompt chunks and their attention, beam search. Argument checks,
-// workspace layout and launches; no allocation, no synchronisation.
+// decode path: pages, prompt chunks and their attention, rotary positions, an encoder's states, beam
+// search and log probabilities. Argument checks, workspace layout and launches; no allocation, no
+// synchronisation.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <climits>
 #include <cmath>
 #include <cstring>
 
@@ -189,6 +191,184 @@ size_t beam_scratch(const sfi_beam *b, char *base, BeamParams *p)
     return o;
 }
 
+sfi_status check_rope(const sfi_rope *r)
+{
+    if (!r || r->rot_dim < 2 || r->rot_dim > kHeadDim || (r->rot_dim & 1) || !std::isfinite(r->amplitude) ||
+        !r->turns || (reinterpret_cast<uintptr_t>(r->turns) & 7u) || !aligned16(r->q_norm) || !aligned16(r->k_norm))
+        return SFI_ERR_INVALID_ARG;
+    if ((r->q_norm || r->k_norm) && !(r->norm_eps > 0.f && std::isfinite(r->norm_eps)))
+        return SFI_ERR_INVALID_ARG;
+    return SFI_OK;
+}
+
+// Rows of `heads` heads each; written in place only where they are packed.
+bool rope_rows_ok(const void *in, int64_t stride, const void *out, int heads)
+{
+    const int64_t packed = static_cast<int64_t>(heads) * kHeadDim;
+    return aligned16(in) && aligned16(out) && stride >= packed && stride % 8 == 0 &&
+           (in != out || stride == packed);
+}
+
+sfi_status rope(bool append, const sfi_kv_cache *kv, const sfi_rope *r, const sfi_rope_rows *rows,
+                const int32_t *row_start, int32_t n_rows, int32_t max_rows, const uint8_t *active,
+                void *stream)
+{
+    sfi_status st = check_kv(kv);
+    if (st != SFI_OK || (st = check_rope(r)) != SFI_OK ||
+        (st = check_rows(kv, row_start, n_rows, max_rows)) != SFI_OK)
+        return st;
+    if (!rows || !rows->q != !rows->q_out || (append ? rows->k_out != nullptr : !rows->k != !rows->k_out))
+        return SFI_ERR_INVALID_ARG;
+    if (n_rows == 0)
+        return SFI_OK;
+    if (append ? !rows->k || !rows->v : !rows->q && !rows->k)
+        return SFI_ERR_INVALID_ARG;
+    if ((rows->q && !rope_rows_ok(rows->q, rows->q_stride, rows->q_out, kv->n_q_heads)) ||
+        (rows->k && !rope_rows_ok(rows->k, rows->k_stride, rows->k_out, kv->n_kv_heads)) ||
+        (append && !rope_rows_ok(rows->v, rows->v_stride, nullptr, kv->n_kv_heads)))
+        return SFI_ERR_INVALID_ARG;
+    RopeParams p;
+    std::memset(&p, 0, sizeof p);
+    p.c.pg = page_params(kv, const_cast<int32_t *>(kv->page_table), nullptr, active);
+    p.c.row_start = row_start;
+    p.c.n_rows = n_rows;
+    p.c.max_rows = max_rows;
+    p.n_layers = kv->n_layers;
+    p.n_q_heads = kv->n_q_heads;
+    p.q = rows->q;
+    p.k = rows->k;
+    p.q_stride = rows->q_stride;
+    p.k_stride = rows->k_stride;
+    p.q_out = rows->q_out;
+    if (append) {
+        p.v = rows->v;
+        p.v_stride = rows->v_stride;
+        p.k_cache = kv->k;
+        p.v_cache = kv->v;
+    } else {
+        p.k_out = rows->k_out;
+    }
+    p.pos = rows->pos;
+    p.rot = r->rot_dim;
+    p.interleaved = r->interleaved ? 1 : 0;
+    p.amplitude = r->amplitude;
+    p.eps = r->norm_eps;
+    p.turns = r->turns;
+    p.q_norm = r->q_norm;
+    p.k_norm = r->k_norm;
+    const int sms = sm_count();
+    if (sms <= 0)
+        return SFI_ERR_CUDA;
+    return launch_status(launch_rope(p, sms, as_stream(stream)));
+}
+
+// sfi_window_attn, or with `cross` rows that see all of their sequence (n_sink 0, n_window INT_MAX).
+sfi_status attend(bool cross, const sfi_kv_cache *kv, const void *q, void *out, int32_t out_fp32,
+                  const int32_t *row_start, int32_t n_rows, int32_t max_rows, int32_t n_sink,
+                  int32_t n_window, const uint8_t *active, void *ws, size_t ws_bytes, void *stream)
+{
+    sfi_status st = check_kv(kv);
+    if (st != SFI_OK)
+        return st;
+    if (n_sink < 0 || n_window < 1)
+        return SFI_ERR_INVALID_ARG;
+    if ((st = check_rows(kv, row_start, n_rows, max_rows)) != SFI_OK)
+        return st;
+    WindowParams p;
+    std::memset(&p, 0, sizeof p);
+    if ((st = check_ws(ws, ws_bytes, window_scratch(kv, n_rows, max_rows, static_cast<char *>(ws), &p))) !=
+        SFI_OK)
+        return st;
+    if (n_rows == 0 || max_rows == 0)
+        return SFI_OK;
+    if (!q || !out || !aligned16(q) || !aligned16(out))
+        return SFI_ERR_INVALID_ARG;
+    const bool fp32 = out_fp32 != 0;
+    const int rows = window_rows(kv, max_rows, n_window, fp32);
+    CUtensorMap tk, tv, tq;
+    if (!make_map(&tk, kv->k, cache_rows(kv), 16u) || !make_map(&tv, kv->v, cache_rows(kv), 16u) ||
+        !make_chunk_map(&tq, q, static_cast<uint64_t>(kv->n_layers) * n_rows,
+                        static_cast<uint32_t>(kv->n_q_heads),
+                        static_cast<uint32_t>(kv->n_q_heads / kv->n_kv_heads), rows == 16 ? 16u : 128u))
+        return SFI_ERR_CUDA;
+    p.n_layers = kv->n_layers;
+    p.batch = kv->batch;
+    p.n_kv_heads = kv->n_kv_heads;
+    p.group = kv->n_q_heads / kv->n_kv_heads;
+    p.group_log2 = p.group == 8 ? 3 : p.group == 4 ? 2 : p.group == 2 ? 1 : 0;
+    p.heads_log2 = -1;
+    for (int i = 0; i < 31; ++i)
+        if (kv->n_kv_heads == 1 << i)
+            p.heads_log2 = i;
+    p.capacity = kv->capacity;
+    p.page_size = kv->page_size;
+    p.n_pages = kv->n_pages;
+    p.max_pages = kv->max_pages_per_seq;
+    p.max_len = kv->max_len;
+    p.page_table = kv->page_table;
+    p.seq_len = kv->seq_len;
+    p.active = active;
+    p.row_start = row_start;
+    p.n_rows = n_rows;
+    p.max_rows = max_rows;
+    p.n_sink = n_sink;
+    p.n_window = n_window;
+    p.out = out;
+    p.out_fp32 = out_fp32 ? 1 : 0;
+    p.out_aligned32 = (reinterpret_cast<uintptr_t>(out) & 31u) == 0;
+    p.err = kv->err;
+    const long long len = kv->max_len, reach = n_window < len ? n_window : len;
+    const WindowShape s = window_shape(kv, n_rows, max_rows, rows, fp32);
+    // Fewer items than CTAs that fit: split their keys, four tiles at least to a split.
+    const int kt = rows == 256 ? 128 : 64;
+    const long long span = reach + rows / p.group < len ? reach + rows / p.group : len;
+    const long long tiles = (span + n_sink + 32 + kt - 1) / kt;
+    long long split = s.most_split < tiles / 4 ? s.most_split : tiles / 4;
+    split = split < 1 ? 1 : split;
+    p.n_split = static_cast<int>(split);
+    p.part_rows = s.part_rows;
+    const long long all = s.items * split;
+    const int grid = static_cast<int>(all < s.slots ? all : s.slots);
+    p.scale_log2 = static_cast<float>(1.4426950408889634074 / std::sqrt(static_cast<double>(kHeadDim)));
+    return launch_status((cross ? launch_cross : launch_window)(p, rows, tk, tv, tq, grid, as_stream(stream)));
+}
+
+sfi_status check_scoring(const sfi_scoring *s)
+{
+    if (!s || s->n_rows < 0 || s->vocab < 1 || s->row_stride < s->vocab || s->n_top < 0 || s->n_top > s->vocab)
+        return SFI_ERR_INVALID_ARG;
+    if (s->n_top > kMaxTop || s->vocab > (1 << 30))
+        return SFI_ERR_UNSUPPORTED;
+    return SFI_OK;
+}
+
+// CTAs per row, as for the beams; rows are split only while there are fewer than two for every SM.
+int score_splits(const sfi_scoring *s, int sms)
+{
+    const int fit = s->n_rows > 0 ? 4 * sms / s->n_rows : 1, most = s->vocab / 4096 + 1;
+    const int n = fit < most ? fit : most;
+    return n < 1 ? 1 : n > 64 ? 64 : n;
+}
+
+size_t score_scratch(const sfi_scoring *s, char *base, ScoreParams *p)
+{
+    const int sms = sm_count();
+    size_t o = 0;
+    auto take = [&](size_t bytes) {
+        char *at = base + o;
+        o = align256(o + bytes);
+        return static_cast<void *>(at);
+    };
+    p->splits = score_splits(s, sms);
+    const size_t parts = p->splits > 1 ? static_cast<size_t>(s->n_rows) * p->splits : 0;
+    // (room that does not depend on the call, so that calls of other shapes leave the tickets zero)
+    p->tickets = static_cast<int *>(take(2 * static_cast<size_t>(sms > 0 ? sms : 1) * sizeof(int)));
+    p->part = static_cast<float4 *>(take(parts * sizeof(float4)));
+    p->part_x = static_cast<float *>(take(parts * s->n_top * sizeof(float)));
+    p->part_v = static_cast<int32_t *>(take(parts * s->n_top * sizeof(int32_t)));
+    return o;
+}
+
 }  // namespace
 
 extern "C" {
@@ -292,70 +472,75 @@ sfi_status sfi_window_attn(const sfi_kv_cache *kv, const void *q, void *out, int
                            int32_t n_sink, int32_t n_window, const uint8_t *active, void *ws,
                            size_t ws_bytes, void *stream)
 {
-    sfi_status st = check_kv(kv);
-    if (st != SFI_OK)
-        return st;
-    if (n_sink < 0 || n_window < 1)
+    return attend(false, kv, q, out, out_fp32, row_start, n_rows, max_rows, n_sink, n_window, active, ws,
+                  ws_bytes, stream);
+}
+
+size_t sfi_cross_workspace_bytes(const sfi_kv_cache *kv, int32_t n_rows, int32_t max_rows)
+{
+    return sfi_window_workspace_bytes(kv, n_rows, max_rows, 0, INT_MAX);
+}
+
+sfi_status sfi_cross_attn(const sfi_kv_cache *kv, const void *q, void *out, int32_t out_fp32,
+                          const int32_t *row_start, int32_t n_rows, int32_t max_rows,
+                          const uint8_t *active, void *ws, size_t ws_bytes, void *stream)
+{
+    return attend(true, kv, q, out, out_fp32, row_start, n_rows, max_rows, 0, INT_MAX, active, ws, ws_bytes,
+                  stream);
+}
+
+sfi_status sfi_rope_turns(int32_t rot_dim, const sfi_rope_scaling *sc, uint64_t *turns, float *amplitude)
+{
+    if (rot_dim < 2 || rot_dim > kHeadDim || (rot_dim & 1) || !sc || !turns || !amplitude || sc->reserved != 0 ||
+        sc->kind < SFI_ROPE_PLAIN || sc->kind > SFI_ROPE_SMOOTH)
         return SFI_ERR_INVALID_ARG;
-    if ((st = check_rows(kv, row_start, n_rows, max_rows)) != SFI_OK)
-        return st;
-    WindowParams p;
-    std::memset(&p, 0, sizeof p);
-    if ((st = check_ws(ws, ws_bytes, window_scratch(kv, n_rows, max_rows, static_cast<char *>(ws), &p))) !=
-        SFI_OK)
-        return st;
-    if (n_rows == 0 || max_rows == 0)
-        return SFI_OK;
-    if (!q || !out || !aligned16(q) || !aligned16(out))
+    const bool stretched = sc->kind != SFI_ROPE_PLAIN;
+    const bool parts = sc->kind == SFI_ROPE_RAMP || sc->kind == SFI_ROPE_SMOOTH;
+    if (!(sc->base > 1.) || !std::isfinite(sc->base) ||
+        (stretched && (!(sc->factor >= 1.) || !std::isfinite(sc->factor))) ||
+        (parts && (!(sc->original_len > 0.) || !std::isfinite(sc->original_len) || !(sc->low > 0.) ||
+                   !(sc->high > sc->low) || !std::isfinite(sc->high))) ||
+        (sc->kind == SFI_ROPE_BASE && rot_dim == 2))
         return SFI_ERR_INVALID_ARG;
-    const bool fp32 = out_fp32 != 0;
-    const int rows = window_rows(kv, max_rows, n_window, fp32);
-    CUtensorMap tk, tv, tq;
-    if (!make_map(&tk, kv->k, cache_rows(kv), 16u) || !make_map(&tv, kv->v, cache_rows(kv), 16u) ||
-        !make_chunk_map(&tq, q, static_cast<uint64_t>(kv->n_layers) * n_rows,
-                        static_cast<uint32_t>(kv->n_q_heads),
-                        static_cast<uint32_t>(kv->n_q_heads / kv->n_kv_heads), rows == 16 ? 16u : 128u))
-        return SFI_ERR_CUDA;
-    p.n_layers = kv->n_layers;
-    p.batch = kv->batch;
-    p.n_kv_heads = kv->n_kv_heads;
-    p.group = kv->n_q_heads / kv->n_kv_heads;
-    p.group_log2 = p.group == 8 ? 3 : p.group == 4 ? 2 : p.group == 2 ? 1 : 0;
-    p.heads_log2 = -1;
-    for (int i = 0; i < 31; ++i)
-        if (kv->n_kv_heads == 1 << i)
-            p.heads_log2 = i;
-    p.capacity = kv->capacity;
-    p.page_size = kv->page_size;
-    p.n_pages = kv->n_pages;
-    p.max_pages = kv->max_pages_per_seq;
-    p.max_len = kv->max_len;
-    p.page_table = kv->page_table;
-    p.seq_len = kv->seq_len;
-    p.active = active;
-    p.row_start = row_start;
-    p.n_rows = n_rows;
-    p.max_rows = max_rows;
-    p.n_sink = n_sink;
-    p.n_window = n_window;
-    p.out = out;
-    p.out_fp32 = out_fp32 ? 1 : 0;
-    p.out_aligned32 = (reinterpret_cast<uintptr_t>(out) & 31u) == 0;
-    p.err = kv->err;
-    const long long len = kv->max_len, reach = n_window < len ? n_window : len;
-    const WindowShape s = window_shape(kv, n_rows, max_rows, rows, fp32);
-    // Fewer items than CTAs that fit: split their keys, four tiles at least to a split.
-    const int kt = rows == 256 ? 128 : 64;
-    const long long span = reach + rows / p.group < len ? reach + rows / p.group : len;
-    const long long tiles = (span + n_sink + 32 + kt - 1) / kt;
-    long long split = s.most_split < tiles / 4 ? s.most_split : tiles / 4;
-    split = split < 1 ? 1 : split;
-    p.n_split = static_cast<int>(split);
-    p.part_rows = s.part_rows;
-    const long long all = s.items * split;
-    const int grid = static_cast<int>(all < s.slots ? all : s.slots);
-    p.scale_log2 = static_cast<float>(1.4426950408889634074 / std::sqrt(static_cast<double>(kHeadDim)));
-    return launch_status(launch_window(p, rows, tk, tv, tq, grid, as_stream(stream)));
+    const double two_pi = 6.283185307179586476925286766559;
+    double base = sc->base, first = 0., last = 0.;
+    if (sc->kind == SFI_ROPE_BASE)
+        base *= std::pow(sc->factor, rot_dim / (rot_dim - 2.));
+    if (sc->kind == SFI_ROPE_RAMP) {
+        auto dim = [&](double t) { return rot_dim * std::log(sc->original_len / (two_pi * t)) / (2. * std::log(base)); };
+        first = std::fmax(0., std::floor(dim(sc->high)));
+        last = std::fmin(rot_dim - 1., std::ceil(dim(sc->low)));
+    }
+    for (int i = 0; i < rot_dim / 2; ++i) {
+        double f = std::pow(base, -2. * i / rot_dim);
+        double keep = 1.;       // the share that is not divided by the factor
+        if (sc->kind == SFI_ROPE_LINEAR)
+            keep = 0.;
+        else if (sc->kind == SFI_ROPE_RAMP)
+            keep = 1. - std::fmin(1., std::fmax(0., (i - first) / std::fmax(last - first, 0.001)));
+        else if (sc->kind == SFI_ROPE_SMOOTH)
+            keep = std::fmin(1., std::fmax(0., (sc->original_len * f / two_pi - sc->low) / (sc->high - sc->low)));
+        if (keep < 1.)
+            f = f * keep + f / sc->factor * (1. - keep);
+        // (f <= 1, so below 2^64 units)
+        turns[i] = static_cast<uint64_t>(std::floor(std::ldexp(f / two_pi, 64) + 0.5));
+    }
+    *amplitude = sc->kind == SFI_ROPE_RAMP ? static_cast<float>(0.1 * std::log(sc->factor) + 1.) : 1.f;
+    return SFI_OK;
+}
+
+sfi_status sfi_rope_apply(const sfi_kv_cache *kv, const sfi_rope *r, const sfi_rope_rows *rows,
+                          const int32_t *row_start, int32_t n_rows, int32_t max_rows,
+                          const uint8_t *active, void *stream)
+{
+    return rope(false, kv, r, rows, row_start, n_rows, max_rows, active, stream);
+}
+
+sfi_status sfi_rope_append(const sfi_kv_cache *kv, const sfi_rope *r, const sfi_rope_rows *rows,
+                           const int32_t *row_start, int32_t n_rows, int32_t max_rows,
+                           const uint8_t *active, void *stream)
+{
+    return rope(true, kv, r, rows, row_start, n_rows, max_rows, active, stream);
 }
 
 sfi_status sfi_reorder(const sfi_kv_cache *kv, const sfi_page_pool *pool,
@@ -445,6 +630,45 @@ sfi_status sfi_beam_select(const sfi_beam *beam, void *ws, size_t ws_bytes, void
     p.cum_out = beam->cum_out;
     p.done_out = beam->done_out;
     return launch_status(launch_beam_select(p, as_stream(stream)));
+}
+
+size_t sfi_scoring_workspace_bytes(const sfi_scoring *scoring)
+{
+    if (check_scoring(scoring) != SFI_OK)
+        return 0;
+    ScoreParams p;
+    return score_scratch(scoring, nullptr, &p);
+}
+
+sfi_status sfi_score_tokens(const sfi_scoring *sc, void *ws, size_t ws_bytes, void *stream)
+{
+    sfi_status st = check_scoring(sc);
+    if (st != SFI_OK)
+        return st;
+    if ((!sc->token && (sc->logprob || sc->rank)) || (sc->n_top > 0 && (!sc->top_token || !sc->top_logprob)) ||
+        (sc->n_top == 0 && !sc->logprob && !sc->rank && !sc->entropy))
+        return SFI_ERR_INVALID_ARG;
+    ScoreParams p;
+    std::memset(&p, 0, sizeof p);
+    if ((st = check_ws(ws, ws_bytes, score_scratch(sc, static_cast<char *>(ws), &p))) != SFI_OK)
+        return st;
+    if (sc->n_rows == 0)
+        return SFI_OK;
+    if (!sc->logits || (reinterpret_cast<uintptr_t>(sc->logits) & (sc->logits_fp32 ? 3u : 1u)))
+        return SFI_ERR_INVALID_ARG;
+    p.n_rows = sc->n_rows;
+    p.vocab = sc->vocab;
+    p.logits_fp32 = sc->logits_fp32 ? 1 : 0;
+    p.n_top = sc->n_top;
+    p.row_stride = sc->row_stride;
+    p.logits = sc->logits;
+    p.token = sc->token;
+    p.logprob = sc->logprob;
+    p.rank = sc->rank;
+    p.entropy = sc->entropy;
+    p.top_token = sc->top_token;
+    p.top_logprob = sc->top_logprob;
+    return launch_status(launch_score(p, as_stream(stream)));
 }
 
 }  // extern "C"

@@ -13,6 +13,7 @@
 //
 // Kernels here that write what a fast step may read before its own wait (packed memory, `ok`
 // masks) let no dependent start early; the others start theirs at entry.
+#include "chunk.cuh"
 #include "sfi_device.cuh"
 
 namespace sfi {
@@ -451,63 +452,7 @@ __global__ void __launch_bounds__(256) compact_move_kernel(const PageParams p, c
 
 // --------------------------------------------------------------------------- chunk appends
 
-// Whether sequence b's chunk is sound: rows within bounds and no other's, room in the cache. A
-// warp call, every lane the same b. Where the starts run backwards somewhere, rows belong to the
-// first sequence that claims them: one that begins before an earlier start is left out.
-__device__ __forceinline__ bool chunk_ok(const ChunkParams &p, int b, int lane, int &r0, int &n, int &L,
-                                         bool report)
-{
-    r0 = p.row_start ? p.row_start[b] : b;
-    const int r1 = p.row_start ? p.row_start[b + 1] : b + 1;
-    n = r1 - r0;
-    L = p.pg.seq_len[b];
-    bool owned = true;
-    if (p.row_start)
-        for (int i = lane; i < b; i += 32)
-            owned = owned && p.row_start[i] <= r0;
-    owned = __all_sync(kFull, owned) != 0;
-    uint32_t bad = 0;
-    if (r0 < 0 || n < 0 || r1 > p.n_rows || n > p.max_rows || (n > 0 && !owned))
-        bad = 0x20u;  // SFI_DEVERR_ROWS
-    else if (L < 0 || L > p.pg.max_len)
-        bad = 0x8u;   // SFI_DEVERR_LENGTH
-    else if (n > p.pg.capacity - L)
-        bad = 0x2u;   // SFI_DEVERR_CAPACITY
-    if (bad && report)
-        raise_error(p.pg.err, bad);
-    return bad == 0;
-}
-
 constexpr int kChunkRows = 8;   // rows per CTA
-
-// The cache row of (layer 0, head 0) for packed row r, -1 where it is not written. One warp,
-// every lane the same r: the row's sequence is the one before the first start behind r, found
-// in one round trip (a sound sequence's own rows are in front of every later start that counts).
-__device__ __forceinline__ long long chunk_dst(const ChunkParams &p, int r, int lane)
-{
-    int b = r;
-    if (r >= p.n_rows)
-        return -1;
-    if (p.row_start) {
-        int behind = p.pg.batch + 1;
-        for (int i = lane; i <= p.pg.batch; i += 32)
-            if (p.row_start[i] > r)
-                behind = min(behind, i);
-        b = __reduce_min_sync(kFull, behind) - 1;
-        if (b < 0 || b >= p.pg.batch)
-            return -1;
-    }
-    int s0, n, L;
-    if ((p.pg.active && !p.pg.active[b]) || !chunk_ok(p, b, lane, s0, n, L, false) || r < s0 || r >= s0 + n)
-        return -1;
-    const int pos = L + r - s0;
-    if (p.pg.page_size == 0)
-        return static_cast<long long>(b) * p.pg.n_kv_heads * p.pg.capacity + pos;
-    const int page = p.pg.table[static_cast<size_t>(b) * p.pg.max_pages + (pos >> 4)];
-    if (page < 0 || page >= p.pg.n_pages)
-        return -1;
-    return static_cast<long long>(page) * p.pg.n_kv_heads * 16 + (pos & 15);
-}
 
 // The new rows are requested before their places are known (a chain of four loads), and the
 // warps find the places of the CTA's rows, one each, meanwhile.
@@ -754,11 +699,15 @@ cudaError_t launch_pages_compact(const PageParams &p, int32_t *n_used, const Pag
 cudaError_t launch_append_chunk(const ChunkParams &p, const void *k_new, const void *v_new, void *k,
                                 void *v, int n_layers, cudaStream_t stream)
 {
-    cudaError_t e = launch_pdl(append_chunk_kernel, dim3((p.n_rows + kChunkRows - 1) / kChunkRows, n_layers),
+    const cudaError_t e = launch_pdl(append_chunk_kernel, dim3((p.n_rows + kChunkRows - 1) / kChunkRows, n_layers),
                    dim3(256), 0, stream, p, static_cast<const uint4 *>(k_new),
                    static_cast<const uint4 *>(v_new), static_cast<uint4 *>(k), static_cast<uint4 *>(v));
-    if (e == cudaSuccess)
-        e = launch_pdl(advance_kernel, dim3(1), dim3(1024), 0, stream, p);
+    return e != cudaSuccess ? e : launch_advance(p, stream);
+}
+
+cudaError_t launch_advance(const ChunkParams &p, cudaStream_t stream)
+{
+    const cudaError_t e = launch_pdl(advance_kernel, dim3(1), dim3(1024), 0, stream, p);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
 

@@ -187,10 +187,28 @@ cudaError_t launch_pages_compact(const PageParams &p, int32_t *n_used, const Pag
                                  void *v, int n_layers, int grid, cudaStream_t stream);
 cudaError_t launch_append_chunk(const ChunkParams &p, const void *k_new, const void *v_new, void *k,
                                 void *v, int n_layers, cudaStream_t stream);
+cudaError_t launch_advance(const ChunkParams &p, cudaStream_t stream);
 cudaError_t launch_reorder_rows(const ReorderParams &p, void *k, void *v, int n_layers,
                                 int rows_per_head, const int32_t *rows, int rows_by_unit,
                                 cudaStream_t stream);
 cudaError_t launch_reorder_ints(const ReorderParams &p, cudaStream_t stream);
+
+// -------------------------------------------------------------------------- rotary positions
+
+struct RopeParams {
+    ChunkParams c;
+    int n_layers, n_q_heads;
+    const void *q, *k, *v;      // rows of heads, strides in elements; null: left out
+    long long q_stride, k_stride, v_stride;
+    void *q_out, *k_out;        // packed
+    void *k_cache, *v_cache;    // append: where k and v go (k_out is null)
+    const int32_t *pos;         // [n_rows] or null: the rows' positions in the cache
+    int rot, interleaved;
+    float amplitude, eps;
+    const uint64_t *turns;
+    const void *q_norm, *k_norm;
+};
+cudaError_t launch_rope(const RopeParams &p, int sms, cudaStream_t stream);
 
 // ------------------------------------------------------------------------------ beam search
 
@@ -212,6 +230,27 @@ struct BeamParams {
     int32_t *part_v;            // and their tokens (-1: none)
 };
 cudaError_t launch_beam_select(const BeamParams &p, cudaStream_t stream);
+
+// ---------------------------------------------------------------- log probabilities of tokens
+
+constexpr int kMaxTop = 32;
+
+struct ScoreParams {
+    int n_rows, vocab, logits_fp32, n_top, splits;
+    long long row_stride;
+    const void *logits;
+    const int32_t *token;
+    float *logprob;
+    int32_t *rank;
+    float *entropy;
+    int32_t *top_token;
+    float *top_logprob;
+    int *tickets;               // [rows that are split], zero between launches
+    float4 *part;               // [rows][splits]: reference, sum, entropy's sum, tokens in front
+    float *part_x;              // [rows][splits][n_top] best logits
+    int32_t *part_v;            // and their tokens (-1: none)
+};
+cudaError_t launch_score(const ScoreParams &p, cudaStream_t stream);
 
 // --------------------------------------------------------- attention with sinks and a window
 
@@ -238,6 +277,10 @@ struct WindowParams {
 cudaError_t launch_window(const WindowParams &p, int rows, const CUtensorMap &tm_k,
                           const CUtensorMap &tm_v, const CUtensorMap &tm_q, int grid,
                           cudaStream_t stream);
+// The same for rows that all see the whole of their sequence (n_sink and n_window are not read).
+cudaError_t launch_cross(const WindowParams &p, int rows, const CUtensorMap &tm_k,
+                         const CUtensorMap &tm_v, const CUtensorMap &tm_q, int grid,
+                         cudaStream_t stream);
 
 size_t attention_smem_bytes();
 // Fast-step attention with its split-KV scratch in a library-owned device array instead of
