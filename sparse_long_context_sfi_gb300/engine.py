@@ -12,12 +12,14 @@ import ctypes as C
 import numpy as np
 import torch
 
-from . import (SfiBeam, SfiBudget, SfiDecodePlan, SfiKvCache, SfiPagePool, SfiSparseMem,
-               sfi_append_chunk, sfi_append_kv, sfi_beam_select, sfi_beam_workspace_bytes,
-               sfi_compact, sfi_decode_run, sfi_dense_decode_attn, sfi_fast_decode_step,
-               sfi_pages_compact, sfi_pages_evict, sfi_pages_release, sfi_pages_reserve,
-               sfi_pages_workspace_bytes, sfi_reorder, sfi_schedule, sfi_schedule_tokens,
-               sfi_select, sfi_sparse_decode_attn, sfi_window_attn, sfi_window_workspace_bytes,
+from . import (SfiBeam, SfiBudget, SfiDecodePlan, SfiKvCache, SfiPagePool, SfiRope, SfiRopeRows,
+               SfiScoring, SfiSparseMem, sfi_append_chunk, sfi_append_kv, sfi_beam_select,
+               sfi_beam_workspace_bytes, sfi_compact, sfi_cross_attn, sfi_cross_workspace_bytes,
+               sfi_decode_run, sfi_dense_decode_attn, sfi_fast_decode_step, sfi_pages_compact,
+               sfi_pages_evict, sfi_pages_release, sfi_pages_reserve, sfi_pages_workspace_bytes,
+               sfi_reorder, sfi_rope_append, sfi_rope_apply, sfi_rope_turns, sfi_schedule,
+               sfi_schedule_tokens, sfi_score_tokens, sfi_scoring_workspace_bytes, sfi_select,
+               sfi_sparse_decode_attn, sfi_window_attn, sfi_window_workspace_bytes,
                sfi_workspace_bytes, sfi_workspace_init)
 
 
@@ -37,6 +39,21 @@ def _want(name, t, dtypes, shape, device):
         have = (f"{t.dtype} {tuple(t.shape)} on {t.device}" if isinstance(t, torch.Tensor) else type(t).__name__)
         raise ValueError(f"{name}: contiguous {' or '.join(map(str, dtypes))} {tuple(shape)} on {device}"
                          f" wanted, not {have}")
+
+
+def _want_rows(name, t, shape, device):
+    """Rows of heads that a rope call reads: packed heads, rows anywhere, as in a fused projection."""
+    if (not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16 or tuple(t.shape) != tuple(shape) or
+            t.device != device):
+        have = (f"{t.dtype} {tuple(t.shape)} on {t.device}" if isinstance(t, torch.Tensor) else type(t).__name__)
+        raise ValueError(f"{name}: torch.bfloat16 {tuple(shape)} on {device} wanted, not {have}")
+    layers, rows, heads, dim = shape
+    step = t.stride(1) if rows > 1 else max(heads * dim, t.stride(1))
+    if (t.stride(3) != 1 or (heads > 1 and t.stride(2) != dim) or step < heads * dim or step % 8 or
+            (layers > 1 and t.stride(0) != rows * step) or t.data_ptr() % 16):
+        raise ValueError(f"{name}: heads lie packed, rows a multiple of 8 elements apart and layers the rows apart,"
+                         f" on 16 bytes; not strides {t.stride()}")
+    return step
 
 
 _MASK = (torch.uint8, torch.bool)
@@ -82,6 +99,30 @@ class _Workspace:
         if not _capturing(stream):
             self.now = ws
         return ws
+
+
+class Rope:
+    """Rotary positions for the calls that take `rope`: frequencies on the device and what goes with
+    them. scaling, factor, original_len, low, high: as for sfi_rope_turns; q_norm, k_norm: weights
+    (bf16 [128]) of the norm that every head goes through first."""
+
+    def __init__(self, rot_dim=128, interleaved=False, base=10000.0, scaling="none", factor=1.0,
+                 original_len=0.0, low=1.0, high=32.0, q_norm=None, k_norm=None, norm_eps=1e-6, device="cuda"):
+        turns, self.amplitude = sfi_rope_turns(rot_dim, base, scaling, factor, original_len, low, high)
+        self.device = _at(device)
+        for name, w in (("q_norm", q_norm), ("k_norm", k_norm)):
+            if w is not None:
+                _want(name, w, torch.bfloat16, (128,), self.device)
+                if w.data_ptr() % 16:
+                    raise ValueError(f"{name}: lies on 16 bytes")
+        if (q_norm is not None or k_norm is not None) and not 0 < norm_eps < float("inf"):
+            raise ValueError("norm_eps is above zero and finite")
+        self.turns = torch.from_numpy(turns.view(np.int64)).to(self.device)
+        self.q_norm, self.k_norm = q_norm, k_norm
+        self.desc = SfiRope(rot_dim=rot_dim, interleaved=1 if interleaved else 0, amplitude=self.amplitude,
+                            norm_eps=norm_eps, turns=self.turns.data_ptr(),
+                            q_norm=None if q_norm is None else q_norm.data_ptr(),
+                            k_norm=None if k_norm is None else k_norm.data_ptr())
 
 
 class SfiState:
@@ -175,13 +216,45 @@ class SfiState:
 
     # -- one decode step through the individual calls -----------------------------------------
     def step(self, q, k_new, v_new, slow_b: np.ndarray, out, out_fp32=True, stream=None,
-             fused=True, active=None):
+             fused=True, active=None, rope=None, pos=None):
         """q [Ly][B][Hq][D] bf16, k_new/v_new [Ly][B][Hkv][D] bf16 (device); slow_b [B] bool.
         fused: the fast sequences' append runs inside sfi_fast_decode_step (as in the native
         driver); otherwise every row is appended first and the fast step is
         sfi_sparse_decode_attn. active: device uint8 [B], e.g. from reserve: the others are left as
-        they are (their rows of out, too)."""
+        they are (their rows of out, too). rope: q and k_new are turned to their positions first
+        (pos: device int32 [B], None: the lengths); rows may then be a fused projection's."""
+        if rope is not None:
+            q, k_new = self._turned(rope, q, k_new, pos, active, stream)
         return self._step(q, k_new, v_new, slow_b, None, active, out, out_fp32, stream, fused)
+
+    def _turned(self, rope, q, k_new, pos, active, stream):
+        """q and k_new of single tokens, turned."""
+        _here(self.device)
+        c, n = self.cfg, self.cfg.batch
+        self._masked(active)
+        io = self._rope_rows(rope, q, k_new, None, pos, n)
+        with torch.cuda.stream(_torch_stream(stream)):
+            q_out, k_out = (torch.empty((c.n_layers, n, h, c.head_dim), dtype=torch.bfloat16, device=self.device)
+                            for h in (c.n_q_heads, c.n_kv_heads))
+        io.q_out, io.k_out = q_out.data_ptr(), k_out.data_ptr()
+        sfi_rope_apply(self._whole(), rope.desc, io, None, n, 1, active=active, stream=stream)
+        return q_out, k_out
+
+    def _rope_rows(self, rope, q, k_new, v_new, pos, n):
+        """The rows that a rope call reads (v_new None: left out)."""
+        c, dev = self.cfg, self.device
+        if rope.device != dev:
+            raise ValueError(f"the rope is on {rope.device}, the state on {dev}")
+        io = SfiRopeRows(q=q.data_ptr(), k=k_new.data_ptr())
+        io.q_stride = _want_rows("q", q, (c.n_layers, n, c.n_q_heads, c.head_dim), dev)
+        io.k_stride = _want_rows("k_new", k_new, (c.n_layers, n, c.n_kv_heads, c.head_dim), dev)
+        if v_new is not None:
+            io.v = v_new.data_ptr()
+            io.v_stride = _want_rows("v_new", v_new, (c.n_layers, n, c.n_kv_heads, c.head_dim), dev)
+        if pos is not None:
+            _want("pos", pos, torch.int32, (n,), dev)
+            io.pos = pos.data_ptr()
+        return io
 
     def _step(self, q, k_new, v_new, slow_b, masks, active, out, out_fp32, stream, fused):
         """masks: slow_b and its complement on the device, if they are there already."""
@@ -406,13 +479,16 @@ class SfiState:
         sfi_pages_compact(self._whole(), pool, used, self._pages_ws, self._pages_bytes, stream=stream)
         return used
 
-    def prefill(self, q, k_new, v_new, rows, out, out_fp32=False, n_window=None, stream=None):
+    def prefill(self, q, k_new, v_new, rows, out, out_fp32=False, n_window=None, stream=None, rope=None,
+                pos=None):
         """One chunk of a prompt: rows[b] (host) new tokens of every sequence, packed in order of
         sequence. Reserves their pages (paged cache), appends k_new/v_new [Ly][n][Hkv][D] and
         attends q [Ly][n][Hq][D] under the sinks and a window of n_window (default: the
         budget's) into out [Ly][n][Hq][D]. A sequence that does not fit its capacity, or whose
         pages the pool does not cover, is left out (its rows of out, too), and the error word
-        says so. Copies rows to the device, so it cannot be captured."""
+        says so. rope: q and k_new are turned to their positions on the way (pos: device int32 [n],
+        None: the cache's); their rows, and v_new's, may then be a fused projection's. Copies rows
+        to the device, so it cannot be captured."""
         rows = np.asarray(rows, dtype=np.int32)
         if rows.shape != (self.cfg.batch,) or (rows < 0).any() or q.dim() != 4:
             raise ValueError("rows: a count for every sequence; q: [Ly][n][Hq][D]")
@@ -420,7 +496,7 @@ class SfiState:
         n, most = int(q.shape[1]), int(rows.max())
         if n < start[-1] or tuple(out.shape) != tuple(q.shape):
             raise ValueError("q and out hold the rows of every sequence")
-        self._chunk(n, q, k_new, v_new, out, out_fp32)
+        io = self._chunk(n, q, k_new, v_new, out, out_fp32, rope, pos)
         window = self.cfg.n_window if n_window is None else n_window
         with torch.cuda.stream(_torch_stream(stream)):
             dev = torch.from_numpy(start).to(self.device)
@@ -428,25 +504,24 @@ class SfiState:
                 active = served = self.reserve(torch.from_numpy(rows).to(self.device), stream=stream)
             else:
                 active, served = None, self._fitting(rows, None, stream)
-        sfi_append_chunk(self._whole(), k_new, v_new, dev, n, most, active=active, stream=stream)
+        q = self._append(q, k_new, v_new, dev, n, most, active, stream, rope, io)
         self._grown(rows)
         self._off_course = True
         self._window(q, out, out_fp32, dev, n, most, window, stream, served)
 
     def window_step(self, q, k_new, v_new, out, out_fp32=True, n_window=None, active=None,
-                    stream=None):
+                    stream=None, rope=None, pos=None):
         """One new token each, attended under the sinks and a window straight from the cache (no
         packed memory): q/out [Ly][B][Hq][D], k_new/v_new [Ly][B][Hkv][D]. A sequence without
-        room is left out, as by prefill."""
+        room is left out, as by prefill. rope, pos: as for prefill."""
         window = self.cfg.n_window if n_window is None else n_window
         self._masked(active)
-        self._chunk(self.cfg.batch, q, k_new, v_new, out, out_fp32)
+        io = self._chunk(self.cfg.batch, q, k_new, v_new, out, out_fp32, rope, pos)
         if self.page_table is not None:
             active = served = self.reserve(active=active, stream=stream)
         else:
             served = self._fitting(1, active, stream)
-        sfi_append_chunk(self._whole(), k_new, v_new, None, self.cfg.batch, 1, active=active,
-                         stream=stream)
+        q = self._append(q, k_new, v_new, None, self.cfg.batch, 1, active, stream, rope, io)
         self._grown(1)
         self.t += 1
         self._off_course = True
@@ -456,13 +531,31 @@ class SfiState:
         if active is not None:
             _want("active", active, _MASK, (self.cfg.batch,), self.device)
 
-    def _chunk(self, n, q, k_new, v_new, out, out_fp32):
-        """The arrays of a chunk of n rows."""
+    def _chunk(self, n, q, k_new, v_new, out, out_fp32, rope=None, pos=None):
+        """The arrays of a chunk of n rows; those of a rope call are returned."""
         c, dev = self.cfg, self.device
-        _want("q", q, torch.bfloat16, (c.n_layers, n, c.n_q_heads, c.head_dim), dev)
-        _want("k_new", k_new, torch.bfloat16, (c.n_layers, n, c.n_kv_heads, c.head_dim), dev)
-        _want("v_new", v_new, torch.bfloat16, (c.n_layers, n, c.n_kv_heads, c.head_dim), dev)
+        io = None
+        if rope is not None:
+            io = self._rope_rows(rope, q, k_new, v_new, pos, n)
+        else:
+            if pos is not None:
+                raise ValueError("pos goes with rope")
+            _want("q", q, torch.bfloat16, (c.n_layers, n, c.n_q_heads, c.head_dim), dev)
+            _want("k_new", k_new, torch.bfloat16, (c.n_layers, n, c.n_kv_heads, c.head_dim), dev)
+            _want("v_new", v_new, torch.bfloat16, (c.n_layers, n, c.n_kv_heads, c.head_dim), dev)
         _want("out", out, torch.float32 if out_fp32 else torch.bfloat16, q.shape, dev)
+        return io
+
+    def _append(self, q, k_new, v_new, start, n, most, active, stream, rope, io):
+        """The chunk's keys and values into the cache; returns the queries, turned where there is rope."""
+        if rope is None:
+            sfi_append_chunk(self._whole(), k_new, v_new, start, n, most, active=active, stream=stream)
+            return q
+        with torch.cuda.stream(_torch_stream(stream)):
+            turned = torch.empty(q.shape, dtype=torch.bfloat16, device=self.device)
+        io.q_out = turned.data_ptr()
+        sfi_rope_append(self._whole(), rope.desc, io, start, n, most, active=active, stream=stream)
+        return turned
 
     def _fitting(self, rows, active, stream):
         """Which of the active sequences of a contiguous cache have room for `rows` more (host int or
@@ -533,3 +626,138 @@ class BeamSearch:
         ws = self._ws.get(sfi_beam_workspace_bytes(beam), stream)
         sfi_beam_select(beam, ws, ws.numel(), stream=stream)
         return self.parent, self.token
+
+
+class EncoderStates:
+    """Keys and values of encoder inputs on the device, one sequence each, and the attention of a
+    decoder's rows to them. Rows of one input lie together: of a prompt's chunk, of its beams."""
+
+    def __init__(self, n_layers, batch, n_q_heads, n_kv_heads, capacity, device="cuda"):
+        self.n_layers, self.batch, self.n_q_heads, self.n_kv_heads = n_layers, batch, n_q_heads, n_kv_heads
+        self.capacity, self.device = capacity, _at(device)
+        dev = dict(device=self.device)
+        self.k, self.v = (torch.zeros((n_layers, batch, n_kv_heads, capacity, 128), dtype=torch.bfloat16, **dev)
+                          for _ in "kv")
+        self.seq_len = torch.zeros(batch, dtype=torch.int32, **dev)
+        self.err = torch.zeros(4, dtype=torch.int32, **dev)
+        self.lens = np.zeros(batch, dtype=np.int64)
+        self.kv = SfiKvCache(
+            n_layers=n_layers, batch=batch, n_q_heads=n_q_heads, n_kv_heads=n_kv_heads, head_dim=128,
+            capacity=capacity, page_size=0, n_pages=0, max_pages_per_seq=0, max_len=0, k=self.k.data_ptr(),
+            v=self.v.data_ptr(), page_table=None, seq_len=self.seq_len.data_ptr(), err=self.err.data_ptr())
+        self._ws = _Workspace(self.device)
+
+    def clear(self, which=None, stream=None):
+        """Empty the inputs of `which` (indices on the host; None: all)."""
+        _here(self.device)
+        which = list(range(self.batch)) if which is None else [int(i) for i in which]
+        if any(i < 0 or i >= self.batch for i in which):
+            raise ValueError(f"inputs are numbered from 0 to {self.batch - 1}")
+        if _capturing(stream):
+            raise ValueError("the host keeps the lengths: no changes in a capture")
+        with torch.cuda.stream(_torch_stream(stream)):
+            if len(which) == self.batch:
+                self.seq_len.zero_()
+            elif which:
+                self.seq_len[torch.tensor(which).to(self.device)] = 0
+        self.lens[which] = 0
+
+    def write(self, k_new, v_new, rows, stream=None):
+        """rows[e] (host) further states of every input, packed: k_new, v_new [Ly][n][Hkv][128]."""
+        _here(self.device)
+        rows = np.asarray(rows, dtype=np.int32)
+        if rows.shape != (self.batch,) or (rows < 0).any():
+            raise ValueError("rows: a count for every input")
+        if (self.lens + rows).max() > self.capacity:
+            raise ValueError(f"an input of more than {self.capacity} states")
+        n = int(rows.sum())
+        for name, t in (("k_new", k_new), ("v_new", v_new)):
+            _want(name, t, torch.bfloat16, (self.n_layers, n, self.n_kv_heads, 128), self.device)
+        if _capturing(stream):
+            raise ValueError("the host keeps the lengths: no changes in a capture")
+        start = np.concatenate([[0], np.cumsum(rows)]).astype(np.int32)
+        with torch.cuda.stream(_torch_stream(stream)):
+            dev = torch.from_numpy(start).to(self.device)
+        self.kv.max_len = int(self.lens.max())
+        sfi_append_chunk(self.kv, k_new, v_new, dev, n, int(rows.max()), stream=stream)
+        self.lens += rows
+
+    def attend(self, q, out, rows=1, out_fp32=False, active=None, stream=None):
+        """q [Ly][n][Hq][128] to all states of their input, into out [Ly][n][Hq][128]: rows[e] rows of
+        every input (host; an int: as many of each, which can be captured). active: device uint8
+        [inputs]. Rows behind the last, and of inputs that are not active, are left as they are."""
+        _here(self.device)
+        each = isinstance(rows, (int, np.integer))
+        counts = np.full(self.batch, rows, dtype=np.int64) if each else np.asarray(rows, dtype=np.int64)
+        if counts.shape != (self.batch,) or (counts < 0).any() or not isinstance(q, torch.Tensor) or q.dim() != 4:
+            raise ValueError("rows: a count for every input; q: [Ly][n][Hq][128]")
+        n, most = int(q.shape[1]), int(counts.max())
+        if counts.sum() > n:
+            raise ValueError("q holds the rows of every input")
+        _want("q", q, torch.bfloat16, (self.n_layers, n, self.n_q_heads, 128), self.device)
+        _want("out", out, torch.float32 if out_fp32 else torch.bfloat16, q.shape, self.device)
+        if active is not None:
+            _want("active", active, _MASK, (self.batch,), self.device)
+        if most == 0:
+            return
+        start = None
+        if not (each and rows == 1 and n == self.batch):
+            with torch.cuda.stream(_torch_stream(stream)):
+                if each:
+                    start = torch.arange(0, (self.batch + 1) * most, most, dtype=torch.int32, device=self.device)
+                else:
+                    start = torch.from_numpy(np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)).to(self.device)
+        # (a captured call is replayed when other inputs may have been written)
+        self.kv.max_len = self.capacity if _capturing(stream) else int(self.lens.max())
+        ws = self._ws.get(sfi_cross_workspace_bytes(self.kv, n, most), stream)
+        sfi_cross_attn(self.kv, q, out, out_fp32, start, n, most, ws, ws.numel(), active=active, stream=stream)
+
+
+class TokenScores:
+    """Log probabilities of tokens under rows of logits."""
+
+    def __init__(self, device="cuda"):
+        self.device = _at(device)
+        self._ws = _Workspace(self.device)
+
+    def score(self, logits, token=None, n_top=0, rank=False, entropy=False, stream=None):
+        """logits [rows][vocab] (bf16 or fp32, rows may be strided), token: device int32 [rows] (below 0:
+        none). Returns a dict of what was asked for: logprob [rows] (with token), rank [rows], entropy
+        [rows], top_token and top_logprob [rows][n_top], as sfi_score_tokens defines them."""
+        if not isinstance(logits, torch.Tensor) or logits.dim() != 2 or logits.shape[1] < 1 or logits.stride(1) != 1:
+            raise ValueError("logits are [rows][vocab] with contiguous rows")
+        if logits.dtype not in (torch.bfloat16, torch.float32):
+            raise ValueError("logits are bf16 or fp32")
+        if logits.device != self.device:
+            raise ValueError(f"logits are on {logits.device}, the scores on {self.device}")
+        _here(self.device)
+        rows, vocab = logits.shape
+        stride = logits.stride(0) if rows > 1 else vocab
+        if stride < vocab:
+            raise ValueError("rows of logits do not overlap")
+        if token is not None:
+            _want("token", token, torch.int32, (rows,), self.device)
+        elif rank:
+            raise ValueError("a rank goes with a token")
+        if not 0 <= n_top <= min(32, vocab):
+            raise ValueError("n_top is at most 32 and the vocabulary")
+        if token is None and not entropy and not n_top:
+            raise ValueError("nothing is asked for")
+        with torch.cuda.stream(_torch_stream(stream)):
+            new = lambda kind, *shape: torch.empty(shape, dtype=kind, device=self.device)
+            out = {}
+            if token is not None:
+                out["logprob"] = new(torch.float32, rows)
+            if rank:
+                out["rank"] = new(torch.int32, rows)
+            if entropy:
+                out["entropy"] = new(torch.float32, rows)
+            if n_top:
+                out["top_token"], out["top_logprob"] = new(torch.int32, rows, n_top), new(torch.float32, rows, n_top)
+        sc = SfiScoring(n_rows=rows, vocab=vocab, logits_fp32=1 if logits.dtype == torch.float32 else 0, n_top=n_top,
+                        row_stride=stride, logits=logits.data_ptr(),
+                        token=None if token is None else token.data_ptr(),
+                        **{name: t.data_ptr() for name, t in out.items()})
+        ws = self._ws.get(sfi_scoring_workspace_bytes(sc), stream)
+        sfi_score_tokens(sc, ws, ws.numel(), stream=stream)
+        return out
