@@ -675,7 +675,7 @@ sfi_status sfi_beam_select(const sfi_beam *beam, void *ws, size_t ws_bytes, void
  * rank -1 and top tokens -1. Sums of terms in fp32, relative to the row's highest logit.
  *   logits       bf16, or fp32 if logits_fp32: [n_rows] of vocab, row_stride elements apart
  *   token        device int32 [n_rows] or NULL: no token (logprob and rank must be NULL then)
- * 0 <= n_top <= 32 (else SFI_ERR_UNSUPPORTED) and n_top <= vocab; vocab <= 2^30; n_rows >= 0.
+ * 0 <= n_top <= 32 (else SFI_ERR_UNSUPPORTED) and n_top <= vocab; vocab and n_rows up to 2^30.
  */
 typedef struct sfi_scoring {
     int32_t n_rows, vocab, logits_fp32, n_top;

@@ -3,18 +3,25 @@
 //     s = sum 2^(x log2 e - R),  t = sum (x log2 e - R) 2^(x log2 e - R),
 //     lse = (R + log2 s) ln 2,   entropy = ln s - ln 2 * t / s,
 // both kept relative to each lane's own running reference and moved by 2^(R - R') when that grows
-// (t also by s (R - R')). The rank counts the tokens in front of the given one on the way; the best
-// tokens are collected as in beam.cu.
+// (t also by s (R - R')). The rank counts the tokens in front of the given one on the way.
 //
-// The bytes of the logits bound it (the floor). A CTA has a row, or the splits of a row one each
-// where there are few, of which the last to finish joins them.
+// The bytes of the logits bound it, and right behind them issue slots: at the copy rate there are 11
+// for a token of bf16. A pass over one takes 5 (unpacked, a packed multiply-add, an exponential, packed
+// sums, and half an instruction of a packed maximum), the rank 1 (pairs compared and counted as
+// pairs), entropy 1, the list of the best nothing: it is made behind the pass, of the few lanes whose
+// highest logits say that they hold one of them. What is left is a row's end, a chain of barriers and
+// reductions: 8192 rows of 32000 bf16 take 84 us (6.2 TB/s) with the log probability alone, 124 with rank,
+// entropy and 3 alternatives (260 with a sorted list kept on the way, a comparison of two conditions
+// per token for the rank and 8 warps per row); 2048 rows of 128001 85 us (6.2 TB/s); 256 rows of 128001 fp32 29
+// (4.6 TB/s), 39 with everything and 20 alternatives. Tried: CTAs that go on to further rows, with
+// the next row's first loads under way while one is finished (198 instead of 151 then: spills, and
+// warps that wait for the one that finishes).
 #include "vocab.cuh"
 
 namespace sfi {
 namespace {
 
-constexpr int kScoreThreads = 256;
-constexpr int kScoreWarps = kScoreThreads / 32;
+constexpr int kScoreWarps = 8;              // most warps of a CTA
 // -150 is below every power that 32 bits hold: a term of it adds nothing, and 0 * -inf does not arise
 constexpr float kNothing = -150.f;
 
@@ -47,173 +54,339 @@ __device__ __forceinline__ Sums join(const Sums &a, const Sums &b)
     return o;
 }
 
-template <typename T, bool TOP, bool RANK, bool ENT>
-__global__ void __launch_bounds__(kScoreThreads, 4) score_kernel(const ScoreParams p)
+__device__ __forceinline__ float max3(float a, float b, float c)
 {
-    // candidates that wait to be inserted, in any order: fewer than 32 and a chunk's
-    __shared__ float cand_x[TOP ? kScoreWarps : 1][TOP ? 32 * kLaneTok + 32 : 1];
-    __shared__ int cand_v[TOP ? kScoreWarps : 1][TOP ? 32 * kLaneTok + 32 : 1], n_cand[kScoreWarps];
-    __shared__ float sh_x[TOP ? kMaxTop : 1][kScoreWarps];
-    __shared__ int sh_v[TOP ? kMaxTop : 1][kScoreWarps];
-    __shared__ volatile int top[kScoreWarps];        // (as order())
-    __shared__ Sums sh_sums[kScoreWarps];
-    __shared__ int sh_last;
-    constexpr int V = Chunk<T>::kV;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int K = p.n_top;
-    const int row = p.splits == 1 ? blockIdx.x : blockIdx.x / p.splits;
-    const int split = p.splits == 1 ? 0 : blockIdx.x - row * p.splits;
-    if (TOP && tid < kScoreWarps) {
-        top[tid] = order(-CUDART_INF_F);
-        n_cand[tid] = 0;
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+// A lane's share of a chunk: four pieces of 16 bytes, 32 pieces apart, as they lie in memory. How its
+// highest logit is found, how many tokens reach a threshold, and its terms of the sums.
+template <typename T>
+struct Part;
+
+template <>
+struct Part<float> {
+    static constexpr int kV = 4;
+    uint64_t n = 0;             // tokens counted, as floats (exact: a lane sees fewer than 2^24 of a row)
+
+    static __device__ __forceinline__ float value(uint32_t u) { return __uint_as_float(u); }
+    static __device__ __forceinline__ float highest(const uint4 *w)     // (max drops NaN)
+    {
+        float m = fmaxf(value(w[0].x), value(w[0].y));
+        m = max3(m, value(w[0].z), value(w[0].w));
+#pragma unroll
+        for (int i = 1; i < 4; ++i)
+            m = max3(max3(m, value(w[i].x), value(w[i].y)), value(w[i].z), value(w[i].w));
+        return m;
     }
+    __device__ __forceinline__ void count(const uint4 &w, float least)
+    {
+        float f[4];
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            asm("set.ge.f32.f32 %0, %1, %2;" : "=f"(f[i]) : "f"(value(u[i])), "f"(least));
+        n = add2(add2(n, pack2(f[0], f[1])), pack2(f[2], f[3]));
+    }
+    __device__ __forceinline__ void settle() {}
+    __device__ __forceinline__ int counted() const
+    {
+        const float2 v = unpack2(n);
+        return static_cast<int>(v.x) + static_cast<int>(v.y);
+    }
+    // the terms of one piece: powers into acc, and times their exponents into ent
+    struct Low {
+        __device__ __forceinline__ explicit Low(float) {}
+    };
+    template <bool ENT>
+    static __device__ __forceinline__ void terms(const uint4 &w, Low, uint64_t c2, uint64_t r2, uint64_t &acc,
+                                                 uint64_t &ent)
+    {
+        const uint64_t x[2] = {pack2(value(w.x), value(w.y)), pack2(value(w.z), value(w.w))};
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const float2 z = unpack2(fma2(x[i], c2, r2));
+            const uint64_t e = pack2(ex2(z.x), ex2(z.y));
+            acc = add2(acc, e);
+            // (no 0 * -inf; a NaN is in acc)
+            if (ENT)
+                ent = fma2(e, pack2(fmaxf(z.x, kNothing), fmaxf(z.y, kNothing)), ent);
+        }
+    }
+};
+
+// Two tokens at a time where bf16 does: 16 instructions for 32 tokens' maximum, 32 to count them.
+template <>
+struct Part<__nv_bfloat16> {
+    static constexpr int kV = 8;
+    __nv_bfloat162 n = __floats2bfloat162_rn(0.f, 0.f);
+    int chunks = 0, all = 0;
+
+    static __device__ __forceinline__ __nv_bfloat162 pair(uint32_t u) { return *reinterpret_cast<const __nv_bfloat162 *>(&u); }
+    static __device__ __forceinline__ float highest(const uint4 *w)
+    {
+        __nv_bfloat162 m = __hmax2(__hmax2(pair(w[0].x), pair(w[0].y)), __hmax2(pair(w[0].z), pair(w[0].w)));
+#pragma unroll
+        for (int i = 1; i < 4; ++i)
+            m = __hmax2(m, __hmax2(__hmax2(pair(w[i].x), pair(w[i].y)), __hmax2(pair(w[i].z), pair(w[i].w))));
+        const float2 f = __bfloat1622float2(m);
+        return fmaxf(f.x, f.y);
+    }
+    __device__ __forceinline__ void count(const uint4 &w, float least)
+    {
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+        const __nv_bfloat162 l = __float2bfloat162_rn(least);       // (exact)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            n = __hadd2(n, __hge2(pair(u[i]), l));
+    }
+    __device__ __forceinline__ void settle()
+    {
+        if (++chunks == 15)         // bf16 counts to 256: 16 in each half of a chunk
+            flush();
+    }
+    __device__ __forceinline__ void flush()
+    {
+        const float2 v = __bfloat1622float2(n);
+        all += static_cast<int>(v.x) + static_cast<int>(v.y);
+        n = __floats2bfloat162_rn(0.f, 0.f);
+        chunks = 0;
+    }
+    __device__ __forceinline__ int counted()
+    {
+        flush();
+        return all;
+    }
+    // Logits below 150 powers under the reference are lifted to there (rounded down): they add
+    // nothing either way, and -inf no 0 * -inf. NaN stays.
+    struct Low {
+        __nv_bfloat162 x;
+        __device__ __forceinline__ explicit Low(float rn)
+        {
+            const __nv_bfloat16 l = __float2bfloat16_rd((4.f * rn + kNothing) * (1.f / kLog2e));
+            x = __halves2bfloat162(l, l);
+        }
+    };
+    template <bool ENT>
+    static __device__ __forceinline__ void terms(const uint4 &w, const Low &low, uint64_t c2, uint64_t r2,
+                                                 uint64_t &acc, uint64_t &ent)
+    {
+        uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (ENT) {
+                const __nv_bfloat162 m = __hmax2_nan(pair(u[i]), low.x);
+                u[i] = *reinterpret_cast<const uint32_t *>(&m);
+            }
+            const uint64_t z2 = fma2(pack2(__uint_as_float(u[i] << 16), __uint_as_float(u[i] & 0xffff0000u)), c2, r2);
+            const float2 z = unpack2(z2);
+            const uint64_t e = pack2(ex2(z.x), ex2(z.y));
+            acc = add2(acc, e);
+            if (ENT)
+                ent = fma2(e, z2, ent);
+        }
+    }
+};
+
+// A chunk that reaches over an end of the row.
+template <typename T>
+__device__ __noinline__ void load_edge(const T *row, int shift, int vocab, int piece, uint4 *w)
+{
+    load_pieces<T, 4>(row, shift, vocab, piece, w);
+}
+
+// The terms of a chunk whose reference is from kLarge on, of either sign, or -inf, or whose logits
+// are not numbers: what vocab.cuh says, one by one.
+template <typename T>
+__device__ __noinline__ Sums odd_chunk(Sums a, float cm, const uint4 *w)
+{
+    constexpr int V = Part<T>::kV;
+    const float rm = cm > -CUDART_INF_F ? fmaxf(a.R, reference(cm)) : a.R;
+    if (a.s != 0.f && rm > a.R) {
+        const float d = 4.f * (a.R - rm), f = ex2(d);
+        a.t = f != 0.f ? (a.t + a.s * d) * f : 0.f;
+        a.s *= f;
+    }
+    a.R = rm;
+#pragma unroll 1
+    for (int i = 0; i < 4; ++i) {
+        float x[V];
+        Chunk<T>::unpack(w[i], x);
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const float z = 4.f * (reference(x[j]) - rm), e = ex2(z);
+            a.s += x[j] > -CUDART_INF_F ? e : x[j] == x[j] ? 0.f : CUDART_NAN_F;
+            if (e != 0.f && x[j] > -CUDART_INF_F)
+                a.t += e * z;
+        }
+    }
+    return a;
+}
+
+// The best K of a list b and n further candidates.
+__device__ __noinline__ Best merged(Best b, const volatile float *x, const volatile int *v, int n, int K, int lane)
+{
+    for (int i = 0; i < n; i += 32) {
+        const float cx = i + lane < n ? x[i + lane] : -CUDART_INF_F;
+        const int cv = i + lane < n ? v[i + lane] : -1;
+        if (i == 0 && b.tv < 0 && !__any_sync(kAll, b.v >= 0))
+            b.start(cx, cv, K, lane);
+        else
+            b.offer(cx, cv, K, lane);
+    }
+    return b;
+}
+
+// The lowest value of the type above x (not NaN).
+__device__ __forceinline__ float above(float x, float)
+{
+    const int i = __float_as_int(x);
+    return x == 0.f ? __int_as_float(1) : __int_as_float(i < 0 ? i - 1 : i + 1);
+}
+__device__ __forceinline__ float above(float x, __nv_bfloat16)
+{
+    const int i = __float_as_int(x);
+    return x == 0.f ? __int_as_float(1 << 16) : __int_as_float(i < 0 ? i - (1 << 16) : i + (1 << 16));
+}
+
+// A row, or a split of one, as its CTA sees it.
+template <typename T>
+struct Place {
+    const T *x;
+    int shift, pieces;      // tokens in front of the row in its first 16-byte piece; pieces of the row
+    int row, split;
+
+    __device__ __forceinline__ Place(const ScoreParams &p, int item)
+    {
+        row = p.splits == 1 ? item : item / p.splits;
+        split = item - row * p.splits;
+        x = static_cast<const T *>(p.logits) + static_cast<size_t>(row) * p.row_stride;
+        shift = static_cast<int>((reinterpret_cast<uintptr_t>(x) & 15u) / sizeof(T));
+        pieces = (p.vocab + shift + Chunk<T>::kV - 1) / Chunk<T>::kV;
+    }
+};
+
+constexpr int kBuffer = 256;        // of the tokens that may be among the best
+constexpr int kAlone = 64;          // pieces that the first warp looks through by itself
+
+// Every lane keeps the highest logit of its chunks, which chunk it is, and the highest of all
+// others. K lanes have a logit of `least`, the K-th highest lane's, or more, so all of the K best
+// tokens do, and they lie in the lanes that reach it: few, of which the one chunk is read again
+// (from L2), or where another one reaches `least`, too, all of the lane's.
+template <typename T, bool TOP, bool RANK, bool ENT>
+__global__ void __launch_bounds__(32 * kScoreWarps, 4) score_kernel(const ScoreParams p)
+{
+    __shared__ float lane_m1[TOP ? 32 * kScoreWarps : 1], lane_m2[TOP ? 32 * kScoreWarps : 1];
+    __shared__ int lane_c1[TOP ? 32 * kScoreWarps : 1];
+    __shared__ uint8_t lanes[TOP ? 64 * kScoreWarps : 1];       // those that reach `least`: with one chunk, with all
+    __shared__ int n_one, n_all, n_cand;
+    __shared__ float sh_least;
+    __shared__ float cand_x[TOP ? kBuffer : 1], sh_x[TOP ? kMaxTop * kScoreWarps : 1];
+    __shared__ int cand_v[TOP ? kBuffer : 1], sh_v[TOP ? kMaxTop * kScoreWarps : 1];
+    __shared__ Sums sh_sums[kScoreWarps];
+    constexpr int V = Part<T>::kV, kPieces = 4;
+    constexpr int kStep = 32 * kPieces;             // pieces per chunk
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
+    const int K = p.n_top, stride = p.splits * warps * kStep;
     pdl_trigger();
     pdl_wait();
-    const T *x0 = static_cast<const T *>(p.logits) + static_cast<size_t>(row) * p.row_stride;
-    const int given = p.token ? p.token[row] : -1;
-    const bool has = given >= 0 && given < p.vocab;
-    const float xg = has ? static_cast<float>(x0[given]) : CUDART_NAN_F;
-    if (TOP)
-        __syncthreads();
-    const int shift = static_cast<int>((reinterpret_cast<uintptr_t>(x0) & 15u) / sizeof(T));
-    const int pieces = (p.vocab + shift + V - 1) / V;
-    constexpr int kStep = 32 * (kLaneTok / V);               // pieces per chunk
-    Best best;
-    best.clear();
-    bool fresh = true;          // (the same in every lane, as is all that decides a branch here)
-    int mine = order(-CUDART_INF_F);    // the warp's highest logit
-    // the candidates that wait go into the list, without those that the CTA's bound has passed
-    auto insert_waiting = [&] {
-        __syncwarp();
-        const int n = n_cand[warp];
-        const float floor = unorder(__reduce_min_sync(kAll, top[lane & (kScoreWarps - 1)]));
-        for (int i = 0; i < n; i += 32) {
-            const float cx = i + lane < n ? cand_x[warp][i + lane] : -CUDART_INF_F;
-            best.offer(cx, i + lane < n && cx >= floor ? cand_v[warp][i + lane] : -1, K, lane);
-        }
-        __syncwarp();
-        if (lane == 0)
-            n_cand[warp] = 0;
-        if (K > kScoreWarps && lane == (K - 1) / kScoreWarps)
-            top[warp] = order(best.x);
-        __syncwarp();
+    const Place<T> at(p, blockIdx.x);
+    const int first = (at.split * warps + warp) * kStep;
+    // chunks [in0, in1) lie within the row
+    const int in0 = at.shift > 0 ? 1 : 0, in1 = (p.vocab + at.shift) / V - kStep;
+    const uint4 *base = reinterpret_cast<const uint4 *>(at.x - at.shift) + lane;
+    uint4 w[kPieces];
+    auto edge = [&](int c) {            // (through a copy, which may lie in memory)
+        uint4 t[kPieces];
+        load_edge(at.x, at.shift, p.vocab, c + lane, t);
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i)
+            w[i] = t[i];
     };
+    if (first < at.pieces) {
+        if (first >= in0 && first <= in1) {
+#pragma unroll
+            for (int i = 0; i < kPieces; ++i)
+                w[i] = __ldcs(base + first + 32 * i);
+        } else {
+            edge(first);
+        }
+    }
+    const int given = p.token ? p.token[at.row] : -1;
+    const bool has = given >= 0 && given < p.vocab;
+    const float xg = has ? static_cast<float>(at.x[given]) : CUDART_NAN_F;
+    // The tokens in front of the given one: up to its own piece those not below it, behind it
+    // those above it. What its own piece has from it on is taken off again (with a given logit of
+    // -inf that is also what lies beyond the row's ends, which counts as -inf).
+    const int given_piece = RANK && has ? (given + at.shift) / V : -1;
+    const float xa = RANK && has ? above(xg, T()) : CUDART_NAN_F;
+    const int behind = given_piece * V - at.shift + lane;
+    const bool counted = RANK && has && at.split == 0 && warp == 0 && lane < V && behind >= given;
+    const float xb = counted && behind < p.vocab ? static_cast<float>(at.x[behind]) : -CUDART_INF_F;
+    Part<T> part;
     Sums a = {-CUDART_INF_F, 0.f, 0.f, 0};
-    int c = (split * kScoreWarps + warp) * kStep;
-    const int stride = p.splits * kScoreWarps * kStep;
-    uint4 w[kLaneTok / V];
-    if (c < pieces)
-        load_chunk(x0, shift, p.vocab, c, lane, w);
-    for (; c < pieces; c += stride) {
-        float x[kLaneTok];
+    float m1 = -CUDART_INF_F, m2 = -CUDART_INF_F;
+    int c1 = first;
+    for (int c = first; c < at.pieces; c += stride) {
+        const float cm = Part<T>::highest(w);
+        if (TOP) {
+            const bool up = cm > m1;
+            m2 = fmaxf(m2, up ? m1 : cm);
+            m1 = up ? cm : m1;
+            c1 = up ? c : c1;
+        }
+        if (RANK) {
 #pragma unroll
-        for (int i = 0; i < kLaneTok / V; ++i)
-            Chunk<T>::unpack(w[i], x + V * i);
-        if (c + stride < pieces)
-            load_chunk(x0, shift, p.vocab, c + stride, lane, w);
-        const int v0 = (c + lane) * V - shift;
-        // (tokens grow with j, so the first of equal logits is the lowest token)
-        auto token = [&](int j) { return v0 + 32 * V * (j / V) + j % V; };
-        float cm = -CUDART_INF_F;       // (fmaxf drops NaN)
-#pragma unroll
-        for (int j = 0; j < kLaneTok; ++j)
-            cm = fmaxf(cm, x[j]);
+            for (int i = 0; i < kPieces; ++i)
+                part.count(w[i], c + 32 * i + lane <= given_piece ? xg : xa);
+            part.settle();
+        }
         const float rn = fmaxf(a.R, cm * kLog2e4);
-        if (fabsf(rn) < kLarge * kLog2e4) {
-            if (a.s != 0.f) {
-                const float d = 4.f * (a.R - rn), f = ex2(d);
-                if (ENT)
-                    a.t = (a.t + a.s * d) * f;
-                a.s *= f;
-                if (ENT && f == 0.f)
-                    a.t = 0.f;          // (d may be beyond what 32 bits hold)
-            }
-            a.R = rn;
-            const uint64_t c2 = pack2(kLog2e, kLog2e), r2 = pack2(-4.f * rn, -4.f * rn);
-            uint64_t acc = 0, ent = 0;
+        const bool usual = fabsf(rn) < kLarge * kLog2e4;
+        if (!usual) {
+            uint4 copy[kPieces];
 #pragma unroll
-            for (int j = 0; j < kLaneTok; j += 2) {
-                float2 z = unpack2(fma2(pack2(x[j], x[j + 1]), c2, r2));
-                const uint64_t e = pack2(ex2(z.x), ex2(z.y));
-                acc = add2(acc, e);
-                if (ENT)
-                    ent = fma2(e, pack2(fmaxf(z.x, kNothing), fmaxf(z.y, kNothing)), ent);
-            }
+            for (int i = 0; i < kPieces; ++i)
+                copy[i] = w[i];
+            a = odd_chunk<T>(a, cm, copy);
+        } else if (rn > a.R) {
+            const float d = 4.f * (a.R - rn), f = ex2(d);
+            if (ENT)                // (d may be beyond what 32 bits hold)
+                a.t = f != 0.f ? (a.t + a.s * d) * f : 0.f;
+            a.s *= f;
+            a.R = rn;
+        }
+        // each piece's successor is asked for when its tokens are in registers: 64 bytes a lane are on
+        // their way (32 are too few to keep HBM busy)
+        const int cn = c + stride;
+        const bool inner = cn <= in1;
+        const uint64_t c2 = pack2(kLog2e, kLog2e), r2 = pack2(-4.f * rn, -4.f * rn);
+        const typename Part<T>::Low low(usual ? rn : 0.f);
+        uint64_t acc = 0, ent = 0;
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) {
+            const uint4 x = w[i];
+            if (inner)
+                w[i] = __ldcs(base + cn + 32 * i);
+            Part<T>::template terms<ENT>(x, low, c2, r2, acc, ent);
+        }
+        if (usual) {
             const float2 s2 = unpack2(acc);
             a.s += s2.x + s2.y;
             if (ENT) {
                 const float2 t2 = unpack2(ent);
                 a.t += t2.x + t2.y;
             }
-        } else {
-            // a largest logit from kLarge on, of either sign, or -inf alone, or NaN or +inf, which
-            // have to show in the sum
-            const float rm = cm > -CUDART_INF_F ? fmaxf(a.R, reference(cm)) : a.R;
-            if (a.s != 0.f && rm > a.R) {
-                const float d = 4.f * (a.R - rm), f = ex2(d);
-                a.t = ENT && f != 0.f ? (a.t + a.s * d) * f : 0.f;
-                a.s *= f;
-            }
-            a.R = rm;
-#pragma unroll
-            for (int j = 0; j < kLaneTok; ++j) {
-                const float z = 4.f * (reference(x[j]) - rm), e = ex2(z);
-                a.s += x[j] > -CUDART_INF_F ? e : x[j] == x[j] ? 0.f : CUDART_NAN_F;
-                if (ENT && e != 0.f && x[j] > -CUDART_INF_F)
-                    a.t += e * z;
-            }
         }
-        if (RANK) {
-#pragma unroll
-            for (int j = 0; j < kLaneTok; ++j) {
-                // (what lies beyond the row's ends is -inf, and may be equal to the token's)
-                const int v = token(j);
-                a.front += x[j] > xg || (x[j] == xg && v < given && v >= 0) ? 1 : 0;
-            }
-        }
-        if (TOP) {
-            // Tokens that beat the K-th best so far; see beam.cu.
-            const float floor = unorder(__reduce_min_sync(kAll, top[lane & (kScoreWarps - 1)]));
-            if (__any_sync(kAll, cm >= floor && (cm > best.tx || best.tv < 0))) {
-                if (K <= kScoreWarps) {
-                    mine = max(mine, __reduce_max_sync(kAll, order(cm)));
-                    if (lane == 0)
-                        top[warp] = mine;
-                }
-                int taken = -1;
-                if (fresh) {
-                    float cx = -CUDART_INF_F;
-#pragma unroll
-                    for (int j = kLaneTok - 1; j >= 0; --j) {
-                        if (x[j] >= cx && token(j) >= 0 && token(j) < p.vocab) {
-                            cx = x[j];
-                            taken = token(j);
-                        }
-                    }
-                    best.start(cx, taken, K, lane);
-                }
-                const float least = fmaxf(floor, best.tx);
-#pragma unroll
-                for (int j = 0; j < kLaneTok; ++j) {
-                    if (x[j] >= least) {
-                        const int v = token(j);
-                        if (v != taken && v >= 0 && v < p.vocab) {
-                            const int at = atomicAdd(&n_cand[warp], 1);
-                            cand_x[warp][at] = x[j];
-                            cand_v[warp][at] = v;
-                        }
-                    }
-                }
-                __syncwarp();
-                if (fresh || n_cand[warp] >= 32)
-                    insert_waiting();
-                fresh = false;
-            }
-        }
+        if (!inner && cn < at.pieces)
+            edge(cn);
     }
-    if (TOP)
-        insert_waiting();
-    // the warp's sums
+    if (RANK)
+        a.front = part.counted() - (counted && xb == xg ? 1 : 0) -
+                  (has && xg == -CUDART_INF_F && at.split == 0 && tid == 0 ? at.shift : 0);
+    // the sums of the warp, of the CTA
     auto warp_join = [&](Sums v) {
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) {
@@ -226,69 +399,165 @@ __global__ void __launch_bounds__(kScoreThreads, 4) score_kernel(const ScorePara
         }
         return v;
     };
+    const Sums none = {-CUDART_INF_F, 0.f, 0.f, 0};
     a = warp_join(a);
     if (lane == 0)
         sh_sums[warp] = a;
-    if (TOP && lane < K) {
-        sh_x[lane][warp] = best.x;
-        sh_v[lane][warp] = best.v;
+    Best best;
+    best.clear();
+    if (TOP) {
+        lane_m1[tid] = m1;
+        lane_m2[tid] = m2;
+        lane_c1[tid] = c1;
     }
     __syncthreads();
-    const Sums none = {-CUDART_INF_F, 0.f, 0.f, 0};
-    if (warp == 0) {
-        a = warp_join(lane < kScoreWarps ? sh_sums[lane] : none);
-        if (TOP) {
-            // all warps' j-th before any (j + 1)-th, so that the first 32 settle most
-            best.clear();
-            best.start((&sh_x[0][0])[lane], lane < K * kScoreWarps ? (&sh_v[0][0])[lane] : -1, K, lane);
-            for (int i = 32; i < K * kScoreWarps; i += 32)
-                best.offer((&sh_x[0][0])[min(i + lane, K * kScoreWarps - 1)],
-                           i + lane < K * kScoreWarps ? (&sh_v[0][0])[i + lane] : -1, K, lane);
-        }
-    }
-    if (p.splits > 1) {
+    if (TOP) {
         if (warp == 0) {
-            const size_t part = static_cast<size_t>(row) * p.splits + split;
-            if (lane == 0)
-                p.part[part] = make_float4(a.R, a.s, a.t, __int_as_float(a.front));
-            if (TOP && lane < K) {
-                const size_t at = (static_cast<size_t>(row) * K + lane) * p.splits + split;
-                p.part_x[at] = best.x;
-                p.part_v[at] = best.v;
+            float h[kScoreWarps], hm = -CUDART_INF_F;
+#pragma unroll
+            for (int i = 0; i < kScoreWarps; ++i) {
+                h[i] = i < warps ? lane_m1[32 * i + lane] : -CUDART_INF_F;
+                hm = fmaxf(hm, h[i]);
             }
-            __threadfence();
+            float least = -CUDART_INF_F;
+            int left = K;
+            while (left > 0) {          // the highest are taken out, one of each lane that holds it
+                least = unorder(__reduce_max_sync(kAll, order(hm)));
+                if (least == -CUDART_INF_F)
+                    break;
+                const bool mine = hm == least;
+                left -= __popc(__ballot_sync(kAll, mine));
+                float rest = -CUDART_INF_F;
+                bool out = !mine;
+#pragma unroll
+                for (int i = 0; i < kScoreWarps; ++i) {
+                    const bool hit = !out && h[i] == least;
+                    h[i] = hit ? -CUDART_INF_F : h[i];
+                    out = out || hit;
+                    rest = fmaxf(rest, h[i]);
+                }
+                hm = rest;
+            }
+            int n1 = 0, n2 = 0;
+            for (int i = 0; i < warps; ++i) {
+                const int l = 32 * i + lane;
+                const bool two = lane_m2[l] >= least, one = !two && lane_m1[l] >= least;
+                const uint32_t k1 = __ballot_sync(kAll, one), k2 = __ballot_sync(kAll, two);
+                const uint32_t before = (1u << lane) - 1u;
+                if (one)
+                    lanes[n1 + __popc(k1 & before)] = static_cast<uint8_t>(l);
+                if (two)
+                    lanes[32 * kScoreWarps + n2 + __popc(k2 & before)] = static_cast<uint8_t>(l);
+                n1 += __popc(k1);
+                n2 += __popc(k2);
+            }
+            if (lane == 0) {
+                n_one = n1;
+                n_all = n2;
+                n_cand = 0;
+                sh_least = least;
+            }
         }
         __syncthreads();
-        if (tid == 0)
-            sh_last = atomic_add_acq_rel_gpu(p.tickets + row, 1) == p.splits - 1;
-        __syncthreads();
-        if (!sh_last || warp != 0)
-            return;
-        __threadfence();
-        if (lane == 0)
-            p.tickets[row] = 0;
-        const size_t part = static_cast<size_t>(row) * p.splits;
-        a = none;
-        for (int i = lane; i < p.splits; i += 32) {
-            const float4 v = __ldcg(p.part + part + i);
-            a = join<ENT>(a, Sums{v.x, v.y, v.z, __float_as_int(v.w)});
+        const float least = sh_least;
+        const int begun = at.split * warps * kStep, mid = n_one * kPieces;
+        const int rounds = at.pieces > begun ? (at.pieces - begun + stride - 1) / stride : 0;
+        const int total = mid + n_all * rounds * kPieces;
+        const bool alone = total <= kAlone;
+        const int step = alone ? 32 : blockDim.x;
+        constexpr int kU = 2;           // pieces of a thread on their way at once
+        for (int i0 = warp * 32; i0 < total && (!alone || warp == 0); i0 += kU * step) {
+            uint4 word[kU];
+            int piece[kU];
+#pragma unroll
+            for (int u = 0; u < kU; ++u) {
+                const int i = i0 + u * step + lane;
+                piece[u] = -1;
+                if (i < mid) {
+                    const int l = lanes[i / kPieces];
+                    piece[u] = lane_c1[l] + 32 * (i % kPieces) + (l & 31);
+                } else if (i < total) {
+                    const int k = i - mid, r = k / n_all, l = lanes[32 * kScoreWarps + k - r * n_all];
+                    piece[u] = begun + (l >> 5) * kStep + (r / kPieces) * stride + 32 * (r % kPieces) + (l & 31);
+                }
+                if (piece[u] >= at.pieces)
+                    piece[u] = -1;
+                if (piece[u] >= 0)
+                    load_pieces<T, 1>(at.x, at.shift, p.vocab, piece[u], word + u);
+            }
+#pragma unroll
+            for (int u = 0; u < kU; ++u) {
+                if (!__any_sync(kAll, piece[u] >= 0))
+                    continue;
+                float x[V];
+                Chunk<T>::unpack(word[u], x);
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    const int v = piece[u] * V - at.shift + j;
+                    const bool in = piece[u] >= 0 && x[j] >= least && v >= 0 && v < p.vocab;
+                    const int to = in ? atomicAdd(&n_cand, 1) : -1;
+                    if (to >= 0 && to < kBuffer) {
+                        cand_x[to] = x[j];
+                        cand_v[to] = v;
+                    }
+                    // (many equal logits, or many high ones in few lanes)
+                    if (__any_sync(kAll, to >= kBuffer))
+                        best.offer(x[j], to >= kBuffer ? v : -1, K, lane);
+                }
+            }
         }
-        a = warp_join(a);
-        if (TOP) {
-            best.clear();
-            const int n = K * p.splits;
-            for (int i = 0; i < n; i += 32) {
-                const float ox = i + lane < n ? __ldcg(p.part_x + part * K + i + lane) : 0.f;
-                const int ov = i + lane < n ? __ldcg(p.part_v + part * K + i + lane) : -1;
-                if (i == 0)
-                    best.start(ox, ov, K, lane);
-                else
-                    best.offer(ox, ov, K, lane);
+        if (!alone) {
+            __syncthreads();
+            if (n_cand > kBuffer) {
+                if (lane < K) {
+                    sh_x[lane * warps + warp] = best.x;
+                    sh_v[lane * warps + warp] = best.v;
+                }
+                __syncthreads();
             }
         }
     }
     if (warp != 0)
         return;
+    __syncwarp();
+    if (TOP) {
+        best.clear();           // (its own list is among the others)
+        if (n_cand > kBuffer)
+            best = merged(best, sh_x, sh_v, K * warps, K, lane);
+        best = merged(best, cand_x, cand_v, min(n_cand, kBuffer), K, lane);
+    }
+    if (warps > 1)
+        a = warp_join(lane < warps ? sh_sums[lane] : none);
+    if (p.splits > 1) {
+        const size_t parts = static_cast<size_t>(at.row) * p.splits;
+        if (lane == 0)
+            p.part[parts + at.split] = make_float4(a.R, a.s, a.t, __int_as_float(a.front));
+        if (TOP && lane < K) {
+            const size_t to = parts * K + static_cast<size_t>(lane) * p.splits + at.split;
+            p.part_x[to] = best.x;
+            p.part_v[to] = best.v;
+        }
+        __threadfence();
+        __syncwarp();
+        int last = 0;
+        if (lane == 0)
+            last = atomic_add_acq_rel_gpu(p.tickets + at.row, 1) == p.splits - 1;
+        if (!__shfl_sync(kAll, last, 0))
+            return;
+        __threadfence();
+        if (lane == 0)
+            p.tickets[at.row] = 0;
+        a = none;
+        for (int i = lane; i < p.splits; i += 32) {
+            const float4 v = __ldcg(p.part + parts + i);
+            a = join<ENT>(a, Sums{v.x, v.y, v.z, __float_as_int(v.w)});
+        }
+        a = warp_join(a);
+        if (TOP) {
+            best.clear();
+            best = merged(best, p.part_x + parts * K, p.part_v + parts * K, K * p.splits, K, lane);
+        }
+    }
     const float ls = logf(a.s);
     const bool sound = isfinite(a.R) && isfinite(ls);
     // lse less ln s, in double: in fp32 it would round at the size of the logits. From kLarge on
@@ -298,23 +567,23 @@ __global__ void __launch_bounds__(kScoreThreads, 4) score_kernel(const ScorePara
     auto log_p = [&](float x) { return sound ? fminf(static_cast<float>(x - ref - ls), 0.f) : CUDART_NAN_F; };
     if (lane == 0) {
         if (p.logprob)
-            p.logprob[row] = given < 0 ? 0.f : has ? log_p(xg) : CUDART_NAN_F;
+            p.logprob[at.row] = given < 0 ? 0.f : has ? log_p(xg) : CUDART_NAN_F;
         if (RANK)
-            p.rank[row] = has && sound ? a.front : -1;
+            p.rank[at.row] = has && sound ? a.front : -1;
         if (ENT)
-            p.entropy[row] = sound ? fmaxf(ls - a.t / a.s * CUDART_LN2_F, 0.f) : CUDART_NAN_F;
+            p.entropy[at.row] = sound ? fmaxf(ls - a.t / a.s * CUDART_LN2_F, 0.f) : CUDART_NAN_F;
     }
     if (TOP && lane < K) {
-        const size_t at = static_cast<size_t>(row) * K + lane;
-        p.top_token[at] = sound ? best.v : -1;
-        p.top_logprob[at] = log_p(best.x);
+        const size_t to = static_cast<size_t>(at.row) * K + lane;
+        p.top_token[to] = sound ? best.v : -1;
+        p.top_logprob[to] = log_p(best.x);
     }
 }
 
 template <typename T, bool TOP>
 cudaError_t launch_top(const ScoreParams &p, cudaStream_t stream)
 {
-    const dim3 grid(p.n_rows * p.splits), block(kScoreThreads);
+    const dim3 grid(p.n_rows * p.splits), block(32 * p.warps);
     if (p.rank)
         return p.entropy ? launch_pdl(score_kernel<T, TOP, true, true>, grid, block, 0, stream, p)
                          : launch_pdl(score_kernel<T, TOP, true, false>, grid, block, 0, stream, p);

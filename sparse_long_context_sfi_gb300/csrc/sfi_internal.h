@@ -234,9 +234,11 @@ cudaError_t launch_beam_select(const BeamParams &p, cudaStream_t stream);
 // ---------------------------------------------------------------- log probabilities of tokens
 
 constexpr int kMaxTop = 32;
+constexpr int kMaxSplitRows = 8192;     // rows of a call that may be split over CTAs
 
 struct ScoreParams {
-    int n_rows, vocab, logits_fp32, n_top, splits;
+    int n_rows, vocab, logits_fp32, n_top;
+    int splits, warps;          // CTAs of a row, warps of a CTA
     long long row_stride;
     const void *logits;
     const int32_t *token;
@@ -247,7 +249,7 @@ struct ScoreParams {
     float *top_logprob;
     int *tickets;               // [rows that are split], zero between launches
     float4 *part;               // [rows][splits]: reference, sum, entropy's sum, tokens in front
-    float *part_x;              // [rows][splits][n_top] best logits
+    float *part_x;              // [rows][n_top][splits] best logits
     int32_t *part_v;            // and their tokens (-1: none)
 };
 cudaError_t launch_score(const ScoreParams &p, cudaStream_t stream);
