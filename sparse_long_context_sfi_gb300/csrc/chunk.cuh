@@ -81,4 +81,33 @@ __device__ __forceinline__ long long chunk_dst(const ChunkParams &p, int r, int 
     return b < 0 ? -1 : cache_row(p.pg, b, pos);
 }
 
+// The lengths after the rows of a chunk, by one block: a warp per sequence, which first looks over
+// the chunk's pages.
+__device__ __forceinline__ void advance_lengths(const ChunkParams &p)
+{
+    const int lane = threadIdx.x & 31;
+    for (int b = threadIdx.x >> 5; b < p.pg.batch; b += static_cast<int>(blockDim.x >> 5)) {
+        if (p.pg.active && !p.pg.active[b])
+            continue;
+        int s0, n, L;
+        if (!chunk_ok(p, b, lane, s0, n, L, lane == 0))
+            continue;
+        bool good = true;
+        if (p.pg.page_size != 0 && n > 0) {
+            for (int c = (L >> 4) + lane; c <= (L + n - 1) >> 4; c += 32) {
+                const int e = p.pg.table[static_cast<size_t>(b) * p.pg.max_pages + c];
+                good = good && e >= 0 && e < p.pg.n_pages;
+            }
+        }
+        good = __all_sync(0xffffffffu, good);
+        __syncwarp();
+        if (lane == 0) {
+            if (good)
+                p.pg.seq_len[b] = L + n;
+            else
+                raise_error(p.pg.err, 0x1u);  // SFI_DEVERR_PAGE_RANGE
+        }
+    }
+}
+
 }  // namespace sfi

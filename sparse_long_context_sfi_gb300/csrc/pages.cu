@@ -508,29 +508,7 @@ __global__ void __launch_bounds__(1024) advance_kernel(const ChunkParams p)
 {
     pdl_trigger();
     pdl_wait();
-    const int lane = threadIdx.x & 31;
-    for (int b = threadIdx.x >> 5; b < p.pg.batch; b += 32) {
-        if (p.pg.active && !p.pg.active[b])
-            continue;
-        int s0, n, L;
-        if (!chunk_ok(p, b, lane, s0, n, L, lane == 0))
-            continue;
-        bool good = true;
-        if (p.pg.page_size != 0 && n > 0) {
-            for (int c = (L >> 4) + lane; c <= (L + n - 1) >> 4; c += 32) {
-                const int e = p.pg.table[static_cast<size_t>(b) * p.pg.max_pages + c];
-                good = good && e >= 0 && e < p.pg.n_pages;
-            }
-        }
-        good = __all_sync(kFull, good);
-        __syncwarp();
-        if (lane == 0) {
-            if (good)
-                p.pg.seq_len[b] = L + n;
-            else
-                raise_error(p.pg.err, 0x1u);  // SFI_DEVERR_PAGE_RANGE
-        }
-    }
+    advance_lengths(p);
 }
 
 // -------------------------------------------------------------------------------- reorder

@@ -8,9 +8,12 @@
 // its upper half is the angle, in half turns as a float for sincospif.
 //
 // Bytes bound it: a row of a head is read and written once. A half-warp holds a row of a head, 8
-// dimensions (16 bytes) a lane. A CTA has the sines and cosines of its rows in shared memory, worked
-// out once for all heads and layers, and each half-warp keeps its row's in registers over the heads
-// it goes through.
+// dimensions (16 bytes) a lane, 4 heads on their way at once. A CTA has the sines and cosines of its 8
+// rows in shared memory, worked out once for all heads, and each half-warp keeps its row's share in
+// registers over the heads it goes through, multiplied by the norm's weights.
+// Four prompts of 8192 tokens, 32 and 8 heads: 133 us, 6.05 TB/s (copy rate 6.75), with norms 142, with
+// neighbouring pairs 133, with 40 of 128 dimensions (partners read one by one) 209; 170 us with 16 rows a
+// CTA, unpacked arithmetic and a list of (layer, head) per step; 135 with 80 instead of 64 registers.
 #include "chunk.cuh"
 #include "sfi_device.cuh"
 
@@ -18,54 +21,97 @@ namespace sfi {
 namespace {
 
 constexpr int kRopeThreads = 256;
-constexpr int kRopeRows = kRopeThreads / 16;    // most rows of a CTA
+constexpr int kRopeRows = 8;                    // most rows of a CTA: one for each warp to look up
 constexpr int kRopeLoads = 4;                   // heads of a half-warp on their way at once
 constexpr uint32_t kEvery = 0xffffffffu;
 
 // How a lane gets the partners of its 8 dimensions.
 enum {
-    kPairs,     // neighbours: its own
-    kLanes,     // half a head apart, a multiple of 8: all in one other lane
-    kAnywhere   // any other distance: read again, one by one
+    kPairs,     // neighbours: its own (rot_dim a multiple of 8: a lane turns all of its dimensions or none)
+    kLanes,     // half of rot_dim apart, a multiple of 8: all in one other lane
+    kAnywhere   // any other rot_dim, either layout: read again, one by one
 };
 
-__device__ __forceinline__ void unpack8(const uint4 &w, float *x)
+__device__ __forceinline__ uint64_t pack2(float a, float b)
 {
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        x[2 * i] = __uint_as_float(u[i] << 16);
-        x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
-    }
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+    return d;
 }
 
-__device__ __forceinline__ uint32_t bf16_pair(float a, float b)
+__device__ __forceinline__ float2 unpack2(uint64_t v)
 {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    float2 f;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
+    return f;
+}
+
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
+{
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+// Two bf16 as two floats.
+__device__ __forceinline__ uint64_t widen(uint32_t u)
+{
+    return pack2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+}
+
+__device__ __forceinline__ uint32_t narrow(uint64_t v)
+{
+    const float2 f = unpack2(v);
+    const __nv_bfloat162 h = __floats2bfloat162_rn(f.x, f.y);
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 
 // A lane's share of the rotation: y = x * c + (partner) * s, weights of the norm included.
 struct Turn {
-    float c[8], s[8];
+    uint64_t c[4], s[4];
 };
 
 template <int MODE, bool NORM>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p, int lg_rows, int need)
+__global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const RopeParams p, int lg_rows, int need, int fused)
 {
     __shared__ float2 cs[kRopeRows][kHeadDim / 2];
     __shared__ long long place[kRopeRows];
     __shared__ int at[kRopeRows];
     __shared__ bool live[kRopeRows];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int n_here = 1 << lg_rows, r0 = blockIdx.x << lg_rows;
-    const int hq = p.q ? p.n_q_heads : 0, hkv = p.c.pg.n_kv_heads, hk = p.k ? hkv : 0;
+    const int n_here = 1 << lg_rows, r0 = blockIdx.x << lg_rows, layer = blockIdx.z;
+    const int hkv = p.c.pg.n_kv_heads, hq = p.q ? p.n_q_heads : 0, hk = p.k ? hkv : 0;
     const bool append = p.k_cache != nullptr;
     const int half = p.rot >> 1;
+    // half-warps: row hw % n_here, and of its heads every `stride`-th from `u` on
+    const int hw = tid >> 4, l = tid & 15, row = hw & (n_here - 1), r = r0 + row;
+    const int stride = ((kRopeThreads / 16) >> lg_rows) * gridDim.y;
+    int u = (hw >> lg_rows) * gridDim.y + blockIdx.y;
+    const long long packed = static_cast<long long>(layer) * p.c.n_rows + r;
+    const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(p.q) + packed * p.q_stride + 8 * l;
+    const bool there = r < p.c.n_rows;
     pdl_trigger();
     pdl_wait();
+    // the first queries are asked for before their positions are known (a chain of four loads)
+    uint4 x[kRopeLoads];
+    auto load = [&](const __nv_bfloat16 *from, int begin, int end, bool on) {
+#pragma unroll
+        for (int i = 0; i < kRopeLoads; ++i) {
+            const int h = u + i * stride - begin;
+            x[i] = on && h < end - begin ? __ldcs(reinterpret_cast<const uint4 *>(from + h * kHeadDim))
+                                         : make_uint4(0, 0, 0, 0);
+        }
+    };
+    load(src, 0, hq, there);
     // (what an append skips is told when the lengths advance)
-    if (!append && blockIdx.x == 0 && blockIdx.y == 0) {
+    if (!append && blockIdx.x == 0 && blockIdx.y == 0 && layer == 0) {
         for (int b = warp; b < p.c.pg.batch; b += kRopeThreads / 32) {
             int s0, n, L;
             if (p.c.pg.active && !p.c.pg.active[b])
@@ -76,159 +122,181 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p, 
                 chunk_ok<kNeedRows>(p.c, b, lane, s0, n, L, lane == 0);
         }
     }
-    for (int i = warp; i < n_here; i += kRopeThreads / 32) {
-        const int r = r0 + i;
+    if (warp < n_here) {
+        const int mine = r0 + warp;
         int pos = 0;
-        const int b = need == kNeedRoom     ? chunk_seq<kNeedRoom>(p.c, r, lane, pos)
-                      : need == kNeedLength ? chunk_seq<kNeedLength>(p.c, r, lane, pos)
-                                            : chunk_seq<kNeedRows>(p.c, r, lane, pos);
+        const int b = need == kNeedRoom     ? chunk_seq<kNeedRoom>(p.c, mine, lane, pos)
+                      : need == kNeedLength ? chunk_seq<kNeedLength>(p.c, mine, lane, pos)
+                                            : chunk_seq<kNeedRows>(p.c, mine, lane, pos);
         if (lane == 0) {
-            live[i] = b >= 0;
-            at[i] = b < 0 ? 0 : p.pos ? p.pos[r] : pos;
-            place[i] = append && b >= 0 ? cache_row(p.c.pg, b, pos) : -1;
+            live[warp] = b >= 0;
+            at[warp] = b < 0 ? 0 : p.pos ? p.pos[mine] : pos;
+            place[warp] = append && b >= 0 ? cache_row(p.c.pg, b, pos) : -1;
         }
     }
     __syncthreads();
     for (int i = tid; i < half << lg_rows; i += kRopeThreads) {
-        const int row = i / half, pair = i - row * half;
-        const uint64_t turn = static_cast<uint64_t>(static_cast<long long>(at[row])) * p.turns[pair];
+        const int which = i / half, pair = i - which * half;
+        const uint64_t turn = static_cast<uint64_t>(static_cast<long long>(at[which])) * p.turns[pair];
         float sn, cn;
         sincospif(static_cast<float>(static_cast<int32_t>(turn >> 32)) * 0x1p-31f, &sn, &cn);
-        cs[row][pair] = make_float2(cn * p.amplitude, sn * p.amplitude);
+        cs[which][pair] = make_float2(cn * p.amplitude, sn * p.amplitude);
     }
     __syncthreads();
 
-    const int hw = tid >> 4, l = tid & 15, row = hw & (n_here - 1), r = r0 + row;
     const bool on = live[row];
-    // the partner's dimension and the factors of each of this lane's 8
-    uint32_t turns8 = 0;            // which of them turn
-    auto partner = [&](int d) {
-        return MODE == kPairs ? d ^ 1 : d < half ? d + half : d - half;
-    };
+    // in the layouts that a lane turns as a whole, whether it does
+    const bool turns = MODE != kAnywhere && 8 * l < p.rot;
+    const bool pairs = MODE == kPairs || (MODE == kAnywhere && p.interleaved);
+    auto partner = [&](int d) { return pairs ? d ^ 1 : d < half ? d + half : d - half; };
     auto factors = [&](const void *weight) {
         Turn t;
         const __nv_bfloat16 *w = static_cast<const __nv_bfloat16 *>(weight);
+        float c[8], s[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const int d = 8 * l + j;
             const bool turned = d < p.rot;
-            const int pair = MODE == kPairs ? d >> 1 : d < half ? d : d - half;
-            const bool first = MODE == kPairs ? (d & 1) == 0 : d < half;
+            const int pair = pairs ? d >> 1 : d < half ? d : d - half;
+            const bool first = pairs ? (d & 1) == 0 : d < half;
             const float2 v = turned ? cs[row][pair] : make_float2(1.f, 0.f);
-            const float self = NORM && w ? __bfloat162float(w[d]) : 1.f;
-            const float other = NORM && w && turned ? __bfloat162float(w[partner(d)]) : 1.f;
-            t.c[j] = v.x * self;
-            t.s[j] = (first ? -v.y : v.y) * other;
-            turns8 |= turned ? 1u << j : 0u;
+            c[j] = NORM && w ? v.x * __bfloat162float(w[d]) : v.x;
+            s[j] = (first ? -v.y : v.y) * (NORM && w && turned ? __bfloat162float(w[partner(d)]) : 1.f);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            t.c[j] = pack2(c[2 * j], c[2 * j + 1]);
+            t.s[j] = pack2(s[2 * j], s[2 * j + 1]);
         }
         return t;
     };
-    const Turn tq = factors(p.q_norm);
-    const Turn tk = NORM ? factors(p.k_norm) : tq;
-    const int other_lane = MODE == kLanes && 8 * l < p.rot ? (8 * l < half ? l + half / 8 : l - half / 8) : l;
-
-    const int heads = hq + hk + (append ? hkv : 0), units = heads * p.n_layers;
-    const int subs = kRopeRows >> lg_rows, stride = subs * gridDim.y;
-    const int first = (hw >> lg_rows) * gridDim.y + blockIdx.y;
-    const long long head = append ? (p.c.pg.page_size ? 16 : p.c.pg.capacity) : 1;
-    const long long layer_rows = append ? (p.c.pg.page_size ? 16LL * p.c.pg.n_pages : 1LL * p.c.pg.batch * p.c.pg.capacity) * hkv : 0;
-    // (both half-warps of a warp go through the same number of steps: shuffles)
-    for (int u0 = 0; u0 < units; u0 += stride * kRopeLoads) {
-        uint4 x[kRopeLoads];
-        const __nv_bfloat16 *src[kRopeLoads];
-        __nv_bfloat16 *dst[kRopeLoads];
-        int kind[kRopeLoads];       // 0 q, 1 k, 2 v
+    const int other_lane = MODE == kLanes && turns ? (8 * l < half ? l + half / 8 : l - half / 8) : l;
+    // The heads [begin, end) of the row, which lie at `from` and go to `to`, to_step elements apart; TURN:
+    // turned by t (and normed), else copied. Both half-warps of a warp go through as many steps.
+    auto heads = [&](int begin, int end, const __nv_bfloat16 *from, __nv_bfloat16 *to, long long to_step, bool turn,
+                     const Turn &t, bool norm, bool loaded) {
+        while (__any_sync(kEvery, u < end)) {
+            if (!loaded)
+                load(from, begin, end, on);
+            loaded = false;
+            if (turn) {
 #pragma unroll
-        for (int i = 0; i < kRopeLoads; ++i) {
-            const int u = u0 + first + i * stride;
-            src[i] = nullptr;
-            dst[i] = nullptr;
-            kind[i] = 2;
-            x[i] = make_uint4(0, 0, 0, 0);
-            if (!on || u >= units)
-                continue;
-            const int layer = p.n_layers == 1 ? 0 : u / heads, h = u - layer * heads;
-            const long long packed = static_cast<long long>(layer) * p.c.n_rows + r;
-            if (h < hq) {
-                kind[i] = 0;
-                src[i] = static_cast<const __nv_bfloat16 *>(p.q) + packed * p.q_stride + h * kHeadDim;
-                dst[i] = static_cast<__nv_bfloat16 *>(p.q_out) + (packed * hq + h) * kHeadDim;
-            } else {
-                const bool is_k = h < hq + hk;
-                const int g = h - hq - (is_k ? 0 : hk);
-                kind[i] = is_k ? 1 : 2;
-                src[i] = is_k ? static_cast<const __nv_bfloat16 *>(p.k) + packed * p.k_stride + g * kHeadDim
-                              : static_cast<const __nv_bfloat16 *>(p.v) + packed * p.v_stride + g * kHeadDim;
-                if (!append)
-                    dst[i] = static_cast<__nv_bfloat16 *>(p.k_out) + (packed * hkv + g) * kHeadDim;
-                else if (place[row] >= 0)
-                    dst[i] = static_cast<__nv_bfloat16 *>(is_k ? p.k_cache : p.v_cache) +
-                             (layer * layer_rows + place[row] + g * head) * kHeadDim;
-            }
-            x[i] = __ldcs(reinterpret_cast<const uint4 *>(src[i]) + l);
-        }
+                for (int i = 0; i < kRopeLoads; ++i) {
+                    const uint64_t a[4] = {widen(x[i].x), widen(x[i].y), widen(x[i].z), widen(x[i].w)};
+                    uint64_t b[4], y[4];
+                    if constexpr (MODE == kLanes) {
+                        b[0] = widen(__shfl_sync(kEvery, x[i].x, other_lane, 16));
+                        b[1] = widen(__shfl_sync(kEvery, x[i].y, other_lane, 16));
+                        b[2] = widen(__shfl_sync(kEvery, x[i].z, other_lane, 16));
+                        b[3] = widen(__shfl_sync(kEvery, x[i].w, other_lane, 16));
+                    } else if constexpr (MODE == kPairs) {
 #pragma unroll
-        for (int i = 0; i < kRopeLoads; ++i) {
-            float a[8], b[8];
-            unpack8(x[i], a);
-            if constexpr (MODE == kLanes) {
-                const uint4 o = make_uint4(__shfl_sync(kEvery, x[i].x, other_lane, 16),
-                                           __shfl_sync(kEvery, x[i].y, other_lane, 16),
-                                           __shfl_sync(kEvery, x[i].z, other_lane, 16),
-                                           __shfl_sync(kEvery, x[i].w, other_lane, 16));
-                unpack8(o, b);
-            } else if constexpr (MODE == kAnywhere) {
+                        for (int j = 0; j < 4; ++j) {
+                            const float2 f = unpack2(a[j]);
+                            b[j] = pack2(f.y, f.x);
+                        }
+                    } else {
+                        // (0 where a dimension stays: no infinity reaches it)
+                        const int h = u + i * stride - begin;
+                        float f[8];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const int d = 8 * l + j;
-                    b[j] = src[i] && d < p.rot ? __bfloat162float(src[i][partner(d)]) : 0.f;
+                        for (int j = 0; j < 8; ++j) {
+                            const int d = 8 * l + j;
+                            f[j] = on && h < end - begin && d < p.rot
+                                       ? __bfloat162float(from[h * kHeadDim + partner(d) - 8 * l]) : 0.f;
+                        }
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            b[j] = pack2(f[2 * j], f[2 * j + 1]);
+                    }
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        y[j] = mul2(a[j], t.c[j]);
+                        if (MODE == kAnywhere || turns)
+                            y[j] = fma2(b[j], t.s[j], y[j]);
+                    }
+                    if constexpr (NORM) {
+                        uint64_t sq = mul2(a[0], a[0]);
+#pragma unroll
+                        for (int j = 1; j < 4; ++j)
+                            sq = fma2(a[j], a[j], sq);
+                        const float2 f = unpack2(sq);
+                        float sum = f.x + f.y;
+#pragma unroll
+                        for (int o = 8; o > 0; o >>= 1)
+                            sum += __shfl_xor_sync(kEvery, sum, o, 16);
+                        const float scale = norm ? rsqrtf(sum * (1.f / kHeadDim) + p.eps) : 1.f;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            y[j] = mul2(y[j], pack2(scale, scale));
+                    }
+                    x[i] = make_uint4(narrow(y[0]), narrow(y[1]), narrow(y[2]), narrow(y[3]));
                 }
-            } else {
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    b[j] = a[j ^ 1];
             }
-            float scale = 1.f;
-            if constexpr (NORM) {
-                float sum = 0.f;
+            if (MODE == kAnywhere)
+                __syncwarp();           // in place, partners have been read
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    sum = fmaf(a[j], a[j], sum);
-#pragma unroll
-                for (int o = 8; o > 0; o >>= 1)
-                    sum += __shfl_xor_sync(kEvery, sum, o, 16);
-                if (kind[i] == 0 ? p.q_norm != nullptr : p.k_norm != nullptr)
-                    scale = rsqrtf(sum * (1.f / kHeadDim) + p.eps);
+            for (int i = 0; i < kRopeLoads; ++i) {
+                const int h = u + i * stride - begin;
+                if (on && to && h < end - begin)
+                    *reinterpret_cast<uint4 *>(to + h * to_step) = x[i];
             }
-            if (kind[i] < 2) {
-                const Turn &t = NORM && kind[i] == 1 ? tk : tq;
-                float y[8];
+            // (kRopeLoads * stride may pass the end: the next heads begin where this class goes on)
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    // (a dimension that stays has no partner whose infinity could reach it)
-                    const float own = a[j] * t.c[j];
-                    y[j] = (turns8 >> j) & 1u ? fmaf(b[j], t.s[j], own) : own;
-                    if (NORM)
-                        y[j] *= scale;
-                }
-                x[i] = make_uint4(bf16_pair(y[0], y[1]), bf16_pair(y[2], y[3]), bf16_pair(y[4], y[5]),
-                                  bf16_pair(y[6], y[7]));
-            }
+            for (int i = 0; i < kRopeLoads; ++i)
+                u += u < end ? stride : 0;
         }
-        __syncwarp();               // in place, partners have been read
-#pragma unroll
-        for (int i = 0; i < kRopeLoads; ++i)
-            if (dst[i])
-                reinterpret_cast<uint4 *>(dst[i])[l] = x[i];
+    };
+    Turn t = factors(p.q_norm);
+    if (hq > 0)
+        heads(0, hq, src, static_cast<__nv_bfloat16 *>(p.q_out) + packed * hq * kHeadDim + 8 * l, kHeadDim, true, t,
+              p.q_norm != nullptr, true);
+    if (hk > 0) {
+        if (NORM)
+            t = factors(p.k_norm);
+        long long step = kHeadDim;
+        __nv_bfloat16 *k_to, *v_to = nullptr;
+        if (append) {
+            step = (p.c.pg.page_size ? 16LL : p.c.pg.capacity) * kHeadDim;
+            const long long rows = p.c.pg.page_size ? 16LL * p.c.pg.n_pages : 1LL * p.c.pg.batch * p.c.pg.capacity;
+            const long long to = (layer * rows * hkv + place[row]) * kHeadDim + 8 * l;
+            k_to = place[row] < 0 ? nullptr : static_cast<__nv_bfloat16 *>(p.k_cache) + to;
+            v_to = place[row] < 0 ? nullptr : static_cast<__nv_bfloat16 *>(p.v_cache) + to;
+        } else {
+            k_to = static_cast<__nv_bfloat16 *>(p.k_out) + packed * hkv * kHeadDim + 8 * l;
+        }
+        heads(hq, hq + hk, static_cast<const __nv_bfloat16 *>(p.k) + packed * p.k_stride + 8 * l, k_to, step, true, t,
+              p.k_norm != nullptr, false);
+        if (append)
+            heads(hq + hk, hq + 2 * hk, static_cast<const __nv_bfloat16 *>(p.v) + packed * p.v_stride + 8 * l, v_to,
+                  step, false, t, false, false);
+    }
+    if (fused > 0) {            // all of the grid, one cluster, has read the lengths
+        if (fused > 1)
+            cluster_sync_all();
+        if (fused == 1 || cluster_ctarank() == 0)
+            advance_lengths(p.c);
     }
 }
 
 template <int MODE>
-cudaError_t launch_mode(const RopeParams &p, dim3 grid, int lg_rows, int need, cudaStream_t stream)
+cudaError_t launch_mode(const RopeParams &p, dim3 grid, int lg_rows, int need, int fused, cudaStream_t stream)
 {
-    return p.q_norm || p.k_norm
-               ? launch_pdl(rope_kernel<MODE, true>, grid, dim3(kRopeThreads), 0, stream, p, lg_rows, need)
-               : launch_pdl(rope_kernel<MODE, false>, grid, dim3(kRopeThreads), 0, stream, p, lg_rows, need);
+    auto *kern = p.q_norm || p.k_norm ? rope_kernel<MODE, true> : rope_kernel<MODE, false>;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(kRopeThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;       // (the whole grid)
+    attr[1].val.clusterDim.x = grid.x;
+    attr[1].val.clusterDim.y = grid.y;
+    attr[1].val.clusterDim.z = grid.z;
+    cfg.attrs = attr;
+    cfg.numAttrs = fused > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kern, p, lg_rows, need, fused);
 }
 
 }  // namespace
@@ -237,22 +305,41 @@ cudaError_t launch_rope(const RopeParams &p, int sms, cudaStream_t stream)
 {
     const bool append = p.k_cache != nullptr;
     const int hkv = p.c.pg.n_kv_heads;
-    const int units = ((p.q ? p.n_q_heads : 0) + (p.k ? hkv : 0) + (append ? hkv : 0)) * p.n_layers;
+    const int heads = (p.q ? p.n_q_heads : 0) + (p.k ? hkv : 0) + (append ? hkv : 0);
     // The most rows per CTA that still fill the GPU, and then CTAs that share a row's heads.
-    int lg = 4;
-    while (lg > 0 && (p.c.n_rows >> lg) < 2 * sms)
+    int lg = 3;
+    while (lg > 0 && (static_cast<long long>(p.c.n_rows) * p.n_layers >> lg) < 2 * sms)
         --lg;
-    const int blocks = (p.c.n_rows + (1 << lg) - 1) >> lg, subs = kRopeRows >> lg;
-    int share = 4 * sms / blocks;
-    const int most = (units + subs - 1) / subs;
-    share = share < most ? share : most;
-    const dim3 grid(blocks, share < 1 ? 1 : share);
+    auto shape = [&](long long ctas) {
+        const long long blocks = (p.c.n_rows + (1LL << lg) - 1) >> lg, subs = (kRopeThreads / 16) >> lg;
+        const long long share = ctas / (blocks * p.n_layers), most = (heads + subs - 1) / subs;
+        return dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(share < 1 ? 1 : share < most ? share : most),
+                    p.n_layers);
+    };
+    dim3 grid = shape(4LL * sms);
+    // A few tokens are one cluster, whose first CTA advances the lengths when all have read them: at
+    // most 16 heads a half-warp, and a sequence for each of that CTA's warps. (One token of 12 heads: 6.2
+    // us with the copy that resets the case, 8.2 in two launches; 4 of 48 8.2 and 8.9; 16, with two sequences
+    // a warp, 10.2 and 9.6. The host issues one launch less.)
+    int fused = 0;
+    for (int i = 0; append && p.c.pg.batch <= 8 && fused == 0 && i <= 3; ++i) {
+        const int keep = lg;
+        lg = i;
+        const dim3 g = shape(8);
+        const unsigned n = g.x * g.y * g.z;
+        if (n <= 8 && heads <= 16LL * ((kRopeThreads / 16) >> i) * g.y) {
+            grid = g;
+            fused = static_cast<int>(n);
+        } else {
+            lg = keep;
+        }
+    }
     const int need = append ? kNeedRoom : p.pos ? kNeedRows : kNeedLength;
-    const int half = p.rot / 2;
-    cudaError_t e = p.interleaved   ? launch_mode<kPairs>(p, grid, lg, need, stream)
-                    : half % 8 == 0 ? launch_mode<kLanes>(p, grid, lg, need, stream)
-                                    : launch_mode<kAnywhere>(p, grid, lg, need, stream);
-    if (e == cudaSuccess && append)
+    const cudaError_t e = p.interleaved && p.rot % 8 == 0 ? launch_mode<kPairs>(p, grid, lg, need, fused, stream)
+                          : !p.interleaved && p.rot % 16 == 0
+                              ? launch_mode<kLanes>(p, grid, lg, need, fused, stream)
+                              : launch_mode<kAnywhere>(p, grid, lg, need, fused, stream);
+    if (e == cudaSuccess && append && fused == 0)
         return launch_advance(p.c, stream);
     return e != cudaSuccess ? e : cudaGetLastError();
 }

@@ -166,6 +166,10 @@ SHAPES = [
     ([0], [1], 1, 1, 1), ([0], [1], 8, 8, 3), ([15], [2], 2, 1, 1), ([4096], [1], 8, 2, 1), ([16], [16], 16, 2, 1),
     ([7, 0, 99, 31], [0, 5, 0, 1], 8, 2, 2), ([1] * 40, [1] * 40, 32, 8, 1), ([3] * 256, [1] * 256, 2, 2, 1),
     ([100, 20], [1501, 333], 32, 4, 2), ([0, 50, 10], [2000, 1, 3000], 4, 4, 1),
+    # one cluster, up to its bounds, and just beyond them
+    ([9], [1], 8, 1, 8), ([9], [1], 8, 1, 9), ([5] * 16, [1] * 16, 16, 2, 1), ([5] * 17, [1] * 17, 16, 2, 1),
+    ([5, 6, 7, 8], [3, 9, 1, 7], 64, 8, 1), ([30] * 8, [8] * 8, 32, 8, 1), ([30, 2], [2, 6], 32, 8, 8),
+    ([15] + [0] * 15, [2] + [0] * 15, 8, 2, 1),
 ]
 
 
