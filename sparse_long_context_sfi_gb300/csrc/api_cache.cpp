@@ -151,6 +151,28 @@ size_t window_scratch(const sfi_kv_cache *kv, int n_rows, int max_rows, char *ba
     return o;
 }
 
+// The shape and the workspace of sfi_cross_attn, whose items are cut where the CTAs' equal shares of
+// all key tiles end: two pieces to a CTA at most, and a ticket to a CTA.
+size_t cross_scratch(const sfi_kv_cache *kv, int max_rows, char *base, WindowParams *p)
+{
+    const int g = kv->n_q_heads / kv->n_kv_heads, sms = sm_count() > 0 ? sm_count() : 1;
+    const long long all = 1LL * max_rows * g;
+    size_t o = 0, rows = 0;
+    for (long long r : {16, 128, 256}) {
+        const size_t n = static_cast<size_t>(all < r ? all : r) * 2 * (r == 256 ? sms : 2 * sms);
+        rows = n > rows && (r == 16 || all > 16) ? n : rows;
+    }
+    auto take = [&](size_t bytes) {
+        char *at = base + o;
+        o = align256(o + bytes);
+        return static_cast<void *>(at);
+    };
+    p->tickets = static_cast<int *>(take(2 * static_cast<size_t>(sms) * sizeof(int)));
+    p->part_ml = static_cast<float2 *>(take(rows * sizeof(float2)));
+    p->parts = static_cast<float *>(take(rows * kHeadDim * sizeof(float)));
+    return o;
+}
+
 sfi_status check_beam(const sfi_beam *b)
 {
     if (!b || b->n_groups < 1 || b->n_beams < 1 || b->vocab < 1 || b->row_stride < b->vocab ||
@@ -276,8 +298,9 @@ sfi_status attend(bool cross, const sfi_kv_cache *kv, const void *q, void *out, 
         return st;
     WindowParams p;
     std::memset(&p, 0, sizeof p);
-    if ((st = check_ws(ws, ws_bytes, window_scratch(kv, n_rows, max_rows, static_cast<char *>(ws), &p))) !=
-        SFI_OK)
+    const size_t need = cross ? cross_scratch(kv, max_rows, static_cast<char *>(ws), &p)
+                              : window_scratch(kv, n_rows, max_rows, static_cast<char *>(ws), &p);
+    if ((st = check_ws(ws, ws_bytes, need)) != SFI_OK)
         return st;
     if (n_rows == 0 || max_rows == 0)
         return SFI_OK;
@@ -319,18 +342,32 @@ sfi_status attend(bool cross, const sfi_kv_cache *kv, const void *q, void *out, 
     p.err = kv->err;
     const long long len = kv->max_len, reach = n_window < len ? n_window : len;
     const WindowShape s = window_shape(kv, n_rows, max_rows, rows, fp32);
-    // Fewer items than CTAs that fit: split their keys, four tiles at least to a split.
     const int kt = rows == 256 ? 128 : 64;
+    p.scale_log2 = static_cast<float>(1.4426950408889634074 / std::sqrt(static_cast<double>(kHeadDim)));
+    p.part_rows = s.part_rows;
+    if (cross) {
+        // Few items are shared out by their key tiles, many taken whole from a queue, which leaves
+        // the CTAs close together in the keys and joins nothing. Measured, us, shares and queue: 32 x 4 rows
+        // of 1000 to 4001 keys (0.8 items a CTA) 61, 86; 300 rows of 8192 keys (0.5) 62, 114; 2048 (1.7) 214,
+        // 222; ragged prompts of up to 701 rows of 0 to 1601 keys (5) 128, 95; 4 x 2048 of 8192 (6.7) 837, 761.
+        // A share has at least as many tiles as join well: one row of 601 keys with 1, 2, 4 tiles 14, 14,
+        // 17; of 8192 keys 31, 28, 22. (Key tiles of one unit are counted in 31 bits.)
+        const double tiles = std::ceil(static_cast<double>(len) / kt);
+        const double unit = (1. * n_rows * p.group / rows + kv->batch) * (tiles + 2.);
+        const bool shares = s.items < 2 * s.slots && unit < 2147483647.;
+        const double least = std::sqrt(tiles / 4.);
+        p.n_split = !shares ? 1 : least > 2. ? static_cast<int>(least + 0.5) : 2;
+        return launch_status(launch_cross(p, rows, shares, tk, tv, tq, s.slots, as_stream(stream)));
+    }
+    // Fewer items than CTAs that fit: split their keys, four tiles at least to a split.
     const long long span = reach + rows / p.group < len ? reach + rows / p.group : len;
     const long long tiles = (span + n_sink + 32 + kt - 1) / kt;
     long long split = s.most_split < tiles / 4 ? s.most_split : tiles / 4;
     split = split < 1 ? 1 : split;
     p.n_split = static_cast<int>(split);
-    p.part_rows = s.part_rows;
     const long long all = s.items * split;
     const int grid = static_cast<int>(all < s.slots ? all : s.slots);
-    p.scale_log2 = static_cast<float>(1.4426950408889634074 / std::sqrt(static_cast<double>(kHeadDim)));
-    return launch_status((cross ? launch_cross : launch_window)(p, rows, tk, tv, tq, grid, as_stream(stream)));
+    return launch_status(launch_window(p, rows, tk, tv, tq, grid, as_stream(stream)));
 }
 
 sfi_status check_scoring(const sfi_scoring *s)
@@ -498,7 +535,10 @@ sfi_status sfi_window_attn(const sfi_kv_cache *kv, const void *q, void *out, int
 
 size_t sfi_cross_workspace_bytes(const sfi_kv_cache *kv, int32_t n_rows, int32_t max_rows)
 {
-    return sfi_window_workspace_bytes(kv, n_rows, max_rows, 0, INT_MAX);
+    if (check_kv(kv) != SFI_OK || n_rows < 0 || max_rows < 0)
+        return 0;
+    WindowParams p;
+    return cross_scratch(kv, max_rows, nullptr, &p);
 }
 
 sfi_status sfi_cross_attn(const sfi_kv_cache *kv, const void *q, void *out, int32_t out_fp32,

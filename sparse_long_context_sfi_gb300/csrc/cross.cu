@@ -4,10 +4,10 @@
 
 namespace sfi {
 
-cudaError_t launch_cross(const WindowParams &p, int rows, const CUtensorMap &tm_k, const CUtensorMap &tm_v,
+cudaError_t launch_cross(const WindowParams &p, int rows, bool shares, const CUtensorMap &tm_k, const CUtensorMap &tm_v,
                          const CUtensorMap &tm_q, int grid, cudaStream_t stream)
 {
-    return launch_rows<true>(p, rows, tm_k, tm_v, tm_q, grid, stream);
+    return launch_rows<true>(p, rows, shares, tm_k, tm_v, tm_q, grid, stream);
 }
 
 }  // namespace sfi

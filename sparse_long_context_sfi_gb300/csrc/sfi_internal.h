@@ -280,7 +280,8 @@ cudaError_t launch_window(const WindowParams &p, int rows, const CUtensorMap &tm
                           const CUtensorMap &tm_v, const CUtensorMap &tm_q, int grid,
                           cudaStream_t stream);
 // The same for rows that all see the whole of their sequence (n_sink and n_window are not read).
-cudaError_t launch_cross(const WindowParams &p, int rows, const CUtensorMap &tm_k,
+// shares: equal shares of all key tiles, at least n_split to a CTA; else a queue of whole items.
+cudaError_t launch_cross(const WindowParams &p, int rows, bool shares, const CUtensorMap &tm_k,
                          const CUtensorMap &tm_v, const CUtensorMap &tm_q, int grid,
                          cudaStream_t stream);
 

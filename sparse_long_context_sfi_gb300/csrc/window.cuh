@@ -23,6 +23,10 @@
 // more than 2^8, so that most tiles leave O alone (an 8K chunk: 491 us with every growth, 417
 // without); weights up to 2^8 are as exact in floating point as weights up to 1.
 //
+// CROSS: rows that see all keys of their sequence. The producer shares the work out as it goes
+// (stream_item, or a queue); 32 x 4 rows of 1000 to 4001 keys 61 us (4.8 TB/s; 95 with one CTA to an item),
+// 4 x 2048 rows of 8192 keys 760 us, 1.45 PFLOP/s (cuBLAS in a loop 1.72).
+//
 // Few rows and a long window: the tiles of an item are split over n_split items, whose
 // unnormalised outputs, maxima and sums the last one to finish joins, in split order.
 //
@@ -241,6 +245,7 @@ struct WItem {
     int sb, nb, base;           // sink blocks, all blocks; position = list column + base behind the sinks
     int t0, t1;                 // tiles of this split
     int slot, sp;
+    int first, pieces;          // CROSS: the item's first piece, and how many CTAs have one
     uint32_t row0;              // row of out that the first position and head is
 };
 constexpr int kItemRing = 4;
@@ -264,8 +269,9 @@ struct WCtrl {
     int last;
     int total;                  // items
     int tiles;                  // q tiles (of 128 NQ rows) of one layer and kv head
-    int pre[kMaxBatch + 1];     // q tiles before each sequence
+    int pre[kMaxBatch + 1];     // q tiles before each sequence (a stream: key tiles of all q tiles)
     int len[kMaxBatch], cnt[kMaxBatch], start[kMaxBatch];
+    uint8_t order[kMaxBatch];   // a queue: the sequences, longest first (pre is in this order)
     WItem items[kItemRing];
 };
 constexpr int kWBars = static_cast<int>((offsetof(WCtrl, tmem)) / sizeof(uint64_t));
@@ -283,7 +289,7 @@ __device__ __forceinline__ WItem item_of(const WCtrl &c, const WindowParams &p, 
     q = qh;
     it.layer = p.n_layers == 1 ? 0 : q / c.tiles;
     // the last rows of a prompt first: they see the most keys
-    const int t = c.tiles - 1 - (q - it.layer * c.tiles);
+    const int t = CROSS ? q - it.layer * c.tiles : c.tiles - 1 - (q - it.layer * c.tiles);
     int lo = 0, hi = p.batch;
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
@@ -292,14 +298,17 @@ __device__ __forceinline__ WItem item_of(const WCtrl &c, const WindowParams &p, 
         else
             hi = mid;
     }
-    it.b = lo;
     const int first = (t - c.pre[lo]) * per;
+    if (CROSS)
+        lo = c.order[lo];
+    it.b = lo;
     it.np = min(per, c.cnt[lo] - first);
     it.r0 = c.start[lo] + first;
     if constexpr (CROSS) {      // (a sequence may be empty: no tiles)
         it.p0 = it.lo = it.sb = it.base = 0;
         it.end = c.len[lo];
         it.nb = (it.end + 15) >> 4;
+        it.pieces = 1;
     } else {
         it.p0 = c.len[lo] - c.cnt[lo] + first;
         it.end = it.p0 + it.np;
@@ -317,6 +326,61 @@ __device__ __forceinline__ WItem item_of(const WCtrl &c, const WindowParams &p, 
         it.t1 = static_cast<int>(static_cast<uint32_t>(n) * (it.sp + 1) / p.n_split);
     }
     it.slot = (it.layer * c.tiles + t) * p.n_kv_heads + it.kvh;
+    it.row0 = (static_cast<uint32_t>(it.layer * p.n_rows + it.r0) * p.n_kv_heads + it.kvh) << p.group_log2;
+    return it;
+}
+
+// A stream: the key tiles of all items in a row, unit by unit, sequence by sequence, q tile by q
+// tile, with kOver tiles' time in front of each item for its start and end; every CTA has an equal
+// share, and an item whose tiles lie in the shares of several is joined.
+constexpr int kOver = 2;
+
+struct Stream {
+    uint64_t per_unit, total, ctas;
+    __device__ __forceinline__ uint64_t start(uint64_t cta) const { return total * cta / ctas; }
+    // the CTA whose share has tile g
+    __device__ __forceinline__ int owner(uint64_t g) const { return static_cast<int>(((g + 1) * ctas - 1) / total); }
+};
+
+// What CTA `cta`, whose share ends at `end`, has of the item at tile g, and where it goes on; np 0: nothing.
+template <int ROWS, int KT>
+__device__ __forceinline__ WItem stream_item(const WCtrl &c, const WindowParams &p, const Stream &s, uint64_t g,
+                                             uint64_t end, int cta, uint64_t &next)
+{
+    WItem it;
+    const int per = ROWS >> p.group_log2;
+    const uint64_t unit = g / s.per_unit;
+    const uint32_t rem = static_cast<uint32_t>(g - unit * s.per_unit);
+    it.layer = static_cast<int>(unit / p.n_kv_heads);
+    it.kvh = static_cast<int>(unit) - it.layer * p.n_kv_heads;
+    int lo = 0, hi = p.batch;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (static_cast<uint32_t>(c.pre[mid]) <= rem)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    it.b = lo;
+    const uint32_t n = static_cast<uint32_t>(c.len[lo] + KT - 1) / KT, n1 = n + kOver;
+    const uint32_t in = rem - static_cast<uint32_t>(c.pre[lo]), tile = in / n1;
+    const int first = static_cast<int>(tile) * per, from = static_cast<int>(in - tile * n1);
+    it.r0 = c.start[lo] + first;
+    it.p0 = it.lo = it.sb = it.base = it.slot = 0;
+    it.end = c.len[lo];
+    it.nb = (it.end + 15) >> 4;
+    const uint64_t begin = g - from, stop = begin + n1;
+    next = stop < end ? stop : end;
+    it.t0 = max(from - kOver, 0);
+    it.t1 = max(static_cast<int>(next - begin) - kOver, 0);
+    // (an item without keys is its start's)
+    it.np = it.t1 > it.t0 || (n == 0 && from == 0) ? min(per, c.cnt[lo] - first) : 0;
+    const int c0 = n > 0 && begin + kOver < s.start(cta) ? s.owner(begin + kOver) : cta;
+    const int c1 = n > 0 && stop > end ? s.owner(stop - 1) : cta;
+    // pieces: a CTA's first is of the item at its share's start, its second of one that goes on
+    it.first = 2 * c0 + (s.start(c0) < begin ? 1 : 0);
+    it.sp = c0 == cta ? it.first : 2 * cta;
+    it.pieces = c1 - c0 + 1;
     it.row0 = (static_cast<uint32_t>(it.layer * p.n_rows + it.r0) * p.n_kv_heads + it.kvh) << p.group_log2;
     return it;
 }
@@ -454,6 +518,9 @@ __global__ void __launch_bounds__(128 + 128 * NQ, NQ == 1 && !F32 ? 2 : 1)
     constexpr int kSW = F32 ? KT + KT / 2 : KT;     // columns of a score buffer
     constexpr int kQTile = NS * kSW + (F32 ? 256 : 128);     // and of a q tile with O (and M)
     constexpr int NH = NS == 1 ? 2 : 1;     // parts in which a tile's weights are handed over
+    // Rows that see all keys are shared out by the producer, as it goes: in equal shares of all key
+    // tiles, or as a queue of whole items, longest first. The other roles take items until one is empty.
+    constexpr bool kStream = SPLIT && CROSS, kFed = CROSS;
     static_assert(NQ * kQTile <= static_cast<int>(kCols) && ST <= kMaxStages && NS <= 2);
     static_assert(!F32 || NQ == 1);
     static_assert((PARTS == 3) == F32 && PARTS >= 1 && PARTS <= 3);
@@ -528,7 +595,9 @@ __global__ void __launch_bounds__(128 + 128 * NQ, NQ == 1 && !F32 ? 2 : 1)
                     raise_error(p.err, bad);
             }
             high = max(high, __shfl_sync(0xffffffffu, upto, 31));
-            const int v = (n + per - 1) / per;
+            int v = (n + per - 1) / per;
+            if (kStream)
+                v *= (b < p.batch ? (c.len[b] + KT - 1) / KT : 0) + kOver;
             int x = v;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -542,7 +611,35 @@ __global__ void __launch_bounds__(128 + 128 * NQ, NQ == 1 && !F32 ? 2 : 1)
         }
         if (lane == 0) {
             c.tiles = run;
-            c.total = run * p.n_kv_heads * p.n_layers * p.n_split;
+            c.total = kStream ? run : run * p.n_kv_heads * p.n_layers * p.n_split;
+        }
+    }
+    if constexpr (CROSS && !SPLIT) {
+        // the queue's order: longest first, and the q tiles in front of each
+        __syncthreads();
+        for (int b = tid; b < p.batch; b += 128 + 128 * NQ) {
+            const int mine = c.len[b];
+            int at = 0;
+            for (int o = 0; o < p.batch; ++o)
+                at += c.len[o] > mine || (c.len[o] == mine && o < b);
+            c.order[at] = static_cast<uint8_t>(b);
+        }
+        __syncthreads();
+        if (warp == 0) {
+            int run = 0;
+            for (int b0 = 0; b0 < p.batch; b0 += 32) {
+                const int b = b0 + lane, v = b < p.batch ? (c.cnt[c.order[b]] + per - 1) / per : 0;
+                int x = v;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int y = __shfl_up_sync(0xffffffffu, x, o);
+                    if (lane >= o)
+                        x += y;
+                }
+                if (b < p.batch)
+                    c.pre[b] = run + x - v;
+                run += __shfl_sync(0xffffffffu, x, 31);
+            }
         }
     }
     tc_fence_before();
@@ -579,10 +676,11 @@ __global__ void __launch_bounds__(128 + 128 * NQ, NQ == 1 && !F32 ? 2 : 1)
         const uint32_t lane_addr = static_cast<uint32_t>(quad * 32) << 16;
         const int dp = rq >> p.group_log2, h = rq & (G - 1), nrows = it.np * G;
         const bool valid = rq < nrows, live = a * 128 + quad * 32 < nrows;
-        const size_t part = SPLIT ? static_cast<size_t>(it.slot) * p.n_split + it.sp : 0;
+        const size_t part = kStream ? it.sp : SPLIT ? static_cast<size_t>(it.slot) * p.n_split + it.sp : 0;
+        const bool cut = kStream ? it.pieces > 1 : SPLIT;
         if (it.t1 > it.t0) {
             const size_t my_row = it.row0 + dp * (p.n_kv_heads * G) + h;
-            const float inv = SPLIT ? 1.f : 1.f / l;
+            const float inv = cut ? 1.f : 1.f / l;
             if (!warp_wait(&c.od[a][(done - 1) % NS], ((done - 1) / NS) & 1, &c.abort))
                 return false;
             tc_fence_after();
@@ -617,7 +715,8 @@ __global__ void __launch_bounds__(128 + 128 * NQ, NQ == 1 && !F32 ? 2 : 1)
                         tmem_ld32(o_col(a) + lane_addr + 32 * q + 32, o[(q + 1) & 1]);
                     else
                         release();
-                    if constexpr (!SPLIT && kLines) {
+                    if (kLines && !cut) {
+                      if constexpr (kLines) {
 #pragma unroll
                         for (int x = 0; x < 16; ++x) {
                             const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * x] * inv, v[2 * x + 1] * inv);
@@ -629,7 +728,8 @@ __global__ void __launch_bounds__(128 + 128 * NQ, NQ == 1 && !F32 ? 2 : 1)
                                 const uint32_t row = it.row0 + (r >> p.group_log2) * (p.n_kv_heads * G) + (r & (G - 1));
                                 return r < nrows ? static_cast<long long>(row) * 256 + 64 * (q - 1) : -1;
                             });
-                    } else if (valid && !SPLIT) {
+                      }
+                    } else if (valid && !cut) {
 #pragma unroll
                         for (int x = 0; x < 32; ++x)
                             v[x] *= inv;
@@ -644,28 +744,91 @@ __global__ void __launch_bounds__(128 + 128 * NQ, NQ == 1 && !F32 ? 2 : 1)
             } else {
                 release();
             }
-        } else if (CROSS && !SPLIT && valid) {      // nothing to see
+        } else if (CROSS && !cut && valid) {        // nothing to see
             const float none[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
             const size_t my_row = it.row0 + dp * (p.n_kv_heads * G) + h;
 #pragma unroll 1
             for (int d = 0; d < kHeadDim; d += 8)
                 store_8<F32>(p, my_row * kHeadDim + d, none);
         }
-        if (SPLIT) {
+        if (SPLIT && cut) {
             if (valid)
                 p.part_ml[part * p.part_rows + rq] = make_float2(m, l);
             // every thread's partials before the ticket, the ticket before any read
             __threadfence();
             if (!out_sync())
                 return false;
+            const int pieces = kStream ? it.pieces : p.n_split;
+            int *ticket = p.tickets + (kStream ? it.first >> 1 : it.slot);
             if (tid == kOut0)
-                c.last = atomic_add_acq_rel_gpu(p.tickets + it.slot, 1) == p.n_split - 1;
+                c.last = atomic_add_acq_rel_gpu(ticket, 1) == pieces - 1;
             if (!out_sync())
                 return false;
             if (c.last != 0) {
                 if (tid == kOut0)
-                    p.tickets[it.slot] = 0;
+                    *ticket = 0;
                 __threadfence();
+                if constexpr (kStream) {
+                    // 32 threads a row, 4 dims each; several rows' loads on their way at once, pieces in
+                    // order of their CTAs, relative to the running maximum
+                    constexpr int kRowsAtOnce = 4;
+                    const int d = (tid - kOut0) & 31, w0 = (tid - kOut0) >> 5;
+                    for (int r0 = w0; r0 < nrows; r0 += 4 * NQ * kRowsAtOnce) {
+                        float4 acc[kRowsAtOnce];
+                        float top[kRowsAtOnce], den[kRowsAtOnce];
+#pragma unroll
+                        for (int i = 0; i < kRowsAtOnce; ++i) {
+                            acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+                            top[i] = -CUDART_INF_F;
+                            den[i] = 0.f;
+                        }
+#pragma unroll 2
+                        for (int sp = 0; sp < pieces; ++sp) {
+                            const size_t at = (sp == 0 ? static_cast<size_t>(it.first)
+                                                       : static_cast<size_t>(it.first & ~1) + 2 * sp) * p.part_rows;
+                            float2 ml[kRowsAtOnce];
+                            float4 v[kRowsAtOnce];
+#pragma unroll
+                            for (int i = 0; i < kRowsAtOnce; ++i) {
+                                const size_t r = at + min(r0 + 4 * NQ * i, nrows - 1);
+                                ml[i] = __ldcg(p.part_ml + r);
+                                v[i] = __ldcg(reinterpret_cast<const float4 *>(p.parts + r * kHeadDim) + d);
+                            }
+#pragma unroll
+                            for (int i = 0; i < kRowsAtOnce; ++i) {
+                                const float mn = fmaxf(top[i], ml[i].x);
+                                // (a piece whose maximum is not there counts as it is: its sum is not a number)
+                                const float was = mn == -CUDART_INF_F ? 1.f : ex2_approx((top[i] - mn) * p.scale_log2);
+                                const float is = mn == -CUDART_INF_F ? 1.f : ex2_approx((ml[i].x - mn) * p.scale_log2);
+                                acc[i].x = fmaf(is, v[i].x, acc[i].x * was);
+                                acc[i].y = fmaf(is, v[i].y, acc[i].y * was);
+                                acc[i].z = fmaf(is, v[i].z, acc[i].z * was);
+                                acc[i].w = fmaf(is, v[i].w, acc[i].w * was);
+                                den[i] = fmaf(is, ml[i].y, den[i] * was);
+                                top[i] = mn;
+                            }
+                        }
+#pragma unroll
+                        for (int i = 0; i < kRowsAtOnce; ++i) {
+                            const int r = r0 + 4 * NQ * i;
+                            if (r >= nrows)
+                                continue;
+                            const size_t o = static_cast<size_t>(it.row0 + (r >> p.group_log2) * (p.n_kv_heads * G) +
+                                                                 (r & (G - 1))) * kHeadDim + 4 * d;
+                            const float inv = 1.f / den[i];
+                            if constexpr (F32) {
+                                *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + o) =
+                                    make_float4(acc[i].x * inv, acc[i].y * inv, acc[i].z * inv, acc[i].w * inv);
+                            } else {
+                                const __nv_bfloat162 h[2] = {__floats2bfloat162_rn(acc[i].x * inv, acc[i].y * inv),
+                                                             __floats2bfloat162_rn(acc[i].z * inv, acc[i].w * inv)};
+                                *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.out) + o) =
+                                    *reinterpret_cast<const uint2 *>(h);
+                            }
+                        }
+                    }
+                    return true;
+                }
                 // a thread per (row, dim): 128 dims, NQ rows at a time; splits in order
                 const int d = (tid - kOut0) & 127;
                 for (int r = (tid - kOut0) >> 7; r < nrows; r += NQ) {
@@ -687,11 +850,10 @@ __global__ void __launch_bounds__(128 + 128 * NQ, NQ == 1 && !F32 ? 2 : 1)
                     const int dpr = r >> p.group_log2;
                     const size_t o = static_cast<size_t>(it.row0 + dpr * (p.n_kv_heads * G) + (r & (G - 1))) *
                                          kHeadDim + d;
-                    const float v = CROSS && it.end == 0 ? 0.f : acc / den;
                     if (F32)
-                        static_cast<float *>(p.out)[o] = v;
+                        static_cast<float *>(p.out)[o] = acc / den;
                     else
-                        static_cast<__nv_bfloat16 *>(p.out)[o] = __float2bfloat16_rn(v);
+                        static_cast<__nv_bfloat16 *>(p.out)[o] = __float2bfloat16_rn(acc / den);
                 }
             }
         }
@@ -712,10 +874,10 @@ __global__ void __launch_bounds__(128 + 128 * NQ, NQ == 1 && !F32 ? 2 : 1)
         bool ok = true;
         const int rq = a * 128 + rowi;
         uint32_t nth = 0;
-        for (int idx = blockIdx.x; idx < total; idx += gridDim.x, ++nth) {
+        for (int idx = blockIdx.x; kFed || idx < total; idx += gridDim.x, ++nth) {
             WItem it;
             ok = next_item(nth, it);
-            if (!ok)
+            if (!ok || (kFed && it.np == 0))
                 break;
             const int dp = rq >> p.group_log2;
             const bool valid = dp < it.np;
@@ -916,8 +1078,44 @@ __global__ void __launch_bounds__(128 + 128 * NQ, NQ == 1 && !F32 ? 2 : 1)
             int use = 0, items = 0;
             bool ok = true;
             uint32_t nth = 0;
-            for (int idx = blockIdx.x; idx < total && ok; idx += gridDim.x, ++nth) {
-                const WItem it = item_of<kRows, KT, SPLIT, CROSS>(c, p, idx);
+            Stream stream = {};
+            uint64_t g = 0, g_end = 0;
+            if constexpr (kStream) {
+                // (as many CTAs as have p.n_split tiles each)
+                stream.per_unit = static_cast<uint32_t>(total);
+                stream.total = stream.per_unit * static_cast<uint32_t>(p.n_kv_heads * p.n_layers);
+                const uint64_t most = (stream.total + p.n_split - 1) / p.n_split;
+                stream.ctas = most < gridDim.x ? most : gridDim.x;
+                if (blockIdx.x < stream.ctas) {
+                    g = stream.start(blockIdx.x);
+                    g_end = stream.start(blockIdx.x + 1);
+                }
+            }
+            bool over = false;          // the item that says so is out
+            int ahead = 0;              // the queue's next item
+            for (int idx = blockIdx.x; (kFed ? !over : idx < total) && ok; idx = CROSS && !SPLIT ? ahead : idx + gridDim.x, ++nth) {
+                WItem it;
+                if constexpr (kStream) {
+                    do {
+                        over = g >= g_end;
+                        if (over)
+                            it.np = 0;
+                        else
+                            it = stream_item<kRows, KT>(c, p, stream, g, g_end, blockIdx.x, g);
+                    } while (!over && it.np == 0);
+                } else if constexpr (CROSS) {
+                    over = idx >= total;
+                    if (over) {
+                        it.np = 0;
+                    } else {
+                        if (lane == 0)
+                            ahead = static_cast<int>(gridDim.x) + atomicAdd(p.tickets, 1);
+                        ahead = __shfl_sync(0xffffffffu, ahead, 0);
+                        it = item_of<kRows, KT, SPLIT, CROSS>(c, p, idx);
+                    }
+                } else {
+                    it = item_of<kRows, KT, SPLIT, CROSS>(c, p, idx);
+                }
                 ok = warp_wait(&c.ite[nth % kItemRing], ((nth / kItemRing) & 1) ^ 1, &c.abort);
                 if (!ok)
                     break;
@@ -926,7 +1124,7 @@ __global__ void __launch_bounds__(128 + 128 * NQ, NQ == 1 && !F32 ? 2 : 1)
                     mbar_arrive(&c.itf[nth % kItemRing]);
                 }
                 __syncwarp();
-                if (it.t0 == it.t1)
+                if (over || it.t0 == it.t1)
                     continue;
                 const long long unit = p.page_size
                                            ? static_cast<long long>(it.layer) * p.n_pages * p.n_kv_heads
@@ -997,6 +1195,14 @@ __global__ void __launch_bounds__(128 + 128 * NQ, NQ == 1 && !F32 ? 2 : 1)
                 }
             }
             if (lane == 0) {
+                if (CROSS && !SPLIT) {
+                    // the last CTA to be done with the queue leaves it as it was
+                    __threadfence();
+                    if (atomic_add_acq_rel_gpu(p.tickets + 1, 1) == static_cast<int>(gridDim.x) - 1) {
+                        p.tickets[0] = 0;
+                        p.tickets[1] = 0;
+                    }
+                }
                 if (!ok)
                     wfail(c, p.err);
                 // never leave a copy in flight into shared memory that is given up
@@ -1049,10 +1255,10 @@ __global__ void __launch_bounds__(128 + 128 * NQ, NQ == 1 && !F32 ? 2 : 1)
                 if (half == NH - 1)
                     umma_commit(&c.od[A][buf]);
             };
-            for (uint32_t idx = blockIdx.x; idx < all && ok; idx += gridDim.x) {
+            for (uint32_t idx = blockIdx.x; (kFed || idx < all) && ok; idx += gridDim.x) {
                 WItem it;
                 ok = next_item(nth++, it);
-                if (!ok)
+                if (!ok || (kFed && it.np == 0))
                     break;
                 const uint32_t end = seq + uniform(it.t1 - it.t0);
                 if (seq == end)
@@ -1127,10 +1333,10 @@ __global__ void __launch_bounds__(128 + 128 * NQ, NQ == 1 && !F32 ? 2 : 1)
             int use = 0;
             uint32_t nth = 0;
             bool ok = true;
-            for (int idx = blockIdx.x; idx < total && ok; idx += gridDim.x) {
+            for (int idx = blockIdx.x; (kFed || idx < total) && ok; idx += gridDim.x) {
                 WItem it;
                 ok = next_item(nth++, it);
-                if (!ok)
+                if (!ok || (kFed && it.np == 0))
                     break;
                 for (int t = it.t0; t < it.t1; ++t, ++use) {
                     const int st = use % ST;
@@ -1188,25 +1394,25 @@ cudaError_t launch_one(const WindowParams &p, const CUtensorMap &tm_k, const CUt
 }
 
 template <bool CROSS, int NQ, int KT, int ST, int NS, int QR, int PARTS, bool F32>
-cudaError_t launch_form(const WindowParams &p, const CUtensorMap &tm_k, const CUtensorMap &tm_v,
+cudaError_t launch_form(const WindowParams &p, bool split, const CUtensorMap &tm_k, const CUtensorMap &tm_v,
                         const CUtensorMap &tm_q, int grid, cudaStream_t stream)
 {
-    return p.n_split > 1 ? launch_one<NQ, KT, ST, NS, QR, PARTS, F32, true, CROSS>(p, tm_k, tm_v, tm_q, grid, stream)
-                         : launch_one<NQ, KT, ST, NS, QR, PARTS, F32, false, CROSS>(p, tm_k, tm_v, tm_q, grid, stream);
+    return split ? launch_one<NQ, KT, ST, NS, QR, PARTS, F32, true, CROSS>(p, tm_k, tm_v, tm_q, grid, stream)
+                 : launch_one<NQ, KT, ST, NS, QR, PARTS, F32, false, CROSS>(p, tm_k, tm_v, tm_q, grid, stream);
 }
 
 // The form for items of `rows` operand rows.
 template <bool CROSS>
-cudaError_t launch_rows(const WindowParams &p, int rows, const CUtensorMap &tm_k, const CUtensorMap &tm_v,
-                        const CUtensorMap &tm_q, int grid, cudaStream_t stream)
+cudaError_t launch_rows(const WindowParams &p, int rows, bool split, const CUtensorMap &tm_k,
+                        const CUtensorMap &tm_v, const CUtensorMap &tm_q, int grid, cudaStream_t stream)
 {
     if (rows == 256)        // (bf16 outputs only)
-        return launch_form<CROSS, 2, 128, 2, 1, 128, 1, false>(p, tm_k, tm_v, tm_q, grid, stream);
+        return launch_form<CROSS, 2, 128, 2, 1, 128, 1, false>(p, split, tm_k, tm_v, tm_q, grid, stream);
     if (rows == 16)
-        return p.out_fp32 ? launch_form<CROSS, 1, 64, 4, 2, 16, 3, true>(p, tm_k, tm_v, tm_q, grid, stream)
-                          : launch_form<CROSS, 1, 64, 3, 2, 16, 2, false>(p, tm_k, tm_v, tm_q, grid, stream);
-    return p.out_fp32 ? launch_form<CROSS, 1, 64, 4, 2, 128, 3, true>(p, tm_k, tm_v, tm_q, grid, stream)
-                      : launch_form<CROSS, 1, 64, 2, 2, 128, 1, false>(p, tm_k, tm_v, tm_q, grid, stream);
+        return p.out_fp32 ? launch_form<CROSS, 1, 64, 4, 2, 16, 3, true>(p, split, tm_k, tm_v, tm_q, grid, stream)
+                          : launch_form<CROSS, 1, 64, 3, 2, 16, 2, false>(p, split, tm_k, tm_v, tm_q, grid, stream);
+    return p.out_fp32 ? launch_form<CROSS, 1, 64, 4, 2, 128, 3, true>(p, split, tm_k, tm_v, tm_q, grid, stream)
+                      : launch_form<CROSS, 1, 64, 2, 2, 128, 1, false>(p, split, tm_k, tm_v, tm_q, grid, stream);
 }
 
 }  // namespace
