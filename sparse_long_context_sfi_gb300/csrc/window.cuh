@@ -56,6 +56,7 @@
 
 #include <climits>
 #include <cstddef>
+#include <type_traits>
 
 namespace sfi {
 namespace {
@@ -241,13 +242,25 @@ constexpr int kMaxStages = 4;
 struct WItem {
     int b, layer, kvh;
     int r0, np, p0;             // first packed row, positions, first position
-    int lo, end;                // first position of the joint window, and one past the last seen
+    int lo;                     // first position of the joint window
     int sb, nb, base;           // sink blocks, all blocks; position = list column + base behind the sinks
     int t0, t1;                 // tiles of this split
     int slot, sp;
-    int first, pieces;          // CROSS: the item's first piece, and how many CTAs have one
     uint32_t row0;              // row of out that the first position and head is
 };
+// Of rows that see all keys: the sequence's length; the item's first piece, and how many CTAs have
+// one. (Fields that an item of the other kind does not have: with them, two q tiles spill.)
+struct CPart {
+    int end, first, pieces;
+};
+struct CItem : WItem, CPart {
+};
+__device__ __forceinline__ int end_of(const WItem &it) { return it.p0 + it.np; }
+__device__ __forceinline__ int end_of(const CItem &it) { return it.end; }
+__device__ __forceinline__ int first_of(const WItem &) { return 0; }
+__device__ __forceinline__ int first_of(const CItem &it) { return it.first; }
+__device__ __forceinline__ int pieces_of(const WItem &) { return 1; }
+__device__ __forceinline__ int pieces_of(const CItem &it) { return it.pieces; }
 constexpr int kItemRing = 4;
 
 struct WCtrl {
@@ -271,15 +284,19 @@ struct WCtrl {
     int tiles;                  // q tiles (of 128 NQ rows) of one layer and kv head
     int pre[kMaxBatch + 1];     // q tiles before each sequence (a stream: key tiles of all q tiles)
     int len[kMaxBatch], cnt[kMaxBatch], start[kMaxBatch];
-    uint8_t order[kMaxBatch];   // a queue: the sequences, longest first (pre is in this order)
     WItem items[kItemRing];
+    CPart parts[kItemRing];
+    uint8_t order[kMaxBatch];   // a queue: the sequences, longest first (pre is in this order)
 };
 constexpr int kWBars = static_cast<int>((offsetof(WCtrl, tmem)) / sizeof(uint64_t));
 
+template <bool CROSS>
+using Item = std::conditional_t<CROSS, CItem, WItem>;
+
 template <int ROWS, int KT, bool SPLIT, bool CROSS>
-__device__ __forceinline__ WItem item_of(const WCtrl &c, const WindowParams &p, int idx)
+__device__ __forceinline__ Item<CROSS> item_of(const WCtrl &c, const WindowParams &p, int idx)
 {
-    WItem it;
+    Item<CROSS> it;
     const int per = ROWS >> p.group_log2;
     // (an integer division costs ~40 instructions: taken only where it says something)
     int q = SPLIT ? idx / p.n_split : idx;
@@ -311,12 +328,11 @@ __device__ __forceinline__ WItem item_of(const WCtrl &c, const WindowParams &p, 
         it.pieces = 1;
     } else {
         it.p0 = c.len[lo] - c.cnt[lo] + first;
-        it.end = it.p0 + it.np;
         it.lo = max(0, it.p0 - p.n_window + 1);
         const int lo_blk = it.lo >> 4;
         it.sb = min((p.n_sink >> 4) + ((p.n_sink & 15) != 0), lo_blk);
         it.base = (lo_blk - it.sb) * 16;
-        it.nb = it.sb + ((it.end - 1) >> 4) - lo_blk + 1;
+        it.nb = it.sb + ((it.p0 + it.np - 1) >> 4) - lo_blk + 1;
     }
     const int n = (it.nb + KT / 16 - 1) / (KT / 16);
     it.t0 = 0;
@@ -344,10 +360,10 @@ struct Stream {
 
 // What CTA `cta`, whose share ends at `end`, has of the item at tile g, and where it goes on; np 0: nothing.
 template <int ROWS, int KT>
-__device__ __forceinline__ WItem stream_item(const WCtrl &c, const WindowParams &p, const Stream &s, uint64_t g,
+__device__ __forceinline__ CItem stream_item(const WCtrl &c, const WindowParams &p, const Stream &s, uint64_t g,
                                              uint64_t end, int cta, uint64_t &next)
 {
-    WItem it;
+    CItem it;
     const int per = ROWS >> p.group_log2;
     const uint64_t unit = g / s.per_unit;
     const uint32_t rem = static_cast<uint32_t>(g - unit * s.per_unit);
@@ -652,10 +668,12 @@ __global__ void __launch_bounds__(128 + 128 * NQ, NQ == 1 && !F32 ? 2 : 1)
 
     // The n-th item of this CTA, for the roles other than the producer: what they do not use of it
     // is never read. False if the wait ran out.
-    auto next_item = [&](uint32_t n, WItem &it) -> bool {
+    auto next_item = [&](uint32_t n, Item<CROSS> &it) -> bool {
         if (!warp_wait(&c.itf[n % kItemRing], (n / kItemRing) & 1, &c.abort))
             return false;
-        it = c.items[n % kItemRing];
+        static_cast<WItem &>(it) = c.items[n % kItemRing];
+        if constexpr (CROSS)
+            static_cast<CPart &>(it) = c.parts[n % kItemRing];
         __syncwarp();
         if (lane == 0)
             mbar_arrive(&c.ite[n % kItemRing]);
@@ -671,13 +689,13 @@ __global__ void __launch_bounds__(128 + 128 * NQ, NQ == 1 && !F32 ? 2 : 1)
     };
     // O of q tile a once its `done`-th tile's product is complete, divided and written (or left as
     // a partial and joined); each thread a row. False if a wait ran out.
-    auto finish = [&](int a, const WItem &it, uint32_t done, float m, float l) -> bool {
+    auto finish = [&](int a, const Item<CROSS> &it, uint32_t done, float m, float l) -> bool {
         const int quad = warp & 3, rq = a * 128 + quad * 32 + lane;
         const uint32_t lane_addr = static_cast<uint32_t>(quad * 32) << 16;
         const int dp = rq >> p.group_log2, h = rq & (G - 1), nrows = it.np * G;
         const bool valid = rq < nrows, live = a * 128 + quad * 32 < nrows;
         const size_t part = kStream ? it.sp : SPLIT ? static_cast<size_t>(it.slot) * p.n_split + it.sp : 0;
-        const bool cut = kStream ? it.pieces > 1 : SPLIT;
+        const bool cut = kStream ? pieces_of(it) > 1 : SPLIT;
         if (it.t1 > it.t0) {
             const size_t my_row = it.row0 + dp * (p.n_kv_heads * G) + h;
             const float inv = cut ? 1.f : 1.f / l;
@@ -758,8 +776,8 @@ __global__ void __launch_bounds__(128 + 128 * NQ, NQ == 1 && !F32 ? 2 : 1)
             __threadfence();
             if (!out_sync())
                 return false;
-            const int pieces = kStream ? it.pieces : p.n_split;
-            int *ticket = p.tickets + (kStream ? it.first >> 1 : it.slot);
+            const int pieces = kStream ? pieces_of(it) : p.n_split;
+            int *ticket = p.tickets + (kStream ? first_of(it) >> 1 : it.slot);
             if (tid == kOut0)
                 c.last = atomic_add_acq_rel_gpu(ticket, 1) == pieces - 1;
             if (!out_sync())
@@ -784,8 +802,8 @@ __global__ void __launch_bounds__(128 + 128 * NQ, NQ == 1 && !F32 ? 2 : 1)
                         }
 #pragma unroll 2
                         for (int sp = 0; sp < pieces; ++sp) {
-                            const size_t at = (sp == 0 ? static_cast<size_t>(it.first)
-                                                       : static_cast<size_t>(it.first & ~1) + 2 * sp) * p.part_rows;
+                            const size_t at = (sp == 0 ? static_cast<size_t>(first_of(it))
+                                                       : static_cast<size_t>(first_of(it) & ~1) + 2 * sp) * p.part_rows;
                             float2 ml[kRowsAtOnce];
                             float4 v[kRowsAtOnce];
 #pragma unroll
@@ -875,7 +893,7 @@ __global__ void __launch_bounds__(128 + 128 * NQ, NQ == 1 && !F32 ? 2 : 1)
         const int rq = a * 128 + rowi;
         uint32_t nth = 0;
         for (int idx = blockIdx.x; kFed || idx < total; idx += gridDim.x, ++nth) {
-            WItem it;
+            Item<CROSS> it;
             ok = next_item(nth, it);
             if (!ok || (kFed && it.np == 0))
                 break;
@@ -885,7 +903,7 @@ __global__ void __launch_bounds__(128 + 128 * NQ, NQ == 1 && !F32 ? 2 : 1)
             const int i = it.p0 + dp;                       // this row's position
             // it sees the list columns [0, e1) and [a2, e2)
             const int e1 = CROSS ? 0 : min(p.n_sink, i + 1);
-            const int a2 = CROSS ? 0 : max(i - p.n_window + 1, 0) - it.base, e2 = CROSS ? it.end : i - it.base + 1;
+            const int a2 = CROSS ? 0 : max(i - p.n_window + 1, 0) - it.base, e2 = CROSS ? end_of(it) : i - it.base + 1;
             float m = -CUDART_INF_F, l = 0.f;
             for (int t = it.t0; t < it.t1; ++t, ++done) {
                 const int buf = done % NS;
@@ -1094,7 +1112,7 @@ __global__ void __launch_bounds__(128 + 128 * NQ, NQ == 1 && !F32 ? 2 : 1)
             bool over = false;          // the item that says so is out
             int ahead = 0;              // the queue's next item
             for (int idx = blockIdx.x; (kFed ? !over : idx < total) && ok; idx = CROSS && !SPLIT ? ahead : idx + gridDim.x, ++nth) {
-                WItem it;
+                Item<CROSS> it;
                 if constexpr (kStream) {
                     do {
                         over = g >= g_end;
@@ -1121,6 +1139,8 @@ __global__ void __launch_bounds__(128 + 128 * NQ, NQ == 1 && !F32 ? 2 : 1)
                     break;
                 if (lane == 0) {
                     c.items[nth % kItemRing] = it;
+                    if constexpr (CROSS)
+                        c.parts[nth % kItemRing] = it;
                     mbar_arrive(&c.itf[nth % kItemRing]);
                 }
                 __syncwarp();
@@ -1256,7 +1276,7 @@ __global__ void __launch_bounds__(128 + 128 * NQ, NQ == 1 && !F32 ? 2 : 1)
                     umma_commit(&c.od[A][buf]);
             };
             for (uint32_t idx = blockIdx.x; (kFed || idx < all) && ok; idx += gridDim.x) {
-                WItem it;
+                Item<CROSS> it;
                 ok = next_item(nth++, it);
                 if (!ok || (kFed && it.np == 0))
                     break;
@@ -1334,10 +1354,11 @@ __global__ void __launch_bounds__(128 + 128 * NQ, NQ == 1 && !F32 ? 2 : 1)
             uint32_t nth = 0;
             bool ok = true;
             for (int idx = blockIdx.x; (kFed || idx < total) && ok; idx += gridDim.x) {
-                WItem it;
+                Item<CROSS> it;
                 ok = next_item(nth++, it);
                 if (!ok || (kFed && it.np == 0))
                     break;
+                const int last = end_of(it) - 1;
                 for (int t = it.t0; t < it.t1; ++t, ++use) {
                     const int st = use % ST;
                     ok = warp_wait(&c.vf[st], (use / ST) & 1, &c.abort);
@@ -1350,7 +1371,7 @@ __global__ void __launch_bounds__(128 + 128 * NQ, NQ == 1 && !F32 ? 2 : 1)
                         const int r = i * 32 + lane, col = t * KT + r, blk = col >> 4;
                         const int pos = col + (blk < it.sb ? 0 : it.base);
                         // (blocks behind the list were filled with zeros)
-                        const bool seen = blk >= it.nb || (pos < it.end && (CROSS || pos < p.n_sink || pos >= it.lo));
+                        const bool seen = blk >= it.nb || (pos <= last && (CROSS || pos < p.n_sink || pos >= it.lo));
                         uint32_t m = __ballot_sync(0xffffffffu, !seen);
                         wrote = wrote || m != 0;
                         while (m) {
