@@ -163,6 +163,54 @@ def test_jumps_of_the_maximum():
     assert torch.isfinite(c.out[:, :64]).all()
 
 
+def jump_case(rows, hq, hkv, n, places, sizes, seed=3):
+    """Keys that a row's query finds at `places` with ever larger logits, of `sizes` in powers of e."""
+    c = Case([n], [rows], hq, hkv, seed=seed)
+    for i, (at, size) in enumerate(zip(places, sizes)):
+        for h in range(hkv):
+            # (the first query head of the group, one row after the other)
+            q = c.q[0, i % rows, h * (hq // hkv)].double()
+            c.flat_k[0, 0, h, at] = (q * (size * D ** 0.5 / float(q @ q))).to(torch.bfloat16)
+    return c
+
+
+@pytest.mark.parametrize("fp32", [False, True])
+@pytest.mark.parametrize("rows,hq,hkv", [(100, 8, 2), (40, 2, 2), (3, 4, 2)])
+@pytest.mark.parametrize("column", [0, 5, 33, 40, 64, 70, 97, 127])
+def test_maxima_far_above_the_first_tile(column, rows, hq, hkv, fp32):
+    """Jumps by 2^64 and more in every 32-column piece of later tiles, of either size of tiles."""
+    n = 1400
+    places = [256 + column, 256 + (column + 31) % 128, 512 + column, 640 + column, 1024 + (column + 64) % 128]
+    c = jump_case(rows, hq, hkv, n, places, [60.0, 120.0, 180.0, 300.0, 500.0], seed=column)
+    c.run(fp32)
+    torch.cuda.synchronize()
+    got = c.out.double().cpu().numpy()[0, :rows]
+    q, k, v = (t.double().cpu().numpy() for t in (c.q, c.flat_k, c.flat_v))
+    o, mag = cross_attention(q[0, :rows], k[0, 0, :, :n], v[0, 0, :, :n])
+    # Logits of up to 500 and more: a weight's relative error is its logit's absolute one, 128 products and a
+    # scaling in fp32 at 2^-24 each of sum |q_d k_d| / sqrt(128) <= |q| |k| / sqrt(128), twice
+    norm = np.linalg.norm(q[0, :rows], axis=-1).max() * np.linalg.norm(k[0, 0, :, :n], axis=-1).max() / 128 ** 0.5
+    err = 2 * 130 * 2.0 ** -24 * norm
+    parts = fp32 or rows * (hq // hkv) <= 16
+    tol = (1e-4 + err + (0 if parts else 2.0 ** -8)) * mag + (0 if fp32 else 2.0 ** -8) * np.abs(o)
+    assert (np.abs(got - o) <= tol).all(), np.abs(got - o).max()
+
+
+def test_keys_of_minus_infinity_first():
+    """A first tile whose logits are all -inf, and a sequence that has no others: its sum is nothing."""
+    c = Case([400, 100], [40, 2], 2, 2)
+    c.q[..., 0] = 1.0
+    c.flat_k[0, 0, :, :300] = 0
+    c.flat_k[0, 0, :, :300, 0] = float("-inf")
+    c.run(False)
+    torch.cuda.synchronize()
+    q, k, v = (t.double().cpu().numpy() for t in (c.q, c.flat_k, c.flat_v))
+    o, mag = cross_attention(q[0, :40], k[0, 0, :, 300:400], v[0, 0, :, 300:400])
+    got = c.out.double().cpu().numpy()
+    assert (np.abs(got[0, :40] - o) <= (1e-4 + 2.0 ** -8) * mag + 2.0 ** -8 * np.abs(o)).all()
+    assert np.isfinite(got[0, 40:42]).all()
+
+
 def test_bad_inputs_are_reported_and_skipped():
     c = Case([300, 200, 100], [50, 60, 70], 8, 2, paged=True)
     c.run(max_rows=60)
