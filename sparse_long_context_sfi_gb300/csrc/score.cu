@@ -268,8 +268,8 @@ struct Place {
     }
 };
 
-constexpr int kBuffer = 256;        // of the tokens that may be among the best
 constexpr int kAlone = 64;          // pieces that the first warp looks through by itself
+constexpr int kBuffer = 8 * kAlone; // of the tokens that may be among the best: all of those, at least
 
 // Every lane keeps the highest logit of its chunks, which chunk it is, and the highest of all
 // others. K lanes have a logit of `least`, the K-th highest lane's, or more, so all of the K best
@@ -294,7 +294,7 @@ __global__ void __launch_bounds__(32 * kScoreWarps, 4) score_kernel(const ScoreP
     pdl_wait();
     const Place<T> at(p, blockIdx.x);
     const int first = (at.split * warps + warp) * kStep;
-    // chunks [in0, in1) lie within the row
+    // chunks from in0 up to in1 lie within the row
     const int in0 = at.shift > 0 ? 1 : 0, in1 = (p.vocab + at.shift) / V - kStep;
     const uint4 *base = reinterpret_cast<const uint4 *>(at.x - at.shift) + lane;
     uint4 w[kPieces];

@@ -128,6 +128,36 @@ def test_ties(n_top):
     Run(x, token, n_top).check()
 
 
+@pytest.mark.parametrize("kind", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("vocab", [255, 256, 257, 300, 511, 600, 1500, 33000])
+def test_equal_logits(vocab, kind):
+    """All tokens are among the best, more than wait anywhere; some of them higher, some masked."""
+    for rows in (1, 700 if vocab < 1000 else 30):
+        x, token = logits(rows, vocab, kind, gap=5)
+        x.fill_(0.25)
+        for n_top in (3, 32):
+            Run(x, token, n_top).check()
+        x[:, vocab // 2:vocab // 2 + 40] = 7.0
+        x[:, :3] = -INF
+        Run(x, token, 32).check()
+        x[:, 5:] = -INF                 # fewer tokens than places
+        Run(x, token, 32).check()
+
+
+@pytest.mark.parametrize("n_top", [4, 20, 32])
+@pytest.mark.parametrize("vocab", [4000, 40000])
+def test_best_tokens_of_few_lanes(vocab, n_top):
+    """The best tokens side by side, and at the distances at which one lane meets them."""
+    for rows in (2, 300):
+        x, token = logits(rows, vocab, torch.bfloat16)
+        x[:, 1000:1040] += 30.0
+        Run(x, token, n_top).check()
+        x, token = logits(rows, vocab, seed=1)
+        x[:, 7::512] += 30.0
+        x[:, 8::1024] += 60.0
+        Run(x, token, n_top).check()
+
+
 @pytest.mark.parametrize("n_top", [1, 16, 32])
 @pytest.mark.parametrize("down", [False, True])
 def test_sorted_rows(down, n_top):
