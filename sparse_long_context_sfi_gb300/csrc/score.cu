@@ -18,6 +18,8 @@
 // warps that wait for the one that finishes).
 #include "vocab.cuh"
 
+#include <cfloat>
+
 namespace sfi {
 namespace {
 
@@ -197,8 +199,8 @@ __device__ __noinline__ void load_edge(const T *row, int shift, int vocab, int p
     load_pieces<T, 4>(row, shift, vocab, piece, w);
 }
 
-// The terms of a chunk whose reference is from kLarge on, of either sign, or -inf, or whose logits
-// are not numbers: what vocab.cuh says, one by one.
+// The terms of a chunk whose reference is from kLarge on, of either sign, or whose highest logit is
+// not a number that counts: what vocab.cuh says, one by one.
 template <typename T>
 __device__ __noinline__ Sums odd_chunk(Sums a, float cm, const uint4 *w)
 {
@@ -332,10 +334,10 @@ __global__ void __launch_bounds__(32 * kScoreWarps, 4) score_kernel(const ScoreP
     for (int c = first; c < at.pieces; c += stride) {
         const float cm = Part<T>::highest(w);
         if (TOP) {
-            const bool up = cm > m1;
-            m2 = fmaxf(m2, up ? m1 : cm);
-            m1 = up ? cm : m1;
-            c1 = up ? c : c1;
+            const bool best = cm > m1;
+            m2 = fmaxf(m2, best ? m1 : cm);
+            m1 = best ? cm : m1;
+            c1 = best ? c : c1;
         }
         if (RANK) {
 #pragma unroll
@@ -343,7 +345,8 @@ __global__ void __launch_bounds__(32 * kScoreWarps, 4) score_kernel(const ScoreP
                 part.count(w[i], c + 32 * i + lane <= given_piece ? xg : xa);
             part.settle();
         }
-        const float rn = fmaxf(a.R, cm * kLog2e4);
+        // (masked tokens alone so far: they add nothing to any reference, and it stays -inf)
+        const float up = fmaxf(a.R, cm * kLog2e4), rn = up == -CUDART_INF_F ? 0.f : up;
         const bool usual = fabsf(rn) < kLarge * kLog2e4;
         if (!usual) {
             uint4 copy[kPieces];
@@ -351,12 +354,12 @@ __global__ void __launch_bounds__(32 * kScoreWarps, 4) score_kernel(const ScoreP
             for (int i = 0; i < kPieces; ++i)
                 copy[i] = w[i];
             a = odd_chunk<T>(a, cm, copy);
-        } else if (rn > a.R) {
-            const float d = 4.f * (a.R - rn), f = ex2(d);
+        } else if (up > a.R) {
+            const float d = 4.f * (a.R - up), f = ex2(d);
             if (ENT)                // (d may be beyond what 32 bits hold)
                 a.t = f != 0.f ? (a.t + a.s * d) * f : 0.f;
             a.s *= f;
-            a.R = rn;
+            a.R = up;
         }
         // each piece's successor is asked for when its tokens are in registers: 64 bytes a lane are on
         // their way (32 are too few to keep HBM busy)
@@ -438,6 +441,9 @@ __global__ void __launch_bounds__(32 * kScoreWarps, 4) score_kernel(const ScoreP
                 }
                 hm = rest;
             }
+            // (fewer than K lanes have a token that is not masked: all such tokens, and the lowest masked
+            // ones behind them)
+            least = fmaxf(least, -FLT_MAX);
             int n1 = 0, n2 = 0;
             for (int i = 0; i < warps; ++i) {
                 const int l = 32 * i + lane;
@@ -525,6 +531,15 @@ __global__ void __launch_bounds__(32 * kScoreWarps, 4) score_kernel(const ScoreP
         if (n_cand > kBuffer)
             best = merged(best, sh_x, sh_v, K * warps, K, lane);
         best = merged(best, cand_x, cand_v, min(n_cand, kBuffer), K, lane);
+        if (sh_least == -FLT_MAX) {
+            const int piece = at.split * warps * kStep;
+            for (int v0 = max(piece * V - at.shift, 0); v0 < p.vocab && best.tv < 0; v0 += 32) {
+                const int v = v0 + lane;
+                const bool own = v < p.vocab && (v + at.shift) / V / (warps * kStep) % p.splits == at.split;
+                const bool masked = own && static_cast<float>(at.x[v]) == -CUDART_INF_F;
+                best.offer(-CUDART_INF_F, masked ? v : -1, K, lane);
+            }
+        }
     }
     if (warps > 1)
         a = warp_join(lane < warps ? sh_sums[lane] : none);

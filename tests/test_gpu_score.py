@@ -181,6 +181,27 @@ def test_masked_tokens(rows):
     assert float(r.lp[2]) == -INF
 
 
+@pytest.mark.parametrize("kind", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("rows,vocab", [(2, 40), (3, 5000), (1, 60000), (700, 2000), (40, 40000)])
+@pytest.mark.parametrize("left", [1, 2, 7, 19, 20, 21, 40])
+def test_few_tokens_left(left, rows, vocab, kind):
+    """A grammar's mask: fewer tokens than places (or as many, or a few more), near each other and apart;
+    the places behind them are the lowest masked tokens."""
+    x, token = logits(rows, vocab, kind, gap=1)
+    keep = torch.zeros((rows, vocab), dtype=torch.bool, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(left)
+    for r in range(rows):
+        if r % 3 == 0:
+            keep[r, torch.randperm(vocab, generator=g, device="cuda")[:left]] = True
+        elif r % 3 == 1:
+            keep[r, :left] = True
+        else:
+            keep[r, vocab - left:] = True
+    x[~keep] = -INF
+    Run(x, token, 20).check()
+    Run(x, token, 32).check()
+
+
 @pytest.mark.parametrize("lowest", [-3.0e38, torch.finfo(torch.float32).min])
 def test_masks_of_the_lowest_value(lowest):
     x, token = logits(3, 5000)
