@@ -270,8 +270,7 @@ struct Place {
     }
 };
 
-constexpr int kAlone = 64;          // pieces that the first warp looks through by itself
-constexpr int kBuffer = 8 * kAlone; // of the tokens that may be among the best: all of those, at least
+constexpr int kBuffer = 256;        // of the tokens that may be among the best
 
 // Every lane keeps the highest logit of its chunks, which chunk it is, and the highest of all
 // others. K lanes have a logit of `least`, the K-th highest lane's, or more, so all of the K best
@@ -469,7 +468,8 @@ __global__ void __launch_bounds__(32 * kScoreWarps, 4) score_kernel(const ScoreP
         const int begun = at.split * warps * kStep, mid = n_one * kPieces;
         const int rounds = at.pieces > begun ? (at.pieces - begun + stride - 1) / stride : 0;
         const int total = mid + n_all * rounds * kPieces;
-        const bool alone = total <= kAlone;
+        // (the first warp looks through as many pieces by itself as surely fit the buffer)
+        const bool alone = total * V <= kBuffer;
         const int step = alone ? 32 : blockDim.x;
         constexpr int kU = 2;           // pieces of a thread on their way at once
         for (int i0 = warp * 32; i0 < total && (!alone || warp == 0); i0 += kU * step) {
