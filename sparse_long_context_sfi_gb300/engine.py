@@ -225,6 +225,8 @@ class SfiState:
         (pos: device int32 [B], None: the lengths); rows may then be a fused projection's."""
         if rope is not None:
             q, k_new = self._turned(rope, q, k_new, pos, active, stream)
+        elif pos is not None:
+            raise ValueError("pos goes with rope")
         return self._step(q, k_new, v_new, slow_b, None, active, out, out_fp32, stream, fused)
 
     def _turned(self, rope, q, k_new, pos, active, stream):
@@ -754,6 +756,8 @@ class TokenScores:
                 out["entropy"] = new(torch.float32, rows)
             if n_top:
                 out["top_token"], out["top_logprob"] = new(torch.int32, rows, n_top), new(torch.float32, rows, n_top)
+        if rows == 0:
+            return out
         sc = SfiScoring(n_rows=rows, vocab=vocab, logits_fp32=1 if logits.dtype == torch.float32 else 0, n_top=n_top,
                         row_stride=stride, logits=logits.data_ptr(),
                         token=None if token is None else token.data_ptr(),

@@ -55,6 +55,13 @@ def test_positions_without_rope():
         state().window_step(out_fp32=False, pos=torch.zeros(B, dtype=torch.int32), **arrays(B))
 
 
+def test_step_positions_without_rope():
+    a = {k: v for k, v in arrays(B).items()}
+    with pytest.raises(ValueError):
+        state().step(a["q"], a["k_new"], a["v_new"], np.ones(B, bool), a["out"],
+                     pos=torch.zeros(B, dtype=torch.int32))
+
+
 def test_rope_arguments():
     w = torch.ones(D, dtype=BF)
     for kw in (dict(q_norm=w.float()), dict(k_norm=torch.ones(64, dtype=BF)), dict(q_norm=w, norm_eps=0.0),

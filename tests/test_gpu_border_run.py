@@ -231,3 +231,33 @@ def test_encoder_inputs_come_and_go():
     enc.attend(q[:, :3].contiguous(), out)
     torch.cuda.synchronize()
     assert (out == 0).all() and int(enc.err[0]) == 0 and enc.lens.tolist() == [0, 0, 0]
+
+
+def test_nothing_to_score():
+    s = TokenScores()
+    out = s.score(torch.zeros((0, 50), device="cuda"), torch.zeros(0, dtype=torch.int32, device="cuda"), n_top=3)
+    assert out["logprob"].shape == (0,) and out["top_token"].shape == (0, 3)
+
+
+def test_rope_rows_of_one_projection():
+    """prefill on rows of a fused projection, and with given positions, as on packed rows turned before."""
+    rope = Rope(rot_dim=64, scaling="ramp", factor=4.0, original_len=64.0)
+    g = torch.Generator(device="cuda").manual_seed(6)
+    rnd = lambda *s: torch.randn(s, generator=g, device="cuda").to(BF)
+    x = rnd(1, 30, HQ + 2 * HKV, D)
+    q, k, v = x.split([HQ, HKV, HKV], 2)
+    pos = torch.randint(0, 100000, (30,), generator=g, device="cuda", dtype=torch.int32)
+    for given in (None, pos):
+        a, b = make_state(batch=2), make_state(batch=2, paged=False)
+        outs = [torch.zeros((1, 30, HQ, D), dtype=BF, device="cuda") for _ in "ab"]
+        a.prefill(q, k, v, [10, 20], outs[0], rope=rope, pos=given)
+        io = sfi.SfiRopeRows(q=q.data_ptr(), q_stride=q.stride(1), k=k.data_ptr(), k_stride=k.stride(1),
+                             pos=None if given is None else given.data_ptr())
+        tq, tk = torch.empty((1, 30, HQ, D), dtype=BF, device="cuda"), torch.empty((1, 30, HKV, D), dtype=BF, device="cuda")
+        io.q_out, io.k_out = tq.data_ptr(), tk.data_ptr()
+        start = torch.tensor([0, 10, 30], dtype=torch.int32, device="cuda")
+        sfi.sfi_rope_apply(b._whole(), rope.desc, io, start, 30, 20)
+        b.prefill(tq, tk, v.contiguous(), [10, 20], outs[1])
+        torch.cuda.synchronize()
+        assert torch.equal(outs[0], outs[1]) and outs[0].abs().sum() > 0
+        assert int(a.err[0]) == 0 and int(b.err[0]) == 0
