@@ -144,6 +144,51 @@ def test_fp32_sums_over_long_states():
         assert np.linalg.norm(d) <= 2e-6 * np.linalg.norm(o)
 
 
+@pytest.mark.parametrize("fp32", [False, True])
+@pytest.mark.parametrize("paged", [False, True])
+def test_many_short_items(paged, fp32):
+    """More items than twice the CTAs, of very different lengths, empty ones in rows: a queue."""
+    g = np.random.default_rng(5)
+    lens = [0] * 9 + g.integers(0, 300, 20).tolist() + [0] * 10 + [1, 2, 16, 17, 400] + [0] * 6
+    rows = g.integers(0, 90, len(lens)).tolist()
+    c = Case(lens, rows, 16, 16, paged=paged, seed=1)
+    c.run(fp32)
+    c.check(fp32)
+
+
+@pytest.mark.parametrize("paged", [False, True])
+def test_many_long_items(paged):
+    """The same with items of two q tiles."""
+    lens = [700, 0, 0, 900, 513, 1, 0, 640, 64, 0]
+    c = Case(lens, [257, 300, 256, 200, 129, 700, 128, 40, 300, 255], 32, 16, paged=paged, seed=2)
+    c.run(False)
+    c.check(False)
+    again = c.out.clone()
+    c.run(False, ws=c.ws)
+    torch.cuda.synchronize()
+    assert torch.equal(again, c.out)
+
+
+@pytest.mark.parametrize("rows", [1, 3])
+def test_widest_batch(rows):
+    lens = [(37 * i) % 97 for i in range(256)]
+    c = Case(lens, [rows if i % 5 else 0 for i in range(256)], 8, 2, paged=True, seed=3)
+    for fp32 in (True, False):
+        c.run(fp32)
+        c.check(fp32)
+
+
+def test_queue_and_shares_use_a_workspace_in_turn():
+    many = Case([100] * 50, [60] * 50, 16, 16, seed=1)
+    few = Case([3000, 10], [4, 2], 8, 2, seed=2)
+    nb = max(sfi.sfi_cross_workspace_bytes(c.kv, c.total, max(c.rows)) for c in (many, few))
+    ws = torch.empty(nb, dtype=torch.uint8, device="cuda")
+    sfi.sfi_workspace_init(ws, nb)
+    for c in (many, few, many, many, few):
+        c.run(ws=ws)
+        c.check()
+
+
 def test_layers_and_inactive_sequences():
     c = Case([500, 320, 0], [90, 320, 4], 8, 2, paged=True, layers=3)
     active = torch.tensor([1, 0, 1], dtype=torch.uint8, device="cuda")

@@ -128,6 +128,21 @@ def test_ties(n_top):
     Run(x, token, n_top).check()
 
 
+@pytest.mark.parametrize("n_top", [0, 5, 32])
+@pytest.mark.parametrize("unit", [1.0, 2.0 ** -130])
+def test_ties_around_zero(unit, n_top):
+    """Zeros of both signs and their neighbours (the smallest numbers of the type), in bf16 and fp32."""
+    for kind in (torch.bfloat16, torch.float32):
+        x, token = logits(6, 3000, kind, seed=n_top)
+        g = torch.Generator(device="cuda").manual_seed(1)
+        pick = torch.randint(0, 5, x.shape, generator=g, device="cuda")
+        values = torch.tensor([0.0, -0.0, unit, -unit, 2 * unit], device="cuda").to(kind)
+        x.copy_(values[pick])
+        for r in range(5):              # a given token of each value
+            token[r] = int((pick[r] == r).nonzero()[200])
+        Run(x, token, n_top).check()
+
+
 @pytest.mark.parametrize("kind", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("vocab", [255, 256, 257, 300, 511, 600, 1500, 33000])
 def test_equal_logits(vocab, kind):
