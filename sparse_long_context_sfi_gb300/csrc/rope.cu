@@ -11,9 +11,10 @@
 // dimensions (16 bytes) a lane, 4 heads on their way at once. A CTA has the sines and cosines of its 8
 // rows in shared memory, worked out once for all heads, and each half-warp keeps its row's share in
 // registers over the heads it goes through, multiplied by the norm's weights.
-// Four prompts of 8192 tokens, 32 and 8 heads: 133 us, 6.05 TB/s (copy rate 6.75), with norms 142, with
-// neighbouring pairs 133, with 40 of 128 dimensions (partners read one by one) 209; 170 us with 16 rows a
-// CTA, unpacked arithmetic and a list of (layer, head) per step; 135 with 80 instead of 64 registers.
+// Four prompts of 8192 tokens, 32 and 8 heads: 133 us, 6.05 TB/s (copy rate 6.75), with norms 141, with
+// neighbouring pairs 132, with 40 of 128 dimensions 135 (209 with the partners read again from the
+// cache), with 66 145; 170 us with 16 rows a CTA, unpacked arithmetic and a list of (layer, head) per
+// step; 135 with 80 instead of 64 registers.
 #include "chunk.cuh"
 #include "sfi_device.cuh"
 
@@ -27,9 +28,9 @@ constexpr uint32_t kEvery = 0xffffffffu;
 
 // How a lane gets the partners of its 8 dimensions.
 enum {
-    kPairs,     // neighbours: its own (rot_dim a multiple of 8: a lane turns all of its dimensions or none)
+    kPairs,     // neighbours: its own
     kLanes,     // half of rot_dim apart, a multiple of 8: all in one other lane
-    kAnywhere   // any other rot_dim, either layout: read again, one by one
+    kAnywhere   // half of any other rot_dim apart: through shared memory
 };
 
 __device__ __forceinline__ uint64_t pack2(float a, float b)
@@ -85,6 +86,7 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const RopeParams 
     __shared__ long long place[kRopeRows];
     __shared__ int at[kRopeRows];
     __shared__ bool live[kRopeRows];
+    __shared__ uint4 held[MODE == kAnywhere ? kRopeThreads * kRopeLoads : 1];   // the heads on their way
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int n_here = 1 << lg_rows, r0 = blockIdx.x << lg_rows, layer = blockIdx.z;
     const int hkv = p.c.pg.n_kv_heads, hq = p.q ? p.n_q_heads : 0, hk = p.k ? hkv : 0;
@@ -145,9 +147,8 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const RopeParams 
     __syncthreads();
 
     const bool on = live[row];
-    // in the layouts that a lane turns as a whole, whether it does
-    const bool turns = MODE != kAnywhere && 8 * l < p.rot;
-    const bool pairs = MODE == kPairs || (MODE == kAnywhere && p.interleaved);
+    const bool turns = 8 * l < p.rot;       // some of its dimensions (kLanes: all)
+    constexpr bool pairs = MODE == kPairs;
     auto partner = [&](int d) { return pairs ? d ^ 1 : d < half ? d + half : d - half; };
     auto factors = [&](const void *weight) {
         Turn t;
@@ -180,6 +181,13 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const RopeParams 
                 load(from, begin, end, on);
             loaded = false;
             if (turn) {
+                if constexpr (MODE == kAnywhere) {
+                    __syncwarp();               // the last heads have been read
+#pragma unroll
+                    for (int i = 0; i < kRopeLoads; ++i)
+                        held[(hw * kRopeLoads + i) * 16 + l] = x[i];
+                    __syncwarp();
+                }
 #pragma unroll
                 for (int i = 0; i < kRopeLoads; ++i) {
                     const uint64_t a[4] = {widen(x[i].x), widen(x[i].y), widen(x[i].z), widen(x[i].w)};
@@ -197,22 +205,23 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const RopeParams 
                         }
                     } else {
                         // (0 where a dimension stays: no infinity reaches it)
-                        const int h = u + i * stride - begin;
-                        float f[8];
+                        const __nv_bfloat16 *from_row = reinterpret_cast<const __nv_bfloat16 *>(held + (hw * kRopeLoads + i) * 16);
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            const int d = 8 * l + j;
-                            f[j] = on && h < end - begin && d < p.rot
-                                       ? __bfloat162float(from[h * kHeadDim + partner(d) - 8 * l]) : 0.f;
+                        for (int j = 0; j < 4; ++j) {
+                            const int d = 8 * l + 2 * j;
+                            if (half % 2 == 0) {        // both on the same side, and aligned
+                                b[j] = d < p.rot ? widen(*reinterpret_cast<const uint32_t *>(from_row + partner(d))) : 0;
+                            } else {
+                                b[j] = d < p.rot ? pack2(__bfloat162float(from_row[partner(d)]),
+                                                         __bfloat162float(from_row[partner(d + 1)])) : 0;
+                            }
                         }
-#pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            b[j] = pack2(f[2 * j], f[2 * j + 1]);
                     }
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         y[j] = mul2(a[j], t.c[j]);
-                        if (MODE == kAnywhere || turns)
+                        // (rot_dim is even: neighbours turn, or stay, together)
+                        if (MODE == kAnywhere || (MODE == kLanes ? turns : 8 * l + 2 * j < p.rot))
                             y[j] = fma2(b[j], t.s[j], y[j]);
                     }
                     if constexpr (NORM) {
@@ -233,8 +242,6 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const RopeParams 
                     x[i] = make_uint4(narrow(y[0]), narrow(y[1]), narrow(y[2]), narrow(y[3]));
                 }
             }
-            if (MODE == kAnywhere)
-                __syncwarp();           // in place, partners have been read
 #pragma unroll
             for (int i = 0; i < kRopeLoads; ++i) {
                 const int h = u + i * stride - begin;
@@ -335,10 +342,9 @@ cudaError_t launch_rope(const RopeParams &p, int sms, cudaStream_t stream)
         }
     }
     const int need = append ? kNeedRoom : p.pos ? kNeedRows : kNeedLength;
-    const cudaError_t e = p.interleaved && p.rot % 8 == 0 ? launch_mode<kPairs>(p, grid, lg, need, fused, stream)
-                          : !p.interleaved && p.rot % 16 == 0
-                              ? launch_mode<kLanes>(p, grid, lg, need, fused, stream)
-                              : launch_mode<kAnywhere>(p, grid, lg, need, fused, stream);
+    const cudaError_t e = p.interleaved       ? launch_mode<kPairs>(p, grid, lg, need, fused, stream)
+                          : p.rot % 16 == 0 ? launch_mode<kLanes>(p, grid, lg, need, fused, stream)
+                                            : launch_mode<kAnywhere>(p, grid, lg, need, fused, stream);
     if (e == cudaSuccess && append && fused == 0)
         return launch_advance(p.c, stream);
     return e != cudaSuccess ? e : cudaGetLastError();
