@@ -390,11 +390,12 @@ void score_shape(const sfi_scoring *s, int sms, ScoreParams *p)
     const double of = s->logits_fp32 ? 512. : 1024., k = s->n_top;
     const double chunks = std::ceil(s->vocab / of), rows = s->n_rows > 0 ? s->n_rows : 1;
     double best = -1.;
+    const double room = s->rank && s->entropy ? 28. : 32.;
     p->splits = 1;
     p->warps = 8;
     for (int warps = 8; warps >= 1; warps /= 2) {
         for (int splits = 1; splits <= 64 && (splits == 1 || (rows <= kMaxSplitRows && splits * warps <= chunks)); ++splits) {
-            const double waves = std::ceil(rows * splits * warps / (32. * (sms > 0 ? sms : 1)));
+            const double waves = std::ceil(rows * splits / (std::floor(room / warps) * (sms > 0 ? sms : 1)));
             const double steps = std::ceil(chunks / (warps * splits));
             const double again = steps * k * (1. / 8. + k / 170.) / (warps * warps);
             const double cost = waves * (steps + again + (k > 0 ? 8. : 4.) + (splits > 1 ? 4. : 0.));

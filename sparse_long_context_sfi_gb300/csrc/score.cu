@@ -277,7 +277,7 @@ constexpr int kBuffer = 256;        // of the tokens that may be among the best
 // tokens do, and they lie in the lanes that reach it: few, of which the one chunk is read again
 // (from L2), or where another one reaches `least`, too, all of the lane's.
 template <typename T, bool TOP, bool RANK, bool ENT>
-__global__ void __launch_bounds__(32 * kScoreWarps, 4) score_kernel(const ScoreParams p)
+__global__ void __maxnreg__(RANK && ENT ? 72 : 64) score_kernel(const ScoreParams p)
 {
     __shared__ float lane_m1[TOP ? 32 * kScoreWarps : 1], lane_m2[TOP ? 32 * kScoreWarps : 1];
     __shared__ int lane_c1[TOP ? 32 * kScoreWarps : 1];
