@@ -233,7 +233,8 @@ __device__ __noinline__ Best merged(Best b, const volatile float *x, const volat
     for (int i = 0; i < n; i += 32) {
         const float cx = i + lane < n ? x[i + lane] : -CUDART_INF_F;
         const int cv = i + lane < n ? v[i + lane] : -1;
-        if (i == 0 && b.tv < 0 && !__any_sync(kAll, b.v >= 0))
+        // (a sort of the warp costs as much as about 12 insertions)
+        if (i == 0 && n > 12 && b.tv < 0 && !__any_sync(kAll, b.v >= 0))
             b.start(cx, cv, K, lane);
         else
             b.offer(cx, cv, K, lane);
@@ -433,6 +434,8 @@ __global__ void __maxnreg__(RANK && ENT ? 72 : 64) score_kernel(const ScoreParam
                 bool out = !mine;
 #pragma unroll
                 for (int i = 0; i < kScoreWarps; ++i) {
+                    if (i >= warps)
+                        break;
                     const bool hit = !out && h[i] == least;
                     h[i] = hit ? -CUDART_INF_F : h[i];
                     out = out || hit;
@@ -500,8 +503,10 @@ __global__ void __maxnreg__(RANK && ENT ? 72 : 64) score_kernel(const ScoreParam
 #pragma unroll
                 for (int j = 0; j < V; ++j) {
                     const int v = piece[u] * V - at.shift + j;
-                    const bool in = piece[u] >= 0 && x[j] >= least && v >= 0 && v < p.vocab;
-                    const int to = in ? atomicAdd(&n_cand, 1) : -1;
+                    const bool in = piece[u] >= 0 && x[j] >= least;
+                    if (!__any_sync(kAll, in))
+                        continue;
+                    const int to = in && v >= 0 && v < p.vocab ? atomicAdd(&n_cand, 1) : -1;
                     if (to >= 0 && to < kBuffer) {
                         cand_x[to] = x[j];
                         cand_v[to] = v;
