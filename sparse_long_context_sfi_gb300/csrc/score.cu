@@ -33,25 +33,16 @@ struct Sums {
     int front;
 };
 
-// a and b relative to the larger reference; a sum that is not a number stays one.
+// The sums relative to a reference that is not below theirs; one that is not a number stays so.
 template <bool ENT>
-__device__ __forceinline__ Sums join(const Sums &a, const Sums &b)
+__device__ __forceinline__ Sums moved(const Sums &v, float R)
 {
-    Sums o;
-    o.R = fmaxf(a.R, b.R);
-    o.front = a.front + b.front;
-    o.s = o.t = 0.f;
-    const Sums *in[2] = {&a, &b};
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const Sums &v = *in[i];
-        if (v.s != 0.f) {
-            const float d = o.R > -CUDART_INF_F ? 4.f * (v.R - o.R) : 0.f;
-            const float w = ex2(d);
-            o.s += v.s * w;
-            if (ENT && w != 0.f)
-                o.t += (v.t + v.s * d) * w;
-        }
+    Sums o = {R, 0.f, 0.f, v.front};
+    if (v.s != 0.f) {
+        const float d = R > -CUDART_INF_F ? 4.f * (v.R - R) : 0.f, w = ex2(d);
+        o.s = v.s * w;
+        if (ENT && w != 0.f)        // (d may be beyond what 32 bits hold)
+            o.t = (v.t + v.s * d) * w;
     }
     return o;
 }
@@ -390,17 +381,16 @@ __global__ void __maxnreg__(RANK && ENT ? 72 : 64) score_kernel(const ScoreParam
         a.front = part.counted() - (counted && xb == xg ? 1 : 0) -
                   (has && xg == -CUDART_INF_F && at.split == 0 && tid == 0 ? at.shift : 0);
     // the sums of the warp, of the CTA
-    auto warp_join = [&](Sums v) {
+    auto warp_join = [&](const Sums &v) {
+        Sums o = moved<ENT>(v, unorder(__reduce_max_sync(kAll, order(v.R))));
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            Sums b;
-            b.R = __shfl_xor_sync(kAll, v.R, o);
-            b.s = __shfl_xor_sync(kAll, v.s, o);
-            b.t = ENT ? __shfl_xor_sync(kAll, v.t, o) : 0.f;
-            b.front = RANK ? __shfl_xor_sync(kAll, v.front, o) : 0;
-            v = join<ENT>(v, b);
+        for (int d = 16; d > 0; d >>= 1) {
+            o.s += __shfl_xor_sync(kAll, o.s, d);
+            if (ENT)
+                o.t += __shfl_xor_sync(kAll, o.t, d);
         }
-        return v;
+        o.front = RANK ? __reduce_add_sync(kAll, v.front) : 0;
+        return o;
     };
     const Sums none = {-CUDART_INF_F, 0.f, 0.f, 0};
     a = warp_join(a);
@@ -570,7 +560,10 @@ __global__ void __maxnreg__(RANK && ENT ? 72 : 64) score_kernel(const ScoreParam
         a = none;
         for (int i = lane; i < p.splits; i += 32) {
             const float4 v = __ldcg(p.part + parts + i);
-            a = join<ENT>(a, Sums{v.x, v.y, v.z, __float_as_int(v.w)});
+            const Sums b = {v.x, v.y, v.z, __float_as_int(v.w)};
+            const float R = fmaxf(a.R, b.R);
+            const Sums x = moved<ENT>(a, R), y = moved<ENT>(b, R);
+            a = Sums{R, x.s + y.s, x.t + y.t, x.front + y.front};
         }
         a = warp_join(a);
         if (TOP) {
