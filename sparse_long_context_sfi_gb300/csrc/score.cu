@@ -114,8 +114,8 @@ struct Part<float> {
 template <>
 struct Part<__nv_bfloat16> {
     static constexpr int kV = 8;
-    __nv_bfloat162 n = __floats2bfloat162_rn(0.f, 0.f);
-    int chunks = 0, all = 0;
+    int n = 0;
+    uint32_t chunk = 0;
 
     static __device__ __forceinline__ __nv_bfloat162 pair(uint32_t u) { return *reinterpret_cast<const __nv_bfloat162 *>(&u); }
     static __device__ __forceinline__ float highest(const uint4 *w)
@@ -127,31 +127,24 @@ struct Part<__nv_bfloat16> {
         const float2 f = __bfloat1622float2(m);
         return fmaxf(f.x, f.y);
     }
+    // (a pair's comparison is all ones in a half where it holds: less it, a sum has the lower halves that
+    // hold in its lower half, and in its upper the upper less the lower ones)
     __device__ __forceinline__ void count(const uint4 &w, float least)
     {
         const uint32_t u[4] = {w.x, w.y, w.z, w.w};
         const __nv_bfloat162 l = __float2bfloat162_rn(least);       // (exact)
+        uint32_t c = 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            n = __hadd2(n, __hge2(pair(u[i]), l));
+            c -= __hge2_mask(pair(u[i]), l);
+        chunk += c;
     }
     __device__ __forceinline__ void settle()
     {
-        if (++chunks == 15)         // bf16 counts to 256: 16 in each half of a chunk
-            flush();
+        n = __dp2a_lo(static_cast<int>(chunk), 0x0102, n);
+        chunk = 0;
     }
-    __device__ __forceinline__ void flush()
-    {
-        const float2 v = __bfloat1622float2(n);
-        all += static_cast<int>(v.x) + static_cast<int>(v.y);
-        n = __floats2bfloat162_rn(0.f, 0.f);
-        chunks = 0;
-    }
-    __device__ __forceinline__ int counted()
-    {
-        flush();
-        return all;
-    }
+    __device__ __forceinline__ int counted() const { return n; }
     // Logits below 150 powers under the reference are lifted to there (rounded down): they add
     // nothing either way, and -inf no 0 * -inf. NaN stays.
     struct Low {
@@ -331,9 +324,16 @@ __global__ void __maxnreg__(RANK && ENT ? 72 : 64) score_kernel(const ScoreParam
             c1 = best ? c : c1;
         }
         if (RANK) {
+            if (c <= given_piece && given_piece < c + kStep) {
 #pragma unroll
-            for (int i = 0; i < kPieces; ++i)
-                part.count(w[i], c + 32 * i + lane <= given_piece ? xg : xa);
+                for (int i = 0; i < kPieces; ++i)
+                    part.count(w[i], c + 32 * i + lane <= given_piece ? xg : xa);
+            } else {
+                const float least = c <= given_piece ? xg : xa;
+#pragma unroll
+                for (int i = 0; i < kPieces; ++i)
+                    part.count(w[i], least);
+            }
             part.settle();
         }
         // (masked tokens alone so far: they add nothing to any reference, and it stays -inf)

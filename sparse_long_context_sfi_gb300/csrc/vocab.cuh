@@ -186,6 +186,9 @@ __device__ __forceinline__ void load_pieces(const T *row, int shift, int vocab, 
         const int at = (piece + 32 * i) * V - shift;           // first token of the piece
         if (at >= 0 && at + V <= vocab) {
             w[i] = __ldcs(reinterpret_cast<const uint4 *>(row + at));
+        } else if (at >= vocab || at + V <= 0) {
+            const uint32_t low = sizeof(T) == 4 ? 0xff800000u : 0xff80ff80u;
+            w[i] = make_uint4(low, low, low, low);
         } else {
             T t[V];
 #pragma unroll
