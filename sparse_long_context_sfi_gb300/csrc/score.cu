@@ -226,6 +226,40 @@ __device__ __noinline__ Best merged(Best b, const volatile float *x, const volat
     return b;
 }
 
+// The best K of up to 64 candidates: each one's place is the number of those before it (all
+// comparisons at once, where insertions wait for one another). out_x and out_v hold K.
+__device__ __noinline__ Best placed(const volatile float *x, const volatile int *v, int n, int K, int lane,
+                                    volatile float *out_x, volatile int *out_v)
+{
+    const bool two = n > 32;
+    const float x0 = lane < n ? x[lane] : -CUDART_INF_F, x1 = lane + 32 < n ? x[lane + 32] : -CUDART_INF_F;
+    const int v0 = lane < n ? v[lane] : -1, v1 = lane + 32 < n ? v[lane + 32] : -1;
+    int r0 = 0, r1 = 0;
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) {
+        const float ox = x[i];
+        const int ov = v[i];
+        r0 += better(ox, ov, x0, v0);
+        if (two)
+            r1 += better(ox, ov, x1, v1);
+    }
+    if (lane < n && r0 < K) {
+        out_x[r0] = x0;
+        out_v[r0] = v0;
+    }
+    if (lane + 32 < n && r1 < K) {
+        out_x[r1] = x1;
+        out_v[r1] = v1;
+    }
+    __syncwarp();
+    Best b;
+    b.x = lane < n && lane < K ? out_x[lane] : -CUDART_INF_F;
+    b.v = lane < n && lane < K ? out_v[lane] : -1;
+    b.tx = __shfl_sync(kAll, b.x, K - 1);
+    b.tv = __shfl_sync(kAll, b.v, K - 1);
+    return b;
+}
+
 // The lowest value of the type above x (not NaN).
 __device__ __forceinline__ float above(float x, float)
 {
@@ -257,20 +291,46 @@ struct Place {
 
 constexpr int kBuffer = 256;        // of the tokens that may be among the best
 
-// Every lane keeps the highest logit of its chunks, which chunk it is, and the highest of all
-// others. K lanes have a logit of `least`, the K-th highest lane's, or more, so all of the K best
-// tokens do, and they lie in the lanes that reach it: few, of which the one chunk is read again
-// (from L2), or where another one reaches `least`, too, all of the lane's.
+// A chunk's highest logit with the number of the chunk (of its warp's, from 0) in the low bits: all
+// that bf16 leaves free, 12 of fp32's own. In order as the logits are, but for those that differ in
+// these bits alone; what a key stands for lies between lo and hi. The last number says "this or a
+// later one". (That of an infinity may be no number: -inf
+// then; a row with +inf has no list.)
+template <typename T>
+struct Key {
+    static constexpr uint32_t kNumber = sizeof(T) == 2 ? 0xffffu : 0xfffu;
+
+    static __device__ __forceinline__ float of(float x, uint32_t number)
+    {
+        return __uint_as_float((__float_as_uint(x) & ~kNumber) | number);
+    }
+    static __device__ __forceinline__ uint32_t number(float k) { return __float_as_uint(k) & kNumber; }
+    static __device__ __forceinline__ float least(float k) { return __uint_as_float(__float_as_uint(k) & ~kNumber); }
+    static __device__ __forceinline__ float most(float k)
+    {
+        return sizeof(T) == 2 ? least(k) : __uint_as_float(__float_as_uint(k) | kNumber);
+    }
+    static __device__ __forceinline__ float lo(float k) { return signbit(k) ? most(k) : least(k); }
+    static __device__ __forceinline__ float hi(float k) { return signbit(k) ? least(k) : most(k); }
+};
+
+// Every lane keeps its three highest chunks' keys. K lanes have a logit of `least`, the K-th highest
+// lane's, or more, so all of the K best tokens do, and they lie in the lanes that reach it: few, of
+// which the one or two chunks that do are read again, or where the third one does, too, all.
 template <typename T, bool TOP, bool RANK, bool ENT>
 __global__ void __maxnreg__(RANK && ENT ? 72 : 64) score_kernel(const ScoreParams p)
 {
-    __shared__ float lane_m1[TOP ? 32 * kScoreWarps : 1], lane_m2[TOP ? 32 * kScoreWarps : 1];
-    __shared__ int lane_c1[TOP ? 32 * kScoreWarps : 1];
-    __shared__ uint8_t lanes[TOP ? 64 * kScoreWarps : 1];       // those that reach `least`: with one chunk, with all
+    // keys of every lane; lists of the best, the warps' own where the buffer is too small, in their place
+    extern __shared__ float sh_top[];
+    float *const lane_k = sh_top, *const sh_x = sh_top;
+    int *const sh_v = reinterpret_cast<int *>(sh_x + blockDim.x);
+    float *const cand_x = lane_k + 3 * blockDim.x;
+    int *const cand_v = reinterpret_cast<int *>(cand_x + kBuffer);
+    // lanes (and which of their chunks, times 256) that reach `least`, and those of which all is read
+    uint16_t *const ones = reinterpret_cast<uint16_t *>(cand_v + kBuffer);
+    uint8_t *const alls = reinterpret_cast<uint8_t *>(ones + 2 * blockDim.x);
     __shared__ int n_one, n_all, n_cand;
     __shared__ float sh_least;
-    __shared__ float cand_x[TOP ? kBuffer : 1], sh_x[TOP ? kMaxTop * kScoreWarps : 1];
-    __shared__ int cand_v[TOP ? kBuffer : 1], sh_v[TOP ? kMaxTop * kScoreWarps : 1];
     __shared__ Sums sh_sums[kScoreWarps];
     constexpr int V = Part<T>::kV, kPieces = 4;
     constexpr int kStep = 32 * kPieces;             // pieces per chunk
@@ -313,15 +373,16 @@ __global__ void __maxnreg__(RANK && ENT ? 72 : 64) score_kernel(const ScoreParam
     const float xb = counted && behind < p.vocab ? static_cast<float>(at.x[behind]) : -CUDART_INF_F;
     Part<T> part;
     Sums a = {-CUDART_INF_F, 0.f, 0.f, 0};
-    float m1 = -CUDART_INF_F, m2 = -CUDART_INF_F;
-    int c1 = first;
+    float k1 = -CUDART_INF_F, k2 = k1, k3 = k1;
+    uint32_t number = 0;
     for (int c = first; c < at.pieces; c += stride) {
         const float cm = Part<T>::highest(w);
         if (TOP) {
-            const bool best = cm > m1;
-            m2 = fmaxf(m2, best ? m1 : cm);
-            m1 = best ? cm : m1;
-            c1 = best ? c : c1;
+            const float k = fmaxf(Key<T>::of(cm, number), -CUDART_INF_F), less = fminf(k1, k);
+            k3 = fmaxf(k3, fminf(k2, less));
+            k2 = fmaxf(k2, less);
+            k1 = fmaxf(k1, k);
+            number = min(number + 1, Key<T>::kNumber);
         }
         if (RANK) {
             if (c <= given_piece && given_piece < c + kStep) {
@@ -399,9 +460,9 @@ __global__ void __maxnreg__(RANK && ENT ? 72 : 64) score_kernel(const ScoreParam
     Best best;
     best.clear();
     if (TOP) {
-        lane_m1[tid] = m1;
-        lane_m2[tid] = m2;
-        lane_c1[tid] = c1;
+        lane_k[tid] = k1;
+        lane_k[tid + blockDim.x] = k2;
+        lane_k[tid + 2 * blockDim.x] = k3;
     }
     __syncthreads();
     if (TOP) {
@@ -409,7 +470,7 @@ __global__ void __maxnreg__(RANK && ENT ? 72 : 64) score_kernel(const ScoreParam
             float h[kScoreWarps], hm = -CUDART_INF_F;
 #pragma unroll
             for (int i = 0; i < kScoreWarps; ++i) {
-                h[i] = i < warps ? lane_m1[32 * i + lane] : -CUDART_INF_F;
+                h[i] = i < warps ? lane_k[32 * i + lane] : -CUDART_INF_F;
                 hm = fmaxf(hm, h[i]);
             }
             float least = -CUDART_INF_F;
@@ -435,19 +496,25 @@ __global__ void __maxnreg__(RANK && ENT ? 72 : 64) score_kernel(const ScoreParam
             }
             // (fewer than K lanes have a token that is not masked: all such tokens, and the lowest masked
             // ones behind them)
-            least = fmaxf(least, -FLT_MAX);
+            least = least == -CUDART_INF_F ? -FLT_MAX : Key<T>::lo(least);
             int n1 = 0, n2 = 0;
             for (int i = 0; i < warps; ++i) {
                 const int l = 32 * i + lane;
-                const bool two = lane_m2[l] >= least, one = !two && lane_m1[l] >= least;
-                const uint32_t k1 = __ballot_sync(kAll, one), k2 = __ballot_sync(kAll, two);
-                const uint32_t before = (1u << lane) - 1u;
-                if (one)
-                    lanes[n1 + __popc(k1 & before)] = static_cast<uint8_t>(l);
-                if (two)
-                    lanes[32 * kScoreWarps + n2 + __popc(k2 & before)] = static_cast<uint8_t>(l);
-                n1 += __popc(k1);
-                n2 += __popc(k2);
+                const float q1 = lane_k[l], q2 = lane_k[l + blockDim.x], q3 = lane_k[l + 2 * blockDim.x];
+                const bool in1 = Key<T>::hi(q1) >= least, in2 = Key<T>::hi(q2) >= least;
+                const bool all = Key<T>::hi(q3) >= least || (in1 && Key<T>::number(q1) == Key<T>::kNumber) ||
+                                 (in2 && Key<T>::number(q2) == Key<T>::kNumber);
+                const uint32_t b1 = __ballot_sync(kAll, in1 && !all), b2 = __ballot_sync(kAll, in2 && !all);
+                const uint32_t b3 = __ballot_sync(kAll, all), before = (1u << lane) - 1u;
+                if (in1 && !all)
+                    ones[n1 + __popc(b1 & before)] = static_cast<uint16_t>(l);
+                n1 += __popc(b1);
+                if (in2 && !all)
+                    ones[n1 + __popc(b2 & before)] = static_cast<uint16_t>(l + 256);
+                n1 += __popc(b2);
+                if (all)
+                    alls[n2 + __popc(b3 & before)] = static_cast<uint8_t>(l);
+                n2 += __popc(b3);
             }
             if (lane == 0) {
                 n_one = n1;
@@ -465,49 +532,62 @@ __global__ void __maxnreg__(RANK && ENT ? 72 : 64) score_kernel(const ScoreParam
         const bool alone = total * V <= kBuffer;
         const int step = alone ? 32 : blockDim.x;
         constexpr int kU = 2;           // pieces of a thread on their way at once
+        int found = 0;
         for (int i0 = warp * 32; i0 < total && (!alone || warp == 0); i0 += kU * step) {
             uint4 word[kU];
             int piece[kU];
 #pragma unroll
             for (int u = 0; u < kU; ++u) {
                 const int i = i0 + u * step + lane;
-                piece[u] = -1;
+                piece[u] = at.pieces;       // (nothing)
                 if (i < mid) {
-                    const int l = lanes[i / kPieces];
-                    piece[u] = lane_c1[l] + 32 * (i % kPieces) + (l & 31);
+                    const int l = ones[i / kPieces], which = l >> 8;
+                    const int r = Key<T>::number(lane_k[(l & 255) + which * blockDim.x]);
+                    piece[u] = begun + (l >> 5 & 7) * kStep + r * stride + 32 * (i % kPieces) + (l & 31);
                 } else if (i < total) {
-                    const int k = i - mid, r = k / n_all, l = lanes[32 * kScoreWarps + k - r * n_all];
+                    const int k = i - mid, r = k / n_all, l = alls[k - r * n_all];
                     piece[u] = begun + (l >> 5) * kStep + (r / kPieces) * stride + 32 * (r % kPieces) + (l & 31);
                 }
-                if (piece[u] >= at.pieces)
-                    piece[u] = -1;
-                if (piece[u] >= 0)
-                    load_pieces<T, 1>(at.x, at.shift, p.vocab, piece[u], word + u);
+                load_pieces<T, 1>(at.x, at.shift, p.vocab, min(piece[u], at.pieces), word + u);
             }
 #pragma unroll
             for (int u = 0; u < kU; ++u) {
-                if (!__any_sync(kAll, piece[u] >= 0))
-                    continue;
                 float x[V];
                 Chunk<T>::unpack(word[u], x);
+                uint32_t hits = 0;
 #pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    const int v = piece[u] * V - at.shift + j;
-                    const bool in = piece[u] >= 0 && x[j] >= least;
-                    if (!__any_sync(kAll, in))
-                        continue;
-                    const int to = in && v >= 0 && v < p.vocab ? atomicAdd(&n_cand, 1) : -1;
+                for (int j = 0; j < V; ++j)     // (what lies beyond the row's ends is -inf)
+                    hits |= x[j] >= least ? 1u << j : 0u;
+                uint32_t some;
+                while ((some = __ballot_sync(kAll, hits != 0)) != 0) {
+                    int base = found;
+                    if (!alone) {
+                        if (lane == 0)
+                            base = atomicAdd(&n_cand, __popc(some));
+                        base = __shfl_sync(kAll, base, 0);
+                    }
+                    found += __popc(some);
+                    const int j = __ffs(hits) - 1, v = piece[u] * V - at.shift + j;
+                    float xj = -CUDART_INF_F;
+#pragma unroll
+                    for (int i = 0; i < V; ++i)
+                        xj = i == j ? x[i] : xj;
+                    const int to = hits ? base + __popc(some & ((1u << lane) - 1u)) : -1;
+                    hits &= hits - 1;
                     if (to >= 0 && to < kBuffer) {
-                        cand_x[to] = x[j];
+                        cand_x[to] = xj;
                         cand_v[to] = v;
                     }
                     // (many equal logits, or many high ones in few lanes)
                     if (__any_sync(kAll, to >= kBuffer))
-                        best.offer(x[j], to >= kBuffer ? v : -1, K, lane);
+                        best.offer(xj, to >= kBuffer ? v : -1, K, lane);
                 }
             }
         }
-        if (!alone) {
+        if (alone) {
+            if (tid == 0)
+                n_cand = found;
+        } else {
             __syncthreads();
             if (n_cand > kBuffer) {
                 if (lane < K) {
@@ -522,10 +602,15 @@ __global__ void __maxnreg__(RANK && ENT ? 72 : 64) score_kernel(const ScoreParam
         return;
     __syncwarp();
     if (TOP) {
-        best.clear();           // (its own list is among the others)
-        if (n_cand > kBuffer)
-            best = merged(best, sh_x, sh_v, K * warps, K, lane);
-        best = merged(best, cand_x, cand_v, min(n_cand, kBuffer), K, lane);
+        const int n = n_cand;
+        if (n <= 64) {
+            best = placed(cand_x, cand_v, n, K, lane, sh_x, sh_v);
+        } else {
+            best.clear();       // (its own list is among the others)
+            if (n > kBuffer)
+                best = merged(best, sh_x, sh_v, K * warps, K, lane);
+            best = merged(best, cand_x, cand_v, min(n, kBuffer), K, lane);
+        }
         if (sh_least == -FLT_MAX) {
             const int piece = at.split * warps * kStep;
             for (int v0 = max(piece * V - at.shift, 0); v0 < p.vocab && best.tv < 0; v0 += 32) {
@@ -597,11 +682,12 @@ template <typename T, bool TOP>
 cudaError_t launch_top(const ScoreParams &p, cudaStream_t stream)
 {
     const dim3 grid(p.n_rows * p.splits), block(32 * p.warps);
+    const size_t sh = TOP ? 32 * p.warps * (3 * sizeof(float) + 2 * sizeof(uint16_t) + 1) + 2 * kBuffer * sizeof(float) : 0;
     if (p.rank)
-        return p.entropy ? launch_pdl(score_kernel<T, TOP, true, true>, grid, block, 0, stream, p)
-                         : launch_pdl(score_kernel<T, TOP, true, false>, grid, block, 0, stream, p);
-    return p.entropy ? launch_pdl(score_kernel<T, TOP, false, true>, grid, block, 0, stream, p)
-                     : launch_pdl(score_kernel<T, TOP, false, false>, grid, block, 0, stream, p);
+        return p.entropy ? launch_pdl(score_kernel<T, TOP, true, true>, grid, block, sh, stream, p)
+                         : launch_pdl(score_kernel<T, TOP, true, false>, grid, block, sh, stream, p);
+    return p.entropy ? launch_pdl(score_kernel<T, TOP, false, true>, grid, block, sh, stream, p)
+                     : launch_pdl(score_kernel<T, TOP, false, false>, grid, block, sh, stream, p);
 }
 
 template <typename T>
