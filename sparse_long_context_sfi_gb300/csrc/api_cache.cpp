@@ -379,12 +379,14 @@ sfi_status check_scoring(const sfi_scoring *s)
     return SFI_OK;
 }
 
-// CTAs of a row and warps of a CTA: the least sum over the waves of CTAs (32 warps to an SM) of a
-// warp's chunks (of 2 KB) and what a row's start and end cost in such steps: more with a list, whose
-// tokens are the more often in lanes that have to be read again the fewer lanes there are, and more
-// where CTAs are joined. Measured, us: 8192 rows of 32000 bf16 with rank and entropy, 8, 4, 2, 1 warps:
-// no list 118, 105, 103, 105; 3 tokens 172, 131, 124, 136; 20 tokens 187, 162, 183, 303; 8192 rows of 1000,
-// 3 tokens: 103, 55, 43, 29. 256 rows of 128001 fp32 with 20 tokens, 8 warps, 2, 4, 7 CTAs a row: 39, 44, 55.
+// CTAs of a row and warps of a CTA: the least sum over the waves of CTAs (32 warps to an SM, 28 of the
+// form with rank and entropy) of a warp's chunks (of 2 KB) and what a row's end costs in such steps: more
+// with a list, for each token of it, for lanes of which three chunks hold one of them, so that all of
+// theirs are read again (of k tokens in n lanes about k^3 / 6 n^2), and where CTAs are joined. Measured,
+// us: 8192 rows of 32000 bf16 with rank and entropy, 1, 2, 4, 8 warps: no list 90, 91, 92, 114; 3 tokens
+// 100, 108, 117, 176; 20 tokens 150, 126, 138, 224; 8192 rows of 1000, 3 tokens: 23, 35, 49, 113; 2048 of
+// 128001, 8 tokens: 151, 99, 101, 125. 256 rows of 128001 fp32 with 20 tokens, 4 warps, 2 and 4 CTAs a
+// row: 47, 39; 8 warps, 1, 2, 4: 45, 60, 59.
 void score_shape(const sfi_scoring *s, int sms, ScoreParams *p)
 {
     const double of = s->logits_fp32 ? 512. : 1024., k = s->n_top;
@@ -397,8 +399,8 @@ void score_shape(const sfi_scoring *s, int sms, ScoreParams *p)
         for (int splits = 1; splits <= 64 && (splits == 1 || (rows <= kMaxSplitRows && splits * warps <= chunks)); ++splits) {
             const double waves = std::ceil(rows * splits / (std::floor(room / warps) * (sms > 0 ? sms : 1)));
             const double steps = std::ceil(chunks / (warps * splits));
-            const double again = steps * k * (1. / 8. + k / 170.) / (warps * warps);
-            const double cost = waves * (steps + again + (k > 0 ? 8. : 4.) + (splits > 1 ? 4. : 0.));
+            const double again = steps * k * k * k / (17000. * warps * warps);
+            const double cost = waves * (steps + again + (k > 0 ? 2.5 + k / 7. : 1.) + (splits > 1 ? 4. : 0.));
             if (best < 0. || cost < best) {
                 best = cost;
                 p->splits = splits;
