@@ -314,3 +314,60 @@ def test_repeatable_captured_and_on_another_stream():
     torch.cuda.synchronize()
     for a, b in zip(first.outs(), again.outs()):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("kind", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("n_top", [3, 20])
+@pytest.mark.parametrize("masked", [False, True])
+def test_chunks_of_one_lane(masked, n_top, kind):
+    """One warp a row (so many rows), and one to four chunks of a lane hold the best, others masked."""
+    rows, piece = 8500, 16 // (4 if kind == torch.float32 else 2)
+    chunk = 128 * piece
+    x, token = logits(rows, 4 * chunk + 5, kind, seed=4)
+    g = torch.Generator(device="cuda").manual_seed(5)
+    pick = lambda n: torch.randint(0, n, (rows,), generator=g, device="cuda")
+    r = torch.arange(rows, device="cuda")
+    for c in range(4):
+        some = pick(4) >= c if not masked else pick(2) > 0
+        at = (r * 5 + c) % 4 * chunk + pick(4) * 32 * piece + r % 32 * piece + pick(piece)
+        x[r[some], at[some]] += 12.0
+        if masked:
+            x[~some, c * chunk:(c + 1) * chunk] = -INF
+    Run(x, token, n_top).check()
+
+
+@pytest.mark.parametrize("rows", [2, 8500])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_logits_that_differ_in_the_last_bits(sign, rows):
+    """The best differ by less than the keys of chunks tell apart, of either sign and around zero."""
+    x, token = logits(rows, 2053, torch.float32)
+    g = torch.Generator(device="cuda").manual_seed(6)
+    step = torch.randint(0, 5000, x.shape, generator=g, device="cuda").float()
+    near = sign * (1.0 + step * 2.0 ** -23)
+    best = torch.rand(x.shape, generator=g, device="cuda") < 0.02
+    x.copy_(torch.where(best, near, x.clamp(max=0.0) - 1.5))
+    for n_top in (1, 6, 32):
+        Run(x, token, n_top).check()
+    x.copy_(torch.where(best, sign * (step - 2500).clamp(min=0.0) * 2.0 ** -149, x))
+    Run(x, token, 20).check()
+
+
+def test_longest_row():
+    """2^30 logits: more chunks to a warp than a key counts, the best among those behind."""
+    n = 1 << 30
+    x = torch.full((1, n), -20.0, device="cuda")
+    last = [n - 1, n - 3, n - 1 - 4 * 128, n - 5 - 64 * 8 * 512, n - 70000, n - 70001, 5, 77777, 512 * 512 * 8 + 9, n // 2]
+    for i, v in enumerate(last):
+        x[0, v] = 10.0 - i
+    token = torch.tensor([77777], dtype=torch.int32, device="cuda")
+    run = Run(x, token, 12)
+    torch.cuda.synchronize()
+    want = last + sorted(set(range(20)) - set(last))[:2]
+    assert run.top[0].tolist() == want and int(run.rank[0]) == 7
+    # 2^30 e^-20 = 2.2 beside e^10 and less: every lane's sum has 2^14 like terms, an error of at most
+    # 2^-10 of what is 1e-4 of the whole
+    lse = math.log((n - len(last)) * math.exp(-20.0) + sum(math.exp(10.0 - i) for i in range(len(last))))
+    got = run.top_lp[0].double().cpu().numpy()
+    assert np.abs(got - ([10.0 - i - lse for i in range(len(last))] + [-20 - lse] * 2)).max() <= 1e-5
+    del x, run
+    torch.cuda.empty_cache()
