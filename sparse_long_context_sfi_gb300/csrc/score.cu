@@ -19,6 +19,7 @@
 #include "vocab.cuh"
 
 #include <cfloat>
+#include <climits>
 
 namespace sfi {
 namespace {
@@ -331,6 +332,7 @@ __global__ void __maxnreg__(RANK && ENT ? 72 : 64) score_kernel(const ScoreParam
     uint8_t *const alls = reinterpret_cast<uint8_t *>(ones + 2 * blockDim.x);
     __shared__ int n_one, n_all, n_cand;
     __shared__ float sh_least;
+    __shared__ int sh_kth;
     __shared__ Sums sh_sums[kScoreWarps];
     constexpr int V = Part<T>::kV, kPieces = 4;
     constexpr int kStep = 32 * kPieces;             // pieces per chunk
@@ -464,35 +466,55 @@ __global__ void __maxnreg__(RANK && ENT ? 72 : 64) score_kernel(const ScoreParam
         lane_k[tid + blockDim.x] = k2;
         lane_k[tid + 2 * blockDim.x] = k3;
     }
+    if (TOP && tid == 0)
+        sh_kth = INT_MAX;
     __syncthreads();
     if (TOP) {
-        if (warp == 0) {
-            float h[kScoreWarps], hm = -CUDART_INF_F;
-#pragma unroll
-            for (int i = 0; i < kScoreWarps; ++i) {
-                h[i] = i < warps ? lane_k[32 * i + lane] : -CUDART_INF_F;
-                hm = fmaxf(hm, h[i]);
+        // the K-th highest key: of many by counting, in every lane, the keys above its own, of a few by
+        // taking the highest out, one after XX
+        const bool many = K > 2 * warps;
+        if (many) {
+            int before = 0;
+            for (int i = 0; i < 8 * warps; ++i) {
+                const float4 q = reinterpret_cast<const float4 *>(lane_k)[i];
+                before += (q.x > k1) + (q.y > k1) + (q.z > k1) + (q.w > k1);
             }
+            const int low = __reduce_min_sync(kAll, before < K ? order(k1) : INT_MAX);
+            if (lane == 0 && low != INT_MAX)
+                atomicMin(&sh_kth, low);
+            __syncthreads();
+        }
+        if (warp == 0) {
             float least = -CUDART_INF_F;
-            int left = K;
-            while (left > 0) {          // the highest are taken out, one of each lane that holds it
-                least = unorder(__reduce_max_sync(kAll, order(hm)));
-                if (least == -CUDART_INF_F)
-                    break;
-                const bool mine = hm == least;
-                left -= __popc(__ballot_sync(kAll, mine));
-                float rest = -CUDART_INF_F;
-                bool out = !mine;
+            if (many) {
+                least = unorder(sh_kth);
+            } else {
+                float h[kScoreWarps], hm = -CUDART_INF_F;
 #pragma unroll
                 for (int i = 0; i < kScoreWarps; ++i) {
-                    if (i >= warps)
-                        break;
-                    const bool hit = !out && h[i] == least;
-                    h[i] = hit ? -CUDART_INF_F : h[i];
-                    out = out || hit;
-                    rest = fmaxf(rest, h[i]);
+                    h[i] = i < warps ? lane_k[32 * i + lane] : -CUDART_INF_F;
+                    hm = fmaxf(hm, h[i]);
                 }
-                hm = rest;
+                int left = K;
+                while (left > 0) {          // the highest are taken out, one of each lane that holds it
+                    least = unorder(__reduce_max_sync(kAll, order(hm)));
+                    if (least == -CUDART_INF_F)
+                        break;
+                    const bool mine = hm == least;
+                    left -= __popc(__ballot_sync(kAll, mine));
+                    float rest = -CUDART_INF_F;
+                    bool out = !mine;
+#pragma unroll
+                    for (int i = 0; i < kScoreWarps; ++i) {
+                        if (i >= warps)
+                            break;
+                        const bool hit = !out && h[i] == least;
+                        h[i] = hit ? -CUDART_INF_F : h[i];
+                        out = out || hit;
+                        rest = fmaxf(rest, h[i]);
+                    }
+                    hm = rest;
+                }
             }
             // (fewer than K lanes have a token that is not masked: all such tokens, and the lowest masked
             // ones behind them)
