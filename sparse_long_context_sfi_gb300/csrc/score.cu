@@ -471,7 +471,8 @@ __global__ void __maxnreg__(RANK && ENT ? 72 : 64) score_kernel(const ScoreParam
     __syncthreads();
     if (TOP) {
         // the K-th highest key: of many by counting, in every lane, the keys above its own, of a few by
-        // taking the highest out, one after XX
+        // taking the highest out, one after the other (6 us more of 126 for 8192 rows with 20
+        // tokens, 2 of 14 for one row with 32)
         const bool many = K > 2 * warps;
         if (many) {
             int before = 0;
