@@ -82,7 +82,7 @@ struct Turn {
 template <int MODE, bool NORM>
 __global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const RopeParams p, int lg_rows, int need, int fused)
 {
-    __shared__ float2 cs[kRopeRows][kHeadDim / 2];
+    __shared__ __align__(16) float2 cs[kRopeRows][kHeadDim / 2];
     __shared__ long long place[kRopeRows];
     __shared__ int at[kRopeRows];
     __shared__ bool live[kRopeRows];
@@ -150,19 +150,49 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const RopeParams 
     const bool turns = 8 * l < p.rot;       // some of its dimensions (kLanes: all)
     constexpr bool pairs = MODE == kPairs;
     auto partner = [&](int d) { return pairs ? d ^ 1 : d < half ? d + half : d - half; };
+    const int other_lane = MODE == kLanes && turns ? (8 * l < half ? l + half / 8 : l - half / 8) : l;
     auto factors = [&](const void *weight) {
         Turn t;
-        const __nv_bfloat16 *w = static_cast<const __nv_bfloat16 *>(weight);
         float c[8], s[8];
+        if constexpr (MODE == kAnywhere) {
+            const __nv_bfloat16 *w = static_cast<const __nv_bfloat16 *>(weight);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int d = 8 * l + j;
-            const bool turned = d < p.rot;
-            const int pair = pairs ? d >> 1 : d < half ? d : d - half;
-            const bool first = pairs ? (d & 1) == 0 : d < half;
-            const float2 v = turned ? cs[row][pair] : make_float2(1.f, 0.f);
-            c[j] = NORM && w ? v.x * __bfloat162float(w[d]) : v.x;
-            s[j] = (first ? -v.y : v.y) * (NORM && w && turned ? __bfloat162float(w[partner(d)]) : 1.f);
+            for (int j = 0; j < 8; ++j) {
+                const int d = 8 * l + j;
+                const bool turned = d < p.rot;
+                const float2 v = turned ? cs[row][d < half ? d : d - half] : make_float2(1.f, 0.f);
+                c[j] = NORM && w ? v.x * __bfloat162float(w[d]) : v.x;
+                s[j] = (d < half ? -v.y : v.y) * (NORM && w && turned ? __bfloat162float(w[partner(d)]) : 1.f);
+            }
+        } else {
+            // (16 bytes at a time; the lane's first pair is a multiple of 4, or of 8)
+            const uint4 *w = static_cast<const uint4 *>(weight);
+            const int pair = pairs ? 4 * l : 8 * l < half ? 8 * l : 8 * l - half;
+            const float4 *v = reinterpret_cast<const float4 *>(cs[row] + (turns ? pair : 0));
+            uint4 own = make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u), other = own;
+            if (NORM && w) {
+                own = w[l];
+                other = pairs ? own : w[other_lane];
+            }
+            const uint32_t wo[4] = {own.x, own.y, own.z, own.w}, wt[4] = {other.x, other.y, other.z, other.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                float4 f;               // cosine, sine of the two dimensions
+                if (pairs) {
+                    const float4 g = v[j / 2];
+                    f = j % 2 == 0 ? make_float4(g.x, -g.y, g.x, g.y) : make_float4(g.z, -g.w, g.z, g.w);
+                } else {
+                    const float4 g = v[j];
+                    f = 8 * l < half ? make_float4(g.x, -g.y, g.z, -g.w) : g;
+                }
+                if (!(pairs ? 8 * l + 2 * j < p.rot : turns))
+                    f = make_float4(1.f, 0.f, 1.f, 0.f);
+                const float2 a = unpack2(widen(wo[j])), b = unpack2(widen(wt[j]));
+                c[2 * j] = f.x * a.x;
+                c[2 * j + 1] = f.z * a.y;
+                s[2 * j] = f.y * (pairs ? b.y : b.x);
+                s[2 * j + 1] = f.w * (pairs ? b.x : b.y);
+            }
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -171,7 +201,6 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const RopeParams 
         }
         return t;
     };
-    const int other_lane = MODE == kLanes && turns ? (8 * l < half ? l + half / 8 : l - half / 8) : l;
     // The heads [begin, end) of the row, which lie at `from` and go to `to`, to_step elements apart; TURN:
     // turned by t (and normed), else copied. Both half-warps of a warp go through as many steps.
     auto heads = [&](int begin, int end, const __nv_bfloat16 *from, __nv_bfloat16 *to, long long to_step, bool turn,
@@ -190,6 +219,8 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const RopeParams 
                 }
 #pragma unroll
                 for (int i = 0; i < kRopeLoads; ++i) {
+                    if (MODE != kAnywhere && !__any_sync(kEvery, u + i * stride < end))
+                        break;
                     const uint64_t a[4] = {widen(x[i].x), widen(x[i].y), widen(x[i].z), widen(x[i].w)};
                     uint64_t b[4], y[4];
                     if constexpr (MODE == kLanes) {
