@@ -11,10 +11,11 @@
 // dimensions (16 bytes) a lane, 4 heads on their way at once. A CTA has the sines and cosines of its 8
 // rows in shared memory, worked out once for all heads, and each half-warp keeps its row's share in
 // registers over the heads it goes through, multiplied by the norm's weights.
-// Four prompts of 8192 tokens, 32 and 8 heads: 133 us, 6.05 TB/s (copy rate 6.75), with norms 141, with
-// neighbouring pairs 132, with 40 of 128 dimensions 135 (209 with the partners read again from the
+// Four prompts of 8192 tokens, 32 and 8 heads: 131 us, 6.15 TB/s (copy rate 6.75), with norms 138, with
+// neighbouring pairs 129, with 40 of 128 dimensions 135 (209 with the partners read again from the
 // cache), with 66 145; 170 us with 16 rows a CTA, unpacked arithmetic and a list of (layer, head) per
-// step; 135 with 80 instead of 64 registers.
+// step; 135 for 133 with 80 instead of 64 registers; 178 (148 with 80 registers) where a head's place
+// is loaded again as soon as the head is stored.
 #include "chunk.cuh"
 #include "sfi_device.cuh"
 

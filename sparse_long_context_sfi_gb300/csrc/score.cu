@@ -6,16 +6,18 @@
 // (t also by s (R - R')). The rank counts the tokens in front of the given one on the way.
 //
 // The bytes of the logits bound it, and right behind them issue slots: at the copy rate there are 11
-// for a token of bf16. A pass over one takes 5 (unpacked, a packed multiply-add, an exponential, packed
-// sums, and half an instruction of a packed maximum), the rank 1 (pairs compared and counted as
-// pairs), entropy 1, the list of the best nothing: it is made behind the pass, of the few lanes whose
-// highest logits say that they hold one of them. What is left is a row's end, a chain of barriers and
-// reductions: 8192 rows of 32000 bf16 take 84 us (6.2 TB/s) with the log probability alone, 124 with rank,
-// entropy and 3 alternatives (260 with a sorted list kept on the way, a comparison of two conditions
-// per token for the rank and 8 warps per row); 2048 rows of 128001 85 us (6.2 TB/s); 256 rows of 128001 fp32 29
-// (4.6 TB/s), 39 with everything and 20 alternatives. Tried: CTAs that go on to further rows, with
-// the next row's first loads under way while one is finished (198 instead of 151 then: spills, and
-// warps that wait for the one that finishes).
+// for a token of bf16. A pass over one takes 5.4 (unpacked, a packed multiply-add, an exponential, packed
+// sums, half an instruction of a packed maximum, and its share of a chunk's loads and reference), the
+// rank 1 (pairs compared, two comparisons added at once as integers), entropy 1.5, the list of the best
+// a third: it is made behind the pass, of the few lanes whose highest chunks say that they hold one of
+// them. What is left is a row's end, a chain of barriers, reductions and loads that come from HBM again:
+// 8192 rows of 32000 bf16 take 84 us (6.2 TB/s) with the log probability alone, 90 with rank and entropy,
+// 100 with 3 alternatives too, 120 with 20 (260 with a sorted list kept on the way, a comparison of two
+// conditions per token for the rank and 8 warps per row); 2048 rows of 128001 85 us (6.2 TB/s); 256 rows of
+// 128001 fp32 29 (4.5 TB/s) with rank and entropy, 37 with 20 alternatives. Tried: CTAs that go on to
+// further rows, with the next row's first loads under way while one is finished (198 instead of 151
+// then: spills, and warps that wait for the one that finishes); mma.sync with ones to add up the rank's
+// comparisons (124 for 120) and with the unit matrix to unpack bf16 (134).
 #include "vocab.cuh"
 
 #include <cfloat>
@@ -322,7 +324,7 @@ template <typename T, bool TOP, bool RANK, bool ENT>
 __global__ void __maxnreg__(RANK && ENT ? 72 : 64) score_kernel(const ScoreParams p)
 {
     // keys of every lane; lists of the best, the warps' own where the buffer is too small, in their place
-    extern __shared__ float sh_top[];
+    extern __shared__ __align__(16) float sh_top[];
     float *const lane_k = sh_top, *const sh_x = sh_top;
     int *const sh_v = reinterpret_cast<int *>(sh_x + blockDim.x);
     float *const cand_x = lane_k + 3 * blockDim.x;

@@ -632,7 +632,9 @@ class BeamSearch:
 
 class EncoderStates:
     """Keys and values of encoder inputs on the device, one sequence each, and the attention of a
-    decoder's rows to them. Rows of one input lie together: of a prompt's chunk, of its beams."""
+    decoder's rows to them. Rows of one input lie together: of a prompt's chunk, of its beams. The
+    calls of one object share its workspace: they follow each other, also in captured graphs, and what
+    runs at once is called on objects of its own."""
 
     def __init__(self, n_layers, batch, n_q_heads, n_kv_heads, capacity, device="cuda"):
         self.n_layers, self.batch, self.n_q_heads, self.n_kv_heads = n_layers, batch, n_q_heads, n_kv_heads
@@ -716,7 +718,8 @@ class EncoderStates:
 
 
 class TokenScores:
-    """Log probabilities of tokens under rows of logits."""
+    """Log probabilities of tokens under rows of logits. The calls of one object share its workspace: they
+    follow each other, also in captured graphs; what runs at once has an object of its own."""
 
     def __init__(self, device="cuda"):
         self.device = _at(device)
