@@ -683,11 +683,21 @@ __global__ void __maxnreg__(RANK && ENT ? 72 : 64) score_kernel(const ScoreParam
     }
     const float ls = logf(a.s);
     const bool sound = isfinite(a.R) && isfinite(ls);
-    // lse less ln s, in double: in fp32 it would round at the size of the logits. From kLarge on
-    // the reference is half the largest logit.
-    const double ref = fabsf(a.R) < kLarge * kLog2e4 ? a.R / static_cast<double>(kLog2e4) : 2. * a.R;
-    // (a probability is at most 1 and entropy at least 0, whatever the roundings say)
-    auto log_p = [&](float x) { return sound ? fminf(static_cast<float>(x - ref - ls), 0.f) : CUDART_NAN_F; };
+    // lse less ln s is 4 R / log2 e, as ref + rest: in fp32 alone it would round at the size of the
+    // logits (and the few units for 64 bits would hold up short rows: 8192 of 1000 tokens 22.5 us then).
+    // From kLarge on the reference is half the largest logit.
+    constexpr double kPerR = 1. / kLog2e4;
+    constexpr float kPer = static_cast<float>(kPerR), kPerRest = static_cast<float>(kPerR - kPer);
+    const bool small = fabsf(a.R) < kLarge * kLog2e4;
+    const float ref = small ? __fmul_rn(a.R, kPer) : 2.f * a.R;
+    const float rest = small ? fmaf(a.R, kPer, -ref) + a.R * kPerRest : 0.f;
+    // (x - ref exactly, as d + lost; a probability is at most 1 and entropy at least 0, whatever the
+    // roundings say)
+    auto log_p = [&](float x) {
+        const float d = x - ref, b = d - x, lost = (x - (d - b)) - (ref + b);
+        const float l = (d - ls) + (fabsf(d) < CUDART_INF_F ? lost - rest : 0.f);
+        return sound ? fminf(l, 0.f) : CUDART_NAN_F;
+    };
     if (lane == 0) {
         if (p.logprob)
             p.logprob[at.row] = given < 0 ? 0.f : has ? log_p(xg) : CUDART_NAN_F;
