@@ -385,8 +385,8 @@ sfi_status check_scoring(const sfi_scoring *s)
 // theirs are read again (of k tokens in n lanes about k^3 / 6 n^2), and where CTAs are joined. Measured,
 // us: 8192 rows of 32000 bf16 with rank and entropy, 1, 2, 4, 8 warps: no list 90, 91, 92, 114; 3 tokens
 // 100, 108, 117, 176; 20 tokens 150, 126, 138, 224; 8192 rows of 1000, 3 tokens: 23, 35, 49, 113; 2048 of
-// 128001, 8 tokens: 151, 99, 101, 125. 256 rows of 128001 fp32 with 20 tokens, 4 warps, 2 and 4 CTAs a
-// row: 47, 39; 8 warps, 1, 2, 4: 45, 60, 59.
+// 128001, 8 tokens: 151, 99, 101, 125. 256 rows of 128001 fp32 with 20 tokens, 4 warps, 2, 3 and 4 CTAs a
+// row: 41, 36, 35; 8 warps, 1, 2, 4: 39, 53, 55; 100 rows, 2 warps and 21 CTAs 29, 8 warps and 3 25.
 void score_shape(const sfi_scoring *s, int sms, ScoreParams *p)
 {
     const double of = s->logits_fp32 ? 512. : 1024., k = s->n_top;
@@ -400,7 +400,7 @@ void score_shape(const sfi_scoring *s, int sms, ScoreParams *p)
             const double waves = std::ceil(rows * splits / (std::floor(room / warps) * (sms > 0 ? sms : 1)));
             const double steps = std::ceil(chunks / (warps * splits));
             const double again = steps * k * k * k / (17000. * warps * warps);
-            const double cost = waves * (steps + again + (k > 0 ? 2.5 + k / 7. : 1.) + (splits > 1 ? 4. : 0.));
+            const double cost = waves * (steps + again + (k > 0 ? 2.5 + k / 7. : 1.) + (splits > 1 ? 4. + k * splits / 40. : 0.));
             if (best < 0. || cost < best) {
                 best = cost;
                 p->splits = splits;
