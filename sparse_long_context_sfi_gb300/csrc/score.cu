@@ -12,9 +12,9 @@
 // a third: it is made behind the pass, of the few lanes whose highest chunks say that they hold one of
 // them. What is left is a row's end, a chain of barriers, reductions and loads that come from HBM again:
 // 8192 rows of 32000 bf16 take 84 us (6.2 TB/s) with the log probability alone, 90 with rank and entropy,
-// 100 with 3 alternatives too, 120 with 20 (260 with a sorted list kept on the way, a comparison of two
+// 99 with 3 alternatives too, 117 with 20 (260 with a sorted list kept on the way, a comparison of two
 // conditions per token for the rank and 8 warps per row); 2048 rows of 128001 85 us (6.2 TB/s); 256 rows of
-// 128001 fp32 29 (4.5 TB/s) with rank and entropy, 37 with 20 alternatives. Tried: CTAs that go on to
+// 128001 fp32 29 (4.5 TB/s) with rank and entropy, 36 with 20 alternatives. Tried: CTAs that go on to
 // further rows, with the next row's first loads under way while one is finished (198 instead of 151
 // then: spills, and warps that wait for the one that finishes); mma.sync with ones to add up the rank's
 // comparisons (124 for 120) and with the unit matrix to unpack bf16 (134).
@@ -321,7 +321,7 @@ struct Key {
 // lane's, or more, so all of the K best tokens do, and they lie in the lanes that reach it: few, of
 // which the one or two chunks that do are read again, or where the third one does, too, all.
 //
-// Registers, 64, 72, 80 (with rank and entropy; us): 8192 rows of 32000 bf16 with 3 tokens 109, 99, 111,
+// At most 64, 72, 80 registers (with rank and entropy; us; of 80 fp32 lists take 72 and keep 28 warps): 8192 rows of 32000 bf16 with 3 tokens 109, 99, 111,
 // without a list 95, 90, 100; of fp32 185, 178, 167 and 169, 163, 181.
 template <typename T, bool TOP, bool RANK, bool ENT>
 __global__ void __maxnreg__(RANK && ENT ? (TOP && sizeof(T) == 4 ? 80 : 72) : 64) score_kernel(const ScoreParams p)
