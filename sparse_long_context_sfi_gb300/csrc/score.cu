@@ -16,7 +16,7 @@
 // conditions per token for the rank and 8 warps per row); 2048 rows of 128001 85 us (6.2 TB/s); 256 rows of
 // 128001 fp32 29 (4.5 TB/s) with rank and entropy, 36 with 20 alternatives. Tried: CTAs that go on to
 // further rows, with the next row's first loads under way while one is finished (198 instead of 151
-// then: spills, and warps that wait for the one that finishes); mma.sync with ones to add up the rank's
+// then: spills, and warps that wait for the one that finishes; of one warp 111 for 99); mma.sync with ones to add up the rank's
 // comparisons (124 for 120) and with the unit matrix to unpack bf16 (134).
 #include "vocab.cuh"
 
@@ -321,8 +321,8 @@ struct Key {
 // lane's, or more, so all of the K best tokens do, and they lie in the lanes that reach it: few, of
 // which the one or two chunks that do are read again, or where the third one does, too, all.
 //
-// At most 64, 72, 80 registers (with rank and entropy; us; of 80 fp32 lists take 72 and keep 28 warps): 8192 rows of 32000 bf16 with 3 tokens 109, 99, 111,
-// without a list 95, 90, 100; of fp32 185, 178, 167 and 169, 163, 181.
+// At most 64, 72, 80 registers with rank and entropy, us: 8192 rows of 32000 bf16 with 3 tokens 109, 99,
+// 111, without a list 95, 90, 100; of fp32 185, 178, 167 (80 allowed, 72 taken) and 169, 163, 181.
 template <typename T, bool TOP, bool RANK, bool ENT>
 __global__ void __maxnreg__(RANK && ENT ? (TOP && sizeof(T) == 4 ? 80 : 72) : 64) score_kernel(const ScoreParams p)
 {
