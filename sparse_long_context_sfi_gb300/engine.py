@@ -222,37 +222,39 @@ class SfiState:
         driver); otherwise every row is appended first and the fast step is
         sfi_sparse_decode_attn. active: device uint8 [B], e.g. from reserve: the others are left as
         they are (their rows of out, too). rope: q and k_new are turned to their positions first
-        (pos: device int32 [B], None: the lengths); rows may then be a fused projection's."""
+        (pos: device int32 [B], None: the lengths); their rows, and v_new's, which are packed then,
+        may be a fused projection's."""
         if rope is not None:
-            q, k_new = self._turned(rope, q, k_new, pos, active, stream)
+            q, k_new, v_new = self._turned(rope, q, k_new, v_new, out, out_fp32, pos, active, stream)
         elif pos is not None:
             raise ValueError("pos goes with rope")
         return self._step(q, k_new, v_new, slow_b, None, active, out, out_fp32, stream, fused)
 
-    def _turned(self, rope, q, k_new, pos, active, stream):
-        """q and k_new of single tokens, turned."""
+    def _turned(self, rope, q, k_new, v_new, out, out_fp32, pos, active, stream):
+        """q and k_new of single tokens, turned, and v_new, all packed: the calls that append on their own
+        take their addresses alone."""
         _here(self.device)
         c, n = self.cfg, self.cfg.batch
         self._masked(active)
-        io = self._rope_rows(rope, q, k_new, None, pos, n)
+        io = self._chunk(n, q, k_new, v_new, out, out_fp32, rope, pos)
         with torch.cuda.stream(_torch_stream(stream)):
+            v_new = v_new.contiguous()
             q_out, k_out = (torch.empty((c.n_layers, n, h, c.head_dim), dtype=torch.bfloat16, device=self.device)
                             for h in (c.n_q_heads, c.n_kv_heads))
         io.q_out, io.k_out = q_out.data_ptr(), k_out.data_ptr()
         sfi_rope_apply(self._whole(), rope.desc, io, None, n, 1, active=active, stream=stream)
-        return q_out, k_out
+        return q_out, k_out, v_new
 
     def _rope_rows(self, rope, q, k_new, v_new, pos, n):
-        """The rows that a rope call reads (v_new None: left out)."""
+        """The rows that a rope call reads."""
         c, dev = self.cfg, self.device
         if rope.device != dev:
             raise ValueError(f"the rope is on {rope.device}, the state on {dev}")
         io = SfiRopeRows(q=q.data_ptr(), k=k_new.data_ptr())
         io.q_stride = _want_rows("q", q, (c.n_layers, n, c.n_q_heads, c.head_dim), dev)
         io.k_stride = _want_rows("k_new", k_new, (c.n_layers, n, c.n_kv_heads, c.head_dim), dev)
-        if v_new is not None:
-            io.v = v_new.data_ptr()
-            io.v_stride = _want_rows("v_new", v_new, (c.n_layers, n, c.n_kv_heads, c.head_dim), dev)
+        io.v = v_new.data_ptr()
+        io.v_stride = _want_rows("v_new", v_new, (c.n_layers, n, c.n_kv_heads, c.head_dim), dev)
         if pos is not None:
             _want("pos", pos, torch.int32, (n,), dev)
             io.pos = pos.data_ptr()
