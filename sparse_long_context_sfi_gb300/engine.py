@@ -48,6 +48,8 @@ def _want_rows(name, t, shape, device):
         have = (f"{t.dtype} {tuple(t.shape)} on {t.device}" if isinstance(t, torch.Tensor) else type(t).__name__)
         raise ValueError(f"{name}: torch.bfloat16 {tuple(shape)} on {device} wanted, not {have}")
     layers, rows, heads, dim = shape
+    if t.numel() == 0:
+        return heads * dim      # (nothing is read, whatever the strides say)
     step = t.stride(1) if rows > 1 else max(heads * dim, t.stride(1))
     if (t.stride(3) != 1 or (heads > 1 and t.stride(2) != dim) or step < heads * dim or step % 8 or
             (layers > 1 and t.stride(0) != rows * step) or t.data_ptr() % 16):
