@@ -50,7 +50,8 @@ def _want_rows(name, t, shape, device):
     layers, rows, heads, dim = shape
     if t.numel() == 0:
         return heads * dim      # (nothing is read, whatever the strides say)
-    step = t.stride(1) if rows > 1 else max(heads * dim, t.stride(1))
+    # (of a single row the layers' distance counts, its own stride says nothing)
+    step = t.stride(1) if rows > 1 else t.stride(0) if layers > 1 else heads * dim
     if (t.stride(3) != 1 or (heads > 1 and t.stride(2) != dim) or step < heads * dim or step % 8 or
             (layers > 1 and t.stride(0) != rows * step) or t.data_ptr() % 16):
         raise ValueError(f"{name}: heads lie packed, rows a multiple of 8 elements apart and layers the rows apart,"

@@ -30,3 +30,23 @@ def test_no_rows(monkeypatch, slices):
     assert [calls[i] for i in (0, 1, 3)] == ["append", "window", "window"]
     # (the library takes a pair of addresses or none)
     assert not calls[2].q and not calls[2].q_out and not calls[2].k and not calls[2].v
+
+
+def one(layers, stride):
+    """One row a layer, rows `stride` apart; the stride of the single row itself says nothing."""
+    x = torch.zeros(layers * stride + 2 * HQ * D, dtype=BF)
+    return [x.as_strided((layers, 1, HQ, D), (stride, own, D, 1)) for own in (stride, HQ * D, 1, 13)]
+
+
+@pytest.mark.parametrize("layers", [1, 3])
+def test_one_row(layers):
+    stride = (HQ + 2 * HKV) * D
+    for t in one(layers, stride):
+        step = engine._want_rows("q", t, (layers, 1, HQ, D), CPU)
+        # what a kernel reads for layer l: (l * rows + 0) * step elements on
+        assert layers == 1 or step == stride
+        assert step >= HQ * D and step % 8 == 0
+    for stride in (HQ * D - 8, HQ * D + 4):
+        for t in one(3, stride):
+            with pytest.raises(ValueError):
+                engine._want_rows("q", t, (3, 1, HQ, D), CPU)
