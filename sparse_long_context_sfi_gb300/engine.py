@@ -253,11 +253,11 @@ class SfiState:
         c, dev = self.cfg, self.device
         if rope.device != dev:
             raise ValueError(f"the rope is on {rope.device}, the state on {dev}")
-        io = SfiRopeRows(q=q.data_ptr(), k=k_new.data_ptr())
+        io = SfiRopeRows()
         io.q_stride = _want_rows("q", q, (c.n_layers, n, c.n_q_heads, c.head_dim), dev)
         io.k_stride = _want_rows("k_new", k_new, (c.n_layers, n, c.n_kv_heads, c.head_dim), dev)
-        io.v = v_new.data_ptr()
         io.v_stride = _want_rows("v_new", v_new, (c.n_layers, n, c.n_kv_heads, c.head_dim), dev)
+        io.q, io.k, io.v = q.data_ptr(), k_new.data_ptr(), v_new.data_ptr()
         if pos is not None:
             _want("pos", pos, torch.int32, (n,), dev)
             io.pos = pos.data_ptr()

@@ -50,3 +50,12 @@ def test_one_row(layers):
         for t in one(3, stride):
             with pytest.raises(ValueError):
                 engine._want_rows("q", t, (3, 1, HQ, D), CPU)
+
+
+@pytest.mark.parametrize("which", ["q", "k_new", "v_new"])
+def test_what_is_no_tensor(which):
+    a = {**arrays(B), "rope": rope(), which: None if which != "q" else np.zeros((LAYERS, B, HQ, D))}
+    with pytest.raises(ValueError):
+        state().window_step(out_fp32=False, **a)
+    with pytest.raises(ValueError):
+        whole_state().step(slow_b=np.ones(B, bool), out_fp32=False, **a)
