@@ -659,7 +659,7 @@ class EncoderStates:
     def clear(self, which=None, stream=None):
         """Empty the inputs of `which` (indices on the host; None: all)."""
         _here(self.device)
-        which = list(range(self.batch)) if which is None else [int(i) for i in which]
+        which = list(range(self.batch)) if which is None else sorted({int(i) for i in which})
         if any(i < 0 or i >= self.batch for i in which):
             raise ValueError(f"inputs are numbered from 0 to {self.batch - 1}")
         if _capturing(stream):
