@@ -161,7 +161,8 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const RopeParams 
             for (int j = 0; j < 8; ++j) {
                 const int d = 8 * l + j;
                 const bool turned = d < p.rot;
-                const float2 v = turned ? cs[row][d < half ? d : d - half] : make_float2(1.f, 0.f);
+                // (a dimension that stays adds 0 * -0 = -0, which leaves a -0 as it is, too)
+                const float2 v = turned ? cs[row][d < half ? d : d - half] : make_float2(1.f, -0.f);
                 c[j] = NORM && w ? v.x * __bfloat162float(w[d]) : v.x;
                 s[j] = (d < half ? -v.y : v.y) * (NORM && w && turned ? __bfloat162float(w[partner(d)]) : 1.f);
             }
