@@ -1,6 +1,6 @@
-// vocab.cuh -- one pass over the logits of a row by the warps of a CTA, for beam.cu and score.cu: chunks
-// of 512 tokens in registers, references that keep the sums of exponentials in range, and the
-// sorted list of a warp's best tokens.
+// vocab.cuh -- one pass over the logits of a row by the warps of a CTA, for beam.cu and score.cu: chunks in
+// registers (of beam.cu 512 tokens; of score.cu 64 bytes a lane, 512 of fp32 and 1024 of bf16), references
+// that keep the sums of exponentials in range, and the sorted list of a warp's best tokens.
 #pragma once
 
 #include "sfi_device.cuh"

@@ -24,8 +24,9 @@
 // without); weights up to 2^8 are as exact in floating point as weights up to 1.
 //
 // CROSS: rows that see all keys of their sequence. The producer shares the work out as it goes
-// (stream_item, or a queue); 32 x 4 rows of 1000 to 4001 keys 61 us (4.8 TB/s; 95 with one CTA to an item),
-// 4 x 2048 rows of 8192 keys 760 us, 1.45 PFLOP/s (cuBLAS in a loop 1.72).
+// (stream_item, or a queue); 32 x 4 rows of 1000 to 4001 keys 59 us (5.0 TB/s; 95 with one CTA to an item),
+// 4 x 2048 rows of 8192 keys 765 to 785 us, 1.40 to 1.44 PFLOP/s (751 in a replayed graph; cuBLAS in a loop 1.72).
+// fp32 outputs of these 121 and 2447.
 //
 // Few rows and a long window: the tiles of an item are split over n_split items, whose
 // unnormalised outputs, maxima and sums the last one to finish joins, in split order.
@@ -517,8 +518,9 @@ constexpr int window_smem() { return 1024 + NQ * QR * 256 + ST * KT * 512 + stat
 // bits, as in the decode kernels (one token of 32 sequences under a window of 4096: 92 us, with one
 // part 87): an output near zero is then off by its own rounding alone. In a chunk's bf16 outputs
 // the second part costs more than it gives: four 32K prompts under a window of 64 take 518 us with
-// it and 446 without, an 8K chunk under 4096 617 and 412, and the error (2-norm) falls from 2.3e-3 to
-// the output's own rounding, 1.7e-3; fp32 outputs are there for who needs more.
+// it and 446 without, an 8K chunk under 4096 617 and 412, 4 x 2048 rows that see 8192 states each 1132 and
+// 765, ragged ones 113 and 91, and the error (2-norm) falls from 2.2e-3 to 2.3e-3 to the output's own
+// rounding, 1.7e-3; fp32 outputs are there for who needs more.
 // F32 (fp32 outputs): three parts, 24 bits, and O is moved every kFlush tiles to a second
 // accumulator M with ordinary additions: the tensor core's own additions do not round to nearest,
 // and 520 of them in a row (two parts, a window of 4096) had left outputs 1.0e-5 off (2-norm). Tensor
