@@ -179,6 +179,30 @@ struct Part<__nv_bfloat16> {
     }
 };
 
+// N 16-byte pieces of a row, 32 apart; pieces that reach over either end of the row are put together
+// from its tokens, those beyond them are -inf, which no sum and no list sees.
+template <typename T, int N>
+__device__ __forceinline__ void load_pieces(const T *row, int shift, int vocab, int piece, uint4 *w)
+{
+    constexpr int V = Chunk<T>::kV;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const int at = (piece + 32 * i) * V - shift;           // first token of the piece
+        if (at >= 0 && at + V <= vocab) {
+            w[i] = __ldcs(reinterpret_cast<const uint4 *>(row + at));
+        } else if (at >= vocab || at + V <= 0) {
+            const uint32_t low = sizeof(T) == 4 ? 0xff800000u : 0xff80ff80u;
+            w[i] = make_uint4(low, low, low, low);
+        } else {
+            T t[V];
+#pragma unroll
+            for (int j = 0; j < V; ++j)
+                t[j] = at + j >= 0 && at + j < vocab ? row[at + j] : static_cast<T>(-CUDART_INF_F);
+            w[i] = *reinterpret_cast<const uint4 *>(t);
+        }
+    }
+}
+
 // A chunk that reaches over an end of the row.
 template <typename T>
 __device__ __noinline__ void load_edge(const T *row, int shift, int vocab, int piece, uint4 *w)

@@ -175,20 +175,19 @@ struct Chunk<__nv_bfloat16> {
     }
 };
 
-// N 16-byte pieces of a row, 32 apart; pieces that reach over either end of the row are put together
-// from its tokens (others: -inf, which no sum and no list sees).
-template <typename T, int N>
-__device__ __forceinline__ void load_pieces(const T *row, int shift, int vocab, int piece, uint4 *w)
+// The pieces of this lane in the chunk that begins with piece0; those that reach over either end of the
+// row are put together from its tokens (others: -inf, which no sum and no list sees). (256 rows of 128001
+// tokens take a selection 31.9 us, with score.cu's load_pieces in its place 32.2.)
+template <typename T>
+__device__ __forceinline__ void load_chunk(const T *row, int shift, int vocab, int piece0, int lane,
+                                           uint4 *w)
 {
     constexpr int V = Chunk<T>::kV;
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const int at = (piece + 32 * i) * V - shift;           // first token of the piece
+    for (int i = 0; i < kLaneTok / V; ++i) {
+        const int at = (piece0 + 32 * i + lane) * V - shift;   // first token of the piece
         if (at >= 0 && at + V <= vocab) {
             w[i] = __ldcs(reinterpret_cast<const uint4 *>(row + at));
-        } else if (at >= vocab || at + V <= 0) {
-            const uint32_t low = sizeof(T) == 4 ? 0xff800000u : 0xff80ff80u;
-            w[i] = make_uint4(low, low, low, low);
         } else {
             T t[V];
 #pragma unroll
@@ -197,14 +196,6 @@ __device__ __forceinline__ void load_pieces(const T *row, int shift, int vocab, 
             w[i] = *reinterpret_cast<const uint4 *>(t);
         }
     }
-}
-
-// The pieces of this lane in the chunk that begins with piece0.
-template <typename T>
-__device__ __forceinline__ void load_chunk(const T *row, int shift, int vocab, int piece0, int lane,
-                                           uint4 *w)
-{
-    load_pieces<T, kLaneTok / Chunk<T>::kV>(row, shift, vocab, piece0 + lane, w);
 }
 
 }  // namespace
